@@ -476,6 +476,39 @@ owq_status owq_linear_backward_batched(const owq_layer* Ls, const uint16_t* cons
                                        uint16_t* const* dxs, float* const* dws,
                                        void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------- gradient norm and clipping --- */
+
+/* One gradient tensor of owq_clip_grad_norm (host struct, device pointers). */
+typedef struct owq_grad {
+    const void* g;    /* n elements of `type` (may be NULL iff n == 0) */
+    void* out;        /* where they go: g itself (in place) or another buffer */
+    int64_t n;        /* 0 <= n <= 2^40 */
+    int32_t type;     /* 0: fp32, 1: fp16 */
+} owq_grad;
+
+/* Bytes of device workspace owq_clip_grad_norm needs for `count` tensors (0 for
+ * count outside 1..4096). */
+size_t owq_clip_grad_norm_workspace_bytes(int32_t count);
+
+/* The global norm over `count` gradient tensors, and clipping by it (what stands
+ * between the weak columns' gradients of owq_linear_backward and the update of
+ * weak-column tuning, [PL] "Weak Column Tuning" (paper "PEFT with Weak Column
+ * Tuning", p.5)):
+ *   norm   = sqrt(sum over every tensor and element of g^2)   fp64 sums
+ *   out    = g * (max_norm / norm) if norm > max_norm, else g  fp64 product,
+ *            rounded once (nearest-even) to the tensor's type
+ * norm is written as fp32 [1] (infinity above its range); the comparison and the
+ * factor use the fp64 value. If it is not finite (an infinity or NaN among the
+ * gradients) nothing is scaled: the caller sees it and drops the step. max_norm:
+ * >= 0; infinity only measures. Tensors may be of both types, and empty.
+ * Overlaps: every out must be disjoint from every other out and, unless it is the
+ * tensor's own g, from every g (OWQ_ERR_RANGE); norm and workspace must be
+ * disjoint from all of them. workspace: >= owq_clip_grad_norm_workspace_bytes
+ * (count) bytes, 256-byte aligned, contents ignored; calls sharing it must be
+ * ordered. items: HOST array. Bitwise deterministic. */
+owq_status owq_clip_grad_norm(const owq_grad* items, int32_t count, double max_norm, float* norm,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------- measurement reference --- */
 
 /* Not a step of the method: a read-only HBM stream with the M = 1 decode

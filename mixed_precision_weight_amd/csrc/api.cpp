@@ -3,10 +3,13 @@
 // every entry point are in include/owq.h.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
+#include <utility>
 #include <vector>
 
 #include "../../include/owq.h"
@@ -46,6 +49,7 @@ owq_status hip_status(hipError_t e, const char* what)
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 constexpr int64_t kMaxK = 65536;
+constexpr int32_t kMaxGrads = 4096;  // tensors per owq_clip_grad_norm
 
 owq_status check_k_dim(int64_t K)
 {
@@ -796,6 +800,68 @@ owq_status owq_linear_batched(const owq_layer* Ls, const uint16_t* const* xs, ui
                 : owq::launch_gemv(d.data() + l0, n, (int)M, (hipStream_t)stream);
     }
     return hip_status(e, "owq_linear_batched launch");
+}
+
+size_t owq_clip_grad_norm_workspace_bytes(int32_t count)
+{
+    if (count < 1 || count > kMaxGrads)
+        return 0;
+    return owq::clip_workspace_bytes(count);
+}
+
+owq_status owq_clip_grad_norm(const owq_grad* items, int32_t count, double max_norm, float* norm, void* workspace,
+                              size_t workspace_bytes, void* stream)
+{
+    if (!items || !norm || !workspace)
+        return fail(OWQ_ERR_NULL, "items, norm and workspace must be non-NULL");
+    if (count < 1 || count > kMaxGrads)
+        return fail(OWQ_ERR_UNSUPPORTED, "count = %d: need 1 <= count <= %d", count, kMaxGrads);
+    if (!(max_norm >= 0.0))
+        return fail(OWQ_ERR_RANGE, "max_norm = %g: need max_norm >= 0", max_norm);
+    if (!aligned(norm, 4) || !aligned(workspace, 256))
+        return fail(OWQ_ERR_ALIGN, "misaligned pointer (norm: 4 B, workspace: 256 B)");
+    if (workspace_bytes < owq::clip_workspace_bytes(count))
+        return fail(OWQ_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", workspace_bytes,
+                    owq::clip_workspace_bytes(count));
+    try {
+        std::vector<owq::ClipEntry> it((size_t)count);
+        std::vector<std::pair<uintptr_t, uintptr_t>> outs;  // [begin, end) of the non-empty outputs
+        outs.reserve((size_t)count);
+        for (int32_t i = 0; i < count; i++) {
+            const owq_grad& g = items[i];
+            if (g.n < 0 || g.n > (int64_t)1 << 40)
+                return fail(OWQ_ERR_SHAPE, "item %d: n = %lld: need 0 <= n <= 2^40", i, (long long)g.n);
+            if (g.type != 0 && g.type != 1)
+                return fail(OWQ_ERR_UNSUPPORTED, "item %d: type = %d: need 0 (fp32) or 1 (fp16)", i, g.type);
+            if (g.n > 0 && (!g.g || !g.out))
+                return fail(OWQ_ERR_NULL, "item %d: g and out must be non-NULL when n > 0", i);
+            const size_t size = g.type ? 2 : 4;
+            if (g.n > 0 && (!aligned(g.g, size) || !aligned(g.out, size)))
+                return fail(OWQ_ERR_ALIGN, "item %d: misaligned pointer (%zu B)", i, size);
+            it[(size_t)i] = owq::ClipEntry{g.g, g.out, g.n, 0, g.type};
+            if (g.n > 0)
+                outs.emplace_back((uintptr_t)g.out, (uintptr_t)g.out + (size_t)g.n * size);
+        }
+        std::sort(outs.begin(), outs.end());
+        for (size_t i = 1; i < outs.size(); i++)
+            if (outs[i].first < outs[i - 1].second)
+                return fail(OWQ_ERR_RANGE, "two outputs overlap (a tensor listed twice?)");
+        for (int32_t i = 0; i < count; i++) {
+            const owq_grad& g = items[i];
+            if (g.n == 0)
+                continue;
+            // the one output that begins in or reaches into [b, e): the last that begins below e
+            const uintptr_t b = (uintptr_t)g.g, e = b + (size_t)g.n * (g.type ? 2 : 4);
+            auto o = std::lower_bound(outs.begin(), outs.end(), std::make_pair(e, (uintptr_t)0));
+            const bool hit = o != outs.begin() && (o - 1)->second > b;
+            if (hit && !(g.out == g.g && (o - 1)->first == b))
+                return fail(OWQ_ERR_RANGE, "item %d: g overlaps an output that is not its own", i);
+        }
+        return hip_status(owq::launch_clip(it.data(), count, max_norm, norm, workspace, (hipStream_t)stream),
+                          "owq_clip_grad_norm launch");
+    } catch (const std::exception& ex) {
+        return fail(OWQ_ERR_HIP, "owq_clip_grad_norm: host memory: %s", ex.what());
+    }
 }
 
 int64_t owq_stream_read_sink_words(int64_t bytes) { return bytes > 0 ? owq::stream_read_sink_words(bytes) : 0; }

@@ -170,6 +170,18 @@ hipError_t launch_pack_optq(const uint16_t* W, int64_t N, int64_t K, const uint1
                             const int32_t* idx, int32_t k, uint32_t* q, uint16_t* scales, uint8_t* zeros,
                             uint16_t* ww, void* ws, const OptqPlan& p, hipStream_t s);
 
+// ------------------------------------------------- gradient norm and clipping --
+struct ClipEntry {
+    const void* g;
+    void* out;       // == g: in place
+    int64_t n;
+    int64_t chunk0;  // first chunk of the tensor (set by launch_clip)
+    int32_t half;    // 1: fp16, 0: fp32
+};
+constexpr int kClipItems = 80;  // tensors per launch of the first pass (kernel arguments below 4 KB)
+size_t clip_workspace_bytes(int count);
+hipError_t launch_clip(const ClipEntry* items, int count, double max_norm, float* norm, void* ws, hipStream_t s);
+
 // read-only streaming reference (stream.hip): one word per 4608-byte wavefront
 int64_t stream_read_sink_words(int64_t bytes);
 hipError_t launch_stream_read(const void* src, int64_t bytes, uint32_t* sink, hipStream_t s);

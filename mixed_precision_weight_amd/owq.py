@@ -49,6 +49,11 @@ class OwqGroupedLayer(ctypes.Structure):
                 ("weak_idx", _P), ("w_weak", _P)]
 
 
+class OwqGrad(ctypes.Structure):
+    """Mirror of ``owq_grad`` (host struct, device pointers)."""
+    _fields_ = [("g", _P), ("out", _P), ("n", _I64), ("type", _I32)]
+
+
 EXPORTS = {
     "owq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "owq_last_error": (ctypes.c_char_p, []),
@@ -86,6 +91,9 @@ EXPORTS = {
     "owq_linear_grouped": (ctypes.c_int, [ctypes.POINTER(OwqGroupedLayer), _P, _I64, _P, _P]),
     "owq_linear_grouped_batched": (ctypes.c_int, [ctypes.POINTER(OwqGroupedLayer), ctypes.POINTER(_P),
                                                   ctypes.POINTER(_P), _I32, _I64, _P]),
+    "owq_clip_grad_norm_workspace_bytes": (ctypes.c_size_t, [_I32]),
+    "owq_clip_grad_norm": (ctypes.c_int, [ctypes.POINTER(OwqGrad), _I32, ctypes.c_double, _P, _P, ctypes.c_size_t,
+                                          _P]),
     "owq_stream_read_sink_words": (_I64, [_I64]),
     "owq_stream_read": (ctypes.c_int, [_P, _I64, _P, _I64, _P]),
 }
@@ -157,6 +165,38 @@ def _dev(t: torch.Tensor, dtype, name: str, shape=None) -> torch.Tensor:
     _meta(t, dtype, name, shape)
     _on_device((name, t))
     return t
+
+
+class _Launch:
+    """Context of one call on GPU `index`: makes that device and the stream to
+    launch on (`stream`, or torch's current stream of the device) current, so that
+    temporaries and outputs allocated inside come from that stream's memory and are
+    not handed out again before it has passed the call. Where they are current
+    already (no stream given, the device is the current one) nothing is switched."""
+
+    __slots__ = ("index", "guard", "handle")
+
+    def __init__(self, index: int, stream):
+        if stream is not None and stream.device.index != index:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{index}")
+        if stream is None:
+            stream = torch.cuda.current_stream(index)
+            self.guard = None if torch.cuda.current_device() == index else torch.cuda.stream(stream)
+        else:
+            self.guard = torch.cuda.stream(stream)
+        self.index = index
+        self.handle = stream.cuda_stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc) if self.guard is not None else False
+
+    def empty(self, shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.index))
 
 
 def _ptr(t):
@@ -907,6 +947,82 @@ class PreparedCalibrate:
         st = self.stream if self.stream is not None else _stream()
         _check(self.fn(self.items, self.n, self.ws, self.ws_bytes, st), "owq_calibrate_score_batched")
         return self.results
+
+
+# ---------------------------------------------------- gradient norm and clipping
+
+
+def clip_grad_norm_workspace_bytes(sizes: list) -> int:
+    """Workspace of clip_grad_norm for tensors of these element counts."""
+    return int(lib().owq_clip_grad_norm_workspace_bytes(len(sizes)))
+
+
+_GRAD_TYPES = {torch.float32: 0, torch.float16: 1}  # owq_grad's type
+
+
+def _grads_checked(grads: list, outs):
+    """Raise for the first gradient or out that clip_grad_norm does not take."""
+    for i, t in enumerate(grads):
+        if isinstance(t, torch.Tensor) and t.dtype not in _GRAD_TYPES:
+            raise TypeError(f"[{i}] gradient must be torch.float32 or torch.float16, got {t.dtype}")
+        _meta(t, getattr(t, "dtype", None), f"[{i}] gradient")
+        if outs is not None:
+            o = _meta(outs[i], t.dtype, f"[{i}] out")
+            if o.numel() != t.numel():
+                raise ValueError(f"[{i}] out has {o.numel()} elements, the gradient has {t.numel()}")
+
+
+def clip_grad_norm(grads: list, max_norm: float, outs: list | None = None, norm: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Global norm of the gradient tensors (fp32 or fp16, any shape, contiguous),
+    and clipping: every tensor is multiplied by max_norm / norm where norm >
+    max_norm, in place or into outs (owq_clip_grad_norm; an out has its gradient's
+    type and number of elements). Returns the norm, fp32
+    [1], on the device; a norm that is not finite scales nothing."""
+    n = len(grads)
+    if n < 1 or n > 4096:
+        raise ValueError(f"need 1 to 4096 gradients, got {n}")
+    if outs is not None and len(outs) != n:
+        raise ValueError(f"need one out per gradient: {n} gradients, {len(outs)} outs")
+    max_norm = float(max_norm)
+    if not max_norm >= 0.0:
+        raise ValueError(f"max_norm = {max_norm}: need max_norm >= 0")
+    # a step has hundreds of tensors: they are checked by whole-list calls, and one
+    # by one (for the message) only when something is wrong
+    T = torch.Tensor
+    every = list(grads) if outs is None else list(grads) + list(outs)
+    if all([isinstance(t, T) for t in every]):
+        types = [t.dtype for t in every]
+        counts = list(map(T.numel, every))
+        good = (all(map(T.is_contiguous, every)) and set(types) <= _GRAD_TYPES.keys()
+                and types[n:] == types[:len(types) - n] and counts[n:] == counts[:len(counts) - n])
+    else:
+        good = False
+    if not good:
+        _grads_checked(grads, outs)
+    if norm is not None:
+        _meta(norm, torch.float32, "norm", (1,))
+    if workspace is not None:
+        _meta(workspace, torch.uint8, "workspace")
+    rest = [t for t in (norm, workspace) if t is not None]
+    devs = set(map(T.get_device, every)) | set(map(T.get_device, rest))
+    if len(devs) != 1 or -1 in devs:
+        _on_device(("norm", norm), ("workspace", workspace), *[(f"[{i % n}] {'out' if i >= n else 'gradient'}", t)
+                                                               for i, t in enumerate(every)])
+    with _Launch(devs.pop(), stream) as run:
+        if norm is None:
+            norm = run.empty(1, torch.float32)
+        if workspace is None:
+            workspace = run.empty(clip_grad_norm_workspace_bytes(every[:n]), torch.uint8)
+        ptrs = list(map(T.data_ptr, every))
+        words = (_I64 * (4 * n))()  # one owq_grad is four 64-bit words (type in the low half of the last)
+        words[0::4] = ptrs[:n]
+        words[1::4] = ptrs[-n:]
+        words[2::4] = counts[:n]
+        words[3::4] = [_GRAD_TYPES[t] for t in types[:n]]
+        _check(lib().owq_clip_grad_norm(ctypes.cast(words, ctypes.POINTER(OwqGrad)), n, max_norm, norm.data_ptr(),
+                                        workspace.data_ptr(), workspace.numel(), run.handle), "owq_clip_grad_norm")
+    return norm
 
 
 # ----------------------------------------------------------- measurement aid

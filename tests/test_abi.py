@@ -404,3 +404,40 @@ def test_linear_grouped_batched_validation(lib):
     assert f(Ls, xs, ys, 2, 1, None) == 5      # layer 1: G = 96
     bad = (P * 2)(FAKE + 8, FAKE)
     assert f(Ls, bad, ys, 1, 1, None) == 4
+
+
+def test_clip_grad_norm_validation(lib):
+    from mixed_precision_weight_amd.owq import OwqGrad
+    need = lib.owq_clip_grad_norm_workspace_bytes(2)
+    assert need > 0
+    assert lib.owq_clip_grad_norm_workspace_bytes(0) == 0
+    assert lib.owq_clip_grad_norm_workspace_bytes(4097) == 0
+
+    def call(items, max_norm=1.0, norm=FAKE, ws=FAKE, size=need, count=None):
+        arr = (OwqGrad * max(len(items), 1))(*[OwqGrad(*i) for i in items])
+        return lib.owq_clip_grad_norm(arr, len(items) if count is None else count, max_norm, norm, ws, size, None)
+
+    ok = (FAKE, FAKE, 100, 0)
+    assert lib.owq_clip_grad_norm(None, 1, 1.0, FAKE, FAKE, need, None) == 1
+    assert call([ok], norm=None) == 1
+    assert call([ok], ws=None) == 1
+    assert call([(None, FAKE, 100, 0)]) == 1
+    assert call([(FAKE, None, 100, 0)]) == 1
+    assert call([ok], count=0) == 5
+    assert call([ok], count=4097) == 5
+    assert call([(FAKE, FAKE, -1, 0)]) == 2
+    assert call([(FAKE, FAKE, 2 ** 40 + 1, 0)]) == 2
+    assert call([(FAKE, FAKE, 100, 2)]) == 5
+    assert call([ok], max_norm=-1.0) == 3
+    assert call([ok], max_norm=float("nan")) == 3
+    assert call([(FAKE + 2, FAKE + 2, 100, 0)]) == 4
+    assert call([(FAKE + 1, FAKE + 1, 100, 1)]) == 4
+    assert call([ok], norm=FAKE + 2) == 4
+    assert call([ok], ws=FAKE + 128) == 4
+    assert call([ok, (FAKE + 8192, FAKE + 8192, 100, 0)], size=need - 1) == 6
+    assert call([ok, ok]) == 3                                            # listed twice, in place
+    assert call([ok, (FAKE + 396, FAKE + 396, 100, 0)]) == 3              # the last element shared
+    assert call([(FAKE, FAKE + 4, 100, 0)]) == 3                          # into itself, shifted
+    assert call([ok, (FAKE + 8, FAKE + 8192, 10, 1)]) == 3                # reads what another writes
+    assert call([(FAKE, FAKE, 100, 0), (FAKE, FAKE + 8192, 100, 0)]) == 3  # reads what it writes elsewhere
+    assert b"item 1" in lib.owq_last_error()

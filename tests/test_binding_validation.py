@@ -218,3 +218,30 @@ def test_grouped_checks_shapes():
     with pytest.raises(ValueError, match="y has shape"):
         owq.linear_grouped(lay, torch.zeros((2, K), dtype=torch.float16), torch.zeros((1, N), dtype=torch.float16))
     _host_only(owq.linear_grouped, lay, torch.zeros((3, K), dtype=torch.float16))
+
+
+def test_clip_grad_norm_checks():
+    a, b = torch.zeros(10), torch.zeros((3, 4), dtype=torch.float16)
+    with pytest.raises(ValueError, match="1 to 4096"):
+        owq.clip_grad_norm([], 1.0)
+    with pytest.raises(ValueError, match="one out per gradient"):
+        owq.clip_grad_norm([a, b], 1.0, outs=[a])
+    with pytest.raises(ValueError, match="max_norm"):
+        owq.clip_grad_norm([a], -1.0)
+    with pytest.raises(ValueError, match="max_norm"):
+        owq.clip_grad_norm([a], float("nan"))
+    with pytest.raises(TypeError, match=r"\[1\] gradient must be torch.float32 or"):
+        owq.clip_grad_norm([a, b.double()], 1.0)
+    with pytest.raises(TypeError, match=r"\[0\] gradient must be a torch.Tensor"):
+        owq.clip_grad_norm([3.0], 1.0)
+    with pytest.raises(ValueError, match=r"\[0\] gradient must be contiguous"):
+        owq.clip_grad_norm([b.t()], 1.0)
+    with pytest.raises(ValueError, match=r"\[1\] out has 11 elements"):
+        owq.clip_grad_norm([a, b], 1.0, outs=[torch.zeros(10), torch.zeros(11, dtype=torch.float16)])
+    with pytest.raises(TypeError, match=r"\[0\] out must be"):
+        owq.clip_grad_norm([a], 1.0, outs=[torch.zeros(10, dtype=torch.float16)])
+    with pytest.raises(TypeError, match="norm must be"):
+        owq.clip_grad_norm([a], 1.0, norm=torch.zeros(1, dtype=torch.float64))
+    with pytest.raises(TypeError, match="workspace"):
+        owq.clip_grad_norm([a], 1.0, workspace=torch.zeros(64))
+    _host_only(owq.clip_grad_norm, [a, b], 1.0)
