@@ -476,6 +476,39 @@ owq_status owq_linear_backward_batched(const owq_layer* Ls, const uint16_t* cons
                                        uint16_t* const* dxs, float* const* dws,
                                        void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------- low-rank adapters of many requests beside a layer --- */
+
+/* `count` low-rank adapters of one layer (HOST struct, device pointers). Adapters
+ * of smaller rank are padded with zero rows of A and zero columns of B. */
+typedef struct owq_adapters {
+    const uint16_t* A;   /* fp16 [count][rank][K], 16-byte aligned */
+    const uint16_t* B;   /* fp16 [count][N][rank], 16-byte aligned */
+    const float* alpha;  /* fp32 [count] */
+    int32_t count;       /* >= 1 */
+    int32_t rank;        /* 1 .. 256 */
+} owq_adapters;
+
+/* Bytes of device workspace owq_linear_adapters needs (0 for sizes outside its range). */
+size_t owq_linear_adapters_workspace_bytes(int32_t rank, int64_t M);
+
+/* owq_linear on a base that many tuned variants share, each token with the
+ * adapter of its own request, or none:
+ *   y[m] = x[m] W^T + alpha_r (x[m] A_r^T) B_r^T,   r = which[m]
+ * with W the packed layer ([PL] "Real-device acceleration" (paper "Acceleration on
+ * Real Device", p.6) for the shared product). which: int32 [M]; any value outside
+ * [0, count) means no adapter for that token: its output is then owq_linear's, bit
+ * for bit. x A_r^T is summed in fp32 and kept in at least 22 bits of the row's
+ * largest value; the sum with the shared product is rounded to fp16 once. A token's
+ * output depends on its own adapter only, also where another's holds values that
+ * are not finite. Two launches (low-rank products; the linear with the second
+ * products in its epilogue) per owq_linear launch of the same M. workspace: >=
+ * owq_linear_adapters_workspace_bytes(rank, M) bytes, 256-byte aligned, contents
+ * ignored; calls sharing it must be ordered. Other arguments and errors as
+ * owq_linear, plus OWQ_ERR_WORKSPACE, and OWQ_ERR_SHAPE for count and rank. */
+owq_status owq_linear_adapters(const owq_layer* L, const owq_adapters* ad, const int32_t* which,
+                               const uint16_t* x, int64_t M, uint16_t* y, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------- gradient norm and clipping --- */
 
 /* One gradient tensor of owq_clip_grad_norm (host struct, device pointers). */

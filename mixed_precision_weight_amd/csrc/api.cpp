@@ -49,6 +49,7 @@ owq_status hip_status(hipError_t e, const char* what)
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 constexpr int64_t kMaxK = 65536;
+constexpr int32_t kMaxRank = 256;    // of a low-rank adapter
 constexpr int32_t kMaxGrads = 4096;  // tensors per owq_clip_grad_norm
 
 owq_status check_k_dim(int64_t K)
@@ -133,10 +134,10 @@ owq::LinearDesc desc_of(const owq_layer* L, const uint16_t* x, uint16_t* y)
 
 namespace owq {
 
-hipError_t launch_linear_any(const LinearDesc& d, int64_t M, hipStream_t s)
+hipError_t launch_linear_any(const LinearDesc& d, int64_t M, hipStream_t s, const AdapterDesc* ad)
 {
     if (M >= gemm_min_m())
-        return launch_gemm(d, M, s);
+        return launch_gemm(d, M, s, ad);
     // decode kernels, in token slices of the chosen kernel's capacity
     hipError_t e = hipSuccess;
     for (int64_t m0 = 0; m0 < M && e == hipSuccess;) {
@@ -146,7 +147,14 @@ hipError_t launch_linear_any(const LinearDesc& d, int64_t M, hipStream_t s)
         LinearDesc dm = d;
         dm.x = d.x + m0 * d.K;
         dm.y = d.y + m0 * d.N;
-        e = mat ? launch_mfv(&dm, 1, (int)mm, s) : launch_gemv(&dm, 1, (int)mm, s);
+        AdapterDesc am;
+        if (ad) {
+            am = *ad;
+            am.which = ad->which + m0;
+            am.t = ad->t + m0 * adapter_rpad(ad->rank);
+        }
+        e = mat ? launch_mfv(&dm, 1, (int)mm, s, ad ? &am : nullptr)
+                : launch_gemv(&dm, 1, (int)mm, s, ad ? &am : nullptr);
         m0 += mm;
     }
     return e;
@@ -800,6 +808,41 @@ owq_status owq_linear_batched(const owq_layer* Ls, const uint16_t* const* xs, ui
                 : owq::launch_gemv(d.data() + l0, n, (int)M, (hipStream_t)stream);
     }
     return hip_status(e, "owq_linear_batched launch");
+}
+
+size_t owq_linear_adapters_workspace_bytes(int32_t rank, int64_t M)
+{
+    if (rank < 1 || rank > kMaxRank || M < 1 || M > INT32_MAX)
+        return 0;
+    return owq::adapter_workspace_bytes(rank, M);
+}
+
+owq_status owq_linear_adapters(const owq_layer* L, const owq_adapters* ad, const int32_t* which, const uint16_t* x,
+                               int64_t M, uint16_t* y, void* workspace, size_t workspace_bytes, void* stream)
+{
+    owq_status st = check_layer(L, M, x, y);
+    if (st != OWQ_OK)
+        return st;
+    if (!ad || !ad->A || !ad->B || !ad->alpha || !which || !workspace)
+        return fail(OWQ_ERR_NULL, "adapters (A, B, alpha), which and workspace must be non-NULL");
+    if (ad->rank < 1 || ad->rank > kMaxRank)
+        return fail(OWQ_ERR_SHAPE, "rank = %d: need 1 <= rank <= %d", ad->rank, kMaxRank);
+    if (ad->count < 1)
+        return fail(OWQ_ERR_SHAPE, "count = %d: need at least one adapter", ad->count);
+    if (!aligned(ad->A, 16) || !aligned(ad->B, 16) || !aligned(ad->alpha, 4) || !aligned(which, 4) ||
+        !aligned(workspace, 256))
+        return fail(OWQ_ERR_ALIGN, "misaligned pointer (A, B: 16 B, alpha, which: 4 B, workspace: 256 B)");
+    if (workspace_bytes < owq::adapter_workspace_bytes(ad->rank, M))
+        return fail(OWQ_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", workspace_bytes,
+                    owq::adapter_workspace_bytes(ad->rank, M));
+    st = check_idx_on_host(L->weak_idx, L->k, L->K, (hipStream_t)stream);
+    if (st != OWQ_OK)
+        return st;
+    const owq::AdapterDesc a{ad->A, ad->B, ad->alpha, which, static_cast<float*>(workspace), ad->count, ad->rank};
+    hipError_t e = owq::launch_adapter_shrink(a, x, M, L->K, (hipStream_t)stream);
+    if (e == hipSuccess)
+        e = owq::launch_linear_any(desc_of(L, x, y), M, (hipStream_t)stream, &a);
+    return hip_status(e, "owq_linear_adapters launch");
 }
 
 size_t owq_clip_grad_norm_workspace_bytes(int32_t count)

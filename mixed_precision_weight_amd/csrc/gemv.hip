@@ -43,6 +43,7 @@
 #include <cstring>
 #include <type_traits>
 
+#include "owq_adapters.h"
 #include "owq_decode.h"
 #include "owq_device.h"
 #include "owq_launch.h"
@@ -131,8 +132,11 @@ __device__ __forceinline__ int reduced_index(int q) { return (q & 1) + ((q >> 1)
 // GRP: the group-wise form (s and z are [N][K / G], one per row and G columns):
 // each code group is decoded with its own zero point, its dot2 sum starts from 0
 // and is scaled by its group's step into the row's accumulator.
-template <int M, bool MMA, int R, bool GRP = false>
-__device__ __forceinline__ void gemv_body(const GemvBatch& b)
+// ADP: low-rank adapters are added to the (only) layer's output: lane l adds its
+// shares B_r[i][c] t[m][c], c = l, l + 64, ..., before the 64-lane reduction, as
+// it does for the weak columns.
+template <int M, bool MMA, int R, bool GRP = false, bool ADP = false>
+__device__ __forceinline__ void gemv_body(const GemvBatch& b, const AdapterArgs& ad = AdapterArgs{})
 {
     static_assert(!(GRP && MMA), "the group-wise form scales each lane's partial sum");
     constexpr int TT = kChunkTiles;
@@ -242,6 +246,24 @@ __device__ __forceinline__ void gemv_body(const GemvBatch& b)
         for (int m = 0; m < M; m++) {
             const float xv = h2f(XW[(int64_t)m * KW + j]);
             xw[m][v] = c < k ? xv : 0.0f;
+        }
+    }
+
+    // adapters: each token's index, its scaled t and the rows' weights (rank up to
+    // 64; more below). Loads clamped to valid adapters, results selected.
+    int aid[ADP ? M : 1];
+    float at[ADP ? M : 1];
+    uint32_t ab[ADP ? R : 1][ADP ? M : 1];
+    if constexpr (ADP) {
+#pragma unroll
+        for (int m = 0; m < M; m++) {
+            const int id = ad.which[m];
+            aid[m] = id >= 0 && id < ad.count ? id : -1;
+            const int ic = aid[m] >= 0 ? id : 0;
+            at[m] = ad.alpha[ic] * ad.t[(int64_t)m * ad.rpad + min(lane, ad.rank - 1)];
+#pragma unroll
+            for (int r = 0; r < R; r++)
+                ab[r][m] = ad.B[((int64_t)ic * N + min(row0 + r, N - 1)) * ad.rank + min(lane, ad.rank - 1)];
         }
     }
 
@@ -392,6 +414,22 @@ __device__ __forceinline__ void gemv_body(const GemvBatch& b)
                 }
             }
         }
+        if constexpr (ADP) {
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                const float t = at[m] * h2f((uint16_t)ab[r][m]);
+                part[r / 4][r % 4] += aid[m] >= 0 && lane < ad.rank ? t : 0.0f;
+            }
+            if (aid[m] >= 0 && ad.rank > 64) {
+                const float al = ad.alpha[aid[m]];
+#pragma unroll
+                for (int r = 0; r < R; r++) {
+                    const uint16_t* br = ad.B + ((int64_t)aid[m] * N + min(row0 + r, N - 1)) * ad.rank;
+                    for (int c = lane + 64; c < ad.rank; c += 64)
+                        part[r / 4][r % 4] += al * ad.t[(int64_t)m * ad.rpad + c] * h2f(br[c]);
+                }
+            }
+        }
 #pragma unroll
         for (int qg = 0; qg < RQ; qg++) {
             reduce4(part[qg]);
@@ -423,9 +461,35 @@ __global__ __launch_bounds__(256) void k_gemv_grouped(GemvBatch b)
     gemv_body<M, false, kRowsPerWave, true>(b);
 }
 
+// the same kernels with low-rank adapters in the epilogue
 template <int M>
-hipError_t launch_m(const GemvBatch& b, int nblocks, size_t lds, hipStream_t s)
+__global__ __launch_bounds__(256) void k_gemv_adapters(GemvBatch b, AdapterArgs ad)
 {
+    gemv_body<M, false, kRowsPerWave, false, true>(b, ad);
+}
+__global__ __launch_bounds__(256) void k_gemv_r2_adapters(GemvBatch b, AdapterArgs ad)
+{
+    gemv_body<1, false, 2, false, true>(b, ad);
+}
+template <int M>
+__global__ __launch_bounds__(256) void k_gemv_mfma_adapters(GemvBatch b, AdapterArgs ad)
+{
+    gemv_body<M, true, kRowsPerWave, false, true>(b, ad);
+}
+
+template <int M>
+hipError_t launch_m(const GemvBatch& b, const AdapterArgs* ad, int nblocks, size_t lds, hipStream_t s)
+{
+    if (ad) {
+        if constexpr (M <= 2) {
+            if (gemv_products_on_matrix_cores(M)) {
+                hipLaunchKernelGGL((k_gemv_mfma_adapters<M>), dim3(nblocks), dim3(256), lds, s, b, *ad);
+                return hipGetLastError();
+            }
+        }
+        hipLaunchKernelGGL((k_gemv_adapters<M>), dim3(nblocks), dim3(256), lds, s, b, *ad);
+        return hipGetLastError();
+    }
     if constexpr (M <= 2) {
         if (gemv_products_on_matrix_cores(M)) {
             hipLaunchKernelGGL((k_gemv_mfma<M>), dim3(nblocks), dim3(256), lds, s, b);
@@ -510,21 +574,30 @@ int build_batch(const LinearDesc* d, int count, const int64_t* groups, GemvBatch
 
 // One launch for the batch; blocks of 4 wavefronts, each wavefront owning
 // kRowsPerWave consecutive rows of its layer.
-hipError_t launch_gemv(const LinearDesc* d, int count, int M, hipStream_t s)
+hipError_t launch_gemv(const LinearDesc* d, int count, int M, hipStream_t s, const AdapterDesc* adapters)
 {
     GemvBatch b;
+    AdapterArgs args;
+    const AdapterArgs* ad = nullptr;
+    if (adapters) {
+        args = adapter_args(*adapters);
+        ad = &args;
+    }
     int nblocks = build_batch(d, count, nullptr, b, kRowsPerWave);
     const size_t lds = (size_t)M * kChunkTiles * 4 * kQuadStride * 16;
     if (M == 1 && nblocks < kSmallLaunchBlocks && !gemv_products_on_matrix_cores(1)) {
         nblocks = build_batch(d, count, nullptr, b, 2);
-        hipLaunchKernelGGL(k_gemv_r2, dim3(nblocks), dim3(256), lds, s, b);
+        if (ad)
+            hipLaunchKernelGGL(k_gemv_r2_adapters, dim3(nblocks), dim3(256), lds, s, b, *ad);
+        else
+            hipLaunchKernelGGL(k_gemv_r2, dim3(nblocks), dim3(256), lds, s, b);
         return hipGetLastError();
     }
     switch (M) {
-    case 1: return launch_m<1>(b, nblocks, lds, s);
-    case 2: return launch_m<2>(b, nblocks, lds, s);
-    case 3: return launch_m<3>(b, nblocks, lds, s);
-    default: return launch_m<4>(b, nblocks, lds, s);
+    case 1: return launch_m<1>(b, ad, nblocks, lds, s);
+    case 2: return launch_m<2>(b, ad, nblocks, lds, s);
+    case 3: return launch_m<3>(b, ad, nblocks, lds, s);
+    default: return launch_m<4>(b, ad, nblocks, lds, s);
     }
 }
 

@@ -33,7 +33,9 @@
 // weights against x gathered at weak_idx), fp16 stores.
 #include <cstdlib>
 #include <cstring>
+#include <type_traits>
 
+#include "owq_adapters.h"
 #include "owq_decode.h"
 #include "owq_device.h"
 #include "owq_launch.h"
@@ -94,8 +96,10 @@ __device__ __forceinline__ void dma_x(__amdgpu_buffer_rsrc_t r, char* lds, int v
 // accumulators to group 0 through LDS. This cuts the chain of dependent chunks
 // of a block by S, so the blocks of long-row layers do not run on alone after
 // the others have finished.
-template <int U, int MC, int W, int S, int D>
-__global__ __launch_bounds__(64 * W * S) void k_mfv(MfvBatch b, int M)
+// ADP: low-rank adapters of the (only) layer in the epilogue.
+struct NoAdapters {};
+template <int U, int MC, int W, int S, int D, typename ADP>
+__global__ __launch_bounds__(64 * W * S) void k_mfv(MfvBatch b, int M, ADP ad)
 {
     using SH = MfvShape<U, MC>;
     constexpr int GC = SH::GC, RS = SH::RS, STAGE = SH::STAGE, PT = SH::PT;
@@ -302,6 +306,29 @@ __global__ __launch_bounds__(64 * W * S) void k_mfv(MfvBatch b, int M)
         }
     }
 
+    if constexpr (!std::is_same_v<ADP, NoAdapters>) {
+        const AdapterToken tk = adapter_token<4, 16>(ad, min(l16, M - 1), l16 < M, qd);
+        uint64_t left = __ballot(tk.id >= 0) & 0xffffu;
+        while (left != 0) {  // wave-uniform: once per distinct adapter among the tokens
+            const int id = __builtin_amdgcn_readlane(tk.id, __builtin_ctzll(left));
+            left &= ~__ballot(tk.id == id);
+            f32x4 hi = f32x4{0.0f, 0.0f, 0.0f, 0.0f}, lo = hi;
+            for (int c = 8 * qd; c < ad.rpad; c += 32) {
+                half8_t th, tl;
+                adapter_operand(tk, id, c, th, tl);
+                const half8_t w = adapter_weights(ad, id, N, brow + rloc, c);
+                hi = __builtin_amdgcn_mfma_f32_16x16x32_f16(th, w, hi, 0, 0, 0);
+                lo = __builtin_amdgcn_mfma_f32_16x16x32_f16(tl, w, lo, 0, 0, 0);
+            }
+            const float f = tk.id == id ? tk.f : 0.0f;
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                const float fr = __shfl(f, 4 * qd + r, 64);
+                acc[r] = fr != 0.0f ? acc[r] + fr * (hi[r] + lo[r]) : acc[r];
+            }
+        }
+    }
+
     // D element r of lane l: token 4 (l / 16) + r, row l % 16
     const int row = wave * 16 + l16;
     if (row < nb) {
@@ -315,9 +342,14 @@ __global__ __launch_bounds__(64 * W * S) void k_mfv(MfvBatch b, int M)
 }
 
 template <int U, int MC, int W, int S, int D>
-hipError_t launch_shape(const MfvBatch& b, int nblocks, int M, hipStream_t s)
+hipError_t launch_shape(const MfvBatch& b, int nblocks, int M, hipStream_t s, const AdapterDesc* ad)
 {
-    hipLaunchKernelGGL((k_mfv<U, MC, W, S, D>), dim3(nblocks), dim3(64 * W * S), 0, s, b, M);
+    if (ad)
+        hipLaunchKernelGGL((k_mfv<U, MC, W, S, D, AdapterArgs>), dim3(nblocks), dim3(64 * W * S), 0, s, b, M,
+                           adapter_args(*ad));
+    else
+        hipLaunchKernelGGL((k_mfv<U, MC, W, S, D, NoAdapters>), dim3(nblocks), dim3(64 * W * S), 0, s, b, M,
+                           NoAdapters{});
     return hipGetLastError();
 }
 
@@ -338,7 +370,7 @@ bool mfv_fits(int64_t M, int64_t K)
     return M >= 1 && M <= kMfvMaxM && M * K * 2 <= INT32_MAX;
 }
 
-hipError_t launch_mfv(const LinearDesc* d, int count, int M, hipStream_t s)
+hipError_t launch_mfv(const LinearDesc* d, int count, int M, hipStream_t s, const AdapterDesc* ad)
 {
     // layers with the longest rows first: their blocks run longest
     int order[kGemvMaxLayers];
@@ -376,14 +408,14 @@ hipError_t launch_mfv(const LinearDesc* d, int count, int M, hipStream_t s)
     // instead of four, 6 % faster); 16 tokens: two ahead (one ahead leaves more
     // waves but was 3-6 % slower)
     if (M <= 4)
-        return launch_shape<4, 4, 2, 2, 1>(b, nblocks, M, s);
+        return launch_shape<4, 4, 2, 2, 1>(b, nblocks, M, s, ad);
     // 5 to 8 tokens: 32-group chunks (whole cache lines of codes, see
     // kCodePolicy), two chunks ahead; 16-token stages of 32 groups would leave
     // one block per CU (32.7 against 32.2 us at M = 8 with 16-group chunks, 39 us
     // at M = 16 with one chunk ahead)
     if (M <= 8)
-        return launch_shape<8, 8, 4, 1, 2>(b, nblocks, M, s);
-    return launch_shape<4, 16, 4, 1, 2>(b, nblocks, M, s);
+        return launch_shape<8, 8, 4, 1, 2>(b, nblocks, M, s, ad);
+    return launch_shape<4, 16, 4, 1, 2>(b, nblocks, M, s, ad);
 }
 
 }  // namespace owq

@@ -96,7 +96,9 @@ constexpr int kGemvMaxLayers = 16;  // layers per batched GEMV launch
 
 // Decode GEMV over `count` layers (count <= kGemvMaxLayers), 1 <= M <= kGemvMaxM,
 // gemv_fits(M, K) for every layer.
-hipError_t launch_gemv(const LinearDesc* d, int count, int M, hipStream_t s);
+// ad: low-rank adapters added to layer 0's output (count == 1), or NULL.
+struct AdapterDesc;
+hipError_t launch_gemv(const LinearDesc* d, int count, int M, hipStream_t s, const AdapterDesc* ad = nullptr);
 // Tokens per GEMV launch for a layer of K columns (x of all tokens is staged in LDS).
 int gemv_max_tokens(int64_t K);
 bool gemv_fits(int64_t M, int64_t K);
@@ -106,7 +108,7 @@ bool gemv_fits(int64_t M, int64_t K);
 bool gemv_products_on_matrix_cores(int64_t M);
 // Matrix-core decode over `count` layers (count <= kGemvMaxLayers), 1 <= M <= kMfvMaxM.
 constexpr int kMfvMaxM = 16;
-hipError_t launch_mfv(const LinearDesc* d, int count, int M, hipStream_t s);
+hipError_t launch_mfv(const LinearDesc* d, int count, int M, hipStream_t s, const AdapterDesc* ad = nullptr);
 bool mfv_fits(int64_t M, int64_t K);
 // Decode kernel choice for M tokens: true = matrix-core decode (launch_mfv), false =
 // vector-ALU decode (launch_gemv). OWQ_DECODE=vector|matrix overrides (read per call).
@@ -120,11 +122,25 @@ hipError_t launch_pack_grouped(const uint16_t* W, int64_t N, int64_t K, const in
 // 1 <= M <= kGemvMaxM tokens; groups[l]: columns per scale group of layer l.
 hipError_t launch_gemv_grouped(const LinearDesc* d, const int64_t* groups, int count, int M, hipStream_t s);
 // Matrix-core GEMM for larger M.
-hipError_t launch_gemm(const LinearDesc& d, int64_t M, hipStream_t s);
+hipError_t launch_gemm(const LinearDesc& d, int64_t M, hipStream_t s, const AdapterDesc* ad = nullptr);
 
 // The linear on the latency-favoured form for any M: the GEMM from gemm_min_m()
 // tokens, else the decode kernels in token slices (api.cpp).
-hipError_t launch_linear_any(const LinearDesc& d, int64_t M, hipStream_t s);
+hipError_t launch_linear_any(const LinearDesc& d, int64_t M, hipStream_t s, const AdapterDesc* ad = nullptr);
+
+// Low-rank adapters beside a linear: t (fp32 [M][adapter_rpad(rank)], workspace)
+// by launch_adapter_shrink, then the linear's launchers with the adapters given.
+struct AdapterDesc {
+    const uint16_t* A;     // [count][rank][K]
+    const uint16_t* B;     // [count][N][rank]
+    const float* alpha;    // [count]
+    const int32_t* which;  // [M]
+    float* t;
+    int32_t count, rank;
+};
+constexpr int adapter_rpad(int rank) { return (rank + 31) & ~31; }
+size_t adapter_workspace_bytes(int rank, int64_t M);
+hipError_t launch_adapter_shrink(const AdapterDesc& a, const uint16_t* x, int64_t M, int64_t K, hipStream_t s);
 
 // ------------------------------------------------------ storage-favoured form --
 // Dense columns rounded up to whole groups; workspace bytes of the product.

@@ -49,6 +49,11 @@ class OwqGroupedLayer(ctypes.Structure):
                 ("weak_idx", _P), ("w_weak", _P)]
 
 
+class OwqAdapters(ctypes.Structure):
+    """Mirror of ``owq_adapters`` (host struct, device pointers)."""
+    _fields_ = [("A", _P), ("B", _P), ("alpha", _P), ("count", _I32), ("rank", _I32)]
+
+
 class OwqGrad(ctypes.Structure):
     """Mirror of ``owq_grad`` (host struct, device pointers)."""
     _fields_ = [("g", _P), ("out", _P), ("n", _I64), ("type", _I32)]
@@ -91,6 +96,9 @@ EXPORTS = {
     "owq_linear_grouped": (ctypes.c_int, [ctypes.POINTER(OwqGroupedLayer), _P, _I64, _P, _P]),
     "owq_linear_grouped_batched": (ctypes.c_int, [ctypes.POINTER(OwqGroupedLayer), ctypes.POINTER(_P),
                                                   ctypes.POINTER(_P), _I32, _I64, _P]),
+    "owq_linear_adapters_workspace_bytes": (ctypes.c_size_t, [_I32, _I64]),
+    "owq_linear_adapters": (ctypes.c_int, [ctypes.POINTER(OwqLayer), ctypes.POINTER(OwqAdapters), _P, _P, _I64, _P,
+                                           _P, ctypes.c_size_t, _P]),
     "owq_clip_grad_norm_workspace_bytes": (ctypes.c_size_t, [_I32]),
     "owq_clip_grad_norm": (ctypes.c_int, [ctypes.POINTER(OwqGrad), _I32, ctypes.c_double, _P, _P, ctypes.c_size_t,
                                           _P]),
@@ -947,6 +955,90 @@ class PreparedCalibrate:
         st = self.stream if self.stream is not None else _stream()
         _check(self.fn(self.items, self.n, self.ws, self.ws_bytes, st), "owq_calibrate_score_batched")
         return self.results
+
+
+# ------------------------------------- low-rank adapters of many requests
+
+
+def _layer_struct_on(layer: dict, tag: str = ""):
+    """(OwqLayer, GPU index) of a packed layer dict: layer_shapes' and _on_device's
+    checks in one pass over its tensors; a layer that fails goes through those, for
+    their message."""
+    try:
+        q, s, z = layer["qcodes"], layer["scales"], layer["zeros"]
+        w, idx = layer["w_weak"], layer["weak_idx"]
+        N, G, three = q.shape
+        k, = idx.shape
+        dev = q.get_device()
+        if (three == 3 and dev >= 0 and s.shape == (N,) and z.shape == (N,) and w.shape == (N, k)
+                and q.dtype is torch.int32 and idx.dtype is torch.int32 and z.dtype is torch.uint8
+                and s.dtype is torch.float16 and w.dtype is torch.float16
+                and q.is_contiguous() and s.is_contiguous() and z.is_contiguous() and w.is_contiguous()
+                and idx.is_contiguous() and s.get_device() == dev and z.get_device() == dev
+                and w.get_device() == dev and idx.get_device() == dev):
+            return OwqLayer(N, 32 * G, k, 3, q.data_ptr(), s.data_ptr(), z.data_ptr(),
+                            idx.data_ptr() if k else None, w.data_ptr() if k else None), dev
+    except (KeyError, AttributeError, ValueError, TypeError):
+        pass
+    try:
+        layer_shapes(layer)
+    except (TypeError, ValueError) as e:
+        raise type(e)(f"{tag}{e}") from None
+    _on_device(*_layer_named(layer, tag))
+    raise ValueError(f"{tag}layer is not a packed layer")
+
+
+def _same_device(index: int, *named):
+    """Every given (name, tensor) is on GPU `index`."""
+    for name, t in named:
+        if t is not None and t.get_device() != index:
+            _on_device((name, t))
+            raise ValueError(f"arguments are on different devices: {name} is on {t.device}, the layer on cuda:{index}")
+
+
+def linear_adapters_workspace_bytes(rank: int, M: int) -> int:
+    return int(lib().owq_linear_adapters_workspace_bytes(rank, M))
+
+
+def linear_adapters(layer: dict, adapters: dict, which: torch.Tensor, x: torch.Tensor, y: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y[m] = x[m] W^T + alpha_r (x[m] A_r^T) B_r^T with r = which[m]
+    (owq_linear_adapters): the shared packed layer and, per token, the low-rank
+    adapter of its request. adapters: dict of A fp16 [count][rank][K], B fp16
+    [count][N][rank] and alpha fp32 [count]; which: int32 [M], any value outside
+    [0, count) for none."""
+    q = layer.get("qcodes")
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        layer_shapes(layer)
+    N, K = q.shape[0], q.shape[1] * 32
+    M = _xy_shapes(N, K, x, y)
+    for name in ("A", "B", "alpha"):
+        if name not in adapters:
+            raise ValueError(f"adapters lacks {name!r}")
+    A, B, alpha = _meta(adapters["A"], torch.float16, "A"), adapters["B"], adapters["alpha"]
+    if A.dim() != 3 or A.shape[2] != K:
+        raise ValueError(f"A must be [count][rank][K = {K}], got {tuple(A.shape)}")
+    count, rank = A.shape[0], A.shape[1]
+    if count < 1 or not 1 <= rank <= 256:
+        raise ValueError(f"count = {count}, rank = {rank}: need at least one adapter and 1 <= rank <= 256")
+    _meta(B, torch.float16, "B", (count, N, rank))
+    _meta(alpha, torch.float32, "alpha", (count,))
+    _meta(which, torch.int32, "which", (M,))
+    if workspace is not None:
+        _meta(workspace, torch.uint8, "workspace")
+    L, dev = _layer_struct_on(layer)
+    _same_device(dev, ("x", x), ("y", y), ("A", A), ("B", B), ("alpha", alpha), ("which", which),
+                 ("workspace", workspace))
+    with _Launch(dev, stream) as run:
+        if y is None:
+            y = run.empty((M, N), torch.float16)
+        if workspace is None:
+            workspace = run.empty(linear_adapters_workspace_bytes(rank, M), torch.uint8)
+        ad = OwqAdapters(A.data_ptr(), B.data_ptr(), alpha.data_ptr(), count, rank)
+        _check(lib().owq_linear_adapters(ctypes.byref(L), ctypes.byref(ad), which.data_ptr(), x.data_ptr(), M,
+                                         y.data_ptr(), workspace.data_ptr(), workspace.numel(), run.handle),
+               "owq_linear_adapters")
+    return y
 
 
 # ---------------------------------------------------- gradient norm and clipping

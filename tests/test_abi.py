@@ -441,3 +441,36 @@ def test_clip_grad_norm_validation(lib):
     assert call([ok, (FAKE + 8, FAKE + 8192, 10, 1)]) == 3                # reads what another writes
     assert call([(FAKE, FAKE, 100, 0), (FAKE, FAKE + 8192, 100, 0)]) == 3  # reads what it writes elsewhere
     assert b"item 1" in lib.owq_last_error()
+
+
+def test_linear_adapters_validation(lib):
+    from mixed_precision_weight_amd.owq import OwqAdapters, OwqLayer
+    need = lib.owq_linear_adapters_workspace_bytes(16, 5)
+    assert need >= 16 * 5 * 4
+    assert lib.owq_linear_adapters_workspace_bytes(0, 5) == 0
+    assert lib.owq_linear_adapters_workspace_bytes(257, 5) == 0
+    assert lib.owq_linear_adapters_workspace_bytes(16, 0) == 0
+
+    def call(layer=None, ad=None, which=FAKE, x=FAKE, M=5, y=FAKE, ws=FAKE, size=need):
+        L = OwqLayer(64, 128, 4, 3, FAKE, FAKE, FAKE, FAKE, FAKE) if layer is None else layer
+        a = OwqAdapters(FAKE, FAKE, FAKE, 3, 16) if ad is None else ad
+        return lib.owq_linear_adapters(ctypes.byref(L), ctypes.byref(a), which, x, M, y, ws, size, None)
+
+    assert call(layer=OwqLayer(64, 100, 4, 3, FAKE, FAKE, FAKE, FAKE, FAKE)) == 2
+    assert call(layer=OwqLayer(64, 128, 4, 4, FAKE, FAKE, FAKE, FAKE, FAKE)) == 5
+    assert call(M=0) == 2
+    assert call(x=None) == 1
+    assert call(which=None) == 1
+    assert call(ws=None) == 1
+    assert call(ad=OwqAdapters(None, FAKE, FAKE, 3, 16)) == 1
+    assert call(ad=OwqAdapters(FAKE, None, FAKE, 3, 16)) == 1
+    assert call(ad=OwqAdapters(FAKE, FAKE, None, 3, 16)) == 1
+    assert call(ad=OwqAdapters(FAKE, FAKE, FAKE, 0, 16)) == 2
+    assert call(ad=OwqAdapters(FAKE, FAKE, FAKE, 3, 0)) == 2
+    assert call(ad=OwqAdapters(FAKE, FAKE, FAKE, 3, 257)) == 2
+    assert call(ad=OwqAdapters(FAKE + 8, FAKE, FAKE, 3, 16)) == 4
+    assert call(ad=OwqAdapters(FAKE, FAKE + 2, FAKE, 3, 16)) == 4
+    assert call(ad=OwqAdapters(FAKE, FAKE, FAKE + 2, 3, 16)) == 4
+    assert call(which=FAKE + 2) == 4
+    assert call(ws=FAKE + 16) == 4
+    assert call(size=need - 1) == 6

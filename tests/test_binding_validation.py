@@ -245,3 +245,38 @@ def test_clip_grad_norm_checks():
     with pytest.raises(TypeError, match="workspace"):
         owq.clip_grad_norm([a], 1.0, workspace=torch.zeros(64))
     _host_only(owq.clip_grad_norm, [a, b], 1.0)
+
+
+def test_linear_adapters_checks():
+    M, r, c = 5, 6, 3
+    x = torch.zeros((M, K), dtype=torch.float16)
+    ads = {"A": torch.zeros((c, r, K), dtype=torch.float16), "B": torch.zeros((c, N, r), dtype=torch.float16),
+           "alpha": torch.ones(c)}
+    which = torch.zeros(M, dtype=torch.int32)
+    with pytest.raises(ValueError, match="x has"):
+        owq.linear_adapters(_layer(), ads, which, x[:, :K - 32].contiguous())
+    with pytest.raises(ValueError, match="lacks 'alpha'"):
+        owq.linear_adapters(_layer(), {"A": ads["A"], "B": ads["B"]}, which, x)
+    with pytest.raises(ValueError, match="A must be"):
+        owq.linear_adapters(_layer(), {**ads, "A": ads["A"][0]}, which, x)
+    with pytest.raises(ValueError, match="rank"):
+        owq.linear_adapters(_layer(), {**ads, "A": torch.zeros((c, 257, K), dtype=torch.float16)}, which, x)
+    with pytest.raises(ValueError, match="at least one adapter"):
+        owq.linear_adapters(_layer(), {**ads, "A": ads["A"][:0]}, which, x)
+    with pytest.raises(ValueError, match="B has shape"):
+        owq.linear_adapters(_layer(), {**ads, "B": ads["B"][:, :-1].contiguous()}, which, x)
+    with pytest.raises(TypeError, match="alpha must be torch.float32"):
+        owq.linear_adapters(_layer(), {**ads, "alpha": ads["alpha"].half()}, which, x)
+    with pytest.raises(TypeError, match="which must be torch.int32"):
+        owq.linear_adapters(_layer(), ads, which.long(), x)
+    with pytest.raises(ValueError, match="which has shape"):
+        owq.linear_adapters(_layer(), ads, which[:-1], x)
+    with pytest.raises(ValueError, match="y has shape"):
+        owq.linear_adapters(_layer(), ads, which, x, y=torch.zeros((M, N - 1), dtype=torch.float16))
+    bad = _layer()
+    bad["scales"] = torch.zeros(N + 1, dtype=torch.float16)
+    with pytest.raises(ValueError, match="scales has shape"):
+        owq.linear_adapters(bad, ads, which, x)
+    with pytest.raises(ValueError, match="lacks 'qcodes'"):
+        owq.linear_adapters({}, ads, which, x)
+    _host_only(owq.linear_adapters, _layer(), ads, which, x)
