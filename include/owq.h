@@ -476,6 +476,32 @@ owq_status owq_linear_backward_batched(const owq_layer* Ls, const uint16_t* cons
                                        uint16_t* const* dxs, float* const* dws,
                                        void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------ gated feed-forward block --- */
+
+/* Activations of the gated block (s the logistic function, P the normal
+ * distribution function):
+ *   OWQ_ACT_SILU v s(v)      OWQ_ACT_GELU v P(v)      OWQ_ACT_RELU max(v, 0)
+ *   OWQ_ACT_GELU_TANH v s(2 sqrt(2/pi) (v + 0.044715 v^3)), the tanh form of gelu */
+typedef enum {
+    OWQ_ACT_SILU = 0,
+    OWQ_ACT_GELU = 1,
+    OWQ_ACT_GELU_TANH = 2,
+    OWQ_ACT_RELU = 3
+} owq_activation;
+
+/* The gated half of a feed-forward block (the gate and up linears of a LLaMA
+ * decoder layer) in one launch:
+ *   g = x Wg^T, u = x Wu^T,  h[m][i] = act(g[m][i]) u[m][i]
+ * each linear as owq_linear ([PL] "Real-device acceleration" (paper "Acceleration
+ * on Real Device", p.6)); activation and product on the fp32 sums, h rounded to
+ * fp16 once. gate, up: HOST pointers to packed layers of the same N and K (their
+ * weak columns may differ); x: fp16 [M][K]; h: fp16 [M][N] (output); g, u: fp32
+ * [M][N] outputs for owq_gated_backward, both or neither NULL. act: an
+ * owq_activation. Errors as owq_linear, plus OWQ_ERR_SHAPE for layers that do not
+ * match, OWQ_ERR_UNSUPPORTED for an unknown act, OWQ_ERR_NULL for one of g, u. */
+owq_status owq_gated(const owq_layer* gate, const owq_layer* up, const uint16_t* x, int64_t M, int32_t act,
+                     uint16_t* h, float* g, float* u, void* stream);
+
 /* ------------------------- low-rank adapters of many requests beside a layer --- */
 
 /* `count` low-rank adapters of one layer (HOST struct, device pointers). Adapters

@@ -130,6 +130,25 @@ owq::LinearDesc desc_of(const owq_layer* L, const uint16_t* x, uint16_t* y)
     return d;
 }
 
+// The two layers of a gated block, its input and an fp16 output.
+owq_status check_gated(const owq_layer* gate, const owq_layer* up, int64_t M, const uint16_t* x, const uint16_t* h,
+                       int32_t act, hipStream_t s)
+{
+    owq_status st = check_layer(gate, M, x, h);
+    if (st != OWQ_OK)
+        return fail_at(st, "layer", 0);
+    st = check_layer(up, M, x, h);
+    if (st != OWQ_OK)
+        return fail_at(st, "layer", 1);
+    if (gate->N != up->N || gate->K != up->K)
+        return fail(OWQ_ERR_SHAPE, "gate is %lld x %lld, up is %lld x %lld", (long long)gate->N, (long long)gate->K,
+                    (long long)up->N, (long long)up->K);
+    if (act < OWQ_ACT_SILU || act > OWQ_ACT_RELU)
+        return fail(OWQ_ERR_UNSUPPORTED, "act = %d is not an owq_activation", act);
+    st = check_idx_on_host(gate->weak_idx, gate->k, gate->K, s);
+    return st != OWQ_OK ? st : check_idx_on_host(up->weak_idx, up->k, up->K, s);
+}
+
 }  // namespace
 
 namespace owq {
@@ -808,6 +827,21 @@ owq_status owq_linear_batched(const owq_layer* Ls, const uint16_t* const* xs, ui
                 : owq::launch_gemv(d.data() + l0, n, (int)M, (hipStream_t)stream);
     }
     return hip_status(e, "owq_linear_batched launch");
+}
+
+owq_status owq_gated(const owq_layer* gate, const owq_layer* up, const uint16_t* x, int64_t M, int32_t act,
+                     uint16_t* h, float* g, float* u, void* stream)
+{
+    owq_status st = check_gated(gate, up, M, x, h, act, (hipStream_t)stream);
+    if (st != OWQ_OK)
+        return st;
+    if (!g != !u)
+        return fail(OWQ_ERR_NULL, "g and u must be given together");
+    if (!aligned(g, 4) || !aligned(u, 4))
+        return fail(OWQ_ERR_ALIGN, "misaligned pointer (g, u: 4 B)");
+    return hip_status(owq::launch_gated(desc_of(gate, x, nullptr), desc_of(up, x, nullptr), M, act, h, g, u,
+                                        (hipStream_t)stream),
+                      "owq_gated launch");
 }
 
 size_t owq_linear_adapters_workspace_bytes(int32_t rank, int64_t M)

@@ -186,6 +186,13 @@ hipError_t launch_pack_optq(const uint16_t* W, int64_t N, int64_t K, const uint1
                             const int32_t* idx, int32_t k, uint32_t* q, uint16_t* scales, uint8_t* zeros,
                             uint16_t* ww, void* ws, const OptqPlan& p, hipStream_t s);
 
+// ------------------------------------------------ gated feed-forward block --
+enum { kActSilu = 0, kActGelu = 1, kActGeluTanh = 2, kActRelu = 3 };
+// h = act(x Wg^T) * (x Wu^T) (fp16 [M][N]); g, u: the pre-activations (fp32 [M][N]), both or neither NULL.
+// x is gate.x.
+hipError_t launch_gated(const LinearDesc& gate, const LinearDesc& up, int64_t M, int act, uint16_t* h, float* g,
+                        float* u, hipStream_t s);
+
 // ------------------------------------------------- gradient norm and clipping --
 struct ClipEntry {
     const void* g;

@@ -96,6 +96,7 @@ EXPORTS = {
     "owq_linear_grouped": (ctypes.c_int, [ctypes.POINTER(OwqGroupedLayer), _P, _I64, _P, _P]),
     "owq_linear_grouped_batched": (ctypes.c_int, [ctypes.POINTER(OwqGroupedLayer), ctypes.POINTER(_P),
                                                   ctypes.POINTER(_P), _I32, _I64, _P]),
+    "owq_gated": (ctypes.c_int, [ctypes.POINTER(OwqLayer), ctypes.POINTER(OwqLayer), _P, _I64, _I32, _P, _P, _P, _P]),
     "owq_linear_adapters_workspace_bytes": (ctypes.c_size_t, [_I32, _I64]),
     "owq_linear_adapters": (ctypes.c_int, [ctypes.POINTER(OwqLayer), ctypes.POINTER(OwqAdapters), _P, _P, _I64, _P,
                                            _P, ctypes.c_size_t, _P]),
@@ -957,13 +958,14 @@ class PreparedCalibrate:
         return self.results
 
 
-# ------------------------------------- low-rank adapters of many requests
+# ---------------------------------------------------- gated feed-forward block
+
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}  # owq_activation
 
 
-def _layer_struct_on(layer: dict, tag: str = ""):
-    """(OwqLayer, GPU index) of a packed layer dict: layer_shapes' and _on_device's
-    checks in one pass over its tensors; a layer that fails goes through those, for
-    their message."""
+def _layer_fast(layer: dict):
+    """(OwqLayer, GPU index) of a packed layer dict that passes layer_shapes' and
+    _on_device's checks, which this makes in one pass over its tensors; else None."""
     try:
         q, s, z = layer["qcodes"], layer["scales"], layer["zeros"]
         w, idx = layer["w_weak"], layer["weak_idx"]
@@ -980,12 +982,22 @@ def _layer_struct_on(layer: dict, tag: str = ""):
                             idx.data_ptr() if k else None, w.data_ptr() if k else None), dev
     except (KeyError, AttributeError, ValueError, TypeError):
         pass
-    try:
-        layer_shapes(layer)
-    except (TypeError, ValueError) as e:
-        raise type(e)(f"{tag}{e}") from None
-    _on_device(*_layer_named(layer, tag))
-    raise ValueError(f"{tag}layer is not a packed layer")
+    return None
+
+
+def _layers_on(*tagged):
+    """(OwqLayer, ...) and the GPU index of (tag, packed layer dict) pairs on one
+    GPU; a layer that fails is reported as layer_shapes and _on_device report it."""
+    found = [_layer_fast(layer) for _, layer in tagged]
+    if None in found or len({dev for _, dev in found}) > 1:
+        for tag, layer in tagged:
+            try:
+                layer_shapes(layer)
+            except (TypeError, ValueError) as e:
+                raise type(e)(f"{tag}{e}") from None
+        _on_device(*[nt for tag, layer in tagged for nt in _layer_named(layer, tag)])
+        raise ValueError("not packed layers")
+    return [L for L, _ in found], found[0][1]
 
 
 def _same_device(index: int, *named):
@@ -994,6 +1006,49 @@ def _same_device(index: int, *named):
         if t is not None and t.get_device() != index:
             _on_device((name, t))
             raise ValueError(f"arguments are on different devices: {name} is on {t.device}, the layer on cuda:{index}")
+
+
+def _gated_args(gate: dict, up: dict, x, act: str):
+    """(OwqLayer of gate, OwqLayer of up, GPU index, M, act code) of a gated block."""
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act = {act!r}: need one of {sorted(ACTIVATIONS)}")
+    shapes = []
+    for tag, layer in (("gate: ", gate), ("up: ", up)):
+        q = layer.get("qcodes")
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            try:
+                layer_shapes(layer)
+            except (TypeError, ValueError) as e:
+                raise type(e)(f"{tag}{e}") from None
+        shapes.append((q.shape[0], 32 * q.shape[1]))
+    if shapes[0] != shapes[1]:
+        raise ValueError(f"gate is {shapes[0]}, up is {shapes[1]}: need the same (N, K)")
+    M = _xy_shapes(*shapes[0], x, None)
+    (Lg, Lu), dev = _layers_on(("gate: ", gate), ("up: ", up))
+    _same_device(dev, ("x", x))
+    return Lg, Lu, dev, M, ACTIVATIONS[act]
+
+
+def gated(gate: dict, up: dict, x: torch.Tensor, act: str = "silu", h: torch.Tensor | None = None, save: bool = False,
+          stream=None):
+    """h = act(x Wg^T) * (x Wu^T) (fp16 [M][N]) for two packed layers of one shape
+    (owq_gated); act: silu, gelu, gelu_tanh or relu. save: return (h, g, u) with the
+    fp32 pre-activations for gated_backward."""
+    if h is not None and isinstance(gate.get("qcodes"), torch.Tensor) and isinstance(x, torch.Tensor):
+        _meta(h, torch.float16, "h", (x.shape[0] if x.dim() == 2 else 1, gate["qcodes"].shape[0]))
+    Lg, Lu, dev, M, code = _gated_args(gate, up, x, act)
+    _same_device(dev, ("h", h))
+    with _Launch(dev, stream) as run:
+        if h is None:
+            h = run.empty((M, Lg.N), torch.float16)
+        g = run.empty((M, Lg.N), torch.float32) if save else None
+        u = run.empty((M, Lg.N), torch.float32) if save else None
+        _check(lib().owq_gated(ctypes.byref(Lg), ctypes.byref(Lu), x.data_ptr(), M, code, h.data_ptr(), _ptr(g),
+                               _ptr(u), run.handle), "owq_gated")
+    return (h, g, u) if save else h
+
+
+# ------------------------------------- low-rank adapters of many requests
 
 
 def linear_adapters_workspace_bytes(rank: int, M: int) -> int:
@@ -1026,7 +1081,7 @@ def linear_adapters(layer: dict, adapters: dict, which: torch.Tensor, x: torch.T
     _meta(which, torch.int32, "which", (M,))
     if workspace is not None:
         _meta(workspace, torch.uint8, "workspace")
-    L, dev = _layer_struct_on(layer)
+    (L,), dev = _layers_on(("", layer))
     _same_device(dev, ("x", x), ("y", y), ("A", A), ("B", B), ("alpha", alpha), ("which", which),
                  ("workspace", workspace))
     with _Launch(dev, stream) as run:

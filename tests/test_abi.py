@@ -474,3 +474,34 @@ def test_linear_adapters_validation(lib):
     assert call(which=FAKE + 2) == 4
     assert call(ws=FAKE + 16) == 4
     assert call(size=need - 1) == 6
+
+
+def test_gated_validation(lib):
+    from mixed_precision_weight_amd.owq import OwqLayer
+
+    def layer(N=64, K=128, k=4, bits=3, q=FAKE, idx=FAKE):
+        return OwqLayer(N, K, k, bits, q, FAKE, FAKE, idx, FAKE)
+
+    def call(gate=None, up=None, x=FAKE, M=5, act=0, h=FAKE, g=None, u=None):
+        a, b = gate or layer(), up or layer()
+        return lib.owq_gated(ctypes.byref(a), ctypes.byref(b), x, M, act, h, g, u, None)
+
+    a = layer()
+    assert lib.owq_gated(None, ctypes.byref(a), FAKE, 1, 0, FAKE, None, None, None) == 1
+    assert lib.owq_gated(ctypes.byref(a), None, FAKE, 1, 0, FAKE, None, None, None) == 1
+    assert call(x=None) == 1
+    assert call(h=None) == 1
+    assert call(M=0) == 2
+    assert call(gate=layer(bits=4)) == 5
+    assert call(up=layer(q=None)) == 1
+    assert b"layer 1" in lib.owq_last_error()
+    assert call(up=layer(idx=None)) == 1
+    assert call(up=layer(N=65)) == 2
+    assert call(up=layer(K=160)) == 2
+    assert call(gate=layer(k=129)) == 3
+    assert call(act=-1) == 5
+    assert call(act=4) == 5
+    assert call(g=FAKE) == 1
+    assert call(u=FAKE) == 1
+    assert call(g=FAKE + 2, u=FAKE) == 4
+    assert call(x=FAKE + 8) == 4

@@ -280,3 +280,26 @@ def test_linear_adapters_checks():
     with pytest.raises(ValueError, match="lacks 'qcodes'"):
         owq.linear_adapters({}, ads, which, x)
     _host_only(owq.linear_adapters, _layer(), ads, which, x)
+
+
+def test_gated_checks():
+    x = torch.zeros((5, K), dtype=torch.float16)
+    with pytest.raises(ValueError, match="act = 'swish'"):
+        owq.gated(_layer(), _layer(), x, act="swish")
+    with pytest.raises(ValueError, match="same"):
+        owq.gated(_layer(), _layer(N + 1), x)
+    with pytest.raises(ValueError, match="same"):
+        owq.gated(_layer(), _layer(K=K + 32), x)
+    with pytest.raises(ValueError, match="x has"):
+        owq.gated(_layer(), _layer(), torch.zeros((5, K + 32), dtype=torch.float16))
+    with pytest.raises(TypeError, match="x must be torch.float16"):
+        owq.gated(_layer(), _layer(), x.float())
+    with pytest.raises(ValueError, match="up: layer lacks"):
+        owq.gated(_layer(), {}, x)
+    bad = _layer()
+    bad["zeros"] = bad["zeros"][:-1]
+    with pytest.raises(ValueError, match="up: zeros has shape"):
+        owq.gated(_layer(), bad, x)
+    with pytest.raises(ValueError, match="h has shape"):
+        owq.gated(_layer(), _layer(), x, h=torch.zeros((5, N + 1), dtype=torch.float16))
+    _host_only(owq.gated, _layer(), _layer(k=0), x, save=True)

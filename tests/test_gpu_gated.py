@@ -1,0 +1,167 @@
+"""The gated half of a feed-forward block (owq_gated) on the GPU, against 64 bits.
+
+Tolerances. The products q - z times x are exact and summed in fp32. A chain of
+roundings of an output's sum is at most K / 4 + 64 long in every kernel (lanes or
+matrix instructions hold K / 128 partial sums at the least, the longest chain is
+the matrix cores' 8-element quarter steps taken one by one), so a pre-activation
+is within e = (K / 4 + 64) 2^-24 of its sum of absolute terms S. The slopes of
+all four activations stay below 1.13 and the activation itself is computed to
+2^-18, so with dg = e Sg and du = e Su
+  |h - ref| <= 1.13 dg (|u| + du) + |act(g)| du + 2^-18 |h| + 2^-11 |h| + 2^-25
+(the last two: half a step of fp16, half its smallest subnormal)."""
+import numpy as np
+import pytest
+
+import gated_util as gu
+from mixed_precision_weight_amd import synth
+from parity_util import dev, host
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def owq():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a HIP device"
+    from mixed_precision_weight_amd import owq as o
+    o.lib()
+    return o
+
+
+def make(owq, N, K, kg, ku, M, seed):
+    rng = np.random.default_rng(seed)
+    layers = []
+    for k in (kg, ku):
+        W = synth.random_layer(rng, N, K, 0.6 / np.sqrt(K))
+        if N > 2:
+            W[N // 2] = 0  # a row whose fit is degenerate
+        idx = np.sort(rng.choice(K, k, replace=False)).astype(np.int32)
+        layers.append(owq.pack(dev(W), dev(idx)))
+    x = rng.standard_normal((M, K)).astype(np.float32)
+    x[:, rng.choice(K, max(1, K // 200), replace=False)] *= 20.0
+    return layers[0], layers[1], x.astype(np.float16)
+
+
+def reference(gate, up, x, act):
+    x64 = x.astype(np.float64)
+    K = x.shape[1]
+    out = []
+    for layer in (gate, up):
+        W = gu.weights(layer)
+        out.append((x64 @ W.T, (K / 4 + 64) * 2.0 ** -24 * (np.abs(x64) @ np.abs(W).T)))
+    (g, dg), (u, du) = out
+    a, _ = gu.act(act, g)
+    h = a * u
+    tol = 1.13 * dg * (np.abs(u) + du) + np.abs(a) * du + (2.0 ** -18 + 2.0 ** -11) * np.abs(h) + 2.0 ** -25
+    return g, dg, u, du, h, tol
+
+
+def check(h, g, u, ref, what):
+    rg, dg, ru, du, rh, tol = ref
+    err = np.abs(host(h).astype(np.float64) - rh)
+    assert (err <= tol).all(), f"{what}: h exceeds its tolerance by {np.max(err - tol)}"
+    if g is not None:
+        assert (np.abs(host(g) - rg) <= dg + 1e-30).all(), f"{what}: g"
+        assert (np.abs(host(u) - ru) <= du + 1e-30).all(), f"{what}: u"
+
+
+CASES = [
+    # N, K, k gate, k up, M
+    (1, 32, 0, 1, 1),
+    (5, 32, 32, 0, 2),
+    (33, 96, 3, 5, 1),
+    (130, 4128, 7, 0, 1),
+    (66, 11008, 86, 221, 1),
+    (131, 8192, 130, 9, 2),
+    (67, 4096, 32, 32, 3),
+    (64, 96, 96, 1, 4),
+    (129, 1056, 9, 4, 5),
+    (65, 4128, 0, 0, 8),
+    (200, 640, 11, 12, 9),
+    (513, 2048, 6, 6, 16),
+    (127, 96, 2, 0, 17),
+    (130, 1056, 40, 3, 33),
+    (257, 512, 0, 7, 127),
+    (256, 4096, 32, 32, 128),
+    (300, 992, 9, 9, 129),
+    (140, 65536, 3, 3, 6),
+    (200, 800, 20, 1, 700),
+]
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_against_64_bits(owq, case):
+    import torch
+    N, K, kg, ku, M = case
+    gate, up, x = make(owq, *case, seed=sum(case))
+    for i, act in enumerate(("silu", "gelu", "gelu_tanh", "relu")):
+        ref = reference(gate, up, x, act)
+        print(f"gated: N={N} K={K} k={kg},{ku} M={M} {act}", flush=True)
+        # outputs inside larger buffers: nothing outside them is written
+        buf = torch.full((M * N + 256,), 7.0, dtype=torch.float16, device="cuda:0")
+        h = owq.gated(gate, up, dev(x), act=act, h=buf[128:128 + M * N].view(M, N))
+        hs, g, u = owq.gated(gate, up, dev(x), act=act, save=True)
+        torch.cuda.synchronize()
+        check(hs, g, u, ref, act)
+        assert host(h).tobytes() == host(hs).tobytes()
+        assert bool((buf[:128] == 7.0).all()) and bool((buf[128 + M * N:] == 7.0).all())
+
+
+def test_one_token_as_a_vector(owq):
+    gate, up, x = make(owq, 70, 256, 3, 2, 1, 4)
+    a, b = owq.gated(gate, up, dev(x)), owq.gated(gate, up, dev(x[0]))
+    assert host(a).tobytes() == host(b).tobytes()
+
+
+def test_far_out_pre_activations(owq):
+    """Pre-activations of hundreds to thousands: exp overflows, no NaN, the left tail goes to zero."""
+    for M in (1, 2, 7, 40, 130):
+        gate, up, x = make(owq, 40, 128, 2, 2, M, 8)
+        x = (x.astype(np.float32) * 1500).clip(-60000, 60000).astype(np.float16)
+        up["scales"].mul_(2.0 ** -9)
+        up["w_weak"].mul_(2.0 ** -9)
+        for act in ("silu", "gelu", "gelu_tanh", "relu"):
+            ref = reference(gate, up, x, act)
+            h, g, u = owq.gated(gate, up, dev(x), act=act, save=True)
+            check_finite = np.abs(ref[4]) < 65000
+            err = np.abs(host(h).astype(np.float64) - ref[4])
+            assert np.isfinite(host(g)).all() and not np.isnan(host(h).astype(np.float32)).any()
+            assert (err[check_finite] <= ref[5][check_finite]).all(), (M, act)
+
+
+def test_same_rows_for_every_token_count(owq):
+    """The tokens of a batch do not influence one another: each regime gives every token's
+    row within the tolerance of its own reference, and a batch's rows equal those of the
+    same batch with the other tokens changed."""
+    for M in (2, 5, 12, 30, 150):
+        gate, up, x = make(owq, 90, 320, 4, 4, M, M)
+        h = host(owq.gated(gate, up, dev(x)))
+        x2 = x.copy()
+        x2[1:] = 60000.0
+        x2[-1, 0] = np.inf
+        h2 = host(owq.gated(gate, up, dev(x2)))
+        assert h[0].tobytes() == h2[0].tobytes(), M
+
+
+def test_graph_and_other_stream(owq):
+    import torch
+    for M in (1, 2, 4, 9, 40, 200):
+        gate, up, x = make(owq, 100, 512, 6, 5, M, M + 1)
+        xd = dev(x)
+        eager = host(owq.gated(gate, up, xd)).copy()
+        torch.cuda.synchronize()
+        h = torch.zeros((M, 100), dtype=torch.float16, device="cuda:0")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            owq.gated(gate, up, xd, h=h)
+        for rep in range(3):
+            h.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert host(h).tobytes() == eager.tobytes()
+            assert host(owq.gated(gate, up, xd)).tobytes() == eager.tobytes()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        z = owq.gated(gate, up, xd, stream=side)
+        side.synchronize()
+        assert host(z).tobytes() == eager.tobytes()
