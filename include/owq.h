@@ -502,6 +502,32 @@ typedef enum {
 owq_status owq_gated(const owq_layer* gate, const owq_layer* up, const uint16_t* x, int64_t M, int32_t act,
                      uint16_t* h, float* g, float* u, void* stream);
 
+/* Bytes of device workspace owq_gated_backward needs (0 for sizes outside its
+ * range): mostly 4 M N for the scaled gradients, plus partial sums. */
+size_t owq_gated_backward_workspace_bytes(int64_t N, int64_t K, int32_t k_gate, int32_t k_up, int64_t M);
+
+/* Backward of owq_gated for Weak Column Tuning ([PL] "Weak Column Tuning" (paper
+ * "PEFT with Weak Column Tuning", p.5), as owq_linear_backward): with da = dh u
+ * act'(g), db = dh act(g) (fp32) and Wg, Wu the dequantised layers with their weak
+ * columns,
+ *   dx[m][j]        = sum_i da[m][i] Wg[i][j] + db[m][i] Wu[i][j]     fp16 [M][K]
+ *   dw_gate[i][c]   = sum_m da[m][i] x[m][idx_gate[c]]                fp32 [N][k gate]
+ *   dw_up[i][c]     = sum_m db[m][i] x[m][idx_up[c]]                  fp32 [N][k up]
+ * g, u: the fp32 [M][N] pre-activations owq_gated kept; x: fp16 [M][K], read only
+ * for the weak gradients (may be NULL without them); dh: fp16 [M][N]. dx, dw_gate,
+ * dw_up: outputs, each may be NULL. dw and the weak columns' part of dx are fp32
+ * sums of fp32 products. In the dense part of dx, s da and s db are rounded to fp16
+ * after scaling each token by a power of two (11 bits of every term that is not
+ * below 2^-28 of the token's largest; no term overflows), the products with q - z
+ * are exact and the sums fp32; relu's slope at 0 is 0. Bitwise deterministic.
+ * workspace: >= owq_gated_backward_workspace_bytes(...) bytes, 256-byte aligned,
+ * contents ignored; calls sharing it must be ordered. M, N <= 2^20. Errors as
+ * owq_gated, plus OWQ_ERR_WORKSPACE. */
+owq_status owq_gated_backward(const owq_layer* gate, const owq_layer* up, const uint16_t* x, const float* g,
+                              const float* u, const uint16_t* dh, int64_t M, int32_t act, uint16_t* dx,
+                              float* dw_gate, float* dw_up, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
 /* ------------------------- low-rank adapters of many requests beside a layer --- */
 
 /* `count` low-rank adapters of one layer (HOST struct, device pointers). Adapters

@@ -33,7 +33,8 @@ RESOURCES = os.path.join(BUILD, "kernel_resources.json")
 _REMARK = re.compile(r"remark: +(Function Name|TotalSGPRs|VGPRs|AGPRs|ScratchSize \[bytes/lane\]|"
                      r"Occupancy \[waves/SIMD\]|SGPRs Spill|VGPRs Spill|LDS Size \[bytes/block\]): (\S+)")
 SOURCES = ["api.cpp", "calib.hip", "topk.hip", "pack.hip", "search.hip", "storage.hip", "backward.hip", "optq.hip",
-           "gemv.hip", "mfv.hip", "gemm.hip", "stream.hip", "grouped.hip", "adapters.hip", "gated.hip", "clip.hip"]
+           "gemv.hip", "mfv.hip", "gemm.hip", "stream.hip", "grouped.hip", "adapters.hip", "gated.hip", "gated_backward.hip",
+           "clip.hip"]
 
 
 def _resources(stderr: str) -> dict:

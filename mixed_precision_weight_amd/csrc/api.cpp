@@ -844,6 +844,45 @@ owq_status owq_gated(const owq_layer* gate, const owq_layer* up, const uint16_t*
                       "owq_gated launch");
 }
 
+size_t owq_gated_backward_workspace_bytes(int64_t N, int64_t K, int32_t k_gate, int32_t k_up, int64_t M)
+{
+    if (N < 1 || N > owq::kGatedBwdMax || M < 1 || M > owq::kGatedBwdMax || K < 32 || K > kMaxK || K % 32 != 0 ||
+        k_gate < 0 || k_gate > K || k_up < 0 || k_up > K)
+        return 0;
+    return owq::gated_bwd_workspace_bytes(N, K, k_gate, k_up, M);
+}
+
+owq_status owq_gated_backward(const owq_layer* gate, const owq_layer* up, const uint16_t* x, const float* g,
+                              const float* u, const uint16_t* dh, int64_t M, int32_t act, uint16_t* dx,
+                              float* dw_gate, float* dw_up, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (!gate || !up)
+        return fail(OWQ_ERR_NULL, "layer is NULL");
+    const bool need_x = (dw_gate && gate->k > 0) || (dw_up && up->k > 0);
+    if (!g || !u || !dh || !workspace || (need_x && !x))
+        return fail(OWQ_ERR_NULL, "g, u, dh and workspace (and x for the weak gradients) must be non-NULL");
+    // check_layer wants an x and an output: x is checked below when it is read
+    owq_status st = check_gated(gate, up, M, reinterpret_cast<const uint16_t*>(workspace), dh, act,
+                                (hipStream_t)stream);
+    if (st != OWQ_OK)
+        return st;
+    if (M > owq::kGatedBwdMax || gate->N > owq::kGatedBwdMax)
+        return fail(OWQ_ERR_SHAPE, "M = %lld, N = %lld: need at most 2^20", (long long)M, (long long)gate->N);
+    if (!aligned(g, 4) || !aligned(u, 4) || !aligned(dh, 2) || !aligned(dx, 2) || !aligned(dw_gate, 4) ||
+        !aligned(dw_up, 4) || (need_x && !aligned(x, 16)) || !aligned(workspace, 256))
+        return fail(OWQ_ERR_ALIGN, "misaligned pointer (x: 16 B, g, u, dw: 4 B, dh, dx: 2 B, workspace: 256 B)");
+    const size_t need = owq::gated_bwd_workspace_bytes(gate->N, gate->K, gate->k, up->k, M);
+    if (workspace_bytes < need)
+        return fail(OWQ_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", workspace_bytes, need);
+    if (!dx && !need_x) {  // nothing to compute
+        g_err[0] = '\0';
+        return OWQ_OK;
+    }
+    return hip_status(owq::launch_gated_backward(desc_of(gate, x, nullptr), desc_of(up, x, nullptr), M, act, g, u, dh,
+                                                 dx, dw_gate, dw_up, workspace, (hipStream_t)stream),
+                      "owq_gated_backward launch");
+}
+
 size_t owq_linear_adapters_workspace_bytes(int32_t rank, int64_t M)
 {
     if (rank < 1 || rank > kMaxRank || M < 1 || M > INT32_MAX)

@@ -1,0 +1,786 @@
+// gated_backward.hip -- backward of the gated feed-forward block (gfx950).
+//
+// For h = act(g) u, g = x Wg^T, u = x Wu^T, upstream dh and the kept fp32 g, u:
+//   da = dh u act'(g),  db = dh act(g)                       fp32, never stored
+//   dx[m][j]    = sum_i da[m][i] Wg[i][j] + db[m][i] Wu[i][j]        fp16
+//   dw_g[i][c]  = sum_m da[m][i] x[m][idx_g[c]],  dw_u likewise      fp32
+// with W the dequantised dense matrix (0 at the weak columns) plus the weak
+// columns, the only trained part.
+//
+// dx is one product over the 2 N rows of both layers, on the fp16 matrix cores:
+// W = s (q - z) splits into the exact small integers q - z (fp16, decoded from the
+// codes) and A = 2^e_m s_i da[m][i], rounded to fp16 with a power of two per token
+// that puts the token's largest |s da|, |s db| into [2^14, 2^15): 11 bits of every
+// term that matters, whatever the gradient's scale, and no overflow. (The rounding
+// is the one a caller who stored da as fp16 would make, without its range. Split
+// into two fp16 values it would double the matrix work for an fp16 result.) The
+// weak columns' part, da w_weak, is a product over the rows in fp32, and so is dw,
+// over the tokens (v_mfma_f32_32x32x2_f32): their results are not limited by fp16.
+//
+// Launches:
+//  1 k_gated_tok   per 32 tokens and a slab of rows: da, db; each token's largest
+//                  |s da|, |s db|; the weak columns' part of dx per slab
+//  2 k_gated_rows  per 64 rows and a slab of tokens: da, db again (two elementwise
+//                  passes read less than storing da, db in fp32 would move); dw;
+//                  A written as [M][2 Np] fp16; the slabs of 1 added up
+//  3 k_gated_dx    the product; splits the rows where tokens and columns alone
+//                  do not fill the GPU
+//  4 k_gated_fin   adds the splits' and the token slabs' partial sums, in order
+// Every sum's order is fixed, so results are deterministic.
+#include "owq_act.h"
+#include "owq_decode.h"
+#include "owq_device.h"
+#include "owq_launch.h"
+
+namespace owq {
+
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+// vectors in rows of any length: element-aligned
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef float f32x2u __attribute__((ext_vector_type(2), aligned(4)));
+typedef uint16_t u16x8u __attribute__((ext_vector_type(8), aligned(2)));
+typedef uint16_t u16x2u __attribute__((ext_vector_type(2), aligned(2)));
+
+struct BwdLayer {
+    const uint32_t* q;
+    const uint16_t* s;
+    const uint8_t* z;
+    const int32_t* idx;
+    const uint16_t* ww;
+    float* dw;    // [N][k], NULL: not wanted
+    float* PD;    // token slabs' partials [tslabs][N][k] (tslabs > 1)
+    int32_t* map; // [K]: the weak column's position, -1 for a dense column
+    int32_t k;
+};
+
+struct GatedBwdArgs {
+    BwdLayer L[2];
+    const uint16_t* x;
+    const float* g;
+    const float* u;
+    const uint16_t* dh;
+    uint16_t* dx;     // NULL: not wanted
+    int32_t* texp;    // [M]: A is scaled by 2^texp
+    float* slabmax;   // [slabs][M]
+    float* PW;        // [slabs][M][kt], kt = k gate + k up
+    float* PWs;       // [M][kt]
+    uint16_t* A;      // [M][2 Np]
+    float* P;         // [split][M][K] (split > 1)
+    int32_t M, N, K, Np;
+    int32_t slabs, slab_rows;      // launch 1
+    int32_t tslabs, slab_tokens;   // launch 2
+    int32_t split, split_steps;    // launch 3
+    int32_t work_blocks, mtiles;
+};
+
+__device__ __forceinline__ f32x16 zero16()
+{
+    f32x16 z;
+#pragma unroll
+    for (int r = 0; r < 16; r++)
+        z[r] = 0.0f;
+    return z;
+}
+
+// ------------------------------------------------------------------- launch 1
+// A wave: 32 tokens (lane l: token l % 32) x one slab of rows, 16 rows per step
+// (lane half h: rows 8 h .. 8 h + 7, consecutive in memory). The matrix cores'
+// k index is the row: step element e pairs da of row 8 h + e with w_weak of that
+// row and column l % 32.
+struct TokRows {
+    float g[8], u[8];
+    uint32_t d[8];
+};
+
+__device__ __forceinline__ void load_tok_rows(const GatedBwdArgs& a, int64_t o, int row, TokRows& t)
+{
+    if (row + 8 <= a.N) {
+#pragma unroll
+        for (int v = 0; v < 8; v += 4) {
+            const f32x4u gv = *reinterpret_cast<const f32x4u*>(a.g + o + row + v);
+            const f32x4u uv = *reinterpret_cast<const f32x4u*>(a.u + o + row + v);
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                t.g[v + e] = gv[e];
+                t.u[v + e] = uv[e];
+            }
+        }
+        const u16x8u dv = *reinterpret_cast<const u16x8u*>(a.dh + o + row);
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            t.d[e] = dv[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const int r = min(row + e, a.N - 1);
+            t.g[e] = a.g[o + r];
+            t.u[e] = a.u[o + r];
+            t.d[e] = a.dh[o + r];
+        }
+    }
+}
+
+template <int ACT>
+__device__ __forceinline__ void tok_slab(const GatedBwdArgs& a, int tile, int slab, int wt)
+{
+    const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+    const int m = tile * 32 + l32;
+    const bool live = m < a.M;
+    const int64_t o = (int64_t)min(m, a.M - 1) * a.N;
+    const int r0 = slab * a.slab_rows, r1 = min(a.N, r0 + a.slab_rows);
+    const int c = wt * 32 + l32;  // weak column
+    const bool on[2] = {wt * 32 < a.L[0].k, wt * 32 < a.L[1].k};  // uniform
+    f32x16 acc[2] = {zero16(), zero16()};
+    float mx = 0.0f;
+    TokRows cur;
+    load_tok_rows(a, o, min(r0 + 8 * h, a.N - 1), cur);
+    for (int r = r0; r < r1; r += 16) {
+        TokRows nxt;
+        load_tok_rows(a, o, min(r + 16 + 8 * h, a.N - 1), nxt);
+        const int rb = r + 8 * h;
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const int row = min(rb + e, a.N - 1);
+            const bool use = live && rb + e < r1;
+            float v, d;
+            act_both<ACT>(cur.g[e], v, d);
+            const float dh = h2f((uint16_t)cur.d[e]);
+            const float da = use ? dh * cur.u[e] * d : 0.0f, db = use ? dh * v : 0.0f;
+            if (wt == 0)  // uniform
+                mx = fmaxf(mx, fmaxf(fabsf(h2f(a.L[0].s[row]) * da), fabsf(h2f(a.L[1].s[row]) * db)));
+#pragma unroll
+            for (int l = 0; l < 2; l++)
+                if (on[l]) {
+                    const int k = a.L[l].k;
+                    const float w = h2f(a.L[l].ww[(int64_t)row * k + min(c, k - 1)]);
+                    acc[l] = __builtin_amdgcn_mfma_f32_32x32x2f32(l ? db : da, w, acc[l], 0, 0, 0);
+                }
+        }
+        cur = nxt;
+    }
+    if (wt == 0) {
+        mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+        if (h == 0 && live)
+            a.slabmax[(int64_t)slab * a.M + m] = mx;
+    }
+    const int kt = a.L[0].k + a.L[1].k;
+#pragma unroll
+    for (int l = 0; l < 2; l++)
+        if (c < a.L[l].k)
+#pragma unroll
+            for (int r = 0; r < 16; r++) {
+                const int t = tile * 32 + 8 * (r >> 2) + 4 * h + (r & 3);
+                if (t < a.M)
+                    a.PW[((int64_t)slab * a.M + t) * kt + (l ? a.L[0].k : 0) + c] = acc[l][r];
+            }
+}
+
+// blocks [0, work_blocks): waves over (token tile, slab); the rest (first row of
+// the grid only): the map from columns to weak columns
+template <int ACT>
+__global__ __launch_bounds__(256) void k_gated_tok(const GatedBwdArgs a)
+{
+    if ((int)blockIdx.x >= a.work_blocks) {
+        const int j = ((int)blockIdx.x - a.work_blocks) * 256 + (int)threadIdx.x;
+        if (blockIdx.y != 0 || j >= a.K)
+            return;
+        for (int l = 0; l < 2; l++) {
+            int lo = 0, hi = a.L[l].k;  // first position whose column is >= j
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (a.L[l].idx[mid] < j)
+                    lo = mid + 1;
+                else
+                    hi = mid;
+            }
+            a.L[l].map[j] = lo < a.L[l].k && a.L[l].idx[lo] == j ? lo : -1;
+        }
+        return;
+    }
+    const int w = (int)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int tiles = (a.M + 31) >> 5;
+    if (w >= tiles * a.slabs)
+        return;
+    tok_slab<ACT>(a, w % tiles, w / tiles, (int)blockIdx.y);
+}
+
+// ------------------------------------------------------------------- launch 2
+// A block: 64 rows (lane l: rows 2 (l % 32), + 1) x one slab of tokens, its 4
+// waves taking pairs of tokens in turn (lane half h: token of the pair). The
+// matrix cores' k index is the token: da of row 2 (l % 32) + e against x at weak
+// column l % 32. The waves' sums are added in order in LDS.
+constexpr int kTokFlight = 4;  // pairs of tokens whose loads are in flight together
+
+__device__ __forceinline__ int scale_exp(float mx)
+{
+    return mx > 0.0f && mx < 0x1p120f ? 15 - __builtin_amdgcn_frexp_expf(mx) : 0;
+}
+
+template <int ACT>
+__device__ __forceinline__ void row_slab(const GatedBwdArgs& a, int tile, int slab, int wt, float* red, int* texp)
+{
+    const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int t0 = slab * a.slab_tokens, t1 = min(a.M, t0 + a.slab_tokens);
+    const int row = tile * 64 + 2 * l32;
+    const bool conv = a.dx && wt == 0;  // this block writes A
+    const bool on[2] = {a.L[0].dw && wt * 32 < a.L[0].k, a.L[1].dw && wt * 32 < a.L[1].k};
+    const int rc[2] = {min(row, a.N - 1), min(row + 1, a.N - 1)};
+    float sc[2][2];
+    int jw[2];
+#pragma unroll
+    for (int l = 0; l < 2; l++) {
+        sc[l][0] = h2f(a.L[l].s[rc[0]]);
+        sc[l][1] = h2f(a.L[l].s[rc[1]]);
+        int j = 0;
+        if (on[l])
+            j = a.L[l].idx[min(wt * 32 + l32, a.L[l].k - 1)];
+        jw[l] = j >= 0 && j < a.K ? j : 0;
+    }
+    f32x16 acc[2][2] = {{zero16(), zero16()}, {zero16(), zero16()}};
+    for (int tb = t0; tb < t1; tb += 256) {
+        const int tn = min(256, t1 - tb);
+        if (conv) {  // uniform
+            __syncthreads();  // the previous tokens' exponents are no longer read
+            if (tid < tn) {
+                float mx = 0.0f;
+                for (int s = 0; s < a.slabs; s++)
+                    mx = fmaxf(mx, a.slabmax[(int64_t)s * a.M + tb + tid]);
+                const int e = scale_exp(mx);
+                texp[tid] = e;
+                if (tile == 0)
+                    a.texp[tb + tid] = e;
+            }
+            __syncthreads();
+        }
+        for (int p = wave; p < (tn + 1) / 2; p += 4 * kTokFlight) {
+            float g[kTokFlight][2], u[kTokFlight][2];
+            uint32_t d[kTokFlight][2], xw[kTokFlight][2];
+#pragma unroll
+            for (int v = 0; v < kTokFlight; v++) {
+                const int64_t m = tb + min(2 * (p + 4 * v) + h, tn - 1);
+                const int64_t o = m * a.N;
+                if (rc[1] == row + 1) {
+                    const f32x2u gv = *reinterpret_cast<const f32x2u*>(a.g + o + row);
+                    const f32x2u uv = *reinterpret_cast<const f32x2u*>(a.u + o + row);
+                    const u16x2u dv = *reinterpret_cast<const u16x2u*>(a.dh + o + row);
+                    g[v][0] = gv[0], g[v][1] = gv[1], u[v][0] = uv[0], u[v][1] = uv[1];
+                    d[v][0] = dv[0], d[v][1] = dv[1];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        g[v][e] = a.g[o + rc[e]];
+                        u[v][e] = a.u[o + rc[e]];
+                        d[v][e] = a.dh[o + rc[e]];
+                    }
+                }
+#pragma unroll
+                for (int l = 0; l < 2; l++)
+                    xw[v][l] = on[l] ? a.x[m * a.K + jw[l]] : 0;
+            }
+#pragma unroll
+            for (int v = 0; v < kTokFlight; v++) {
+                const int t = 2 * (p + 4 * v) + h;
+                if (2 * (p + 4 * v) >= tn)  // uniform
+                    break;
+                float dab[2][2];
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const bool use = t < tn && row + e < a.N;
+                    float va, sl;
+                    act_both<ACT>(g[v][e], va, sl);
+                    const float dh = h2f((uint16_t)d[v][e]);
+                    dab[0][e] = use ? dh * u[v][e] * sl : 0.0f;
+                    dab[1][e] = use ? dh * va : 0.0f;
+                }
+                if (conv && t < tn && row < a.Np) {
+                    const int e = texp[t];
+                    uint16_t* dst = a.A + (int64_t)(tb + t) * 2 * a.Np + row;
+#pragma unroll
+                    for (int l = 0; l < 2; l++) {
+                        const uint32_t lo = f2h(__builtin_amdgcn_ldexpf(dab[l][0] * sc[l][0], e));
+                        const uint32_t hi = f2h(__builtin_amdgcn_ldexpf(dab[l][1] * sc[l][1], e));
+                        *reinterpret_cast<uint32_t*>(dst + l * a.Np) = lo | (hi << 16);
+                    }
+                }
+#pragma unroll
+                for (int l = 0; l < 2; l++)
+                    if (on[l]) {
+                        const float xv = h2f((uint16_t)xw[v][l]);
+#pragma unroll
+                        for (int e = 0; e < 2; e++)
+                            acc[l][e] = __builtin_amdgcn_mfma_f32_32x32x2f32(dab[l][e], xv, acc[l][e], 0, 0, 0);
+                    }
+            }
+        }
+    }
+    // D element r of lane l: row 2 (8 (r / 4) + 4 h + r % 4) + e, weak column l % 32
+#pragma unroll
+    for (int l = 0; l < 2; l++) {
+        if (!on[l])
+            continue;
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            __syncthreads();
+            if (wave > 0)
+#pragma unroll
+                for (int r = 0; r < 16; r++)
+                    red[((wave - 1) * 16 + r) * 64 + lane] = acc[l][e][r];
+            __syncthreads();
+            if (wave == 0)
+#pragma unroll
+                for (int r = 0; r < 16; r++) {
+                    const float v = ((acc[l][e][r] + red[r * 64 + lane]) + red[(16 + r) * 64 + lane]) +
+                                    red[(32 + r) * 64 + lane];
+                    const int i = tile * 64 + 2 * (8 * (r >> 2) + 4 * h + (r & 3)) + e;
+                    const int c = wt * 32 + l32;
+                    if (i < a.N && c < a.L[l].k) {
+                        const int64_t at = (int64_t)i * a.L[l].k + c;
+                        if (a.tslabs > 1)
+                            a.L[l].PD[(int64_t)slab * a.N * a.L[l].k + at] = v;
+                        else
+                            a.L[l].dw[at] = v;
+                    }
+                }
+        }
+    }
+}
+
+// blocks [0, work_blocks): (row tile, token slab); the rest (first row of the grid
+// only): the sums over the slabs of launch 1
+template <int ACT>
+__global__ __launch_bounds__(256) void k_gated_rows(const GatedBwdArgs a)
+{
+    __shared__ float red[48 * 64];
+    __shared__ int texp[256];
+    const int b = blockIdx.x;
+    if (b >= a.work_blocks) {
+        const int64_t n = (int64_t)a.M * (a.L[0].k + a.L[1].k);
+        const int64_t e = (int64_t)(b - a.work_blocks) * 256 + threadIdx.x;
+        if (blockIdx.y != 0 || e >= n)
+            return;
+        float t = 0.0f;
+        for (int s = 0; s < a.slabs; s++)
+            t += a.PW[s * n + e];
+        a.PWs[e] = t;
+        return;
+    }
+    const int tiles = (a.Np + 63) / 64;
+    row_slab<ACT>(a, b % tiles, b / tiles, (int)blockIdx.y, red, texp);
+}
+
+// ------------------------------------------------------------------- launch 3
+// dx: D[m][j] = sum over r < 2 Np of A[m][r] (q - z)[r][j], rows of gate, then of
+// up. A block owns BM tokens x BN columns and steps of RS rows: thread t decodes
+// one 32-column group of one row into the LDS tile [row][column] (exact fp16), the
+// A tile comes by direct-to-LDS loads two steps ahead. v_mfma_f32_32x32x16_f16
+// takes 8 consecutive rows per lane: contiguous for A; for the decoded tile the
+// transposing LDS read (ds_read_b64_tr_b16: in 16 lanes, lane i receives element i
+// of four rows of 16 columns) gives 4 rows of the lane's column. Tile rows are
+// padded to 64 bytes past a multiple of 256, so the four rows of a read lie in
+// distinct banks.
+template <int FM, int FN, int WM, int WN, int RS>
+struct DxTile {
+    static constexpr int NT = 64 * WM * WN;
+    static constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN;
+    static constexpr int BROW = BN * 2 + 64;         // LDS bytes of a decoded row
+    static constexpr int AROW = RS * 2;              // LDS bytes of a token's rows
+    static constexpr int PIECES = AROW / 16;         // 4 or 8
+    static constexpr int ASTAGE = BM * AROW;
+    static constexpr int DPW = ASTAGE / 16 / NT;     // 16-byte units per thread and step
+    static_assert(RS * (BN / 32) == NT, "one group per thread and step");
+    static_assert(ASTAGE % (16 * NT) == 0, "an A stage must split evenly over the threads");
+    static_assert((BN * 2) % 256 == 0, "tile rows 64 bytes apart modulo the banks");
+};
+
+__device__ __forceinline__ int a_swizzle(int pieces, int token)
+{
+    return pieces == 8 ? (token >> 1) & 7 : (token >> 2) & 3;
+}
+
+__device__ __forceinline__ void dma_a(__amdgpu_buffer_rsrc_t r, char* lds, int voff)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff, 0, 0, 0);
+}
+
+// four rows of this lane's column from each of two places in the decoded tile
+__device__ __forceinline__ half8_t read_columns(const char* a, const char* b)
+{
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)a);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)b);
+    return __builtin_bit_cast(half8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+template <int FM, int FN, int WM, int WN, int RS>
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2))) void k_gated_dx(const GatedBwdArgs a)
+{
+    using T = DxTile<FM, FN, WM, WN, RS>;
+    __shared__ __attribute__((aligned(1024))) char as0[T::ASTAGE];
+    __shared__ __attribute__((aligned(1024))) char as1[T::ASTAGE];
+    __shared__ __attribute__((aligned(1024))) char as2[T::ASTAGE];
+    __shared__ __attribute__((aligned(1024))) char bs[2][RS * T::BROW];
+
+    const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+    const int K = a.K, G = K >> 5, M = a.M, N = a.N, Np = a.Np;
+    const int ctiles = (K + T::BN - 1) / T::BN;
+    const int b = blockIdx.x;
+    const int m0 = (b % a.mtiles) * T::BM;
+    const int j0 = (b / a.mtiles % ctiles) * T::BN;
+    const int sp = b / (a.mtiles * ctiles);
+    const int mv = min(T::BM, M - m0);
+    const int steps = 2 * Np / RS;
+    const int st0 = sp * a.split_steps, st1 = min(steps, st0 + a.split_steps);
+
+    // A: unit n of a stage is slot n % PIECES of token n / PIECES, holding piece
+    // slot ^ swizzle; tokens past M repeat the last one (not stored). The range
+    // check covers the block's tokens; steps past the end read zeros.
+    const __amdgpu_buffer_rsrc_t ar = __builtin_amdgcn_make_buffer_rsrc(
+        a.A + (int64_t)m0 * 2 * Np, (short)0, (int)((int64_t)mv * 2 * Np * 2), 0x00020000);
+    int asrc[T::DPW];
+#pragma unroll
+    for (int t = 0; t < T::DPW; t++) {
+        const int n = (wave * T::DPW + t) * 64 + lane;
+        const int tok = n / T::PIECES, piece = (n % T::PIECES) ^ a_swizzle(T::PIECES, tok);
+        asrc[t] = min(tok, mv - 1) * 2 * Np * 2 + piece * 16;
+    }
+    auto dma = [&](int st, char* stage) {
+        const int off = st < st1 ? st * RS * 2 : 0x40000000;
+#pragma unroll
+        for (int t = 0; t < T::DPW; t++)
+            dma_a(ar, stage + (wave * T::DPW + t) * 1024, asrc[t] + off);
+    };
+    // codes: thread t decodes group t % (BN / 32) of row t / (BN / 32) of a step.
+    // Rows past N and groups past K read valid ones (A is zero there, the columns
+    // are not stored).
+    constexpr int GB = T::BN / 32;
+    const int lrow = tid / GB, lg = tid % GB;
+    const int gg = min(j0 / 32 + lg, G - 1);
+    struct Codes {
+        uint32_t w0, w1, w2, z;
+    };
+    auto load_q = [&](int st, Codes& c) {
+        const int r = min(st, st1 - 1) * RS + lrow;
+        const BwdLayer& L = r < Np ? a.L[0] : a.L[1];
+        const int row = min(r < Np ? r : r - Np, N - 1);
+        const uint32_t* src = L.q + ((int64_t)row * G + gg) * 3;
+        c.w0 = src[0];
+        c.w1 = src[1];
+        c.w2 = src[2];
+        c.z = L.z[row];
+    };
+    const Magic mg = make_magic();
+    auto stage_b = [&](const Codes& c, char* tile) {
+        uint32_t p[16];
+        decode_group(c.w0, c.w1, c.w2, mg, make_zero_sub(c.z), p);
+        uint4* dst = reinterpret_cast<uint4*>(tile + lrow * T::BROW + lg * 64);
+#pragma unroll
+        for (int q4 = 0; q4 < 4; q4++)
+            dst[q4] = make_uint4(p[4 * q4], p[4 * q4 + 1], p[4 * q4 + 2], p[4 * q4 + 3]);
+    };
+
+    f32x16 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; i++)
+#pragma unroll
+        for (int f = 0; f < FN; f++)
+            acc[i][f] = zero16();
+
+    // this lane's operands of 16-row step ks: A piece 2 ks + h of its token; the
+    // decoded rows 16 ks + 8 h + 4 t + (l % 16) / 4, columns of its 16-lane group
+    int atok[FM], aswz[FM];
+#pragma unroll
+    for (int i = 0; i < FM; i++) {
+        const int tok = wm * 32 * FM + 32 * i + l32;
+        atok[i] = tok * T::AROW;
+        aswz[i] = a_swizzle(T::PIECES, tok);
+    }
+    const int boff = (8 * h + ((lane & 15) >> 2)) * T::BROW + (wn * 32 * FN + 16 * ((lane >> 4) & 1) + 4 * (lane & 3)) * 2;
+
+    // Step st computes on stage as_cur and tile st & 1; it starts the loads of step
+    // st + 2 and decodes step st + 1 (its codes were loaded one step ago) into the
+    // other tile.
+    auto step = [&](int st, const char* cur, char* nxt2, Codes& mine, Codes& next) {
+        // A of step st has arrived once at most the loads of the last step remain
+        // (A and 2 or 4 code loads: counted as 2); the barrier also closes the
+        // tile written during that step, and the reads of the tile and stage that
+        // this step overwrites
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(T::DPW + 2) : "memory");
+        dma(st + 2, nxt2);
+        load_q(st + 2, next);
+        const char* tile = bs[(st - st0) & 1];
+        if (st + 1 < st1)  // uniform
+            stage_b(mine, bs[(st + 1 - st0) & 1]);
+        if (st < st1) {
+#pragma unroll
+            for (int ks = 0; ks < RS / 16; ks++) {
+                half8_t av[FM];
+#pragma unroll
+                for (int i = 0; i < FM; i++)
+                    av[i] = *reinterpret_cast<const half8_t*>(cur + atok[i] + (((2 * ks + h) ^ aswz[i]) << 4));
+#pragma unroll
+                for (int f = 0; f < FN; f++) {
+                    const char* src = tile + boff + ks * 16 * T::BROW + f * 64;
+                    const half8_t bv = read_columns(src, src + 4 * T::BROW);
+#pragma unroll
+                    for (int i = 0; i < FM; i++)
+                        acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(av[i], bv, acc[i][f], 0, 0, 0);
+                }
+            }
+        }
+    };
+
+    Codes qa, qb;
+    dma(st0, as0);
+    load_q(st0, qa);
+    asm volatile("" ::: "memory");
+    dma(st0 + 1, as1);
+    load_q(st0 + 1, qb);
+    asm volatile("" ::: "memory");
+    stage_b(qa, bs[0]);
+    for (int st = st0; st < st1; st += 6) {
+        step(st, as0, as2, qb, qa);
+        step(st + 1, as1, as0, qa, qb);
+        step(st + 2, as2, as1, qb, qa);
+        step(st + 3, as0, as2, qa, qb);
+        step(st + 4, as1, as0, qb, qa);
+        step(st + 5, as2, as1, qa, qb);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may write LDS after the block has ended
+
+    // D element r of lane l: token 8 (r / 4) + 4 h + r % 4, column l % 32
+    const int kt = a.L[0].k + a.L[1].k;
+#pragma unroll
+    for (int f = 0; f < FN; f++) {
+        const int j = j0 + wn * 32 * FN + 32 * f + l32;
+        if (j >= K)
+            continue;
+        if (a.split > 1) {
+#pragma unroll
+            for (int i = 0; i < FM; i++)
+#pragma unroll
+                for (int r = 0; r < 16; r++) {
+                    const int m = m0 + wm * 32 * FM + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
+                    if (m < M)
+                        a.P[((int64_t)sp * M + m) * K + j] = acc[i][f][r];
+                }
+            continue;
+        }
+        const int wg = a.L[0].map[j], wu = a.L[1].map[j];
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+#pragma unroll
+            for (int r = 0; r < 16; r++) {
+                const int m = m0 + wm * 32 * FM + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
+                if (m < M) {
+                    float v = __builtin_amdgcn_ldexpf(acc[i][f][r], -a.texp[m]);
+                    if (wg >= 0)
+                        v += a.PWs[(int64_t)m * kt + wg];
+                    if (wu >= 0)
+                        v += a.PWs[(int64_t)m * kt + a.L[0].k + wu];
+                    a.dx[(int64_t)m * K + j] = f2h(v);
+                }
+            }
+    }
+}
+
+// ------------------------------------------------------------------- launch 4
+// blocks [0, work_blocks): dx, a thread per 4 columns; then dw of gate, of up
+__global__ __launch_bounds__(256) void k_gated_fin(const GatedBwdArgs a, int blocks_g)
+{
+    const int64_t b = blockIdx.x;
+    if (b < a.work_blocks) {
+        const int64_t n = (int64_t)a.M * a.K;
+        const int64_t e = (b * 256 + threadIdx.x) * 4;
+        if (e >= n)
+            return;
+        float4 t = *reinterpret_cast<const float4*>(a.P + e);
+        for (int s = 1; s < a.split; s++) {
+            const float4 v = *reinterpret_cast<const float4*>(a.P + s * n + e);
+            t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+        }
+        const int64_t m = e / a.K;
+        const int j = (int)(e - m * a.K);
+        const int ex = -a.texp[m], kt = a.L[0].k + a.L[1].k;
+        float o[4] = {t.x, t.y, t.z, t.w};
+        uint32_t q[4];
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+            float v = __builtin_amdgcn_ldexpf(o[c], ex);
+            const int wg = a.L[0].map[j + c], wu = a.L[1].map[j + c];
+            if (wg >= 0)
+                v += a.PWs[m * kt + wg];
+            if (wu >= 0)
+                v += a.PWs[m * kt + a.L[0].k + wu];
+            q[c] = f2h(v);
+        }
+        uint16_t* dst = a.dx + e;  // dx may start at any even address
+#pragma unroll
+        for (int c = 0; c < 4; c++)
+            dst[c] = (uint16_t)q[c];
+        return;
+    }
+    const int64_t c = b - a.work_blocks;
+    const BwdLayer& L = c < blocks_g ? a.L[0] : a.L[1];
+    const int64_t n = (int64_t)a.N * L.k;
+    const int64_t e = (c < blocks_g ? c : c - blocks_g) * 256 + threadIdx.x;
+    if (e >= n)
+        return;
+    float t = L.PD[e];
+    for (int s = 1; s < a.tslabs; s++)
+        t += L.PD[s * n + e];
+    L.dw[e] = t;
+}
+
+constexpr size_t al256(size_t v) { return (v + 255) & ~(size_t)255; }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t clampi(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : (v > hi ? hi : v); }
+
+// tile of launch 3 for M tokens: tokens x columns, rows per step
+struct DxShape {
+    int bm, bn, rs;
+};
+DxShape dx_shape(int64_t M)
+{
+    if (M <= 32)
+        return {32, 128, 64};
+    if (M <= 64)
+        return {64, 128, 64};
+    return {128, 256, 32};
+}
+
+struct GatedBwdPlan {
+    int64_t Np, slabs, slab_rows, tslabs, slab_tokens, split, split_steps;
+    size_t off_texp, off_max, off_map, off_pw, off_pws, off_a, off_pd, off_p, total;
+};
+
+GatedBwdPlan gated_bwd_plan(int64_t N, int64_t K, int64_t kt, int64_t M)
+{
+    GatedBwdPlan p;
+    const size_t budget = (size_t)64 << 20;  // of each set of partial sums, unless one slab alone is larger
+    p.Np = cdiv(N, 64) * 64;
+    // launch 1: 2048 waves where the rows allow slabs of 16 at least
+    const int64_t tiles = cdiv(M, 32);
+    p.slabs = clampi(cdiv(2048, tiles), 1, cdiv(N, 16));
+    if (kt > 0)
+        p.slabs = clampi((int64_t)(budget / ((size_t)M * kt * 4)), 1, p.slabs);
+    p.slab_rows = cdiv(cdiv(N, p.slabs), 16) * 16;
+    p.slabs = cdiv(N, p.slab_rows);
+    // launch 2: about 1024 blocks of 64 rows, 32 tokens per slab at least
+    const int64_t rtiles = p.Np / 64;
+    p.tslabs = clampi(cdiv(1024, rtiles), 1, cdiv(M, 32));
+    if (kt > 0)
+        p.tslabs = clampi((int64_t)(budget / ((size_t)N * kt * 4)), 1, p.tslabs);
+    p.slab_tokens = cdiv(cdiv(M, p.tslabs), 8) * 8;
+    p.tslabs = cdiv(M, p.slab_tokens);
+    // launch 3: 512 blocks, 8 steps each at least
+    const DxShape d = dx_shape(M);
+    const int64_t steps = 2 * p.Np / d.rs;
+    p.split = clampi(cdiv(512, cdiv(M, d.bm) * cdiv(K, d.bn)), 1, cdiv(steps, 8));
+    p.split_steps = cdiv(steps, p.split);
+    p.split = cdiv(steps, p.split_steps);
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = o;
+        o += al256(bytes);
+        return at;
+    };
+    p.off_texp = take((size_t)M * 4);
+    p.off_max = take((size_t)p.slabs * M * 4);
+    p.off_map = take((size_t)2 * K * 4);
+    p.off_pw = take((size_t)p.slabs * M * kt * 4);
+    p.off_pws = take((size_t)M * kt * 4);
+    p.off_a = take((size_t)M * 2 * p.Np * 2);
+    p.off_pd = take(p.tslabs > 1 ? (size_t)p.tslabs * N * kt * 4 : 0);
+    p.off_p = take(p.split > 1 ? (size_t)p.split * M * K * 4 : 0);
+    p.total = o;
+    return p;
+}
+
+template <int FM, int FN, int WM, int WN, int RS>
+hipError_t launch_dx(GatedBwdArgs& a, hipStream_t s)
+{
+    using T = DxTile<FM, FN, WM, WN, RS>;
+    a.mtiles = (int)cdiv(a.M, T::BM);
+    const int64_t nb = (int64_t)a.mtiles * cdiv(a.K, T::BN) * a.split;
+    if (nb > INT32_MAX)
+        return hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_gated_dx<FM, FN, WM, WN, RS>), dim3((unsigned)nb), dim3(T::NT), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t gated_bwd_workspace_bytes(int64_t N, int64_t K, int32_t kg, int32_t ku, int64_t M)
+{
+    return gated_bwd_plan(N, K, (int64_t)kg + ku, M).total;
+}
+
+hipError_t launch_gated_backward(const LinearDesc& gate, const LinearDesc& up, int64_t M, int act, const float* g,
+                                 const float* u, const uint16_t* dh, uint16_t* dx, float* dw_gate, float* dw_up,
+                                 void* ws, hipStream_t s)
+{
+    const int64_t N = gate.N, K = gate.K, kt = (int64_t)gate.k + up.k;
+    const GatedBwdPlan p = gated_bwd_plan(N, K, kt, M);
+    char* const w = static_cast<char*>(ws);
+    GatedBwdArgs a{};
+    const LinearDesc* d[2] = {&gate, &up};
+    float* dw[2] = {gate.k > 0 ? dw_gate : nullptr, up.k > 0 ? dw_up : nullptr};
+    for (int l = 0; l < 2; l++) {
+        BwdLayer& L = a.L[l];
+        L.q = d[l]->q, L.s = d[l]->s, L.z = d[l]->z, L.idx = d[l]->idx, L.ww = d[l]->ww, L.k = d[l]->k;
+        L.dw = dw[l];
+        L.PD = reinterpret_cast<float*>(w + p.off_pd) + (l ? p.tslabs * N * gate.k : 0);
+        L.map = reinterpret_cast<int32_t*>(w + p.off_map) + l * K;
+    }
+    a.x = gate.x, a.g = g, a.u = u, a.dh = dh, a.dx = dx;
+    a.texp = reinterpret_cast<int32_t*>(w + p.off_texp);
+    a.slabmax = reinterpret_cast<float*>(w + p.off_max);
+    a.PW = reinterpret_cast<float*>(w + p.off_pw);
+    a.PWs = reinterpret_cast<float*>(w + p.off_pws);
+    a.A = reinterpret_cast<uint16_t*>(w + p.off_a);
+    a.P = reinterpret_cast<float*>(w + p.off_p);
+    a.M = (int32_t)M, a.N = (int32_t)N, a.K = (int32_t)K, a.Np = (int32_t)p.Np;
+    a.slabs = (int32_t)p.slabs, a.slab_rows = (int32_t)p.slab_rows;
+    a.tslabs = (int32_t)p.tslabs, a.slab_tokens = (int32_t)p.slab_tokens;
+    a.split = (int32_t)p.split, a.split_steps = (int32_t)p.split_steps;
+    const int kmax = gate.k > up.k ? gate.k : up.k;
+    const unsigned wtiles = kmax > 0 ? (unsigned)cdiv(kmax, 32) : 1u;
+    if (dx) {
+        a.work_blocks = (int32_t)cdiv(cdiv(M, 32) * p.slabs, 4);
+        const dim3 grid((unsigned)(a.work_blocks + cdiv(K, 256)), wtiles);
+        for_act(act, [&](auto c) {
+            hipLaunchKernelGGL((k_gated_tok<decltype(c)::value>), grid, dim3(256), 0, s, a);
+        });
+    }
+    a.work_blocks = (int32_t)(p.Np / 64 * p.tslabs);
+    const unsigned sums = dx && kt > 0 ? (unsigned)cdiv(M * kt, 256) : 0u;
+    const unsigned wdw = dw[0] || dw[1] ? wtiles : 1u;
+    for_act(act, [&](auto c) {
+        hipLaunchKernelGGL((k_gated_rows<decltype(c)::value>), dim3((unsigned)a.work_blocks + sums, wdw), dim3(256), 0, s,
+                           a);
+    });
+    hipError_t e = hipGetLastError();
+    if (dx && e == hipSuccess) {
+        if (M <= 32)
+            e = launch_dx<1, 1, 1, 4, 64>(a, s);
+        else if (M <= 64)
+            e = launch_dx<2, 1, 1, 4, 64>(a, s);
+        else
+            e = launch_dx<2, 4, 2, 2, 32>(a, s);
+    }
+    if (e != hipSuccess)
+        return e;
+    a.work_blocks = dx && p.split > 1 ? (int32_t)cdiv(M * K, 1024) : 0;
+    const int64_t bg = dw[0] && p.tslabs > 1 ? cdiv(N * gate.k, 256) : 0;
+    const int64_t bu = dw[1] && p.tslabs > 1 ? cdiv(N * up.k, 256) : 0;
+    if (a.work_blocks + bg + bu > 0)
+        hipLaunchKernelGGL(k_gated_fin, dim3((unsigned)(a.work_blocks + bg + bu)), dim3(256), 0, s, a, (int)bg);
+    return hipGetLastError();
+}
+
+}  // namespace owq

@@ -60,11 +60,23 @@ __device__ __forceinline__ void act_both(float v, float& a, float& d)
     }
 }
 
-// f(integral constant of act): the activation as a compile-time value
+// f(integral constant of act): the activation as a compile-time value, chosen in
+// the kernel (uniform) or by the host
 template <typename F>
 __device__ __forceinline__ void with_act(int act, F f)
 {
-    switch (act) {  // uniform
+    switch (act) {
+    case kActSilu: f(std::integral_constant<int, kActSilu>{}); break;
+    case kActGelu: f(std::integral_constant<int, kActGelu>{}); break;
+    case kActGeluTanh: f(std::integral_constant<int, kActGeluTanh>{}); break;
+    default: f(std::integral_constant<int, kActRelu>{}); break;
+    }
+}
+
+template <typename F>
+void for_act(int act, F f)
+{
+    switch (act) {
     case kActSilu: f(std::integral_constant<int, kActSilu>{}); break;
     case kActGelu: f(std::integral_constant<int, kActGelu>{}); break;
     case kActGeluTanh: f(std::integral_constant<int, kActGeluTanh>{}); break;

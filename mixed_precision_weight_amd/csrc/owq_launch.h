@@ -192,6 +192,13 @@ enum { kActSilu = 0, kActGelu = 1, kActGeluTanh = 2, kActRelu = 3 };
 // x is gate.x.
 hipError_t launch_gated(const LinearDesc& gate, const LinearDesc& up, int64_t M, int act, uint16_t* h, float* g,
                         float* u, hipStream_t s);
+// Its backward from the kept g and u: dx (fp16 [M][K]), dw_gate, dw_up (fp32
+// [N][k]), each may be NULL. M, N <= kGatedBwdMax.
+constexpr int64_t kGatedBwdMax = (int64_t)1 << 20;
+size_t gated_bwd_workspace_bytes(int64_t N, int64_t K, int32_t kg, int32_t ku, int64_t M);
+hipError_t launch_gated_backward(const LinearDesc& gate, const LinearDesc& up, int64_t M, int act, const float* g,
+                                 const float* u, const uint16_t* dh, uint16_t* dx, float* dw_gate, float* dw_up,
+                                 void* ws, hipStream_t s);
 
 // ------------------------------------------------- gradient norm and clipping --
 struct ClipEntry {

@@ -97,6 +97,9 @@ EXPORTS = {
     "owq_linear_grouped_batched": (ctypes.c_int, [ctypes.POINTER(OwqGroupedLayer), ctypes.POINTER(_P),
                                                   ctypes.POINTER(_P), _I32, _I64, _P]),
     "owq_gated": (ctypes.c_int, [ctypes.POINTER(OwqLayer), ctypes.POINTER(OwqLayer), _P, _I64, _I32, _P, _P, _P, _P]),
+    "owq_gated_backward_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I32, _I32, _I64]),
+    "owq_gated_backward": (ctypes.c_int, [ctypes.POINTER(OwqLayer), ctypes.POINTER(OwqLayer), _P, _P, _P, _P, _I64,
+                                          _I32, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "owq_linear_adapters_workspace_bytes": (ctypes.c_size_t, [_I32, _I64]),
     "owq_linear_adapters": (ctypes.c_int, [ctypes.POINTER(OwqLayer), ctypes.POINTER(OwqAdapters), _P, _P, _I64, _P,
                                            _P, ctypes.c_size_t, _P]),
@@ -1008,8 +1011,8 @@ def _same_device(index: int, *named):
             raise ValueError(f"arguments are on different devices: {name} is on {t.device}, the layer on cuda:{index}")
 
 
-def _gated_args(gate: dict, up: dict, x, act: str):
-    """(OwqLayer of gate, OwqLayer of up, GPU index, M, act code) of a gated block."""
+def _gated_shape(gate: dict, up: dict, act: str):
+    """(N, K) of the two layers of a gated block and the code of its activation."""
     if act not in ACTIVATIONS:
         raise ValueError(f"act = {act!r}: need one of {sorted(ACTIVATIONS)}")
     shapes = []
@@ -1023,10 +1026,7 @@ def _gated_args(gate: dict, up: dict, x, act: str):
         shapes.append((q.shape[0], 32 * q.shape[1]))
     if shapes[0] != shapes[1]:
         raise ValueError(f"gate is {shapes[0]}, up is {shapes[1]}: need the same (N, K)")
-    M = _xy_shapes(*shapes[0], x, None)
-    (Lg, Lu), dev = _layers_on(("gate: ", gate), ("up: ", up))
-    _same_device(dev, ("x", x))
-    return Lg, Lu, dev, M, ACTIVATIONS[act]
+    return shapes[0][0], shapes[0][1], ACTIVATIONS[act]
 
 
 def gated(gate: dict, up: dict, x: torch.Tensor, act: str = "silu", h: torch.Tensor | None = None, save: bool = False,
@@ -1034,18 +1034,59 @@ def gated(gate: dict, up: dict, x: torch.Tensor, act: str = "silu", h: torch.Ten
     """h = act(x Wg^T) * (x Wu^T) (fp16 [M][N]) for two packed layers of one shape
     (owq_gated); act: silu, gelu, gelu_tanh or relu. save: return (h, g, u) with the
     fp32 pre-activations for gated_backward."""
-    if h is not None and isinstance(gate.get("qcodes"), torch.Tensor) and isinstance(x, torch.Tensor):
-        _meta(h, torch.float16, "h", (x.shape[0] if x.dim() == 2 else 1, gate["qcodes"].shape[0]))
-    Lg, Lu, dev, M, code = _gated_args(gate, up, x, act)
-    _same_device(dev, ("h", h))
+    N, K, code = _gated_shape(gate, up, act)
+    M = _xy_shapes(N, K, x, None)
+    if h is not None:
+        _meta(h, torch.float16, "h", (M, N))
+    (Lg, Lu), dev = _layers_on(("gate: ", gate), ("up: ", up))
+    _same_device(dev, ("x", x), ("h", h))
     with _Launch(dev, stream) as run:
         if h is None:
-            h = run.empty((M, Lg.N), torch.float16)
-        g = run.empty((M, Lg.N), torch.float32) if save else None
-        u = run.empty((M, Lg.N), torch.float32) if save else None
+            h = run.empty((M, N), torch.float16)
+        g = run.empty((M, N), torch.float32) if save else None
+        u = run.empty((M, N), torch.float32) if save else None
         _check(lib().owq_gated(ctypes.byref(Lg), ctypes.byref(Lu), x.data_ptr(), M, code, h.data_ptr(), _ptr(g),
                                _ptr(u), run.handle), "owq_gated")
     return (h, g, u) if save else h
+
+
+def gated_backward_workspace_bytes(N: int, K: int, k_gate: int, k_up: int, M: int) -> int:
+    return int(lib().owq_gated_backward_workspace_bytes(N, K, k_gate, k_up, M))
+
+
+def gated_backward(gate: dict, up: dict, x: torch.Tensor | None, g: torch.Tensor, u: torch.Tensor, dh: torch.Tensor,
+                   act: str = "silu", want_dx: bool = True, want_dw: bool = True,
+                   workspace: torch.Tensor | None = None, stream=None):
+    """Backward of gated (owq_gated_backward) for the upstream gradient dh fp16
+    [M][N] and the (g, u) that gated(..., save=True) returned: (dx fp16 [M][K] or
+    None, dw_gate fp32 [N][k] or None, dw_up or None), the gradients of the input
+    and of both layers' weak columns. x is needed for the latter."""
+    N, K, code = _gated_shape(gate, up, act)
+    _meta(dh, torch.float16, "dh")
+    if dh.dim() != 2 or dh.shape[1] != N or dh.shape[0] < 1:
+        raise ValueError(f"dh has shape {tuple(dh.shape)}, expected (M, {N})")
+    M = dh.shape[0]
+    _meta(g, torch.float32, "g", (M, N))
+    _meta(u, torch.float32, "u", (M, N))
+    if x is not None:
+        _xy_shapes(N, K, x, None, M=M)
+    if workspace is not None:
+        _meta(workspace, torch.uint8, "workspace")
+    (Lg, Lu), dev = _layers_on(("gate: ", gate), ("up: ", up))
+    if want_dw and (Lg.k or Lu.k) and x is None:
+        raise ValueError("x is needed for the weak columns' gradients")
+    _same_device(dev, ("x", x), ("g", g), ("u", u), ("dh", dh), ("workspace", workspace))
+    with _Launch(dev, stream) as run:
+        dx = run.empty((M, K), torch.float16) if want_dx else None
+        dw_gate = run.empty((N, Lg.k), torch.float32) if want_dw else None
+        dw_up = run.empty((N, Lu.k), torch.float32) if want_dw else None
+        if workspace is None:
+            workspace = run.empty(gated_backward_workspace_bytes(N, K, Lg.k, Lu.k, M), torch.uint8)
+        _check(lib().owq_gated_backward(ctypes.byref(Lg), ctypes.byref(Lu), _ptr(x), g.data_ptr(), u.data_ptr(),
+                                        dh.data_ptr(), M, code, _ptr(dx), _ptr(dw_gate) if Lg.k else None,
+                                        _ptr(dw_up) if Lu.k else None, workspace.data_ptr(), workspace.numel(),
+                                        run.handle), "owq_gated_backward")
+    return dx, dw_gate, dw_up
 
 
 # ------------------------------------- low-rank adapters of many requests

@@ -505,3 +505,45 @@ def test_gated_validation(lib):
     assert call(u=FAKE) == 1
     assert call(g=FAKE + 2, u=FAKE) == 4
     assert call(x=FAKE + 8) == 4
+
+
+def test_gated_backward_validation(lib):
+    from mixed_precision_weight_amd.owq import OwqLayer
+    need = lib.owq_gated_backward_workspace_bytes(64, 128, 4, 5, 7)
+    assert need > 4 * 7 * 64
+    for bad in ((0, 128, 4, 5, 7), (64, 100, 4, 5, 7), (64, 128, -1, 5, 7), (64, 128, 4, 129, 7), (64, 128, 4, 5, 0),
+                (2 ** 20 + 1, 128, 4, 5, 7), (64, 128, 4, 5, 2 ** 20 + 1)):
+        assert lib.owq_gated_backward_workspace_bytes(*bad) == 0, bad
+
+    def layer(N=64, K=128, k=4, idx=FAKE):
+        return OwqLayer(N, K, k, 3, FAKE, FAKE, FAKE, idx, FAKE)
+
+    def call(gate=None, up=None, x=FAKE, g=FAKE, u=FAKE, dh=FAKE, M=7, act=0, dx=FAKE, dwg=FAKE, dwu=FAKE, ws=FAKE,
+             size=need):
+        a, b = gate or layer(), up or layer(k=5)
+        return lib.owq_gated_backward(ctypes.byref(a), ctypes.byref(b), x, g, u, dh, M, act, dx, dwg, dwu, ws, size,
+                                      None)
+
+    a = layer()
+    assert lib.owq_gated_backward(None, ctypes.byref(a), FAKE, FAKE, FAKE, FAKE, 7, 0, FAKE, FAKE, FAKE, FAKE, need,
+                                  None) == 1
+    assert call(x=None) == 1
+    assert call(g=None) == 1
+    assert call(u=None) == 1
+    assert call(dh=None) == 1
+    assert call(ws=None) == 1
+    assert call(M=0) == 2
+    assert call(M=2 ** 20 + 1) == 2
+    assert call(up=layer(N=65)) == 2
+    assert call(gate=layer(idx=None)) == 1
+    assert call(act=4) == 5
+    assert call(size=need - 1) == 6
+    assert call(g=FAKE + 2) == 4
+    assert call(dh=FAKE + 1) == 4
+    assert call(dx=FAKE + 1) == 4
+    assert call(dwg=FAKE + 2) == 4
+    assert call(x=FAKE + 8) == 4
+    assert call(ws=FAKE + 64) == 4
+    # nothing wanted: nothing is enqueued
+    assert call(x=None, dx=None, dwg=None, dwu=None) == 0
+    assert call(gate=layer(k=0, idx=None), up=layer(k=0, idx=None), x=None, dx=None) == 0

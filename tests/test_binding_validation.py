@@ -303,3 +303,24 @@ def test_gated_checks():
     with pytest.raises(ValueError, match="h has shape"):
         owq.gated(_layer(), _layer(), x, h=torch.zeros((5, N + 1), dtype=torch.float16))
     _host_only(owq.gated, _layer(), _layer(k=0), x, save=True)
+
+
+def test_gated_backward_checks():
+    M = 5
+    x, dh = torch.zeros((M, K), dtype=torch.float16), torch.zeros((M, N), dtype=torch.float16)
+    g, u = torch.zeros((M, N)), torch.zeros((M, N))
+    with pytest.raises(ValueError, match="act"):
+        owq.gated_backward(_layer(), _layer(), x, g, u, dh, act="tanh")
+    with pytest.raises(ValueError, match="dh has shape"):
+        owq.gated_backward(_layer(), _layer(), x, g, u, dh[:, :-1].contiguous())
+    with pytest.raises(TypeError, match="g must be torch.float32"):
+        owq.gated_backward(_layer(), _layer(), x, g.half(), u, dh)
+    with pytest.raises(ValueError, match="u has shape"):
+        owq.gated_backward(_layer(), _layer(), x, g, u[:-1].contiguous(), dh)
+    with pytest.raises(ValueError, match="x has 4 rows"):
+        owq.gated_backward(_layer(), _layer(), x[:-1].contiguous(), g, u, dh)
+    with pytest.raises(ValueError, match="contiguous"):
+        owq.gated_backward(_layer(), _layer(), x, g.t().contiguous().t(), u, dh)
+    with pytest.raises(TypeError, match="workspace"):
+        owq.gated_backward(_layer(), _layer(), x, g, u, dh, workspace=torch.zeros(64))
+    _host_only(owq.gated_backward, _layer(), _layer(), x, g, u, dh)
