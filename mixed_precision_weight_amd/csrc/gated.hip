@@ -806,9 +806,21 @@ hipError_t launch_gated(const LinearDesc& gate, const LinearDesc& up, int64_t M,
         return gated_mfv<8, 8, 4, 1, 2>(a, s);
     if (M <= 16)
         return gated_mfv<4, 16, 4, 1, 2>(a, s);
-    if (M < 128)
-        return gated_gemm<1, 1, 1, 4>(a, s);  // 32 tokens x 128 rows of each
-    return gated_gemm<2, 2, 2, 2>(a, s);      // 128 tokens x 128 rows of each
+    // The largest tile (tokens x rows of each layer) that still gives 600 blocks,
+    // more than two per CU: each layer 11008 x 4096, us with 128 x 128 / 128 x 64 /
+    // 64 x 64 / 64 x 32 / 32 x 32 at M = 64: 71 / 62 / 43 / 44 / 36, 128: 80 / 72 /
+    // 57 / 50 / 64, 256: 86 / 92 / 72 / 83 / 115, 512: 125 / 118 / 151 / 162 / 213,
+    // 2048: 388 / 433 / 485 / 571 / 802
+    auto blocks = [&](int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((gate.N + bn - 1) / bn); };
+    if (blocks(128, 128) >= 600)
+        return gated_gemm<4, 1, 1, 4>(a, s);
+    if (blocks(128, 64) >= 600)
+        return gated_gemm<4, 1, 1, 2>(a, s);
+    if (blocks(64, 64) >= 600)
+        return gated_gemm<2, 1, 1, 2>(a, s);
+    if (blocks(64, 32) >= 600)
+        return gated_gemm<2, 1, 1, 1>(a, s);
+    return gated_gemm<1, 1, 1, 1>(a, s);
 }
 
 }  // namespace owq

@@ -20,12 +20,13 @@
 // Launches:
 //  1 k_gated_tok   per 32 tokens and a slab of rows: da, db; each token's largest
 //                  |s da|, |s db|; the weak columns' part of dx per slab
-//  2 k_gated_rows  per 64 rows and a slab of tokens: da, db again (two elementwise
+//  2 k_gated_sums  the slabs added up: the token's power of two, its weak part
+//  3 k_gated_rows  per 64 rows and a slab of tokens: da, db again (two elementwise
 //                  passes read less than storing da, db in fp32 would move); dw;
-//                  A written as [M][2 Np] fp16; the slabs of 1 added up
-//  3 k_gated_dx    the product; splits the rows where tokens and columns alone
+//                  A written as [M][2 Np] fp16
+//  4 k_gated_dx    the product; splits the rows where tokens and columns alone
 //                  do not fill the GPU
-//  4 k_gated_fin   adds the splits' and the token slabs' partial sums, in order
+//  5 k_gated_fin   adds the splits' and the token slabs' partial sums, in order
 // Every sum's order is fixed, so results are deterministic.
 #include "owq_act.h"
 #include "owq_decode.h"
@@ -38,11 +39,7 @@ namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-// vectors in rows of any length: element-aligned
-typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
-typedef float f32x2u __attribute__((ext_vector_type(2), aligned(4)));
-typedef uint16_t u16x8u __attribute__((ext_vector_type(8), aligned(2)));
-typedef uint16_t u16x2u __attribute__((ext_vector_type(2), aligned(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 struct BwdLayer {
     const uint32_t* q;
@@ -64,16 +61,17 @@ struct GatedBwdArgs {
     const uint16_t* dh;
     uint16_t* dx;     // NULL: not wanted
     int32_t* texp;    // [M]: A is scaled by 2^texp
-    float* slabmax;   // [slabs][M]
+    float* slabmax;   // [M][slabs]
     float* PW;        // [slabs][M][kt], kt = k gate + k up
     float* PWs;       // [M][kt]
+    uint16_t* XW;     // [M][kt]: x at the weak columns of gate, then of up
     uint16_t* A;      // [M][2 Np]
     float* P;         // [split][M][K] (split > 1)
     int32_t M, N, K, Np;
     int32_t slabs, slab_rows;      // launch 1
-    int32_t tslabs, slab_tokens;   // launch 2
-    int32_t split, split_steps;    // launch 3
-    int32_t work_blocks, mtiles;
+    int32_t tslabs, slab_tokens;   // launch 3
+    int32_t split, split_steps;    // launch 4
+    int32_t work_blocks, map_blocks, mtiles;
 };
 
 __device__ __forceinline__ f32x16 zero16()
@@ -85,86 +83,127 @@ __device__ __forceinline__ f32x16 zero16()
     return z;
 }
 
+// The elementwise passes load through buffer resources, whose range check returns
+// zero past the end: no load sits under a branch (at whose end it would be waited
+// for), and rows past N or tokens past M need no clamping, only the masks below.
+// (p and bytes are wave-uniform; readfirstlane keeps them in scalar registers also
+// where the compiler computed them on the vector ALUs)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, int64_t bytes)
+{
+    const uint64_t v = (uint64_t)(uintptr_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((uintptr_t)(((uint64_t)hi << 32) | lo)), (short)0,
+                                             __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
+}
+
+__device__ __forceinline__ f32x4 buf_f4(__amdgpu_buffer_rsrc_t r, int off)
+{
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
+__device__ __forceinline__ uint32_t buf_u16(__amdgpu_buffer_rsrc_t r, int off)
+{
+    return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+}
+
 // ------------------------------------------------------------------- launch 1
 // A wave: 32 tokens (lane l: token l % 32) x one slab of rows, 16 rows per step
 // (lane half h: rows 8 h .. 8 h + 7, consecutive in memory). The matrix cores'
 // k index is the row: step element e pairs da of row 8 h + e with w_weak of that
-// row and column l % 32.
+// row and column l % 32. The next step's loads are issued before this one's
+// arithmetic. EVEN: rows of dh start at 4-byte addresses (N even), so 8 values are
+// one load.
 struct TokRows {
-    float g[8], u[8];
-    uint32_t d[8];
+    f32x4 g[2], u[2];
+    uint32_t d[8];             // EVEN: d[0..3], two values each
+    uint32_t w[2][8];          // w_weak
 };
 
-__device__ __forceinline__ void load_tok_rows(const GatedBwdArgs& a, int64_t o, int row, TokRows& t)
-{
-    if (row + 8 <= a.N) {
-#pragma unroll
-        for (int v = 0; v < 8; v += 4) {
-            const f32x4u gv = *reinterpret_cast<const f32x4u*>(a.g + o + row + v);
-            const f32x4u uv = *reinterpret_cast<const f32x4u*>(a.u + o + row + v);
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                t.g[v + e] = gv[e];
-                t.u[v + e] = uv[e];
-            }
-        }
-        const u16x8u dv = *reinterpret_cast<const u16x8u*>(a.dh + o + row);
-#pragma unroll
-        for (int e = 0; e < 8; e++)
-            t.d[e] = dv[e];
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; e++) {
-            const int r = min(row + e, a.N - 1);
-            t.g[e] = a.g[o + r];
-            t.u[e] = a.u[o + r];
-            t.d[e] = a.dh[o + r];
-        }
-    }
-}
-
-template <int ACT>
+template <int ACT, bool EVEN>
 __device__ __forceinline__ void tok_slab(const GatedBwdArgs& a, int tile, int slab, int wt)
 {
     const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
     const int m = tile * 32 + l32;
     const bool live = m < a.M;
-    const int64_t o = (int64_t)min(m, a.M - 1) * a.N;
-    const int r0 = slab * a.slab_rows, r1 = min(a.N, r0 + a.slab_rows);
+    const int N = a.N;
+    const int r0 = slab * a.slab_rows, r1 = min(N, r0 + a.slab_rows);
     const int c = wt * 32 + l32;  // weak column
     const bool on[2] = {wt * 32 < a.L[0].k, wt * 32 < a.L[1].k};  // uniform
+    const int64_t o0 = (int64_t)tile * 32 * N, n0 = (int64_t)min(32, a.M - tile * 32) * N;
+    const __amdgpu_buffer_rsrc_t gr = rsrc(a.g + o0, n0 * 4), ur = rsrc(a.u + o0, n0 * 4), dr = rsrc(a.dh + o0, n0 * 2);
+    const int lo = l32 * N + 8 * h;
+    int woff[2];
+#pragma unroll
+    for (int l = 0; l < 2; l++)
+        woff[l] = 2 * (8 * h * a.L[l].k + min(c, max(a.L[l].k - 1, 0)));
+    auto load = [&](int r, TokRows& t) {  // r uniform
+        const int o = lo + r;
+#pragma unroll
+        for (int v = 0; v < 2; v++) {
+            t.g[v] = buf_f4(gr, 4 * o + 16 * v);
+            t.u[v] = buf_f4(ur, 4 * o + 16 * v);
+        }
+        if constexpr (EVEN) {
+            const auto v = __builtin_amdgcn_raw_buffer_load_b128(dr, 2 * o, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                t.d[e] = v[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                t.d[e] = buf_u16(dr, 2 * (o + e));
+        }
+        const int left = max(min(N - r, 16), 0);  // rows of the step
+#pragma unroll
+        for (int l = 0; l < 2; l++) {
+            // an empty resource (zeros) for a layer without this tile of weak columns
+            const BwdLayer& L = a.L[l];
+            const __amdgpu_buffer_rsrc_t wr =
+                rsrc(L.ww + (int64_t)min(r, N) * L.k, on[l] ? (int64_t)left * L.k * 2 : 0);
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                t.w[l][e] = buf_u16(wr, woff[l] + 2 * e * L.k);
+        }
+    };
     f32x16 acc[2] = {zero16(), zero16()};
     float mx = 0.0f;
-    TokRows cur;
-    load_tok_rows(a, o, min(r0 + 8 * h, a.N - 1), cur);
-    for (int r = r0; r < r1; r += 16) {
-        TokRows nxt;
-        load_tok_rows(a, o, min(r + 16 + 8 * h, a.N - 1), nxt);
-        const int rb = r + 8 * h;
+    // one step on `cur`; `nxt` is loaded for the one after. The rows' steps s_i are
+    // loaded ahead of that, so waiting for them waits for none of it.
+    auto work = [&](int r, const TokRows& cur, TokRows& nxt) {
+        uint32_t sv[2][8];
+#pragma unroll
+        for (int l = 0; l < 2; l++) {
+            const __amdgpu_buffer_rsrc_t sr = rsrc(a.L[l].s + min(r, N), max(N - r, 0) * 2);
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                sv[l][e] = buf_u16(sr, 16 * h + 2 * e);
+        }
+        asm volatile("" ::: "memory");
+        load(r + 16, nxt);
+        asm volatile("" ::: "memory");
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            const int row = min(rb + e, a.N - 1);
-            const bool use = live && rb + e < r1;
+            const bool use = live && r + 8 * h + e < r1;
             float v, d;
-            act_both<ACT>(cur.g[e], v, d);
-            const float dh = h2f((uint16_t)cur.d[e]);
-            const float da = use ? dh * cur.u[e] * d : 0.0f, db = use ? dh * v : 0.0f;
-            if (wt == 0)  // uniform
-                mx = fmaxf(mx, fmaxf(fabsf(h2f(a.L[0].s[row]) * da), fabsf(h2f(a.L[1].s[row]) * db)));
-#pragma unroll
-            for (int l = 0; l < 2; l++)
-                if (on[l]) {
-                    const int k = a.L[l].k;
-                    const float w = h2f(a.L[l].ww[(int64_t)row * k + min(c, k - 1)]);
-                    acc[l] = __builtin_amdgcn_mfma_f32_32x32x2f32(l ? db : da, w, acc[l], 0, 0, 0);
-                }
+            act_both<ACT>(cur.g[e / 4][e % 4], v, d);
+            const float dh = h2f((uint16_t)(EVEN ? cur.d[e / 2] >> (16 * (e % 2)) : cur.d[e]));
+            const float da = use ? dh * cur.u[e / 4][e % 4] * d : 0.0f, db = use ? dh * v : 0.0f;
+            acc[0] = __builtin_amdgcn_mfma_f32_32x32x2f32(da, h2f((uint16_t)cur.w[0][e]), acc[0], 0, 0, 0);
+            acc[1] = __builtin_amdgcn_mfma_f32_32x32x2f32(db, h2f((uint16_t)cur.w[1][e]), acc[1], 0, 0, 0);
+            mx = fmaxf(mx, fmaxf(fabsf(h2f((uint16_t)sv[0][e]) * da), fabsf(h2f((uint16_t)sv[1][e]) * db)));
         }
-        cur = nxt;
+    };
+    TokRows ta, tb;
+    load(r0, ta);
+    for (int r = r0; r < r1; r += 32) {
+        work(r, ta, tb);
+        work(r + 16, tb, ta);
     }
     if (wt == 0) {
         mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
         if (h == 0 && live)
-            a.slabmax[(int64_t)slab * a.M + m] = mx;
+            a.slabmax[(int64_t)m * a.slabs + slab] = mx;
     }
     const int kt = a.L[0].k + a.L[1].k;
 #pragma unroll
@@ -178,11 +217,24 @@ __device__ __forceinline__ void tok_slab(const GatedBwdArgs& a, int tile, int sl
             }
 }
 
-// blocks [0, work_blocks): waves over (token tile, slab); the rest (first row of
-// the grid only): the map from columns to weak columns
-template <int ACT>
-__global__ __launch_bounds__(256) void k_gated_tok(const GatedBwdArgs a)
+// blocks [0, work_blocks): waves over (token tile, slab); then (first row of the
+// grid only) map_blocks: the map from columns to weak columns; then x at the weak
+// columns, gathered once (launch 3 reads it once per 64 rows: gathers there would
+// fetch a cache line per value each time)
+template <int ACT, bool EVEN>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k_gated_tok(const GatedBwdArgs a)
 {
+    if ((int)blockIdx.x >= a.work_blocks + a.map_blocks) {
+        const int kt = a.L[0].k + a.L[1].k;
+        const int64_t e = (int64_t)((int)blockIdx.x - a.work_blocks - a.map_blocks) * 256 + threadIdx.x;
+        if (blockIdx.y != 0 || e >= (int64_t)a.M * kt)
+            return;
+        const int64_t m = e / kt;
+        const int c = (int)(e - m * kt);
+        const int j = c < a.L[0].k ? a.L[0].idx[c] : a.L[1].idx[c - a.L[0].k];
+        a.XW[e] = a.x[m * a.K + (j >= 0 && j < a.K ? j : 0)];
+        return;
+    }
     if ((int)blockIdx.x >= a.work_blocks) {
         const int j = ((int)blockIdx.x - a.work_blocks) * 256 + (int)threadIdx.x;
         if (blockIdx.y != 0 || j >= a.K)
@@ -204,23 +256,24 @@ __global__ __launch_bounds__(256) void k_gated_tok(const GatedBwdArgs a)
     const int tiles = (a.M + 31) >> 5;
     if (w >= tiles * a.slabs)
         return;
-    tok_slab<ACT>(a, w % tiles, w / tiles, (int)blockIdx.y);
+    const int slab = __builtin_amdgcn_readfirstlane(w / tiles);
+    tok_slab<ACT, EVEN>(a, w - slab * tiles, slab, (int)blockIdx.y);
 }
 
-// ------------------------------------------------------------------- launch 2
+// ------------------------------------------------------------- launches 2 and 3
 // A block: 64 rows (lane l: rows 2 (l % 32), + 1) x one slab of tokens, its 4
 // waves taking pairs of tokens in turn (lane half h: token of the pair). The
 // matrix cores' k index is the token: da of row 2 (l % 32) + e against x at weak
 // column l % 32. The waves' sums are added in order in LDS.
-constexpr int kTokFlight = 4;  // pairs of tokens whose loads are in flight together
+constexpr int kTokFlight = 2;  // pairs of tokens whose loads are in flight together
 
 __device__ __forceinline__ int scale_exp(float mx)
 {
     return mx > 0.0f && mx < 0x1p120f ? 15 - __builtin_amdgcn_frexp_expf(mx) : 0;
 }
 
-template <int ACT>
-__device__ __forceinline__ void row_slab(const GatedBwdArgs& a, int tile, int slab, int wt, float* red, int* texp)
+template <int ACT, bool EVEN>
+__device__ __forceinline__ void row_slab(const GatedBwdArgs& a, int tile, int slab, int wt, float* red)
 {
     const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -230,92 +283,86 @@ __device__ __forceinline__ void row_slab(const GatedBwdArgs& a, int tile, int sl
     const bool on[2] = {a.L[0].dw && wt * 32 < a.L[0].k, a.L[1].dw && wt * 32 < a.L[1].k};
     const int rc[2] = {min(row, a.N - 1), min(row + 1, a.N - 1)};
     float sc[2][2];
-    int jw[2];
+    const int kt = a.L[0].k + a.L[1].k;
+    int jw[2];  // this lane's weak columns in a row of XW
 #pragma unroll
     for (int l = 0; l < 2; l++) {
         sc[l][0] = h2f(a.L[l].s[rc[0]]);
         sc[l][1] = h2f(a.L[l].s[rc[1]]);
-        int j = 0;
-        if (on[l])
-            j = a.L[l].idx[min(wt * 32 + l32, a.L[l].k - 1)];
-        jw[l] = j >= 0 && j < a.K ? j : 0;
+        jw[l] = on[l] ? (l ? a.L[0].k : 0) + min(wt * 32 + l32, a.L[l].k - 1) : 0;
     }
     f32x16 acc[2][2] = {{zero16(), zero16()}, {zero16(), zero16()}};
-    for (int tb = t0; tb < t1; tb += 256) {
-        const int tn = min(256, t1 - tb);
-        if (conv) {  // uniform
-            __syncthreads();  // the previous tokens' exponents are no longer read
-            if (tid < tn) {
-                float mx = 0.0f;
-                for (int s = 0; s < a.slabs; s++)
-                    mx = fmaxf(mx, a.slabmax[(int64_t)s * a.M + tb + tid]);
-                const int e = scale_exp(mx);
-                texp[tid] = e;
-                if (tile == 0)
-                    a.texp[tb + tid] = e;
+    // kTokFlight pairs of tokens per step; the next step's loads are issued before
+    // this one's arithmetic
+    struct Pairs {
+        uint32_t g[kTokFlight][2], u[kTokFlight][2];
+        uint32_t d[kTokFlight][2], xw[kTokFlight][2];  // EVEN: d[v][0], both values
+        int ex[kTokFlight];
+    };
+    const int po = h * a.N + row;  // this lane's element of a pair of tokens
+    auto load = [&](int t, Pairs& q) {  // t uniform
+#pragma unroll
+        for (int v = 0; v < kTokFlight; v++) {
+            const int tp = min(t + 8 * v, t1 - 1);  // the pair's first token; past the slab: not used
+            const int64_t o = (int64_t)tp * a.N, n = (int64_t)min(2, a.M - tp) * a.N;
+            const auto gv = __builtin_amdgcn_raw_buffer_load_b64(rsrc(a.g + o, n * 4), 4 * po, 0, 0);
+            const auto uv = __builtin_amdgcn_raw_buffer_load_b64(rsrc(a.u + o, n * 4), 4 * po, 0, 0);
+            q.g[v][0] = gv[0], q.g[v][1] = gv[1], q.u[v][0] = uv[0], q.u[v][1] = uv[1];
+            const __amdgpu_buffer_rsrc_t dr = rsrc(a.dh + o, n * 2);
+            if constexpr (EVEN) {
+                q.d[v][0] = __builtin_amdgcn_raw_buffer_load_b32(dr, 2 * po, 0, 0);
+            } else {
+                q.d[v][0] = buf_u16(dr, 2 * po);
+                q.d[v][1] = buf_u16(dr, 2 * po + 2);
             }
-            __syncthreads();
+            const int64_t m = min(tp + h, a.M - 1);
+#pragma unroll
+            for (int l = 0; l < 2; l++)  // (workspace: readable also where not used)
+                q.xw[v][l] = a.XW[m * kt + jw[l]];
+            q.ex[v] = a.texp[m];
         }
-        for (int p = wave; p < (tn + 1) / 2; p += 4 * kTokFlight) {
-            float g[kTokFlight][2], u[kTokFlight][2];
-            uint32_t d[kTokFlight][2], xw[kTokFlight][2];
+    };
+    auto work = [&](int tb, const Pairs& cur, Pairs& nxt) {
+        load(tb + 8 * kTokFlight, nxt);
+        asm volatile("" ::: "memory");
 #pragma unroll
-            for (int v = 0; v < kTokFlight; v++) {
-                const int64_t m = tb + min(2 * (p + 4 * v) + h, tn - 1);
-                const int64_t o = m * a.N;
-                if (rc[1] == row + 1) {
-                    const f32x2u gv = *reinterpret_cast<const f32x2u*>(a.g + o + row);
-                    const f32x2u uv = *reinterpret_cast<const f32x2u*>(a.u + o + row);
-                    const u16x2u dv = *reinterpret_cast<const u16x2u*>(a.dh + o + row);
-                    g[v][0] = gv[0], g[v][1] = gv[1], u[v][0] = uv[0], u[v][1] = uv[1];
-                    d[v][0] = dv[0], d[v][1] = dv[1];
-                } else {
+        for (int v = 0; v < kTokFlight; v++) {
+            const int t = tb + 8 * v + h;
+            float dab[2][2];
 #pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        g[v][e] = a.g[o + rc[e]];
-                        u[v][e] = a.u[o + rc[e]];
-                        d[v][e] = a.dh[o + rc[e]];
-                    }
+            for (int e = 0; e < 2; e++) {
+                const bool use = t < t1 && row + e < a.N;
+                float va, sl;
+                act_both<ACT>(__builtin_bit_cast(float, cur.g[v][e]), va, sl);
+                const float dh = h2f((uint16_t)(EVEN ? cur.d[v][0] >> (16 * e) : cur.d[v][e]));
+                dab[0][e] = use ? dh * __builtin_bit_cast(float, cur.u[v][e]) * sl : 0.0f;
+                dab[1][e] = use ? dh * va : 0.0f;
+            }
+            if (conv && t < t1 && row < a.Np) {
+                uint16_t* dst = a.A + (int64_t)t * 2 * a.Np + row;
+#pragma unroll
+                for (int l = 0; l < 2; l++) {
+                    const uint32_t lo = f2h(__builtin_amdgcn_ldexpf(dab[l][0] * sc[l][0], cur.ex[v]));
+                    const uint32_t hi = f2h(__builtin_amdgcn_ldexpf(dab[l][1] * sc[l][1], cur.ex[v]));
+                    *reinterpret_cast<uint32_t*>(dst + l * a.Np) = lo | (hi << 16);
                 }
-#pragma unroll
-                for (int l = 0; l < 2; l++)
-                    xw[v][l] = on[l] ? a.x[m * a.K + jw[l]] : 0;
             }
 #pragma unroll
-            for (int v = 0; v < kTokFlight; v++) {
-                const int t = 2 * (p + 4 * v) + h;
-                if (2 * (p + 4 * v) >= tn)  // uniform
-                    break;
-                float dab[2][2];
+            for (int l = 0; l < 2; l++) {
+                const float xv = h2f((uint16_t)cur.xw[v][l]);
 #pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    const bool use = t < tn && row + e < a.N;
-                    float va, sl;
-                    act_both<ACT>(g[v][e], va, sl);
-                    const float dh = h2f((uint16_t)d[v][e]);
-                    dab[0][e] = use ? dh * u[v][e] * sl : 0.0f;
-                    dab[1][e] = use ? dh * va : 0.0f;
-                }
-                if (conv && t < tn && row < a.Np) {
-                    const int e = texp[t];
-                    uint16_t* dst = a.A + (int64_t)(tb + t) * 2 * a.Np + row;
-#pragma unroll
-                    for (int l = 0; l < 2; l++) {
-                        const uint32_t lo = f2h(__builtin_amdgcn_ldexpf(dab[l][0] * sc[l][0], e));
-                        const uint32_t hi = f2h(__builtin_amdgcn_ldexpf(dab[l][1] * sc[l][1], e));
-                        *reinterpret_cast<uint32_t*>(dst + l * a.Np) = lo | (hi << 16);
-                    }
-                }
-#pragma unroll
-                for (int l = 0; l < 2; l++)
-                    if (on[l]) {
-                        const float xv = h2f((uint16_t)xw[v][l]);
-#pragma unroll
-                        for (int e = 0; e < 2; e++)
-                            acc[l][e] = __builtin_amdgcn_mfma_f32_32x32x2f32(dab[l][e], xv, acc[l][e], 0, 0, 0);
-                    }
+                for (int e = 0; e < 2; e++)
+                    acc[l][e] = __builtin_amdgcn_mfma_f32_32x32x2f32(dab[l][e], xv, acc[l][e], 0, 0, 0);
             }
         }
+    };
+    Pairs pa, pb;
+    const int first = t0 + 2 * wave;
+    if (first < t1)
+        load(first, pa);
+    for (int t = first; t < t1; t += 16 * kTokFlight) {
+        work(t, pa, pb);
+        work(t + 8 * kTokFlight, pb, pa);
     }
     // D element r of lane l: row 2 (8 (r / 4) + 4 h + r % 4) + e, weak column l % 32
 #pragma unroll
@@ -349,30 +396,52 @@ __device__ __forceinline__ void row_slab(const GatedBwdArgs& a, int tile, int sl
     }
 }
 
-// blocks [0, work_blocks): (row tile, token slab); the rest (first row of the grid
-// only): the sums over the slabs of launch 1
-template <int ACT>
-__global__ __launch_bounds__(256) void k_gated_rows(const GatedBwdArgs a)
+template <int ACT, bool EVEN>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void k_gated_rows(const GatedBwdArgs a)
 {
     __shared__ float red[48 * 64];
-    __shared__ int texp[256];
-    const int b = blockIdx.x;
-    if (b >= a.work_blocks) {
-        const int64_t n = (int64_t)a.M * (a.L[0].k + a.L[1].k);
-        const int64_t e = (int64_t)(b - a.work_blocks) * 256 + threadIdx.x;
-        if (blockIdx.y != 0 || e >= n)
-            return;
-        float t = 0.0f;
-        for (int s = 0; s < a.slabs; s++)
-            t += a.PW[s * n + e];
-        a.PWs[e] = t;
-        return;
-    }
     const int tiles = (a.Np + 63) / 64;
-    row_slab<ACT>(a, b % tiles, b / tiles, (int)blockIdx.y, red, texp);
+    const int slab = __builtin_amdgcn_readfirstlane((int)blockIdx.x / tiles);
+    row_slab<ACT, EVEN>(a, (int)blockIdx.x - slab * tiles, slab, (int)blockIdx.y, red);
 }
 
-// ------------------------------------------------------------------- launch 3
+// Between the two: blocks [0, work_blocks): a wave per token, its exponent from the
+// slabs' largest values; the rest: the slabs' weak sums added in order.
+__global__ __launch_bounds__(256) void k_gated_sums(const GatedBwdArgs a)
+{
+    if ((int)blockIdx.x < a.work_blocks) {
+        const int m = (int)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+        if (m >= a.M)
+            return;
+        float mx = 0.0f;
+        for (int s = threadIdx.x & 63; s < a.slabs; s += 64)
+            mx = fmaxf(mx, a.slabmax[(int64_t)m * a.slabs + s]);
+        mx = wave_max_dpp(mx);
+        if ((threadIdx.x & 63) == 0)
+            a.texp[m] = scale_exp(mx);
+        return;
+    }
+    const int64_t n = (int64_t)a.M * (a.L[0].k + a.L[1].k);
+    const int64_t e = (int64_t)((int)blockIdx.x - a.work_blocks) * 256 + threadIdx.x;
+    if (e >= n)
+        return;
+    float t = 0.0f;
+    int s = 0;
+    for (; s + 8 <= a.slabs; s += 8) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            v[i] = a.PW[(s + i) * n + e];
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            t += v[i];
+    }
+    for (; s < a.slabs; s++)
+        t += a.PW[s * n + e];
+    a.PWs[e] = t;
+}
+
+// ------------------------------------------------------------------- launch 4
 // dx: D[m][j] = sum over r < 2 Np of A[m][r] (q - z)[r][j], rows of gate, then of
 // up. A block owns BM tokens x BN columns and steps of RS rows: thread t decodes
 // one 32-column group of one row into the LDS tile [row][column] (exact fp16), the
@@ -588,7 +657,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
     }
 }
 
-// ------------------------------------------------------------------- launch 4
+// ------------------------------------------------------------------- launch 5
 // blocks [0, work_blocks): dx, a thread per 4 columns; then dw of gate, of up
 __global__ __launch_bounds__(256) void k_gated_fin(const GatedBwdArgs a, int blocks_g)
 {
@@ -640,7 +709,7 @@ constexpr size_t al256(size_t v) { return (v + 255) & ~(size_t)255; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t clampi(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : (v > hi ? hi : v); }
 
-// tile of launch 3 for M tokens: tokens x columns, rows per step
+// tile of launch 4 for M tokens: tokens x columns, rows per step
 struct DxShape {
     int bm, bn, rs;
 };
@@ -655,7 +724,7 @@ DxShape dx_shape(int64_t M)
 
 struct GatedBwdPlan {
     int64_t Np, slabs, slab_rows, tslabs, slab_tokens, split, split_steps;
-    size_t off_texp, off_max, off_map, off_pw, off_pws, off_a, off_pd, off_p, total;
+    size_t off_texp, off_max, off_map, off_pw, off_pws, off_xw, off_a, off_pd, off_p, total;
 };
 
 GatedBwdPlan gated_bwd_plan(int64_t N, int64_t K, int64_t kt, int64_t M)
@@ -663,21 +732,23 @@ GatedBwdPlan gated_bwd_plan(int64_t N, int64_t K, int64_t kt, int64_t M)
     GatedBwdPlan p;
     const size_t budget = (size_t)64 << 20;  // of each set of partial sums, unless one slab alone is larger
     p.Np = cdiv(N, 64) * 64;
-    // launch 1: 2048 waves where the rows allow slabs of 16 at least
+    // launch 1: 2048 waves (what the GPU holds at two per SIMD) where the rows
+    // allow slabs of 32 at least
     const int64_t tiles = cdiv(M, 32);
-    p.slabs = clampi(cdiv(2048, tiles), 1, cdiv(N, 16));
+    p.slabs = clampi(2048 / tiles, 1, cdiv(N, 32));
     if (kt > 0)
         p.slabs = clampi((int64_t)(budget / ((size_t)M * kt * 4)), 1, p.slabs);
     p.slab_rows = cdiv(cdiv(N, p.slabs), 16) * 16;
     p.slabs = cdiv(N, p.slab_rows);
-    // launch 2: about 1024 blocks of 64 rows, 32 tokens per slab at least
+    // launch 3: blocks of 64 rows, as many as the GPU holds at once (768, three
+    // waves per SIMD), 32 tokens per slab at least
     const int64_t rtiles = p.Np / 64;
-    p.tslabs = clampi(cdiv(1024, rtiles), 1, cdiv(M, 32));
+    p.tslabs = clampi(768 / rtiles, 1, cdiv(M, 32));
     if (kt > 0)
         p.tslabs = clampi((int64_t)(budget / ((size_t)N * kt * 4)), 1, p.tslabs);
     p.slab_tokens = cdiv(cdiv(M, p.tslabs), 8) * 8;
     p.tslabs = cdiv(M, p.slab_tokens);
-    // launch 3: 512 blocks, 8 steps each at least
+    // launch 4: 512 blocks, 8 steps each at least
     const DxShape d = dx_shape(M);
     const int64_t steps = 2 * p.Np / d.rs;
     p.split = clampi(cdiv(512, cdiv(M, d.bm) * cdiv(K, d.bn)), 1, cdiv(steps, 8));
@@ -694,6 +765,7 @@ GatedBwdPlan gated_bwd_plan(int64_t N, int64_t K, int64_t kt, int64_t M)
     p.off_map = take((size_t)2 * K * 4);
     p.off_pw = take((size_t)p.slabs * M * kt * 4);
     p.off_pws = take((size_t)M * kt * 4);
+    p.off_xw = take((size_t)M * kt * 2);
     p.off_a = take((size_t)M * 2 * p.Np * 2);
     p.off_pd = take(p.tslabs > 1 ? (size_t)p.tslabs * N * kt * 4 : 0);
     p.off_p = take(p.split > 1 ? (size_t)p.split * M * K * 4 : 0);
@@ -742,6 +814,7 @@ hipError_t launch_gated_backward(const LinearDesc& gate, const LinearDesc& up, i
     a.slabmax = reinterpret_cast<float*>(w + p.off_max);
     a.PW = reinterpret_cast<float*>(w + p.off_pw);
     a.PWs = reinterpret_cast<float*>(w + p.off_pws);
+    a.XW = reinterpret_cast<uint16_t*>(w + p.off_xw);
     a.A = reinterpret_cast<uint16_t*>(w + p.off_a);
     a.P = reinterpret_cast<float*>(w + p.off_p);
     a.M = (int32_t)M, a.N = (int32_t)N, a.K = (int32_t)K, a.Np = (int32_t)p.Np;
@@ -750,20 +823,33 @@ hipError_t launch_gated_backward(const LinearDesc& gate, const LinearDesc& up, i
     a.split = (int32_t)p.split, a.split_steps = (int32_t)p.split_steps;
     const int kmax = gate.k > up.k ? gate.k : up.k;
     const unsigned wtiles = kmax > 0 ? (unsigned)cdiv(kmax, 32) : 1u;
-    if (dx) {
-        a.work_blocks = (int32_t)cdiv(cdiv(M, 32) * p.slabs, 4);
-        const dim3 grid((unsigned)(a.work_blocks + cdiv(K, 256)), wtiles);
+    const bool any_dw = dw[0] || dw[1];
+    const bool even = N % 2 == 0 && (reinterpret_cast<uintptr_t>(dh) & 3) == 0;
+    a.work_blocks = dx ? (int32_t)cdiv(cdiv(M, 32) * p.slabs, 4) : 0;
+    a.map_blocks = dx ? (int32_t)cdiv(K, 256) : 0;
+    const int64_t first = a.work_blocks + a.map_blocks + (any_dw ? cdiv(M * kt, 256) : 0);
+    {
+        const dim3 grid((unsigned)first, wtiles);
         for_act(act, [&](auto c) {
-            hipLaunchKernelGGL((k_gated_tok<decltype(c)::value>), grid, dim3(256), 0, s, a);
+            if (even)
+                hipLaunchKernelGGL((k_gated_tok<decltype(c)::value, true>), grid, dim3(256), 0, s, a);
+            else
+                hipLaunchKernelGGL((k_gated_tok<decltype(c)::value, false>), grid, dim3(256), 0, s, a);
         });
     }
-    a.work_blocks = (int32_t)(p.Np / 64 * p.tslabs);
-    const unsigned sums = dx && kt > 0 ? (unsigned)cdiv(M * kt, 256) : 0u;
-    const unsigned wdw = dw[0] || dw[1] ? wtiles : 1u;
-    for_act(act, [&](auto c) {
-        hipLaunchKernelGGL((k_gated_rows<decltype(c)::value>), dim3((unsigned)a.work_blocks + sums, wdw), dim3(256), 0, s,
-                           a);
-    });
+    if (dx) {
+        a.work_blocks = (int32_t)cdiv(M, 4);
+        hipLaunchKernelGGL(k_gated_sums, dim3((unsigned)(a.work_blocks + cdiv(M * kt, 256))), dim3(256), 0, s, a);
+    }
+    {
+        const dim3 grid((unsigned)(p.Np / 64 * p.tslabs), any_dw ? wtiles : 1u);
+        for_act(act, [&](auto c) {
+            if (even)
+                hipLaunchKernelGGL((k_gated_rows<decltype(c)::value, true>), grid, dim3(256), 0, s, a);
+            else
+                hipLaunchKernelGGL((k_gated_rows<decltype(c)::value, false>), grid, dim3(256), 0, s, a);
+        });
+    }
     hipError_t e = hipGetLastError();
     if (dx && e == hipSuccess) {
         if (M <= 32)

@@ -1,12 +1,16 @@
 // owq_act.h -- the activations of the gated feed-forward block and their slopes,
-// in fp32 (device expf / erfcf, IEEE division).
+// in fp32.
 //   silu       v s(v),  s(v) = 1 / (1 + exp(-v))
 //   gelu       v P(v),  P(v) = erfc(-v / sqrt 2) / 2 (the normal distribution; erfc
 //              keeps its relative accuracy in the left tail, 1 + erf does not)
 //   gelu_tanh  v s(2 c (v + 0.044715 v^3)),  c = sqrt(2 / pi): the tanh form,
 //              (1 + tanh t) / 2 = s(2 t)
 //   relu       max(v, 0)
-// Far out exp overflows to infinity and the quotients to 0: no NaN from finite v
+// The logistic function uses the hardware's 2^v and reciprocal (one ulp each): its
+// relative error is |v| 2^-24 from the rounded exponent plus 2^-22, as large as the
+// change of s(v) from the fp32 rounding of v itself; an accurate exp and an IEEE
+// division cost four times the instructions, and the two elementwise passes of the
+// backward are bound by them. Far out exp overflows to infinity and the quotients to 0: no NaN from finite v
 // (|v| < 2^51 for finite fp16 layer inputs, so v^2 stays finite).
 #pragma once
 
@@ -23,7 +27,10 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTwoC = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kCube = 0.044715f;
 
-__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
+__device__ __forceinline__ float sigmoid(float v)
+{
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * v));
+}
 
 template <int ACT>
 __device__ __forceinline__ float act_value(float v)
