@@ -397,7 +397,7 @@ __device__ __forceinline__ void row_slab(const GatedBwdArgs& a, int tile, int sl
 }
 
 template <int ACT, bool EVEN>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void k_gated_rows(const GatedBwdArgs a)
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void k_gated_rows(const GatedBwdArgs a)
 {
     __shared__ float red[48 * 64];
     const int tiles = (a.Np + 63) / 64;
@@ -460,7 +460,17 @@ struct DxTile {
     static constexpr int PIECES = AROW / 16;         // 4 or 8
     static constexpr int ASTAGE = BM * AROW;
     static constexpr int DPW = ASTAGE / 16 / NT;     // 16-byte units per thread and step
-    static_assert(RS * (BN / 32) == NT, "one group per thread and step");
+    // The 16-byte pieces of group g of row r are stored at piece ^ b_swizzle: rows and
+    // groups 64 bytes apart would put the 16 lanes of a write on 4 of the 16 places
+    // that the banks hold (415 -> 395 us at M = 2048, 2 x 11008 x 4096). Constant over
+    // a lane's reads: its rows agree modulo 4, a wave's groups share g / 4.
+    static constexpr int GB = BN / 32;
+    __device__ static __forceinline__ int b_swizzle(int g, int r)
+    {
+        return GB == 8 ? ((g >> 2) & 1) | ((r & 1) << 1) : r & 3;
+    }
+    static_assert((GB == 8 && FN == 4) || GB == 4, "a wave's groups must share their swizzle");
+    static_assert(RS * GB == NT, "one group per thread and step");
     static_assert(ASTAGE % (16 * NT) == 0, "an A stage must split evenly over the threads");
     static_assert((BN * 2) % 256 == 0, "tile rows 64 bytes apart modulo the banks");
 };
@@ -526,7 +536,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
     // codes: thread t decodes group t % (BN / 32) of row t / (BN / 32) of a step.
     // Rows past N and groups past K read valid ones (A is zero there, the columns
     // are not stored).
-    constexpr int GB = T::BN / 32;
+    constexpr int GB = T::GB;
     const int lrow = tid / GB, lg = tid % GB;
     const int gg = min(j0 / 32 + lg, G - 1);
     struct Codes {
@@ -547,9 +557,10 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
         uint32_t p[16];
         decode_group(c.w0, c.w1, c.w2, mg, make_zero_sub(c.z), p);
         uint4* dst = reinterpret_cast<uint4*>(tile + lrow * T::BROW + lg * 64);
+        const int swz = T::b_swizzle(lg, lrow);
 #pragma unroll
         for (int q4 = 0; q4 < 4; q4++)
-            dst[q4] = make_uint4(p[4 * q4], p[4 * q4 + 1], p[4 * q4 + 2], p[4 * q4 + 3]);
+            dst[q4 ^ swz] = make_uint4(p[4 * q4], p[4 * q4 + 1], p[4 * q4 + 2], p[4 * q4 + 3]);
     };
 
     f32x16 acc[FM][FN];
@@ -568,7 +579,8 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
         atok[i] = tok * T::AROW;
         aswz[i] = a_swizzle(T::PIECES, tok);
     }
-    const int boff = (8 * h + ((lane & 15) >> 2)) * T::BROW + (wn * 32 * FN + 16 * ((lane >> 4) & 1) + 4 * (lane & 3)) * 2;
+    const int brow = (lane & 15) >> 2, bpiece = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    const int boff = (8 * h + brow) * T::BROW + wn * FN * 64 + ((bpiece ^ T::b_swizzle(wn * FN, brow)) << 4) + 8 * (lane & 1);
 
     // Step st computes on stage as_cur and tile st & 1; it starts the loads of step
     // st + 2 and decodes step st + 1 (its codes were loaded one step ago) into the
@@ -740,10 +752,10 @@ GatedBwdPlan gated_bwd_plan(int64_t N, int64_t K, int64_t kt, int64_t M)
         p.slabs = clampi((int64_t)(budget / ((size_t)M * kt * 4)), 1, p.slabs);
     p.slab_rows = cdiv(cdiv(N, p.slabs), 16) * 16;
     p.slabs = cdiv(N, p.slab_rows);
-    // launch 3: blocks of 64 rows, as many as the GPU holds at once (768, three
+    // launch 3: blocks of 64 rows, as many as the GPU holds at once (1024, four
     // waves per SIMD), 32 tokens per slab at least
     const int64_t rtiles = p.Np / 64;
-    p.tslabs = clampi(768 / rtiles, 1, cdiv(M, 32));
+    p.tslabs = clampi(1024 / rtiles, 1, cdiv(M, 32));
     if (kt > 0)
         p.tslabs = clampi((int64_t)(budget / ((size_t)N * kt * 4)), 1, p.tslabs);
     p.slab_tokens = cdiv(cdiv(M, p.tslabs), 8) * 8;
