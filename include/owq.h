@@ -548,12 +548,13 @@ size_t owq_linear_adapters_workspace_bytes(int32_t rank, int64_t M);
  *   y[m] = x[m] W^T + alpha_r (x[m] A_r^T) B_r^T,   r = which[m]
  * with W the packed layer ([PL] "Real-device acceleration" (paper "Acceleration on
  * Real Device", p.6) for the shared product). which: int32 [M]; any value outside
- * [0, count) means no adapter for that token: its output is then owq_linear's, bit
- * for bit. x A_r^T is summed in fp32 and kept in at least 22 bits of the row's
+ * [0, count) means no adapter for that token: its output is the shared product
+ * (bit for bit owq_linear's up to 16 tokens; above, summed in another order).
+ * x A_r^T is summed in fp32 and kept in at least 22 bits of the row's
  * largest value; the sum with the shared product is rounded to fp16 once. A token's
  * output depends on its own adapter only, also where another's holds values that
- * are not finite. Two launches (low-rank products; the linear with the second
- * products in its epilogue) per owq_linear launch of the same M. workspace: >=
+ * are not finite. Two launches: the low-rank products; the linear with the second
+ * products in its epilogue. workspace: >=
  * owq_linear_adapters_workspace_bytes(rank, M) bytes, 256-byte aligned, contents
  * ignored; calls sharing it must be ordered. Other arguments and errors as
  * owq_linear, plus OWQ_ERR_WORKSPACE, and OWQ_ERR_SHAPE for count and rank. */

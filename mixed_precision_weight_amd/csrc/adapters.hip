@@ -1,8 +1,9 @@
 // adapters.hip -- the shrink half of low-rank adapters (gfx950):
 //   t[m][c] = sum_j x[m][j] A_r[c][j],   r = which[m]
 // for tokens of many requests at once, each with its own adapter or none. The
-// expand half runs in the epilogue of the shared projection (owq_adapters.h), so
-// the whole operator is two launches.
+// expand half runs in the epilogue of the shared projection (owq_adapters.h: up to
+// 16 tokens in the linear's decode kernels, above in k_adapter_gemm), so the whole
+// operator is two launches.
 //
 // Work: A_r is rank x K fp16 (128 KB at rank 16, K = 4096), read once per tile of
 // 16 tokens that uses it; the products are negligible. A block takes a tile of 16
@@ -14,6 +15,7 @@
 // l % 16, both read from memory in 16-byte pieces without staging: every byte is
 // used by one lane once. Exact fp16 products, fp32 sums.
 #include "owq_adapters.h"
+#include "owq_pair_gemm.h"
 
 namespace owq {
 
@@ -32,8 +34,15 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void k_adapter_shrink(const uint
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, qd = lane >> 4;
-    const int r0 = (int)blockIdx.y * 16;
-    const int64_t m = (int64_t)blockIdx.x * 16 + l16;
+    // The rank tiles of a token tile run on one XCD (blocks go to the 8 XCDs in
+    // turn), so its x comes into one L2 once: 47 -> 25 us at 1000 tokens, rank 64,
+    // K = 11008
+    const int xcd = (int)blockIdx.x & 7, slot = (int)blockIdx.x >> 3;
+    const int rt = rpad >> 4;
+    const int tile = xcd + 8 * (slot / rt), r0 = (slot % rt) * 16;
+    if (tile * 16 >= M)
+        return;
+    const int64_t m = (int64_t)tile * 16 + l16;
     const int64_t mc = m < M ? m : M - 1;
     int id = which[mc];
     if (m >= M || id < 0 || id >= count)
@@ -48,11 +57,12 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void k_adapter_shrink(const uint
     for (int d = 0; left != 0; d++) {
         const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
         left &= ~__ballot(id == a);
-        if (d % (int)gridDim.z != (int)blockIdx.z)
+        if (d % (int)gridDim.y != (int)blockIdx.y)
             continue;
         const uint16_t* ar = A + ((int64_t)a * rank + min(r0 + l16, rank - 1)) * K + 8 * qd;
         float4_t acc[2] = {float4_t{0.0f, 0.0f, 0.0f, 0.0f}, float4_t{0.0f, 0.0f, 0.0f, 0.0f}};
-        for (int s = s0; s < s1; s += kShrinkFlight) {
+        // (a tile of padding ranks only stores its zeros)
+        for (int s = r0 < rank ? s0 : s1; s < s1; s += kShrinkFlight) {
             half8_t xv[kShrinkFlight], av[kShrinkFlight];
 #pragma unroll
             for (int u = 0; u < kShrinkFlight; u++) {
@@ -82,7 +92,83 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void k_adapter_shrink(const uint
             for (int r = 0; r < 4; r++) {
                 const int tok = 4 * qd + r;
                 if (__shfl(id, tok, 64) == a)
-                    t[((int64_t)blockIdx.x * 16 + tok) * rpad + r0 + l16] = live ? o[r] : 0.0f;
+                    t[((int64_t)tile * 16 + tok) * rpad + r0 + l16] = live ? o[r] : 0.0f;
+            }
+        }
+    }
+}
+
+// Low-rank adapters of 32 tokens (tk: this lane's) and 32 rows (n: this lane's):
+// z[r] += their sum for D element r, once per distinct adapter among the tokens.
+__device__ __forceinline__ void adapter_block(const AdapterArgs& ad, const AdapterToken& tk, int N, int n, f32x16& z)
+{
+    const int h = (threadIdx.x & 63) >> 5;
+    uint64_t left = __ballot(tk.id >= 0) & 0xffffffffu;
+    while (left != 0) {  // wave-uniform
+        const int id = __builtin_amdgcn_readlane(tk.id, __builtin_ctzll(left));
+        left &= ~__ballot(tk.id == id);
+        f32x16 s;
+#pragma unroll
+        for (int r = 0; r < 16; r++)
+            s[r] = 0.0f;
+#pragma unroll 1
+        for (int c = 8 * h; c < ad.rpad; c += 16) {
+            half8_t th, tl;
+            adapter_operand(tk, id, c, th, tl);
+            const half8_t w = adapter_weights(ad, id, N, n, c);
+            s = __builtin_amdgcn_mfma_f32_32x32x16_f16(th, w, s, 0, 0, 0);
+            s = __builtin_amdgcn_mfma_f32_32x32x16_f16(tl, w, s, 0, 0, 0);
+        }
+        const float f = tk.id == id ? tk.f : 0.0f;
+#pragma unroll
+        for (int r = 0; r < 16; r++) {
+            const float fr = __shfl(f, 8 * (r >> 2) + 4 * h + (r & 3), 64);
+            z[r] += fr != 0.0f ? fr * s[r] : 0.0f;
+        }
+    }
+}
+
+struct AdapterGemmArgs {
+    PairLayer L[2];  // the layer, twice
+    const uint16_t* x;
+    uint16_t* y;
+    int32_t M, N, K, mblocks;
+};
+
+// More than 16 tokens: the pair product (owq_pair_gemm.h) over two runs of rows of
+// the layer, the adapters added block by block before the one rounding (only one
+// block's sums are carried through their loop, so no register is spilled).
+template <int FM, int WN, int S>
+__global__ __launch_bounds__(64 * WN * S) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_adapter_gemm(
+    const AdapterGemmArgs a, const AdapterArgs ad)
+{
+    using T = PairTile<FM, WN, S>;
+    const int M = a.M, N = a.N;
+    const int m0 = ((int)blockIdx.x % a.mblocks) * T::BM;
+    const int n0 = ((int)blockIdx.x / a.mblocks) * 2 * T::BN;
+    const int rows[2] = {n0, n0 + T::BN};
+    f32x16 acc[2][FM];
+    if (!pair_gemm<FM, WN, S>(a.L, a.x, M, N, a.K, m0, rows, acc))
+        return;
+    const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+    const int wn = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) % WN;
+#pragma unroll
+    for (int i = 0; i < FM; i++) {
+        const int mt = m0 + 32 * i + l32;
+        const AdapterToken tk = adapter_token<2, 32>(ad, min(mt, M - 1), mt < M, h);
+#pragma unroll
+        for (int l = 0; l < 2; l++) {
+            const int n = rows[l] + wn * 32 + l32;
+            f32x16 z;
+#pragma unroll
+            for (int r = 0; r < 16; r++)
+                z[r] = 0.0f;
+            adapter_block(ad, tk, N, min(n, N - 1), z);
+#pragma unroll
+            for (int r = 0; r < 16; r++) {
+                const int m = m0 + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
+                if (m < M && n < N)
+                    a.y[(int64_t)m * N + n] = f2h(acc[l][i][r] + z[r]);
             }
         }
     }
@@ -106,9 +192,26 @@ hipError_t launch_adapter_shrink(const AdapterDesc& a, const uint16_t* x, int64_
     slots = slots < 1 ? 1 : (slots > 16 ? 16 : slots);
     if (slots > M)
         slots = M;
-    hipLaunchKernelGGL(k_adapter_shrink, dim3((unsigned)tiles, (unsigned)rt, (unsigned)slots),
-                       dim3(64 * kShrinkWaves), 0, s, x, a.A, a.which, a.t, (int)M, (int)K, a.count, a.rank, rpad);
+    const int64_t nb = (tiles + 7) / 8 * 8 * rt;
+    if (nb > INT32_MAX)
+        return hipErrorInvalidValue;
+    hipLaunchKernelGGL(k_adapter_shrink, dim3((unsigned)nb, (unsigned)slots), dim3(64 * kShrinkWaves), 0, s, x, a.A, a.which, a.t, (int)M, (int)K, a.count, a.rank, rpad);
     return hipGetLastError();
+}
+
+hipError_t launch_adapter_gemm(const LinearDesc& d, const AdapterDesc& ad, int64_t M, hipStream_t s)
+{
+    AdapterGemmArgs a{{pair_layer(d), pair_layer(d)}, d.x, d.y, (int32_t)M, (int32_t)d.N, (int32_t)d.K, 1};
+    return pair_tile(M, (d.N + 1) / 2, [&](auto fm, auto wn, auto sk) {
+        using T = PairTile<decltype(fm)::value, decltype(wn)::value, decltype(sk)::value>;
+        a.mblocks = (int32_t)((M + T::BM - 1) / T::BM);
+        const int64_t nb = (int64_t)a.mblocks * ((d.N + 2 * T::BN - 1) / (2 * T::BN));
+        if (nb > INT32_MAX)
+            return hipErrorInvalidValue;
+        hipLaunchKernelGGL((k_adapter_gemm<decltype(fm)::value, decltype(wn)::value, decltype(sk)::value>),
+                           dim3((unsigned)nb), dim3(T::NT), 0, s, a, adapter_args(ad));
+        return hipGetLastError();
+    });
 }
 
 }  // namespace owq

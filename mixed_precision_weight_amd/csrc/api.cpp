@@ -153,10 +153,10 @@ owq_status check_gated(const owq_layer* gate, const owq_layer* up, int64_t M, co
 
 namespace owq {
 
-hipError_t launch_linear_any(const LinearDesc& d, int64_t M, hipStream_t s, const AdapterDesc* ad)
+hipError_t launch_linear_any(const LinearDesc& d, int64_t M, hipStream_t s)
 {
     if (M >= gemm_min_m())
-        return launch_gemm(d, M, s, ad);
+        return launch_gemm(d, M, s);
     // decode kernels, in token slices of the chosen kernel's capacity
     hipError_t e = hipSuccess;
     for (int64_t m0 = 0; m0 < M && e == hipSuccess;) {
@@ -166,14 +166,7 @@ hipError_t launch_linear_any(const LinearDesc& d, int64_t M, hipStream_t s, cons
         LinearDesc dm = d;
         dm.x = d.x + m0 * d.K;
         dm.y = d.y + m0 * d.N;
-        AdapterDesc am;
-        if (ad) {
-            am = *ad;
-            am.which = ad->which + m0;
-            am.t = ad->t + m0 * adapter_rpad(ad->rank);
-        }
-        e = mat ? launch_mfv(&dm, 1, (int)mm, s, ad ? &am : nullptr)
-                : launch_gemv(&dm, 1, (int)mm, s, ad ? &am : nullptr);
+        e = mat ? launch_mfv(&dm, 1, (int)mm, s) : launch_gemv(&dm, 1, (int)mm, s);
         m0 += mm;
     }
     return e;
@@ -914,7 +907,15 @@ owq_status owq_linear_adapters(const owq_layer* L, const owq_adapters* ad, const
     const owq::AdapterDesc a{ad->A, ad->B, ad->alpha, which, static_cast<float*>(workspace), ad->count, ad->rank};
     hipError_t e = owq::launch_adapter_shrink(a, x, M, L->K, (hipStream_t)stream);
     if (e == hipSuccess)
-        e = owq::launch_linear_any(desc_of(L, x, y), M, (hipStream_t)stream, &a);
+    {
+        const owq::LinearDesc d = desc_of(L, x, y);
+        if (M > owq::kMfvMaxM)
+            e = owq::launch_adapter_gemm(d, a, M, (hipStream_t)stream);
+        else if (owq::decode_on_matrix_cores(M))
+            e = owq::launch_mfv(&d, 1, (int)M, (hipStream_t)stream, &a);
+        else
+            e = owq::launch_gemv(&d, 1, (int)M, (hipStream_t)stream, &a);
+    }
     return hip_status(e, "owq_linear_adapters launch");
 }
 

@@ -22,25 +22,16 @@
 #include "owq_device.h"
 #include "owq_gemv.h"
 #include "owq_launch.h"
+#include "owq_pair_gemm.h"
 
 namespace owq {
 
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-struct GatedLayer {
-    const uint32_t* q;
-    const uint16_t* s;
-    const uint8_t* z;
-    const int32_t* idx;
-    const uint16_t* ww;
-    int32_t k;
-};
 
 struct GatedArgs {
-    GatedLayer L[2];  // gate, up
+    PairLayer L[2];  // gate, up
     const uint16_t* x;
     uint16_t* h;
     float* g;  // NULL: not kept
@@ -48,11 +39,6 @@ struct GatedArgs {
     int32_t M, N, K, act;
     int32_t mblocks;  // token blocks of the GEMM form (the fastest-varying block index)
 };
-
-__device__ __forceinline__ half8_t gh8(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
-{
-    return __builtin_bit_cast(half8_t, make_uint4(a, b, c, d));
-}
 
 // ------------------------------------------------------------- one or two tokens
 // The linear's decode kernel (gemv.hip) with R = 2 RP rows per wave: rows
@@ -125,7 +111,7 @@ __device__ __forceinline__ void gated_gemv_body(const GatedArgs& a)
     float wwv[R][2], xw[2][M][2];
 #pragma unroll
     for (int r = 0; r < R; r++) {
-        const GatedLayer& L = a.L[r / RP];
+        const PairLayer& L = a.L[r / RP];
         const int row = min(row0 + r % RP, N - 1);
 #pragma unroll
         for (int v = 0; v < 2; v++) {
@@ -199,7 +185,7 @@ __device__ __forceinline__ void gated_gemv_body(const GatedArgs& a)
                     for (int r = 0; r < R; r++) {
                         uint32_t p[4];
                         decode_quad<qd>(cw[r][u].x, cw[r][u].y, cw[r][u].z, mg, make_zero_sub(zr[r]), p);
-                        const half8_t bq = gh8(p[0], p[1], p[2], p[3]);
+                        const half8_t bq = pair_h8(p[0], p[1], p[2], p[3]);
 #pragma unroll
                         for (int m = 0; m < M; m++)
                             macc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, xv[m]), bq,
@@ -266,7 +252,7 @@ __device__ __forceinline__ void gated_gemv_body(const GatedArgs& a)
                     part[r] += wwv[r][v] * xw[r / RP][m][v];
             }
         }
-        auto tail = [&](const GatedLayer& L, int r, float& sum) {  // weak columns from the 129th, from global memory
+        auto tail = [&](const PairLayer& L, int r, float& sum) {  // weak columns from the 129th, from global memory
             const int row = min(row0 + r, N - 1);
             for (int c = lane + 128; c < L.k; c += 64) {
                 int j = L.idx[c];
@@ -313,11 +299,6 @@ struct GatedShape {
     static constexpr int CL = 16 * CQ / 64;
     static_assert(GC % 16 == 0 && (16 * CQ) % 64 == 0 && CRS % 16 == 0, "codes and x must split evenly");
 };
-
-__device__ __forceinline__ void gated_dma(__amdgpu_buffer_rsrc_t r, char* lds, int voff)
-{
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff, 0, 0, 0);
-}
 
 template <int U, int MC, int W, int S, int D>
 __global__ __launch_bounds__(64 * W * S) void k_gated_mfv(const GatedArgs a)
@@ -366,7 +347,7 @@ __global__ __launch_bounds__(64 * W * S) void k_gated_mfv(const GatedArgs a)
             const int m = qi / PT, part = qi % PT;
             const int g = cc * GC + part * 16 + (lane >> 2);
             const int off = (min(m, M - 1) * K + g * 32) * 2 + (lane & 3) * 16;
-            gated_dma(xr, stage + m * RS + part * 1024, off + (g >= G ? 0x40000000 : dead));
+            pair_dma(xr, stage + m * RS + part * 1024, off + (g >= G ? 0x40000000 : dead));
         }
     };
     typedef uint4 QRegs[2][CL];
@@ -427,7 +408,7 @@ __global__ __launch_bounds__(64 * W * S) void k_gated_mfv(const GatedArgs a)
                         const half8_t av = __builtin_bit_cast(
                             half8_t, *reinterpret_cast<const uint4*>(cur + arow + 4 * u * 64 + st * 16));
                         accu[l][u % AU] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                            av, gh8(p[4 * st], p[4 * st + 1], p[4 * st + 2], p[4 * st + 3]), accu[l][u % AU], 0, 0, 0);
+                            av, pair_h8(p[4 * st], p[4 * st + 1], p[4 * st + 2], p[4 * st + 3]), accu[l][u % AU], 0, 0, 0);
                     }
                 }
             }
@@ -485,7 +466,7 @@ __global__ __launch_bounds__(64 * W * S) void k_gated_mfv(const GatedArgs a)
     const uint16_t* xm = a.x + (int64_t)min(l16, M - 1) * K;
 #pragma unroll
     for (int l = 0; l < 2; l++) {
-        const GatedLayer& L = a.L[l];
+        const PairLayer& L = a.L[l];
         acc[l] *= sc[l];
         const uint16_t* wr = L.ww + (int64_t)(brow + rloc) * L.k;
         for (int cs2 = 0; cs2 < L.k; cs2 += 32) {
@@ -505,8 +486,8 @@ __global__ __launch_bounds__(64 * W * S) void k_gated_mfv(const GatedArgs a)
                 bw[e2] = wv[0] | (wv[1] << 16);
                 aw[e2] = xv[0] | (xv[1] << 16);
             }
-            acc[l] = __builtin_amdgcn_mfma_f32_16x16x32_f16(gh8(aw[0], aw[1], aw[2], aw[3]),
-                                                           gh8(bw[0], bw[1], bw[2], bw[3]), acc[l], 0, 0, 0);
+            acc[l] = __builtin_amdgcn_mfma_f32_16x16x32_f16(pair_h8(aw[0], aw[1], aw[2], aw[3]),
+                                                           pair_h8(bw[0], bw[1], bw[2], bw[3]), acc[l], 0, 0, 0);
         }
     }
 
@@ -530,225 +511,35 @@ __global__ __launch_bounds__(64 * W * S) void k_gated_mfv(const GatedArgs a)
 }
 
 // ------------------------------------------------------------- prompts, training
-// The linear's prefill kernel (gemm.hip, k_gemm_dma: x by direct-to-LDS loads three
-// chunks deep, weights decoded into the B operands) over FM x 32 tokens and FP x 32
-// rows of gate and of up per wave, WM x WN waves per block.
-template <int FM, int FP, int WM, int WN>
-struct GatedTile {
-    static constexpr int NT = 64 * WM * WN;
-    static constexpr int BM = 32 * FM * WM;
-    static constexpr int BN = 32 * FP * WN;  // rows of each layer
-    static constexpr int STAGE = BM * 128;
-    static constexpr int DPW = STAGE / 16 / NT;
-    static_assert(STAGE % (16 * NT) == 0, "a stage must split evenly over the threads");
-};
-
-template <int FM, int FP, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_gated_gemm(
-    const GatedArgs a)
+// The pair product (owq_pair_gemm.h) with gate's rows as one set and up's as the
+// other: a wave has the same tokens and rows of both.
+template <int FM, int WN, int S>
+__global__ __launch_bounds__(64 * WN * S) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_gated_gemm(const GatedArgs a)
 {
-    using T = GatedTile<FM, FP, WM, WN>;
-    constexpr int BM = T::BM, BN = T::BN, STAGE = T::STAGE, DPW = T::DPW;
-    __shared__ __attribute__((aligned(1024))) char xs0[STAGE];
-    __shared__ __attribute__((aligned(1024))) char xs1[STAGE];
-    __shared__ __attribute__((aligned(1024))) char xs2[STAGE];
-
-    const int M = a.M, N = a.N, K = a.K;
-    const int G = K >> 5;
-    const int nchunks = (G + 1) >> 1;
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave % WM, wn = wave / WM;
-    const int l32 = lane & 31, h = lane >> 5;
-    const int m0 = ((int)blockIdx.x % a.mblocks) * BM;
-    const int n0 = ((int)blockIdx.x / a.mblocks) * BN;
-    const int mv = min(BM, M - m0);
-    const int nv = min(BN, N - n0);
-
-    const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint16_t*>(a.x) + (int64_t)m0 * K, (short)0, mv * K * 2, 0x00020000);
-    __amdgpu_buffer_rsrc_t qr[2];
-#pragma unroll
-    for (int l = 0; l < 2; l++)
-        qr[l] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint32_t*>(a.L[l].q) + (int64_t)n0 * G * 3, (short)0,
-                                                  nv * G * 12, 0x00020000);
-
-    // DMA unit u: token u / 8, slot u % 8 holds piece slot ^ (token & 7); with an
-    // odd group count the last chunk's second group is read out of range (zeros)
-    const int last = nchunks - 1;
-    const bool odd_tail = (G & 1) != 0;
-    int xsrc[DPW], xdead[DPW];
-#pragma unroll
-    for (int t = 0; t < DPW; t++) {
-        const int u = (wave * DPW + t) * 64 + lane;
-        const int row = u >> 3, piece = (u & 7) ^ (row & 7);
-        xsrc[t] = min(row, mv - 1) * K * 2 + piece * 16;
-        xdead[t] = (odd_tail && piece >= 4) ? 0x40000000 : 0;
-    }
-    auto dma = [&](int c, char* stage) {
-        const int cc = min(c, last);
-        const int dead = c > last ? 0x40000000 : 0;
-#pragma unroll
-        for (int t = 0; t < DPW; t++)
-            gated_dma(xr, stage + (wave * DPW + t) * 1024, xsrc[t] + cc * 128 + (cc == last ? xdead[t] : 0) + dead);
-    };
-
-    const int rbase = wn * 32 * FP + l32;
-    auto row_of = [&](int f) { return min(rbase + 32 * f, nv - 1); };
-    uint32_t zpk = 0;  // zero points: byte l FP + f
-#pragma unroll
-    for (int l = 0; l < 2; l++)
-#pragma unroll
-        for (int f = 0; f < FP; f++)
-            zpk |= (uint32_t)a.L[l].z[n0 + row_of(f)] << (8 * (l * FP + f));
-    typedef u32x3 QRegs[2][FP];
-    auto load_q = [&](int c, QRegs& cw) {
-        const int g = min(2 * min(c, last) + h, G - 1);
-        const int dead = c > last ? 0x40000000 : 0;
-#pragma unroll
-        for (int l = 0; l < 2; l++)
-#pragma unroll
-            for (int f = 0; f < FP; f++)
-                cw[l][f] = __builtin_amdgcn_raw_buffer_load_b96(qr[l], (row_of(f) * G + g) * 12 + dead, 0, 0);
-    };
-
-    const Magic mg = make_magic();
-    f32x16 acc[2][FM][FP];
-#pragma unroll
-    for (int l = 0; l < 2; l++)
-#pragma unroll
-        for (int i = 0; i < FM; i++)
-#pragma unroll
-            for (int f = 0; f < FP; f++)
-#pragma unroll
-                for (int r = 0; r < 16; r++)
-                    acc[l][i][f][r] = 0.0f;
-
-    const int arow = (wm * 32 * FM + l32) * 128;
-    int aoff[4];
-#pragma unroll
-    for (int st = 0; st < 4; st++)
-        aoff[st] = ((h * 4 + st) ^ (l32 & 7)) * 16;
-    auto step = [&](int c, const char* cur, char* nxt2, const QRegs& qc, QRegs& q2) {
-        // x of chunk c has arrived once at most the codes of c and x and codes of
-        // c + 1 remain; after the barrier every wave's has, and every wave is done
-        // with the stage chunk c + 2 goes to
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * 2 * FP + DPW) : "memory");
-        dma(c + 2, nxt2);
-        load_q(c + 2, q2);
-        if (c < nchunks) {  // block-uniform
-            half8_t av[4][FM];
-#pragma unroll
-            for (int st = 0; st < 4; st++)
-#pragma unroll
-                for (int i = 0; i < FM; i++)
-                    av[st][i] =
-                        __builtin_bit_cast(half8_t, *reinterpret_cast<const uint4*>(cur + arow + i * 32 * 128 + aoff[st]));
-#pragma unroll
-            for (int l = 0; l < 2; l++)
-#pragma unroll
-                for (int f = 0; f < FP; f++) {
-                    uint32_t p[16];
-                    decode_group(qc[l][f].x, qc[l][f].y, qc[l][f].z, mg,
-                                 make_zero_sub((zpk >> (8 * (l * FP + f))) & 7u), p);
-#pragma unroll
-                    for (int st = 0; st < 4; st++) {
-                        const half8_t bv = gh8(p[4 * st], p[4 * st + 1], p[4 * st + 2], p[4 * st + 3]);
-#pragma unroll
-                        for (int i = 0; i < FM; i++)
-                            acc[l][i][f] =
-                                __builtin_amdgcn_mfma_f32_32x32x16_f16(av[st][i], bv, acc[l][i][f], 0, 0, 0);
-                    }
-                }
-        }
-    };
-
-    QRegs qa, qb, qc3;
-    dma(0, xs0);
-    load_q(0, qa);
-    asm volatile("" ::: "memory");
-    dma(1, xs1);
-    load_q(1, qb);
-    asm volatile("" ::: "memory");
-    for (int c = 0; c < nchunks; c += 3) {
-        step(c, xs0, xs2, qa, qc3);
-        step(c + 1, xs1, xs0, qb, qa);
-        step(c + 2, xs2, xs1, qc3, qb);
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may write LDS after the block has ended
-
-    // row steps, then the weak columns as 16-deep steps
-#pragma unroll
-    for (int l = 0; l < 2; l++) {
-        const GatedLayer& L = a.L[l];
-#pragma unroll
-        for (int f = 0; f < FP; f++) {
-            const float sc = h2f(L.s[n0 + row_of(f)]);
-#pragma unroll
-            for (int i = 0; i < FM; i++)
-#pragma unroll
-                for (int r = 0; r < 16; r++)
-                    acc[l][i][f][r] *= sc;
-        }
-        for (int cs = 0; cs < L.k; cs += 16) {
-            uint32_t jw[8];
-            bool on[8];
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-                const int c = cs + 8 * h + e;
-                on[e] = c < L.k;
-                const int j = L.idx[min(c, L.k - 1)];
-                jw[e] = (uint32_t)((j >= 0 && j < K) ? j : 0);
-            }
-            uint32_t bw[FP][4];
-#pragma unroll
-            for (int f = 0; f < FP; f++) {
-                const uint16_t* wr = L.ww + (int64_t)(n0 + row_of(f)) * L.k;
-#pragma unroll
-                for (int e2 = 0; e2 < 4; e2++) {
-                    const int c = cs + 8 * h + 2 * e2;
-                    const uint32_t lo = on[2 * e2] ? wr[c] : 0u;
-                    const uint32_t hi = on[2 * e2 + 1] ? wr[c + 1] : 0u;
-                    bw[f][e2] = lo | (hi << 16);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < FM; i++) {
-                const uint16_t* xm = a.x + (int64_t)(m0 + min(wm * 32 * FM + 32 * i + l32, mv - 1)) * K;
-                uint32_t aw[4];
-#pragma unroll
-                for (int e2 = 0; e2 < 4; e2++) {
-                    const uint32_t lo = on[2 * e2] ? xm[jw[2 * e2]] : 0u;
-                    const uint32_t hi = on[2 * e2 + 1] ? xm[jw[2 * e2 + 1]] : 0u;
-                    aw[e2] = lo | (hi << 16);
-                }
-#pragma unroll
-                for (int f = 0; f < FP; f++)
-                    acc[l][i][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                        gh8(aw[0], aw[1], aw[2], aw[3]), gh8(bw[f][0], bw[f][1], bw[f][2], bw[f][3]), acc[l][i][f], 0,
-                        0, 0);
-            }
-        }
-    }
-
+    using T = PairTile<FM, WN, S>;
+    const int M = a.M, N = a.N;
+    const int m0 = ((int)blockIdx.x % a.mblocks) * T::BM;
+    const int n0 = ((int)blockIdx.x / a.mblocks) * T::BN;
+    const int rows[2] = {n0, n0};
+    f32x16 acc[2][FM];
+    if (!pair_gemm<FM, WN, S>(a.L, a.x, M, N, a.K, m0, rows, acc))
+        return;
+    const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+    const int n = n0 + (__builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) % WN) * 32 + l32;
     // D element r of lane l: token 8 (r / 4) + 4 h + r % 4, row l % 32
     with_act(a.act, [&](auto act) {
 #pragma unroll
         for (int i = 0; i < FM; i++)
 #pragma unroll
-            for (int f = 0; f < FP; f++) {
-                const int n = n0 + wn * 32 * FP + 32 * f + l32;
-#pragma unroll
-                for (int r = 0; r < 16; r++) {
-                    const int m = m0 + wm * 32 * FM + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
-                    if (m < M && n < N) {
-                        const int64_t o = (int64_t)m * N + n;
-                        const float gv = acc[0][i][f][r], uv = acc[1][i][f][r];
-                        a.h[o] = f2h(act_value<decltype(act)::value>(gv) * uv);
-                        if (a.g) {
-                            a.g[o] = gv;
-                            a.u[o] = uv;
-                        }
+            for (int r = 0; r < 16; r++) {
+                const int m = m0 + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
+                if (m < M && n < N) {
+                    const int64_t o = (int64_t)m * N + n;
+                    const float gv = acc[0][i][r], uv = acc[1][i][r];
+                    a.h[o] = f2h(act_value<decltype(act)::value>(gv) * uv);
+                    if (a.g) {
+                        a.g[o] = gv;
+                        a.u[o] = uv;
                     }
                 }
             }
@@ -771,23 +562,16 @@ hipError_t gated_mfv(const GatedArgs& a, hipStream_t s)
     return hipGetLastError();
 }
 
-template <int FM, int FP, int WM, int WN>
+template <int FM, int WN, int S>
 hipError_t gated_gemm(GatedArgs a, hipStream_t s)
 {
-    using T = GatedTile<FM, FP, WM, WN>;
+    using T = PairTile<FM, WN, S>;
     a.mblocks = (int)(((int64_t)a.M + T::BM - 1) / T::BM);
     const int64_t nblocks = (int64_t)a.mblocks * (((int64_t)a.N + T::BN - 1) / T::BN);
     if (nblocks > INT32_MAX)
         return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_gated_gemm<FM, FP, WM, WN>), dim3((unsigned)nblocks), dim3(T::NT), 0, s, a);
+    hipLaunchKernelGGL((k_gated_gemm<FM, WN, S>), dim3((unsigned)nblocks), dim3(T::NT), 0, s, a);
     return hipGetLastError();
-}
-
-GatedLayer gated_layer(const LinearDesc& d)
-{
-    // with no weak columns, the weak arrays point at valid memory (never used)
-    return GatedLayer{d.q, d.s, d.z, d.k > 0 ? d.idx : reinterpret_cast<const int32_t*>(d.x),
-                      d.k > 0 ? d.ww : d.s, d.k};
 }
 
 }  // namespace
@@ -795,32 +579,30 @@ GatedLayer gated_layer(const LinearDesc& d)
 hipError_t launch_gated(const LinearDesc& gate, const LinearDesc& up, int64_t M, int act, uint16_t* h, float* g,
                         float* u, hipStream_t s)
 {
-    GatedArgs a{{gated_layer(gate), gated_layer(up)}, gate.x, h, g, u, (int32_t)M, (int32_t)gate.N, (int32_t)gate.K, act, 1};
+    GatedArgs a{{pair_layer(gate), pair_layer(up)}, gate.x, h, g, u, (int32_t)M, (int32_t)gate.N, (int32_t)gate.K, act, 1};
+    // Enough rows for four per wave: 1024 blocks of 8 rows of each layer stay busy
+    // longer than the launch takes to fill and drain. 28672 x 8192, us with four /
+    // two rows: M = 1 42.9 / 47.7, M = 2 50.6 / 66.4; 11008 x 4096: 11.2 / 10.7 and
+    // 14.5 / 14.3 (two rows of two tokens: v_dot2, 16.3 on the matrix cores)
+    const bool many = gate.N >= 16384;
     if (M == 1)
-        return gated_gemv<1, false, 1>(a, s);
+        return many ? gated_gemv<1, false, 2>(a, s) : gated_gemv<1, false, 1>(a, s);
     if (M == 2)
-        return gated_gemv<2, true, 1>(a, s);
+        return many ? gated_gemv<2, true, 2>(a, s) : gated_gemv<2, false, 1>(a, s);
+    // 4 row waves, or 2 x 2 K groups where the rows are few: us at M = 4, 28672 x
+    // 8192 46.7 / 53.0, 11008 x 4096 18.0 / 16.1; M = 8 48.1 / 55.0, 17.3 / 18.3, 2731 x
+    // 1056 10.1 / 8.7; M = 16 53.6 / 58.5, 18.2 / 20.4, 11.1 / 9.6 (codes two chunks
+    // ahead leave one wave per SIMD: 63 at M = 8)
     if (M <= 4)
-        return gated_mfv<4, 4, 2, 2, 1>(a, s);
+        return many ? gated_mfv<4, 4, 4, 1, 1>(a, s) : gated_mfv<4, 4, 2, 2, 1>(a, s);
+    const bool few = gate.N < 8192;
     if (M <= 8)
-        return gated_mfv<8, 8, 4, 1, 2>(a, s);
+        return few ? gated_mfv<4, 8, 2, 2, 1>(a, s) : gated_mfv<4, 8, 4, 1, 1>(a, s);
     if (M <= 16)
-        return gated_mfv<4, 16, 4, 1, 2>(a, s);
-    // The largest tile (tokens x rows of each layer) that still gives 600 blocks,
-    // more than two per CU: each layer 11008 x 4096, us with 128 x 128 / 128 x 64 /
-    // 64 x 64 / 64 x 32 / 32 x 32 at M = 64: 71 / 62 / 43 / 44 / 36, 128: 80 / 72 /
-    // 57 / 50 / 64, 256: 86 / 92 / 72 / 83 / 115, 512: 125 / 118 / 151 / 162 / 213,
-    // 2048: 388 / 433 / 485 / 571 / 802
-    auto blocks = [&](int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((gate.N + bn - 1) / bn); };
-    if (blocks(128, 128) >= 600)
-        return gated_gemm<4, 1, 1, 4>(a, s);
-    if (blocks(128, 64) >= 600)
-        return gated_gemm<4, 1, 1, 2>(a, s);
-    if (blocks(64, 64) >= 600)
-        return gated_gemm<2, 1, 1, 2>(a, s);
-    if (blocks(64, 32) >= 600)
-        return gated_gemm<2, 1, 1, 1>(a, s);
-    return gated_gemm<1, 1, 1, 1>(a, s);
+        return few ? gated_mfv<4, 16, 2, 2, 1>(a, s) : gated_mfv<4, 16, 4, 1, 1>(a, s);
+    return pair_tile(M, gate.N, [&](auto fm, auto wn, auto sk) {
+        return gated_gemm<decltype(fm)::value, decltype(wn)::value, decltype(sk)::value>(a, s);
+    });
 }
 
 }  // namespace owq

@@ -39,9 +39,7 @@
 // MALL, and an XCD's blocks share tokens of x in its L2 when the token blocks
 // number 8.
 #include <cstdlib>
-#include <type_traits>
 
-#include "owq_adapters.h"
 #include "owq_decode.h"
 #include "owq_device.h"
 #include "owq_launch.h"
@@ -84,77 +82,8 @@ struct Tile {
     static constexpr int LDS = 2 * BM * RB + KG * 64;   // double buffer + a spare staging row
 };
 
-struct NoAdapters {};
-
-// Low-rank adapters of 32 tokens (tk: this lane's) and 32 rows (n: this lane's):
-// z[r] += their sum for D element r, once per distinct adapter among the tokens.
-__device__ __forceinline__ void adapter_block(const AdapterArgs& ad, const AdapterToken& tk, int N, int n, f32x16& z)
-{
-    const int h = (threadIdx.x & 63) >> 5;
-    uint64_t left = __ballot(tk.id >= 0) & 0xffffffffu;
-    while (left != 0) {  // wave-uniform
-        const int id = __builtin_amdgcn_readlane(tk.id, __builtin_ctzll(left));
-        left &= ~__ballot(tk.id == id);
-        f32x16 s;
-#pragma unroll
-        for (int r = 0; r < 16; r++)
-            s[r] = 0.0f;
-#pragma unroll 1
-        for (int c = 8 * h; c < ad.rpad; c += 16) {
-            half8_t th, tl;
-            adapter_operand(tk, id, c, th, tl);
-            const half8_t w = adapter_weights(ad, id, N, n, c);
-            s = __builtin_amdgcn_mfma_f32_32x32x16_f16(th, w, s, 0, 0, 0);
-            s = __builtin_amdgcn_mfma_f32_32x32x16_f16(tl, w, s, 0, 0, 0);
-        }
-        const float f = tk.id == id ? tk.f : 0.0f;
-#pragma unroll
-        for (int r = 0; r < 16; r++) {
-            const float fr = __shfl(f, 8 * (r >> 2) + 4 * h + (r & 3), 64);
-            z[r] += fr != 0.0f ? fr * s[r] : 0.0f;
-        }
-    }
-}
-
-// Epilogue of a wave's FM x 32 tokens (from m0) and FN x 32 rows (from n0):
-// rounds to fp16 and stores; with adapters, adds them block by block, so that
-// only one block's sums are carried through their loop. D element r of lane l:
-// token 8 (r / 4) + 4 (l / 32) + r % 4, row l % 32.
-template <int FM, int FN, typename ADP>
-__device__ __forceinline__ void store_tile(const f32x16 (&acc)[FM][FN], uint16_t* y, int m0, int n0, int M, int N,
-                                           const ADP& ad)
-{
-    const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
-#pragma unroll
-    for (int i = 0; i < FM; i++) {
-        [[maybe_unused]] AdapterToken tk;
-        if constexpr (!std::is_same_v<ADP, NoAdapters>)
-            tk = adapter_token<2, 32>(ad, min(m0 + 32 * i + l32, M - 1), m0 + 32 * i + l32 < M, h);
-#pragma unroll
-        for (int f = 0; f < FN; f++) {
-            const int n = n0 + 32 * f + l32;
-            [[maybe_unused]] f32x16 z;
-            if constexpr (!std::is_same_v<ADP, NoAdapters>) {
-#pragma unroll
-                for (int r = 0; r < 16; r++)
-                    z[r] = 0.0f;
-                adapter_block(ad, tk, N, min(n, N - 1), z);
-            }
-#pragma unroll
-            for (int r = 0; r < 16; r++) {
-                const int m = m0 + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
-                float v = acc[i][f][r];
-                if constexpr (!std::is_same_v<ADP, NoAdapters>)
-                    v = z[r] != 0.0f ? v + z[r] : v;  // -0 stays -0 without an adapter
-                if (m < M && n < N)
-                    y[(int64_t)m * N + n] = f2h(v);
-            }
-        }
-    }
-}
-
-template <int FM, int FN, int WM, int WN, int KH, int WPE, typename ADP>
-__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_gemm(GemmArgs a, ADP ad)
+template <int FM, int FN, int WM, int WN, int KH, int WPE>
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_gemm(GemmArgs a)
 {
     using T = Tile<FM, FN, WM, WN, KH, WPE>;
     constexpr int NT = T::NT, BM = T::BM, BN = T::BN, KG = T::KG, RB = T::RB, XI = T::XI;
@@ -365,11 +294,23 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WP
         }
     }
 
-    store_tile<FM, FN>(acc, a.y, m0 + wm * 32 * FM, n0 + wn * 32 * FN, M, N, ad);
+    // D element r of lane l: token 8 (r / 4) + 4 h + r % 4, row l % 32
+#pragma unroll
+    for (int i = 0; i < FM; i++)
+#pragma unroll
+        for (int f = 0; f < FN; f++) {
+            const int n = n0 + wn * 32 * FN + 32 * f + l32;
+#pragma unroll
+            for (int r = 0; r < 16; r++) {
+                const int m = m0 + wm * 32 * FM + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
+                if (m < M && n < N)
+                    a.y[(int64_t)m * N + n] = f2h(acc[i][f][r]);
+            }
+        }
 }
 
-template <int FM, int FN, int WM, int WN, int KH, int WPE, typename ADP>
-hipError_t launch_tile(GemmArgs a, hipStream_t s, const ADP& ad)
+template <int FM, int FN, int WM, int WN, int KH, int WPE>
+hipError_t launch_tile(GemmArgs a, hipStream_t s)
 {
     using T = Tile<FM, FN, WM, WN, KH, WPE>;
     a.mblocks = (a.M + T::BM - 1) / T::BM;
@@ -377,11 +318,11 @@ hipError_t launch_tile(GemmArgs a, hipStream_t s, const ADP& ad)
     if (nblocks > INT32_MAX)
         return hipErrorInvalidValue;
     static const hipError_t attr =
-        hipFuncSetAttribute(reinterpret_cast<const void*>(&k_gemm<FM, FN, WM, WN, KH, WPE, ADP>),
+        hipFuncSetAttribute(reinterpret_cast<const void*>(&k_gemm<FM, FN, WM, WN, KH, WPE>),
                             hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS);
     if (attr != hipSuccess)
         return attr;
-    hipLaunchKernelGGL((k_gemm<FM, FN, WM, WN, KH, WPE, ADP>), dim3((unsigned)nblocks), dim3(T::NT), T::LDS, s, a, ad);
+    hipLaunchKernelGGL((k_gemm<FM, FN, WM, WN, KH, WPE>), dim3((unsigned)nblocks), dim3(T::NT), T::LDS, s, a);
     return hipGetLastError();
 }
 
@@ -408,8 +349,8 @@ struct DmaTile {
     static_assert(STAGE % (16 * NT) == 0, "a stage must split evenly over the threads");
 };
 
-template <int FM, int FN, int WM, int WN, typename ADP>
-__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_gemm_dma(GemmArgs a, ADP ad)
+template <int FM, int FN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_gemm_dma(GemmArgs a)
 {
     using T = DmaTile<FM, FN, WM, WN>;
     constexpr int BM = T::BM, BN = T::BN, STAGE = T::STAGE, DPW = T::DPW;
@@ -600,18 +541,30 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
         }
     }
 
-    store_tile<FM, FN>(acc, a.y, m0 + wm * 32 * FM, n0 + wn * 32 * FN, M, N, ad);
+    // D element r of lane l: token 8 (r / 4) + 4 h + r % 4, row l % 32
+#pragma unroll
+    for (int i = 0; i < FM; i++)
+#pragma unroll
+        for (int f = 0; f < FN; f++) {
+            const int n = n0 + wn * 32 * FN + 32 * f + l32;
+#pragma unroll
+            for (int r = 0; r < 16; r++) {
+                const int m = m0 + wm * 32 * FM + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
+                if (m < M && n < N)
+                    a.y[(int64_t)m * N + n] = f2h(acc[i][f][r]);
+            }
+        }
 }
 
-template <int FM, int FN, int WM, int WN, typename ADP>
-hipError_t launch_dma(GemmArgs a, hipStream_t s, const ADP& ad)
+template <int FM, int FN, int WM, int WN>
+hipError_t launch_dma(GemmArgs a, hipStream_t s)
 {
     using T = DmaTile<FM, FN, WM, WN>;
     a.mblocks = (a.M + T::BM - 1) / T::BM;
     const int64_t nblocks = (int64_t)a.mblocks * ((a.N + T::BN - 1) / T::BN);
     if (nblocks > INT32_MAX)
         return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_gemm_dma<FM, FN, WM, WN, ADP>), dim3((unsigned)nblocks), dim3(T::NT), 0, s, a, ad);
+    hipLaunchKernelGGL((k_gemm_dma<FM, FN, WM, WN>), dim3((unsigned)nblocks), dim3(T::NT), 0, s, a);
     return hipGetLastError();
 }
 
@@ -634,7 +587,7 @@ int64_t gemm_min_m()
     return v;
 }
 
-hipError_t launch_gemm(const LinearDesc& d, int64_t M, hipStream_t s, const AdapterDesc* ad)
+hipError_t launch_gemm(const LinearDesc& d, int64_t M, hipStream_t s)
 {
     GemmArgs a;
     a.q = d.q;
@@ -649,11 +602,9 @@ hipError_t launch_gemm(const LinearDesc& d, int64_t M, hipStream_t s, const Adap
     a.K = (int32_t)d.K;
     a.k = d.k;
     a.mblocks = 1;
-    // 128 tokens x 256 rows, 4 waves of 64 x 128; below, 32 tokens x 256 rows, 4 waves of 32 x 64
-    if (ad)
-        return M >= 128 ? launch_dma<2, 4, 2, 2>(a, s, adapter_args(*ad))
-                        : launch_tile<1, 2, 1, 4, 1, 2>(a, s, adapter_args(*ad));
-    return M >= 128 ? launch_dma<2, 4, 2, 2>(a, s, NoAdapters{}) : launch_tile<1, 2, 1, 4, 1, 2>(a, s, NoAdapters{});
+    if (M >= 128)
+        return launch_dma<2, 4, 2, 2>(a, s);     // 128 tokens x 256 rows, 4 waves of 64 x 128
+    return launch_tile<1, 2, 1, 4, 1, 2>(a, s);  // 32 tokens x 256 rows, 4 waves of 32 x 64
 }
 
 }  // namespace owq

@@ -73,7 +73,7 @@ __device__ __forceinline__ AdapterToken adapter_token(const AdapterArgs& ad, int
 __device__ __forceinline__ void adapter_operand(const AdapterToken& k, int id, int c, half8_t& hi, half8_t& lo)
 {
     float v[8] = {};
-    if (k.id == id) {
+    if (k.id == id && id >= 0) {
         const float4 a = *reinterpret_cast<const float4*>(k.t + c), b = *reinterpret_cast<const float4*>(k.t + c + 4);
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     }

@@ -122,11 +122,11 @@ hipError_t launch_pack_grouped(const uint16_t* W, int64_t N, int64_t K, const in
 // 1 <= M <= kGemvMaxM tokens; groups[l]: columns per scale group of layer l.
 hipError_t launch_gemv_grouped(const LinearDesc* d, const int64_t* groups, int count, int M, hipStream_t s);
 // Matrix-core GEMM for larger M.
-hipError_t launch_gemm(const LinearDesc& d, int64_t M, hipStream_t s, const AdapterDesc* ad = nullptr);
+hipError_t launch_gemm(const LinearDesc& d, int64_t M, hipStream_t s);
 
 // The linear on the latency-favoured form for any M: the GEMM from gemm_min_m()
 // tokens, else the decode kernels in token slices (api.cpp).
-hipError_t launch_linear_any(const LinearDesc& d, int64_t M, hipStream_t s, const AdapterDesc* ad = nullptr);
+hipError_t launch_linear_any(const LinearDesc& d, int64_t M, hipStream_t s);
 
 // Low-rank adapters beside a linear: t (fp32 [M][adapter_rpad(rank)], workspace)
 // by launch_adapter_shrink, then the linear's launchers with the adapters given.
@@ -141,6 +141,9 @@ struct AdapterDesc {
 constexpr int adapter_rpad(int rank) { return (rank + 31) & ~31; }
 size_t adapter_workspace_bytes(int rank, int64_t M);
 hipError_t launch_adapter_shrink(const AdapterDesc& a, const uint16_t* x, int64_t M, int64_t K, hipStream_t s);
+// The shared product with the adapters' second products: up to 16 tokens
+// launch_gemv / launch_mfv with the adapters given, above this.
+hipError_t launch_adapter_gemm(const LinearDesc& d, const AdapterDesc& ad, int64_t M, hipStream_t s);
 
 // ------------------------------------------------------ storage-favoured form --
 // Dense columns rounded up to whole groups; workspace bytes of the product.

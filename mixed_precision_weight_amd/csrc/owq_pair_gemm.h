@@ -1,0 +1,313 @@
+// owq_pair_gemm.h -- matrix-core product of a tile of tokens with two sets of
+// packed rows (gfx950), shared by the gated block (rows of gate and of up) and the
+// linear with low-rank adapters (two runs of rows of one layer):
+//   acc[l][i] = x[m0 ..] W_l^T for 32 FM tokens and 32 rows per wave of set l = 0, 1
+//
+// A wave holds all the block's tokens and 32 rows of each set, so every code group
+// is decoded once per block, straight into the B operand of v_mfma_f32_32x32x16_f16
+// (lane l: row l % 32, group 2 chunk + l / 32; the 32 exact q - z of a group feed
+// four steps). x goes by direct-to-LDS loads three chunks of 64 columns deep, codes
+// two chunks ahead in registers, one barrier per chunk. S groups of WN waves split
+// K (stages of their own, all in step) and are added in LDS at the end: where tokens
+// and rows give few waves, and where K is long, the chain of chunks is what counts.
+#pragma once
+
+#include <type_traits>
+
+#include "owq_decode.h"
+#include "owq_device.h"
+#include "owq_launch.h"
+
+namespace owq {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float pair_f4 __attribute__((ext_vector_type(4)));
+
+struct PairLayer {
+    const uint32_t* q;
+    const uint16_t* s;
+    const uint8_t* z;
+    const int32_t* idx;
+    const uint16_t* ww;
+    int32_t k;
+};
+
+inline PairLayer pair_layer(const LinearDesc& d)
+{
+    // with no weak columns, the weak arrays point at valid memory (never used)
+    return PairLayer{d.q, d.s, d.z, d.k > 0 ? d.idx : reinterpret_cast<const int32_t*>(d.x), d.k > 0 ? d.ww : d.s, d.k};
+}
+
+__device__ __forceinline__ half8_t pair_h8(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    return __builtin_bit_cast(half8_t, make_uint4(a, b, c, d));
+}
+
+__device__ __forceinline__ void pair_dma(__amdgpu_buffer_rsrc_t r, char* lds, int voff)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff, 0, 0, 0);
+}
+
+template <int FM, int WN, int S>
+struct PairTile {
+    static constexpr int NT = 64 * WN * S;
+    static constexpr int BM = 32 * FM;
+    static constexpr int BN = 32 * WN;  // rows of each set
+    static constexpr int STAGE = BM * 128;
+    static constexpr int DPW = STAGE / 16 / (64 * WN);
+    static_assert(STAGE % (16 * 64 * WN) == 0, "a stage must split evenly over a group's threads");
+    static_assert((S - 1) * WN * 4096 <= S * STAGE, "one accumulator block of every other group fits a stage set");
+};
+
+// The sums of one wave of the block (its rows: row set l starts at n0[l], which may
+// lie past N; tokens from m0). Returns false for the K groups that handed theirs
+// over, whose waves are done.
+template <int FM, int WN, int S>
+__device__ __forceinline__ bool pair_gemm(const PairLayer (&L)[2], const uint16_t* x, int M, int N, int K, int m0,
+                                          const int (&n0)[2], f32x16 (&acc)[2][FM])
+{
+    using T = PairTile<FM, WN, S>;
+    constexpr int BM = T::BM, BN = T::BN, STAGE = T::STAGE, DPW = T::DPW;
+    __shared__ __attribute__((aligned(1024))) char xs0[S][STAGE];
+    __shared__ __attribute__((aligned(1024))) char xs1[S][STAGE];
+    __shared__ __attribute__((aligned(1024))) char xs2[S][STAGE];
+
+    const int G = K >> 5;
+    const int nchunks = (G + 1) >> 1;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wid % WN, kg = wid / WN;  // row wave in the block, K group
+    const int per = (nchunks + S - 1) / S;
+    const int c0 = kg * per, c1 = min(nchunks, c0 + per);  // this group's chunks (none: it only keeps the barriers)
+    const int l32 = lane & 31, h = lane >> 5;
+    const int mv = min(BM, M - m0);
+
+    const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t*>(x) + (int64_t)m0 * K, (short)0, mv * K * 2, 0x00020000);
+    // row sets: first row and rows (a set past N reads the last row; never stored)
+    int nb[2], nv[2];
+    __amdgpu_buffer_rsrc_t qr[2];
+#pragma unroll
+    for (int l = 0; l < 2; l++) {
+        nb[l] = min(n0[l], N - 1);
+        nv[l] = min(BN, N - nb[l]);
+        qr[l] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint32_t*>(L[l].q) + (int64_t)nb[l] * G * 3, (short)0,
+                                                  nv[l] * G * 12, 0x00020000);
+    }
+
+    // DMA unit u: token u / 8, slot u % 8 holds piece slot ^ (token & 7); with an
+    // odd group count the last chunk's second group is read out of range (zeros),
+    // as are the chunks past the group's end
+    const int last = nchunks - 1;
+    const bool odd_tail = (G & 1) != 0;
+    int xsrc[DPW], xdead[DPW];
+#pragma unroll
+    for (int t = 0; t < DPW; t++) {
+        const int u = (wn * DPW + t) * 64 + lane;
+        const int row = u >> 3, piece = (u & 7) ^ (row & 7);
+        xsrc[t] = min(row, mv - 1) * K * 2 + piece * 16;
+        xdead[t] = (odd_tail && piece >= 4) ? 0x40000000 : 0;
+    }
+    auto dma = [&](int c, char* stage) {
+        const int cc = min(c, last);
+        const int dead = c >= c1 ? 0x40000000 : 0;
+#pragma unroll
+        for (int t = 0; t < DPW; t++)
+            pair_dma(xr, stage + (wn * DPW + t) * 1024, xsrc[t] + cc * 128 + (cc == last ? xdead[t] : 0) + dead);
+    };
+
+    // this lane's row of each set, relative to the set's first
+    int row[2];
+    ZeroSub zs[2];
+#pragma unroll
+    for (int l = 0; l < 2; l++) {
+        row[l] = min(wn * 32 + l32, nv[l] - 1);
+        zs[l] = make_zero_sub((uint32_t)L[l].z[nb[l] + row[l]]);
+    }
+    typedef u32x3 QRegs[2];
+    auto load_q = [&](int c, QRegs& cw) {
+        const int g = min(2 * min(c, last) + h, G - 1);
+        const int dead = c >= c1 ? 0x40000000 : 0;
+#pragma unroll
+        for (int l = 0; l < 2; l++)
+            cw[l] = __builtin_amdgcn_raw_buffer_load_b96(qr[l], (row[l] * G + g) * 12 + dead, 0, 0);
+    };
+
+    const Magic mg = make_magic();
+#pragma unroll
+    for (int l = 0; l < 2; l++)
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+#pragma unroll
+            for (int r = 0; r < 16; r++)
+                acc[l][i][r] = 0.0f;
+
+    const int arow = l32 * 128;
+    int aoff[4];
+#pragma unroll
+    for (int st = 0; st < 4; st++)
+        aoff[st] = ((h * 4 + st) ^ (l32 & 7)) * 16;
+    auto step = [&](int c, const char* cur, char* nxt2, const QRegs& qc, QRegs& q2) {
+        // x of chunk c has arrived once at most the codes of c and x and codes of
+        // c + 1 remain; after the barrier every wave's has, and every wave is done
+        // with the stage chunk c + 2 goes to
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(4 + DPW) : "memory");
+        dma(c + 2, nxt2);
+        load_q(c + 2, q2);
+        if (c < c1) {  // wave-uniform
+            half8_t av[4][FM];
+#pragma unroll
+            for (int st = 0; st < 4; st++)
+#pragma unroll
+                for (int i = 0; i < FM; i++)
+                    av[st][i] =
+                        __builtin_bit_cast(half8_t, *reinterpret_cast<const uint4*>(cur + arow + i * 32 * 128 + aoff[st]));
+#pragma unroll
+            for (int l = 0; l < 2; l++) {
+                uint32_t p[16];
+                decode_group(qc[l].x, qc[l].y, qc[l].z, mg, zs[l], p);
+#pragma unroll
+                for (int st = 0; st < 4; st++) {
+                    const half8_t bv = pair_h8(p[4 * st], p[4 * st + 1], p[4 * st + 2], p[4 * st + 3]);
+#pragma unroll
+                    for (int i = 0; i < FM; i++)
+                        acc[l][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(av[st][i], bv, acc[l][i], 0, 0, 0);
+                }
+            }
+        }
+    };
+
+    QRegs qa, qb, qc3;
+    dma(c0, xs0[kg]);
+    load_q(c0, qa);
+    asm volatile("" ::: "memory");
+    dma(c0 + 1, xs1[kg]);
+    load_q(c0 + 1, qb);
+    asm volatile("" ::: "memory");
+    for (int c = c0; c < c0 + per; c += 3) {  // the same trip count in every group
+        step(c, xs0[kg], xs2[kg], qa, qc3);
+        step(c + 1, xs1[kg], xs0[kg], qb, qa);
+        step(c + 2, xs2[kg], xs1[kg], qc3, qb);
+    }
+    // no load may write LDS after this point (reused below, and the block may end)
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+    if constexpr (S > 1) {  // the other groups hand their sums to group 0, a block of accumulators at a time
+        pair_f4* red = reinterpret_cast<pair_f4*>(&xs0[0][0]);
+#pragma unroll
+        for (int l = 0; l < 2; l++)
+#pragma unroll
+            for (int i = 0; i < FM; i++) {
+                __syncthreads();
+                if (kg > 0)
+#pragma unroll
+                    for (int r = 0; r < 16; r += 4)
+                        red[(((kg - 1) * WN + wn) * 4 + r / 4) * 64 + lane] =
+                            pair_f4{acc[l][i][r], acc[l][i][r + 1], acc[l][i][r + 2], acc[l][i][r + 3]};
+                __syncthreads();
+                if (kg == 0)
+#pragma unroll
+                    for (int g2 = 1; g2 < S; g2++)
+#pragma unroll
+                        for (int r = 0; r < 16; r += 4) {
+                            const pair_f4 v = red[(((g2 - 1) * WN + wn) * 4 + r / 4) * 64 + lane];
+#pragma unroll
+                            for (int e = 0; e < 4; e++)
+                                acc[l][i][r + e] += v[e];
+                        }
+            }
+        if (kg > 0)
+            return false;
+    }
+
+    // row steps, then the weak columns as 16-deep steps
+#pragma unroll
+    for (int l = 0; l < 2; l++) {
+        const PairLayer& P = L[l];
+        const float sc = h2f(P.s[nb[l] + row[l]]);
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+#pragma unroll
+            for (int r = 0; r < 16; r++)
+                acc[l][i][r] *= sc;
+        const uint16_t* wr = P.ww + (int64_t)(nb[l] + row[l]) * P.k;
+        for (int cs = 0; cs < P.k; cs += 16) {
+            uint32_t jw[8], bw[4];
+            bool on[8];
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                const int c = cs + 8 * h + e;
+                on[e] = c < P.k;
+                const int j = P.idx[min(c, P.k - 1)];
+                jw[e] = (uint32_t)((j >= 0 && j < K) ? j : 0);
+            }
+#pragma unroll
+            for (int e2 = 0; e2 < 4; e2++) {
+                const int c = cs + 8 * h + 2 * e2;
+                const uint32_t lo = on[2 * e2] ? wr[c] : 0u;
+                const uint32_t hi = on[2 * e2 + 1] ? wr[c + 1] : 0u;
+                bw[e2] = lo | (hi << 16);
+            }
+#pragma unroll
+            for (int i = 0; i < FM; i++) {
+                const uint16_t* xm = x + (int64_t)(m0 + min(32 * i + l32, mv - 1)) * K;
+                uint32_t aw[4];
+#pragma unroll
+                for (int e2 = 0; e2 < 4; e2++) {
+                    const uint32_t lo = on[2 * e2] ? xm[jw[2 * e2]] : 0u;
+                    const uint32_t hi = on[2 * e2 + 1] ? xm[jw[2 * e2 + 1]] : 0u;
+                    aw[e2] = lo | (hi << 16);
+                }
+                acc[l][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pair_h8(aw[0], aw[1], aw[2], aw[3]),
+                                                                   pair_h8(bw[0], bw[1], bw[2], bw[3]), acc[l][i], 0, 0,
+                                                                   0);
+            }
+        }
+    }
+    return true;
+}
+
+// The tile for M tokens and `rows` rows of each set: f(FM, WN, S) as integral
+// constants. Measured for the gated block (us at the M given, N x K of each layer;
+// FM WN S):
+//   11008 x 4096  32: 114 28, 112 29, 111 32, 222 33      64: 111 34, 112 36, 222 38
+//                128: 211 49, 222 50, 111 62              256: 221 72, 241 80, 211 82
+//                512: 421 117, 441 124, 241 133           2048: 441 377, 421 432
+//   4096 x 11008  64: 114 43, 112 46, 222 63              128: 112 59, 111 68, 222 66
+//                256: 222 77, 241 96, 111 102             512: 241 112, 222 121, 441 157
+//   28672 x 8192  64: 241 95, 222 98, 441 128             128: 441 138, 241 153
+//   2731 x 1056   64: 114 12.7, 111 14.9                  512: 211 25, 221 29
+// The list takes the largest tile that still gives 600 blocks, more than two per
+// CU; where a larger one gives about one block per CU of several waves, that.
+template <typename F>
+hipError_t pair_tile(int64_t M, int64_t rows, F f)
+{
+    auto blocks = [&](int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((rows + bn - 1) / bn); };
+#define OWQ_TILE(FM, WN, S)                                                                               \
+    return f(std::integral_constant<int, FM>{}, std::integral_constant<int, WN>{},                  \
+             std::integral_constant<int, S>{})
+    if (blocks(128, 128) >= 600)
+        OWQ_TILE(4, 4, 1);
+    if (blocks(128, 64) >= 600)
+        OWQ_TILE(4, 2, 1);
+    if (M > 64 && blocks(128, 128) >= 224)
+        OWQ_TILE(4, 4, 1);
+    if (blocks(64, 64) >= 600)
+        OWQ_TILE(2, 2, 1);
+    if (blocks(64, 128) >= 224)
+        OWQ_TILE(2, 4, 1);
+    if (blocks(64, 32) >= 600 && M > 64)
+        OWQ_TILE(2, 1, 1);
+    if (blocks(64, 64) >= 200 && M > 64)
+        OWQ_TILE(2, 2, 2);
+    if (blocks(32, 32) >= 600)
+        OWQ_TILE(1, 1, 1);
+    if (blocks(32, 32) >= 300)
+        OWQ_TILE(1, 1, 2);
+    OWQ_TILE(1, 1, 4);
+#undef OWQ_TILE
+}
+
+}  // namespace
+}  // namespace owq

@@ -83,6 +83,10 @@ CASES = [
     (260, 1024, 9, 128, 32, 7),
     (333, 992, 0, 300, 7, 130),
     (70, 65536, 9, 5, 3, 2),
+    (190, 11008, 9, 40, 16, 3),
+    (4200, 544, 9, 150, 8, 3),
+    (20000, 96, 3, 260, 8, 3),
+    (40000, 64, 3, 260, 4, 3),
 ]
 
 
@@ -109,7 +113,8 @@ def test_against_the_definition(owq, case):
         ref, bound = _reference(layer, x, A, B, alpha, which)
         _check(y, ref, bound, name)
         none = (which < 0) | (which >= count)
-        assert host(y)[none].tobytes() == base[none].tobytes(), name
+        if M <= 16:  # the linear's own kernels; above, the sums have another order
+            assert host(y)[none].tobytes() == base[none].tobytes(), name
 
 
 @pytest.mark.parametrize("M", [2, 16, 40, 200])
