@@ -98,38 +98,91 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void k_adapter_shrink(const uint
     }
 }
 
-// Low-rank adapters of 32 tokens (tk: this lane's) and 32 rows (n: this lane's):
-// z[r] += their sum for D element r, once per distinct adapter among the tokens.
-__device__ __forceinline__ void adapter_block(const AdapterArgs& ad, const AdapterToken& tk, int N, int n, f32x16& z)
+// The adapters of 32 tokens (tk: this lane's) for 32 rows of each of the two row
+// sets (n: this lane's): z[l][r] += their sum for D element r. CS 16-rank steps at a
+// time: this lane's token's values are split into their operands once, and the
+// weights of both row sets and all steps are loaded together, one adapter ahead of
+// the products where the registers allow (AHEAD).
+template <int CS, bool AHEAD, bool WIDE, int NL>
+__device__ __forceinline__ void adapter_block(const AdapterArgs& ad, const AdapterToken& tk, int N, const int (&n)[NL],
+                                              f32x16 (&z)[NL])
 {
     const int h = (threadIdx.x & 63) >> 5;
-    uint64_t left = __ballot(tk.id >= 0) & 0xffffffffu;
-    while (left != 0) {  // wave-uniform
-        const int id = __builtin_amdgcn_readlane(tk.id, __builtin_ctzll(left));
-        left &= ~__ballot(tk.id == id);
-        f32x16 s;
+    const uint64_t all = __ballot(tk.id >= 0) & 0xffffffffu;
+    if (all == 0)
+        return;
+    for (int c0 = 8 * h; c0 < ad.rpad; c0 += 16 * CS) {
+        half8_t th[CS], tl[CS];
 #pragma unroll
-        for (int r = 0; r < 16; r++)
-            s[r] = 0.0f;
-#pragma unroll 1
-        for (int c = 8 * h; c < ad.rpad; c += 16) {
-            half8_t th, tl;
-            adapter_operand(tk, id, c, th, tl);
-            const half8_t w = adapter_weights(ad, id, N, n, c);
-            s = __builtin_amdgcn_mfma_f32_32x32x16_f16(th, w, s, 0, 0, 0);
-            s = __builtin_amdgcn_mfma_f32_32x32x16_f16(tl, w, s, 0, 0, 0);
-        }
-        const float f = tk.id == id ? tk.f : 0.0f;
+        for (int c = 0; c < CS; c++)
+            adapter_operand(tk, c0 + 16 * c < ad.rpad ? tk.id : -2, min(c0 + 16 * c, ad.rpad - 8), th[c], tl[c]);
+        struct Weights {
+            half8_t w[NL][CS];
+        };
+        auto load = [&](int id, Weights& w) {
 #pragma unroll
-        for (int r = 0; r < 16; r++) {
-            const float fr = __shfl(f, 8 * (r >> 2) + 4 * h + (r & 3), 64);
-            z[r] += fr != 0.0f ? fr * s[r] : 0.0f;
+            for (int l = 0; l < NL; l++)
+#pragma unroll
+                for (int c = 0; c < CS; c++)
+                    w.w[l][c] = adapter_weights<WIDE>(ad, id, N, n[l], c0 + 16 * c);
+        };
+        auto products = [&](int id, const Weights& w) {
+            const float f = tk.id == id ? tk.f : 0.0f;
+#pragma unroll
+            for (int l = 0; l < NL; l++) {
+                f32x16 s;
+#pragma unroll
+                for (int r = 0; r < 16; r++)
+                    s[r] = 0.0f;
+#pragma unroll
+                for (int c = 0; c < CS; c++) {
+                    s = __builtin_amdgcn_mfma_f32_32x32x16_f16(th[c], w.w[l][c], s, 0, 0, 0);
+                    s = __builtin_amdgcn_mfma_f32_32x32x16_f16(tl[c], w.w[l][c], s, 0, 0, 0);
+                }
+#pragma unroll
+                for (int r = 0; r < 16; r++) {
+                    const float fr = __shfl(f, 8 * (r >> 2) + 4 * h + (r & 3), 64);
+                    z[l][r] += fr != 0.0f ? fr * s[r] : 0.0f;
+                }
+            }
+        };
+        uint64_t left = all;
+        auto next_id = [&]() {  // wave-uniform: the next distinct adapter, -1 after the last
+            if (left == 0)
+                return -1;
+            const int id = __builtin_amdgcn_readlane(tk.id, __builtin_ctzll(left));
+            left &= ~__ballot(tk.id == id);
+            return id;
+        };
+        int id = next_id();
+        if constexpr (AHEAD) {
+            Weights wa, wb;
+            load(id, wa);
+            while (id >= 0) {
+                const int nid = next_id();
+                load(max(nid, 0), wb);
+                products(id, wa);
+                id = nid;
+                if (id < 0)
+                    break;
+                const int mid = next_id();
+                load(max(mid, 0), wa);
+                products(id, wb);
+                id = mid;
+            }
+        } else {
+            while (id >= 0) {
+                Weights w;
+                load(id, w);
+                products(id, w);
+                id = next_id();
+            }
         }
     }
 }
 
 struct AdapterGemmArgs {
-    PairLayer L[2];  // the layer, twice
+    PairLayer L;
     const uint16_t* x;
     uint16_t* y;
     int32_t M, N, K, mblocks;
@@ -148,7 +201,7 @@ __global__ __launch_bounds__(64 * WN * S) __attribute__((amdgpu_waves_per_eu(2, 
     const int n0 = ((int)blockIdx.x / a.mblocks) * 2 * T::BN;
     const int rows[2] = {n0, n0 + T::BN};
     f32x16 acc[2][FM];
-    if (!pair_gemm<FM, WN, S>(a.L, a.x, M, N, a.K, m0, rows, acc))
+    if (!pair_gemm<FM, WN, S, true>(&a.L, a.x, M, N, a.K, m0, rows, acc))
         return;
     const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
     const int wn = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) % WN;
@@ -156,19 +209,37 @@ __global__ __launch_bounds__(64 * WN * S) __attribute__((amdgpu_waves_per_eu(2, 
     for (int i = 0; i < FM; i++) {
         const int mt = m0 + 32 * i + l32;
         const AdapterToken tk = adapter_token<2, 32>(ad, min(mt, M - 1), mt < M, h);
+        // both row sets together where the registers allow
+        constexpr int NL = FM == 4 ? 1 : 2;
 #pragma unroll
-        for (int l = 0; l < 2; l++) {
-            const int n = rows[l] + wn * 32 + l32;
-            f32x16 z;
+        for (int l0 = 0; l0 < 2; l0 += NL) {
+            int nc[NL];
+            f32x16 z[NL];
 #pragma unroll
-            for (int r = 0; r < 16; r++)
-                z[r] = 0.0f;
-            adapter_block(ad, tk, N, min(n, N - 1), z);
+            for (int l = 0; l < NL; l++) {
+                nc[l] = min(rows[l0 + l] + wn * 32 + l32, N - 1);
 #pragma unroll
-            for (int r = 0; r < 16; r++) {
-                const int m = m0 + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
-                if (m < M && n < N)
-                    a.y[(int64_t)m * N + n] = f2h(acc[l][i][r] + z[r]);
+                for (int r = 0; r < 16; r++)
+                    z[l][r] = 0.0f;
+            }
+            if ((ad.rank & 7) == 0)  // uniform
+                adapter_block<FM == 4 ? 1 : 4, FM == 1, true, NL>(ad, tk, N, nc, z);
+            else
+                adapter_block<1, false, false, NL>(ad, tk, N, nc, z);
+#pragma unroll
+            for (int l = 0; l < NL; l++) {
+                const int n = rows[l0 + l] + wn * 32 + l32;
+                uint16_t* y = a.y + (int64_t)(m0 + 32 * i + 4 * h) * N + n;
+                int left = n < N ? M - (m0 + 32 * i + 4 * h) : 0;
+                // opaque: shared between the row sets, the 16 comparisons below would
+                // be kept in scalar registers and spill
+                asm volatile("" : "+v"(left));
+#pragma unroll
+                for (int r = 0; r < 16; r++) {
+                    const int t = 8 * (r >> 2) + (r & 3);
+                    if (t < left)
+                        y[(int64_t)t * N] = f2h(acc[l0 + l][i][r] + z[l][r]);
+                }
             }
         }
     }
@@ -201,7 +272,7 @@ hipError_t launch_adapter_shrink(const AdapterDesc& a, const uint16_t* x, int64_
 
 hipError_t launch_adapter_gemm(const LinearDesc& d, const AdapterDesc& ad, int64_t M, hipStream_t s)
 {
-    AdapterGemmArgs a{{pair_layer(d), pair_layer(d)}, d.x, d.y, (int32_t)M, (int32_t)d.N, (int32_t)d.K, 1};
+    AdapterGemmArgs a{pair_layer(d), d.x, d.y, (int32_t)M, (int32_t)d.N, (int32_t)d.K, 1};
     return pair_tile(M, (d.N + 1) / 2, [&](auto fm, auto wn, auto sk) {
         using T = PairTile<decltype(fm)::value, decltype(wn)::value, decltype(sk)::value>;
         a.mblocks = (int32_t)((M + T::BM - 1) / T::BM);

@@ -309,8 +309,6 @@ __global__ __launch_bounds__(64 * W * S) void k_mfv(MfvBatch b, int M, ADP ad)
     if constexpr (!std::is_same_v<ADP, NoAdapters>) {
         const AdapterToken tk = adapter_token<4, 16>(ad, min(l16, M - 1), l16 < M, qd);
         uint64_t left = __ballot(tk.id >= 0) & 0xffffu;
-        // once per distinct adapter among the tokens (wave-uniform); the next one's
-        // first weights are loaded before this one's products
         auto next_id = [&]() {
             if (left == 0)
                 return -1;
@@ -318,32 +316,41 @@ __global__ __launch_bounds__(64 * W * S) void k_mfv(MfvBatch b, int M, ADP ad)
             left &= ~__ballot(tk.id == id);
             return id;
         };
-        int id = next_id();
-        half8_t w0 = adapter_weights(ad, max(id, 0), N, brow + rloc, 8 * qd);
-        half8_t th, tl;  // this lane's token's first 8 values: the same for every adapter
-        adapter_operand(tk, tk.id, 8 * qd, th, tl);
-        while (id >= 0) {
-            const int nid = next_id();
-            const half8_t wn = adapter_weights(ad, max(nid, 0), N, brow + rloc, 8 * qd);
-            f32x4 hi = f32x4{0.0f, 0.0f, 0.0f, 0.0f}, lo = hi;
-            hi = __builtin_amdgcn_mfma_f32_16x16x32_f16(th, w0, hi, 0, 0, 0);
-            lo = __builtin_amdgcn_mfma_f32_16x16x32_f16(tl, w0, lo, 0, 0, 0);
-            for (int c = 32 + 8 * qd; c < ad.rpad; c += 32) {
-                half8_t h2, l2;
-                adapter_operand(tk, id, c, h2, l2);
-                const half8_t w = adapter_weights(ad, id, N, brow + rloc, c);
-                hi = __builtin_amdgcn_mfma_f32_16x16x32_f16(h2, w, hi, 0, 0, 0);
-                lo = __builtin_amdgcn_mfma_f32_16x16x32_f16(l2, w, lo, 0, 0, 0);
+        // once per distinct adapter among the tokens (wave-uniform); the next one's
+        // first weights are loaded before this one's products
+        auto expand = [&](auto wide) {
+            constexpr bool WIDE = decltype(wide)::value;
+            int id = next_id();
+            half8_t w0 = adapter_weights<WIDE>(ad, max(id, 0), N, brow + rloc, 8 * qd);
+            half8_t th, tl;  // this lane's token's first 8 values: the same for every adapter
+            adapter_operand(tk, tk.id, 8 * qd, th, tl);
+            while (id >= 0) {
+                const int nid = next_id();
+                const half8_t wn = adapter_weights<WIDE>(ad, max(nid, 0), N, brow + rloc, 8 * qd);
+                f32x4 hi = f32x4{0.0f, 0.0f, 0.0f, 0.0f}, lo = hi;
+                hi = __builtin_amdgcn_mfma_f32_16x16x32_f16(th, w0, hi, 0, 0, 0);
+                lo = __builtin_amdgcn_mfma_f32_16x16x32_f16(tl, w0, lo, 0, 0, 0);
+                for (int c = 32 + 8 * qd; c < ad.rpad; c += 32) {
+                    half8_t h2, l2;
+                    adapter_operand(tk, id, c, h2, l2);
+                    const half8_t w = adapter_weights<WIDE>(ad, id, N, brow + rloc, c);
+                    hi = __builtin_amdgcn_mfma_f32_16x16x32_f16(h2, w, hi, 0, 0, 0);
+                    lo = __builtin_amdgcn_mfma_f32_16x16x32_f16(l2, w, lo, 0, 0, 0);
+                }
+                const float f = tk.id == id ? tk.f : 0.0f;
+    #pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    const float fr = __shfl(f, 4 * qd + r, 64);
+                    acc[r] = fr != 0.0f ? acc[r] + fr * (hi[r] + lo[r]) : acc[r];
+                }
+                id = nid;
+                w0 = wn;
             }
-            const float f = tk.id == id ? tk.f : 0.0f;
-#pragma unroll
-            for (int r = 0; r < 4; r++) {
-                const float fr = __shfl(f, 4 * qd + r, 64);
-                acc[r] = fr != 0.0f ? acc[r] + fr * (hi[r] + lo[r]) : acc[r];
-            }
-            id = nid;
-            w0 = wn;
-        }
+        };
+        if ((ad.rank & 7) == 0)  // uniform
+            expand(std::true_type{});
+        else
+            expand(std::false_type{});
     }
 
     // D element r of lane l: token 4 (l / 16) + r, row l % 16

@@ -72,11 +72,12 @@ __device__ __forceinline__ AdapterToken adapter_token(const AdapterArgs& ad, int
 // (zero for a token of another adapter).
 __device__ __forceinline__ void adapter_operand(const AdapterToken& k, int id, int c, half8_t& hi, half8_t& lo)
 {
-    float v[8] = {};
-    if (k.id == id && id >= 0) {
-        const float4 a = *reinterpret_cast<const float4*>(k.t + c), b = *reinterpret_cast<const float4*>(k.t + c + 4);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    }
+    const float4 a = *reinterpret_cast<const float4*>(k.t + c), b = *reinterpret_cast<const float4*>(k.t + c + 4);
+    const bool on = k.id == id && id >= 0;  // (the row of a token without one is workspace: readable, not used)
+    float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+        v[e] = on ? v[e] : 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; e++) {
         const float s = __builtin_amdgcn_ldexpf(v[e], k.e);
@@ -85,22 +86,27 @@ __device__ __forceinline__ void adapter_operand(const AdapterToken& k, int id, i
     }
 }
 
-// Values c .. c + 7 of row B_id[i], zeros past the rank. With a rank that is a
-// multiple of 8 every piece is 16-byte aligned and whole.
+// Values c .. c + 7 of row B_id[i], zeros past the rank. WIDE: the rank is a multiple
+// of 8, so every piece is 16-byte aligned and whole.
+template <bool WIDE>
 __device__ __forceinline__ half8_t adapter_weights(const AdapterArgs& ad, int id, int64_t N, int64_t i, int c)
 {
+    // loads clamped to the row, values past it selected away: no branch per lane
     const uint16_t* row = ad.B + ((int64_t)id * N + i) * ad.rank;
-    if ((ad.rank & 7) == 0) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (c < ad.rank)
-            v = *reinterpret_cast<const uint4*>(row + c);
-        return __builtin_bit_cast(half8_t, v);
+    if constexpr (WIDE) {
+        const uint4 v = *reinterpret_cast<const uint4*>(row + min(c, ad.rank - 8));
+        const bool on = c < ad.rank;
+        return __builtin_bit_cast(half8_t, make_uint4(on ? v.x : 0u, on ? v.y : 0u, on ? v.z : 0u, on ? v.w : 0u));
     }
-    half8_t w;
+    uint32_t v[8];
 #pragma unroll
     for (int e = 0; e < 8; e++)
-        w[e] = c + e < ad.rank ? __builtin_bit_cast(_Float16, row[c + e]) : (_Float16)0.0f;
-    return w;
+        v[e] = row[min(c + e, ad.rank - 1)];
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+        v[e] = c + e < ad.rank ? v[e] : 0u;
+    return __builtin_bit_cast(half8_t, make_uint4(v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16),
+                                                  v[6] | (v[7] << 16)));
 }
 
 }  // namespace

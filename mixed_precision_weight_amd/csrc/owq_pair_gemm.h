@@ -60,11 +60,27 @@ struct PairTile {
     static_assert((S - 1) * WN * 4096 <= S * STAGE, "one accumulator block of every other group fits a stage set");
 };
 
+// w_weak[row][c .. c + 7] as an operand, zeros past the weak columns
+__device__ __forceinline__ half8_t pair_weak(const PairLayer& P, int64_t row, int c)
+{
+    typedef uint16_t u16x8 __attribute__((ext_vector_type(8), aligned(2)));  // rows of any length
+    const uint16_t* w = P.ww + row * P.k;
+    u16x8 v = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (c + 8 <= P.k)
+        v = *reinterpret_cast<const u16x8*>(w + c);
+    else
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            if (c + e < P.k)
+                v[e] = w[c + e];
+    return __builtin_bit_cast(half8_t, v);
+}
+
 // The sums of one wave of the block (its rows: row set l starts at n0[l], which may
-// lie past N; tokens from m0). Returns false for the K groups that handed theirs
+// lie past N; tokens from m0; SAME: both sets are rows of the one layer L[0]). Returns false for the K groups that handed theirs
 // over, whose waves are done.
-template <int FM, int WN, int S>
-__device__ __forceinline__ bool pair_gemm(const PairLayer (&L)[2], const uint16_t* x, int M, int N, int K, int m0,
+template <int FM, int WN, int S, bool SAME>
+__device__ __forceinline__ bool pair_gemm(const PairLayer* L, const uint16_t* x, int M, int N, int K, int m0,
                                           const int (&n0)[2], f32x16 (&acc)[2][FM])
 {
     using T = PairTile<FM, WN, S>;
@@ -92,7 +108,7 @@ __device__ __forceinline__ bool pair_gemm(const PairLayer (&L)[2], const uint16_
     for (int l = 0; l < 2; l++) {
         nb[l] = min(n0[l], N - 1);
         nv[l] = min(BN, N - nb[l]);
-        qr[l] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint32_t*>(L[l].q) + (int64_t)nb[l] * G * 3, (short)0,
+        qr[l] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint32_t*>(L[SAME ? 0 : l].q) + (int64_t)nb[l] * G * 3, (short)0,
                                                   nv[l] * G * 12, 0x00020000);
     }
 
@@ -123,7 +139,7 @@ __device__ __forceinline__ bool pair_gemm(const PairLayer (&L)[2], const uint16_
 #pragma unroll
     for (int l = 0; l < 2; l++) {
         row[l] = min(wn * 32 + l32, nv[l] - 1);
-        zs[l] = make_zero_sub((uint32_t)L[l].z[nb[l] + row[l]]);
+        zs[l] = make_zero_sub((uint32_t)L[SAME ? 0 : l].z[nb[l] + row[l]]);
     }
     typedef u32x3 QRegs[2];
     auto load_q = [&](int c, QRegs& cw) {
@@ -193,6 +209,71 @@ __device__ __forceinline__ bool pair_gemm(const PairLayer (&L)[2], const uint16_
     // no load may write LDS after this point (reused below, and the block may end)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
+    // row steps (of every K group's sums), then the weak columns, 64 at a time: x at
+    // their indices is gathered once per block into a stage, laid out as a chunk of x
+    // (a gather reads a cache line per value, and the row waves need the same ones),
+    // and meets w_weak as four 16-deep steps. The K groups take the 64s in turn.
+#pragma unroll
+    for (int l = 0; l < 2; l++) {
+        const float sc = h2f(L[SAME ? 0 : l].s[nb[l] + row[l]]);
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+#pragma unroll
+            for (int r = 0; r < 16; r++)
+                acc[l][i][r] *= sc;
+    }
+    char* const xw = xs0[kg];
+#pragma unroll
+    for (int l = 0; l < (SAME ? 1 : 2); l++) {
+        const PairLayer& P = L[l];
+        const int passes = (P.k + 63) >> 6;
+        for (int p0 = 0; p0 < passes; p0 += S) {  // the same trip count in every group
+            const int c = (p0 + kg) * 64;
+            __syncthreads();  // the stage is no longer read
+            if (c < P.k) {  // wave-uniform
+                const bool on = c + lane < P.k;
+                int j = P.idx[min(c + lane, P.k - 1)];
+                j = (j >= 0 && j < K) ? j : 0;
+                constexpr int TW = BM / WN, TB = TW < 8 ? TW : 8;  // tokens of a wave; loads in flight
+#pragma unroll 1
+                for (int t0 = 0; t0 < TW; t0 += TB) {
+                    uint32_t v[TB];
+#pragma unroll
+                    for (int t = 0; t < TB; t++)
+                        v[t] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
+                            xr, 2 * (min(wn + WN * (t0 + t), mv - 1) * K + j), 0, 0);
+#pragma unroll
+                    for (int t = 0; t < TB; t++) {
+                        const int tok = wn + WN * (t0 + t);
+                        *reinterpret_cast<uint16_t*>(xw + tok * 128 + (((lane >> 3) ^ (tok & 7)) << 4) +
+                                                     2 * (lane & 7)) = (uint16_t)(on ? v[t] : 0u);
+                    }
+                }
+            }
+            __syncthreads();
+            if (c < P.k) {
+#pragma unroll
+                for (int st = 0; st < 4; st++) {
+                    half8_t bv[2];
+#pragma unroll
+                    for (int w = 0; w < (SAME ? 2 : 1); w++)
+                        bv[w] = pair_weak(P, nb[SAME ? w : l] + row[SAME ? w : l], c + 32 * h + 8 * st);
+#pragma unroll
+                    for (int i = 0; i < FM; i++) {
+                        const half8_t av =
+                            __builtin_bit_cast(half8_t, *reinterpret_cast<const uint4*>(xw + arow + i * 32 * 128 + aoff[st]));
+                        if constexpr (SAME) {
+                            acc[0][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(av, bv[0], acc[0][i], 0, 0, 0);
+                            acc[1][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(av, bv[1], acc[1][i], 0, 0, 0);
+                        } else {
+                            acc[l][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(av, bv[0], acc[l][i], 0, 0, 0);
+                        }
+                    }
+                }
+            }
+        }
+    }
+
     if constexpr (S > 1) {  // the other groups hand their sums to group 0, a block of accumulators at a time
         pair_f4* red = reinterpret_cast<pair_f4*>(&xs0[0][0]);
 #pragma unroll
@@ -221,92 +302,34 @@ __device__ __forceinline__ bool pair_gemm(const PairLayer (&L)[2], const uint16_
             return false;
     }
 
-    // row steps, then the weak columns as 16-deep steps
-#pragma unroll
-    for (int l = 0; l < 2; l++) {
-        const PairLayer& P = L[l];
-        const float sc = h2f(P.s[nb[l] + row[l]]);
-#pragma unroll
-        for (int i = 0; i < FM; i++)
-#pragma unroll
-            for (int r = 0; r < 16; r++)
-                acc[l][i][r] *= sc;
-        const uint16_t* wr = P.ww + (int64_t)(nb[l] + row[l]) * P.k;
-        for (int cs = 0; cs < P.k; cs += 16) {
-            uint32_t jw[8], bw[4];
-            bool on[8];
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-                const int c = cs + 8 * h + e;
-                on[e] = c < P.k;
-                const int j = P.idx[min(c, P.k - 1)];
-                jw[e] = (uint32_t)((j >= 0 && j < K) ? j : 0);
-            }
-#pragma unroll
-            for (int e2 = 0; e2 < 4; e2++) {
-                const int c = cs + 8 * h + 2 * e2;
-                const uint32_t lo = on[2 * e2] ? wr[c] : 0u;
-                const uint32_t hi = on[2 * e2 + 1] ? wr[c + 1] : 0u;
-                bw[e2] = lo | (hi << 16);
-            }
-#pragma unroll
-            for (int i = 0; i < FM; i++) {
-                const uint16_t* xm = x + (int64_t)(m0 + min(32 * i + l32, mv - 1)) * K;
-                uint32_t aw[4];
-#pragma unroll
-                for (int e2 = 0; e2 < 4; e2++) {
-                    const uint32_t lo = on[2 * e2] ? xm[jw[2 * e2]] : 0u;
-                    const uint32_t hi = on[2 * e2 + 1] ? xm[jw[2 * e2 + 1]] : 0u;
-                    aw[e2] = lo | (hi << 16);
-                }
-                acc[l][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pair_h8(aw[0], aw[1], aw[2], aw[3]),
-                                                                   pair_h8(bw[0], bw[1], bw[2], bw[3]), acc[l][i], 0, 0,
-                                                                   0);
-            }
-        }
-    }
     return true;
 }
 
 // The tile for M tokens and `rows` rows of each set: f(FM, WN, S) as integral
-// constants. Measured for the gated block (us at the M given, N x K of each layer;
-// FM WN S):
-//   11008 x 4096  32: 114 28, 112 29, 111 32, 222 33      64: 111 34, 112 36, 222 38
-//                128: 211 49, 222 50, 111 62              256: 221 72, 241 80, 211 82
-//                512: 421 117, 441 124, 241 133           2048: 441 377, 421 432
-//   4096 x 11008  64: 114 43, 112 46, 222 63              128: 112 59, 111 68, 222 66
-//                256: 222 77, 241 96, 111 102             512: 241 112, 222 121, 441 157
-//   28672 x 8192  64: 241 95, 222 98, 441 128             128: 441 138, 241 153
-//   2731 x 1056   64: 114 12.7, 111 14.9                  512: 211 25, 221 29
-// The list takes the largest tile that still gives 600 blocks, more than two per
-// CU; where a larger one gives about one block per CU of several waves, that.
+// constants. Measured for the gated block, us, N x K of each layer, as FM WN S: time
+//   11008 x 4096  M = 32  114: 27, 222: 30, 241: 39      64  222: 32, 241: 41, 114: 44
+//                    128  241: 44, 222: 45, 441: 62     256  441: 64, 241: 68, 222: 73
+//                   2048  441: 330, 241: 393, 222: 460
+//   4096 x 11008     64  114: 38, 222: 56, 241: 90      256  222: 69, 241: 92, 441: 139
+//                   1024  441: 165, 241: 194, 222: 208
+//   28672 x 8192     64  241: 89, 222: 94, 441: 122     128  441: 127, 241: 151
+//   2731 x 1056     256  222: 17, 241: 19, 114: 25      512  241: 20, 222: 24, 441: 27
+// So: the largest tile that gives about 170 blocks (two thirds of the CUs), K split
+// in two where 64 x 64 gives 128, else 32 x 32 with K split in four. (Tiles of 128 x
+// 64, 64 x 32 and 32 x 32 with K whole or in two were never the fastest by more
+// than 3 %.)
 template <typename F>
 hipError_t pair_tile(int64_t M, int64_t rows, F f)
 {
     auto blocks = [&](int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((rows + bn - 1) / bn); };
-#define OWQ_TILE(FM, WN, S)                                                                               \
-    return f(std::integral_constant<int, FM>{}, std::integral_constant<int, WN>{},                  \
-             std::integral_constant<int, S>{})
-    if (blocks(128, 128) >= 600)
-        OWQ_TILE(4, 4, 1);
-    if (blocks(128, 64) >= 600)
-        OWQ_TILE(4, 2, 1);
-    if (M > 64 && blocks(128, 128) >= 224)
-        OWQ_TILE(4, 4, 1);
-    if (blocks(64, 64) >= 600)
-        OWQ_TILE(2, 2, 1);
-    if (blocks(64, 128) >= 224)
-        OWQ_TILE(2, 4, 1);
-    if (blocks(64, 32) >= 600 && M > 64)
-        OWQ_TILE(2, 1, 1);
-    if (blocks(64, 64) >= 200 && M > 64)
-        OWQ_TILE(2, 2, 2);
-    if (blocks(32, 32) >= 600)
-        OWQ_TILE(1, 1, 1);
-    if (blocks(32, 32) >= 300)
-        OWQ_TILE(1, 1, 2);
-    OWQ_TILE(1, 1, 4);
-#undef OWQ_TILE
+    using std::integral_constant;
+    if (M > 64 && blocks(128, 128) >= 170)
+        return f(integral_constant<int, 4>{}, integral_constant<int, 4>{}, integral_constant<int, 1>{});
+    if (blocks(64, 128) >= 170)
+        return f(integral_constant<int, 2>{}, integral_constant<int, 4>{}, integral_constant<int, 1>{});
+    if (M > 32 && blocks(64, 64) >= 128)
+        return f(integral_constant<int, 2>{}, integral_constant<int, 2>{}, integral_constant<int, 2>{});
+    return f(integral_constant<int, 1>{}, integral_constant<int, 1>{}, integral_constant<int, 4>{});
 }
 
 }  // namespace

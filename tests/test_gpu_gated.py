@@ -88,13 +88,12 @@ CASES = [
     (200, 800, 20, 1, 700),
     # every tile of the matrix-core form (tokens x rows, K groups), by its block count
     (9700, 96, 3, 2, 40),
-    (4900, 160, 3, 2, 64),
-    (9700, 64, 1, 2, 65),
-    (6500, 64, 1, 2, 150),
-    (14400, 64, 1, 2, 40),
+    (8100, 160, 3, 130, 64),
+    (11000, 64, 1, 2, 65),
+    (6500, 64, 1, 64, 150),
+    (21900, 96, 65, 2, 40),
     (19300, 96, 3, 2, 300),
     (28700, 64, 3, 2, 100),
-    (39000, 64, 0, 2, 260),
     (300, 11008, 9, 7, 100),
     # many rows: four per wave, four row waves
     (16500, 64, 3, 2, 1),
