@@ -679,30 +679,47 @@ __global__ __launch_bounds__(256) void k_gated_fin(const GatedBwdArgs a, int blo
         const int64_t e = (b * 256 + threadIdx.x) * 4;
         if (e >= n)
             return;
-        float4 t = *reinterpret_cast<const float4*>(a.P + e);
-        for (int s = 1; s < a.split; s++) {
-            const float4 v = *reinterpret_cast<const float4*>(a.P + s * n + e);
-            t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
-        }
+        float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        int s = 0;
+        auto add = [&](auto count) {  // that many loads in flight, added in order
+            constexpr int C = decltype(count)::value;
+            for (; s + C <= a.split; s += C) {
+                float4 v[C];
+#pragma unroll
+                for (int i = 0; i < C; i++)
+                    v[i] = *reinterpret_cast<const float4*>(a.P + (s + i) * n + e);
+#pragma unroll
+                for (int i = 0; i < C; i++)
+                    t.x += v[i].x, t.y += v[i].y, t.z += v[i].z, t.w += v[i].w;
+            }
+        };
+        add(std::integral_constant<int, 8>{});
+        add(std::integral_constant<int, 2>{});
+        add(std::integral_constant<int, 1>{});
         const int64_t m = e / a.K;
         const int j = (int)(e - m * a.K);
         const int ex = -a.texp[m], kt = a.L[0].k + a.L[1].k;
-        float o[4] = {t.x, t.y, t.z, t.w};
+        const float o[4] = {t.x, t.y, t.z, t.w};
+        const int4 mg = *reinterpret_cast<const int4*>(a.L[0].map + j), mu = *reinterpret_cast<const int4*>(a.L[1].map + j);
+        const int wg[4] = {mg.x, mg.y, mg.z, mg.w}, wu[4] = {mu.x, mu.y, mu.z, mu.w};
         uint32_t q[4];
 #pragma unroll
         for (int c = 0; c < 4; c++) {
             float v = __builtin_amdgcn_ldexpf(o[c], ex);
-            const int wg = a.L[0].map[j + c], wu = a.L[1].map[j + c];
-            if (wg >= 0)
-                v += a.PWs[m * kt + wg];
-            if (wu >= 0)
-                v += a.PWs[m * kt + a.L[0].k + wu];
+            if (wg[c] >= 0)
+                v += a.PWs[m * kt + wg[c]];
+            if (wu[c] >= 0)
+                v += a.PWs[m * kt + a.L[0].k + wu[c]];
             q[c] = f2h(v);
         }
-        uint16_t* dst = a.dx + e;  // dx may start at any even address
+        uint16_t* dst = a.dx + e;
+        if ((reinterpret_cast<uintptr_t>(a.dx) & 7) == 0) {  // uniform; dx may start at any even address
+            *reinterpret_cast<uint2*>(dst) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+        } else {
 #pragma unroll
-        for (int c = 0; c < 4; c++)
-            dst[c] = (uint16_t)q[c];
+            for (int c = 0; c < 4; c++)
+                dst[c] = (uint16_t)q[c];
+        }
         return;
     }
     const int64_t c = b - a.work_blocks;
@@ -711,9 +728,17 @@ __global__ __launch_bounds__(256) void k_gated_fin(const GatedBwdArgs a, int blo
     const int64_t e = (c < blocks_g ? c : c - blocks_g) * 256 + threadIdx.x;
     if (e >= n)
         return;
-    float t = L.PD[e];
-    for (int s = 1; s < a.tslabs; s++)
-        t += L.PD[s * n + e];
+    float t = 0.0f;
+    for (int s = 0; s < a.tslabs; s += 8) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            v[i] = L.PD[min(s + i, a.tslabs - 1) * n + e];
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (s + i < a.tslabs)  // uniform
+                t += v[i];
+    }
     L.dw[e] = t;
 }
 
@@ -760,10 +785,10 @@ GatedBwdPlan gated_bwd_plan(int64_t N, int64_t K, int64_t kt, int64_t M)
         p.tslabs = clampi((int64_t)(budget / ((size_t)N * kt * 4)), 1, p.tslabs);
     p.slab_tokens = cdiv(cdiv(M, p.tslabs), 8) * 8;
     p.tslabs = cdiv(M, p.slab_tokens);
-    // launch 4: 512 blocks, 8 steps each at least
+    // launch 4: 512 blocks, 4 steps each at least
     const DxShape d = dx_shape(M);
     const int64_t steps = 2 * p.Np / d.rs;
-    p.split = clampi(cdiv(512, cdiv(M, d.bm) * cdiv(K, d.bn)), 1, cdiv(steps, 8));
+    p.split = clampi(cdiv(512, cdiv(M, d.bm) * cdiv(K, d.bn)), 1, cdiv(steps, 4));
     p.split_steps = cdiv(steps, p.split);
     p.split = cdiv(steps, p.split_steps);
     size_t o = 0;
