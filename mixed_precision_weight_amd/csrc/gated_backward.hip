@@ -23,7 +23,7 @@
 //  2 k_gated_sums  the slabs added up: the token's power of two, its weak part
 //  3 k_gated_rows  per 64 rows and a slab of tokens: da, db again (two elementwise
 //                  passes read less than storing da, db in fp32 would move); dw;
-//                  A written as [M][2 Np] fp16
+//                  A written in the product's operand order, fp16
 //  4 k_gated_dx    the product; splits the rows where tokens and columns alone
 //                  do not fill the GPU
 //  5 k_gated_fin   adds the splits' and the token slabs' partial sums, in order
@@ -65,7 +65,7 @@ struct GatedBwdArgs {
     float* PW;        // [slabs][M][kt], kt = k gate + k up
     float* PWs;       // [M][kt]
     uint16_t* XW;     // [M][kt]: x at the weak columns of gate, then of up
-    uint16_t* A;      // [M][2 Np]
+    uint16_t* A;      // operand order, see a_offset
     float* P;         // [split][M][K] (split > 1)
     int32_t M, N, K, Np;
     int32_t slabs, slab_rows;      // launch 1
@@ -73,6 +73,14 @@ struct GatedBwdArgs {
     int32_t split, split_steps;    // launch 4
     int32_t work_blocks, map_blocks, mtiles;
 };
+
+// A is stored as launch 4 reads it: per 32 tokens and 16 rows (of the 2 Np) the 64
+// lanes' operands of v_mfma_f32_32x32x16_f16, 16 bytes each: lane 32 h + t holds
+// rows 8 h .. 8 h + 7 of token t. Element of (token, row):
+__device__ __forceinline__ int64_t a_offset(int Np, int64_t token, int row)
+{
+    return ((token >> 5) * (Np >> 3) + (row >> 4)) * 512 + (((row >> 3) & 1) * 32 + (token & 31)) * 8 + (row & 7);
+}
 
 __device__ __forceinline__ f32x16 zero16()
 {
@@ -262,7 +270,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k
 
 // ------------------------------------------------------------- launches 2 and 3
 // A block: 64 rows (lane l: rows 2 (l % 32), + 1) x one slab of tokens, its 4
-// waves taking pairs of tokens in turn (lane half h: token of the pair). The
+// waves taking four tokens in turn, two pairs (lane half h: token of the pair). The
 // matrix cores' k index is the token: da of row 2 (l % 32) + e against x at weak
 // column l % 32. The waves' sums are added in order in LDS.
 constexpr int kTokFlight = 2;  // pairs of tokens whose loads are in flight together
@@ -270,6 +278,11 @@ constexpr int kTokFlight = 2;  // pairs of tokens whose loads are in flight toge
 __device__ __forceinline__ int scale_exp(float mx)
 {
     return mx > 0.0f && mx < 0x1p120f ? 15 - __builtin_amdgcn_frexp_expf(mx) : 0;
+}
+
+__device__ __forceinline__ uint32_t swap_neighbours(uint32_t v)  // lane 2 i <-> 2 i + 1
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true);  // quad_perm [1, 0, 3, 2]
 }
 
 template <int ACT, bool EVEN>
@@ -300,10 +313,19 @@ __device__ __forceinline__ void row_slab(const GatedBwdArgs& a, int tile, int sl
         int ex[kTokFlight];
     };
     const int po = h * a.N + row;  // this lane's element of a pair of tokens
+    // Neighbouring lanes swap half of what they have for A, so that each stores four
+    // rows of one token: odd lanes of the second pair, even lanes of the first. Four
+    // tokens are then 64 bytes in a row and half the stores (84 -> 72 us at M = 2048
+    // with rows of 11008 against 4 bytes per lane as computed)
+    const int odd = lane & 1;
+    int aoff[2];  // byte of those four rows in a tile of A, for the tile's first tokens
+#pragma unroll
+    for (int l = 0; l < 2; l++)
+        aoff[l] = (int)a_offset(a.Np, 2 * odd + h, l * a.Np + row - 2 * odd) * 2;
     auto load = [&](int t, Pairs& q) {  // t uniform
 #pragma unroll
         for (int v = 0; v < kTokFlight; v++) {
-            const int tp = min(t + 8 * v, t1 - 1);  // the pair's first token; past the slab: not used
+            const int tp = min(t + 2 * v, t1 - 1);  // the pair's first token; past the slab: not used
             const int64_t o = (int64_t)tp * a.N, n = (int64_t)min(2, a.M - tp) * a.N;
             const auto gv = __builtin_amdgcn_raw_buffer_load_b64(rsrc(a.g + o, n * 4), 4 * po, 0, 0);
             const auto uv = __builtin_amdgcn_raw_buffer_load_b64(rsrc(a.u + o, n * 4), 4 * po, 0, 0);
@@ -324,10 +346,11 @@ __device__ __forceinline__ void row_slab(const GatedBwdArgs& a, int tile, int sl
     };
     auto work = [&](int tb, const Pairs& cur, Pairs& nxt) {
         load(tb + 8 * kTokFlight, nxt);
+        uint32_t as[2][kTokFlight];
         asm volatile("" ::: "memory");
 #pragma unroll
         for (int v = 0; v < kTokFlight; v++) {
-            const int t = tb + 8 * v + h;
+            const int t = tb + 2 * v + h;
             float dab[2][2];
 #pragma unroll
             for (int e = 0; e < 2; e++) {
@@ -338,15 +361,11 @@ __device__ __forceinline__ void row_slab(const GatedBwdArgs& a, int tile, int sl
                 dab[0][e] = use ? dh * __builtin_bit_cast(float, cur.u[v][e]) * sl : 0.0f;
                 dab[1][e] = use ? dh * va : 0.0f;
             }
-            if (conv && t < t1 && row < a.Np) {
-                uint16_t* dst = a.A + (int64_t)t * 2 * a.Np + row;
+            if (conv)  // uniform
 #pragma unroll
-                for (int l = 0; l < 2; l++) {
-                    const uint32_t lo = f2h(__builtin_amdgcn_ldexpf(dab[l][0] * sc[l][0], cur.ex[v]));
-                    const uint32_t hi = f2h(__builtin_amdgcn_ldexpf(dab[l][1] * sc[l][1], cur.ex[v]));
-                    *reinterpret_cast<uint32_t*>(dst + l * a.Np) = lo | (hi << 16);
-                }
-            }
+                for (int l = 0; l < 2; l++)
+                    as[l][v] = f2h(__builtin_amdgcn_ldexpf(dab[l][0] * sc[l][0], cur.ex[v])) |
+                               (uint32_t)f2h(__builtin_amdgcn_ldexpf(dab[l][1] * sc[l][1], cur.ex[v])) << 16;
 #pragma unroll
             for (int l = 0; l < 2; l++) {
                 const float xv = h2f((uint16_t)cur.xw[v][l]);
@@ -355,11 +374,26 @@ __device__ __forceinline__ void row_slab(const GatedBwdArgs& a, int tile, int sl
                     acc[l][e] = __builtin_amdgcn_mfma_f32_32x32x2f32(dab[l][e], xv, acc[l][e], 0, 0, 0);
             }
         }
+        if (conv) {
+            // the four tokens are a quarter of a 32-token tile of A; lanes without
+            // rows or token store out of range
+            const __amdgpu_buffer_rsrc_t dst = rsrc(a.A + (int64_t)(tb >> 5) * 64 * a.Np, (int64_t)128 * a.Np);
+            const int dead = tb + 2 * odd + h < t1 && row < a.Np ? 0 : 0x40000000;
+#pragma unroll
+            for (int l = 0; l < 2; l++) {
+                const uint32_t mine = odd ? as[l][1] : as[l][0];
+                const uint32_t got = swap_neighbours(odd ? as[l][0] : as[l][1]);
+                typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+                const u32x2 v = {odd ? got : mine, odd ? mine : got};
+                __builtin_amdgcn_raw_buffer_store_b64(v, dst, (aoff[l] | dead) + (tb & 31) * 16, 0, 0);
+            }
+        }
     };
     Pairs pa, pb;
-    const int first = t0 + 2 * wave;
+    const int first = t0 + 4 * wave;
     if (first < t1)
         load(first, pa);
+    static_assert(kTokFlight == 2, "a step is four tokens");
     for (int t = first; t < t1; t += 16 * kTokFlight) {
         work(t, pa, pb);
         work(t + 8 * kTokFlight, pb, pa);
@@ -444,22 +478,20 @@ __global__ __launch_bounds__(256) void k_gated_sums(const GatedBwdArgs a)
 // ------------------------------------------------------------------- launch 4
 // dx: D[m][j] = sum over r < 2 Np of A[m][r] (q - z)[r][j], rows of gate, then of
 // up. A block owns BM tokens x BN columns and steps of RS rows: thread t decodes
-// one 32-column group of one row into the LDS tile [row][column] (exact fp16), the
-// A tile comes by direct-to-LDS loads two steps ahead. v_mfma_f32_32x32x16_f16
-// takes 8 consecutive rows per lane: contiguous for A; for the decoded tile the
-// transposing LDS read (ds_read_b64_tr_b16: in 16 lanes, lane i receives element i
-// of four rows of 16 columns) gives 4 rows of the lane's column. Tile rows are
-// padded to 64 bytes past a multiple of 256, so the four rows of a read lie in
-// distinct banks.
+// one 32-column group of one row into the LDS tile [row][column] (exact fp16), one
+// step ahead of the products; A goes from memory into the operand registers two
+// steps ahead, as whole kilobytes in operand order: through LDS it would take a
+// third of the LDS bandwidth, which bounds the step (397 -> 365 us at M = 2048,
+// 2 x 11008 x 4096). v_mfma_f32_32x32x16_f16
+// takes 8 consecutive rows per lane; for the decoded tile the transposing LDS read
+// (ds_read_b64_tr_b16: in 16 lanes, lane i receives element i of four rows of 16
+// columns) gives 4 rows of the lane's column. Tile rows are padded to 64 bytes past
+// a multiple of 256, so the four rows of a read lie in distinct banks.
 template <int FM, int FN, int WM, int WN, int RS>
 struct DxTile {
     static constexpr int NT = 64 * WM * WN;
     static constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN;
     static constexpr int BROW = BN * 2 + 64;         // LDS bytes of a decoded row
-    static constexpr int AROW = RS * 2;              // LDS bytes of a token's rows
-    static constexpr int PIECES = AROW / 16;         // 4 or 8
-    static constexpr int ASTAGE = BM * AROW;
-    static constexpr int DPW = ASTAGE / 16 / NT;     // 16-byte units per thread and step
     // The 16-byte pieces of group g of row r are stored at piece ^ b_swizzle: rows and
     // groups 64 bytes apart would put the 16 lanes of a write on 4 of the 16 places
     // that the banks hold (415 -> 395 us at M = 2048, 2 x 11008 x 4096). Constant over
@@ -471,19 +503,8 @@ struct DxTile {
     }
     static_assert((GB == 8 && FN == 4) || GB == 4, "a wave's groups must share their swizzle");
     static_assert(RS * GB == NT, "one group per thread and step");
-    static_assert(ASTAGE % (16 * NT) == 0, "an A stage must split evenly over the threads");
     static_assert((BN * 2) % 256 == 0, "tile rows 64 bytes apart modulo the banks");
 };
-
-__device__ __forceinline__ int a_swizzle(int pieces, int token)
-{
-    return pieces == 8 ? (token >> 1) & 7 : (token >> 2) & 3;
-}
-
-__device__ __forceinline__ void dma_a(__amdgpu_buffer_rsrc_t r, char* lds, int voff)
-{
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff, 0, 0, 0);
-}
 
 // four rows of this lane's column from each of two places in the decoded tile
 __device__ __forceinline__ half8_t read_columns(const char* a, const char* b)
@@ -497,9 +518,6 @@ template <int FM, int FN, int WM, int WN, int RS>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2))) void k_gated_dx(const GatedBwdArgs a)
 {
     using T = DxTile<FM, FN, WM, WN, RS>;
-    __shared__ __attribute__((aligned(1024))) char as0[T::ASTAGE];
-    __shared__ __attribute__((aligned(1024))) char as1[T::ASTAGE];
-    __shared__ __attribute__((aligned(1024))) char as2[T::ASTAGE];
     __shared__ __attribute__((aligned(1024))) char bs[2][RS * T::BROW];
 
     const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
@@ -511,27 +529,29 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
     const int m0 = (b % a.mtiles) * T::BM;
     const int j0 = (b / a.mtiles % ctiles) * T::BN;
     const int sp = b / (a.mtiles * ctiles);
-    const int mv = min(T::BM, M - m0);
     const int steps = 2 * Np / RS;
     const int st0 = sp * a.split_steps, st1 = min(steps, st0 + a.split_steps);
 
-    // A: unit n of a stage is slot n % PIECES of token n / PIECES, holding piece
-    // slot ^ swizzle; tokens past M repeat the last one (not stored). The range
-    // check covers the block's tokens; steps past the end read zeros.
-    const __amdgpu_buffer_rsrc_t ar = __builtin_amdgcn_make_buffer_rsrc(
-        a.A + (int64_t)m0 * 2 * Np, (short)0, (int)((int64_t)mv * 2 * Np * 2), 0x00020000);
-    int asrc[T::DPW];
+    // A of this wave's 32-token tiles (tiles past M repeat the last: not stored);
+    // steps past the end repeat the last
+    constexpr int KS = RS / 16;
+    __amdgpu_buffer_rsrc_t ar[FM];
 #pragma unroll
-    for (int t = 0; t < T::DPW; t++) {
-        const int n = (wave * T::DPW + t) * 64 + lane;
-        const int tok = n / T::PIECES, piece = (n % T::PIECES) ^ a_swizzle(T::PIECES, tok);
-        asrc[t] = min(tok, mv - 1) * 2 * Np * 2 + piece * 16;
+    for (int i = 0; i < FM; i++) {
+        const int tile = min((m0 >> 5) + wm * FM + i, (M - 1) >> 5);
+        ar[i] = rsrc(a.A + (int64_t)tile * 64 * Np, (int64_t)128 * Np);
     }
-    auto dma = [&](int st, char* stage) {
-        const int off = st < st1 ? st * RS * 2 : 0x40000000;
+    struct Tokens {
+        half8_t v[KS][FM];
+    };
+    auto load_a = [&](int st, Tokens& t) {
+        const int o = min(st, st1 - 1) * KS * 1024;
 #pragma unroll
-        for (int t = 0; t < T::DPW; t++)
-            dma_a(ar, stage + (wave * T::DPW + t) * 1024, asrc[t] + off);
+        for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+            for (int i = 0; i < FM; i++)
+                t.v[ks][i] = __builtin_bit_cast(
+                    half8_t, __builtin_amdgcn_raw_buffer_load_b128(ar[i], lane * 16, o + ks * 1024, 0));
     };
     // codes: thread t decodes group t % (BN / 32) of row t / (BN / 32) of a step.
     // Rows past N and groups past K read valid ones (A is zero there, the columns
@@ -570,68 +590,54 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
         for (int f = 0; f < FN; f++)
             acc[i][f] = zero16();
 
-    // this lane's operands of 16-row step ks: A piece 2 ks + h of its token; the
-    // decoded rows 16 ks + 8 h + 4 t + (l % 16) / 4, columns of its 16-lane group
-    int atok[FM], aswz[FM];
-#pragma unroll
-    for (int i = 0; i < FM; i++) {
-        const int tok = wm * 32 * FM + 32 * i + l32;
-        atok[i] = tok * T::AROW;
-        aswz[i] = a_swizzle(T::PIECES, tok);
-    }
+    // this lane's columns of 16-row step ks: decoded rows 16 ks + 8 h + 4 t + (l % 16)
+    // / 4, columns of its 16-lane group
     const int brow = (lane & 15) >> 2, bpiece = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
     const int boff = (8 * h + brow) * T::BROW + wn * FN * 64 + ((bpiece ^ T::b_swizzle(wn * FN, brow)) << 4) + 8 * (lane & 1);
 
-    // Step st computes on stage as_cur and tile st & 1; it starts the loads of step
-    // st + 2 and decodes step st + 1 (its codes were loaded one step ago) into the
-    // other tile.
-    auto step = [&](int st, const char* cur, char* nxt2, Codes& mine, Codes& next) {
-        // A of step st has arrived once at most the loads of the last step remain
-        // (A and 2 or 4 code loads: counted as 2); the barrier also closes the
-        // tile written during that step, and the reads of the tile and stage that
-        // this step overwrites
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(T::DPW + 2) : "memory");
-        dma(st + 2, nxt2);
+    // Step st computes on cur and tile st & 1; it starts the loads of step st + 2 and
+    // decodes step st + 1 (its codes were loaded one step ago) into the other tile.
+    auto step = [&](int st, const Tokens& cur, Tokens& nxt2, Codes& mine, Codes& next) {
+        // closes the tile written in the last step, and the reads of the one that this
+        // step overwrites; loads in flight stay in flight
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        load_a(st + 2, nxt2);
         load_q(st + 2, next);
         const char* tile = bs[(st - st0) & 1];
         if (st + 1 < st1)  // uniform
             stage_b(mine, bs[(st + 1 - st0) & 1]);
         if (st < st1) {
 #pragma unroll
-            for (int ks = 0; ks < RS / 16; ks++) {
-                half8_t av[FM];
-#pragma unroll
-                for (int i = 0; i < FM; i++)
-                    av[i] = *reinterpret_cast<const half8_t*>(cur + atok[i] + (((2 * ks + h) ^ aswz[i]) << 4));
+            for (int ks = 0; ks < KS; ks++) {
 #pragma unroll
                 for (int f = 0; f < FN; f++) {
                     const char* src = tile + boff + ks * 16 * T::BROW + f * 64;
                     const half8_t bv = read_columns(src, src + 4 * T::BROW);
 #pragma unroll
                     for (int i = 0; i < FM; i++)
-                        acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(av[i], bv, acc[i][f], 0, 0, 0);
+                        acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(cur.v[ks][i], bv, acc[i][f], 0, 0, 0);
                 }
             }
         }
     };
 
     Codes qa, qb;
-    dma(st0, as0);
+    Tokens ta, tb, tc;
+    load_a(st0, ta);
     load_q(st0, qa);
     asm volatile("" ::: "memory");
-    dma(st0 + 1, as1);
+    load_a(st0 + 1, tb);
     load_q(st0 + 1, qb);
     asm volatile("" ::: "memory");
     stage_b(qa, bs[0]);
     for (int st = st0; st < st1; st += 6) {
-        step(st, as0, as2, qb, qa);
-        step(st + 1, as1, as0, qa, qb);
-        step(st + 2, as2, as1, qb, qa);
-        step(st + 3, as0, as2, qa, qb);
-        step(st + 4, as1, as0, qb, qa);
-        step(st + 5, as2, as1, qa, qb);
+        step(st, ta, tc, qb, qa);
+        step(st + 1, tb, ta, qa, qb);
+        step(st + 2, tc, tb, qb, qa);
+        step(st + 3, ta, tc, qa, qb);
+        step(st + 4, tb, ta, qb, qa);
+        step(st + 5, tc, tb, qa, qb);
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may write LDS after the block has ended
 
     // D element r of lane l: token 8 (r / 4) + 4 h + r % 4, column l % 32
     const int kt = a.L[0].k + a.L[1].k;
@@ -783,7 +789,7 @@ GatedBwdPlan gated_bwd_plan(int64_t N, int64_t K, int64_t kt, int64_t M)
     p.tslabs = clampi(1024 / rtiles, 1, cdiv(M, 32));
     if (kt > 0)
         p.tslabs = clampi((int64_t)(budget / ((size_t)N * kt * 4)), 1, p.tslabs);
-    p.slab_tokens = cdiv(cdiv(M, p.tslabs), 8) * 8;
+    p.slab_tokens = cdiv(cdiv(M, p.tslabs), 16) * 16;  // four tokens for each of four waves
     p.tslabs = cdiv(M, p.slab_tokens);
     // launch 4: 512 blocks, 4 steps each at least
     const DxShape d = dx_shape(M);
@@ -803,7 +809,7 @@ GatedBwdPlan gated_bwd_plan(int64_t N, int64_t K, int64_t kt, int64_t M)
     p.off_pw = take((size_t)p.slabs * M * kt * 4);
     p.off_pws = take((size_t)M * kt * 4);
     p.off_xw = take((size_t)M * kt * 2);
-    p.off_a = take((size_t)M * 2 * p.Np * 2);
+    p.off_a = take((size_t)cdiv(M, 32) * 32 * 2 * p.Np * 2);
     p.off_pd = take(p.tslabs > 1 ? (size_t)p.tslabs * N * kt * 4 : 0);
     p.off_p = take(p.split > 1 ? (size_t)p.split * M * K * 4 : 0);
     p.total = o;
