@@ -14,6 +14,13 @@
 // l % 16, columns 8 (l / 16) .. + 7 of each 32), B operand the adapter's row
 // l % 16, both read from memory in 16-byte pieces without staging: every byte is
 // used by one lane once. Exact fp16 products, fp32 sums.
+//
+// Both halves run once per distinct adapter of a tile of tokens, so above 16 tokens
+// the tiles are taken from an order in which the tokens of one adapter stand
+// together (runs of 1024 tokens ordered each by itself, group_tokens; every block
+// computes its run's order, the first of each tile stores it for the second half):
+// 2000 tokens of 20 requests in turn, 4096 -> 4096, rank 64: 645 -> 153 us, 1000 of
+// 3 (11008 -> 4096) 199 -> 155; where requests follow one another it costs 2 - 3 us.
 #include "owq_adapters.h"
 #include "owq_pair_gemm.h"
 
@@ -23,31 +30,113 @@ namespace {
 
 constexpr int kShrinkWaves = 16;
 constexpr int kShrinkFlight = 8;  // 32-column steps whose loads are in flight together
+constexpr int kBuckets = 256;     // that tokens are grouped by: the adapter's index modulo this
+
+struct GroupScratch {
+    int count[kShrinkWaves][kBuckets];  // tokens of a bucket in earlier waves
+    int first[kBuckets];                // position of its first token
+    int part[4];
+    int token[16], id[16];              // the block's tile
+};
+
+// The tokens base .. base + kPairRun - 1, one per thread, in the order of their
+// buckets, each bucket's in their own order; tokens without an adapter share the
+// last one. Fills g.token and g.id (-1: no adapter) with the 16 tokens from position
+// p0, those that exist.
+__device__ __forceinline__ void group_tokens(GroupScratch& g, const int32_t* which, int M, int count, int base, int p0)
+{
+    static_assert(kPairRun == 64 * kShrinkWaves, "one token of a run per thread");
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const bool on = tid < M - base;
+    const int w = on ? which[base + tid] : -1;
+    const int id = w < count ? w : -1;
+    const int key = id >= 0 ? id & (kBuckets - 1) : kBuckets - 1;
+#pragma unroll
+    for (int i = 0; i < kShrinkWaves * kBuckets; i += kPairRun)
+        (&g.count[0][0])[i + tid] = 0;
+    uint64_t same = __ballot(on);  // this wave's tokens of the same bucket
+#pragma unroll
+    for (int b = 1; b < kBuckets; b *= 2) {
+        const uint64_t set = __ballot((key & b) != 0);
+        same &= (key & b) ? set : ~set;
+    }
+    const int before = (int)__popcll(same & ((1ull << lane) - 1));
+    __syncthreads();
+    if (on && before == 0)
+        g.count[wave][key] = (int)__popcll(same);
+    __syncthreads();
+    int sum = 0, upto = 0;
+    if (tid < kBuckets) {
+#pragma unroll
+        for (int w = 0; w < kShrinkWaves; w++) {
+            const int c = g.count[w][tid];
+            g.count[w][tid] = sum;
+            sum += c;
+        }
+        upto = sum;
+#pragma unroll
+        for (int o = 1; o < 64; o *= 2) {
+            const int v = __shfl_up(upto, o, 64);
+            upto += lane >= o ? v : 0;
+        }
+        if (lane == 63)
+            g.part[wave] = upto;
+    }
+    __syncthreads();
+    if (tid < kBuckets) {
+        for (int w = 0; w < wave; w++)
+            upto += g.part[w];
+        g.first[tid] = upto - sum;
+    }
+    __syncthreads();
+    const int at = g.first[key] + g.count[wave][key] + before - (p0 - base);
+    if (on && at >= 0 && at < 16)
+        g.token[at] = base + tid, g.id[at] = id;
+    __syncthreads();
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t shrink_rsrc(const uint16_t* p, int64_t elems)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), (short)0, (int)(elems * 2), 0x00020000);
+}
 
 __global__ __launch_bounds__(64 * kShrinkWaves) void k_adapter_shrink(const uint16_t* __restrict__ x,
                                                                       const uint16_t* __restrict__ A,
                                                                       const int32_t* __restrict__ which,
-                                                                      float* __restrict__ t, int M, int K, int count,
-                                                                      int rank, int rpad)
+                                                                      float* __restrict__ t, int32_t* __restrict__ order,
+                                                                      int M, int K, int count, int rank, int rpad)
 {
     __shared__ float4 red[kShrinkWaves][64];
+    __shared__ GroupScratch group;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, qd = lane >> 4;
-    // The rank tiles of a token tile run on one XCD (blocks go to the 8 XCDs in
-    // turn), so its x comes into one L2 once: 47 -> 25 us at 1000 tokens, rank 64,
-    // K = 11008
+    // Blocks go to the 8 XCDs in turn: the rank tiles of a token tile run on one XCD,
+    // so its x comes into one L2 once (47 -> 25 us at 1000 tokens, rank 64, K = 11008).
+    // Token tiles go round the XCDs: with runs of tiles on one, 27 us became 46
     const int xcd = (int)blockIdx.x & 7, slot = (int)blockIdx.x >> 3;
-    const int rt = rpad >> 4;
+    const int rt = rpad >> 4, tiles = (M + 15) >> 4;
     const int tile = xcd + 8 * (slot / rt), r0 = (slot % rt) * 16;
-    if (tile * 16 >= M)
+    if (tile >= tiles)
         return;
-    const int64_t m = (int64_t)tile * 16 + l16;
-    const int64_t mc = m < M ? m : M - 1;
-    int id = which[mc];
-    if (m >= M || id < 0 || id >= count)
+    // this lane's token, at position p of the order
+    const int p = tile * 16 + l16;
+    const int base = M > kMfvMaxM ? tile * 16 / kPairRun * kPairRun : 0;
+    int m = min(p, M - 1), id;
+    if (M > kMfvMaxM) {  // uniform
+        group_tokens(group, which, M, count, base, tile * 16);
+        const int at = m - tile * 16;  // (m < M: that position is filled)
+        m = group.token[at], id = group.id[at];
+        if (r0 == 0 && blockIdx.y == 0 && threadIdx.x < 16 && p < M)
+            order[p] = m;
+    } else {
+        id = which[m];
+    }
+    if (p >= M || id < 0 || id >= count)
         id = -1;
-    const uint16_t* xr = x + mc * K + 8 * qd;
+    const __amdgpu_buffer_rsrc_t xr = shrink_rsrc(x + (int64_t)base * K, (int64_t)min(M - base, kPairRun) * K);
+    const int xo = (m - base) * K * 2 + 16 * qd;
+    const int ao = min(r0 + l16, rank - 1) * K * 2 + 16 * qd;
     const int steps = K >> 5;
     const int per = (steps + kShrinkWaves - 1) / kShrinkWaves;
     const int s0 = wave * per, s1 = min(steps, s0 + per);
@@ -59,21 +148,33 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void k_adapter_shrink(const uint
         left &= ~__ballot(id == a);
         if (d % (int)gridDim.y != (int)blockIdx.y)
             continue;
-        const uint16_t* ar = A + ((int64_t)a * rank + min(r0 + l16, rank - 1)) * K + 8 * qd;
+        const __amdgpu_buffer_rsrc_t ar = shrink_rsrc(A + (int64_t)a * rank * K, (int64_t)rank * K);
         float4_t acc[2] = {float4_t{0.0f, 0.0f, 0.0f, 0.0f}, float4_t{0.0f, 0.0f, 0.0f, 0.0f}};
-        // (a tile of padding ranks only stores its zeros)
-        for (int s = r0 < rank ? s0 : s1; s < s1; s += kShrinkFlight) {
+        if (r0 < rank) {  // (a tile of padding ranks only stores its zeros)
+            // steps past the wave's end are read out of range: zeros, nothing fetched
             half8_t xv[kShrinkFlight], av[kShrinkFlight];
+            auto load = [&](int s, int u) {
+                const int o = s + u < s1 ? (s + u) * 64 : 0x40000000;
+                xv[u] = __builtin_bit_cast(half8_t, __builtin_amdgcn_raw_buffer_load_b128(xr, xo + o, 0, 0));
+                av[u] = __builtin_bit_cast(half8_t, __builtin_amdgcn_raw_buffer_load_b128(ar, ao + o, 0, 0));
+            };
+            auto product = [&](int u) {
+                acc[u & 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv[u], av[u], acc[u & 1], 0, 0, 0);
+            };
 #pragma unroll
-            for (int u = 0; u < kShrinkFlight; u++) {
-                const int64_t o = (int64_t)min(s + u, s1 - 1) * 32;
-                xv[u] = *reinterpret_cast<const half8_t*>(xr + o);
-                av[u] = *reinterpret_cast<const half8_t*>(ar + o);
+            for (int u = 0; u < kShrinkFlight; u++)
+                load(s0, u);
+            int s = s0;
+            for (; s + kShrinkFlight < s1; s += kShrinkFlight) {
+#pragma unroll
+                for (int u = 0; u < kShrinkFlight; u++) {
+                    product(u);
+                    load(s + kShrinkFlight, u);
+                }
             }
 #pragma unroll
             for (int u = 0; u < kShrinkFlight; u++)
-                if (s + u < s1)  // wave-uniform
-                    acc[u & 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv[u], av[u], acc[u & 1], 0, 0, 0);
+                product(u);
         }
         const float4_t sum = acc[0] + acc[1];
         __syncthreads();  // the previous adapter's sums are no longer read
@@ -83,8 +184,8 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void k_adapter_shrink(const uint
             float4 v = red[0][lane];
 #pragma unroll
             for (int w = 1; w < kShrinkWaves; w++) {
-                const float4 p = red[w][lane];
-                v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+                const float4 q = red[w][lane];
+                v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
             }
             // D element r of lane l: token 4 (l / 16) + r, rank l % 16
             const float o[4] = {v.x, v.y, v.z, v.w};
@@ -103,7 +204,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void k_adapter_shrink(const uint
 // time: this lane's token's values are split into their operands once, and the
 // weights of both row sets and all steps are loaded together, one adapter ahead of
 // the products where the registers allow (AHEAD).
-template <int CS, bool AHEAD, bool WIDE, int NL>
+template <int CS, bool AHEAD, int PIECE, int NL>
 __device__ __forceinline__ void adapter_block(const AdapterArgs& ad, const AdapterToken& tk, int N, const int (&n)[NL],
                                               f32x16 (&z)[NL])
 {
@@ -124,7 +225,7 @@ __device__ __forceinline__ void adapter_block(const AdapterArgs& ad, const Adapt
             for (int l = 0; l < NL; l++)
 #pragma unroll
                 for (int c = 0; c < CS; c++)
-                    w.w[l][c] = adapter_weights<WIDE>(ad, id, N, n[l], c0 + 16 * c);
+                    w.w[l][c] = adapter_weights<PIECE>(ad, id, N, n[l], c0 + 16 * c);
         };
         auto products = [&](int id, const Weights& w) {
             const float f = tk.id == id ? tk.f : 0.0f;
@@ -201,14 +302,16 @@ __global__ __launch_bounds__(64 * WN * S) __attribute__((amdgpu_waves_per_eu(2, 
     const int n0 = ((int)blockIdx.x / a.mblocks) * 2 * T::BN;
     const int rows[2] = {n0, n0 + T::BN};
     f32x16 acc[2][FM];
-    if (!pair_gemm<FM, WN, S, true>(&a.L, a.x, M, N, a.K, m0, rows, acc))
+    if (!pair_gemm<FM, WN, S, true>(&a.L, a.x, ad.order, M, N, a.K, m0, rows, acc))
         return;
     const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
     const int wn = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) % WN;
 #pragma unroll
     for (int i = 0; i < FM; i++) {
-        const int mt = m0 + 32 * i + l32;
-        const AdapterToken tk = adapter_token<2, 32>(ad, min(mt, M - 1), mt < M, h);
+        const int mt = m0 + 32 * i + l32, mc = min(mt, M - 1);
+        const int tok = ad.order[mc];
+        const AdapterToken tk = adapter_token<2, 32>(ad, tok, mc, mt < M, h);
+        const int dst = mt < M ? tok : -1;
         // both row sets together where the registers allow
         constexpr int NL = FM == 4 ? 1 : 2;
 #pragma unroll
@@ -223,21 +326,19 @@ __global__ __launch_bounds__(64 * WN * S) __attribute__((amdgpu_waves_per_eu(2, 
                     z[l][r] = 0.0f;
             }
             if ((ad.rank & 7) == 0)  // uniform
-                adapter_block<FM == 4 ? 1 : 4, FM == 1, true, NL>(ad, tk, N, nc, z);
+                adapter_block<FM == 4 ? 1 : FM == 2 ? 4 : 2, FM == 1, 8, NL>(ad, tk, N, nc, z);
+            else if ((ad.rank & 3) == 0)
+                adapter_block<1, false, 4, NL>(ad, tk, N, nc, z);
             else
-                adapter_block<1, false, false, NL>(ad, tk, N, nc, z);
+                adapter_block<1, false, 1, NL>(ad, tk, N, nc, z);
 #pragma unroll
             for (int l = 0; l < NL; l++) {
                 const int n = rows[l0 + l] + wn * 32 + l32;
-                uint16_t* y = a.y + (int64_t)(m0 + 32 * i + 4 * h) * N + n;
-                int left = n < N ? M - (m0 + 32 * i + 4 * h) : 0;
-                // opaque: shared between the row sets, the 16 comparisons below would
-                // be kept in scalar registers and spill
-                asm volatile("" : "+v"(left));
+                uint16_t* y = a.y + n;
 #pragma unroll
                 for (int r = 0; r < 16; r++) {
-                    const int t = 8 * (r >> 2) + (r & 3);
-                    if (t < left)
+                    const int t = __shfl(dst, 8 * (r >> 2) + 4 * h + (r & 3), 64);
+                    if (t >= 0 && n < N)
                         y[(int64_t)t * N] = f2h(acc[l0 + l][i][r] + z[l][r]);
                 }
             }
@@ -249,7 +350,7 @@ __global__ __launch_bounds__(64 * WN * S) __attribute__((amdgpu_waves_per_eu(2, 
 
 size_t adapter_workspace_bytes(int rank, int64_t M)
 {
-    return (size_t)M * adapter_rpad(rank) * sizeof(float);
+    return (size_t)M * (adapter_rpad(rank) * sizeof(float) + sizeof(int32_t));
 }
 
 hipError_t launch_adapter_shrink(const AdapterDesc& a, const uint16_t* x, int64_t M, int64_t K, hipStream_t s)
@@ -266,7 +367,7 @@ hipError_t launch_adapter_shrink(const AdapterDesc& a, const uint16_t* x, int64_
     const int64_t nb = (tiles + 7) / 8 * 8 * rt;
     if (nb > INT32_MAX)
         return hipErrorInvalidValue;
-    hipLaunchKernelGGL(k_adapter_shrink, dim3((unsigned)nb, (unsigned)slots), dim3(64 * kShrinkWaves), 0, s, x, a.A, a.which, a.t, (int)M, (int)K, a.count, a.rank, rpad);
+    hipLaunchKernelGGL(k_adapter_shrink, dim3((unsigned)nb, (unsigned)slots), dim3(64 * kShrinkWaves), 0, s, x, a.A, a.which, a.t, a.order, (int)M, (int)K, a.count, a.rank, rpad);
     return hipGetLastError();
 }
 

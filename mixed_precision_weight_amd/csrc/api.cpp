@@ -904,7 +904,9 @@ owq_status owq_linear_adapters(const owq_layer* L, const owq_adapters* ad, const
     st = check_idx_on_host(L->weak_idx, L->k, L->K, (hipStream_t)stream);
     if (st != OWQ_OK)
         return st;
-    const owq::AdapterDesc a{ad->A, ad->B, ad->alpha, which, static_cast<float*>(workspace), ad->count, ad->rank};
+    float* const t = static_cast<float*>(workspace);
+    int32_t* const order = reinterpret_cast<int32_t*>(t + M * owq::adapter_rpad(ad->rank));
+    const owq::AdapterDesc a{ad->A, ad->B, ad->alpha, which, t, order, ad->count, ad->rank};
     hipError_t e = owq::launch_adapter_shrink(a, x, M, L->K, (hipStream_t)stream);
     if (e == hipSuccess)
     {

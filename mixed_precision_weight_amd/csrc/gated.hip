@@ -522,7 +522,7 @@ __global__ __launch_bounds__(64 * WN * S) __attribute__((amdgpu_waves_per_eu(2, 
     const int n0 = ((int)blockIdx.x / a.mblocks) * T::BN;
     const int rows[2] = {n0, n0};
     f32x16 acc[2][FM];
-    if (!pair_gemm<FM, WN, S, false>(a.L, a.x, M, N, a.K, m0, rows, acc))
+    if (!pair_gemm<FM, WN, S, false>(a.L, a.x, nullptr, M, N, a.K, m0, rows, acc))
         return;
     const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
     const int n = n0 + (__builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) % WN) * 32 + l32;

@@ -187,6 +187,11 @@ __global__ __launch_bounds__(64 * W * S) void k_mfv(MfvBatch b, int M, ADP ad)
     };
     char* const crow = cs[wid];
 
+    [[maybe_unused]] int aid = -1;  // this lane's token's adapter
+    if constexpr (!std::is_same_v<ADP, NoAdapters>) {
+        const int id = ad.which[min(l16, M - 1)];
+        aid = l16 < M && id >= 0 && id < ad.count ? id : -1;
+    }
     const float sc = h2f(L.s[brow + rloc]);
     const ZeroSub zs = make_zero_sub((uint32_t)L.z[brow + rloc]);
     const Magic mg = make_magic();
@@ -307,50 +312,67 @@ __global__ __launch_bounds__(64 * W * S) void k_mfv(MfvBatch b, int M, ADP ad)
     }
 
     if constexpr (!std::is_same_v<ADP, NoAdapters>) {
-        const AdapterToken tk = adapter_token<4, 16>(ad, min(l16, M - 1), l16 < M, qd);
-        uint64_t left = __ballot(tk.id >= 0) & 0xffffu;
-        auto next_id = [&]() {
-            if (left == 0)
-                return -1;
-            const int id = __builtin_amdgcn_readlane(tk.id, __builtin_ctzll(left));
-            left &= ~__ballot(tk.id == id);
-            return id;
-        };
-        // once per distinct adapter among the tokens (wave-uniform); the next one's
-        // first weights are loaded before this one's products
-        auto expand = [&](auto wide) {
-            constexpr bool WIDE = decltype(wide)::value;
-            int id = next_id();
-            half8_t w0 = adapter_weights<WIDE>(ad, max(id, 0), N, brow + rloc, 8 * qd);
-            half8_t th, tl;  // this lane's token's first 8 values: the same for every adapter
-            adapter_operand(tk, tk.id, 8 * qd, th, tl);
-            while (id >= 0) {
-                const int nid = next_id();
-                const half8_t wn = adapter_weights<WIDE>(ad, max(nid, 0), N, brow + rloc, 8 * qd);
-                f32x4 hi = f32x4{0.0f, 0.0f, 0.0f, 0.0f}, lo = hi;
-                hi = __builtin_amdgcn_mfma_f32_16x16x32_f16(th, w0, hi, 0, 0, 0);
-                lo = __builtin_amdgcn_mfma_f32_16x16x32_f16(tl, w0, lo, 0, 0, 0);
-                for (int c = 32 + 8 * qd; c < ad.rpad; c += 32) {
-                    half8_t h2, l2;
-                    adapter_operand(tk, id, c, h2, l2);
-                    const half8_t w = adapter_weights<WIDE>(ad, id, N, brow + rloc, c);
-                    hi = __builtin_amdgcn_mfma_f32_16x16x32_f16(h2, w, hi, 0, 0, 0);
-                    lo = __builtin_amdgcn_mfma_f32_16x16x32_f16(l2, w, lo, 0, 0, 0);
+        const uint64_t all = __ballot(aid >= 0) & 0xffffu;
+        // 32 ranks after another, the distinct adapters among the tokens (wave-uniform)
+        // AH at a time: their weights are loaded together, the next ones before these
+        // ones' products
+        auto expand = [&](auto piece) {
+            constexpr int PIECE = decltype(piece)::value, AH = PIECE == 1 ? 1 : 4;
+            struct Some {
+                int id[AH];
+                half8_t w[AH];
+            };
+            uint64_t left = all;
+            auto load = [&](int c, Some& q) {
+#pragma unroll
+                for (int j = 0; j < AH; j++) {
+                    q.id[j] = left != 0 ? __builtin_amdgcn_readlane(aid, __builtin_ctzll(left)) : -1;
+                    left &= ~__ballot(aid == q.id[j]);
+                    q.w[j] = adapter_weights<PIECE>(ad, max(q.id[j], 0), N, brow + rloc, c);
                 }
-                const float f = tk.id == id ? tk.f : 0.0f;
-    #pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    const float fr = __shfl(f, 4 * qd + r, 64);
-                    acc[r] = fr != 0.0f ? acc[r] + fr * (hi[r] + lo[r]) : acc[r];
+            };
+            Some qa4, qb4;
+            load(8 * qd, qa4);
+            const AdapterToken tk = adapter_token<4, 16>(ad, min(l16, M - 1), min(l16, M - 1), l16 < M, qd);
+            half8_t th, tl;  // this lane's token's values c .. c + 7
+            auto products = [&](const Some& q) {
+#pragma unroll
+                for (int j = 0; j < AH; j++) {
+                    if (q.id[j] < 0)
+                        return;
+                    f32x4 hi = f32x4{0.0f, 0.0f, 0.0f, 0.0f}, lo = hi;
+                    hi = __builtin_amdgcn_mfma_f32_16x16x32_f16(th, q.w[j], hi, 0, 0, 0);
+                    lo = __builtin_amdgcn_mfma_f32_16x16x32_f16(tl, q.w[j], lo, 0, 0, 0);
+                    const float f = tk.id == q.id[j] ? tk.f : 0.0f;
+#pragma unroll
+                    for (int r = 0; r < 4; r++) {
+                        const float fr = __shfl(f, 4 * qd + r, 64);
+                        acc[r] = fr != 0.0f ? acc[r] + fr * (hi[r] + lo[r]) : acc[r];
+                    }
                 }
-                id = nid;
-                w0 = wn;
+            };
+            for (int c = 8 * qd; c < ad.rpad; c += 32) {
+                if (c >= 32) {
+                    left = all;
+                    load(c, qa4);
+                }
+                adapter_operand(tk, tk.id, c, th, tl);
+                while (qa4.id[0] >= 0) {
+                    load(c, qb4);
+                    products(qa4);
+                    if (qb4.id[0] < 0)
+                        break;
+                    load(c, qa4);
+                    products(qb4);
+                }
             }
         };
         if ((ad.rank & 7) == 0)  // uniform
-            expand(std::true_type{});
+            expand(std::integral_constant<int, 8>{});
+        else if ((ad.rank & 3) == 0)
+            expand(std::integral_constant<int, 4>{});
         else
-            expand(std::false_type{});
+            expand(std::integral_constant<int, 1>{});
     }
 
     // D element r of lane l: token 4 (l / 16) + r, row l % 16

@@ -3,7 +3,9 @@
 //   y[m][i] += alpha_r sum_c B_r[i][c] t[m][c],   r = which[m], t[m] = A_r x[m]
 // t is fp32 [M][rpad] (adapters.hip writes it, rpad = rank rounded up to 32, the
 // padding zero); a token whose which[m] lies outside [0, count) has no adapter,
-// and its row of t is not defined.
+// and its row of t is not defined. Above 16 tokens the products take the tokens
+// grouped by adapter: position p of that order is token order[p], and row p of t
+// is that token's.
 //
 // On the matrix cores the tokens of a tile may belong to different adapters: the
 // tile runs once per distinct adapter among them, into accumulators of its own,
@@ -25,12 +27,13 @@ struct AdapterArgs {
     const float* alpha;   // [count]
     const int32_t* which; // [M]
     const float* t;       // [M][rpad]
+    const int32_t* order; // [M], above 16 tokens
     int32_t count, rank, rpad;
 };
 
 inline AdapterArgs adapter_args(const AdapterDesc& a)
 {
-    return AdapterArgs{a.B, a.alpha, a.which, a.t, a.count, a.rank, adapter_rpad(a.rank)};
+    return AdapterArgs{a.B, a.alpha, a.which, a.t, a.order, a.count, a.rank, adapter_rpad(a.rank)};
 }
 
 // A lane's view of one token's adapter: its index (-1: none), the exponent that
@@ -41,14 +44,14 @@ struct AdapterToken {
     float f;
 };
 
-// The token m of this lane (live: it exists); PARTS lanes share a token, at lane
+// The token m of this lane (live: it exists), row p of t; PARTS lanes share a token, at lane
 // distances D, 2 D, ..., and lane part p reads values 8 p .. 8 p + 7 of every
 // 8 PARTS of the row.
 template <int PARTS, int D>
-__device__ __forceinline__ AdapterToken adapter_token(const AdapterArgs& ad, int64_t m, bool live, int part)
+__device__ __forceinline__ AdapterToken adapter_token(const AdapterArgs& ad, int64_t m, int64_t p, bool live, int part)
 {
     AdapterToken k;
-    k.t = ad.t + m * ad.rpad;
+    k.t = ad.t + p * ad.rpad;
     const int id = ad.which[m];
     k.id = live && id >= 0 && id < ad.count ? id : -1;
     float mx = 0.0f;
@@ -86,17 +89,25 @@ __device__ __forceinline__ void adapter_operand(const AdapterToken& k, int id, i
     }
 }
 
-// Values c .. c + 7 of row B_id[i], zeros past the rank. WIDE: the rank is a multiple
-// of 8, so every piece is 16-byte aligned and whole.
-template <bool WIDE>
+// Values c .. c + 7 of row B_id[i], zeros past the rank. PIECE: values per load, 8 or
+// 4 where the rank is a multiple (pieces are then whole and aligned), else 1: single
+// values cost the vector memory path as many cycles as whole pieces (8 tokens of 8
+// requests, 4096 -> 4096 at rank 100: 38 us by ones, 24 by fours).
+template <int PIECE>
 __device__ __forceinline__ half8_t adapter_weights(const AdapterArgs& ad, int id, int64_t N, int64_t i, int c)
 {
     // loads clamped to the row, values past it selected away: no branch per lane
     const uint16_t* row = ad.B + ((int64_t)id * N + i) * ad.rank;
-    if constexpr (WIDE) {
+    if constexpr (PIECE == 8) {
         const uint4 v = *reinterpret_cast<const uint4*>(row + min(c, ad.rank - 8));
         const bool on = c < ad.rank;
         return __builtin_bit_cast(half8_t, make_uint4(on ? v.x : 0u, on ? v.y : 0u, on ? v.z : 0u, on ? v.w : 0u));
+    }
+    if constexpr (PIECE == 4) {
+        const uint2 v = *reinterpret_cast<const uint2*>(row + min(c, ad.rank - 4));
+        const uint2 w = *reinterpret_cast<const uint2*>(row + min(c + 4, ad.rank - 4));
+        const bool on = c < ad.rank, on4 = c + 4 < ad.rank;
+        return __builtin_bit_cast(half8_t, make_uint4(on ? v.x : 0u, on ? v.y : 0u, on4 ? w.x : 0u, on4 ? w.y : 0u));
     }
     uint32_t v[8];
 #pragma unroll

@@ -136,10 +136,11 @@ struct AdapterDesc {
     const float* alpha;    // [count]
     const int32_t* which;  // [M]
     float* t;
+    int32_t* order;        // [M] (workspace): the tokens grouped by adapter, above kMfvMaxM tokens
     int32_t count, rank;
 };
 constexpr int adapter_rpad(int rank) { return (rank + 31) & ~31; }
-size_t adapter_workspace_bytes(int rank, int64_t M);
+size_t adapter_workspace_bytes(int rank, int64_t M);  // t, then order
 hipError_t launch_adapter_shrink(const AdapterDesc& a, const uint16_t* x, int64_t M, int64_t K, hipStream_t s);
 // The shared product with the adapters' second products: up to 16 tokens
 // launch_gemv / launch_mfv with the adapters given, above this.

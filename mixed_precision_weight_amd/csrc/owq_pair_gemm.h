@@ -76,12 +76,17 @@ __device__ __forceinline__ half8_t pair_weak(const PairLayer& P, int64_t row, in
     return __builtin_bit_cast(half8_t, v);
 }
 
+// Tokens whose order is given are permuted within runs of this many, so that a run's
+// rows of x stay within 32-bit offsets.
+constexpr int kPairRun = 1024;
+
 // The sums of one wave of the block (its rows: row set l starts at n0[l], which may
-// lie past N; tokens from m0; SAME: both sets are rows of the one layer L[0]). Returns false for the K groups that handed theirs
-// over, whose waves are done.
-template <int FM, int WN, int S, bool SAME>
-__device__ __forceinline__ bool pair_gemm(const PairLayer* L, const uint16_t* x, int M, int N, int K, int m0,
-                                          const int (&n0)[2], f32x16 (&acc)[2][FM])
+// lie past N; tokens from m0; ONE: both sets are rows of the one layer L[0], and
+// row m of the product is token order[m]). Returns false for the K groups that
+// handed theirs over, whose waves are done.
+template <int FM, int WN, int S, bool ONE>
+__device__ __forceinline__ bool pair_gemm(const PairLayer* L, const uint16_t* x, const int32_t* order, int M, int N, int K,
+                                          int m0, const int (&n0)[2], f32x16 (&acc)[2][FM])
 {
     using T = PairTile<FM, WN, S>;
     constexpr int BM = T::BM, BN = T::BN, STAGE = T::STAGE, DPW = T::DPW;
@@ -99,8 +104,17 @@ __device__ __forceinline__ bool pair_gemm(const PairLayer* L, const uint16_t* x,
     const int l32 = lane & 31, h = lane >> 5;
     const int mv = min(BM, M - m0);
 
+    static_assert(kPairRun % BM == 0, "a tile lies in one run");
+    const int base = ONE ? m0 / kPairRun * kPairRun : m0;
     const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint16_t*>(x) + (int64_t)m0 * K, (short)0, mv * K * 2, 0x00020000);
+        const_cast<uint16_t*>(x) + (int64_t)base * K, (short)0, (ONE ? min(kPairRun, M - base) : mv) * K * 2, 0x00020000);
+    // row of x, relative to the base, of the tile's token t (past M: the last one)
+    auto token = [&](int t) {
+        if constexpr (ONE)
+            return order[m0 + min(t, mv - 1)] - base;
+        else
+            return min(t, mv - 1);
+    };
     // row sets: first row and rows (a set past N reads the last row; never stored)
     int nb[2], nv[2];
     __amdgpu_buffer_rsrc_t qr[2];
@@ -108,7 +122,7 @@ __device__ __forceinline__ bool pair_gemm(const PairLayer* L, const uint16_t* x,
     for (int l = 0; l < 2; l++) {
         nb[l] = min(n0[l], N - 1);
         nv[l] = min(BN, N - nb[l]);
-        qr[l] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint32_t*>(L[SAME ? 0 : l].q) + (int64_t)nb[l] * G * 3, (short)0,
+        qr[l] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint32_t*>(L[ONE ? 0 : l].q) + (int64_t)nb[l] * G * 3, (short)0,
                                                   nv[l] * G * 12, 0x00020000);
     }
 
@@ -122,7 +136,7 @@ __device__ __forceinline__ bool pair_gemm(const PairLayer* L, const uint16_t* x,
     for (int t = 0; t < DPW; t++) {
         const int u = (wn * DPW + t) * 64 + lane;
         const int row = u >> 3, piece = (u & 7) ^ (row & 7);
-        xsrc[t] = min(row, mv - 1) * K * 2 + piece * 16;
+        xsrc[t] = token(row) * K * 2 + piece * 16;
         xdead[t] = (odd_tail && piece >= 4) ? 0x40000000 : 0;
     }
     auto dma = [&](int c, char* stage) {
@@ -139,7 +153,7 @@ __device__ __forceinline__ bool pair_gemm(const PairLayer* L, const uint16_t* x,
 #pragma unroll
     for (int l = 0; l < 2; l++) {
         row[l] = min(wn * 32 + l32, nv[l] - 1);
-        zs[l] = make_zero_sub((uint32_t)L[SAME ? 0 : l].z[nb[l] + row[l]]);
+        zs[l] = make_zero_sub((uint32_t)L[ONE ? 0 : l].z[nb[l] + row[l]]);
     }
     typedef u32x3 QRegs[2];
     auto load_q = [&](int c, QRegs& cw) {
@@ -215,7 +229,7 @@ __device__ __forceinline__ bool pair_gemm(const PairLayer* L, const uint16_t* x,
     // and meets w_weak as four 16-deep steps. The K groups take the 64s in turn.
 #pragma unroll
     for (int l = 0; l < 2; l++) {
-        const float sc = h2f(L[SAME ? 0 : l].s[nb[l] + row[l]]);
+        const float sc = h2f(L[ONE ? 0 : l].s[nb[l] + row[l]]);
 #pragma unroll
         for (int i = 0; i < FM; i++)
 #pragma unroll
@@ -224,7 +238,7 @@ __device__ __forceinline__ bool pair_gemm(const PairLayer* L, const uint16_t* x,
     }
     char* const xw = xs0[kg];
 #pragma unroll
-    for (int l = 0; l < (SAME ? 1 : 2); l++) {
+    for (int l = 0; l < (ONE ? 1 : 2); l++) {
         const PairLayer& P = L[l];
         const int passes = (P.k + 63) >> 6;
         for (int p0 = 0; p0 < passes; p0 += S) {  // the same trip count in every group
@@ -241,7 +255,7 @@ __device__ __forceinline__ bool pair_gemm(const PairLayer* L, const uint16_t* x,
 #pragma unroll
                     for (int t = 0; t < TB; t++)
                         v[t] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
-                            xr, 2 * (min(wn + WN * (t0 + t), mv - 1) * K + j), 0, 0);
+                            xr, 2 * (token(wn + WN * (t0 + t)) * K + j), 0, 0);
 #pragma unroll
                     for (int t = 0; t < TB; t++) {
                         const int tok = wn + WN * (t0 + t);
@@ -256,13 +270,13 @@ __device__ __forceinline__ bool pair_gemm(const PairLayer* L, const uint16_t* x,
                 for (int st = 0; st < 4; st++) {
                     half8_t bv[2];
 #pragma unroll
-                    for (int w = 0; w < (SAME ? 2 : 1); w++)
-                        bv[w] = pair_weak(P, nb[SAME ? w : l] + row[SAME ? w : l], c + 32 * h + 8 * st);
+                    for (int w = 0; w < (ONE ? 2 : 1); w++)
+                        bv[w] = pair_weak(P, nb[ONE ? w : l] + row[ONE ? w : l], c + 32 * h + 8 * st);
 #pragma unroll
                     for (int i = 0; i < FM; i++) {
                         const half8_t av =
                             __builtin_bit_cast(half8_t, *reinterpret_cast<const uint4*>(xw + arow + i * 32 * 128 + aoff[st]));
-                        if constexpr (SAME) {
+                        if constexpr (ONE) {
                             acc[0][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(av, bv[0], acc[0][i], 0, 0, 0);
                             acc[1][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(av, bv[1], acc[1][i], 0, 0, 0);
                         } else {

@@ -173,6 +173,31 @@ def test_every_decode_kernel(owq, decode, M, monkeypatch):
         _check(y, ref, bound, f"{decode} {products}")
 
 
+@pytest.mark.parametrize("M", [17, 1023, 1024, 1025, 2100])
+def test_tokens_of_many_requests(owq, M):
+    """More tokens than are grouped at a time, adapters 256 apart (one bucket), one token or all of one request:
+    a token's output is that of the same token on its own rows, wherever it stands."""
+    N, K, k, rank, count = 37, 96, 2, 4, 600
+    W, idx, x, A, B, alpha = _make(N, K, k, M, rank, count, M)
+    layer = _layer(owq, W, idx)
+    ads = {"A": dev(A), "B": dev(B), "alpha": dev(alpha)}
+    rng = np.random.default_rng(M)
+    for name, which in (("any", rng.integers(-3, count + 3, M)),
+                        ("one bucket", 7 + 256 * rng.integers(0, 3, M)),
+                        ("descending", (M - 1 - np.arange(M)) % count),
+                        ("a lone one", np.where(np.arange(M) == M - 1, 255, -1)),
+                        ("all", np.full(M, 511))):
+        which = which.astype(np.int32)
+        print(f"adapters: {M} tokens, {name}", flush=True)
+        y = host(owq.linear_adapters(layer, ads, dev(which), dev(x)))
+        ref, bound = _reference(layer, x, A, B, alpha, which)
+        err = np.abs(y.astype(np.float64) - ref)
+        assert (err <= 2e-3 * bound + 1e-5).all(), name
+        turn = rng.permutation(M)
+        z = host(owq.linear_adapters(layer, ads, dev(which[turn]), dev(np.ascontiguousarray(x[turn]))))
+        assert z.tobytes() == y[turn].tobytes(), name
+
+
 def test_graph_and_other_stream(owq):
     """Captured and replayed with the requests' adapters changing between replays; another stream."""
     import torch
