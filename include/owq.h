@@ -582,7 +582,7 @@ size_t owq_clip_grad_norm_workspace_bytes(int32_t count);
  * Tuning", p.5)):
  *   norm   = sqrt(sum over every tensor and element of g^2)   fp64 sums
  *   out    = g * (max_norm / norm) if norm > max_norm, else g  fp64 product,
- *            rounded once (nearest-even) to the tensor's type
+ *            rounded to the tensor's type (nearest-even; fp16 by way of fp32)
  * norm is written as fp32 [1] (infinity above its range); the comparison and the
  * factor use the fp64 value. If it is not finite (an infinity or NaN among the
  * gradients) nothing is scaled: the caller sees it and drops the step. max_norm:

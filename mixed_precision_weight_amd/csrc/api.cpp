@@ -957,7 +957,7 @@ owq_status owq_clip_grad_norm(const owq_grad* items, int32_t count, double max_n
             const size_t size = g.type ? 2 : 4;
             if (g.n > 0 && (!aligned(g.g, size) || !aligned(g.out, size)))
                 return fail(OWQ_ERR_ALIGN, "item %d: misaligned pointer (%zu B)", i, size);
-            it[(size_t)i] = owq::ClipEntry{g.g, g.out, g.n, 0, g.type};
+            it[(size_t)i] = owq::ClipEntry{g.g, g.out, g.n, g.type};
             if (g.n > 0)
                 outs.emplace_back((uintptr_t)g.out, (uintptr_t)g.out + (size_t)g.n * size);
         }

@@ -209,10 +209,9 @@ struct ClipEntry {
     const void* g;
     void* out;       // == g: in place
     int64_t n;
-    int64_t chunk0;  // first chunk of the tensor (set by launch_clip)
     int32_t half;    // 1: fp16, 0: fp32
 };
-constexpr int kClipItems = 80;  // tensors per launch of the first pass (kernel arguments below 4 KB)
+constexpr int kClipItems = 240;  // tensors per launch (kernel arguments below 4 KB)
 size_t clip_workspace_bytes(int count);
 hipError_t launch_clip(const ClipEntry* items, int count, double max_norm, float* norm, void* ws, hipStream_t s);
 

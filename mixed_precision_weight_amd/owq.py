@@ -7,8 +7,10 @@ fallback path.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
+from itertools import chain
 
 import torch
 
@@ -1146,6 +1148,7 @@ def clip_grad_norm_workspace_bytes(sizes: list) -> int:
 
 
 _GRAD_TYPES = {torch.float32: 0, torch.float16: 1}  # owq_grad's type
+_TENSORS = {torch.Tensor, torch.nn.Parameter}
 
 
 def _grads_checked(grads: list, outs):
@@ -1179,7 +1182,7 @@ def clip_grad_norm(grads: list, max_norm: float, outs: list | None = None, norm:
     # by one (for the message) only when something is wrong
     T = torch.Tensor
     every = list(grads) if outs is None else list(grads) + list(outs)
-    if all([isinstance(t, T) for t in every]):
+    if set(map(type, every)) <= _TENSORS or all([isinstance(t, T) for t in every]):
         types = [t.dtype for t in every]
         counts = list(map(T.numel, every))
         good = (all(map(T.is_contiguous, every)) and set(types) <= _GRAD_TYPES.keys()
@@ -1203,12 +1206,11 @@ def clip_grad_norm(grads: list, max_norm: float, outs: list | None = None, norm:
         if workspace is None:
             workspace = run.empty(clip_grad_norm_workspace_bytes(every[:n]), torch.uint8)
         ptrs = list(map(T.data_ptr, every))
-        words = (_I64 * (4 * n))()  # one owq_grad is four 64-bit words (type in the low half of the last)
-        words[0::4] = ptrs[:n]
-        words[1::4] = ptrs[-n:]
-        words[2::4] = counts[:n]
-        words[3::4] = [_GRAD_TYPES[t] for t in types[:n]]
-        _check(lib().owq_clip_grad_norm(ctypes.cast(words, ctypes.POINTER(OwqGrad)), n, max_norm, norm.data_ptr(),
+        # one owq_grad is four 64-bit words (type in the low half of the last)
+        kinds = map(_GRAD_TYPES.__getitem__, types)
+        words = array.array("q", chain.from_iterable(zip(ptrs[:n], ptrs[-n:], counts, kinds)))
+        table = (OwqGrad * n).from_buffer(words)
+        _check(lib().owq_clip_grad_norm(table, n, max_norm, norm.data_ptr(),
                                         workspace.data_ptr(), workspace.numel(), run.handle), "owq_clip_grad_norm")
     return norm
 

@@ -65,6 +65,10 @@ CASES = [
     ([3 * i * i % 20011 + 1 for i in range(301)], [np.float32 if i % 3 else np.float16 for i in range(301)]),
     ([7 + i for i in range(80)], [np.float16] * 80),
     ([7 + i for i in range(81)], [np.float32] * 81),
+    ([5 + 40 * i for i in range(240)], [np.float32, np.float16] * 120),
+    ([8193 - 30 * i for i in range(241)], [np.float16] * 241),
+    ([0] * 240 + [9000, 0, 3], [np.float32] * 243),
+    ([100 + i % 7 for i in range(483)], [np.float32] * 483),
 ]
 
 
