@@ -497,8 +497,8 @@ typedef enum {
  * fp16 once. gate, up: HOST pointers to packed layers of the same N and K (their
  * weak columns may differ); x: fp16 [M][K]; h: fp16 [M][N] (output); g, u: fp32
  * [M][N] outputs for owq_gated_backward, both or neither NULL. act: an
- * owq_activation. Errors as owq_linear, plus OWQ_ERR_SHAPE for layers that do not
- * match, OWQ_ERR_UNSUPPORTED for an unknown act, OWQ_ERR_NULL for one of g, u. */
+ * owq_activation. M, N <= 2^30. Errors as owq_linear, plus OWQ_ERR_SHAPE for layers
+ * that do not match, OWQ_ERR_UNSUPPORTED for an unknown act, OWQ_ERR_NULL for one of g, u. */
 owq_status owq_gated(const owq_layer* gate, const owq_layer* up, const uint16_t* x, int64_t M, int32_t act,
                      uint16_t* h, float* g, float* u, void* stream);
 
@@ -556,8 +556,8 @@ size_t owq_linear_adapters_workspace_bytes(int32_t rank, int64_t M);
  * are not finite. Two launches: the low-rank products; the linear with the second
  * products in its epilogue. workspace: >=
  * owq_linear_adapters_workspace_bytes(rank, M) bytes, 256-byte aligned, contents
- * ignored; calls sharing it must be ordered. Other arguments and errors as
- * owq_linear, plus OWQ_ERR_WORKSPACE, and OWQ_ERR_SHAPE for count and rank. */
+ * ignored; calls sharing it must be ordered. M, N <= 2^30. Other arguments and errors
+ * as owq_linear, plus OWQ_ERR_WORKSPACE, and OWQ_ERR_SHAPE for count and rank. */
 owq_status owq_linear_adapters(const owq_layer* L, const owq_adapters* ad, const int32_t* which,
                                const uint16_t* x, int64_t M, uint16_t* y, void* workspace,
                                size_t workspace_bytes, void* stream);

@@ -50,6 +50,7 @@ bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 constexpr int64_t kMaxK = 65536;
 constexpr int32_t kMaxRank = 256;    // of a low-rank adapter
+constexpr int64_t kMaxBlock = (int64_t)1 << 30;  // tokens and rows of the gated block and the adapted linear
 constexpr int32_t kMaxGrads = 4096;  // tensors per owq_clip_grad_norm
 
 owq_status check_k_dim(int64_t K)
@@ -140,6 +141,8 @@ owq_status check_gated(const owq_layer* gate, const owq_layer* up, int64_t M, co
     st = check_layer(up, M, x, h);
     if (st != OWQ_OK)
         return fail_at(st, "layer", 1);
+    if (M > kMaxBlock || gate->N > kMaxBlock)
+        return fail(OWQ_ERR_SHAPE, "M = %lld, N = %lld: need at most 2^30", (long long)M, (long long)gate->N);
     if (gate->N != up->N || gate->K != up->K)
         return fail(OWQ_ERR_SHAPE, "gate is %lld x %lld, up is %lld x %lld", (long long)gate->N, (long long)gate->K,
                     (long long)up->N, (long long)up->K);
@@ -878,7 +881,7 @@ owq_status owq_gated_backward(const owq_layer* gate, const owq_layer* up, const 
 
 size_t owq_linear_adapters_workspace_bytes(int32_t rank, int64_t M)
 {
-    if (rank < 1 || rank > kMaxRank || M < 1 || M > INT32_MAX)
+    if (rank < 1 || rank > kMaxRank || M < 1 || M > kMaxBlock)
         return 0;
     return owq::adapter_workspace_bytes(rank, M);
 }
@@ -889,6 +892,8 @@ owq_status owq_linear_adapters(const owq_layer* L, const owq_adapters* ad, const
     owq_status st = check_layer(L, M, x, y);
     if (st != OWQ_OK)
         return st;
+    if (M > kMaxBlock || L->N > kMaxBlock)
+        return fail(OWQ_ERR_SHAPE, "M = %lld, N = %lld: need at most 2^30", (long long)M, (long long)L->N);
     if (!ad || !ad->A || !ad->B || !ad->alpha || !which || !workspace)
         return fail(OWQ_ERR_NULL, "adapters (A, B, alpha), which and workspace must be non-NULL");
     if (ad->rank < 1 || ad->rank > kMaxRank)

@@ -547,3 +547,15 @@ def test_gated_backward_validation(lib):
     # nothing wanted: nothing is enqueued
     assert call(x=None, dx=None, dwg=None, dwu=None) == 0
     assert call(gate=layer(k=0, idx=None), up=layer(k=0, idx=None), x=None, dx=None) == 0
+
+
+def test_block_size_limits(lib):
+    """Tokens and rows beyond 2^30 are refused before a launch could count them in 32 bits."""
+    from mixed_precision_weight_amd.owq import OwqAdapters, OwqLayer
+    big = 2 ** 30 + 1
+    a = OwqAdapters(FAKE, FAKE, FAKE, 3, 16)
+    for N, M in ((64, big), (big, 5)):
+        L = ctypes.byref(OwqLayer(N, 128, 4, 3, FAKE, FAKE, FAKE, FAKE, FAKE))
+        assert lib.owq_gated(L, L, FAKE, M, 0, FAKE, None, None, None) == 2
+        assert lib.owq_linear_adapters(L, ctypes.byref(a), FAKE, FAKE, M, FAKE, FAKE, 2 ** 62, None) == 2
+    assert lib.owq_linear_adapters_workspace_bytes(16, big) == 0
