@@ -100,11 +100,17 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t shrink_rsrc(const uint16_t* p,
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), (short)0, (int)(elems * 2), 0x00020000);
 }
 
+// Units (a tile's slot) are counted by this many tiles: whole rounds of the XCDs
+__host__ __device__ constexpr int shrink_round(int tiles)
+{
+    return tiles < 8 ? tiles : (tiles + 7) / 8 * 8;
+}
+
 __global__ __launch_bounds__(64 * kShrinkWaves) void k_adapter_shrink(const uint16_t* __restrict__ x,
                                                                       const uint16_t* __restrict__ A,
                                                                       const int32_t* __restrict__ which,
                                                                       float* __restrict__ t, int32_t* __restrict__ order,
-                                                                      int M, int K, int count, int rank, int rpad)
+                                                                      int M, int K, int count, int rank, int rpad, int slots)
 {
     __shared__ float4 red[kShrinkWaves][64];
     __shared__ GroupScratch group;
@@ -113,11 +119,16 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void k_adapter_shrink(const uint
     const int l16 = lane & 15, qd = lane >> 4;
     // Blocks go to the 8 XCDs in turn: the rank tiles of a token tile run on one XCD,
     // so its x comes into one L2 once (47 -> 25 us at 1000 tokens, rank 64, K = 11008).
-    // Token tiles go round the XCDs: with runs of tiles on one, 27 us became 46
-    const int xcd = (int)blockIdx.x & 7, slot = (int)blockIdx.x >> 3;
-    const int rt = rpad >> 4, tiles = (M + 15) >> 4;
-    const int tile = xcd + 8 * (slot / rt), r0 = (slot % rt) * 16;
-    if (tile >= tiles)
+    // Token tiles go round the XCDs (with runs of tiles on one, 27 us became 46). The
+    // slots of a tile stay on its XCD, too (33 us where they did not), but for few
+    // tiles, whose adapters would all come through one XCD (8 tokens of 8 requests,
+    // rank 100, K = 4096: 16.8 us on one, 9.5 on all)
+    const int xcd = (int)blockIdx.x & 7, i = (int)blockIdx.x >> 3;
+    const int rt = (rank + 15) >> 4, tiles = (M + 15) >> 4;
+    const int unit = xcd + 8 * (i / rt), r0 = (i % rt) * 16;
+    const int round = shrink_round(tiles);
+    const int tile = unit % round, slot = unit / round;
+    if (tile >= tiles || slot >= slots)
         return;
     // this lane's token, at position p of the order
     const int p = tile * 16 + l16;
@@ -127,7 +138,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void k_adapter_shrink(const uint
         group_tokens(group, which, M, count, base, tile * 16);
         const int at = m - tile * 16;  // (m < M: that position is filled)
         m = group.token[at], id = group.id[at];
-        if (r0 == 0 && blockIdx.y == 0 && threadIdx.x < 16 && p < M)
+        if (r0 == 0 && slot == 0 && threadIdx.x < 16 && p < M)
             order[p] = m;
     } else {
         id = which[m];
@@ -146,36 +157,34 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void k_adapter_shrink(const uint
     for (int d = 0; left != 0; d++) {
         const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
         left &= ~__ballot(id == a);
-        if (d % (int)gridDim.y != (int)blockIdx.y)
+        if (d % slots != slot)
             continue;
         const __amdgpu_buffer_rsrc_t ar = shrink_rsrc(A + (int64_t)a * rank * K, (int64_t)rank * K);
         float4_t acc[2] = {float4_t{0.0f, 0.0f, 0.0f, 0.0f}, float4_t{0.0f, 0.0f, 0.0f, 0.0f}};
-        if (r0 < rank) {  // (a tile of padding ranks only stores its zeros)
-            // steps past the wave's end are read out of range: zeros, nothing fetched
-            half8_t xv[kShrinkFlight], av[kShrinkFlight];
-            auto load = [&](int s, int u) {
-                const int o = s + u < s1 ? (s + u) * 64 : 0x40000000;
-                xv[u] = __builtin_bit_cast(half8_t, __builtin_amdgcn_raw_buffer_load_b128(xr, xo + o, 0, 0));
-                av[u] = __builtin_bit_cast(half8_t, __builtin_amdgcn_raw_buffer_load_b128(ar, ao + o, 0, 0));
-            };
-            auto product = [&](int u) {
-                acc[u & 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv[u], av[u], acc[u & 1], 0, 0, 0);
-            };
+        // steps past the wave's end are read out of range: zeros, nothing fetched
+        half8_t xv[kShrinkFlight], av[kShrinkFlight];
+        auto load = [&](int s, int u) {
+            const int o = s + u < s1 ? (s + u) * 64 : 0x40000000;
+            xv[u] = __builtin_bit_cast(half8_t, __builtin_amdgcn_raw_buffer_load_b128(xr, xo + o, 0, 0));
+            av[u] = __builtin_bit_cast(half8_t, __builtin_amdgcn_raw_buffer_load_b128(ar, ao + o, 0, 0));
+        };
+        auto product = [&](int u) {
+            acc[u & 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv[u], av[u], acc[u & 1], 0, 0, 0);
+        };
 #pragma unroll
-            for (int u = 0; u < kShrinkFlight; u++)
-                load(s0, u);
-            int s = s0;
-            for (; s + kShrinkFlight < s1; s += kShrinkFlight) {
+        for (int u = 0; u < kShrinkFlight; u++)
+            load(s0, u);
+        int s = s0;
+        for (; s + kShrinkFlight < s1; s += kShrinkFlight) {
 #pragma unroll
-                for (int u = 0; u < kShrinkFlight; u++) {
-                    product(u);
-                    load(s + kShrinkFlight, u);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kShrinkFlight; u++)
+            for (int u = 0; u < kShrinkFlight; u++) {
                 product(u);
+                load(s + kShrinkFlight, u);
+            }
         }
+#pragma unroll
+        for (int u = 0; u < kShrinkFlight; u++)
+            product(u);
         const float4_t sum = acc[0] + acc[1];
         __syncthreads();  // the previous adapter's sums are no longer read
         red[wave][lane] = make_float4(sum[0], sum[1], sum[2], sum[3]);
@@ -192,8 +201,12 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void k_adapter_shrink(const uint
 #pragma unroll
             for (int r = 0; r < 4; r++) {
                 const int tok = 4 * qd + r;
-                if (__shfl(id, tok, 64) == a)
-                    t[((int64_t)tile * 16 + tok) * rpad + r0 + l16] = live ? o[r] : 0.0f;
+                if (__shfl(id, tok, 64) == a) {
+                    float* tr = t + ((int64_t)tile * 16 + tok) * rpad + r0 + l16;
+                    tr[0] = live ? o[r] : 0.0f;
+                    if (r0 + 16 >= rank && r0 + 16 < rpad)
+                        tr[16] = 0.0f;
+                }
             }
         }
     }
@@ -357,17 +370,19 @@ hipError_t launch_adapter_shrink(const AdapterDesc& a, const uint16_t* x, int64_
 {
     const int rpad = adapter_rpad(a.rank);
     const int64_t tiles = (M + 15) / 16;
-    const int rt = rpad / 16;
-    // blocks per tile that share its distinct adapters: all 16 of a decode step's
-    // tile side by side; with many tiles each walks its own (prompts: one or two)
+    const int rt = (a.rank + 15) / 16;
+    // blocks per tile that share its distinct adapters: the 16 of a decode step's tile
+    // side by side; grouped tiles hold one mostly, and the few that hold two would run
+    // on alone after the others (1000 tokens, rank 64: 43 us with one slot, 27 with two)
     int64_t slots = 512 / (tiles * rt);
-    slots = slots < 1 ? 1 : (slots > 16 ? 16 : slots);
+    slots = slots < 2 ? 2 : (slots > 16 ? 16 : slots);
     if (slots > M)
         slots = M;
-    const int64_t nb = (tiles + 7) / 8 * 8 * rt;
+    const int64_t nb = ((int64_t)shrink_round((int)tiles) * slots + 7) / 8 * 8 * rt;
     if (nb > INT32_MAX)
         return hipErrorInvalidValue;
-    hipLaunchKernelGGL(k_adapter_shrink, dim3((unsigned)nb, (unsigned)slots), dim3(64 * kShrinkWaves), 0, s, x, a.A, a.which, a.t, a.order, (int)M, (int)K, a.count, a.rank, rpad);
+    hipLaunchKernelGGL(k_adapter_shrink, dim3((unsigned)nb), dim3(64 * kShrinkWaves), 0, s, x, a.A, a.which, a.t, a.order,
+                       (int)M, (int)K, a.count, a.rank, rpad, (int)slots);
     return hipGetLastError();
 }
 
