@@ -331,14 +331,19 @@ __device__ __forceinline__ bool pair_gemm(const PairLayer* L, const uint16_t* x,
 // So: the largest tile that gives about 170 blocks (two thirds of the CUs), K split
 // in two where 64 x 64 gives 128, else 32 x 32 with K split in four. (Tiles of 128 x
 // 64, 64 x 32 and 32 x 32 with K whole or in two were never the fastest by more
-// than 3 %.)
+// than 3 %.) The largest tile splits K in two as well while no CU gets a second block,
+// so that each SIMD still has two waves: 4096 x 11008, M = 512 140 -> 130, 640 144 ->
+// 135, 1000 165 -> 163 (344 blocks, 2048 x 4096 x 11008: 344 -> 401). For 64 x 128 that
+// came to between - 7 and + 5 %, and it stays whole.
 template <typename F>
 hipError_t pair_tile(int64_t M, int64_t rows, F f)
 {
     auto blocks = [&](int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((rows + bn - 1) / bn); };
     using std::integral_constant;
-    if (M > 64 && blocks(128, 128) >= 170)
+    if (M > 64 && blocks(128, 128) > 256)
         return f(integral_constant<int, 4>{}, integral_constant<int, 4>{}, integral_constant<int, 1>{});
+    if (M > 64 && blocks(128, 128) >= 170)
+        return f(integral_constant<int, 4>{}, integral_constant<int, 4>{}, integral_constant<int, 2>{});
     if (blocks(64, 128) >= 170)
         return f(integral_constant<int, 2>{}, integral_constant<int, 4>{}, integral_constant<int, 1>{});
     if (M > 32 && blocks(64, 64) >= 128)

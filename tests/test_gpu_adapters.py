@@ -87,6 +87,9 @@ CASES = [
     (4200, 544, 9, 150, 8, 3),
     (20000, 96, 3, 260, 8, 3),
     (40000, 64, 3, 260, 4, 3),
+    (44000, 64, 2, 40, 16, 3),
+    (16600, 96, 3, 50, 12, 5),
+    (22000, 160, 3, 200, 3, 4),
 ]
 
 

@@ -95,6 +95,7 @@ CASES = [
     (19300, 96, 3, 2, 300),
     (28700, 64, 3, 2, 100),
     (300, 11008, 9, 7, 100),
+    (14000, 1056, 40, 70, 200),
     # many rows: four per wave, four row waves
     (16500, 64, 3, 2, 1),
     (16500, 160, 3, 140, 2),
