@@ -28,6 +28,15 @@
 //                  do not fill the GPU
 //  5 k_gated_fin   adds the splits' and the token slabs' partial sums, in order
 // Every sum's order is fixed, so results are deterministic.
+//
+// Measured, M = 2048, two layers of 11008 x 4096, 32 weak columns each, us:
+//  1   77  225 MB read, 2.9 TB/s; the vector memory path is 61 % busy (a token's row
+//          per lane), the fp32 matrix instructions and the activations fill the rest
+//  2    5
+//  3   73  225 MB read, 90 written: 4.3 TB/s
+//  4  366  369 GFLOP: 1.01 PFLOP/s; matrix cores and the decode that feeds them
+//  5   22  67 MB of partial sums read, 17 written: 3.8 TB/s
+// At M = 77, 2731 x 1056 each launch takes 6 - 13 us: their latencies.
 #include "owq_act.h"
 #include "owq_decode.h"
 #include "owq_device.h"
