@@ -1,5 +1,7 @@
 """MI355X-native OWQ hot path: 3-bit mixed-precision linear layer and its
-calibration (Hessian diagonal, column sensitivity, weak-column selection).
+calibration (Hessian diagonal, column sensitivity, weak-column selection), and the
+operators round that linear: the gated half of a feed-forward block with its
+backward, low-rank adapters of many requests, gradient norm and clipping.
 
 Every step runs in hand-written HIP kernels for gfx950 behind the C ABI of
 ``libowq.so`` (declared in ``include/owq.h``); ``mixed_precision_weight_amd.owq``

@@ -146,3 +146,37 @@ def test_calls_side_by_side(owq):
         for outs in got[i]:
             for t, w in zip(outs, want[i]):
                 assert host(t).tobytes() == w.tobytes()
+
+
+@pytest.mark.parametrize("M", [1, 2, 4, 7, 16, 17, 70, 130])
+def test_nothing_is_written_behind_the_ends(owq, M):
+    """Outputs and workspaces of exactly the stated size, inside larger buffers whose other bytes stay as they were."""
+    import torch
+    N, K, count, rank = 131, 160, 3, 12
+    rng = np.random.default_rng(M)
+    gate, up = _layer(owq, rng, N, K, 4), _layer(owq, rng, N, K, 0)
+    _, ads = _adapters(rng, count, rank, N, K)
+    x = dev(rng.standard_normal((M, K)).astype(np.float16))
+    dh = dev(rng.standard_normal((M, N)).astype(np.float16))
+    which = dev(rng.integers(-1, count, M).astype(np.int32))
+    guard, buffers = 4096, []
+
+    def inside(shape, dtype):
+        n = int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size()
+        buf = torch.full((guard + n + guard,), 0xa5, dtype=torch.uint8, device="cuda:0")
+        buffers.append((buf, n))
+        return buf[guard:guard + n].view(dtype).view(shape)
+
+    owq.linear_adapters(gate, ads, which, x, y=inside((M, N), torch.float16),
+                        workspace=inside((owq.linear_adapters_workspace_bytes(rank, M),), torch.uint8))
+    owq.gated(gate, up, x, h=inside((M, N), torch.float16))
+    _, g, u = owq.gated(gate, up, x, save=True)
+    dx, dwg, dwu = owq.gated_backward(gate, up, x, g, u, dh, workspace=inside(
+        (owq.gated_backward_workspace_bytes(N, K, 4, 0, M),), torch.uint8))
+    grads = [dwg, dx]
+    outs = [inside(tuple(t.shape), t.dtype) for t in grads]
+    owq.clip_grad_norm(grads, 1e-3, outs=outs,
+                       workspace=inside((owq.clip_grad_norm_workspace_bytes([0, 0]),), torch.uint8))
+    torch.cuda.synchronize()
+    for i, (buf, n) in enumerate(buffers):
+        assert int((buf[:guard] != 0xa5).sum()) == 0 and int((buf[guard + n:] != 0xa5).sum()) == 0, i
