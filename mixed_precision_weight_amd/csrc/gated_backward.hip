@@ -474,23 +474,29 @@ __global__ __launch_bounds__(256) void k_gated_sums(const GatedBwdArgs a)
             a.texp[m] = scale_exp(mx);
         return;
     }
+    // 64 values per block, a quarter of the slabs per wave, 8 loads in flight
+    __shared__ float part[3][64];
     const int64_t n = (int64_t)a.M * (a.L[0].k + a.L[1].k);
-    const int64_t e = (int64_t)((int)blockIdx.x - a.work_blocks) * 256 + threadIdx.x;
-    if (e >= n)
-        return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t e = (int64_t)((int)blockIdx.x - a.work_blocks) * 64 + lane;
+    const int64_t ec = e < n ? e : n - 1;
+    const int per = (a.slabs + 3) >> 2, s1 = min(a.slabs, (wave + 1) * per);
     float t = 0.0f;
-    int s = 0;
-    for (; s + 8 <= a.slabs; s += 8) {
+    for (int s = wave * per; s < s1; s += 8) {
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; i++)
-            v[i] = a.PW[(s + i) * n + e];
+            v[i] = a.PW[min(s + i, s1 - 1) * n + ec];
 #pragma unroll
         for (int i = 0; i < 8; i++)
-            t += v[i];
+            t += s + i < s1 ? v[i] : 0.0f;
     }
-    for (; s < a.slabs; s++)
-        t += a.PW[s * n + e];
+    if (wave > 0)
+        part[wave - 1][lane] = t;
+    __syncthreads();
+    if (wave > 0 || e >= n)
+        return;
+    t = ((t + part[0][lane]) + part[1][lane]) + part[2][lane];
     a.PWs[e] = t;
 }
 
@@ -902,7 +908,7 @@ hipError_t launch_gated_backward(const LinearDesc& gate, const LinearDesc& up, i
     }
     if (dx) {
         a.work_blocks = (int32_t)cdiv(M, 4);
-        hipLaunchKernelGGL(k_gated_sums, dim3((unsigned)(a.work_blocks + cdiv(M * kt, 256))), dim3(256), 0, s, a);
+        hipLaunchKernelGGL(k_gated_sums, dim3((unsigned)(a.work_blocks + cdiv(M * kt, 64))), dim3(256), 0, s, a);
     }
     {
         const dim3 grid((unsigned)(p.Np / 64 * p.tslabs), any_dw ? wtiles : 1u);

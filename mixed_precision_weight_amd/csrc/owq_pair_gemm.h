@@ -60,20 +60,34 @@ struct PairTile {
     static_assert((S - 1) * WN * 4096 <= S * STAGE, "one accumulator block of every other group fits a stage set");
 };
 
-// w_weak[row][c .. c + 7] as an operand, zeros past the weak columns
+// w_weak[row][c .. c + 7] as an operand, zeros past the weak columns (c: a multiple of
+// 8). The piece is loaded whole, clamped to the row, and moved down where it reaches
+// past the end: no branch per lane, at whose end the loads would be waited for. (Value
+// by value 1000 tokens, 2 x 86 columns took 4 us more.)
 __device__ __forceinline__ half8_t pair_weak(const PairLayer& P, int64_t row, int c)
 {
-    typedef uint16_t u16x8 __attribute__((ext_vector_type(8), aligned(2)));  // rows of any length
+    typedef uint16_t u16x8 __attribute__((ext_vector_type(8), aligned(2)));  // any address
     const uint16_t* w = P.ww + row * P.k;
-    u16x8 v = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (c + 8 <= P.k)
-        v = *reinterpret_cast<const u16x8*>(w + c);
-    else
+    if (P.k >= 8) {  // uniform
+        uint4 u = __builtin_bit_cast(uint4, *reinterpret_cast<const u16x8*>(w + min(c, P.k - 8)));
+        if ((P.k & 7) != 0) {  // uniform
+            const uint32_t past = (uint32_t)max(c - (P.k - 8), 0), bits = 16 * (past & 1);
+            u = make_uint4(__builtin_amdgcn_alignbit(u.y, u.x, bits), __builtin_amdgcn_alignbit(u.z, u.y, bits),
+                           __builtin_amdgcn_alignbit(u.w, u.z, bits), u.w >> bits);
+            if (past & 2)
+                u = make_uint4(u.y, u.z, u.w, 0u);
+            if (past & 4)
+                u = make_uint4(u.z, u.w, 0u, 0u);
+        }
+        return __builtin_bit_cast(half8_t, c < P.k ? u : make_uint4(0u, 0u, 0u, 0u));
+    }
+    uint32_t u[8];
 #pragma unroll
-        for (int e = 0; e < 8; e++)
-            if (c + e < P.k)
-                v[e] = w[c + e];
-    return __builtin_bit_cast(half8_t, v);
+    for (int e = 0; e < 8; e++) {
+        const uint32_t one = w[min(e, P.k - 1)];
+        u[e] = c == 0 && e < P.k ? one : 0u;
+    }
+    return pair_h8(u[0] | (u[1] << 16), u[2] | (u[3] << 16), u[4] | (u[5] << 16), u[6] | (u[7] << 16));
 }
 
 // Tokens whose order is given are permuted within runs of this many, so that a run's
@@ -147,6 +161,19 @@ __device__ __forceinline__ bool pair_gemm(const PairLayer* L, const uint16_t* x,
             pair_dma(xr, stage + (wn * DPW + t) * 1024, xsrc[t] + cc * 128 + (cc == last ? xdead[t] : 0) + dead);
     };
 
+    // weak columns go in turns of 64; the lane's columns of this group's first turn are
+    // loaded ahead, and so are the row steps where the registers allow. BOTH: the two
+    // layers' turns run side by side
+    constexpr bool BOTH = FM < 4 && !ONE;
+    auto weak_column = [&](const PairLayer& P, int it) {
+        const int j = P.idx[min(it * 64 + lane, P.k - 1)];
+        return j >= 0 && j < K ? j : 0;
+    };
+    int jfirst[2];
+#pragma unroll
+    for (int l = 0; l < (BOTH ? 2 : 1); l++)
+        jfirst[l] = FM < 4 && kg * 64 < L[l].k ? weak_column(L[l], kg) : 0;
+
     // this lane's row of each set, relative to the set's first
     int row[2];
     ZeroSub zs[2];
@@ -155,6 +182,14 @@ __device__ __forceinline__ bool pair_gemm(const PairLayer* L, const uint16_t* x,
         row[l] = min(wn * 32 + l32, nv[l] - 1);
         zs[l] = make_zero_sub((uint32_t)L[ONE ? 0 : l].z[nb[l] + row[l]]);
     }
+    float sc[2];
+    auto load_scales = [&]() {
+#pragma unroll
+        for (int l = 0; l < 2; l++)
+            sc[l] = h2f(L[ONE ? 0 : l].s[nb[l] + row[l]]);
+    };
+    if constexpr (FM < 4)
+        load_scales();
     typedef u32x3 QRegs[2];
     auto load_q = [&](int c, QRegs& cw) {
         const int g = min(2 * min(c, last) + h, G - 1);
@@ -226,64 +261,119 @@ __device__ __forceinline__ bool pair_gemm(const PairLayer* L, const uint16_t* x,
     // row steps (of every K group's sums), then the weak columns, 64 at a time: x at
     // their indices is gathered once per block into a stage, laid out as a chunk of x
     // (a gather reads a cache line per value, and the row waves need the same ones),
-    // and meets w_weak as four 16-deep steps. The K groups take the 64s in turn.
+    // and meets w_weak as four 16-deep steps. The K groups take the 64s in turn. The
+    // loads of a turn are issued before any of them is waited for (2731 x 1056 at 77
+    // tokens 12.8 -> 10.8 us, 11008 x 4096 at 64 32.3 -> 29.1 against loads as they are
+    // needed, one layer after the other).
+    if constexpr (FM == 4)
+        load_scales();
 #pragma unroll
-    for (int l = 0; l < 2; l++) {
-        const float sc = h2f(L[ONE ? 0 : l].s[nb[l] + row[l]]);
+    for (int l = 0; l < 2; l++)
 #pragma unroll
         for (int i = 0; i < FM; i++)
 #pragma unroll
             for (int r = 0; r < 16; r++)
-                acc[l][i][r] *= sc;
-    }
-    char* const xw = xs0[kg];
+                acc[l][i][r] *= sc[l];
+    constexpr int TW = BM / WN, TB = FM == 4 || ONE ? 8 : TW;  // tokens of a wave; of a batch of loads
+    int tokens = 0;                                     // lane t: the row of x of this wave's token t
+    if (lane < TW)
+        tokens = token(wn + WN * lane);
+    auto gather = [&](int j, int t0, uint32_t (&v)[TB]) {
 #pragma unroll
-    for (int l = 0; l < (ONE ? 1 : 2); l++) {
-        const PairLayer& P = L[l];
-        const int passes = (P.k + 63) >> 6;
+        for (int t = 0; t < TB; t++)
+            v[t] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
+                xr, 2 * j, 2 * K * __builtin_amdgcn_readlane(tokens, t0 + t), 0);
+    };
+    auto store = [&](char* stage, bool on, int t0, const uint32_t (&v)[TB]) {
+#pragma unroll
+        for (int t = 0; t < TB; t++) {
+            const int tok = wn + WN * (t0 + t);
+            *reinterpret_cast<uint16_t*>(stage + tok * 128 + (((lane >> 3) ^ (tok & 7)) << 4) + 2 * (lane & 7)) =
+                (uint16_t)(on ? v[t] : 0u);
+        }
+    };
+    auto weights = [&](const PairLayer& P, int set, int c, half8_t (&w)[4]) {
+#pragma unroll
+        for (int st = 0; st < 4; st++)
+            w[st] = pair_weak(P, nb[set] + row[set], c + 32 * h + 8 * st);
+    };
+    auto product = [&](f32x16 (&sum)[FM], const char* stage, int st, const half8_t& w) {
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+            sum[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                __builtin_bit_cast(half8_t, *reinterpret_cast<const uint4*>(stage + arow + i * 32 * 128 + aoff[st])), w,
+                sum[i], 0, 0, 0);
+    };
+    if constexpr (BOTH) {
+        char* const stage[2] = {xs0[kg], xs1[kg]};
+        const int passes = (max(L[0].k, L[1].k) + 63) >> 6;
         for (int p0 = 0; p0 < passes; p0 += S) {  // the same trip count in every group
-            const int c = (p0 + kg) * 64;
-            __syncthreads();  // the stage is no longer read
-            if (c < P.k) {  // wave-uniform
-                const bool on = c + lane < P.k;
-                int j = P.idx[min(c + lane, P.k - 1)];
-                j = (j >= 0 && j < K) ? j : 0;
-                constexpr int TW = BM / WN, TB = TW < 8 ? TW : 8;  // tokens of a wave; loads in flight
-#pragma unroll 1
-                for (int t0 = 0; t0 < TW; t0 += TB) {
-                    uint32_t v[TB];
+            const int it = p0 + kg;
+            half8_t w[2][4];
+            uint32_t v[2][TB];
 #pragma unroll
-                    for (int t = 0; t < TB; t++)
-                        v[t] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
-                            xr, 2 * (token(wn + WN * (t0 + t)) * K + j), 0, 0);
-#pragma unroll
-                    for (int t = 0; t < TB; t++) {
-                        const int tok = wn + WN * (t0 + t);
-                        *reinterpret_cast<uint16_t*>(xw + tok * 128 + (((lane >> 3) ^ (tok & 7)) << 4) +
-                                                     2 * (lane & 7)) = (uint16_t)(on ? v[t] : 0u);
-                    }
+            for (int l = 0; l < 2; l++)
+                if (it * 64 < L[l].k) {  // wave-uniform
+                    weights(L[l], l, it * 64, w[l]);
+                    gather(p0 == 0 ? jfirst[l] : weak_column(L[l], it), 0, v[l]);
                 }
-            }
+            __syncthreads();  // the stages are no longer read
+#pragma unroll
+            for (int l = 0; l < 2; l++)
+                if (it * 64 < L[l].k)
+                    store(stage[l], it * 64 + lane < L[l].k, 0, v[l]);
             __syncthreads();
-            if (c < P.k) {
 #pragma unroll
-                for (int st = 0; st < 4; st++) {
-                    half8_t bv[2];
+            for (int l = 0; l < 2; l++)
+                if (it * 64 < L[l].k)
 #pragma unroll
-                    for (int w = 0; w < (ONE ? 2 : 1); w++)
-                        bv[w] = pair_weak(P, nb[ONE ? w : l] + row[ONE ? w : l], c + 32 * h + 8 * st);
+                    for (int st = 0; st < 4; st++)
+                        product(acc[l], stage[l], st, w[l][st]);
+        }
+    } else {
+        char* const stage = xs0[kg];
 #pragma unroll
-                    for (int i = 0; i < FM; i++) {
-                        const half8_t av =
-                            __builtin_bit_cast(half8_t, *reinterpret_cast<const uint4*>(xw + arow + i * 32 * 128 + aoff[st]));
-                        if constexpr (ONE) {
-                            acc[0][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(av, bv[0], acc[0][i], 0, 0, 0);
-                            acc[1][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(av, bv[1], acc[1][i], 0, 0, 0);
-                        } else {
-                            acc[l][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(av, bv[0], acc[l][i], 0, 0, 0);
-                        }
+        for (int l = 0; l < (ONE ? 1 : 2); l++) {
+            const PairLayer& P = L[l];
+            for (int p0 = 0; p0 * 64 < P.k; p0 += S) {
+                const int it = p0 + kg;
+                const bool mine = it * 64 < P.k;  // wave-uniform
+                const int j = FM < 4 && p0 == 0 ? jfirst[0] : (mine ? weak_column(P, it) : 0);
+                constexpr bool EARLY = FM < 4 || !ONE;  // (else the registers are full)
+                constexpr int SETS = ONE ? 2 : 1;
+                half8_t w[SETS][4];
+                uint32_t v[TB];
+                if (mine) {
+                    if constexpr (EARLY)
+#pragma unroll
+                        for (int q = 0; q < SETS; q++)
+                            weights(P, l + q, it * 64, w[q]);
+                    gather(j, 0, v);
+                }
+                __syncthreads();  // the stage is no longer read
+                if (mine) {
+                    const bool on = it * 64 + lane < P.k;
+                    store(stage, on, 0, v);
+#pragma unroll 1
+                    for (int t0 = TB; t0 < TW; t0 += TB) {
+                        gather(j, t0, v);
+                        store(stage, on, t0, v);
                     }
                 }
+                __syncthreads();
+                if (mine)
+#pragma unroll
+                    for (int st = 0; st < 4; st++) {
+                        if constexpr (!EARLY) {
+                            asm volatile("" ::: "memory");  // one step's weights at a time
+#pragma unroll
+                            for (int q = 0; q < SETS; q++)
+                                w[q][st] = pair_weak(P, nb[l + q] + row[l + q], it * 64 + 32 * h + 8 * st);
+                        }
+#pragma unroll
+                        for (int q = 0; q < SETS; q++)
+                            product(acc[l + q], stage, st, w[q][st]);
+                    }
             }
         }
     }
