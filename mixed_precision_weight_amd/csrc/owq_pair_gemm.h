@@ -411,20 +411,20 @@ __device__ __forceinline__ bool pair_gemm(const PairLayer* L, const uint16_t* x,
 
 // The tile for M tokens and `rows` rows of each set: f(FM, WN, S) as integral
 // constants. Measured for the gated block, us, N x K of each layer, as FM WN S: time
-//   11008 x 4096  M = 32  114: 27, 222: 30, 241: 39      64  222: 32, 241: 41, 114: 44
-//                    128  241: 44, 222: 45, 441: 62     256  441: 64, 241: 68, 222: 73
-//                   2048  441: 330, 241: 393, 222: 460
-//   4096 x 11008     64  114: 38, 222: 56, 241: 90      256  222: 69, 241: 92, 441: 139
-//                   1024  441: 165, 241: 194, 222: 208
-//   28672 x 8192     64  241: 89, 222: 94, 441: 122     128  441: 127, 241: 151
-//   2731 x 1056     256  222: 17, 241: 19, 114: 25      512  241: 20, 222: 24, 441: 27
-// So: the largest tile that gives about 170 blocks (two thirds of the CUs), K split
-// in two where 64 x 64 gives 128, else 32 x 32 with K split in four. (Tiles of 128 x
-// 64, 64 x 32 and 32 x 32 with K whole or in two were never the fastest by more
-// than 3 %.) The largest tile splits K in two as well while no CU gets a second block,
-// so that each SIMD still has two waves: 4096 x 11008, M = 512 140 -> 130, 640 144 ->
-// 135, 1000 165 -> 163 (344 blocks, 2048 x 4096 x 11008: 344 -> 401). For 64 x 128 that
-// came to between - 7 and + 5 %, and it stays whole.
+//   11008 x 4096  M = 32  114: 24, 222: 27, 241: 37     64  222: 29, 241: 38, 114: 40
+//                    128  241: 42, 222: 44, 442: 60     256  442: 64, 441: 67, 241: 68, 222: 71
+//                   2048  441: 336, 241: 388, 442: 399, 222: 449
+//   4096 x 11008     64  114: 35, 222: 52, 241: 83     256  222: 65, 241: 87, 114: 109
+//                    512  241: 101, 222: 114, 442: 130 640  442: 134, 441: 148, 222: 157, 241: 173
+//                   1024  441: 165, 442: 166, 241: 191
+//   28672 x 8192     64  241: 90, 222: 93, 442: 122     128  442: 133, 441: 135, 241: 144
+//   2731 x 1056     256  222: 14, 241: 16, 114: 21     512  241: 18, 222: 21, 441: 26
+// So: 64 x 128 while it gives 170 to 256 blocks, one for most CUs. Past that the CUs
+// would hold two of them, and 128 x 128 takes over: K split in two up to 256 blocks, so
+// that each SIMD still has two waves, whole above. For fewer blocks 64 x 64 with K
+// split in two where that gives 128, else 32 x 32 with K split in four. (Tiles of 128 x
+// 64, 64 x 32 and 32 x 32 with K whole or in two were never the fastest by more than
+// 3 %; 64 x 128 with K split in two came to between - 7 and + 5 %.)
 template <typename F>
 hipError_t pair_tile(int64_t M, int64_t rows, F f)
 {
@@ -432,7 +432,7 @@ hipError_t pair_tile(int64_t M, int64_t rows, F f)
     using std::integral_constant;
     if (M > 64 && blocks(128, 128) > 256)
         return f(integral_constant<int, 4>{}, integral_constant<int, 4>{}, integral_constant<int, 1>{});
-    if (M > 64 && blocks(128, 128) >= 170)
+    if (M > 64 && blocks(64, 128) > 256)
         return f(integral_constant<int, 4>{}, integral_constant<int, 4>{}, integral_constant<int, 2>{});
     if (blocks(64, 128) >= 170)
         return f(integral_constant<int, 2>{}, integral_constant<int, 4>{}, integral_constant<int, 1>{});
