@@ -26,8 +26,8 @@
 // latencies, the launch); 16 tokens of 15 requests 12; 1000 tokens of three requests
 // one after the other, rank 64, K = 11008, 28: each XCD fetches the adapters of its
 // tiles, 50 MB for 26 MB of x and A. The products above 16 tokens: see
-// owq_pair_gemm.h; 1000 tokens of 11008 -> 4096 in 112 - 128 us (800 TFLOP/s: 256
-// blocks, one wave per SIMD).
+// owq_pair_gemm.h; 1000 tokens of 11008 -> 4096 in 111 us (810 TFLOP/s: 256 blocks,
+// one wave per SIMD).
 #include "owq_adapters.h"
 #include "owq_pair_gemm.h"
 

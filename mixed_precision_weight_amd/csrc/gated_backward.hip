@@ -36,7 +36,8 @@
 //  3   73  225 MB read, 90 written: 4.3 TB/s
 //  4  366  369 GFLOP: 1.01 PFLOP/s; matrix cores and the decode that feeds them
 //  5   22  67 MB of partial sums read, 17 written: 3.8 TB/s
-// At M = 77, 2731 x 1056 each launch takes 6 - 13 us: their latencies.
+// At M = 77, 2731 x 1056 each launch takes 4 - 13 us: their latencies (launch 2 with
+// one thread per sum over all slabs took 6.4, now 3.9).
 #include "owq_act.h"
 #include "owq_decode.h"
 #include "owq_device.h"
