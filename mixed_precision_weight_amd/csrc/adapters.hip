@@ -23,7 +23,7 @@
 // 3 (11008 -> 4096) 199 -> 155; where requests follow one another it costs 2 - 3 us.
 //
 // Measured: one token of rank 16, K = 4096, 7 us (which, then x and A: two memory
-// latencies, the launch); 16 tokens of 15 requests 12; 1000 tokens of three requests
+// latencies, the launch); 16 tokens of 15 requests 8 - 9; 1000 tokens of three requests
 // one after the other, rank 64, K = 11008, 28: each XCD fetches the adapters of its
 // tiles, 50 MB for 26 MB of x and A. The products above 16 tokens: see
 // owq_pair_gemm.h; 1000 tokens of 11008 -> 4096 in 111 us (810 TFLOP/s: 256 blocks,
@@ -168,11 +168,13 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void k_adapter_shrink(const uint
             continue;
         const __amdgpu_buffer_rsrc_t ar = shrink_rsrc(A + (int64_t)a * rank * K, (int64_t)rank * K);
         float4_t acc[2] = {float4_t{0.0f, 0.0f, 0.0f, 0.0f}, float4_t{0.0f, 0.0f, 0.0f, 0.0f}};
-        // steps past the wave's end are read out of range: zeros, nothing fetched
+        // steps past the wave's end, and the tokens of other adapters, are read out of
+        // range: zeros, nothing fetched (16 tokens of 15 requests: 11 -> 8.5 us)
+        const int xa = id == a ? xo : 0x40000000;
         half8_t xv[kShrinkFlight], av[kShrinkFlight];
         auto load = [&](int s, int u) {
             const int o = s + u < s1 ? (s + u) * 64 : 0x40000000;
-            xv[u] = __builtin_bit_cast(half8_t, __builtin_amdgcn_raw_buffer_load_b128(xr, xo + o, 0, 0));
+            xv[u] = __builtin_bit_cast(half8_t, __builtin_amdgcn_raw_buffer_load_b128(xr, xa + o, 0, 0));
             av[u] = __builtin_bit_cast(half8_t, __builtin_amdgcn_raw_buffer_load_b128(ar, ao + o, 0, 0));
         };
         auto product = [&](int u) {
