@@ -180,3 +180,33 @@ def test_nothing_is_written_behind_the_ends(owq, M):
     torch.cuda.synchronize()
     for i, (buf, n) in enumerate(buffers):
         assert int((buf[:guard] != 0xa5).sum()) == 0 and int((buf[guard + n:] != 0xa5).sum()) == 0, i
+
+
+@pytest.mark.parametrize("M", [1, 3, 20, 100])
+def test_arrays_at_any_element(owq, M):
+    """Scales, weak weights, upstream gradients and outputs that start at an odd element give the same bits."""
+    import torch
+    N, K, count, rank = 96, 160, 3, 8
+    rng = np.random.default_rng(M)
+    gate, up = _layer(owq, rng, N, K, 9), _layer(owq, rng, N, K, 16)
+    _, ads = _adapters(rng, count, rank, N, K)
+    x = dev(rng.standard_normal((M, K)).astype(np.float16))
+    dh = dev(rng.standard_normal((M, N)).astype(np.float16))
+    which = dev(rng.integers(-1, count, M).astype(np.int32))
+
+    def shifted(t):
+        buf = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+        buf[1:].copy_(t.reshape(-1))
+        return buf[1:].view(t.shape)
+
+    def run(gate, up, dh, h, y):
+        owq.gated(gate, up, x, h=h)
+        owq.linear_adapters(gate, ads, which, x, y=y)
+        _, g, u = owq.gated(gate, up, x, save=True)
+        return [host(t).tobytes() for t in (h, y) + tuple(owq.gated_backward(gate, up, x, g, u, dh))]
+
+    out = torch.zeros((M, N), dtype=torch.float16, device="cuda:0")
+    want = run(gate, up, dh, out, out.clone())
+    moved = [{n: shifted(t) if t.dtype == torch.float16 else t for n, t in layer.items()} for layer in (gate, up)]
+    assert moved[0]["scales"].data_ptr() % 4 == 2
+    assert run(*moved, shifted(dh), shifted(out), shifted(out)) == want
