@@ -530,14 +530,18 @@ __global__ __launch_bounds__(64 * WN * S) __attribute__((amdgpu_waves_per_eu(2, 
     if (!pair_gemm<FM, WN, S, false>(a.L, a.x, nullptr, M, N, a.K, m0, rows, acc))
         return;
     const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
-    const int n = n0 + (__builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) % WN) * 32 + l32;
-    // D element r of lane l: token 8 (r / 4) + 4 h + r % 4, row l % 32
+    const int wid = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), kg = wid / WN;
+    const int n = n0 + wid % WN * 32 + l32;
+    // D element r of lane l: token 8 (r / 4) + 4 h + r % 4, row l % 32; of these the
+    // waves hold their K group's share
+    constexpr int REGS = S > 1 && T::SHARE == 1 ? 4 : 16;
+    const int mt = m0 + 4 * h + kg * (REGS == 4 ? 8 : T::SHARE > 1 ? 32 * T::OWN : 0);
     with_act(a.act, [&](auto act) {
 #pragma unroll
-        for (int i = 0; i < FM; i++)
+        for (int i = 0; i < T::OWN; i++)
 #pragma unroll
-            for (int r = 0; r < 16; r++) {
-                const int m = m0 + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
+            for (int r = 0; r < REGS; r++) {
+                const int m = mt + 32 * i + 8 * (r >> 2) + (r & 3);
                 if (m < M && n < N) {
                     const int64_t o = (int64_t)m * N + n;
                     const float gv = acc[0][i][r], uv = acc[1][i][r];
