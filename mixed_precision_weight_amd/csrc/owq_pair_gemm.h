@@ -345,7 +345,7 @@ __device__ __forceinline__ bool pair_gemm(const PairLayer* L, const uint16_t* x,
                 const int it = p0 + kg;
                 const bool mine = it * 64 < P.k;  // wave-uniform
                 const int j = FM < 4 && p0 == 0 ? jfirst[0] : (mine ? weak_column(P, it) : 0);
-                constexpr bool EARLY = FM < 4 || !ONE;  // (else the registers are full)
+                constexpr bool EARLY = FM < 4;  // (128 tokens fill the registers: 344 us at 2048, else 340)
                 constexpr int SETS = ONE ? 2 : 1;
                 half8_t w[SETS][4];
                 uint32_t v[TB];
