@@ -6,6 +6,8 @@
 //   gelu_tanh  v s(2 c (v + 0.044715 v^3)),  c = sqrt(2 / pi): the tanh form,
 //              (1 + tanh t) / 2 = s(2 t)
 //   relu       max(v, 0)
+// All four keep a NaN (relu compares: the hardware's maximum of NaN and 0 is 0), in the
+// value and in the slope, so that a step that diverged shows in its gradients.
 // The logistic function uses the hardware's 2^v and reciprocal (one ulp each): its
 // relative error is |v| 2^-24 from the rounded exponent plus 2^-22, as large as the
 // change of s(v) from the fp32 rounding of v itself; an accurate exp and an IEEE
@@ -78,7 +80,7 @@ __device__ __forceinline__ float act_value(float v)
     } else if constexpr (ACT == kActGeluTanh)
         return v * sigmoid(kTwoC * (v + kCube * v * v * v));
     else
-        return fmaxf(v, 0.0f);
+        return v <= 0.0f ? 0.0f : v;
 }
 
 // value and slope at v
@@ -99,8 +101,8 @@ __device__ __forceinline__ void act_both(float v, float& a, float& d)
         a = v * p;
         d = p + v * (p * (1.0f - p)) * (kTwoC * (1.0f + 3.0f * kCube * v * v));
     } else {
-        a = fmaxf(v, 0.0f);
-        d = v > 0.0f ? 1.0f : 0.0f;
+        a = v <= 0.0f ? 0.0f : v;
+        d = v > 0.0f ? 1.0f : a;
     }
 }
 
