@@ -12,8 +12,10 @@
 // codes) and A = 2^e_m s_i da[m][i], rounded to fp16 with a power of two per token
 // that puts the token's largest |s da|, |s db| into [2^14, 2^15): 11 bits of every
 // term that matters, whatever the gradient's scale, and no overflow. (The rounding
-// is the one a caller who stored da as fp16 would make, without its range. Split
-// into two fp16 values it would double the matrix work for an fp16 result.) The
+// is the one a caller who stored da as fp16 would make, without its range, and as
+// large as the one of dx itself: 2.1e-4 of dx in the root mean square each, 2.9e-4
+// together. With A in two fp16 values, 22 bits, the whole backward took 850 us in
+// place of 500 at M = 2048, 2 x 11008 x 4096, 62 in place of 48 at M = 1.) The
 // weak columns' part, da w_weak, is a product over the rows in fp32, and so is dw,
 // over the tokens (v_mfma_f32_32x32x2_f32): their results are not limited by fp16.
 //
