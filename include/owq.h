@@ -497,7 +497,8 @@ typedef enum {
  * fp16 once. gate, up: HOST pointers to packed layers of the same N and K (their
  * weak columns may differ); x: fp16 [M][K]; h: fp16 [M][N] (output); g, u: fp32
  * [M][N] outputs for owq_gated_backward, both or neither NULL. act: an
- * owq_activation. M, N <= 2^30. Errors as owq_linear, plus OWQ_ERR_SHAPE for layers
+ * owq_activation. M, N <= 2^30 and M N <= 2^36; N <= 2^26 for M <= 2, 2^29 for M <= 16
+ * (OWQ_ERR_SHAPE where the launch would count 2^32 threads). Errors as owq_linear, plus OWQ_ERR_SHAPE for layers
  * that do not match, OWQ_ERR_UNSUPPORTED for an unknown act, OWQ_ERR_NULL for one of g, u. */
 owq_status owq_gated(const owq_layer* gate, const owq_layer* up, const uint16_t* x, int64_t M, int32_t act,
                      uint16_t* h, float* g, float* u, void* stream);
@@ -521,8 +522,9 @@ size_t owq_gated_backward_workspace_bytes(int64_t N, int64_t K, int32_t k_gate, 
  * below 2^-28 of the token's largest; no term overflows), the products with q - z
  * are exact and the sums fp32; relu's slope at 0 is 0. Bitwise deterministic.
  * workspace: >= owq_gated_backward_workspace_bytes(...) bytes, 256-byte aligned,
- * contents ignored; calls sharing it must be ordered. M, N <= 2^20. Errors as
- * owq_gated, plus OWQ_ERR_WORKSPACE. */
+ * contents ignored; calls sharing it must be ordered. M, N <= 2^20 and M (k gate + k up)
+ * <= 2^29 (OWQ_ERR_SHAPE where a launch would count 2^32 threads). Errors as owq_gated,
+ * plus OWQ_ERR_WORKSPACE. */
 owq_status owq_gated_backward(const owq_layer* gate, const owq_layer* up, const uint16_t* x, const float* g,
                               const float* u, const uint16_t* dh, int64_t M, int32_t act, uint16_t* dx,
                               float* dw_gate, float* dw_up, void* workspace, size_t workspace_bytes,
@@ -556,8 +558,10 @@ size_t owq_linear_adapters_workspace_bytes(int32_t rank, int64_t M);
  * are not finite. Two launches: the low-rank products; the linear with the second
  * products in its epilogue. workspace: >=
  * owq_linear_adapters_workspace_bytes(rank, M) bytes, 256-byte aligned, contents
- * ignored; calls sharing it must be ordered. M, N <= 2^30. Other arguments and errors
- * as owq_linear, plus OWQ_ERR_WORKSPACE, and OWQ_ERR_SHAPE for count and rank. */
+ * ignored; calls sharing it must be ordered. M, N <= 2^30, M N <= 2^36 and M ceil(rank / 16)
+ * <= 2^24; N <= 2^27 for M <= 16 (OWQ_ERR_SHAPE, and workspace bytes 0, where a launch
+ * would count 2^32 threads). Other arguments and errors as owq_linear, plus
+ * OWQ_ERR_WORKSPACE, and OWQ_ERR_SHAPE for count and rank. */
 owq_status owq_linear_adapters(const owq_layer* L, const owq_adapters* ad, const int32_t* which,
                                const uint16_t* x, int64_t M, uint16_t* y, void* workspace,
                                size_t workspace_bytes, void* stream);

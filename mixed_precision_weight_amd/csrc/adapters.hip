@@ -28,6 +28,8 @@
 // tiles, 50 MB for 26 MB of x and A. The products above 16 tokens: see
 // owq_pair_gemm.h; 1000 tokens of 11008 -> 4096 in 111 us (810 TFLOP/s: 256 blocks,
 // one wave per SIMD).
+#include <algorithm>
+
 #include "owq_adapters.h"
 #include "owq_pair_gemm.h"
 
@@ -375,35 +377,59 @@ size_t adapter_workspace_bytes(int rank, int64_t M)
     return (size_t)M * (adapter_rpad(rank) * sizeof(float) + sizeof(int32_t));
 }
 
+namespace {
+
+// blocks per tile that share its distinct adapters: the 16 of a decode step's tile
+// side by side; grouped tiles hold one mostly, and the few that hold two would run
+// on alone after the others (1000 tokens, rank 64: 43 us with one slot, 27 with two)
+int64_t shrink_slots(int rank, int64_t M)
+{
+    const int64_t slots = 512 / ((M + 15) / 16 * ((rank + 15) / 16));
+    return std::min(M, std::clamp<int64_t>(slots, 2, 16));
+}
+
+int64_t shrink_blocks(int rank, int64_t M)
+{
+    const int tiles = (int)((M + 15) / 16);
+    return (shrink_round(tiles) * shrink_slots(rank, M) + 7) / 8 * 8 * ((rank + 15) / 16);
+}
+
+// f(tile as integral constants, blocks) for launch_adapter_gemm's choice of tile
+template <typename F>
+hipError_t adapter_gemm_tile(int64_t M, int64_t N, F f)
+{
+    return pair_tile(M, (N + 1) / 2, [&](auto fm, auto wn, auto sk) {
+        using T = PairTile<decltype(fm)::value, decltype(wn)::value, decltype(sk)::value>;
+        const int64_t nb = (M + T::BM - 1) / T::BM * ((N + 2 * T::BN - 1) / (2 * T::BN));
+        return grid_fits(nb, T::NT) ? f(fm, wn, sk, nb) : hipErrorInvalidConfiguration;
+    });
+}
+
+}  // namespace
+
+bool adapter_shrink_grid_fits(int rank, int64_t M) { return grid_fits(shrink_blocks(rank, M), 64 * kShrinkWaves); }
+
+bool adapter_gemm_grid_fits(int64_t M, int64_t N)
+{
+    return adapter_gemm_tile(M, N, [](auto, auto, auto, int64_t) { return hipSuccess; }) == hipSuccess;
+}
+
 hipError_t launch_adapter_shrink(const AdapterDesc& a, const uint16_t* x, int64_t M, int64_t K, hipStream_t s)
 {
-    const int rpad = adapter_rpad(a.rank);
-    const int64_t tiles = (M + 15) / 16;
-    const int rt = (a.rank + 15) / 16;
-    // blocks per tile that share its distinct adapters: the 16 of a decode step's tile
-    // side by side; grouped tiles hold one mostly, and the few that hold two would run
-    // on alone after the others (1000 tokens, rank 64: 43 us with one slot, 27 with two)
-    int64_t slots = 512 / (tiles * rt);
-    slots = slots < 2 ? 2 : (slots > 16 ? 16 : slots);
-    if (slots > M)
-        slots = M;
-    const int64_t nb = ((int64_t)shrink_round((int)tiles) * slots + 7) / 8 * 8 * rt;
-    if (nb > INT32_MAX)
-        return hipErrorInvalidValue;
-    hipLaunchKernelGGL(k_adapter_shrink, dim3((unsigned)nb), dim3(64 * kShrinkWaves), 0, s, x, a.A, a.which, a.t, a.order,
-                       (int)M, (int)K, a.count, a.rank, rpad, (int)slots);
+    if (!adapter_shrink_grid_fits(a.rank, M))
+        return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL(k_adapter_shrink, dim3((unsigned)shrink_blocks(a.rank, M)), dim3(64 * kShrinkWaves), 0, s, x, a.A,
+                       a.which, a.t, a.order, (int)M, (int)K, a.count, a.rank, adapter_rpad(a.rank),
+                       (int)shrink_slots(a.rank, M));
     return hipGetLastError();
 }
 
 hipError_t launch_adapter_gemm(const LinearDesc& d, const AdapterDesc& ad, int64_t M, hipStream_t s)
 {
     AdapterGemmArgs a{pair_layer(d), d.x, d.y, (int32_t)M, (int32_t)d.N, (int32_t)d.K, 1};
-    return pair_tile(M, (d.N + 1) / 2, [&](auto fm, auto wn, auto sk) {
+    return adapter_gemm_tile(M, d.N, [&](auto fm, auto wn, auto sk, int64_t nb) {
         using T = PairTile<decltype(fm)::value, decltype(wn)::value, decltype(sk)::value>;
         a.mblocks = (int32_t)((M + T::BM - 1) / T::BM);
-        const int64_t nb = (int64_t)a.mblocks * ((d.N + 2 * T::BN - 1) / (2 * T::BN));
-        if (nb > INT32_MAX)
-            return hipErrorInvalidValue;
         hipLaunchKernelGGL((k_adapter_gemm<decltype(fm)::value, decltype(wn)::value, decltype(sk)::value>),
                            dim3((unsigned)nb), dim3(T::NT), 0, s, a, adapter_args(ad));
         return hipGetLastError();

@@ -46,6 +46,14 @@ owq_status hip_status(hipError_t e, const char* what)
     return fail(OWQ_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
+// Of a launcher that checks its grids before it launches anything
+owq_status launch_status(hipError_t e, const char* what)
+{
+    if (e == hipErrorInvalidConfiguration)
+        return fail(OWQ_ERR_SHAPE, "%s: these sizes need more threads than one launch counts (2^32)", what);
+    return hip_status(e, what);
+}
+
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 constexpr int64_t kMaxK = 65536;
@@ -835,9 +843,9 @@ owq_status owq_gated(const owq_layer* gate, const owq_layer* up, const uint16_t*
         return fail(OWQ_ERR_NULL, "g and u must be given together");
     if (!aligned(g, 4) || !aligned(u, 4))
         return fail(OWQ_ERR_ALIGN, "misaligned pointer (g, u: 4 B)");
-    return hip_status(owq::launch_gated(desc_of(gate, x, nullptr), desc_of(up, x, nullptr), M, act, h, g, u,
-                                        (hipStream_t)stream),
-                      "owq_gated launch");
+    return launch_status(owq::launch_gated(desc_of(gate, x, nullptr), desc_of(up, x, nullptr), M, act, h, g, u,
+                                           (hipStream_t)stream),
+                         "owq_gated launch");
 }
 
 size_t owq_gated_backward_workspace_bytes(int64_t N, int64_t K, int32_t k_gate, int32_t k_up, int64_t M)
@@ -874,14 +882,14 @@ owq_status owq_gated_backward(const owq_layer* gate, const owq_layer* up, const 
         g_err[0] = '\0';
         return OWQ_OK;
     }
-    return hip_status(owq::launch_gated_backward(desc_of(gate, x, nullptr), desc_of(up, x, nullptr), M, act, g, u, dh,
-                                                 dx, dw_gate, dw_up, workspace, (hipStream_t)stream),
-                      "owq_gated_backward launch");
+    return launch_status(owq::launch_gated_backward(desc_of(gate, x, nullptr), desc_of(up, x, nullptr), M, act, g, u,
+                                                    dh, dx, dw_gate, dw_up, workspace, (hipStream_t)stream),
+                         "owq_gated_backward launch");
 }
 
 size_t owq_linear_adapters_workspace_bytes(int32_t rank, int64_t M)
 {
-    if (rank < 1 || rank > kMaxRank || M < 1 || M > kMaxBlock)
+    if (rank < 1 || rank > kMaxRank || M < 1 || M > kMaxBlock || !owq::adapter_shrink_grid_fits(rank, M))
         return 0;
     return owq::adapter_workspace_bytes(rank, M);
 }
@@ -900,6 +908,10 @@ owq_status owq_linear_adapters(const owq_layer* L, const owq_adapters* ad, const
         return fail(OWQ_ERR_SHAPE, "rank = %d: need 1 <= rank <= %d", ad->rank, kMaxRank);
     if (ad->count < 1)
         return fail(OWQ_ERR_SHAPE, "count = %d: need at least one adapter", ad->count);
+    const bool gemm = M > owq::kMfvMaxM, mat = !gemm && owq::decode_on_matrix_cores(M);
+    if (!owq::adapter_shrink_grid_fits(ad->rank, M) ||
+        !(gemm ? owq::adapter_gemm_grid_fits(M, L->N) : mat ? owq::mfv_grid_fits(M, L->N) : owq::gemv_grid_fits(L->N)))
+        return launch_status(hipErrorInvalidConfiguration, "owq_linear_adapters launch");
     if (!aligned(ad->A, 16) || !aligned(ad->B, 16) || !aligned(ad->alpha, 4) || !aligned(which, 4) ||
         !aligned(workspace, 256))
         return fail(OWQ_ERR_ALIGN, "misaligned pointer (A, B: 16 B, alpha, which: 4 B, workspace: 256 B)");
@@ -916,14 +928,14 @@ owq_status owq_linear_adapters(const owq_layer* L, const owq_adapters* ad, const
     if (e == hipSuccess)
     {
         const owq::LinearDesc d = desc_of(L, x, y);
-        if (M > owq::kMfvMaxM)
+        if (gemm)
             e = owq::launch_adapter_gemm(d, a, M, (hipStream_t)stream);
-        else if (owq::decode_on_matrix_cores(M))
+        else if (mat)
             e = owq::launch_mfv(&d, 1, (int)M, (hipStream_t)stream, &a);
         else
             e = owq::launch_gemv(&d, 1, (int)M, (hipStream_t)stream, &a);
     }
-    return hip_status(e, "owq_linear_adapters launch");
+    return launch_status(e, "owq_linear_adapters launch");
 }
 
 size_t owq_clip_grad_norm_workspace_bytes(int32_t count)
@@ -981,8 +993,8 @@ owq_status owq_clip_grad_norm(const owq_grad* items, int32_t count, double max_n
             if (hit && !(g.out == g.g && (o - 1)->first == b))
                 return fail(OWQ_ERR_RANGE, "item %d: g overlaps an output that is not its own", i);
         }
-        return hip_status(owq::launch_clip(it.data(), count, max_norm, norm, workspace, (hipStream_t)stream),
-                          "owq_clip_grad_norm launch");
+        return launch_status(owq::launch_clip(it.data(), count, max_norm, norm, workspace, (hipStream_t)stream),
+                             "owq_clip_grad_norm launch");
     } catch (const std::exception& ex) {
         return fail(OWQ_ERR_HIP, "owq_clip_grad_norm: host memory: %s", ex.what());
     }

@@ -335,7 +335,7 @@ hipError_t launch_clip(const ClipEntry* items, int count, double max_norm, float
     };
     for (int i0 = 0; i0 < count; i0 += kClipItems)
         if (chunks(i0) > INT32_MAX)
-            return hipErrorInvalidValue;
+            return hipErrorInvalidConfiguration;
     int nparts = 0;
     for (int i0 = 0; i0 < count; i0 += kClipItems) {
         ClipArgs a{};

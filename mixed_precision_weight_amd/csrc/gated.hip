@@ -559,6 +559,8 @@ template <int M, bool MMA, int RP>
 hipError_t gated_gemv(const GatedArgs& a, hipStream_t s)
 {
     const int nblocks = (a.N + 4 * RP - 1) / (4 * RP);
+    if (!grid_fits(nblocks, 256))
+        return hipErrorInvalidConfiguration;
     const size_t lds = (size_t)M * kChunkTiles * 4 * kQuadStride * 16;
     hipLaunchKernelGGL((k_gated_gemv<M, MMA, RP>), dim3(nblocks), dim3(256), lds, s, a);
     return hipGetLastError();
@@ -567,7 +569,10 @@ hipError_t gated_gemv(const GatedArgs& a, hipStream_t s)
 template <int U, int MC, int W, int S, int D>
 hipError_t gated_mfv(const GatedArgs& a, hipStream_t s)
 {
-    hipLaunchKernelGGL((k_gated_mfv<U, MC, W, S, D>), dim3((a.N + 16 * W - 1) / (16 * W)), dim3(64 * W * S), 0, s, a);
+    const int nblocks = (a.N + 16 * W - 1) / (16 * W);
+    if (!grid_fits(nblocks, 64 * W * S))
+        return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((k_gated_mfv<U, MC, W, S, D>), dim3(nblocks), dim3(64 * W * S), 0, s, a);
     return hipGetLastError();
 }
 
@@ -577,8 +582,8 @@ hipError_t gated_gemm(GatedArgs a, hipStream_t s)
     using T = PairTile<FM, WN, S>;
     a.mblocks = (int)(((int64_t)a.M + T::BM - 1) / T::BM);
     const int64_t nblocks = (int64_t)a.mblocks * (((int64_t)a.N + T::BN - 1) / T::BN);
-    if (nblocks > INT32_MAX)
-        return hipErrorInvalidValue;
+    if (!grid_fits(nblocks, T::NT))
+        return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((k_gated_gemm<FM, WN, S>), dim3((unsigned)nblocks), dim3(T::NT), 0, s, a);
     return hipGetLastError();
 }

@@ -845,14 +845,11 @@ GatedBwdPlan gated_bwd_plan(int64_t N, int64_t K, int64_t kt, int64_t M)
 }
 
 template <int FM, int FN, int WM, int WN, int RS>
-hipError_t launch_dx(GatedBwdArgs& a, hipStream_t s)
+hipError_t launch_dx(const GatedBwdArgs& a, int64_t blocks, hipStream_t s)
 {
     using T = DxTile<FM, FN, WM, WN, RS>;
-    a.mtiles = (int)cdiv(a.M, T::BM);
-    const int64_t nb = (int64_t)a.mtiles * cdiv(a.K, T::BN) * a.split;
-    if (nb > INT32_MAX)
-        return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_gated_dx<FM, FN, WM, WN, RS>), dim3((unsigned)nb), dim3(T::NT), 0, s, a);
+    static_assert(T::NT == 256, "the threads per block that the grids are checked with");
+    hipLaunchKernelGGL((k_gated_dx<FM, FN, WM, WN, RS>), dim3((unsigned)blocks), dim3(T::NT), 0, s, a);
     return hipGetLastError();
 }
 
@@ -899,7 +896,19 @@ hipError_t launch_gated_backward(const LinearDesc& gate, const LinearDesc& up, i
                                       reinterpret_cast<uintptr_t>(up.s)) & 3) == 0;
     a.work_blocks = dx ? (int32_t)cdiv(cdiv(M, 32) * p.slabs, 4) : 0;
     a.map_blocks = dx ? (int32_t)cdiv(K, 256) : 0;
+    // every launch's blocks (256 threads each), checked before the first
+    const DxShape tile = dx_shape(M);
+    a.mtiles = (int)cdiv(M, tile.bm);
     const int64_t first = a.work_blocks + a.map_blocks + (any_dw ? cdiv(M * kt, 256) : 0);
+    const int64_t sums = cdiv(M, 4) + cdiv(M * kt, 64);
+    const int64_t rows = p.Np / 64 * p.tslabs;
+    const int64_t product = a.mtiles * cdiv(K, tile.bn) * p.split;
+    const int64_t fin = dx && p.split > 1 ? cdiv(M * K, 1024) : 0;
+    const int64_t bg = dw[0] && p.tslabs > 1 ? cdiv(N * gate.k, 256) : 0;
+    const int64_t bu = dw[1] && p.tslabs > 1 ? cdiv(N * up.k, 256) : 0;
+    for (const int64_t blocks : {first, dx ? sums : 1, rows, dx ? product : 1, fin + bg + bu + 1})
+        if (!grid_fits(blocks, 256))
+            return hipErrorInvalidConfiguration;
     {
         const dim3 grid((unsigned)first, wtiles);
         for_act(act, [&](auto c) {
@@ -911,10 +920,10 @@ hipError_t launch_gated_backward(const LinearDesc& gate, const LinearDesc& up, i
     }
     if (dx) {
         a.work_blocks = (int32_t)cdiv(M, 4);
-        hipLaunchKernelGGL(k_gated_sums, dim3((unsigned)(a.work_blocks + cdiv(M * kt, 64))), dim3(256), 0, s, a);
+        hipLaunchKernelGGL(k_gated_sums, dim3((unsigned)sums), dim3(256), 0, s, a);
     }
     {
-        const dim3 grid((unsigned)(p.Np / 64 * p.tslabs), any_dw ? wtiles : 1u);
+        const dim3 grid((unsigned)rows, any_dw ? wtiles : 1u);
         for_act(act, [&](auto c) {
             if (even)
                 hipLaunchKernelGGL((k_gated_rows<decltype(c)::value, true>), grid, dim3(256), 0, s, a);
@@ -925,19 +934,17 @@ hipError_t launch_gated_backward(const LinearDesc& gate, const LinearDesc& up, i
     hipError_t e = hipGetLastError();
     if (dx && e == hipSuccess) {
         if (M <= 32)
-            e = launch_dx<1, 1, 1, 4, 64>(a, s);
+            e = launch_dx<1, 1, 1, 4, 64>(a, product, s);
         else if (M <= 64)
-            e = launch_dx<2, 1, 1, 4, 64>(a, s);
+            e = launch_dx<2, 1, 1, 4, 64>(a, product, s);
         else
-            e = launch_dx<2, 4, 2, 2, 32>(a, s);
+            e = launch_dx<2, 4, 2, 2, 32>(a, product, s);
     }
     if (e != hipSuccess)
         return e;
-    a.work_blocks = dx && p.split > 1 ? (int32_t)cdiv(M * K, 1024) : 0;
-    const int64_t bg = dw[0] && p.tslabs > 1 ? cdiv(N * gate.k, 256) : 0;
-    const int64_t bu = dw[1] && p.tslabs > 1 ? cdiv(N * up.k, 256) : 0;
-    if (a.work_blocks + bg + bu > 0)
-        hipLaunchKernelGGL(k_gated_fin, dim3((unsigned)(a.work_blocks + bg + bu)), dim3(256), 0, s, a, (int)bg);
+    a.work_blocks = (int32_t)fin;
+    if (fin + bg + bu > 0)
+        hipLaunchKernelGGL(k_gated_fin, dim3((unsigned)(fin + bg + bu)), dim3(256), 0, s, a, (int)bg);
     return hipGetLastError();
 }
 

@@ -486,6 +486,9 @@ bool gemv_fits(int64_t M, int64_t K)
     return M >= 1 && M <= kGemvMaxM;
 }
 
+// (launches of two rows per wave have at most kSmallLaunchBlocks * 3 / 2 blocks)
+bool gemv_grid_fits(int64_t N) { return grid_fits((N + 4 * kRowsPerWave - 1) / (4 * kRowsPerWave), 256); }
+
 namespace {
 
 // The launch arguments of a batch (layers with the longest rows first: their

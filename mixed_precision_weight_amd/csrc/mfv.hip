@@ -416,6 +416,15 @@ bool mfv_fits(int64_t M, int64_t K)
     return M >= 1 && M <= kMfvMaxM && M * K * 2 <= INT32_MAX;
 }
 
+namespace {
+// Row waves per block: up to 4 tokens blocks of 2 row waves x 2 K groups (the 4096 x
+// 11008 blocks then finish with the rest); more tokens: 4 row waves over the whole
+// row (the 8- and 16-token x stages leave LDS for no second K group)
+constexpr int row_waves(int64_t M) { return M <= 4 ? 2 : 4; }
+}  // namespace
+
+bool mfv_grid_fits(int64_t M, int64_t N) { return grid_fits((N + 16 * row_waves(M) - 1) / (16 * row_waves(M)), 256); }
+
 hipError_t launch_mfv(const LinearDesc* d, int count, int M, hipStream_t s, const AdapterDesc* ad)
 {
     // layers with the longest rows first: their blocks run longest
@@ -428,10 +437,7 @@ hipError_t launch_mfv(const LinearDesc* d, int count, int M, hipStream_t s, cons
             order[c] = order[c - 1];
             order[c - 1] = t;
         }
-    // up to 4 tokens: blocks of 2 row waves x 2 K groups (the 4096 x 11008
-    // blocks then finish with the rest); more tokens: 4 row waves over the whole
-    // row (the 8- and 16-token x stages leave LDS for no second K group)
-    const int W = M <= 4 ? 2 : 4;
+    const int W = row_waves(M);
     MfvBatch b{};
     int nblocks = 0;
     for (int o = 0; o < count; o++) {

@@ -72,6 +72,11 @@ hipError_t launch_pack_given(const uint16_t* W, int64_t N, int64_t K, const int3
 hipError_t launch_search(const uint16_t* W, int64_t N, int64_t K, const int32_t* idx, int32_t k,
                          const double* lambda, uint16_t* scales, uint8_t* zeros, hipStream_t s);
 
+// HIP counts a grid's threads per dimension in 32 bits. The launchers of the block
+// operators return hipErrorInvalidConfiguration where a grid holds more, before
+// anything is launched; the C entries report it as OWQ_ERR_SHAPE.
+constexpr bool grid_fits(int64_t blocks, int threads) { return blocks >= 1 && blocks * threads < (int64_t)1 << 32; }
+
 // ------------------------------------------------------------------- linear --
 struct LinearDesc {
     const uint32_t* q;
@@ -102,6 +107,7 @@ hipError_t launch_gemv(const LinearDesc* d, int count, int M, hipStream_t s, con
 // Tokens per GEMV launch for a layer of K columns (x of all tokens is staged in LDS).
 int gemv_max_tokens(int64_t K);
 bool gemv_fits(int64_t M, int64_t K);
+bool gemv_grid_fits(int64_t N);  // one layer of N rows
 // Products of the vector-ALU decode for M tokens: true = one v_mfma_f32_16x16x32_f16
 // per token and 8 columns (M <= 2), false = v_dot2 per column pair.
 // OWQ_GEMV_PRODUCTS=dot2|mfma overrides (read per call).
@@ -110,6 +116,7 @@ bool gemv_products_on_matrix_cores(int64_t M);
 constexpr int kMfvMaxM = 16;
 hipError_t launch_mfv(const LinearDesc* d, int count, int M, hipStream_t s, const AdapterDesc* ad = nullptr);
 bool mfv_fits(int64_t M, int64_t K);
+bool mfv_grid_fits(int64_t M, int64_t N);  // one layer of N rows
 // Decode kernel choice for M tokens: true = matrix-core decode (launch_mfv), false =
 // vector-ALU decode (launch_gemv). OWQ_DECODE=vector|matrix overrides (read per call).
 bool decode_on_matrix_cores(int64_t M);
@@ -141,6 +148,9 @@ struct AdapterDesc {
 };
 constexpr int adapter_rpad(int rank) { return (rank + 31) & ~31; }
 size_t adapter_workspace_bytes(int rank, int64_t M);  // t, then order
+// Whether both launches of the operator count their threads in 32 bits.
+bool adapter_shrink_grid_fits(int rank, int64_t M);
+bool adapter_gemm_grid_fits(int64_t M, int64_t N);
 hipError_t launch_adapter_shrink(const AdapterDesc& a, const uint16_t* x, int64_t M, int64_t K, hipStream_t s);
 // The shared product with the adapters' second products: up to 16 tokens
 // launch_gemv / launch_mfv with the adapters given, above this.

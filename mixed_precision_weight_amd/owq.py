@@ -1083,7 +1083,7 @@ def gated_backward(gate: dict, up: dict, x: torch.Tensor | None, g: torch.Tensor
         dw_gate = run.empty((N, Lg.k), torch.float32) if want_dw else None
         dw_up = run.empty((N, Lu.k), torch.float32) if want_dw else None
         if workspace is None:
-            workspace = run.empty(gated_backward_workspace_bytes(N, K, Lg.k, Lu.k, M), torch.uint8)
+            workspace = run.empty(max(gated_backward_workspace_bytes(N, K, Lg.k, Lu.k, M), 256), torch.uint8)
         _check(lib().owq_gated_backward(ctypes.byref(Lg), ctypes.byref(Lu), _ptr(x), g.data_ptr(), u.data_ptr(),
                                         dh.data_ptr(), M, code, _ptr(dx), _ptr(dw_gate) if Lg.k else None,
                                         _ptr(dw_up) if Lu.k else None, workspace.data_ptr(), workspace.numel(),
@@ -1131,7 +1131,7 @@ def linear_adapters(layer: dict, adapters: dict, which: torch.Tensor, x: torch.T
         if y is None:
             y = run.empty((M, N), torch.float16)
         if workspace is None:
-            workspace = run.empty(linear_adapters_workspace_bytes(rank, M), torch.uint8)
+            workspace = run.empty(max(linear_adapters_workspace_bytes(rank, M), 256), torch.uint8)
         ad = OwqAdapters(A.data_ptr(), B.data_ptr(), alpha.data_ptr(), count, rank)
         _check(lib().owq_linear_adapters(ctypes.byref(L), ctypes.byref(ad), which.data_ptr(), x.data_ptr(), M,
                                          y.data_ptr(), workspace.data_ptr(), workspace.numel(), run.handle),
