@@ -587,9 +587,11 @@ size_t owq_clip_grad_norm_workspace_bytes(int32_t count);
  *   norm   = sqrt(sum over every tensor and element of g^2)   fp64 sums
  *   out    = g * (max_norm / norm) if norm > max_norm, else g  fp64 product,
  *            rounded to the tensor's type (nearest-even; fp16 by way of fp32)
- * norm is written as fp32 [1] (infinity above its range); the comparison and the
- * factor use the fp64 value. If it is not finite (an infinity or NaN among the
- * gradients) nothing is scaled: the caller sees it and drops the step. max_norm:
+ * norm is written as fp32 [1]; the comparison and the factor use the fp64 value. With
+ * an infinity or NaN among the gradients the fp64 value is infinite or NaN and nothing
+ * is scaled: the caller sees it in norm and drops the step. Finite gradients whose norm
+ * lies above fp32's range are scaled as any others while norm reads infinity, so an
+ * infinite norm does not say that tensors clipped in place are as they were. max_norm:
  * >= 0; infinity only measures. Tensors may be of both types, and empty.
  * Overlaps: every out must be disjoint from every other out and, unless it is the
  * tensor's own g, from every g (OWQ_ERR_RANGE); norm and workspace must be

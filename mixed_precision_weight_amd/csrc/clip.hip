@@ -2,6 +2,8 @@
 //
 //   norm = sqrt(sum over every tensor and element of g^2)
 //   out  = g * max_norm / norm  where norm > max_norm (and finite), else g
+// both with the fp64 norm: the fp32 one that is reported is infinite also for finite
+// gradients whose norm lies above fp32's range, and those are scaled.
 //
 // The weak columns of every linear are the parameters weak-column tuning trains,
 // so a step has one small gradient per linear: hundreds of tensors of 10^5 - 10^6

@@ -1168,8 +1168,10 @@ def clip_grad_norm(grads: list, max_norm: float, outs: list | None = None, norm:
     """Global norm of the gradient tensors (fp32 or fp16, any shape, contiguous),
     and clipping: every tensor is multiplied by max_norm / norm where norm >
     max_norm, in place or into outs (owq_clip_grad_norm; an out has its gradient's
-    type and number of elements). Returns the norm, fp32
-    [1], on the device; a norm that is not finite scales nothing."""
+    type and number of elements). Returns the norm, fp32 [1], on the device. An infinity
+    or NaN among the gradients makes it infinite or NaN, and nothing is scaled; it also
+    reads infinity where finite gradients have a norm above fp32's range (the factor
+    uses the fp64 norm), and those are scaled."""
     n = len(grads)
     if n < 1 or n > 4096:
         raise ValueError(f"need 1 to 4096 gradients, got {n}")
