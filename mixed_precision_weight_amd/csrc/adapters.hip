@@ -172,12 +172,13 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void k_adapter_shrink(const uint
         float4_t acc[2] = {float4_t{0.0f, 0.0f, 0.0f, 0.0f}, float4_t{0.0f, 0.0f, 0.0f, 0.0f}};
         // steps past the wave's end, and the tokens of other adapters, are read out of
         // range: zeros, nothing fetched (16 tokens of 15 requests: 11 -> 8.5 us)
-        const int xa = id == a ? xo : 0x40000000;
+        const int other = id == a ? 0 : kPairDead;
         half8_t xv[kShrinkFlight], av[kShrinkFlight];
         auto load = [&](int s, int u) {
-            const int o = s + u < s1 ? (s + u) * 64 : 0x40000000;
-            xv[u] = __builtin_bit_cast(half8_t, __builtin_amdgcn_raw_buffer_load_b128(xr, xa + o, 0, 0));
-            av[u] = __builtin_bit_cast(half8_t, __builtin_amdgcn_raw_buffer_load_b128(ar, ao + o, 0, 0));
+            const int past = s + u < s1 ? 0 : kPairDead, o = past ? 0 : (s + u) * 64;
+            xv[u] = __builtin_bit_cast(half8_t,
+                                       __builtin_amdgcn_raw_buffer_load_b128(xr, pair_offset(xo, o, past, other), 0, 0));
+            av[u] = __builtin_bit_cast(half8_t, __builtin_amdgcn_raw_buffer_load_b128(ar, pair_offset(ao, o, past, 0), 0, 0));
         };
         auto product = [&](int u) {
             acc[u & 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv[u], av[u], acc[u & 1], 0, 0, 0);

@@ -401,7 +401,8 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
         const int dead = c > last ? 0x40000000 : 0;
 #pragma unroll
         for (int t = 0; t < DPW; t++)
-            dma16(xr, stage + (wave * DPW + t) * 1024, xsrc[t] + cc * 128 + (cc == last ? xdead[t] : 0) + dead);
+            // (both marks are one bit: their sum would not be an int)
+            dma16(xr, stage + (wave * DPW + t) * 1024, xsrc[t] + cc * 128 + ((cc == last ? xdead[t] : 0) | dead));
     };
 
     const int rbase = wn * 32 * FN + l32;

@@ -95,9 +95,21 @@ __device__ __forceinline__ half8_t pair_weak(const PairLayer& P, int64_t row, in
     return pair_h8(u[0] | (u[1] << 16), u[2] | (u[3] << 16), u[4] | (u[5] << 16), u[6] | (u[7] << 16));
 }
 
+// Byte offset of a load that is put out of the buffer's range (zeros, nothing fetched)
+// by any of its marks, each 0 or kPairDead: together they are one bit, so the sum stays
+// an int for offsets below 2^30.
+constexpr int kPairDead = 0x40000000;
+__host__ __device__ constexpr int pair_offset(int start, int step, int dead, int dead2)
+{
+    return start + step + (dead | dead2);
+}
+
 // Tokens whose order is given are permuted within runs of this many, so that a run's
 // rows of x stay within 32-bit offsets.
 constexpr int kPairRun = 1024;
+// (the last token of a run of the longest rows, the last piece, both marks; a constant
+// expression does not overflow)
+static_assert(pair_offset((kPairRun - 1) * 65536 * 2 + 112, 1023 * 128, kPairDead, kPairDead) > 0, "offsets are int");
 
 // The sums of one wave of the block (its rows: row set l starts at n0[l], which may
 // lie past N; tokens from m0; ONE: both sets are rows of the one layer L[0], and
@@ -157,14 +169,14 @@ __device__ __forceinline__ bool pair_gemm(const PairLayer* L, const uint16_t* x,
         const int u = (wn * DPW + t) * 64 + lane;
         const int row = u >> 3, piece = (u & 7) ^ (row & 7);
         xsrc[t] = token(row) * K * 2 + piece * 16;
-        xdead[t] = (odd_tail && piece >= 4) ? 0x40000000 : 0;
+        xdead[t] = (odd_tail && piece >= 4) ? kPairDead : 0;
     }
     auto dma = [&](int c, char* stage) {
         const int cc = min(c, last);
-        const int dead = c >= c1 ? 0x40000000 : 0;
+        const int dead = c >= c1 ? kPairDead : 0;
 #pragma unroll
         for (int t = 0; t < DPW; t++)
-            pair_dma(xr, stage + (wn * DPW + t) * 1024, xsrc[t] + cc * 128 + (cc == last ? xdead[t] : 0) + dead);
+            pair_dma(xr, stage + (wn * DPW + t) * 1024, pair_offset(xsrc[t], cc * 128, cc == last ? xdead[t] : 0, dead));
     };
 
     // weak columns go in turns of 64; the lane's columns of this group's first turn are
@@ -199,7 +211,7 @@ __device__ __forceinline__ bool pair_gemm(const PairLayer* L, const uint16_t* x,
     typedef u32x3 QRegs[2];
     auto load_q = [&](int c, QRegs& cw) {
         const int g = min(2 * min(c, last) + h, G - 1);
-        const int dead = c >= c1 ? 0x40000000 : 0;
+        const int dead = c >= c1 ? kPairDead : 0;
 #pragma unroll
         for (int l = 0; l < 2; l++)
             cw[l] = __builtin_amdgcn_raw_buffer_load_b96(qr[l], (row[l] * G + g) * 12 + dead, 0, 0);
