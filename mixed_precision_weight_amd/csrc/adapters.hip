@@ -253,7 +253,8 @@ __device__ __forceinline__ void adapter_block(const AdapterArgs& ad, const Adapt
                     w.w[l][c] = adapter_weights<PIECE>(ad, id, N, n[l], c0 + 16 * c);
         };
         auto products = [&](int id, const Weights& w) {
-            const float f = tk.id == id ? tk.f : 0.0f;
+            // (by the tokens' adapters, not their factors: 0 times a NaN is NaN)
+            const int mine = (int)((uint32_t)__ballot(tk.id == id) >> (4 * h));
 #pragma unroll
             for (int l = 0; l < NL; l++) {
                 f32x16 s;
@@ -267,8 +268,9 @@ __device__ __forceinline__ void adapter_block(const AdapterArgs& ad, const Adapt
                 }
 #pragma unroll
                 for (int r = 0; r < 16; r++) {
-                    const float fr = __shfl(f, 8 * (r >> 2) + 4 * h + (r & 3), 64);
-                    z[l][r] += fr != 0.0f ? fr * s[r] : 0.0f;
+                    const float fr = __shfl(tk.f, 8 * (r >> 2) + 4 * h + (r & 3), 64);
+                    const int on = __builtin_amdgcn_sbfe(mine, 8 * (r >> 2) + (r & 3), 1);  // 0 or all bits
+                    z[l][r] += __builtin_bit_cast(float, __builtin_bit_cast(int, fr * s[r]) & on);
                 }
             }
         };

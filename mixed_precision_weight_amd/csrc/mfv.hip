@@ -335,6 +335,10 @@ __global__ __launch_bounds__(64 * W * S) void k_mfv(MfvBatch b, int M, ADP ad)
             load(8 * qd, qa4);
             const AdapterToken tk = adapter_token<4, 16>(ad, min(l16, M - 1), min(l16, M - 1), l16 < M, qd);
             half8_t th, tl;  // this lane's token's values c .. c + 7
+            float fr[4];     // the factors of this lane's outputs
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+                fr[r] = __shfl(tk.f, 4 * qd + r, 64);
             auto products = [&](const Some& q) {
 #pragma unroll
                 for (int j = 0; j < AH; j++) {
@@ -343,12 +347,11 @@ __global__ __launch_bounds__(64 * W * S) void k_mfv(MfvBatch b, int M, ADP ad)
                     f32x4 hi = f32x4{0.0f, 0.0f, 0.0f, 0.0f}, lo = hi;
                     hi = __builtin_amdgcn_mfma_f32_16x16x32_f16(th, q.w[j], hi, 0, 0, 0);
                     lo = __builtin_amdgcn_mfma_f32_16x16x32_f16(tl, q.w[j], lo, 0, 0, 0);
-                    const float f = tk.id == q.id[j] ? tk.f : 0.0f;
+                    // (by the tokens' adapters, not their factors: 0 times a NaN is NaN)
+                    const uint32_t mine = (uint32_t)__ballot(tk.id == q.id[j]) >> (4 * qd);
 #pragma unroll
-                    for (int r = 0; r < 4; r++) {
-                        const float fr = __shfl(f, 4 * qd + r, 64);
-                        acc[r] = fr != 0.0f ? acc[r] + fr * (hi[r] + lo[r]) : acc[r];
-                    }
+                    for (int r = 0; r < 4; r++)
+                        acc[r] = (mine & (1u << r)) != 0 ? acc[r] + fr[r] * (hi[r] + lo[r]) : acc[r];
                 }
             };
             for (int c = 8 * qd; c < ad.rpad; c += 32) {

@@ -37,7 +37,7 @@ inline AdapterArgs adapter_args(const AdapterDesc& a)
 }
 
 // A lane's view of one token's adapter: its index (-1: none), the exponent that
-// t is scaled by and the factor that undoes it with alpha in it (0: none).
+// t is scaled by and the factor that undoes it with alpha in it (0 without one).
 struct AdapterToken {
     const float* t;
     int id, e;
