@@ -496,7 +496,8 @@ typedef enum {
  * on Real Device", p.6)); activation and product on the fp32 sums, h rounded to
  * fp16 once. gate, up: HOST pointers to packed layers of the same N and K (their
  * weak columns may differ); x: fp16 [M][K]; h: fp16 [M][N] (output); g, u: fp32
- * [M][N] outputs for owq_gated_backward, both or neither NULL. act: an
+ * [M][N] outputs for owq_gated_backward, both or neither NULL. Outputs must not overlap
+ * one another, x or the layers (OWQ_ERR_RANGE). act: an
  * owq_activation. M, N <= 2^30 and M N <= 2^36; N <= 2^26 for M <= 2, 2^29 for M <= 16
  * (OWQ_ERR_SHAPE where the launch would count 2^32 threads). Errors as owq_linear, plus OWQ_ERR_SHAPE for layers
  * that do not match, OWQ_ERR_UNSUPPORTED for an unknown act, OWQ_ERR_NULL for one of g, u. */
@@ -521,6 +522,9 @@ size_t owq_gated_backward_workspace_bytes(int64_t N, int64_t K, int32_t k_gate, 
  * after scaling each token by a power of two (11 bits of every term that is not
  * below 2^-28 of the token's largest; no term overflows), the products with q - z
  * are exact and the sums fp32; relu's slope at 0 is 0. Bitwise deterministic.
+ * dx may lie over x, g, u or dh, which are read before it is written; all other
+ * outputs and the workspace must not overlap one another, an input or a layer
+ * (OWQ_ERR_RANGE).
  * workspace: >= owq_gated_backward_workspace_bytes(...) bytes, 256-byte aligned,
  * contents ignored; calls sharing it must be ordered. M, N <= 2^20 and M (k gate + k up)
  * <= 2^29 (OWQ_ERR_SHAPE where a launch would count 2^32 threads). Errors as owq_gated,
@@ -558,7 +562,8 @@ size_t owq_linear_adapters_workspace_bytes(int32_t rank, int64_t M);
  * are not finite. Two launches: the low-rank products; the linear with the second
  * products in its epilogue. workspace: >=
  * owq_linear_adapters_workspace_bytes(rank, M) bytes, 256-byte aligned, contents
- * ignored; calls sharing it must be ordered. M, N <= 2^30, M N <= 2^36 and M ceil(rank / 16)
+ * ignored; calls sharing it must be ordered. y and workspace must not overlap each other
+ * or an input (OWQ_ERR_RANGE). M, N <= 2^30, M N <= 2^36 and M ceil(rank / 16)
  * <= 2^24; N <= 2^27 for M <= 16 (OWQ_ERR_SHAPE, and workspace bytes 0, where a launch
  * would count 2^32 threads). Other arguments and errors as owq_linear, plus
  * OWQ_ERR_WORKSPACE, and OWQ_ERR_SHAPE for count and rank. */
@@ -594,8 +599,8 @@ size_t owq_clip_grad_norm_workspace_bytes(int32_t count);
  * infinite norm does not say that tensors clipped in place are as they were. max_norm:
  * >= 0; infinity only measures. Tensors may be of both types, and empty.
  * Overlaps: every out must be disjoint from every other out and, unless it is the
- * tensor's own g, from every g (OWQ_ERR_RANGE); norm and workspace must be
- * disjoint from all of them. workspace: >= owq_clip_grad_norm_workspace_bytes
+ * tensor's own g, from every g; norm and workspace must be disjoint from all of them
+ * and from each other (OWQ_ERR_RANGE). workspace: >= owq_clip_grad_norm_workspace_bytes
  * (count) bytes, 256-byte aligned, contents ignored; calls sharing it must be
  * ordered. items: HOST array. Bitwise deterministic. */
 owq_status owq_clip_grad_norm(const owq_grad* items, int32_t count, double max_norm, float* norm,

@@ -9,6 +9,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <exception>
+#include <initializer_list>
 #include <utility>
 #include <vector>
 
@@ -137,6 +138,38 @@ owq::LinearDesc desc_of(const owq_layer* L, const uint16_t* x, uint16_t* y)
     d.K = L->K;
     d.k = L->k;
     return d;
+}
+
+// An array of a call, for the checks that none of its outputs lies over another array
+struct Span {
+    const char* name;
+    const void* p;  // NULL: not given
+    uint64_t bytes;
+};
+
+bool overlap(const Span& a, const Span& b)
+{
+    const uintptr_t pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
+    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && (pa < pb ? a.bytes > pb - pa : b.bytes > pa - pb);
+}
+
+owq_status check_apart(const Span& out, std::initializer_list<Span> others)
+{
+    for (const Span& s : others)
+        if (overlap(out, s))
+            return fail(OWQ_ERR_RANGE, "%s overlaps %s", out.name, s.name);
+    return OWQ_OK;
+}
+
+// (a scale, zero point or index that lies under an output is as wrong as a code)
+owq_status check_apart(const Span& out, const owq_layer* L)
+{
+    const uint64_t N = (uint64_t)L->N, K = (uint64_t)L->K, k = (uint64_t)L->k;
+    return check_apart(out, {{"qcodes", L->qcodes, N * K / 8 * 3},
+                             {"scales", L->scales, 2 * N},
+                             {"zeros", L->zeros, N},
+                             {"weak_idx", L->weak_idx, 4 * k},
+                             {"w_weak", L->w_weak, 2 * N * k}});
 }
 
 // The two layers of a gated block, its input and an fp16 output.
@@ -843,6 +876,16 @@ owq_status owq_gated(const owq_layer* gate, const owq_layer* up, const uint16_t*
         return fail(OWQ_ERR_NULL, "g and u must be given together");
     if (!aligned(g, 4) || !aligned(u, 4))
         return fail(OWQ_ERR_ALIGN, "misaligned pointer (g, u: 4 B)");
+    const uint64_t n = (uint64_t)M * (uint64_t)gate->N;
+    const Span in{"x", x, 2 * (uint64_t)M * (uint64_t)gate->K};
+    const Span outs[3] = {{"h", h, 2 * n}, {"g", g, 4 * n}, {"u", u, 4 * n}};
+    for (int i = 0; i < 3; i++) {
+        st = check_apart(outs[i], {in, outs[(i + 1) % 3]});
+        for (const owq_layer* L : {gate, up})
+            st = st != OWQ_OK ? st : check_apart(outs[i], L);
+        if (st != OWQ_OK)
+            return st;
+    }
     return launch_status(owq::launch_gated(desc_of(gate, x, nullptr), desc_of(up, x, nullptr), M, act, h, g, u,
                                            (hipStream_t)stream),
                          "owq_gated launch");
@@ -882,6 +925,21 @@ owq_status owq_gated_backward(const owq_layer* gate, const owq_layer* up, const 
         g_err[0] = '\0';
         return OWQ_OK;
     }
+    // dx is written after x, g, u and dh have been read; everything else stays apart
+    const uint64_t n = (uint64_t)M * (uint64_t)gate->N, mk = 2 * (uint64_t)M * (uint64_t)gate->K;
+    const Span sx{"x", need_x ? x : nullptr, mk}, sg{"g", g, 4 * n}, su{"u", u, 4 * n}, sh{"dh", dh, 2 * n};
+    const Span sdx{"dx", dx, mk}, ws{"workspace", workspace, need};
+    const Span dwg{"dw_gate", dw_gate, 4 * (uint64_t)gate->N * (uint64_t)gate->k};
+    const Span dwu{"dw_up", dw_up, 4 * (uint64_t)up->N * (uint64_t)up->k};
+    st = check_apart(sdx, {dwg, dwu, ws});
+    st = st != OWQ_OK ? st : check_apart(dwg, {sx, sg, su, sh, dwu, ws});
+    st = st != OWQ_OK ? st : check_apart(dwu, {sx, sg, su, sh, ws});
+    st = st != OWQ_OK ? st : check_apart(ws, {sx, sg, su, sh});
+    for (const Span* out : {&sdx, &dwg, &dwu, &ws})
+        for (const owq_layer* L : {gate, up})
+            st = st != OWQ_OK ? st : check_apart(*out, L);
+    if (st != OWQ_OK)
+        return st;
     return launch_status(owq::launch_gated_backward(desc_of(gate, x, nullptr), desc_of(up, x, nullptr), M, act, g, u,
                                                     dh, dx, dw_gate, dw_up, workspace, (hipStream_t)stream),
                          "owq_gated_backward launch");
@@ -918,6 +976,19 @@ owq_status owq_linear_adapters(const owq_layer* L, const owq_adapters* ad, const
     if (workspace_bytes < owq::adapter_workspace_bytes(ad->rank, M))
         return fail(OWQ_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", workspace_bytes,
                     owq::adapter_workspace_bytes(ad->rank, M));
+    const uint64_t K = (uint64_t)L->K, N = (uint64_t)L->N, ranks = (uint64_t)ad->count * (uint64_t)ad->rank;
+    const Span sy{"y", y, 2 * (uint64_t)M * N}, ws{"workspace", workspace, owq::adapter_workspace_bytes(ad->rank, M)};
+    for (const Span* out : {&sy, &ws}) {
+        st = check_apart(*out, {{"x", x, 2 * (uint64_t)M * K},
+                                {"A", ad->A, 2 * ranks * K},
+                                {"B", ad->B, 2 * ranks * N},
+                                {"alpha", ad->alpha, 4 * (uint64_t)ad->count},
+                                {"which", which, 4 * (uint64_t)M},
+                                out == &sy ? ws : sy});
+        st = st != OWQ_OK ? st : check_apart(*out, L);
+        if (st != OWQ_OK)
+            return st;
+    }
     st = check_idx_on_host(L->weak_idx, L->k, L->K, (hipStream_t)stream);
     if (st != OWQ_OK)
         return st;
@@ -959,6 +1030,7 @@ owq_status owq_clip_grad_norm(const owq_grad* items, int32_t count, double max_n
     if (workspace_bytes < owq::clip_workspace_bytes(count))
         return fail(OWQ_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", workspace_bytes,
                     owq::clip_workspace_bytes(count));
+    owq_status st = OWQ_OK;
     try {
         std::vector<owq::ClipEntry> it((size_t)count);
         std::vector<std::pair<uintptr_t, uintptr_t>> outs;  // [begin, end) of the non-empty outputs
@@ -993,6 +1065,18 @@ owq_status owq_clip_grad_norm(const owq_grad* items, int32_t count, double max_n
             if (hit && !(g.out == g.g && (o - 1)->first == b))
                 return fail(OWQ_ERR_RANGE, "item %d: g overlaps an output that is not its own", i);
         }
+        const Span sn{"norm", norm, 4}, ws{"workspace", workspace, owq::clip_workspace_bytes(count)};
+        st = check_apart(sn, {ws});
+        for (int32_t i = 0; i < count && st == OWQ_OK; i++) {
+            const owq_grad& g = items[i];
+            const uint64_t bytes = (uint64_t)g.n * (g.type ? 2 : 4);
+            for (const Span* s : {&sn, &ws})
+                st = st != OWQ_OK ? st : check_apart(*s, {{"a gradient", g.g, bytes}, {"an output", g.out, bytes}});
+            if (st != OWQ_OK)
+                return fail_at(st, "item", i);
+        }
+        if (st != OWQ_OK)
+            return st;
         return launch_status(owq::launch_clip(it.data(), count, max_norm, norm, workspace, (hipStream_t)stream),
                              "owq_clip_grad_norm launch");
     } catch (const std::exception& ex) {
