@@ -642,7 +642,8 @@ def linear_storage_batched(layers: list, xs: list, ys: list | None = None, works
 
 def layer_shapes(layer: dict):
     """(N, K, k) of a packed layer dict, after checking that its five tensors
-    agree with one another."""
+    agree with one another and are not the storage-favoured form's (with fewer than 32
+    weak columns its codes have the same shape)."""
     for name in _PACK_OUT + ("weak_idx",):
         if name not in layer:
             raise ValueError(f"layer lacks {name!r}")
@@ -655,6 +656,9 @@ def layer_shapes(layer: dict):
     if idx.dim() != 1:
         raise ValueError(f"weak_idx must be 1-D, got {tuple(idx.shape)}")
     k = idx.numel()
+    if k and "K" in layer:
+        raise ValueError(f"qcodes hold the dense columns only (storage-favoured form, K = {layer['K']}): need a layer "
+                         "with all columns")
     for name, (shape, dt) in _pack_out_shapes(N, K, k).items():
         _meta(layer[name], dt, name, shape)
     return N, K, k
@@ -977,7 +981,7 @@ def _layer_fast(layer: dict):
         N, G, three = q.shape
         k, = idx.shape
         dev = q.get_device()
-        if (three == 3 and dev >= 0 and s.shape == (N,) and z.shape == (N,) and w.shape == (N, k)
+        if (three == 3 and dev >= 0 and not (k and "K" in layer) and s.shape == (N,) and z.shape == (N,) and w.shape == (N, k)
                 and q.dtype is torch.int32 and idx.dtype is torch.int32 and z.dtype is torch.uint8
                 and s.dtype is torch.float16 and w.dtype is torch.float16
                 and q.is_contiguous() and s.is_contiguous() and z.is_contiguous() and w.is_contiguous()
