@@ -24,8 +24,9 @@
 //
 // Measured: one token of rank 16, K = 4096, 7 us (which, then x and A: two memory
 // latencies, the launch); 16 tokens of 15 requests 8 - 9; 1000 tokens of three requests
-// one after the other, rank 64, K = 11008, 28: each XCD fetches the adapters of its
-// tiles, 50 MB for 26 MB of x and A. The products above 16 tokens: see
+// one after the other, rank 64, K = 11008, 25: the 16 x 16 tile reads x once per 16
+// ranks and A once per 16 tokens, 142 MB through the L2s, and each XCD fetches the
+// adapters of its tiles, 50 MB for 26 MB of x and A. The products above 16 tokens: see
 // owq_pair_gemm.h; 1000 tokens of 11008 -> 4096 in 111 us (810 TFLOP/s: 256 blocks,
 // one wave per SIMD).
 #include <algorithm>

@@ -25,9 +25,10 @@
 //
 // Bound: memory, two reads and a write of every element; the second read comes from
 // the 256 MB last-level cache where the tensors fit. Measured, 224 fp32 tensors of
-// 5.1e7 elements: 57 us for pass 1 (3.5 TB/s, while the caches write back what was
-// written before) and 69 us for pass 2 (5.9 TB/s); with three launches of pass 1 in
-// place of one it took 66 us.
+// 5.1e7 elements: 57 us for pass 1 (3.5 TB/s) right after a call that wrote its outputs,
+// which the caches write back meanwhile; 39 us (5.2 TB/s) after calls that wrote nothing
+// or with 1 GiB read in between; 70 us for pass 2 (5.8 TB/s). With three launches of pass
+// 1 in place of one it took 66 us.
 #include "owq_device.h"
 #include "owq_launch.h"
 

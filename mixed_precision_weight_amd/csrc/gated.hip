@@ -16,10 +16,10 @@
 //                           v_mfma_f32_32x32x16_f16; matrix cores and decode
 // Products of fp16 x with the integers q - z are exact; sums are fp32.
 //
-// Measured, two layers of 11008 x 4096: M = 1 11.2 us (3.15 TB/s of codes and weak
-// columns), M = 2048 340 us (1.09 PFLOP/s, where a plain library product of 8192^3
-// reaches 1.16), 370 with g and u kept; 28672 x 8192 at M = 8
-// 49 us (3.7 TB/s); 2048 x 768 at M = 1 4.6 us, launch and one memory latency.
+// Measured, two layers of 11008 x 4096: M = 1 10.7 us (3.3 TB/s of codes and weak
+// columns; 9.2 one after another in a graph), M = 2048 325 us (1.14 PFLOP/s, where a
+// plain library product of 8192^3 reaches 1.16), 342 with g and u kept; 28672 x 8192 at
+// M = 8 49 us (3.8 TB/s); 2048 x 768 at M = 1 4.4 us, launch and one memory latency.
 #include <type_traits>
 
 #include "owq_act.h"

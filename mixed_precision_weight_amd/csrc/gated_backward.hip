@@ -32,12 +32,16 @@
 // Every sum's order is fixed, so results are deterministic.
 //
 // Measured, M = 2048, two layers of 11008 x 4096, 32 weak columns each, us:
-//  1   77  225 MB read, 2.9 TB/s; the vector memory path is 61 % busy (a token's row
+//  1   76  225 MB read, 2.9 TB/s; the vector memory path is 61 % busy (a token's row
 //          per lane), the fp32 matrix instructions and the activations fill the rest
 //  2    5
-//  3   73  225 MB read, 90 written: 4.3 TB/s
-//  4  366  369 GFLOP: 1.01 PFLOP/s; matrix cores and the decode that feeds them
+//  3   72  225 MB read, 90 written: 4.3 TB/s
+//  4  316  369 GFLOP: 1.17 PFLOP/s; matrix cores and the decode that feeds them (over
+//          390 in the first dozen launches after an idle time, at a lower clock: the
+//          steps named below were timed so)
 //  5   22  67 MB of partial sums read, 17 written: 3.8 TB/s
+// Launches 1 and 3 run once per 32 weak columns, the reads and activations again for
+// each: 63 columns 148 and 117, 86 columns 228 and 153, 130 columns 358 and 224.
 // At M = 77, 2731 x 1056 each launch takes 4 - 13 us: their latencies (launch 2 with
 // one thread per sum over all slabs took 6.4, now 3.9).
 #include "owq_act.h"
