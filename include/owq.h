@@ -497,10 +497,11 @@ typedef enum {
  * fp16 once. gate, up: HOST pointers to packed layers of the same N and K (their
  * weak columns may differ); x: fp16 [M][K]; h: fp16 [M][N] (output); g, u: fp32
  * [M][N] outputs for owq_gated_backward, both or neither NULL. Outputs must not overlap
- * one another, x or the layers (OWQ_ERR_RANGE). act: an
- * owq_activation. M, N <= 2^30 and M N <= 2^36; N <= 2^26 for M <= 2, 2^29 for M <= 16
- * (OWQ_ERR_SHAPE where the launch would count 2^32 threads). Errors as owq_linear, plus OWQ_ERR_SHAPE for layers
- * that do not match, OWQ_ERR_UNSUPPORTED for an unknown act, OWQ_ERR_NULL for one of g, u. */
+ * one another, x or the layers (OWQ_ERR_RANGE). act: an owq_activation. M, N <= 2^30
+ * and M N <= 2^36; N <= 2^26 for M <= 2, 2^29 for M <= 16 (OWQ_ERR_SHAPE where the
+ * launch would count 2^32 threads). Errors as owq_linear, plus OWQ_ERR_SHAPE for layers
+ * that do not match, OWQ_ERR_UNSUPPORTED for an unknown act, OWQ_ERR_NULL for one of
+ * g, u. */
 owq_status owq_gated(const owq_layer* gate, const owq_layer* up, const uint16_t* x, int64_t M, int32_t act,
                      uint16_t* h, float* g, float* u, void* stream);
 
