@@ -1,4 +1,4 @@
-"""The 8-bit form of the mixed-precision linear and the orthogonalised update, as
+"""The integer form of the mixed-precision linear and the orthogonalised update, as
 they are measured.
 
 Four kinds of call:
@@ -216,11 +216,11 @@ def prepare(case, seed):
         s["dy"] = (torch.randn(M, case["N"], generator=g, device=DEV) * 0.01).half()
     if own:
         if case["op"] == "grad":
-            need = owq.linear_int8_backward_workspace_bytes(case["N"], case["K"], case["k"], M)
+            need = owq.linear_integer_backward_workspace_bytes(case["N"], case["K"], case["k"], M)
         elif case["op"] == "batched":
-            need = owq.linear_int8_batched_workspace_bytes(shapes, M)
+            need = owq.linear_integer_batched_workspace_bytes(shapes, M)
         else:
-            need = owq.linear_int8_workspace_bytes(case["N"], case["K"], case["k"], M)
+            need = owq.linear_integer_workspace_bytes(case["N"], case["K"], case["k"], M)
         s["workspace"] = torch.empty(max(need, 256), dtype=torch.uint8, device=DEV)
     return s
 
@@ -276,11 +276,11 @@ def run(state):
                           eps=EPS, workspace=s["workspace"])
         return s["flat"]
     if op == "grad":
-        dx, dw_weak = owq.linear_int8_backward(s["layers"][0], s["xs"][0], s["dy"], workspace=s["workspace"])
+        dx, dw_weak = owq.linear_integer_backward(s["layers"][0], s["xs"][0], s["dy"], workspace=s["workspace"])
         return {"dx": dx, "dw_weak": dw_weak}
     if op == "batched":
-        return owq.linear_int8_batched(s["layers"], s["xs"], workspace=s["workspace"])
-    return owq.linear_int8(s["layers"][0], s["xs"][0], workspace=s["workspace"])
+        return owq.linear_integer_batched(s["layers"], s["xs"], workspace=s["workspace"])
+    return owq.linear_integer(s["layers"][0], s["xs"][0], workspace=s["workspace"])
 
 
 # ------------------------------------------------------------------ in 64 bits
