@@ -163,8 +163,9 @@ def _layer(g, N, K, k):
     dense = W.float()
     dense[:, idx] = 0.0
     top = dense.abs().amax(1, keepdim=True)
-    codes = torch.round(dense * torch.where(top > 0, 127.0 / top, torch.zeros_like(top)))
-    return {"codes": codes.to(torch.int8), "scales": (top / 127.0).view(N).contiguous(),
+    full = torch.full_like(top, 127.0)  # (of tensors, so that each is one division)
+    codes = torch.round(dense * torch.where(top > 0, full / top, torch.zeros_like(top)))
+    return {"codes": codes.to(torch.int8), "scales": (top / full).view(N).contiguous(),
             "w_weak": W[:, idx].contiguous(), "weak_idx": idx.to(torch.int32)}
 
 
@@ -234,8 +235,9 @@ def _plain_linear(layer, x):
     dense = x.clone()
     dense[:, idx] = 0.0
     top = dense.abs().amax(1, keepdim=True)
-    codes = torch.round(dense * torch.where(top > 0, 127.0 / top, torch.zeros_like(top)))
-    y = (codes @ layer["codes"].float().t()) * (top / 127.0) * layer["scales"][None, :]
+    full = torch.full_like(top, 127.0)
+    codes = torch.round(dense * torch.where(top > 0, full / top, torch.zeros_like(top)))
+    y = (codes @ layer["codes"].float().t()) * (top / full) * layer["scales"][None, :]
     return (y + weak @ layer["w_weak"].float().t()).half()
 
 
