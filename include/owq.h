@@ -607,6 +607,121 @@ size_t owq_clip_grad_norm_workspace_bytes(int32_t count);
 owq_status owq_clip_grad_norm(const owq_grad* items, int32_t count, double max_norm, float* norm,
                               void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------ integer form --- */
+
+/* The integer form: the layer with 8-bit codes on both sides of its product. The weak
+ * columns, whose activations are the loud ones, stay fp16 in the weights and in the
+ * tokens ([PL] "Weak-column selection" (paper p.4)), and everything else is multiplied
+ * in 8-bit integers with a scale per output channel and one per token. For layers that
+ * are served where the products, not the weights' bytes, decide (prompts), or that
+ * should lose less than at 3 bits. Definition (the pages give none; it is the library's):
+ *   t_i       = max |W[i][j]| over the dense columns j        (0 if there are none)
+ *   scales[i] = t_i / 127                                     one fp32 division
+ *   codes[i][j] = rint(W[i][j] * (127 / t_i))                 fp32 division and product,
+ *               rint = round half to even; 0 at the weak columns and where t_i = 0
+ *   w_weak[i][c] = W[i][weak_idx[c]]
+ * W, weak_idx: as owq_pack. codes: int8 [N][K], 16-byte aligned; scales: fp32 [N];
+ * w_weak: fp16 [N][k]. Outputs must not overlap one another or an input
+ * (OWQ_ERR_RANGE). N < 2^24. Bitwise the definition. */
+owq_status owq_pack_integer(const uint16_t* W, int64_t N, int64_t K, const int32_t* weak_idx, int32_t k, int8_t* codes,
+                         float* scales, uint16_t* w_weak, void* stream);
+
+/* One layer in the integer form (owq_pack_integer). HOST struct, device pointers. */
+typedef struct owq_integer_layer {
+    int64_t N, K;               /* output rows, input columns */
+    int32_t k;                  /* weak columns */
+    const int8_t* codes;        /* [N][K] */
+    const float* scales;        /* [N] */
+    const int32_t* weak_idx;    /* [k], ascending (NULL iff k == 0) */
+    const uint16_t* w_weak;     /* fp16 [N][k] (NULL iff k == 0) */
+} owq_integer_layer;
+
+/* Bytes of device workspace owq_linear_integer needs (the tokens' codes): 0 up to 4
+ * tokens, and 0 for sizes outside its range. */
+size_t owq_linear_integer_workspace_bytes(int64_t N, int64_t K, int32_t k, int64_t M);
+
+/* Product of the integer form. Every token is quantised on the way in as a row of W is
+ * (its dense columns only, t_m, s_m = t_m / 127, q_mj = rint(x_mj * (127 / t_m))):
+ *   y[m][i] = s_m scales[i] sum_j q_mj codes[i][j] + sum_c x[m][weak_idx[c]] w_weak[i][c]
+ * with exact integer sums, the rest in fp32, y rounded to fp16 once. A token with an
+ * infinity or NaN in a dense column has infinite or NaN outputs and leaves the others
+ * as they are. x: fp16 [M][K]; y: fp16 [M][N]. One launch up to 4 tokens, two above.
+ * workspace: >= owq_linear_integer_workspace_bytes(...) bytes, 256-byte aligned (may be NULL
+ * where that is 0), contents ignored; calls sharing it must be ordered. y and workspace
+ * must not overlap each other, x or the layer (OWQ_ERR_RANGE). M < 2^24; OWQ_ERR_SHAPE
+ * where a launch would count 2^32 threads. Errors as owq_linear, plus OWQ_ERR_WORKSPACE. */
+owq_status owq_linear_integer(const owq_integer_layer* L, const uint16_t* x, int64_t M, uint16_t* y, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace owq_linear_integer_batched needs: the sum of its layers'
+ * (0 up to 4 tokens, for invalid sizes, or count outside 1..64). */
+size_t owq_linear_integer_batched_workspace_bytes(const owq_integer_layer* Ls, int32_t count, int64_t M);
+
+/* owq_linear_integer for `count` layers on the same number of tokens M <= 16 (the linears of
+ * a decoder layer), bit for bit the same outputs, in one launch (two above 4 tokens) per
+ * 16 layers. Ls, xs, ys: HOST arrays [count]; several layers may read one x; an output
+ * must not overlap any input, layer or other output. Returns OWQ_ERR_UNSUPPORTED unless
+ * 1 <= M <= 16 and 1 <= count <= 64; other errors as owq_linear_integer, with the layer's
+ * index. */
+owq_status owq_linear_integer_batched(const owq_integer_layer* Ls, const uint16_t* const* xs, uint16_t* const* ys,
+                                   int32_t count, int64_t M, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace owq_linear_integer_backward needs (0 for sizes outside its
+ * range): mostly 2 M N for the scaled gradients. */
+size_t owq_linear_integer_backward_workspace_bytes(int64_t N, int64_t K, int32_t k, int64_t M);
+
+/* Backward of owq_linear_integer for Weak Column Tuning, as owq_linear_backward ([PL] "Weak
+ * Column Tuning" (paper "PEFT with Weak Column Tuning", p.5)); gradients pass the tokens'
+ * rounding to 8 bits as they would the identity. With W = scales codes and the weak
+ * columns:
+ *   dx[m][j]      = sum_i dy[m][i] W[i][j]         fp16 [M][K]
+ *   dw_weak[i][c] = sum_m dy[m][i] x[m][idx_c]     fp32 [N][k]
+ * x: fp16 [M][K], read only for dw_weak (may be NULL without it); dy: fp16 [M][N]; dx,
+ * dw_weak: outputs, each may be NULL. In the dense part of dx, dy times the scale is
+ * rounded to fp16 after scaling each token by a power of two (11 bits of every term that
+ * is not below 2^-28 of the token's largest; no term overflows); every other product is
+ * exact and every sum fp32. Bitwise deterministic. No output and not the workspace may
+ * overlap one another, an input or the layer (OWQ_ERR_RANGE). M, N <= 2^20. workspace: >=
+ * owq_linear_integer_backward_workspace_bytes(...) bytes, 256-byte aligned, contents ignored;
+ * calls sharing it must be ordered. Errors as owq_linear_integer. */
+owq_status owq_linear_integer_backward(const owq_integer_layer* L, const uint16_t* x, const uint16_t* dy, int64_t M,
+                                    uint16_t* dx, float* dw_weak, void* workspace, size_t workspace_bytes, void* stream);
+
+/* --------------------------------------------------- orthogonalised update --- */
+
+/* One matrix of owq_orthogonalize (host struct, device pointers). */
+typedef struct owq_update {
+    const void* g;       /* [rows][cols] of `type` (may be NULL iff it is empty) */
+    void* out;           /* where the update goes: g itself (in place) or another buffer */
+    int64_t rows, cols;  /* >= 0; at most 2^20, the shorter at most 16384 */
+    float scale;         /* of the update (a step size, sqrt(rows / cols), ...) */
+    int32_t type;        /* 0: fp32, 1: fp16 */
+} owq_update;
+
+/* Bytes of device workspace owq_orthogonalize needs for these matrices (their rows and
+ * cols; 0 for sizes outside its range or count outside 1..4096). */
+size_t owq_orthogonalize_workspace_bytes(const owq_update* items, int32_t count);
+
+/* Each gradient matrix replaced by a nearly orthogonal factor of itself: the step of
+ * weak-column tuning between owq_clip_grad_norm and the weights ([PL] "Weak Column
+ * Tuning" (paper "PEFT with Weak Column Tuning", p.5): the trainable blocks are the
+ * N x k matrices of the weak columns). By Newton-Schulz products,
+ *   X = g / (|g|_F + eps),  `steps` times  X <- a X + b (X X^T) X + c (X X^T)^2 X,
+ *   out = scale X
+ * which moves every singular value towards 1 and keeps the singular vectors. (a, b, c):
+ * coefficients, HOST array [3]; (1.875, -1.25, 0.375) converges to the factor itself,
+ * (3.4445, -4.7750, 2.0315) lifts small values faster and ends between 0.7 and 1.2. |g|_F
+ * and, up to a shorter side of 96, the polynomial of X X^T are fp64, all else fp32, out
+ * rounded once. A matrix of zeros gives zeros; one with an infinity or NaN gives NaN
+ * throughout, and the others are as without it. 1 <= steps <= 16; coefficients finite;
+ * eps > 0. Every out must be disjoint from every other out and, unless it is the matrix's
+ * own g, from every g; the workspace from all of them (OWQ_ERR_RANGE). workspace: >=
+ * owq_orthogonalize_workspace_bytes(items, count) bytes, 256-byte aligned, contents
+ * ignored; calls sharing it must be ordered. items: HOST array. Bitwise deterministic,
+ * and a matrix's result does not depend on the others of the call. */
+owq_status owq_orthogonalize(const owq_update* items, int32_t count, int32_t steps, const double* coefficients,
+                             double eps, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------- measurement reference --- */
 
 /* Not a step of the method: a read-only HBM stream with the M = 1 decode

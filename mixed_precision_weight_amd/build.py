@@ -34,7 +34,8 @@ _REMARK = re.compile(r"remark: +(Function Name|TotalSGPRs|VGPRs|AGPRs|ScratchSiz
                      r"Occupancy \[waves/SIMD\]|SGPRs Spill|VGPRs Spill|LDS Size \[bytes/block\]): (\S+)")
 SOURCES = ["api.cpp", "calib.hip", "topk.hip", "pack.hip", "search.hip", "storage.hip", "backward.hip", "optq.hip",
            "gemv.hip", "mfv.hip", "gemm.hip", "stream.hip", "grouped.hip", "adapters.hip", "gated.hip", "gated_backward.hip",
-           "clip.hip"]
+           "clip.hip", "int8.hip", "int8_backward.hip",
+           "orthogonalize.hip"]
 
 
 def _resources(stderr: str) -> dict:

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -60,7 +61,8 @@ bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 constexpr int64_t kMaxK = 65536;
 constexpr int32_t kMaxRank = 256;    // of a low-rank adapter
 constexpr int64_t kMaxBlock = (int64_t)1 << 30;  // tokens and rows of the gated block and the adapted linear
-constexpr int32_t kMaxGrads = 4096;  // tensors per owq_clip_grad_norm
+constexpr int32_t kMaxGrads = 4096;  // tensors per owq_clip_grad_norm and owq_orthogonalize
+constexpr int32_t kMaxNsSteps = 16;
 
 owq_status check_k_dim(int64_t K)
 {
@@ -161,6 +163,38 @@ owq_status check_apart(const Span& out, std::initializer_list<Span> others)
     return OWQ_OK;
 }
 
+// One tensor of a list whose outputs are written beside each other: out may be its own
+// g, and is otherwise disjoint from every g and every other out.
+struct InOut {
+    const void* g;
+    const void* out;
+    uint64_t bytes;
+};
+owq_status check_list_apart(const std::vector<InOut>& list)
+{
+    std::vector<std::pair<uintptr_t, uintptr_t>> outs;  // [begin, end) of the non-empty outputs
+    outs.reserve(list.size());
+    for (const InOut& t : list)
+        if (t.bytes > 0)
+            outs.emplace_back((uintptr_t)t.out, (uintptr_t)t.out + t.bytes);
+    std::sort(outs.begin(), outs.end());
+    for (size_t i = 1; i < outs.size(); i++)
+        if (outs[i].first < outs[i - 1].second)
+            return fail(OWQ_ERR_RANGE, "two outputs overlap (a tensor listed twice?)");
+    for (size_t i = 0; i < list.size(); i++) {
+        const InOut& t = list[i];
+        if (t.bytes == 0)
+            continue;
+        // the one output that begins in or reaches into [b, e): the last that begins below e
+        const uintptr_t b = (uintptr_t)t.g, e = b + t.bytes;
+        auto o = std::lower_bound(outs.begin(), outs.end(), std::make_pair(e, (uintptr_t)0));
+        const bool hit = o != outs.begin() && (o - 1)->second > b;
+        if (hit && !(t.out == t.g && (o - 1)->first == b))
+            return fail(OWQ_ERR_RANGE, "item %zu: g overlaps an output that is not its own", i);
+    }
+    return OWQ_OK;
+}
+
 // (a scale, zero point or index that lies under an output is as wrong as a code)
 owq_status check_apart(const Span& out, const owq_layer* L)
 {
@@ -170,6 +204,73 @@ owq_status check_apart(const Span& out, const owq_layer* L)
                              {"zeros", L->zeros, N},
                              {"weak_idx", L->weak_idx, 4 * k},
                              {"w_weak", L->w_weak, 2 * N * k}});
+}
+
+// --- 8-bit form
+
+bool int8_sizes_ok(int64_t N, int64_t K, int32_t k, int64_t M)
+{
+    return N >= 1 && N <= kMaxBlock && K >= 32 && K <= kMaxK && K % 32 == 0 && k >= 0 && k <= K && M >= 1 &&
+           M <= kMaxBlock && owq::int8_grid_fits(M, N);
+}
+
+owq_status check_int8_layer(const owq_integer_layer* L, int64_t M, const uint16_t* x, const uint16_t* y, hipStream_t s)
+{
+    if (!L)
+        return fail(OWQ_ERR_NULL, "layer is NULL");
+    if (L->N < 1 || L->N > kMaxBlock)
+        return fail(OWQ_ERR_SHAPE, "N = %lld out of range", (long long)L->N);
+    owq_status st = check_k_dim(L->K);
+    if (st != OWQ_OK)
+        return st;
+    if (M < 1 || M > kMaxBlock)
+        return fail(OWQ_ERR_SHAPE, "M = %lld out of range", (long long)M);
+    if (L->k < 0 || L->k > L->K)
+        return fail(OWQ_ERR_RANGE, "k = %d outside [0, K = %lld]", L->k, (long long)L->K);
+    if (!L->codes || !L->scales || !x || !y)
+        return fail(OWQ_ERR_NULL, "codes, scales, x and y must be non-NULL");
+    if (L->k > 0 && (!L->weak_idx || !L->w_weak))
+        return fail(OWQ_ERR_NULL, "weak_idx and w_weak must be non-NULL when k > 0");
+    if (!aligned(x, 16) || !aligned(L->codes, 16) || !aligned(L->scales, 4) || !aligned(y, 2) ||
+        (L->k > 0 && (!aligned(L->weak_idx, 4) || !aligned(L->w_weak, 2))))
+        return fail(OWQ_ERR_ALIGN, "misaligned pointer (x, codes: 16 B, scales, weak_idx: 4 B, fp16 arrays: 2 B)");
+    if (!owq::int8_grid_fits(M, L->N))
+        return launch_status(hipErrorInvalidConfiguration, "8-bit form");
+    return check_idx_on_host(L->weak_idx, L->k, L->K, s);
+}
+
+owq_status check_apart(const Span& out, const owq_integer_layer* L)
+{
+    const uint64_t N = (uint64_t)L->N, K = (uint64_t)L->K, k = (uint64_t)L->k;
+    return check_apart(out, {{"codes", L->codes, N * K},
+                             {"scales", L->scales, 4 * N},
+                             {"weak_idx", L->weak_idx, 4 * k},
+                             {"w_weak", L->w_weak, 2 * N * k}});
+}
+
+// y and the workspace of a product: large enough, and apart from everything read
+owq_status check_int8_spans(const owq_integer_layer* L, const uint16_t* x, int64_t M, const uint16_t* y, const void* workspace,
+                            size_t need, size_t have)
+{
+    if (need > 0 && !workspace)
+        return fail(OWQ_ERR_NULL, "workspace must be non-NULL above %d tokens", owq::kInt8GemvMaxM);
+    if (need > 0 && !aligned(workspace, 256))
+        return fail(OWQ_ERR_ALIGN, "misaligned pointer (workspace: 256 B)");
+    if (have < need)
+        return fail(OWQ_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", have, need);
+    const Span sx{"x", x, 2 * (uint64_t)M * (uint64_t)L->K}, sy{"y", y, 2 * (uint64_t)M * (uint64_t)L->N};
+    const Span ws{"workspace", workspace, need};
+    owq_status st = check_apart(sy, {sx, ws});
+    st = st != OWQ_OK ? st : check_apart(ws, {sx});
+    for (const Span* out : {&sy, &ws})
+        st = st != OWQ_OK ? st : check_apart(*out, L);
+    return st;
+}
+
+owq::Int8Desc int8_desc(const owq_integer_layer* L, const uint16_t* x, uint16_t* y)
+{
+    return owq::Int8Desc{L->codes, L->scales, L->k > 0 ? L->weak_idx : nullptr, L->k > 0 ? L->w_weak : nullptr, x, y,
+                         L->N, L->K, L->k};
 }
 
 // The two layers of a gated block, its input and an fp16 output.
@@ -1033,8 +1134,8 @@ owq_status owq_clip_grad_norm(const owq_grad* items, int32_t count, double max_n
     owq_status st = OWQ_OK;
     try {
         std::vector<owq::ClipEntry> it((size_t)count);
-        std::vector<std::pair<uintptr_t, uintptr_t>> outs;  // [begin, end) of the non-empty outputs
-        outs.reserve((size_t)count);
+        std::vector<InOut> list;
+        list.reserve((size_t)count);
         for (int32_t i = 0; i < count; i++) {
             const owq_grad& g = items[i];
             if (g.n < 0 || g.n > (int64_t)1 << 40)
@@ -1047,24 +1148,11 @@ owq_status owq_clip_grad_norm(const owq_grad* items, int32_t count, double max_n
             if (g.n > 0 && (!aligned(g.g, size) || !aligned(g.out, size)))
                 return fail(OWQ_ERR_ALIGN, "item %d: misaligned pointer (%zu B)", i, size);
             it[(size_t)i] = owq::ClipEntry{g.g, g.out, g.n, g.type};
-            if (g.n > 0)
-                outs.emplace_back((uintptr_t)g.out, (uintptr_t)g.out + (size_t)g.n * size);
+            list.push_back(InOut{g.g, g.out, (uint64_t)g.n * size});
         }
-        std::sort(outs.begin(), outs.end());
-        for (size_t i = 1; i < outs.size(); i++)
-            if (outs[i].first < outs[i - 1].second)
-                return fail(OWQ_ERR_RANGE, "two outputs overlap (a tensor listed twice?)");
-        for (int32_t i = 0; i < count; i++) {
-            const owq_grad& g = items[i];
-            if (g.n == 0)
-                continue;
-            // the one output that begins in or reaches into [b, e): the last that begins below e
-            const uintptr_t b = (uintptr_t)g.g, e = b + (size_t)g.n * (g.type ? 2 : 4);
-            auto o = std::lower_bound(outs.begin(), outs.end(), std::make_pair(e, (uintptr_t)0));
-            const bool hit = o != outs.begin() && (o - 1)->second > b;
-            if (hit && !(g.out == g.g && (o - 1)->first == b))
-                return fail(OWQ_ERR_RANGE, "item %d: g overlaps an output that is not its own", i);
-        }
+        st = check_list_apart(list);
+        if (st != OWQ_OK)
+            return st;
         const Span sn{"norm", norm, 4}, ws{"workspace", workspace, owq::clip_workspace_bytes(count)};
         st = check_apart(sn, {ws});
         for (int32_t i = 0; i < count && st == OWQ_OK; i++) {
@@ -1081,6 +1169,244 @@ owq_status owq_clip_grad_norm(const owq_grad* items, int32_t count, double max_n
                              "owq_clip_grad_norm launch");
     } catch (const std::exception& ex) {
         return fail(OWQ_ERR_HIP, "owq_clip_grad_norm: host memory: %s", ex.what());
+    }
+}
+
+// ---------------------------------------------------------------- 8-bit form --
+
+owq_status owq_pack_integer(const uint16_t* W, int64_t N, int64_t K, const int32_t* weak_idx, int32_t k, int8_t* codes,
+                         float* scales, uint16_t* w_weak, void* stream)
+{
+    if (N < 1 || !owq::grid_fits(N, 256))
+        return fail(OWQ_ERR_SHAPE, "N = %lld: need 1 <= N < 2^24", (long long)N);
+    owq_status st = check_k_dim(K);
+    if (st != OWQ_OK)
+        return st;
+    if (k < 0 || k > K)
+        return fail(OWQ_ERR_RANGE, "k = %d outside [0, K = %lld]", k, (long long)K);
+    if (!W || !codes || !scales || (k > 0 && (!weak_idx || !w_weak)))
+        return fail(OWQ_ERR_NULL, "W, codes and scales (and weak_idx, w_weak when k > 0) must be non-NULL");
+    if (!aligned(W, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(weak_idx, 4) || !aligned(w_weak, 2))
+        return fail(OWQ_ERR_ALIGN, "misaligned pointer (W, codes: 16 B, scales, weak_idx: 4 B, w_weak: 2 B)");
+    const uint64_t n = (uint64_t)N, nk = n * (uint64_t)K;
+    const Span outs[3] = {{"codes", codes, nk}, {"scales", scales, 4 * n}, {"w_weak", w_weak, 2 * n * (uint64_t)k}};
+    for (int i = 0; i < 3; i++) {
+        st = check_apart(outs[i], {{"W", W, 2 * nk}, {"weak_idx", weak_idx, 4 * (uint64_t)k}, outs[(i + 1) % 3]});
+        if (st != OWQ_OK)
+            return st;
+    }
+    st = check_idx_on_host(weak_idx, k, K, (hipStream_t)stream);
+    if (st != OWQ_OK)
+        return st;
+    return launch_status(owq::launch_pack_int8(W, N, K, weak_idx, k, codes, scales, w_weak, (hipStream_t)stream),
+                         "owq_pack_integer launch");
+}
+
+size_t owq_linear_integer_workspace_bytes(int64_t N, int64_t K, int32_t k, int64_t M)
+{
+    if (!int8_sizes_ok(N, K, k, M))
+        return 0;
+    return owq::int8_plan(N, K, k, M).total;
+}
+
+size_t owq_linear_integer_batched_workspace_bytes(const owq_integer_layer* Ls, int32_t count, int64_t M)
+{
+    if (!Ls || count < 1 || count > 64 || M < 1 || M > owq::kInt8DecodeMaxM)
+        return 0;
+    size_t total = 0;
+    for (int32_t l = 0; l < count; l++) {
+        if (!int8_sizes_ok(Ls[l].N, Ls[l].K, Ls[l].k, M))
+            return 0;
+        total += owq::int8_plan(Ls[l].N, Ls[l].K, Ls[l].k, M).total;
+    }
+    return total;
+}
+
+owq_status owq_linear_integer(const owq_integer_layer* L, const uint16_t* x, int64_t M, uint16_t* y, void* workspace,
+                           size_t workspace_bytes, void* stream)
+{
+    owq_status st = check_int8_layer(L, M, x, y, (hipStream_t)stream);
+    if (st != OWQ_OK)
+        return st;
+    const size_t need = owq::int8_plan(L->N, L->K, L->k, M).total;
+    st = check_int8_spans(L, x, M, y, workspace, need, workspace_bytes);
+    if (st != OWQ_OK)
+        return st;
+    const owq::Int8Desc d = int8_desc(L, x, y);
+    return launch_status(owq::launch_linear_int8(&d, 1, M, &workspace, (hipStream_t)stream), "owq_linear_integer launch");
+}
+
+owq_status owq_linear_integer_batched(const owq_integer_layer* Ls, const uint16_t* const* xs, uint16_t* const* ys,
+                                   int32_t count, int64_t M, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (!Ls || !xs || !ys)
+        return fail(OWQ_ERR_NULL, "Ls, xs and ys must be non-NULL");
+    if (count < 1 || count > 64)
+        return fail(OWQ_ERR_UNSUPPORTED, "count = %d: need 1 <= count <= 64", count);
+    if (M < 1 || M > owq::kInt8DecodeMaxM)
+        return fail(OWQ_ERR_UNSUPPORTED, "M = %lld: the batched launch needs 1 <= M <= %d", (long long)M,
+                    owq::kInt8DecodeMaxM);
+    owq::Int8Desc d[64];
+    void* ws[64];
+    size_t need = 0;
+    for (int32_t l = 0; l < count; l++) {
+        owq_status st = check_int8_layer(&Ls[l], M, xs[l], ys[l], (hipStream_t)stream);
+        if (st != OWQ_OK)
+            return fail_at(st, "layer", l);
+        ws[l] = static_cast<char*>(workspace) + need;
+        need += owq::int8_plan(Ls[l].N, Ls[l].K, Ls[l].k, M).total;
+        d[l] = int8_desc(&Ls[l], xs[l], ys[l]);
+    }
+    for (int32_t l = 0; l < count; l++) {
+        owq_status st = check_int8_spans(&Ls[l], xs[l], M, ys[l], workspace, need, workspace_bytes);
+        // an output also stays apart from the other layers, their inputs and outputs
+        const Span out{"y", ys[l], 2 * (uint64_t)M * (uint64_t)Ls[l].N};
+        for (int32_t o = 0; o < count && st == OWQ_OK; o++) {
+            if (o == l)
+                continue;
+            st = check_apart(out, {{"another x", xs[o], 2 * (uint64_t)M * (uint64_t)Ls[o].K},
+                                   {"another y", ys[o], 2 * (uint64_t)M * (uint64_t)Ls[o].N}});
+            st = st != OWQ_OK ? st : check_apart(out, &Ls[o]);
+        }
+        if (st != OWQ_OK)
+            return fail_at(st, "layer", l);
+    }
+    // the layers of a launch share its grid: every launch is checked before the first
+    for (int32_t l0 = 0; l0 < count; l0 += owq::kInt8MaxLayers) {
+        int64_t rows = 0;
+        for (int32_t l = l0; l < count && l < l0 + owq::kInt8MaxLayers; l++)
+            rows += (Ls[l].N + 15) / 16 * 16;
+        if (!owq::int8_grid_fits(M, rows))
+            return launch_status(hipErrorInvalidConfiguration, "owq_linear_integer_batched launch");
+    }
+    hipError_t e = hipSuccess;
+    for (int32_t l0 = 0; l0 < count && e == hipSuccess; l0 += owq::kInt8MaxLayers) {
+        const int n = count - l0 < owq::kInt8MaxLayers ? count - l0 : owq::kInt8MaxLayers;
+        e = owq::launch_linear_int8(d + l0, n, M, ws + l0, (hipStream_t)stream);
+    }
+    return launch_status(e, "owq_linear_integer_batched launch");
+}
+
+size_t owq_linear_integer_backward_workspace_bytes(int64_t N, int64_t K, int32_t k, int64_t M)
+{
+    if (!int8_sizes_ok(N, K, k, M) || N > owq::kInt8BwdMax || M > owq::kInt8BwdMax)
+        return 0;
+    return owq::int8_bwd_plan(N, K, k, M).total;
+}
+
+owq_status owq_linear_integer_backward(const owq_integer_layer* L, const uint16_t* x, const uint16_t* dy, int64_t M,
+                                    uint16_t* dx, float* dw_weak, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (!L)
+        return fail(OWQ_ERR_NULL, "layer is NULL");
+    const bool need_x = dw_weak && L->k > 0;
+    if (!dy || !workspace || (need_x && !x))
+        return fail(OWQ_ERR_NULL, "dy and workspace (and x for the weak gradient) must be non-NULL");
+    // check_int8_layer wants an x and an output: x is checked below when it is read
+    owq_status st = check_int8_layer(L, M, static_cast<const uint16_t*>(workspace), dy, (hipStream_t)stream);
+    if (st != OWQ_OK)
+        return st;
+    if (M > owq::kInt8BwdMax || L->N > owq::kInt8BwdMax)
+        return fail(OWQ_ERR_SHAPE, "M = %lld, N = %lld: need at most 2^20", (long long)M, (long long)L->N);
+    if (!aligned(dx, 2) || !aligned(dw_weak, 4) || (need_x && !aligned(x, 16)) || !aligned(workspace, 256))
+        return fail(OWQ_ERR_ALIGN, "misaligned pointer (x: 16 B, dw_weak: 4 B, dy, dx: 2 B, workspace: 256 B)");
+    const owq::Int8BwdPlan p = owq::int8_bwd_plan(L->N, L->K, L->k, M);
+    if (workspace_bytes < p.total)
+        return fail(OWQ_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", workspace_bytes, p.total);
+    if (!dx && !need_x) {  // nothing to compute
+        g_err[0] = '\0';
+        return OWQ_OK;
+    }
+    const uint64_t m = (uint64_t)M, N = (uint64_t)L->N, K = (uint64_t)L->K;
+    const Span sx{"x", need_x ? x : nullptr, 2 * m * K}, sdy{"dy", dy, 2 * m * N}, sdx{"dx", dx, 2 * m * K};
+    const Span sdw{"dw_weak", dw_weak, 4 * N * (uint64_t)L->k}, ws{"workspace", workspace, p.total};
+    st = check_apart(sdx, {sx, sdy, sdw, ws});
+    st = st != OWQ_OK ? st : check_apart(sdw, {sx, sdy, ws});
+    st = st != OWQ_OK ? st : check_apart(ws, {sx, sdy});
+    for (const Span* out : {&sdx, &sdw, &ws})
+        st = st != OWQ_OK ? st : check_apart(*out, L);
+    if (st != OWQ_OK)
+        return st;
+    return launch_status(owq::launch_linear_int8_backward(int8_desc(L, x, nullptr), dy, M, dx, need_x ? dw_weak : nullptr,
+                                                          workspace, p, (hipStream_t)stream),
+                         "owq_linear_integer_backward launch");
+}
+
+// ------------------------------------------------------- orthogonalised update --
+
+size_t owq_orthogonalize_workspace_bytes(const owq_update* items, int32_t count)
+{
+    if (!items || count < 1 || count > kMaxGrads)
+        return 0;
+    try {
+        std::vector<owq::OrthoEntry> it((size_t)count);
+        for (int32_t i = 0; i < count; i++) {
+            if (items[i].rows < 0 || items[i].cols < 0 || !owq::orthogonalize_fits(items[i].rows, items[i].cols))
+                return 0;
+            it[(size_t)i].rows = items[i].rows;
+            it[(size_t)i].cols = items[i].cols;
+        }
+        return owq::orthogonalize_workspace_bytes(it.data(), count);
+    } catch (const std::exception&) {
+        return 0;
+    }
+}
+
+owq_status owq_orthogonalize(const owq_update* items, int32_t count, int32_t steps, const double* coefficients,
+                             double eps, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (!items || !coefficients || !workspace)
+        return fail(OWQ_ERR_NULL, "items, coefficients and workspace must be non-NULL");
+    if (count < 1 || count > kMaxGrads)
+        return fail(OWQ_ERR_UNSUPPORTED, "count = %d: need 1 <= count <= %d", count, kMaxGrads);
+    if (steps < 1 || steps > kMaxNsSteps)
+        return fail(OWQ_ERR_RANGE, "steps = %d: need 1 <= steps <= %d", steps, kMaxNsSteps);
+    for (int i = 0; i < 3; i++)
+        if (!std::isfinite(coefficients[i]))
+            return fail(OWQ_ERR_RANGE, "coefficient %d is not finite", i);
+    if (!(eps > 0.0) || !std::isfinite(eps))
+        return fail(OWQ_ERR_RANGE, "eps = %g: need a finite eps > 0", eps);
+    if (!aligned(workspace, 256))
+        return fail(OWQ_ERR_ALIGN, "misaligned pointer (workspace: 256 B)");
+    try {
+        std::vector<owq::OrthoEntry> it((size_t)count);
+        std::vector<InOut> list;
+        list.reserve((size_t)count);
+        for (int32_t i = 0; i < count; i++) {
+            const owq_update& u = items[i];
+            if (u.rows < 0 || u.cols < 0 || !owq::orthogonalize_fits(u.rows, u.cols))
+                return fail(OWQ_ERR_SHAPE, "item %d: %lld x %lld: need at most 2^20 and, for the shorter side, %lld", i,
+                            (long long)u.rows, (long long)u.cols, (long long)owq::kOrthoMaxShort);
+            if (u.type != 0 && u.type != 1)
+                return fail(OWQ_ERR_UNSUPPORTED, "item %d: type = %d: need 0 (fp32) or 1 (fp16)", i, u.type);
+            if (!std::isfinite(u.scale))
+                return fail(OWQ_ERR_RANGE, "item %d: the scale is not finite", i);
+            const uint64_t n = (uint64_t)u.rows * (uint64_t)u.cols, size = u.type ? 2 : 4;
+            if (n > 0 && (!u.g || !u.out))
+                return fail(OWQ_ERR_NULL, "item %d: g and out must be non-NULL", i);
+            if (n > 0 && (!aligned(u.g, size) || !aligned(u.out, size)))
+                return fail(OWQ_ERR_ALIGN, "item %d: misaligned pointer (%d B)", i, (int)size);
+            it[(size_t)i] = owq::OrthoEntry{u.g, u.out, u.rows, u.cols, u.scale, u.type};
+            list.push_back(InOut{u.g, u.out, n * size});
+        }
+        const size_t need = owq::orthogonalize_workspace_bytes(it.data(), count);
+        if (workspace_bytes < need)
+            return fail(OWQ_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", workspace_bytes, need);
+        owq_status st = check_list_apart(list);
+        const Span ws{"workspace", workspace, need};
+        for (int32_t i = 0; i < count && st == OWQ_OK; i++) {
+            const InOut& t = list[(size_t)i];
+            st = check_apart(ws, {{"a matrix", t.g, t.bytes}, {"an output", t.out, t.bytes}});
+            if (st != OWQ_OK)
+                return fail_at(st, "item", i);
+        }
+        if (st != OWQ_OK)
+            return st;
+        return launch_status(owq::launch_orthogonalize(it.data(), count, coefficients[0], coefficients[1], coefficients[2],
+                                                       eps, steps, workspace, (hipStream_t)stream),
+                             "owq_orthogonalize launch");
+    } catch (const std::exception& ex) {
+        return fail(OWQ_ERR_HIP, "owq_orthogonalize: host memory: %s", ex.what());
     }
 }
 

@@ -225,6 +225,59 @@ constexpr int kClipItems = 240;  // tensors per launch (kernel arguments below 4
 size_t clip_workspace_bytes(int count);
 hipError_t launch_clip(const ClipEntry* items, int count, double max_norm, float* norm, void* ws, hipStream_t s);
 
+// ----------------------------------------------------------------- 8-bit form --
+struct Int8Desc {
+    const int8_t* q;      // [N][K]
+    const float* s;       // [N]
+    const int32_t* idx;   // [k] (NULL iff k == 0)
+    const uint16_t* ww;   // [N][k]
+    const uint16_t* x;
+    uint16_t* y;
+    int64_t N, K;
+    int32_t k;
+};
+constexpr int kInt8MaxLayers = 16;   // layers per launch
+constexpr int kInt8GemvMaxM = 4;     // tokens quantised by every block for itself
+constexpr int kInt8DecodeMaxM = 16;  // tokens of one B tile
+// Workspace of one layer at M tokens: their codes (Kq columns), scales, weak columns
+// padded to kp
+struct Int8Plan {
+    int64_t Kq;
+    int32_t kp;
+    size_t off_sx, off_xw, total;
+};
+Int8Plan int8_plan(int64_t N, int64_t K, int32_t k, int64_t M);
+bool int8_grid_fits(int64_t M, int64_t N);  // one layer of N rows at M tokens
+hipError_t launch_pack_int8(const uint16_t* W, int64_t N, int64_t K, const int32_t* idx, int32_t k, int8_t* codes,
+                            float* scales, uint16_t* ww, hipStream_t s);
+// count <= kInt8MaxLayers, and 1 above kInt8DecodeMaxM tokens; ws[l]: layer l's workspace
+hipError_t launch_linear_int8(const Int8Desc* d, int count, int64_t M, void* const* ws, hipStream_t s);
+
+// Its backward: padded sizes, row slices of the weak columns' part of dx, workspace offsets
+struct Int8BwdPlan {
+    int64_t Np, Mp, kp, slices;
+    size_t off_un, off_wwt, off_xwt, off_part, total;
+};
+constexpr int64_t kInt8BwdMax = (int64_t)1 << 20;  // tokens and rows
+Int8BwdPlan int8_bwd_plan(int64_t N, int64_t K, int32_t k, int64_t M);
+// dx (fp16 [M][K]) and dw (fp32 [N][k]), each may be NULL; d.y unused
+hipError_t launch_linear_int8_backward(const Int8Desc& d, const uint16_t* dy, int64_t M, uint16_t* dx, float* dw,
+                                       void* ws, const Int8BwdPlan& p, hipStream_t s);
+
+// --------------------------------------------------------- orthogonalised update --
+struct OrthoEntry {
+    const void* g;
+    void* out;       // == g: in place
+    int64_t rows, cols;
+    float scale;
+    int32_t half;    // 1: fp16, 0: fp32
+};
+constexpr int64_t kOrthoMaxLong = (int64_t)1 << 20, kOrthoMaxShort = 16384;
+bool orthogonalize_fits(int64_t rows, int64_t cols);
+size_t orthogonalize_workspace_bytes(const OrthoEntry* items, int count);
+hipError_t launch_orthogonalize(const OrthoEntry* items, int count, double a, double b, double c, double eps, int steps,
+                                void* ws, hipStream_t s);
+
 // read-only streaming reference (stream.hip): one word per 4608-byte wavefront
 int64_t stream_read_sink_words(int64_t bytes);
 hipError_t launch_stream_read(const void* src, int64_t bytes, uint32_t* sink, hipStream_t s);

@@ -61,6 +61,16 @@ class OwqGrad(ctypes.Structure):
     _fields_ = [("g", _P), ("out", _P), ("n", _I64), ("type", _I32)]
 
 
+class OwqIntegerLayer(ctypes.Structure):
+    """Mirror of ``owq_integer_layer`` (host struct, device pointers)."""
+    _fields_ = [("N", _I64), ("K", _I64), ("k", _I32), ("codes", _P), ("scales", _P), ("weak_idx", _P), ("w_weak", _P)]
+
+
+class OwqUpdate(ctypes.Structure):
+    """Mirror of ``owq_update`` (host struct, device pointers)."""
+    _fields_ = [("g", _P), ("out", _P), ("rows", _I64), ("cols", _I64), ("scale", ctypes.c_float), ("type", _I32)]
+
+
 EXPORTS = {
     "owq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "owq_last_error": (ctypes.c_char_p, []),
@@ -108,6 +118,18 @@ EXPORTS = {
     "owq_clip_grad_norm_workspace_bytes": (ctypes.c_size_t, [_I32]),
     "owq_clip_grad_norm": (ctypes.c_int, [ctypes.POINTER(OwqGrad), _I32, ctypes.c_double, _P, _P, ctypes.c_size_t,
                                           _P]),
+    "owq_pack_integer": (ctypes.c_int, [_P, _I64, _I64, _P, _I32, _P, _P, _P, _P]),
+    "owq_linear_integer_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I32, _I64]),
+    "owq_linear_integer": (ctypes.c_int, [ctypes.POINTER(OwqIntegerLayer), _P, _I64, _P, _P, ctypes.c_size_t, _P]),
+    "owq_linear_integer_batched_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(OwqIntegerLayer), _I32, _I64]),
+    "owq_linear_integer_batched": (ctypes.c_int, [ctypes.POINTER(OwqIntegerLayer), ctypes.POINTER(_P),
+                                                  ctypes.POINTER(_P), _I32, _I64, _P, ctypes.c_size_t, _P]),
+    "owq_linear_integer_backward_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I32, _I64]),
+    "owq_linear_integer_backward": (ctypes.c_int, [ctypes.POINTER(OwqIntegerLayer), _P, _P, _I64, _P, _P, _P,
+                                                   ctypes.c_size_t, _P]),
+    "owq_orthogonalize_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(OwqUpdate), _I32]),
+    "owq_orthogonalize": (ctypes.c_int, [ctypes.POINTER(OwqUpdate), _I32, _I32, ctypes.POINTER(ctypes.c_double),
+                                         ctypes.c_double, _P, ctypes.c_size_t, _P]),
     "owq_stream_read_sink_words": (_I64, [_I64]),
     "owq_stream_read": (ctypes.c_int, [_P, _I64, _P, _I64, _P]),
 }
@@ -1219,6 +1241,257 @@ def clip_grad_norm(grads: list, max_norm: float, outs: list | None = None, norm:
         _check(lib().owq_clip_grad_norm(table, n, max_norm, norm.data_ptr(),
                                         workspace.data_ptr(), workspace.numel(), run.handle), "owq_clip_grad_norm")
     return norm
+
+
+# --------------------------------------------------------------- integer form
+
+_INTEGER = ("codes", "scales", "w_weak", "weak_idx")
+
+
+def pack_integer(W: torch.Tensor, weak_idx: torch.Tensor, out: dict | None = None, stream=None) -> dict:
+    """Layer in the integer form (owq_pack_integer) of fp16 W [N][K]: codes int8
+    [N][K], scales fp32 [N], w_weak fp16 [N][k], weak_idx. out: a layer dict to write."""
+    _meta(W, torch.float16, "W")
+    _meta(weak_idx, torch.int32, "weak_idx")
+    if W.dim() != 2 or weak_idx.dim() != 1:
+        raise ValueError(f"W must be 2-D and weak_idx 1-D, got {tuple(W.shape)} and {tuple(weak_idx.shape)}")
+    N, K = W.shape
+    k = weak_idx.numel()
+    if K % 32 or k > K:
+        raise ValueError(f"K = {K} must be a multiple of 32 and k = {k} at most K")
+    want = {"codes": ((N, K), torch.int8), "scales": ((N,), torch.float32), "w_weak": ((N, k), torch.float16)}
+    if out is not None:
+        for name, (shape, dt) in want.items():
+            if name not in out:
+                raise ValueError(f"out lacks {name!r}")
+            _meta(out[name], dt, f"out[{name!r}]", shape)
+    _on_device(("W", W), ("weak_idx", weak_idx), *[(f"out[{n!r}]", out[n]) for n in (want if out else ())])
+    with _Launch(W.get_device(), stream) as run:
+        if out is None:
+            out = {name: run.empty(shape, dt) for name, (shape, dt) in want.items()}
+        _check(lib().owq_pack_integer(W.data_ptr(), N, K, _ptr(weak_idx) if k else None, k, out["codes"].data_ptr(),
+                                      out["scales"].data_ptr(), _ptr(out["w_weak"]) if k else None, run.handle),
+               "owq_pack_integer")
+    out["weak_idx"] = weak_idx
+    return out
+
+
+def _integer_layer(layer: dict, tag: str = ""):
+    """(OwqIntegerLayer, GPU index) of a checked layer dict of the integer form."""
+    try:
+        q, s, w, idx = layer["codes"], layer["scales"], layer["w_weak"], layer["weak_idx"]
+        N, K = q.shape
+        k, = idx.shape
+        dev = q.get_device()
+        if (dev >= 0 and K % 32 == 0 and s.shape == (N,) and w.shape == (N, k) and q.dtype is torch.int8
+                and s.dtype is torch.float32 and w.dtype is torch.float16 and idx.dtype is torch.int32
+                and q.is_contiguous() and s.is_contiguous() and w.is_contiguous() and idx.is_contiguous()
+                and s.get_device() == dev and w.get_device() == dev and idx.get_device() == dev):
+            return OwqIntegerLayer(N, K, k, q.data_ptr(), s.data_ptr(), idx.data_ptr() if k else None,
+                                   w.data_ptr() if k else None), dev
+    except (KeyError, AttributeError, ValueError, TypeError):
+        pass
+    # something is wrong: say what
+    for name in _INTEGER:
+        if name not in layer:
+            raise ValueError(f"{tag}layer lacks {name!r} (integer form: {', '.join(_INTEGER)})")
+    q = _meta(layer["codes"], torch.int8, f"{tag}codes")
+    idx = _meta(layer["weak_idx"], torch.int32, f"{tag}weak_idx")
+    if q.dim() != 2 or q.shape[1] % 32 or idx.dim() != 1:
+        raise ValueError(f"{tag}codes must be [N][K], K a multiple of 32, and weak_idx 1-D, got {tuple(q.shape)} and "
+                         f"{tuple(idx.shape)}")
+    _meta(layer["scales"], torch.float32, f"{tag}scales", (q.shape[0],))
+    _meta(layer["w_weak"], torch.float16, f"{tag}w_weak", (q.shape[0], idx.numel()))
+    _on_device(*[(tag + n, layer[n]) for n in _INTEGER])
+    raise ValueError(f"{tag}not a layer of the integer form")
+
+
+def _integer_sizes(layer: dict, tag: str = ""):
+    """(N, K) of a layer dict, for the checks of shapes that come before those of devices."""
+    q = layer.get("codes")
+    if not isinstance(q, torch.Tensor) or q.dim() != 2:
+        _integer_layer(layer, tag)
+    return q.shape
+
+
+def linear_integer_workspace_bytes(N: int, K: int, k: int, M: int) -> int:
+    return int(lib().owq_linear_integer_workspace_bytes(N, K, k, M))
+
+
+def linear_integer(layer: dict, x: torch.Tensor, y: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y = x W^T (fp16 [M][N]) for a layer in the integer form (owq_linear_integer): the
+    tokens' dense columns are rounded to 8 bits with a scale per token, the products of
+    codes are summed in integers, the weak columns multiply in fp16."""
+    N, K = _integer_sizes(layer)
+    M = _xy_shapes(N, K, x, y)
+    if workspace is not None:
+        _meta(workspace, torch.uint8, "workspace")
+    L, dev = _integer_layer(layer)
+    _same_device(dev, ("x", x), ("y", y), ("workspace", workspace))
+    with _Launch(dev, stream) as run:
+        if y is None:
+            y = run.empty((M, N), torch.float16)
+        if workspace is None:
+            need = linear_integer_workspace_bytes(N, K, L.k, M)
+            workspace = run.empty(need, torch.uint8) if need else None
+        _check(lib().owq_linear_integer(ctypes.byref(L), x.data_ptr(), M, y.data_ptr(), _ptr(workspace),
+                                        0 if workspace is None else workspace.numel(), run.handle), "owq_linear_integer")
+    return y
+
+
+def linear_integer_batched_workspace_bytes(shapes: list, M: int) -> int:
+    """Workspace of linear_integer_batched for (N, K, k) per layer."""
+    n = len(shapes)
+    Ls = (OwqIntegerLayer * max(n, 1))(*[OwqIntegerLayer(N, K, k, None, None, None, None) for N, K, k in shapes])
+    return int(lib().owq_linear_integer_batched_workspace_bytes(Ls, n, M))
+
+
+def linear_integer_batched(layers: list, xs: list, ys: list | None = None, workspace: torch.Tensor | None = None,
+                           stream=None) -> list:
+    """linear_integer of several layers on the same number of tokens (1 <= M <= 16)
+    in one launch, two above 4 tokens (owq_linear_integer_batched)."""
+    n = len(layers)
+    if n < 1 or len(xs) != n or (ys is not None and len(ys) != n):
+        raise ValueError(f"need as many x (and y) as layers: {n} layers, {len(xs)} x"
+                         + ("" if ys is None else f", {len(ys)} y"))
+    M = None
+    for i, layer in enumerate(layers):
+        N, K = _integer_sizes(layer, f"[{i}] ")
+        M = _xy_shapes(N, K, xs[i], None if ys is None else ys[i], f"[{i}] ", M)
+    if workspace is not None:
+        _meta(workspace, torch.uint8, "workspace")
+    checked = [_integer_layer(layer, f"[{i}] ") for i, layer in enumerate(layers)]
+    dev = checked[0][1]
+    for i, (_, d) in enumerate(checked):
+        if d != dev:
+            raise ValueError(f"arguments are on different devices: layer {i} is on cuda:{d}, the first on cuda:{dev}")
+        _same_device(dev, (f"[{i}] x", xs[i]), (f"[{i}] y", None if ys is None else ys[i]))
+    _same_device(dev, ("workspace", workspace))
+    Ls = (OwqIntegerLayer * n)(*[L for L, _ in checked])
+    with _Launch(dev, stream) as run:
+        if ys is None:
+            ys = [run.empty((M, L.N), torch.float16) for L, _ in checked]
+        if workspace is None:
+            need = int(lib().owq_linear_integer_batched_workspace_bytes(Ls, n, M))
+            workspace = run.empty(need, torch.uint8) if need else None
+        xp = (_P * n)(*[x.data_ptr() for x in xs])
+        yp = (_P * n)(*[y.data_ptr() for y in ys])
+        _check(lib().owq_linear_integer_batched(Ls, xp, yp, n, M, _ptr(workspace),
+                                                0 if workspace is None else workspace.numel(), run.handle),
+               "owq_linear_integer_batched")
+    return ys
+
+
+def linear_integer_backward_workspace_bytes(N: int, K: int, k: int, M: int) -> int:
+    return int(lib().owq_linear_integer_backward_workspace_bytes(N, K, k, M))
+
+
+def linear_integer_backward(layer: dict, x: torch.Tensor | None, dy: torch.Tensor, want_dx: bool = True,
+                            want_dw: bool = True, workspace: torch.Tensor | None = None, stream=None):
+    """Weak-column-tuning backward of linear_integer (owq_linear_integer_backward): (dx
+    fp16 [M][K] or None, dw_weak fp32 [N][k] or None) for the upstream gradient dy fp16
+    [M][N]; the tokens' rounding to 8 bits passes gradients as the identity does. x is
+    needed for dw_weak."""
+    N, K = _integer_sizes(layer)
+    _meta(dy, torch.float16, "dy")
+    if dy.dim() != 2 or dy.shape[1] != N or dy.shape[0] < 1:
+        raise ValueError(f"dy has shape {tuple(dy.shape)}, expected (M, {N})")
+    M = dy.shape[0]
+    if x is not None:
+        _xy_shapes(N, K, x, None, M=M)
+    if workspace is not None:
+        _meta(workspace, torch.uint8, "workspace")
+    L, dev = _integer_layer(layer)
+    if want_dw and L.k and x is None:
+        raise ValueError("x is needed for dw_weak")
+    _same_device(dev, ("x", x), ("dy", dy), ("workspace", workspace))
+    with _Launch(dev, stream) as run:
+        dx = run.empty((M, K), torch.float16) if want_dx else None
+        dw = run.empty((N, L.k), torch.float32) if want_dw else None
+        if workspace is None:
+            workspace = run.empty(max(linear_integer_backward_workspace_bytes(N, K, L.k, M), 256), torch.uint8)
+        _check(lib().owq_linear_integer_backward(ctypes.byref(L), _ptr(x), dy.data_ptr(), M, _ptr(dx),
+                                                 _ptr(dw) if L.k else None, workspace.data_ptr(), workspace.numel(),
+                                                 run.handle), "owq_linear_integer_backward")
+    return dx, dw
+
+
+# --------------------------------------------------------- orthogonalised update
+
+# (a, b, c) of the quintic: lifts small singular values fastest and ends between 0.7 and 1.2
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
+
+
+def orthogonalize_workspace_bytes(shapes: list) -> int:
+    """Workspace of orthogonalize for matrices of these (rows, cols)."""
+    n = len(shapes)
+    items = (OwqUpdate * max(n, 1))(*[OwqUpdate(None, None, r, c, 1.0, 0) for r, c in shapes])
+    return int(lib().owq_orthogonalize_workspace_bytes(items, n))
+
+
+def _updates_checked(updates: list, outs):
+    """Raise for the first matrix or out that orthogonalize does not take."""
+    for i, t in enumerate(updates):
+        if isinstance(t, torch.Tensor) and t.dtype not in _GRAD_TYPES:
+            raise TypeError(f"[{i}] matrix must be torch.float32 or torch.float16, got {t.dtype}")
+        _meta(t, getattr(t, "dtype", None), f"[{i}] matrix")
+        if t.dim() != 2:
+            raise ValueError(f"[{i}] matrix must be 2-D, got {tuple(t.shape)}")
+        if outs is not None:
+            _meta(outs[i], t.dtype, f"[{i}] out", tuple(t.shape))
+
+
+def orthogonalize(updates: list, outs: list | None = None, scales: list | None = None, steps: int = 5,
+                  coefficients: tuple = NEWTON_SCHULZ, eps: float = 1e-7, workspace: torch.Tensor | None = None,
+                  stream=None) -> list:
+    """Each matrix (fp32 or fp16, 2-D, contiguous, e.g. the weak columns' gradients after
+    clip_grad_norm) replaced by scale times a nearly orthogonal factor of itself
+    (owq_orthogonalize): X = g / (|g| + eps), then `steps` times X <- a X + b (X X^T) X +
+    c (X X^T)^2 X with coefficients (a, b, c). In place or into outs; scales: one number
+    per matrix (default 1). Returns the list of results."""
+    n = len(updates)
+    if n < 1 or n > 4096:
+        raise ValueError(f"need 1 to 4096 matrices, got {n}")
+    for name, other in (("out", outs), ("scale", scales)):
+        if other is not None and len(other) != n:
+            raise ValueError(f"need one {name} per matrix: {n} matrices, {len(other)} {name}s")
+    if len(coefficients) != 3:
+        raise ValueError(f"need three coefficients, got {len(coefficients)}")
+    # hundreds of matrices: checked by whole-list calls, and one by one (for the message)
+    # only when something is wrong
+    T = torch.Tensor
+    every = list(updates) if outs is None else list(updates) + list(outs)
+    if set(map(type, every)) <= _TENSORS or all([isinstance(t, T) for t in every]):
+        types = [t.dtype for t in every]
+        shapes = [t.shape for t in every]
+        good = (all(map(T.is_contiguous, every)) and set(types) <= _GRAD_TYPES.keys() and set(map(len, shapes)) == {2}
+                and types[n:] == types[:len(types) - n] and shapes[n:] == shapes[:len(shapes) - n])
+    else:
+        good = False
+    if not good:
+        _updates_checked(updates, outs)
+    if workspace is not None:
+        _meta(workspace, torch.uint8, "workspace")
+    devs = set(map(T.get_device, every)) | ({workspace.get_device()} if workspace is not None else set())
+    if len(devs) != 1 or -1 in devs:
+        _on_device(("workspace", workspace), *[(f"[{i % n}] {'out' if i >= n else 'matrix'}", t)
+                                               for i, t in enumerate(every)])
+    with _Launch(devs.pop(), stream) as run:
+        ptrs = list(map(T.data_ptr, every))
+        # one owq_update is five 64-bit words: scale in the low half of the last, type in the high
+        kinds = map(_GRAD_TYPES.__getitem__, types)
+        halves = array.array("f", [1.0] * n if scales is None else scales)
+        low = memoryview(halves).cast("B").cast("I")
+        words = array.array("q", chain.from_iterable(
+            (p, o, s[0], s[1], (k << 32) | b)
+            for p, o, s, k, b in zip(ptrs[:n], ptrs[-n:], shapes, kinds, low)))
+        table = (OwqUpdate * n).from_buffer(words)
+        if workspace is None:
+            workspace = run.empty(max(int(lib().owq_orthogonalize_workspace_bytes(table, n)), 256), torch.uint8)
+        _check(lib().owq_orthogonalize(table, n, int(steps), (ctypes.c_double * 3)(*coefficients), float(eps),
+                                       workspace.data_ptr(), workspace.numel(), run.handle), "owq_orthogonalize")
+    return list(updates) if outs is None else list(outs)
 
 
 # ----------------------------------------------------------- measurement aid
