@@ -1211,7 +1211,7 @@ size_t owq_linear_integer_workspace_bytes(int64_t N, int64_t K, int32_t k, int64
 
 size_t owq_linear_integer_batched_workspace_bytes(const owq_integer_layer* Ls, int32_t count, int64_t M)
 {
-    if (!Ls || count < 1 || count > 64 || M < 1 || M > owq::kInt8DecodeMaxM)
+    if (!Ls || count < 1 || count > 64 || M < 1 || M > owq::kInt8BatchMaxM)
         return 0;
     size_t total = 0;
     for (int32_t l = 0; l < count; l++) {
@@ -1243,9 +1243,9 @@ owq_status owq_linear_integer_batched(const owq_integer_layer* Ls, const uint16_
         return fail(OWQ_ERR_NULL, "Ls, xs and ys must be non-NULL");
     if (count < 1 || count > 64)
         return fail(OWQ_ERR_UNSUPPORTED, "count = %d: need 1 <= count <= 64", count);
-    if (M < 1 || M > owq::kInt8DecodeMaxM)
+    if (M < 1 || M > owq::kInt8BatchMaxM)
         return fail(OWQ_ERR_UNSUPPORTED, "M = %lld: the batched launch needs 1 <= M <= %d", (long long)M,
-                    owq::kInt8DecodeMaxM);
+                    owq::kInt8BatchMaxM);
     owq::Int8Desc d[64];
     void* ws[64];
     size_t need = 0;

@@ -14,22 +14,21 @@ namespace {
 // -------------------------------------------------------------------- pack --
 
 // One block per row: the largest dense magnitude, then the codes and the weak weights.
-// Compiled like the rest of the file with FMA contraction: code8 has no sum to contract.
+template <bool WIDE>
 __global__ __launch_bounds__(256) void k_pack_int8(const uint16_t* __restrict__ W, int K, const int32_t* __restrict__ idx,
                                                    int k, int8_t* __restrict__ codes, float* __restrict__ scales,
                                                    uint16_t* __restrict__ ww)
 {
-    __shared__ uint32_t mask[65536 / 32];
+    __shared__ DenseMask<WIDE> mask;
     __shared__ uint32_t red[4];
     const int tid = threadIdx.x;
     const int64_t row = blockIdx.x;
     const uint4* w = reinterpret_cast<const uint4*>(W + row * K);
-    weak_mask<256>(mask, idx, k, K);
-    const uint8_t* m8 = reinterpret_cast<const uint8_t*>(mask);
+    mask.template fill<256>(idx, k, K);
     uint32_t top = 0;
     for (int p = tid; p < K >> 3; p += 256)
-        top = top8(w[p], m8[p], top);
-    top = wave_max_u32(top);
+        top = mask.top(w[p], p, top);
+    top = wave_max_u32(mask.both(top));
     if ((tid & 63) == 0)
         red[tid >> 6] = top;
     __syncthreads();
@@ -39,21 +38,12 @@ __global__ __launch_bounds__(256) void k_pack_int8(const uint16_t* __restrict__ 
     uint2* q = reinterpret_cast<uint2*>(codes + row * K);
     for (int p = tid; p < K >> 3; p += 256) {
         const uint4 v = w[p];
-        uint2 c = make_uint2(code8x4(v.x, v.y, rs.factor), code8x4(v.z, v.w, rs.factor));
-        const uint32_t b = m8[p];
-        if (b) {
-            uint32_t keep[2];
+        uint32_t c[2] = {code8x4(v.x, v.y, rs.factor), code8x4(v.z, v.w, rs.factor)};
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-                keep[h] = 0;
-#pragma unroll
-                for (int e = 0; e < 4; e++)
-                    keep[h] |= (b >> (4 * h + e)) & 1u ? 0u : 0xffu << (8 * e);
-            }
-            c.x &= keep[0];
-            c.y &= keep[1];
-        }
-        q[p] = c;
+        for (int e = 0; e < 8; e++)
+            if (mask.weak(8 * p + e))
+                c[e >> 2] &= ~(0xffu << (8 * (e & 3)));
+        q[p] = make_uint2(c[0], c[1]);
     }
     for (int c = tid; c < k; c += 256) {
         const int j = idx[c];
@@ -61,60 +51,163 @@ __global__ __launch_bounds__(256) void k_pack_int8(const uint16_t* __restrict__ 
     }
 }
 
+// The tiled product's sizes
+constexpr int kGemmCols = 64;     // columns per stage
+constexpr int kGemmTokens = 256;  // tokens per tile, and per panel of their codes
+constexpr int kWeakPanel = 128;   // rows per panel of the weak weights: a small tile's
+constexpr int kSumVectors = 256 * 128 / 4;  // four sums each: of a small tile
+
 // ---------------------------------------------------------------- the tokens --
 
 struct QuantLayer {
     const uint16_t* x;
     const int32_t* idx;
+    const uint16_t* ww;
     int8_t* x8;
     float* sx;
     uint16_t* xw;
-    int32_t K, Kq, k, kp;
+    uint16_t* wwp;
+    int32_t N, K, Kq, k, kp;
 };
 struct QuantBatch {
     QuantLayer L[kInt8MaxLayers];
 };
 
-// One block per token (and layer, blockIdx.y): its scale, its codes up to Kq columns
-// (zeros past K) and its weak columns padded to kp with zeros. OPERAND: the codes in the
-// order of the decode's B operand (64-column steps, lane 16 g + m holds the 16 columns
-// g of token m); else row-major [M][Kq].
-template <bool OPERAND>
+// Byte of the 16-byte piece p of a row in the panel layout: panels of `rows` rows, 64
+// bytes of each row together (a stage of the tiled product; rows K bytes apart would
+// keep the loads to 64-byte pieces all over the matrix).
+__device__ __forceinline__ int64_t panel_at(int64_t row, int rows, int64_t row_bytes, int p)
+{
+    const int64_t panel = row / rows;
+    return panel * rows * row_bytes + ((int64_t)(p >> 2) * rows + (row - panel * rows)) * 64 + (p & 3) * 16;
+}
+
+// The tokens of the streaming product: one block per token and layer (blockIdx.y), its
+// scale, its codes up to Kq columns (zeros past K) and its weak columns padded to kp with
+// zeros. The codes go in the order of that product's B operand (16 tokens together,
+// 64-column steps, lane 16 g + m holds the 16 columns g of token m). P: 16-column pieces a
+// thread holds (longer rows are read twice).
+template <bool WIDE, int P>
 __global__ __launch_bounds__(256) void k_int8_tokens(const QuantBatch b)
 {
-    __shared__ uint32_t mask[65536 / 32];
+    __shared__ DenseMask<WIDE> mask;
     __shared__ uint32_t red[4];
     const QuantLayer& L = b.L[blockIdx.y];
     const int tid = threadIdx.x;
+    const int K = L.K, kp = L.kp;
     const int64_t m = blockIdx.x;
-    const int K = L.K;
     const uint16_t* xr = L.x + m * K;
     const uint4* xp = reinterpret_cast<const uint4*>(xr);
-    weak_mask<256>(mask, L.idx, L.k, K);
-    const uint8_t* m8 = reinterpret_cast<const uint8_t*>(mask);
+    const int pieces = K >> 4;
+    uint4 v[P][2];
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+        const int p = tid + 256 * i;
+        if (p < pieces) {
+            v[i][0] = xp[2 * p];
+            v[i][1] = xp[2 * p + 1];
+        }
+    }
+    mask.template fill<256>(L.idx, L.k, K);
     uint32_t top = 0;
-    for (int p = tid; p < K >> 3; p += 256)
-        top = top8(xp[p], m8[p], top);
-    top = wave_max_u32(top);
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+        const int p = tid + 256 * i;
+        if (p < pieces) {
+            top = mask.top(v[i][0], 2 * p, mask.top(v[i][1], 2 * p + 1, top));
+        }
+    }
+    for (int p = tid + 256 * P; p < pieces; p += 256)
+        top = mask.top(xp[2 * p], 2 * p, mask.top(xp[2 * p + 1], 2 * p + 1, top));
+    top = wave_max_u32(mask.both(top));
     if ((tid & 63) == 0)
         red[tid >> 6] = top;
     __syncthreads();
     const RowScale rs = row_scale(max(max(red[0], red[1]), max(red[2], red[3])));
     if (tid == 0)
         L.sx[m] = rs.scale;
-    for (int p = tid; p < L.Kq >> 4; p += 256) {  // 16 columns, K is a multiple of 32
-        uint4 c = make_uint4(0u, 0u, 0u, 0u);
-        if (p < K >> 4) {
-            const uint4 v = xp[2 * p], w = xp[2 * p + 1];
-            c = make_uint4(code8x4(v.x, v.y, rs.factor), code8x4(v.z, v.w, rs.factor), code8x4(w.x, w.y, rs.factor),
-                           code8x4(w.z, w.w, rs.factor));
-        }
-        const int64_t at = OPERAND ? (int64_t)(p >> 2) * 1024 + (p & 3) * 256 + m * 16 : m * L.Kq + (int64_t)p * 16;
-        *reinterpret_cast<uint4*>(L.x8 + at) = c;
+    int8_t* x8 = L.x8 + (m >> 4) * 16 * L.Kq + (m & 15) * 16;
+    auto put = [&](int p, uint4 c) { *reinterpret_cast<uint4*>(x8 + (int64_t)(p >> 2) * 1024 + (p & 3) * 256) = c; };
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+        const int p = tid + 256 * i;
+        if (p < pieces)
+            put(p, code8x16(v[i][0], v[i][1], rs.factor));
     }
-    for (int c = tid; c < L.kp; c += 256) {
+    for (int p = tid + 256 * P; p < pieces; p += 256)
+        put(p, code8x16(xp[2 * p], xp[2 * p + 1], rs.factor));
+    for (int p = pieces + tid; p < L.Kq >> 4; p += 256)
+        put(p, make_uint4(0u, 0u, 0u, 0u));
+    for (int c = tid; c < kp; c += 256) {
         const int j = c < L.k ? L.idx[c] : -1;
-        L.xw[m * L.kp + c] = j >= 0 && j < K ? xr[j] : (uint16_t)0;
+        L.xw[m * kp + c] = j >= 0 && j < K ? xr[j] : (uint16_t)0;
+    }
+}
+
+// The tokens of the tiled product: a wave per token, which holds P pieces of 16 columns per
+// lane, so that only the mask of the weak columns is shared (one barrier). Codes and weak
+// columns go in panels, and the blocks past the tokens lay the layer's weak weights out
+// alike.
+template <bool WIDE, int P>
+__global__ __launch_bounds__(256) void k_int8_token_panels(const QuantLayer L, int M)
+{
+    __shared__ DenseMask<WIDE> mask;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int K = L.K, kp = L.kp;
+    const int rows = (M + 3) >> 2;  // blocks of tokens
+    if ((int)blockIdx.x >= rows) {
+        const PairLayer pl{nullptr, nullptr, nullptr, nullptr, L.ww, L.k};
+        for (int64_t u = (int64_t)((int)blockIdx.x - rows) * 256 + tid; u < (int64_t)L.N * (kp >> 3);
+             u += (int64_t)((int)gridDim.x - rows) * 256) {
+            const int64_t row = u / (kp >> 3);
+            const int p = (int)(u - row * (kp >> 3));
+            *reinterpret_cast<half8_t*>(reinterpret_cast<char*>(L.wwp) + panel_at(row, kWeakPanel, 2 * kp, p)) =
+                pair_weak(pl, row, 8 * p);
+        }
+        return;
+    }
+    const int64_t m = min((int)blockIdx.x * 4 + (tid >> 6), M - 1);  // (the last block's spare waves repeat the last token)
+    const uint16_t* xr = L.x + m * K;
+    const uint4* xp = reinterpret_cast<const uint4*>(xr);
+    const int pieces = K >> 4;
+    uint4 v[P][2];
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+        const int p = lane + 64 * i;
+        if (p < pieces) {
+            v[i][0] = xp[2 * p];
+            v[i][1] = xp[2 * p + 1];
+        }
+    }
+    mask.template fill<256>(L.idx, L.k, K);
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+        const int p = lane + 64 * i;
+        if (p < pieces) {
+            top = mask.top(v[i][0], 2 * p, mask.top(v[i][1], 2 * p + 1, top));
+        }
+    }
+    for (int p = lane + 64 * P; p < pieces; p += 64)
+        top = mask.top(xp[2 * p], 2 * p, mask.top(xp[2 * p + 1], 2 * p + 1, top));
+    const RowScale rs = row_scale(wave_max_u32(mask.both(top)));
+    if (lane == 0)
+        L.sx[m] = rs.scale;
+    auto put = [&](int p, uint4 c) { *reinterpret_cast<uint4*>(L.x8 + panel_at(m, kGemmTokens, L.Kq, p)) = c; };
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+        const int p = lane + 64 * i;
+        if (p < pieces)
+            put(p, code8x16(v[i][0], v[i][1], rs.factor));
+    }
+    for (int p = lane + 64 * P; p < pieces; p += 64)
+        put(p, code8x16(xp[2 * p], xp[2 * p + 1], rs.factor));
+    for (int p = pieces + lane; p < L.Kq >> 4; p += 64)
+        put(p, make_uint4(0u, 0u, 0u, 0u));
+    for (int c = lane; c < kp; c += 64) {
+        const int j = c < L.k ? L.idx[c] : -1;
+        *reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(L.xw) + panel_at(m, kGemmTokens, 2 * kp, c >> 3) + (c & 7) * 2) =
+            j >= 0 && j < K ? xr[j] : (uint16_t)0;
     }
 }
 
@@ -140,11 +233,11 @@ constexpr int kDecTiles = kDecChunk / 1024;
 
 // A block of 4 waves computes 4 kDecRows rows; it quantises the tokens for itself (they
 // come from the caches), which saves the launch that would do it once.
-template <int M>
+template <int M, bool WIDE>
 __global__ __launch_bounds__(256) void k_int8_gemv(const DecBatch b)
 {
     constexpr int R = kDecRows;
-    __shared__ uint32_t mask[65536 / 32];
+    __shared__ DenseMask<WIDE> mask;
     __shared__ uint4 x8[M][kDecChunk / 16];
     __shared__ uint32_t red[M][4];
     int li = 0;
@@ -174,8 +267,7 @@ __global__ __launch_bounds__(256) void k_int8_gemv(const DecBatch b)
     };
     uint4 cv[R][kDecTiles];
     load(0, cv);
-    weak_mask<256>(mask, L.idx, k, K);
-    const uint8_t* m8 = reinterpret_cast<const uint8_t*>(mask);
+    mask.template fill<256>(L.idx, k, K);
     RowScale rs[M];
     {
         uint32_t top[M];
@@ -184,8 +276,8 @@ __global__ __launch_bounds__(256) void k_int8_gemv(const DecBatch b)
             top[m] = 0;
             const uint4* xp = reinterpret_cast<const uint4*>(L.x + (int64_t)m * K);
             for (int p = tid; p < K >> 3; p += 256)
-                top[m] = top8(xp[p], m8[p], top[m]);
-            top[m] = wave_max_u32(top[m]);
+                top[m] = mask.top(xp[p], p, top[m]);
+            top[m] = wave_max_u32(mask.both(top[m]));
             if (lane == 0)
                 red[m][wave] = top[m];
         }
@@ -212,8 +304,7 @@ __global__ __launch_bounds__(256) void k_int8_gemv(const DecBatch b)
             uint4 c = make_uint4(0u, 0u, 0u, 0u);
             if (c0 + p * 16 < K) {
                 const uint4 v = xp[2 * p], w = xp[2 * p + 1];
-                c = make_uint4(code8x4(v.x, v.y, rs[m].factor), code8x4(v.z, v.w, rs[m].factor),
-                               code8x4(w.x, w.y, rs[m].factor), code8x4(w.z, w.w, rs[m].factor));
+                c = code8x16(v, w, rs[m].factor);
             }
             x8[m][p] = c;
         }
@@ -265,7 +356,7 @@ __global__ __launch_bounds__(256) void k_int8_gemv(const DecBatch b)
         }
 }
 
-// ------------------------------------------------ up to 16 tokens: one B tile --
+// ------------------------------ up to 64 tokens: codes straight into the operands --
 
 struct MfvLayer {
     const int8_t* q;
@@ -275,7 +366,7 @@ struct MfvLayer {
     const int8_t* x8;
     const float* sx;
     const uint16_t* xw;
-    int32_t N, K, k, kp, block0;
+    int32_t N, K, Kq, k, kp, block0;
 };
 struct MfvBatch {
     MfvLayer L[kInt8MaxLayers];
@@ -283,13 +374,16 @@ struct MfvBatch {
 };
 
 constexpr int kMfvWaves = 4;  // waves that split K
-constexpr int kMfvStep = 8;   // 64-column steps whose loads are in flight together
 
-// A block computes 16 rows for all tokens: v_mfma_i32_16x16x64_i8 with the codes as A
-// (lane l: row l % 16, 16 columns 16 (l / 16) of a 64-column step) and the tokens as B.
+// A block computes 16 RT rows for 16 MT tokens: v_mfma_i32_16x16x64_i8 with the codes as A
+// (lane l: row l % 16, 16 columns 16 (l / 16) of a 64-column step) and the tokens as B,
+// which k_int8_tokens has laid out in that order. Both come straight from memory into the
+// operands, U steps ahead of their products. The waves' sums meet in LDS.
+template <int RT, int MT, int U>
 __global__ __launch_bounds__(64 * kMfvWaves) void k_int8_mfv(const MfvBatch b)
 {
-    __shared__ i32x4 part[kMfvWaves - 1][64];
+    constexpr int W = kMfvWaves;
+    __shared__ i32x4 part[W][RT * MT][64];
     int li = 0;
     for (int l = 1; l < b.count; l++)
         if ((int)blockIdx.x >= b.L[l].block0)
@@ -298,57 +392,89 @@ __global__ __launch_bounds__(64 * kMfvWaves) void k_int8_mfv(const MfvBatch b)
     const int N = L.N, K = L.K;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int row0 = ((int)blockIdx.x - L.block0) * 16;
-    const int nb = min(N - row0, 16);
+    const int row0 = ((int)blockIdx.x - L.block0) * 16 * RT;
+    const int nb = min(N - row0, 16 * RT);
     const int r16 = lane & 15, g = lane >> 4;
     const __amdgpu_buffer_rsrc_t qr = bytes_rsrc(L.q + (int64_t)row0 * K, (int64_t)nb * K);
+    // (the range holds the tiles that have tokens, others read zeros)
+    const __amdgpu_buffer_rsrc_t xr = bytes_rsrc(L.x8, (int64_t)((b.M + 15) & ~15) * L.Kq);
     const int steps = (K + 63) >> 6;
-    const int per = (steps + kMfvWaves - 1) / kMfvWaves;
+    const int per = (steps + W - 1) / W;
     const int s0 = min(steps, wave * per), s1 = min(steps, s0 + per);
-    const int qoff = min(r16, nb - 1) * K + g * 16;
-    const uint4* xb = reinterpret_cast<const uint4*>(L.x8) + lane;
-    i32x4 acc = {0, 0, 0, 0};
-    for (int st = s0; st < s1; st += kMfvStep) {
-        uint4 cv[kMfvStep], xv[kMfvStep];
+    int qoff[RT];
 #pragma unroll
-        for (int u = 0; u < kMfvStep; u++) {
-            const int dead = st + u < s1 ? 0 : 0x40000000;
-            cv[u] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(qr, qoff + (st + u) * 64 + dead, 0, 2));
+    for (int r = 0; r < RT; r++)
+        qoff[r] = min(16 * r + r16, nb - 1) * K + g * 16;
+    struct Set {
+        i32x4 c[U][RT], x[U][MT];
+    };
+    // steps past the wave's last are read out of range: zeros
+    auto load = [&](int st, Set& v) {
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int dead = st + u < s1 ? 0 : kDeadLoad;
+#pragma unroll
+            for (int r = 0; r < RT; r++)
+                v.c[u][r] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(qr, qoff[r] + (st + u) * 64 + dead, 0, 0));
+#pragma unroll
+            for (int m = 0; m < MT; m++)
+                v.x[u][m] = __builtin_bit_cast(
+                    i32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, m * 16 * L.Kq + lane * 16 + (st + u) * 1024 + dead, 0, 0));
         }
+    };
+    i32x4 acc[RT][MT];
 #pragma unroll
-        for (int u = 0; u < kMfvStep; u++)
-            xv[u] = xb[min(st + u, s1 - 1) * 64];
+    for (int r = 0; r < RT; r++)
 #pragma unroll
-        for (int u = 0; u < kMfvStep; u++)
-            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, cv[u]),
-                                                        __builtin_bit_cast(i32x4, xv[u]), acc, 0, 0, 0);
+        for (int m = 0; m < MT; m++)
+            acc[r][m] = i32x4{0, 0, 0, 0};
+    auto mul = [&](const Set& v) {
+#pragma unroll
+        for (int u = 0; u < U; u++)
+#pragma unroll
+            for (int r = 0; r < RT; r++)
+#pragma unroll
+                for (int m = 0; m < MT; m++)
+                    acc[r][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v.c[u][r], v.x[u][m], acc[r][m], 0, 0, 0);
+    };
+    Set a, c;
+    load(s0, a);
+    for (int st = s0; st < s1; st += 2 * U) {
+        load(st + U, c);
+        mul(a);
+        load(st + 2 * U, a);
+        mul(c);
     }
-    if (wave > 0)
-        part[wave - 1][lane] = acc;
+#pragma unroll
+    for (int r = 0; r < RT; r++)
+#pragma unroll
+        for (int m = 0; m < MT; m++)
+            part[wave][r * MT + m][lane] = acc[r][m];
     __syncthreads();
-    if (wave > 0)
-        return;
-#pragma unroll
-    for (int w = 0; w < kMfvWaves - 1; w++)
-        acc += part[w][lane];
-    // lane l: token l % 16, rows 4 (l / 16) + r
-    const int m = min(r16, b.M - 1);
-    const float sm = L.sx[m];
-    i8_f4v out;
-#pragma unroll
-    for (int r = 0; r < 4; r++)
-        out[r] = (float)acc[r] * (sm * L.s[row0 + min(4 * g + r, nb - 1)]);
     const PairLayer P{nullptr, nullptr, nullptr, nullptr, L.ww, L.k};
-    for (int c = 0; c < L.kp; c += 32) {
-        const half8_t wv = pair_weak(P, row0 + min(r16, nb - 1), c + 8 * g);
-        const half8_t xv = *reinterpret_cast<const half8_t*>(L.xw + (int64_t)m * L.kp + c + 8 * g);
-        out = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv, xv, out, 0, 0, 0);
-    }
-    if (r16 < b.M)
+    for (int t = wave; t < RT * MT; t += W) {
+        const int rb = 16 * (t / MT), m = 16 * (t % MT) + r16;
+        if (rb >= nb)
+            continue;
+        i32x4 sum = part[0][t][lane];
+#pragma unroll
+        for (int w = 1; w < W; w++)
+            sum += part[w][t][lane];
+        // lane l: token l % 16, rows 4 (l / 16) + r
+        const int mc = min(m, b.M - 1);
+        const float sm = L.sx[mc];
+        i8_f4v out;
 #pragma unroll
         for (int r = 0; r < 4; r++)
-            if (4 * g + r < nb)
-                L.y[(int64_t)r16 * N + row0 + 4 * g + r] = f2h(out[r]);
+            out[r] = (float)sum[r] * (sm * L.s[row0 + min(rb + 4 * g + r, nb - 1)]);
+        for (int e = 0; e < L.kp; e += 32) {
+            const half8_t wv = pair_weak(P, row0 + min(rb + r16, nb - 1), e + 8 * g);
+            const half8_t xv = *reinterpret_cast<const half8_t*>(L.xw + (int64_t)mc * L.kp + e + 8 * g);
+            out = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv, xv, out, 0, 0, 0);
+        }
+        if (m < b.M)
+            store4(L.y + (int64_t)m * N, row0 + rb + 4 * g, N, out);
+    }
 }
 
 // ----------------------------------------------------- more tokens: tiled GEMM --
@@ -356,62 +482,75 @@ __global__ __launch_bounds__(64 * kMfvWaves) void k_int8_mfv(const MfvBatch b)
 struct GemmArgs8 {
     const int8_t* q;
     const float* s;
-    const uint16_t* ww;
     uint16_t* y;
-    const int8_t* x8;
+    const int8_t* x8;     // panels
     const float* sx;
-    const uint16_t* xw;
-    int32_t M, N, K, Kq, k, kp;
+    const uint16_t* xw;   // panels, [M][kp]
+    const uint16_t* wwp;  // panels, [N][kp]
+    int32_t M, N, K, Kq, kp;
     int32_t mblocks;
+    int32_t whole;   // 256 x 256 tiles that stay whole
+    int32_t splits;  // runs of stages that the blocks of one 256 x 128 tile take
+    i32x4* sums;     // their sums, where splits > 1: [split][tile][wave][registers / 4][lane]
 };
+
 
 template <int FM, int FN, int WM, int WN>
 struct Tile8 {
     static constexpr int NT = 64 * WM * WN;
     static constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN;
-    static constexpr int DA = BM * 128 / 16 / NT, DB = BN * 128 / 16 / NT;  // 16-byte units per thread and stage
-    static_assert(DA * NT * 16 == BM * 128 && DB * NT * 16 == BN * 128, "a stage must split evenly over the threads");
+    static constexpr int STAGE = (BM + BN) * kGemmCols;
+    static constexpr int DA = BM * 4 / NT, DB = BN * 4 / NT;  // 16-byte units per thread and stage
+    static_assert(DA * NT == BM * 4 && DB * NT == BN * 4, "a stage must split evenly over the threads");
 };
 
-// BM tokens x BN rows per block, both operands through LDS in stages of 128 columns
-// (direct-to-LDS loads, the piece c of row r in slot c ^ (r & 7) of the row's 128 bytes,
-// so that the operand reads of a wave spread over the banks), two stages.
-template <int FM, int FN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4))) void k_int8_gemm(const GemmArgs8 a)
+// BM tokens x BN rows per tile, both operands through LDS by direct-to-LDS loads in a ring
+// of four stages of 64 columns, up to three stages ahead; operands are read from LDS one
+// 32-column step ahead of their products, also across the stages: at a barrier the stage
+// after the current one has landed too. The weak columns follow as stages of 32 fp16
+// columns in the same ring, for which the sums have become fp32 and scaled. The rows are
+// the matrix instruction's A, so that a lane ends with four consecutive outputs of one
+// token; they leave through LDS in whole lines. PART: only the integer sums of stages
+// c0 .. c1 - 1, to `sums`.
+template <int FM, int FN, int WM, int WN, bool PART = false>
+__device__ __forceinline__ void gemm_tile(const GemmArgs8& a, char* s0, char* s1, char* s2, char* s3, float* sm, float* sn,
+                                          int m0, int n0, int c0, int c1, i32x4* sums = nullptr)
 {
     using T = Tile8<FM, FN, WM, WN>;
-    constexpr int BM = T::BM, BN = T::BN;
-    __shared__ __attribute__((aligned(1024))) char s0[(BM + BN) * 128];
-    __shared__ __attribute__((aligned(1024))) char s1[(BM + BN) * 128];
-    const int M = a.M, N = a.N, K = a.K, Kq = a.Kq;
+    constexpr int BM = T::BM, BN = T::BN, DPW = T::DA + T::DB;
+    const int M = a.M, N = a.N, K = a.K;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % WM, wn = wave / WM;
     const int l32 = lane & 31, h = lane >> 5;
-    const int m0 = ((int)blockIdx.x % a.mblocks) * BM, n0 = ((int)blockIdx.x / a.mblocks) * BN;
+    // this lane's pieces h and 2 + h of its rows
+    const int p0 = stage_at(l32, h), p1 = stage_at(l32, 2 + h);
+    const int abase = wm * FM * 2048, bbase = (BM + wn * 32 * FN) * kGemmCols;
     const int mv = min(BM, M - m0), nv = min(BN, N - n0);
-    const __amdgpu_buffer_rsrc_t xr = bytes_rsrc(a.x8 + (int64_t)m0 * Kq, (int64_t)mv * Kq);
-    const __amdgpu_buffer_rsrc_t qr = bytes_rsrc(a.q + (int64_t)n0 * K, (int64_t)nv * K);
+    __amdgpu_buffer_rsrc_t xr = uniform_rsrc(a.x8 + (int64_t)m0 * a.Kq, (int64_t)BM * a.Kq);
+    __amdgpu_buffer_rsrc_t qr = uniform_rsrc(a.q + (int64_t)n0 * K, (int64_t)nv * K);
     int xsrc[T::DA], qsrc[T::DB];
 #pragma unroll
     for (int t = 0; t < T::DA; t++) {
-        const int u = (wave * T::DA + t) * 64 + lane, row = u >> 3;
-        xsrc[t] = min(row, mv - 1) * Kq + ((u & 7) ^ (row & 7)) * 16;
+        const int u = (wave * T::DA + t) * 64 + lane;
+        xsrc[t] = stage_row(u) * kGemmCols + stage_piece(u) * 16;
     }
 #pragma unroll
     for (int t = 0; t < T::DB; t++) {
-        const int u = (wave * T::DB + t) * 64 + lane, row = u >> 3;
-        qsrc[t] = min(row, nv - 1) * K + ((u & 7) ^ (row & 7)) * 16;
+        const int u = (wave * T::DB + t) * 64 + lane;
+        qsrc[t] = min(stage_row(u), nv - 1) * K + stage_piece(u) * 16;
     }
     // (pieces past K of the last stage hold the next row's codes, or zeros past the
     // last row: the tokens' codes there are zeros)
+    int end = c1, row_step = kGemmCols;
     auto dma = [&](int c, char* stage) {
+        const int ox = c < end ? c * (BM * kGemmCols) : kDeadLoad, oq = c < end ? c * row_step : kDeadLoad;
 #pragma unroll
         for (int t = 0; t < T::DA; t++)
-            dma16_lds(xr, stage + (wave * T::DA + t) * 1024, xsrc[t] + c * 128);
+            dma16_lds(xr, stage + (wave * T::DA + t) * 1024, xsrc[t] + ox);
 #pragma unroll
         for (int t = 0; t < T::DB; t++)
-            dma16_lds(qr, stage + BM * 128 + (wave * T::DB + t) * 1024, qsrc[t] + c * 128);
+            dma16_lds(qr, stage + BM * kGemmCols + (wave * T::DB + t) * 1024, qsrc[t] + oq);
     };
     i32x16 acc[FM][FN];
 #pragma unroll
@@ -421,83 +560,254 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WM
 #pragma unroll
             for (int r = 0; r < 16; r++)
                 acc[i][f][r] = 0;
-    const int arow = (wm * 32 * FM + l32) * 128, brow = (BM + wn * 32 * FN + l32) * 128;
-    const int chunks = Kq >> 7;
-    auto step = [&](int c, const char* cur, char* nxt) {
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (c + 1 < chunks)
-            dma(c + 1, nxt);
-        if (c < chunks) {
+    i32x4 av[2][FM], bv[2][FN];
+    auto read = [&](const char* stage, int set, int p) {
 #pragma unroll
-            for (int st = 0; st < 4; st++) {
-                const int slot = ((st * 2 + h) ^ (l32 & 7)) * 16;
-                i32x4 av[FM], bv[FN];
+        for (int f = 0; f < FN; f++)
+            bv[set][f] = *reinterpret_cast<const i32x4*>(stage + bbase + f * 2048 + p);
 #pragma unroll
-                for (int i = 0; i < FM; i++)
-                    av[i] = *reinterpret_cast<const i32x4*>(cur + arow + i * 4096 + slot);
+        for (int i = 0; i < FM; i++)
+            av[set][i] = *reinterpret_cast<const i32x4*>(stage + abase + i * 2048 + p);
+    };
+    auto mul = [&](int set) {
 #pragma unroll
-                for (int f = 0; f < FN; f++)
-                    bv[f] = *reinterpret_cast<const i32x4*>(cur + brow + f * 4096 + slot);
+        for (int i = 0; i < FM; i++)
 #pragma unroll
-                for (int i = 0; i < FM; i++)
+            for (int f = 0; f < FN; f++)
+                acc[i][f] = __builtin_amdgcn_mfma_i32_32x32x32_i8(bv[set][f], av[set][i], acc[i][f], 0, 0, 0);
+        // the other set's reads between these products
+        constexpr int per = FM * FN / (FM + FN);
 #pragma unroll
-                    for (int f = 0; f < FN; f++)
-                        acc[i][f] = __builtin_amdgcn_mfma_i32_32x32x32_i8(av[i], bv[f], acc[i][f], 0, 0, 0);
-            }
+        for (int i = 0; i < FM + FN; i++) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, per, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, FM * FN - (FM + FN) * per, 0);
+    };
+    auto arrived = [&](int set) {  // the reads of a set are done
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+            asm volatile("" ::"v"(av[set][i]));
+#pragma unroll
+        for (int f = 0; f < FN; f++)
+            asm volatile("" ::"v"(bv[set][f]));
+    };
+    // stage c is in cur and stage c + 1 in next, whole; stage c + 3 goes where c - 1 was
+    auto step = [&](int c, const char* cur, const char* next, char* fill) {
+        stage_barrier<DPW, 15>();
+        dma(c + 3, fill);
+        if (c < c1) {
+            read(cur, 1, p1);
+            mul(0);
+            read(next, 0, p0);
+            mul(1);
+            arrived(1);  // before this wave lets cur be overwritten
         }
     };
-    dma(0, s0);
-    for (int c = 0; c < chunks; c += 2) {
-        step(c, s0, s1);
-        step(c + 1, s1, s0);
+    __syncthreads();  // the stages are free
+    dma(c0, s0);
+    dma(c0 + 1, s1);
+    dma(c0 + 2, s2);
+    for (int e = tid; e < BM + BN; e += T::NT) {
+        if (e < BM)
+            sm[e] = a.sx[m0 + min(e, mv - 1)];
+        else
+            sn[e - BM] = a.s[n0 + min(e - BM, nv - 1)];
     }
-    // D element r of lane l: token 8 (r / 4) + 4 h + r % 4, row l % 32
-    const PairLayer P{nullptr, nullptr, nullptr, nullptr, a.ww, a.k};
+    stage_barrier<0>();
+    read(s0, 0, p0);
+    for (int c = c0; c < c1; c += 4) {
+        step(c, s0, s1, s3);
+        step(c + 1, s1, s2, s0);
+        step(c + 2, s2, s3, s1);
+        step(c + 3, s3, s0, s2);
+    }
+    arrived(0);
+    stage_barrier<0>();  // the loads past the end have written their zeros
+    if (PART) {
+        sums += (int64_t)wave * (FM * FN * 4) * 64 + lane;
 #pragma unroll
-    for (int i = 0; i < FM; i++) {
-        const int mb = wm * 32 * FM + 32 * i;
-        float sm[16];
+        for (int i = 0; i < FM; i++)
 #pragma unroll
-        for (int r = 0; r < 16; r++)
-            sm[r] = a.sx[m0 + min(mb + 8 * (r >> 2) + 4 * h + (r & 3), mv - 1)];
+            for (int f = 0; f < FN; f++)
 #pragma unroll
-        for (int f = 0; f < FN; f++) {
-            const int nr = min(wn * 32 * FN + 32 * f + l32, nv - 1);
-            const float sn = a.s[n0 + nr];
-            i8_f16v out;
+                for (int q = 0; q < 4; q++)
+                    sums[((i * FN + f) * 4 + q) * 64] =
+                        i32x4{acc[i][f][4 * q], acc[i][f][4 * q + 1], acc[i][f][4 * q + 2], acc[i][f][4 * q + 3]};
+        return;
+    }
+    // the weak columns' first stages
+    const int ws = a.kp >> 5;
+    xr = uniform_rsrc(a.xw + (int64_t)m0 * a.kp, (int64_t)2 * BM * a.kp);
+    // (panels of pn rows: this tile's are one or two, the second may lie past N)
+    qr = uniform_rsrc(a.wwp + (int64_t)n0 * a.kp, (int64_t)2 * ((nv + kWeakPanel - 1) / kWeakPanel * kWeakPanel) * a.kp);
+#pragma unroll
+    for (int t = 0; t < T::DB; t++) {
+        const int u = (wave * T::DB + t) * 64 + lane;
+        const int row = stage_row(u), in = row & (kWeakPanel - 1);
+        qsrc[t] = (row - in) * 2 * a.kp + in * kGemmCols + stage_piece(u) * 16;
+    }
+    end = ws;
+    row_step = kWeakPanel * kGemmCols;
+    if (ws > 0) {
+        dma(0, s0);
+        dma(1, s1);
+    }
+    // element r of a lane: row 8 (r / 4) + 4 h + r % 4, token l % 32
+    i8_f16v out[FM][FN];
+#pragma unroll
+    for (int f = 0; f < FN; f++) {
+        i8_f4v sr[4];
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+            sr[q] = *reinterpret_cast<const i8_f4v*>(&sn[wn * 32 * FN + 32 * f + 8 * q + 4 * h]);
+#pragma unroll
+        for (int i = 0; i < FM; i++) {
+            const float sx = sm[wm * 32 * FM + 32 * i + l32];
 #pragma unroll
             for (int r = 0; r < 16; r++)
-                out[r] = (float)acc[i][f][r] * (sm[r] * sn);
-            for (int c = 0; c < a.kp; c += 16) {
-                const half8_t xv = *reinterpret_cast<const half8_t*>(a.xw + (int64_t)(m0 + min(mb + l32, mv - 1)) * a.kp + c + 8 * h);
-                out = __builtin_amdgcn_mfma_f32_32x32x16_f16(xv, pair_weak(P, n0 + nr, c + 8 * h), out, 0, 0, 0);
-            }
-            const int n = n0 + wn * 32 * FN + 32 * f + l32;
-#pragma unroll
-            for (int r = 0; r < 16; r++) {
-                const int m = m0 + mb + 8 * (r >> 2) + 4 * h + (r & 3);
-                if (m < M && n < N)
-                    a.y[(int64_t)m * N + n] = f2h(out[r]);
-            }
+                out[i][f][r] = (float)acc[i][f][r] * (sx * sr[r >> 2][r & 3]);
         }
+    }
+    for (int c = 0; c < ws; c++) {
+        stage_barrier<0>();
+        const char* const cur = c & 1 ? s1 : s0;
+#pragma unroll
+        for (int st = 0; st < 2; st++) {
+            read(cur, st, st ? p1 : p0);
+#pragma unroll
+            for (int i = 0; i < FM; i++)
+#pragma unroll
+                for (int f = 0; f < FN; f++)
+                    out[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, bv[st][f]),
+                                                                       __builtin_bit_cast(half8_t, av[st][i]), out[i][f], 0,
+                                                                       0, 0);
+        }
+        if (c + 2 < ws) {
+            stage_barrier<0>();
+            dma(c + 2, c & 1 ? s1 : s0);
+        }
+    }
+    // 32 tokens x 32 FN rows of the wave at a time: token t's piece of 8 rows p in slot
+    // p ^ (t % 8) of its 64 FN bytes
+    static_assert(WM * WN / 2 * 32 * FN * 64 <= T::STAGE, "the waves' outputs pass through two stages");
+    char* const mine = (wave < (WM * WN + 1) / 2 ? s2 : s3) + wave % ((WM * WN + 1) / 2) * (32 * FN * 64);
+    constexpr int PIECES = 4 * FN;
+#pragma unroll
+    for (int i = 0; i < FM; i++) {
+#pragma unroll
+        for (int f = 0; f < FN; f++)
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const i8_f16v& o = out[i][f];
+                *reinterpret_cast<uint2*>(mine + l32 * (64 * FN) + ((f * 4 + q) ^ (l32 & (PIECES - 1) & 7)) * 16 + h * 8) =
+                    make_uint2(f2h(o[4 * q]) | ((uint32_t)f2h(o[4 * q + 1]) << 16),
+                               f2h(o[4 * q + 2]) | ((uint32_t)f2h(o[4 * q + 3]) << 16));
+            }
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int e = 0; e < 32 * PIECES / 64; e++) {
+            const int t = (e * 64 + lane) / PIECES, p = lane % PIECES;
+            const uint4 v = *reinterpret_cast<const uint4*>(mine + t * (64 * FN) + (p ^ (t & (PIECES - 1) & 7)) * 16);
+            const int m = m0 + wm * 32 * FM + 32 * i + t, n = n0 + wn * 32 * FN + 8 * p;
+            if (m < M)
+                store8(a.y + (int64_t)m * N, n, N, v);
+        }
+        asm volatile("" ::: "memory");
     }
 }
 
-template <int FM, int FN, int WM, int WN>
-bool tile8_fits(int64_t M, int64_t N)
+// Tiles of 256 tokens x 256 rows, one per block, as many as fill whole rounds of the GPU;
+// the rest as tiles of 256 x 128, two in place of one (blocks start in this order, so the
+// small ones fill the last round). Where even the small ones leave CUs idle, `splits`
+// blocks share each, and k_int8_gemm_sum adds their sums up.
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_int8_gemm(const GemmArgs8 a)
 {
-    using T = Tile8<FM, FN, WM, WN>;
-    return grid_fits((M + T::BM - 1) / T::BM * ((N + T::BN - 1) / T::BN), T::NT);
+    using T = Tile8<4, 2, 2, 4>;
+    __shared__ __attribute__((aligned(1024))) char s0[T::STAGE];
+    __shared__ __attribute__((aligned(1024))) char s1[T::STAGE];
+    __shared__ __attribute__((aligned(1024))) char s2[T::STAGE];
+    __shared__ __attribute__((aligned(1024))) char s3[T::STAGE];
+    __shared__ float sm[T::BM], sn[T::BN];
+    const int chunks = a.Kq / kGemmCols;
+    if ((int)blockIdx.x < a.whole) {
+        const int tile = xcd_place((int)blockIdx.x, a.whole);
+        gemm_tile<4, 2, 2, 4>(a, s0, s1, s2, s3, sm, sn, (tile % a.mblocks) * T::BM, (tile / a.mblocks) * T::BN, 0, chunks);
+        return;
+    }
+    const int part = xcd_place((int)blockIdx.x - a.whole, (int)gridDim.x - a.whole);
+    if (a.splits == 1) {
+        // parts 2 t and 2 t + 1: the halves of tile whole + t
+        const int tile = a.whole + (part >> 1), n0 = (tile / a.mblocks) * T::BN + (part & 1) * (T::BN / 2);
+        if (n0 < a.N)
+            gemm_tile<2, 2, 4, 2>(a, s0, s1, s2, s3, sm, sn, (tile % a.mblocks) * T::BM, n0, 0, chunks);
+        return;
+    }
+    const int tiles = ((int)gridDim.x - a.whole) / a.splits, tile = part % tiles, split = part / tiles;
+    gemm_tile<2, 2, 4, 2, true>(a, s0, s1, s2, s3, sm, sn, (tile % a.mblocks) * T::BM, (tile / a.mblocks) * (T::BN / 2),
+                                (int)((int64_t)chunks * split / a.splits), (int)((int64_t)chunks * (split + 1) / a.splits),
+                                a.sums + (int64_t)part * kSumVectors);
 }
 
-template <int FM, int FN, int WM, int WN>
-hipError_t launch_tile8(GemmArgs8 a, hipStream_t s)
+// The splits' sums of one 32 x 32 piece, a wave each: scaled, the weak columns, stored.
+__global__ __launch_bounds__(64) void k_int8_gemm_sum(const GemmArgs8 a, int tiles)
 {
-    using T = Tile8<FM, FN, WM, WN>;
-    a.mblocks = (a.M + T::BM - 1) / T::BM;
-    const int64_t blocks = (int64_t)a.mblocks * ((a.N + T::BN - 1) / T::BN);
-    hipLaunchKernelGGL((k_int8_gemm<FM, FN, WM, WN>), dim3((unsigned)blocks), dim3(T::NT), 0, s, a);
-    return hipGetLastError();
+    const int lane = threadIdx.x, l32 = lane & 31, h = lane >> 5;
+    const int piece = (int)blockIdx.x & 31, tile = (int)blockIdx.x >> 5;
+    const int wave = piece >> 2, i = (piece >> 1) & 1, f = piece & 1;  // as in gemm_tile<2, 2, 4, 2>
+    const int mb = (tile % a.mblocks) * 256 + (wave % 4) * 64 + 32 * i, nb = (tile / a.mblocks) * 128 + (wave / 4) * 64 + 32 * f;
+    if (mb >= a.M || nb >= a.N)
+        return;
+    const i32x4* p = a.sums + (int64_t)tile * kSumVectors + (wave * 16 + (i * 2 + f) * 4) * 64 + lane;
+    i32x4 sum[4];
+#pragma unroll
+    for (int q = 0; q < 4; q++)
+        sum[q] = p[q * 64];
+    for (int s = 1; s < a.splits; s++)
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+            sum[q] += p[(int64_t)s * tiles * kSumVectors + q * 64];
+    const int m = min(mb + l32, a.M - 1);
+    const float sx = a.sx[m];
+    i8_f16v out;
+#pragma unroll
+    for (int r = 0; r < 16; r++)
+        out[r] = (float)sum[r >> 2][r & 3] * (sx * a.s[min(nb + 8 * (r >> 2) + 4 * h + (r & 3), a.N - 1)]);
+    const char* xw = reinterpret_cast<const char*>(a.xw);
+    const char* wwp = reinterpret_cast<const char*>(a.wwp);
+    const int n = min(nb + l32, a.N - 1);
+    for (int c = 0; c < a.kp >> 3; c += 2)
+        out = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const half8_t*>(wwp + panel_at(n, kWeakPanel, 2 * a.kp, c + h)),
+                                                     *reinterpret_cast<const half8_t*>(xw + panel_at(m, 256, 2 * a.kp, c + h)), out,
+                                                     0, 0, 0);
+    if (mb + l32 < a.M)
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+            store4(a.y + (int64_t)m * a.N, nb + 8 * q + 4 * h, a.N, i8_f4v{out[4 * q], out[4 * q + 1], out[4 * q + 2], out[4 * q + 3]});
+}
+
+constexpr int kCus = 256;
+
+// How the tiles of a product are dealt out: whole 256 x 256 tiles, small ones (256 x 128),
+// blocks per small one
+struct GemmGrid {
+    int64_t whole, small;
+    int32_t splits;
+    int64_t blocks() const { return whole + small * splits; }
+};
+
+GemmGrid gemm_grid(int64_t M, int64_t N, int64_t chunks)
+{
+    const int64_t mb = (M + kGemmTokens - 1) / kGemmTokens, large = mb * ((N + 255) / 256), small = mb * ((N + 127) / 128);
+    if (2 * small <= kCus) {
+        // fewer small tiles than half the CUs; a block keeps at least 8 stages
+        int64_t sp = kCus / small;
+        sp = sp < chunks / 8 ? sp : chunks / 8;
+        if (sp > 1)
+            return GemmGrid{0, small, (int32_t)sp};
+    }
+    const int64_t rest = large % kCus, whole = 2 * rest <= kCus ? large - rest : large;
+    return GemmGrid{whole, 2 * (large - whole), 1};
 }
 
 constexpr int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -506,36 +816,54 @@ constexpr int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 Int8Plan int8_plan(int64_t N, int64_t K, int32_t k, int64_t M)
 {
-    (void)N;
     Int8Plan p{};
     if (M <= kInt8GemvMaxM)
         return p;
-    p.Kq = up(K, 128);
+    p.Kq = up(K, kGemmCols);
     p.kp = (int32_t)up(k, 32);
-    p.off_sx = (size_t)(p.Kq * (M <= kInt8DecodeMaxM ? 16 : M));
+    if (M <= kInt8StreamMaxM) {
+        p.off_sx = (size_t)(p.Kq * up(M, 16));
+        p.off_xw = p.off_sx + (size_t)up(M * 4, 256);
+        p.total = p.off_xw + (size_t)up(M * p.kp * 2, 256);
+        return p;
+    }
+    const GemmGrid g = gemm_grid(M, N, p.Kq / kGemmCols);
+    const int64_t Mp = up(M, kGemmTokens), Np = up(N, kWeakPanel);  // whole panels
+    p.off_sx = (size_t)(p.Kq * Mp);
     p.off_xw = p.off_sx + (size_t)up(M * 4, 256);
-    p.total = p.off_xw + (size_t)up(M * p.kp * 2, 256);
+    p.off_wwp = p.off_xw + (size_t)up(Mp * p.kp * 2, 256);
+    p.off_sums = p.off_wwp + (size_t)up(Np * p.kp * 2, 256);
+    p.total = p.off_sums + (g.splits > 1 ? (size_t)(g.splits * g.small) * kSumVectors * 16 : 0);
     return p;
 }
+
+// Token tiles of 16 and row tiles of 16 per block of the streaming product
+int mfv_rows(int64_t M) { return M <= 32 ? 16 : 32; }
 
 bool int8_grid_fits(int64_t M, int64_t N)
 {
     if (M <= kInt8GemvMaxM)
         return grid_fits((N + 4 * kDecRows - 1) / (4 * kDecRows), 256);
-    if (M <= kInt8DecodeMaxM)
-        return grid_fits((N + 15) / 16, 64 * kMfvWaves);
-    return grid_fits(M, 256) && (M > 128 ? tile8_fits<4, 2, 2, 4>(M, N) : tile8_fits<1, 1, 1, 4>(M, N));
+    if (M <= kInt8StreamMaxM)
+        return grid_fits((N + mfv_rows(M) - 1) / mfv_rows(M), 64 * kMfvWaves);
+    return grid_fits(M, 256) && grid_fits(gemm_grid(M, N, 1024).blocks(), 512);
 }
 
 hipError_t launch_pack_int8(const uint16_t* W, int64_t N, int64_t K, const int32_t* idx, int32_t k, int8_t* codes,
                             float* scales, uint16_t* ww, hipStream_t s)
 {
-    hipLaunchKernelGGL(k_pack_int8, dim3((unsigned)N), dim3(256), 0, s, W, (int)K, idx, k, codes, scales, ww);
+    if (K <= kWideMask)
+        hipLaunchKernelGGL(k_pack_int8<true>, dim3((unsigned)N), dim3(256), 0, s, W, (int)K, idx, k, codes, scales, ww);
+    else
+        hipLaunchKernelGGL(k_pack_int8<false>, dim3((unsigned)N), dim3(256), 0, s, W, (int)K, idx, k, codes, scales, ww);
     return hipGetLastError();
 }
 
 hipError_t launch_linear_int8(const Int8Desc* d, int count, int64_t M, void* const* ws, hipStream_t s)
 {
+    int64_t longest = 0;
+    for (int l = 0; l < count; l++)
+        longest = longest < d[l].K ? d[l].K : longest;
     if (M <= kInt8GemvMaxM) {
         DecBatch b{};
         b.count = count;
@@ -548,53 +876,83 @@ hipError_t launch_linear_int8(const Int8Desc* d, int count, int64_t M, void* con
         if (!grid_fits(blocks, 256))
             return hipErrorInvalidConfiguration;
         const dim3 grid((unsigned)blocks), block(256);
-        if (M == 1)
-            hipLaunchKernelGGL(k_int8_gemv<1>, grid, block, 0, s, b);
-        else if (M == 2)
-            hipLaunchKernelGGL(k_int8_gemv<2>, grid, block, 0, s, b);
-        else if (M == 3)
-            hipLaunchKernelGGL(k_int8_gemv<3>, grid, block, 0, s, b);
+        auto launch = [&](auto wide) {
+            constexpr bool WIDE = decltype(wide)::value;
+            if (M == 1)
+                hipLaunchKernelGGL((k_int8_gemv<1, WIDE>), grid, block, 0, s, b);
+            else if (M == 2)
+                hipLaunchKernelGGL((k_int8_gemv<2, WIDE>), grid, block, 0, s, b);
+            else if (M == 3)
+                hipLaunchKernelGGL((k_int8_gemv<3, WIDE>), grid, block, 0, s, b);
+            else
+                hipLaunchKernelGGL((k_int8_gemv<4, WIDE>), grid, block, 0, s, b);
+        };
+        if (longest <= kWideMask)
+            launch(std::true_type{});
         else
-            hipLaunchKernelGGL(k_int8_gemv<4>, grid, block, 0, s, b);
+            launch(std::false_type{});
         return hipGetLastError();
     }
     QuantBatch qb{};
     Int8Plan p[kInt8MaxLayers];
-    int64_t mfv_blocks = 0;
     for (int l = 0; l < count; l++) {
         p[l] = int8_plan(d[l].N, d[l].K, d[l].k, M);
         char* const w = static_cast<char*>(ws[l]);
-        qb.L[l] = QuantLayer{d[l].x, d[l].idx, reinterpret_cast<int8_t*>(w), reinterpret_cast<float*>(w + p[l].off_sx),
-                             reinterpret_cast<uint16_t*>(w + p[l].off_xw), (int32_t)d[l].K, (int32_t)p[l].Kq, d[l].k, p[l].kp};
-        mfv_blocks += (d[l].N + 15) / 16;
+        qb.L[l] = QuantLayer{d[l].x, d[l].idx, d[l].ww, reinterpret_cast<int8_t*>(w),
+                             reinterpret_cast<float*>(w + p[l].off_sx), reinterpret_cast<uint16_t*>(w + p[l].off_xw), nullptr,
+                             (int32_t)d[l].N, (int32_t)d[l].K, (int32_t)p[l].Kq, d[l].k, p[l].kp};
     }
-    const dim3 tokens((unsigned)M, (unsigned)count);
-    if (M <= kInt8DecodeMaxM) {
-        if (!grid_fits(mfv_blocks, 64 * kMfvWaves))
-            return hipErrorInvalidConfiguration;
-        hipLaunchKernelGGL(k_int8_tokens<true>, tokens, dim3(256), 0, s, qb);
+    if (M <= kInt8StreamMaxM) {
         MfvBatch b{};
         b.count = count;
         b.M = (int32_t)M;
         int64_t blocks = 0;
+        const int rows = mfv_rows(M);
         for (int l = 0; l < count; l++) {
             const QuantLayer& q = qb.L[l];
-            b.L[l] = MfvLayer{d[l].q, d[l].s, d[l].ww, d[l].y, q.x8, q.sx, q.xw, (int32_t)d[l].N, (int32_t)d[l].K, d[l].k,
+            b.L[l] = MfvLayer{d[l].q, d[l].s, d[l].ww, d[l].y, q.x8, q.sx, q.xw, (int32_t)d[l].N, (int32_t)d[l].K, q.Kq, d[l].k,
                               q.kp, (int32_t)blocks};
-            blocks += (d[l].N + 15) / 16;
+            blocks += (d[l].N + rows - 1) / rows;
         }
-        hipLaunchKernelGGL(k_int8_mfv, dim3((unsigned)blocks), dim3(64 * kMfvWaves), 0, s, b);
+        if (!grid_fits(blocks, 64 * kMfvWaves))
+            return hipErrorInvalidConfiguration;
+        const dim3 tokens((unsigned)M, (unsigned)count);
+        if (longest <= 4096)
+            hipLaunchKernelGGL((k_int8_tokens<true, 1>), tokens, dim3(256), 0, s, qb);
+        else if (longest <= kWideMask)
+            hipLaunchKernelGGL((k_int8_tokens<true, 3>), tokens, dim3(256), 0, s, qb);
+        else
+            hipLaunchKernelGGL((k_int8_tokens<false, 3>), tokens, dim3(256), 0, s, qb);
+        const dim3 grid((unsigned)blocks), block(64 * kMfvWaves);
+        if (M <= 16)
+            hipLaunchKernelGGL((k_int8_mfv<1, 1, 8>), grid, block, 0, s, b);
+        else if (M <= 32)
+            hipLaunchKernelGGL((k_int8_mfv<1, 2, 8>), grid, block, 0, s, b);
+        else
+            hipLaunchKernelGGL((k_int8_mfv<2, 4, 2>), grid, block, 0, s, b);
         return hipGetLastError();
     }
     if (count != 1 || !int8_grid_fits(M, d[0].N))  // before the first launch
         return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(k_int8_tokens<false>, tokens, dim3(256), 0, s, qb);
-    const QuantLayer& q = qb.L[0];
-    const GemmArgs8 a{d[0].q, d[0].s, d[0].ww, d[0].y, q.x8, q.sx, q.xw, (int32_t)M, (int32_t)d[0].N, (int32_t)d[0].K,
-                      q.Kq, q.k, q.kp, 1};
-    if (M > 128)
-        return launch_tile8<4, 2, 2, 4>(a, s);  // 256 tokens x 256 rows
-    return launch_tile8<1, 1, 1, 4>(a, s);      // 32 tokens x 128 rows
+    char* const w = static_cast<char*>(ws[0]);
+    QuantLayer& q = qb.L[0];
+    q.wwp = reinterpret_cast<uint16_t*>(w + p[0].off_wwp);
+    const int64_t units = (d[0].N * (q.kp / 8) + 255) / 256;
+    const dim3 panels((unsigned)((M + 3) / 4 + (units < 512 ? units : 512)));
+    if (longest <= 4096)
+        hipLaunchKernelGGL((k_int8_token_panels<true, 4>), panels, dim3(256), 0, s, q, (int)M);
+    else if (longest <= kWideMask)
+        hipLaunchKernelGGL((k_int8_token_panels<true, 11>), panels, dim3(256), 0, s, q, (int)M);
+    else
+        hipLaunchKernelGGL((k_int8_token_panels<false, 11>), panels, dim3(256), 0, s, q, (int)M);
+    const GemmGrid g = gemm_grid(M, d[0].N, q.Kq / kGemmCols);
+    const GemmArgs8 a{d[0].q, d[0].s, d[0].y, q.x8, q.sx, q.xw, q.wwp, (int32_t)M, (int32_t)d[0].N, (int32_t)d[0].K, q.Kq, q.kp,
+                      (int32_t)((M + kGemmTokens - 1) / kGemmTokens), (int32_t)g.whole, g.splits,
+                      reinterpret_cast<i32x4*>(w + p[0].off_sums)};
+    hipLaunchKernelGGL(k_int8_gemm, dim3((unsigned)g.blocks()), dim3(512), 0, s, a);
+    if (g.splits > 1)
+        hipLaunchKernelGGL(k_int8_gemm_sum, dim3((unsigned)(32 * g.small)), dim3(64), 0, s, a, (int)g.small);
+    return hipGetLastError();
 }
 
 }  // namespace owq

@@ -306,7 +306,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WM
     const int chunks = Np >> 6;
     uint32_t cv[T::GROUPS][8];
     auto step = [&](int c, const char* cur, char* nxt) {
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        stage_barrier<0>();
         if (c + 1 < chunks) {
             dma(c + 1, nxt);
             put(cv, nxt);

@@ -18,14 +18,6 @@ typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef float i8_f16v __attribute__((ext_vector_type(16)));
 typedef float i8_f4v __attribute__((ext_vector_type(4)));
 
-// |v| of both halves as integers: they order like the values, and a NaN lies above
-// infinity, so the largest of a row that holds one is a NaN
-__device__ __forceinline__ uint32_t abs_bits_max(uint32_t pair, uint32_t top)
-{
-    const uint32_t lo = pair & 0x7fffu, hi = (pair >> 16) & 0x7fffu;
-    return max(top, max(lo, hi));
-}
-
 // Scale and factor of a row whose largest dense magnitude has these bits: t / 127 and
 // 127 / t, each one IEEE division; a row of zeros has both 0. An infinity or a NaN gives
 // a scale that makes every output of the row NaN or infinite (its codes are 0).
@@ -38,48 +30,87 @@ __device__ __forceinline__ RowScale row_scale(uint32_t top)
     return RowScale{t / 127.0f, top == 0 ? 0.0f : (top >= 0x7c00u ? 0.0f : 127.0f / t)};
 }
 
-// The code of one value: the fp32 product rounded half to even. Values outside the
-// fitted columns may exceed the range (their codes are multiplied by 0): they are
-// held to it, and a NaN becomes some code.
-__device__ __forceinline__ int code8(float v, float factor)
+// The codes of four values (two pairs): each fp32 product v factor rounded half to even.
+// Adding 1.5 2^23 rounds to integers and leaves the code in the low byte, for the fitted
+// columns, where |v factor| <= 127 (1 + 2^-23). Weak columns' values may lie outside and
+// give any byte: it is multiplied by 0.
+__device__ __forceinline__ uint32_t code8x4(uint32_t a, uint32_t b, float factor)
 {
-    return (int)__builtin_amdgcn_fmed3f(rintf(v * factor), -127.0f, 127.0f);
+    constexpr float kRound = 12582912.0f;
+    const half2_t va = __builtin_bit_cast(half2_t, a), vb = __builtin_bit_cast(half2_t, b);
+    // (a fused multiply-add with zero is the product rounded once, and takes fp16 operands)
+    const uint32_t c0 = __builtin_bit_cast(uint32_t, __builtin_fmaf((float)va.x, factor, 0.0f) + kRound);
+    const uint32_t c1 = __builtin_bit_cast(uint32_t, __builtin_fmaf((float)va.y, factor, 0.0f) + kRound);
+    const uint32_t c2 = __builtin_bit_cast(uint32_t, __builtin_fmaf((float)vb.x, factor, 0.0f) + kRound);
+    const uint32_t c3 = __builtin_bit_cast(uint32_t, __builtin_fmaf((float)vb.y, factor, 0.0f) + kRound);
+    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(c3, c2, 0x0c0c0400u), __builtin_amdgcn_perm(c1, c0, 0x0c0c0400u),
+                                 0x05040100u);
 }
 
-__device__ __forceinline__ uint32_t code8x4(uint32_t a, uint32_t b, float f)
+__device__ __forceinline__ uint4 code8x16(uint4 a, uint4 b, float f)
 {
-    const int c0 = code8(h2f((uint16_t)(a & 0xffffu)), f), c1 = code8(h2f((uint16_t)(a >> 16)), f);
-    const int c2 = code8(h2f((uint16_t)(b & 0xffffu)), f), c3 = code8(h2f((uint16_t)(b >> 16)), f);
-    return (uint32_t)(c0 & 0xff) | ((uint32_t)(c1 & 0xff) << 8) | ((uint32_t)(c2 & 0xff) << 16) | ((uint32_t)c3 << 24);
+    return make_uint4(code8x4(a.x, a.y, f), code8x4(a.z, a.w, f), code8x4(b.x, b.y, f), code8x4(b.z, b.w, f));
 }
 
-// Bits of the weak columns, K / 32 words in LDS. All threads of the block call it.
-template <int NT>
-__device__ __forceinline__ void weak_mask(uint32_t* mask, const int32_t* idx, int k, int K)
-{
-    for (int i = threadIdx.x; i < K >> 5; i += NT)
-        mask[i] = 0;
-    __syncthreads();
-    for (int c = threadIdx.x; c < k; c += NT) {
-        const int j = idx[c];
-        if (j >= 0 && j < K)
-            atomicOr(&mask[j >> 5], 1u << (j & 31));
+// The dense columns' mask in LDS, for the largest magnitude of a row: a 16-bit word per
+// column (0x7fff, or 0 for a weak one: two instructions per pair of values) up to
+// kWideMask columns, a bit per column (set: weak) above.
+constexpr int kWideMask = 16384;
+template <bool WIDE>
+struct DenseMask {
+    uint32_t w[WIDE ? kWideMask / 2 : 65536 / 32];
+
+    // All threads of the block call it.
+    template <int NT>
+    __device__ __forceinline__ void fill(const int32_t* idx, int k, int K)
+    {
+        for (int i = threadIdx.x; i < (WIDE ? K >> 3 : K >> 7); i += NT)
+            reinterpret_cast<uint4*>(w)[i] = WIDE ? make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu)
+                                                  : make_uint4(0u, 0u, 0u, 0u);
+        if (!WIDE && (int)threadIdx.x < ((K >> 5) & 3))
+            w[((K >> 7) << 2) + threadIdx.x] = 0;
+        __syncthreads();
+        for (int c = threadIdx.x; c < k; c += NT) {
+            const int j = idx[c];
+            if (j >= 0 && j < K) {
+                if (WIDE)
+                    reinterpret_cast<uint16_t*>(w)[j] = 0;
+                else
+                    atomicOr(&w[j >> 5], 1u << (j & 31));
+            }
+        }
+        __syncthreads();
     }
-    __syncthreads();
-}
 
-// Largest |v| bits of 8 values whose weak columns have their bit set in w
-__device__ __forceinline__ uint32_t top8(uint4 v, uint32_t w, uint32_t top)
-{
-    const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+    // The largest of top and |v| over the dense ones of the 8 columns 8 p ..., as bits of
+    // the magnitudes (which order like them, a NaN above infinity), two 16-bit maxima
+    __device__ __forceinline__ uint32_t top(uint4 v, int p, uint32_t t) const
+    {
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+        const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+        uint32_t m[4];
+        if (WIDE) {
+            const uint4 q = reinterpret_cast<const uint4*>(w)[p];
+            m[0] = q.x, m[1] = q.y, m[2] = q.z, m[3] = q.w;
+        } else {
+            const uint32_t b = reinterpret_cast<const uint8_t*>(w)[p];
 #pragma unroll
-    for (int e = 0; e < 4; e++) {
-        const uint32_t lo = (w >> (2 * e)) & 1u ? 0u : d[e] & 0x7fffu;
-        const uint32_t hi = (w >> (2 * e + 1)) & 1u ? 0u : (d[e] >> 16) & 0x7fffu;
-        top = max(top, max(lo, hi));
+            for (int e = 0; e < 4; e++)
+                m[e] = ((b >> (2 * e)) & 1u ? 0u : 0x7fffu) | ((b >> (2 * e + 1)) & 1u ? 0u : 0x7fff0000u);
+        }
+        u16x2 r = __builtin_bit_cast(u16x2, t);
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            r = __builtin_elementwise_max(r, __builtin_bit_cast(u16x2, d[e] & m[e]));
+        return __builtin_bit_cast(uint32_t, r);
     }
-    return top;
-}
+    static __device__ __forceinline__ uint32_t both(uint32_t t) { return max(t & 0xffffu, t >> 16); }
+
+    __device__ __forceinline__ bool weak(int j) const
+    {
+        return WIDE ? reinterpret_cast<const uint16_t*>(w)[j] == 0 : (w[j >> 5] >> (j & 31)) & 1u;
+    }
+};
 
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v)
 {
@@ -89,15 +120,91 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v)
     return v;
 }
 
+// Eight consecutive values of a row of n fp16 from column c on (those that lie in the row)
+__device__ __forceinline__ void store8(uint16_t* row, int c, int n, uint4 v)
+{
+    typedef uint32_t u4_any __attribute__((ext_vector_type(4), aligned(2)));  // rows begin anywhere
+    if (c + 8 <= n) {
+        *reinterpret_cast<u4_any*>(row + c) = u4_any{v.x, v.y, v.z, v.w};
+        return;
+    }
+    const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+        if (c + e < n)
+            row[c + e] = (uint16_t)(d[e >> 1] >> (16 * (e & 1)));
+}
+
+// Four of them, from a lane's sums
+__device__ __forceinline__ void store4(uint16_t* row, int c, int n, i8_f4v v)
+{
+    typedef uint32_t u2_any __attribute__((ext_vector_type(2), aligned(2)));
+    const uint32_t lo = f2h(v[0]) | ((uint32_t)f2h(v[1]) << 16), hi = f2h(v[2]) | ((uint32_t)f2h(v[3]) << 16);
+    if (c + 4 <= n) {
+        *reinterpret_cast<u2_any*>(row + c) = u2_any{lo, hi};
+        return;
+    }
+    const uint32_t d[2] = {lo, hi};
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+        if (c + e < n)
+            row[c + e] = (uint16_t)(d[e >> 1] >> (16 * (e & 1)));
+}
+
+// A block's place among `blocks`: consecutive places share an XCD (blocks go to the eight
+// XCDs in turn), so that neighbouring tiles meet in one L2.
+__device__ __forceinline__ int xcd_place(int block, int blocks)
+{
+    const int per = blocks >> 3, even = per << 3;
+    return block < even ? (block & 7) * per + (block >> 3) : block;
+}
+
 __device__ __forceinline__ void dma16_lds(__amdgpu_buffer_rsrc_t r, char* lds, int voff)
 {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff, 0, 0, 0);
 }
 
+// At most VM of the wave's loads are still in flight (and LGKM of its LDS accesses, 15: any),
+// then the block's barrier. The builtin wait is one the compiler counts: it adds no wait of its
+// own for the loads of other stages before a stage is read (an asm statement's wait does
+// not spare that one).
+template <int VM, int LGKM = 0>
+__device__ __forceinline__ void stage_barrier()
+{
+    static_assert(VM < 64 && LGKM < 16, "fields of the instruction");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((VM & 15) | 0x70 | (LGKM << 8) | ((VM >> 4) << 14));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Stages of 64 bytes per row, four 16-byte pieces: piece p of row r lies in line r / 2
+// (128 bytes), slot (4 (r % 2) + p) ^ ((r / 4) % 4), so that 16 consecutive rows' pieces p
+// fall on all 64 banks. Byte of a piece; row and piece of the 16-byte unit u of a stage.
+__device__ __forceinline__ int stage_at(int r, int p)
+{
+    return (r >> 1) * 128 + ((((r & 1) << 2) | p) ^ ((r >> 2) & 3)) * 16;
+}
+__device__ __forceinline__ int stage_row(int u) { return (u >> 3) * 2 + ((((u & 7) ^ ((u >> 4) & 3))) >> 2); }
+__device__ __forceinline__ int stage_piece(int u) { return ((u & 7) ^ ((u >> 4) & 3)) & 3; }
+
+constexpr int kDeadLoad = 0x40000000;  // added to an offset: out of the buffer's range, zeros, nothing fetched
+
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t bytes_rsrc(const void* p, int64_t bytes)
 {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0,
                                              (int)(bytes < 0x7fffffff ? bytes : 0x7fffffff), 0x00020000);
+}
+
+// The same where the compiler cannot see that every lane has the same pointer (the
+// descriptor of a load must be scalar, or the load becomes a loop over the lanes)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* p, int64_t bytes)
+{
+    const uint64_t u = (uint64_t)(uintptr_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)u), hi = __builtin_amdgcn_readfirstlane((uint32_t)(u >> 32));
+    const int n = __builtin_amdgcn_readfirstlane((int)(bytes < 0x7fffffff ? bytes : 0x7fffffff));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((uintptr_t)(((uint64_t)hi << 32) | lo)), (short)0, n,
+                                             0x00020000);
 }
 
 }  // namespace

@@ -1,5 +1,5 @@
 """The integer form's pack and product against the definition in 64 bits, over the
-forms' borders (tokens 1, 4 | 5, 16 | 17, 128 | 129), odd and ragged sizes, no weak
+forms' borders (tokens 4 | 5, 16 | 17, 32 | 33, 64 | 65, 256 | 257), odd and ragged sizes, no weak
 column, every column weak, zero rows, non-finite tokens, streams, graphs."""
 import pytest
 import torch
@@ -36,7 +36,7 @@ def test_pack_is_the_definition(N, K, k):
     assert torch.equal(out["codes"], L["codes"])
 
 
-@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 16, 17, 33, 128, 129, 300])
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 16, 17, 32, 33, 64, 65, 128, 256, 257, 300, 513])
 @pytest.mark.parametrize("N,K,k", SIZES)
 def test_product(N, K, k, M):
     owq = _owq()
