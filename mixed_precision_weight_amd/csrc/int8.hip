@@ -73,15 +73,6 @@ struct QuantBatch {
     QuantLayer L[kInt8MaxLayers];
 };
 
-// Byte of the 16-byte piece p of a row in the panel layout: panels of `rows` rows, 64
-// bytes of each row together (a stage of the tiled product; rows K bytes apart would
-// keep the loads to 64-byte pieces all over the matrix).
-__device__ __forceinline__ int64_t panel_at(int64_t row, int rows, int64_t row_bytes, int p)
-{
-    const int64_t panel = row / rows;
-    return panel * rows * row_bytes + ((int64_t)(p >> 2) * rows + (row - panel * rows)) * 64 + (p & 3) * 16;
-}
-
 // The tokens of the streaming product: one block per token and layer (blockIdx.y), its
 // scale, its codes up to Kq columns (zeros past K) and its weak columns padded to kp with
 // zeros. The codes go in the order of that product's B operand (16 tokens together,

@@ -17,6 +17,11 @@ namespace {
 typedef uint16_t u16x8_any __attribute__((ext_vector_type(8), aligned(2)));
 typedef float f4_any8 __attribute__((ext_vector_type(4), aligned(4)));
 
+constexpr int kDxTokens = 128, kDxCols = 128;  // of a tile
+constexpr int kDxRows = 32;                    // of the layer per stage
+constexpr int kDxStage = kDxTokens * 64 + kDxRows * kDxCols;
+constexpr int kDxLoads = 2 + 1;  // per wave and stage, of g and of the codes
+
 struct BwdArgs8 {
     const int8_t* q;
     const float* s;
@@ -26,22 +31,39 @@ struct BwdArgs8 {
     const uint16_t* dy;
     uint16_t* dx;
     float* dw;
-    uint16_t* g;     // [M][Np]
+    uint16_t* g;     // [M][Np] in panels of kDxTokens
     float* unscale;  // [M]
     uint16_t* wwt;   // [kp][Np]
     uint16_t* xwt;   // [kp][Mp]
     float* part;     // [slices][M][kp]
-    int32_t M, N, K, k, Np, Mp, kp, slices, mblocks;
+    i8_f4v* sums;    // [split][tile][wave][16][lane], where splits > 1
+    int32_t M, N, K, k, Np, Mp, kp, slices, mblocks, splits;
 };
 
 // ------------------------------------------------------- the scaled gradients --
 
-// One block per token: g = dy scale 2^e, the largest magnitude in [2^14, 2^15), zeros
-// from N to Np.
-__global__ __launch_bounds__(256) void k_int8_scale_dy(const BwdArgs8 a)
+// The first blocks: one per token, g = dy scale 2^e, the largest magnitude in [2^14, 2^15),
+// zeros from N to Np. The others: the weak weights and the tokens' weak columns with the
+// long side contiguous, padded with zeros: wwt[c][i], xwt[c][m].
+__global__ __launch_bounds__(256) void k_int8_prepare(const BwdArgs8 a, int tokens)
 {
     __shared__ float red[4];
     const int tid = threadIdx.x, N = a.N;
+    if ((int)blockIdx.x >= tokens) {
+        const int64_t nw = a.dx ? (int64_t)a.kp * a.Np : 0, nx = a.dw ? (int64_t)a.kp * a.Mp : 0;
+        const int64_t step = (int64_t)((int)gridDim.x - tokens) * 256;
+        for (int64_t e = (int64_t)((int)blockIdx.x - tokens) * 256 + tid; e < nw + nx; e += step) {
+            if (e < nw) {
+                const int c = (int)(e / a.Np), i = (int)(e % a.Np);
+                a.wwt[e] = c < a.k && i < N ? a.ww[(int64_t)i * a.k + c] : (uint16_t)0;
+            } else {
+                const int c = (int)((e - nw) / a.Mp), m = (int)((e - nw) % a.Mp);
+                const int j = c < a.k ? a.idx[c] : -1;
+                a.xwt[e - nw] = m < a.M && j >= 0 && j < a.K ? a.x[(int64_t)m * a.K + j] : (uint16_t)0;
+            }
+        }
+        return;
+    }
     const int64_t m = blockIdx.x;
     const uint16_t* dy = a.dy + m * N;
     uint32_t top = 0;  // as bits: a NaN is the largest
@@ -69,8 +91,8 @@ __global__ __launch_bounds__(256) void k_int8_scale_dy(const BwdArgs8 a)
     const float f = scaled ? __builtin_bit_cast(float, (uint32_t)min(max(268 - ex, 1), 254) << 23) : 1.0f;
     if (tid == 0)  // codes come as code 2^-9
         a.unscale[m] = 512.0f / f;
-    uint16_t* g = a.g + m * a.Np;
-    for (int p = tid * 8; p < a.Np; p += 2048) {  // Np is a multiple of 64
+    char* const g = reinterpret_cast<char*>(a.g);
+    for (int p = tid * 8; p < a.Np; p += 2048) {  // Np is a multiple of 32
         uint32_t o[4];
         if (p + 8 <= N) {
             const u16x8_any v = *reinterpret_cast<const u16x8_any*>(dy + p);
@@ -87,24 +109,7 @@ __global__ __launch_bounds__(256) void k_int8_scale_dy(const BwdArgs8 a)
                        ((uint32_t)(n + 1 < N ? f2h(h2f(dy[n + 1]) * a.s[n + 1] * f) : 0u) << 16);
             }
         }
-        *reinterpret_cast<uint4*>(g + p) = make_uint4(o[0], o[1], o[2], o[3]);
-    }
-}
-
-// The weak weights and the tokens' weak columns with the long side contiguous, padded
-// with zeros: wwt[c][i], xwt[c][m].
-__global__ __launch_bounds__(256) void k_int8_weak_t(const BwdArgs8 a)
-{
-    const int64_t nw = a.dx ? (int64_t)a.kp * a.Np : 0, nx = a.dw ? (int64_t)a.kp * a.Mp : 0;
-    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < nw + nx; e += (int64_t)gridDim.x * 256) {
-        if (e < nw) {
-            const int c = (int)(e / a.Np), i = (int)(e % a.Np);
-            a.wwt[e] = c < a.k && i < a.N ? a.ww[(int64_t)i * a.k + c] : (uint16_t)0;
-        } else {
-            const int c = (int)((e - nw) / a.Mp), m = (int)((e - nw) % a.Mp);
-            const int j = c < a.k ? a.idx[c] : -1;
-            a.xwt[e - nw] = m < a.M && j >= 0 && j < a.K ? a.x[(int64_t)m * a.K + j] : (uint16_t)0;
-        }
+        *reinterpret_cast<uint4*>(g + panel_at(m, kDxTokens, (int64_t)2 * a.Np, p >> 3)) = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
@@ -130,12 +135,11 @@ __device__ __forceinline__ void add_waves(float (*red)[16 * 64], const i8_f16v& 
 }
 
 // dy w_weak: 32 tokens x 32 weak columns over a slice of the rows
-__global__ __launch_bounds__(64 * kWeakWaves) void k_int8_weak_dx(const BwdArgs8 a)
+__device__ __forceinline__ void weak_dx(const BwdArgs8& a, float (*red)[16 * 64], int block)
 {
-    __shared__ float red[kWeakWaves][16 * 64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l32 = lane & 31, h = lane >> 5;
-    const int m0 = (int)blockIdx.x * 32, c0 = (int)blockIdx.y * 32, sl = blockIdx.z;
+    const int c0 = (int)blockIdx.y * 32, sl = block % a.slices, m0 = block / a.slices * 32;
     const int steps = a.Np >> 4, per = (steps + a.slices - 1) / a.slices;
     const int s0 = sl * per, s1 = min(steps, s0 + per);
     const uint16_t* dy = a.dy + (int64_t)min(m0 + l32, a.M - 1) * a.N;
@@ -166,28 +170,12 @@ __global__ __launch_bounds__(64 * kWeakWaves) void k_int8_weak_dx(const BwdArgs8
     }
 }
 
-// The slices' sums into dx's weak columns
-__global__ __launch_bounds__(256) void k_int8_weak_put(const BwdArgs8 a)
-{
-    const int64_t n = (int64_t)a.M * a.k;
-    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
-        const int64_t m = e / a.k;
-        const int c = (int)(e % a.k), j = a.idx[c];
-        float v = 0.0f;
-        for (int sl = 0; sl < a.slices; sl++)
-            v += a.part[((int64_t)sl * a.M + m) * a.kp + c];
-        if (j >= 0 && j < a.K)
-            a.dx[m * a.K + j] = f2h(v);
-    }
-}
-
 // dy^T x_weak: 32 rows x 32 weak columns over all tokens
-__global__ __launch_bounds__(64 * kWeakWaves) void k_int8_weak_dw(const BwdArgs8 a)
+__device__ __forceinline__ void weak_dw(const BwdArgs8& a, float (*red)[16 * 64], int block)
 {
-    __shared__ float red[kWeakWaves][16 * 64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l32 = lane & 31, h = lane >> 5;
-    const int i0 = (int)blockIdx.x * 32, c0 = (int)blockIdx.y * 32;
+    const int i0 = block * 32, c0 = (int)blockIdx.y * 32;
     const uint16_t* dy = a.dy + min(i0 + l32, a.N - 1);
     const uint16_t* xw = a.xwt + (int64_t)(c0 + l32) * a.Mp;
     i8_f16v acc;
@@ -213,163 +201,283 @@ __global__ __launch_bounds__(64 * kWeakWaves) void k_int8_weak_dw(const BwdArgs8
     }
 }
 
-// ------------------------------------------------------------- dense part of dx --
-
-template <int FM, int FN, int WM, int WN>
-struct TileDx {
-    static constexpr int NT = 64 * WM * WN;
-    static constexpr int BM = 32 * FM * WM, BJ = 32 * FN * WN;
-    static constexpr int DA = BM * 128 / 16 / NT;
-    static constexpr int QUADS = BJ / 4;           // 4-column groups
-    static constexpr int GROUPS = QUADS * 8 / NT;  // (4 columns, 8 rows) pieces per thread and stage
-    static_assert(DA * NT * 16 == BM * 128 && GROUPS * NT == QUADS * 8, "a stage must split evenly over the threads");
-};
-
-// slot of piece p (8 values of the contraction) of row r of a stage: reads take 32
-// consecutive rows, the writes of codes every fourth row
-__device__ __forceinline__ int dx_slot(int r, int p) { return p ^ ((r ^ (r >> 3)) & 7); }
-
-// BM tokens x BJ columns per block; the contraction runs over the layer's rows, 64 at a
-// time: g by direct-to-LDS loads, the codes through registers, where 8 rows of 4 columns
-// are turned round and widened (a byte pair becomes two fp16 subnormals, one fused
-// multiply-add makes them code 2^-9).
-template <int FM, int FN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4))) void k_int8_dx(const BwdArgs8 a)
+// Both sums over dy in one launch: the first `dws` blocks the weights', the others the tokens'
+__global__ __launch_bounds__(64 * kWeakWaves) void k_int8_weak_sums(const BwdArgs8 a, int dws)
 {
-    using T = TileDx<FM, FN, WM, WN>;
-    constexpr int BM = T::BM, BJ = T::BJ;
-    __shared__ __attribute__((aligned(1024))) char s0[(BM + BJ) * 128];
-    __shared__ __attribute__((aligned(1024))) char s1[(BM + BJ) * 128];
-    const int M = a.M, N = a.N, K = a.K, Np = a.Np;
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave % WM, wn = wave / WM;
-    const int l32 = lane & 31, h = lane >> 5;
-    const int m0 = ((int)blockIdx.x % a.mblocks) * BM, j0 = ((int)blockIdx.x / a.mblocks) * BJ;
-    const int mv = min(BM, M - m0);
-    const __amdgpu_buffer_rsrc_t gr = bytes_rsrc(a.g + (int64_t)m0 * Np, (int64_t)mv * Np * 2);
-    int gsrc[T::DA];
-#pragma unroll
-    for (int t = 0; t < T::DA; t++) {
-        const int u = (wave * T::DA + t) * 64 + lane, row = u >> 3;
-        gsrc[t] = min(row, mv - 1) * Np * 2 + dx_slot(row, u & 7) * 16;
+    __shared__ float red[kWeakWaves][16 * 64];
+    if ((int)blockIdx.x < dws)
+        weak_dw(a, red, (int)blockIdx.x);
+    else
+        weak_dx(a, red, (int)blockIdx.x - dws);
+}
+
+// dx's weak columns among columns j0 .. j0 + cols - 1, of tokens m0 .. m0 + n - 1, from the
+// slices' sums, by one wave, which has written other values there: over those.
+__device__ __forceinline__ void weak_put(const BwdArgs8& a, int m0, int n, int j0, int cols)
+{
+    if (a.k == 0)
+        return;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    int c = 0;  // the first weak column at or behind j0 (they ascend)
+    for (int hi = a.k; c < hi;) {
+        const int mid = (c + hi) >> 1;
+        if (__builtin_amdgcn_readfirstlane(a.idx[mid]) < j0)
+            c = mid + 1;
+        else
+            hi = mid;
     }
-    auto dma = [&](int c, char* stage) {
-#pragma unroll
-        for (int t = 0; t < T::DA; t++)
-            dma16_lds(gr, stage + (wave * T::DA + t) * 1024, gsrc[t] + c * 128);
-    };
-    // this thread's pieces: 4 columns 4 q4, rows 8 o .. 8 o + 7 of the stage
-    auto load = [&](int c, uint32_t (&v)[T::GROUPS][8]) {
-        const int64_t i0 = (int64_t)c * 64;
-        const __amdgpu_buffer_rsrc_t qr =
-            bytes_rsrc(a.q + (i0 < N ? i0 * K + j0 : 0), i0 < N ? (int64_t)min(64, (int)(N - i0)) * K - j0 : 0);
-#pragma unroll
-        for (int t = 0; t < T::GROUPS; t++) {
-            const int u = t * T::NT + tid, q4 = u % T::QUADS, o = u / T::QUADS;
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                v[t][e] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(qr, (8 * o + e) * K + 4 * q4, 0, 0);
-        }
-    };
-    auto put = [&](const uint32_t (&v)[T::GROUPS][8], char* stage) {
-        const half2_t mul = {(_Float16)32768.0f, (_Float16)32768.0f}, add = {(_Float16)-0.25f, (_Float16)-0.25f};
-#pragma unroll
-        for (int t = 0; t < T::GROUPS; t++) {
-            const int u = t * T::NT + tid, q4 = u % T::QUADS, o = u / T::QUADS;
-            uint32_t d[8];
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                d[e] = v[t][e] ^ 0x80808080u;  // code + 128
-#pragma unroll
-            for (int b = 0; b < 4; b++) {
-                uint32_t w[4];
-#pragma unroll
-                for (int p = 0; p < 4; p++) {
-                    const uint32_t two = __builtin_amdgcn_perm(d[2 * p + 1], d[2 * p],
-                                                               0x0c000c00u | (uint32_t)((4 + b) << 16) | (uint32_t)b);
-                    w[p] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(half2_t, two), mul, add));
-                }
-                const int row = 4 * q4 + b;
-                *reinterpret_cast<uint4*>(stage + (BM + row) * 128 + dx_slot(row, o) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
-    };
-    i8_f16v acc[FM][FN];
-#pragma unroll
-    for (int i = 0; i < FM; i++)
-#pragma unroll
-        for (int f = 0; f < FN; f++)
-#pragma unroll
-            for (int r = 0; r < 16; r++)
-                acc[i][f][r] = 0.0f;
-    const int chunks = Np >> 6;
-    uint32_t cv[T::GROUPS][8];
-    auto step = [&](int c, const char* cur, char* nxt) {
-        stage_barrier<0>();
-        if (c + 1 < chunks) {
-            dma(c + 1, nxt);
-            put(cv, nxt);
-            load(c + 2, cv);
-        }
-        if (c < chunks) {
-#pragma unroll
-            for (int st = 0; st < 4; st++) {
-                half8_t av[FM], bv[FN];
-#pragma unroll
-                for (int i = 0; i < FM; i++) {
-                    const int row = wm * 32 * FM + 32 * i + l32;
-                    av[i] = *reinterpret_cast<const half8_t*>(cur + row * 128 + dx_slot(row, st * 2 + h) * 16);
-                }
-#pragma unroll
-                for (int f = 0; f < FN; f++) {
-                    const int row = wn * 32 * FN + 32 * f + l32;
-                    bv[f] = *reinterpret_cast<const half8_t*>(cur + (BM + row) * 128 + dx_slot(row, st * 2 + h) * 16);
-                }
-#pragma unroll
-                for (int i = 0; i < FM; i++)
-#pragma unroll
-                    for (int f = 0; f < FN; f++)
-                        acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(av[i], bv[f], acc[i][f], 0, 0, 0);
-            }
-        }
-    };
-    load(0, cv);
-    dma(0, s0);
-    put(cv, s0);
-    load(1, cv);
-    for (int c = 0; c < chunks; c += 2) {
-        step(c, s0, s1);
-        step(c + 1, s1, s0);
-    }
-#pragma unroll
-    for (int i = 0; i < FM; i++) {
-        const int mb = wm * 32 * FM + 32 * i;
-        float un[16];
-#pragma unroll
-        for (int r = 0; r < 16; r++)
-            un[r] = a.unscale[m0 + min(mb + 8 * (r >> 2) + 4 * h + (r & 3), mv - 1)];
-#pragma unroll
-        for (int f = 0; f < FN; f++) {
-            const int j = j0 + wn * 32 * FN + 32 * f + l32;
-#pragma unroll
-            for (int r = 0; r < 16; r++) {
-                const int m = m0 + mb + 8 * (r >> 2) + 4 * h + (r & 3);
-                if (m < M && j < K)
-                    a.dx[(int64_t)m * K + j] = f2h(acc[i][f][r] * un[r]);
-            }
+    for (; c < a.k; c++) {
+        const int j = __builtin_amdgcn_readfirstlane(a.idx[c]);
+        if (j < j0 || j >= min(j0 + cols, a.K))
+            break;
+        for (int t = threadIdx.x & 63; t < n; t += 64) {
+            float v = 0.0f;
+            for (int sl = 0; sl < a.slices; sl++)
+                v += a.part[((int64_t)sl * a.M + m0 + t) * a.kp + c];
+            a.dx[(int64_t)(m0 + t) * a.K + j] = f2h(v);
         }
     }
 }
 
-template <int FM, int FN, int WM, int WN>
-hipError_t launch_dx(BwdArgs8 a, hipStream_t s)
+// ------------------------------------------------------------- dense part of dx --
+
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+
+// 128 tokens x 128 columns per block of 4 waves (64 x 64 each), two blocks per CU, which
+// run at their own pace; the contraction runs over the layer's rows, 32 at a time, in a
+// ring of six stages, two per barrier, that is filled two to four ahead by direct-to-LDS
+// loads: g (panels of 128 tokens, 64 bytes of each together) as in the forward product,
+// the codes as they lie. ds_read_tr turns 8 rows of the codes round on the way to the
+// registers, where they become fp16: a byte pair is read as two fp16 subnormals, which one
+// fused multiply-add makes code 2^-9, exactly. (Turning the codes round on the way into LDS
+// instead needs registers and eight-way bank conflicts: 315 us for 2048 tokens, 11008 x
+// 4096.) The columns are the matrix instruction's A, so that a lane ends with four
+// consecutive columns of one token.
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_int8_dx(const BwdArgs8 a)
 {
-    using T = TileDx<FM, FN, WM, WN>;
-    a.mblocks = (a.M + T::BM - 1) / T::BM;
-    const int64_t blocks = (int64_t)a.mblocks * ((a.K + T::BJ - 1) / T::BJ);
-    hipLaunchKernelGGL((k_int8_dx<FM, FN, WM, WN>), dim3((unsigned)blocks), dim3(T::NT), 0, s, a);
-    return hipGetLastError();
+    __shared__ __attribute__((aligned(1024))) char s0[kDxStage];
+    __shared__ __attribute__((aligned(1024))) char s1[kDxStage];
+    __shared__ __attribute__((aligned(1024))) char s2[kDxStage];
+    __shared__ __attribute__((aligned(1024))) char s3[kDxStage];
+    __shared__ __attribute__((aligned(1024))) char s4[kDxStage];
+    __shared__ __attribute__((aligned(1024))) char s5[kDxStage];
+    __shared__ float un[kDxTokens];
+    constexpr int FM = 2, FJ = 2;
+    const int M = a.M, N = a.N, K = a.K;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave & 1, wj = wave >> 1;
+    const int l32 = lane & 31, h = lane >> 5;
+    const int place = xcd_place((int)blockIdx.x, (int)gridDim.x), tiles = (int)gridDim.x / a.splits;
+    const int tile = place % tiles, split = place / tiles;
+    const int m0 = (tile % a.mblocks) * kDxTokens, j0 = (tile / a.mblocks) * kDxCols;
+    const int mv = min(kDxTokens, M - m0);
+    const __amdgpu_buffer_rsrc_t gr = uniform_rsrc(a.g + (int64_t)m0 * a.Np, (int64_t)2 * kDxTokens * a.Np);
+    int gsrc[2];
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+        const int u = (wave * 2 + t) * 64 + lane;
+        gsrc[t] = stage_row(u) * 64 + stage_piece(u) * 16;
+    }
+    // codes: 128 bytes per row; the 16-byte piece p of row r in slot p ^ (r % 8)
+    const int qrow = tid >> 3, qcol = ((tid & 7) ^ (qrow & 7)) * 16;
+    const int qsrc = j0 + qcol < K ? qrow * K + qcol : kDeadLoad;
+    const int all = a.Np / kDxRows;
+    const int c0 = (int)((int64_t)all * split / a.splits), c1 = (int)((int64_t)all * (split + 1) / a.splits);
+    auto dma = [&](int c, char* stage) {
+        const int dead = c < c1 ? 0 : kDeadLoad;
+        const int i0 = min(c, c1 - 1) * kDxRows;  // (Np is N rounded up: the last stage has a row)
+        const __amdgpu_buffer_rsrc_t qr = uniform_rsrc(a.q + (int64_t)i0 * K + j0, (int64_t)min(kDxRows, N - i0) * K - j0);
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+            dma16_lds(gr, stage + (wave * 2 + t) * 1024, gsrc[t] + (i0 * (2 * kDxTokens) | dead));
+        dma16_lds(qr, stage + kDxTokens * 64 + wave * 1024, qsrc | dead);
+    };
+    i8_f16v acc[FM][FJ];
+#pragma unroll
+    for (int i = 0; i < FM; i++)
+#pragma unroll
+        for (int f = 0; f < FJ; f++)
+#pragma unroll
+            for (int r = 0; r < 16; r++)
+                acc[i][f][r] = 0.0f;
+    // g: this lane's pieces h and 2 + h of its tokens. Codes: in a group of 16 lanes, lane i
+    // names 8 bytes of row i / 2, columns 8 (i % 2), and gets column i of the 8 rows.
+    const int p0 = wm * FM * 2048 + stage_at(l32, h), p1 = wm * FM * 2048 + stage_at(l32, 2 + h);
+    int qa[2][FJ];
+#pragma unroll
+    for (int st = 0; st < 2; st++)
+#pragma unroll
+        for (int f = 0; f < FJ; f++) {
+            const int r = 16 * st + 8 * h + ((lane & 15) >> 1), piece = (wj * FJ + f) * 2 + ((lane >> 4) & 1);
+            qa[st][f] = kDxTokens * 64 + r * kDxCols + ((piece ^ (r & 7)) * 16) + (lane & 1) * 8;
+        }
+    // codes as read (two 16-row steps of a stage) and as fp16, g: the codes are read two
+    // steps ahead of their products and widened one ahead, g is read one ahead
+    i32x2 raw[2][FJ];
+    half8_t cv[2][FJ], gv[2][FM];
+    auto read_codes = [&](const char* stage, int st) {
+#pragma unroll
+        for (int f = 0; f < FJ; f++)
+            raw[st][f] = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2*)(stage + qa[st][f]));
+    };
+    auto read_g = [&](const char* stage, int st) {
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+            gv[st][i] = *reinterpret_cast<const half8_t*>(stage + (st ? p1 : p0) + i * 2048);
+    };
+    const half2_t mul = {(_Float16)32768.0f, (_Float16)32768.0f}, add = {(_Float16)-0.25f, (_Float16)-0.25f};
+    auto widen = [&](int st) {
+#pragma unroll
+        for (int f = 0; f < FJ; f++) {
+            const uint32_t d[2] = {(uint32_t)raw[st][f].x ^ 0x80808080u, (uint32_t)raw[st][f].y ^ 0x80808080u};  // code + 128
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const uint32_t two = __builtin_amdgcn_perm(0u, d[e >> 1], e & 1 ? 0x0c030c02u : 0x0c010c00u);
+                w[e] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(half2_t, two), mul, add));
+            }
+            cv[st][f] = __builtin_bit_cast(half8_t, make_uint4(w[0], w[1], w[2], w[3]));
+        }
+    };
+    auto product = [&](int st) {
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+#pragma unroll
+            for (int f = 0; f < FJ; f++)
+                acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(cv[st][f], gv[st][i], acc[i][f], 0, 0, 0);
+        // the reads and the widening between the products
+#pragma unroll
+        for (int i = 0; i < FM * FJ; i++) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+        }
+    };
+    // products of the stage in cur, and the reads ahead from next
+    auto stage = [&](const char* cur, const char* next) {
+        read_codes(next, 0);
+        read_g(cur, 1);
+        widen(1);
+        product(0);
+        read_codes(next, 1);
+        read_g(next, 0);
+        widen(0);
+        product(1);
+    };
+    // two stages per barrier: c in sa, c + 1 in sb, c + 2 in next, all whole; c + 4 and c + 5
+    // go where the two before were
+    auto step = [&](int c, const char* sa, const char* sb, const char* next, char* fa, char* fb) {
+        stage_barrier<kDxLoads, 15>();
+        dma(c + 4, fa);
+        dma(c + 5, fb);
+        if (c < c1) {
+            stage(sa, sb);
+            stage(sb, next);
+            // their reads are done before this wave lets them be overwritten
+#pragma unroll
+            for (int i = 0; i < FM; i++)
+                asm volatile("" ::"v"(gv[1][i]));
+        }
+    };
+    dma(c0, s0);
+    dma(c0 + 1, s1);
+    dma(c0 + 2, s2);
+    dma(c0 + 3, s3);
+    if (tid < kDxTokens)
+        un[tid] = a.unscale[m0 + min(tid, mv - 1)];
+    stage_barrier<0>();
+    read_codes(s0, 0);
+    read_codes(s0, 1);
+    read_g(s0, 0);
+    widen(0);
+    for (int c = c0; c < c1; c += 6) {  // (a stage past c1 holds zeros)
+        step(c, s0, s1, s2, s4, s5);
+        step(c + 2, s2, s3, s4, s0, s1);
+        step(c + 4, s4, s5, s0, s2, s3);
+    }
+#pragma unroll
+    for (int f = 0; f < FJ; f++)
+        asm volatile("" ::"v"(raw[0][f]), "v"(raw[1][f]));
+    stage_barrier<0>();  // the loads past the end have written their zeros
+    if (a.splits > 1) {
+        i8_f4v* const sums = a.sums + ((int64_t)place * 4 + wave) * (FM * FJ * 4 * 64) + lane;
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+#pragma unroll
+            for (int f = 0; f < FJ; f++)
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                    sums[((i * FJ + f) * 4 + q) * 64] =
+                        i8_f4v{acc[i][f][4 * q], acc[i][f][4 * q + 1], acc[i][f][4 * q + 2], acc[i][f][4 * q + 3]};
+        return;
+    }
+    // 32 tokens x 64 columns of the wave at a time: token t's piece p of 8 columns in slot
+    // p ^ (t % 8) of its 128 bytes
+    char* const mine = (wave < 2 ? s0 : s1) + (wave & 1) * 4096;
+#pragma unroll
+    for (int i = 0; i < FM; i++) {
+        const float sc = un[wm * 32 * FM + 32 * i + l32];
+#pragma unroll
+        for (int f = 0; f < FJ; f++)
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const i8_f16v& o = acc[i][f];
+                *reinterpret_cast<uint2*>(mine + l32 * 128 + ((f * 4 + q) ^ (l32 & 7)) * 16 + h * 8) =
+                    make_uint2(f2h(o[4 * q] * sc) | ((uint32_t)f2h(o[4 * q + 1] * sc) << 16),
+                               f2h(o[4 * q + 2] * sc) | ((uint32_t)f2h(o[4 * q + 3] * sc) << 16));
+            }
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const int t = e * 8 + (lane >> 3), p = lane & 7;
+            const uint4 v = *reinterpret_cast<const uint4*>(mine + t * 128 + (p ^ (t & 7)) * 16);
+            const int m = m0 + wm * 32 * FM + 32 * i + t;
+            if (m < M)
+                store8(a.dx + (int64_t)m * K, j0 + wj * 64 + 8 * p, K, v);
+        }
+        asm volatile("" ::: "memory");
+    }
+    weak_put(a, m0 + wm * 64, min(64, M - (m0 + wm * 64)), j0 + wj * 64, 64);
+}
+
+// The splits' sums of 32 tokens x 32 columns, a wave each
+__global__ __launch_bounds__(64) void k_int8_dx_sum(const BwdArgs8 a, int tiles)
+{
+    const int lane = threadIdx.x, l32 = lane & 31, h = lane >> 5;
+    const int piece = (int)blockIdx.x & 15, tile = (int)blockIdx.x >> 4;
+    const int wave = piece >> 2, i = (piece >> 1) & 1, f = piece & 1;  // as in k_int8_dx
+    const int m0 = (tile % a.mblocks) * kDxTokens + (wave & 1) * 64 + 32 * i;
+    const int j0 = (tile / a.mblocks) * kDxCols + (wave >> 1) * 64 + 32 * f;
+    if (m0 >= a.M || j0 >= a.K)
+        return;
+    const i8_f4v* p = a.sums + ((int64_t)tile * 4 + wave) * (16 * 64) + (i * 2 + f) * (4 * 64) + lane;
+    i8_f4v sum[4];
+#pragma unroll
+    for (int q = 0; q < 4; q++)
+        sum[q] = p[q * 64];
+    for (int s = 1; s < a.splits; s++)
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+            sum[q] += p[(int64_t)s * tiles * 4 * (16 * 64) + q * 64];
+    const int m = m0 + l32;
+    if (m < a.M) {
+        const float f = a.unscale[m];
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+            store4(a.dx + (int64_t)m * a.K, j0 + 8 * q + 4 * h, a.K, sum[q] * f);
+    }
+    weak_put(a, m0, min(32, a.M - m0), j0, 32);
+}
+
+// Blocks per tile: as many as fill the CUs, each with at least 8 stages
+int dx_splits(int64_t M, int64_t N, int64_t K)
+{
+    const int64_t tiles = (M + kDxTokens - 1) / kDxTokens * ((K + kDxCols - 1) / kDxCols);
+    int64_t sp = 512 / tiles;
+    const int64_t most = (N + kDxRows - 1) / kDxRows / 8;
+    sp = sp < most ? sp : most;
+    return (int)(sp < 1 ? 1 : sp);
 }
 
 constexpr int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -378,25 +486,27 @@ constexpr int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 Int8BwdPlan int8_bwd_plan(int64_t N, int64_t K, int32_t k, int64_t M)
 {
-    (void)K;
     Int8BwdPlan p{};
-    p.Np = up(N, 64);
+    p.Np = up(N, kDxRows);
     p.Mp = up(M, 16);
     p.kp = up(k, 32);
+    p.splits = dx_splits(M, N, K);
+    p.tiles = up(M, kDxTokens) / kDxTokens * (up(K, kDxCols) / kDxCols);
     // slices of the weak columns' sums: enough blocks, at least 512 rows each
     const int64_t tiles = (M + 31) / 32 * (p.kp / 32 > 0 ? p.kp / 32 : 1);
     int64_t sl = (512 + tiles - 1) / tiles;
     sl = sl < p.Np / 512 ? sl : p.Np / 512;
     p.slices = sl < 1 ? 1 : sl;
-    size_t off = (size_t)up(2 * M * p.Np, 256);
-    p.off_un = off;
-    off += (size_t)up(4 * M, 256);
-    p.off_wwt = off;
-    off += (size_t)up(2 * p.kp * p.Np, 256);
-    p.off_xwt = off;
-    off += (size_t)up(2 * p.kp * p.Mp, 256);
-    p.off_part = off;
-    off += (size_t)up(4 * p.slices * M * p.kp, 256);
+    size_t off = (size_t)(2 * up(M, kDxTokens) * p.Np);  // whole panels
+    auto take = [&](size_t& at, int64_t bytes) {
+        at = off;
+        off += (size_t)up(bytes, 256);
+    };
+    take(p.off_un, 4 * M);
+    take(p.off_wwt, 2 * p.kp * p.Np);
+    take(p.off_xwt, 2 * p.kp * p.Mp);
+    take(p.off_part, 4 * p.slices * M * p.kp);
+    take(p.off_sums, p.splits > 1 ? 4LL * p.splits * p.tiles * kDxTokens * kDxCols : 0);
     p.total = off;
     return p;
 }
@@ -407,28 +517,22 @@ hipError_t launch_linear_int8_backward(const Int8Desc& d, const uint16_t* dy, in
     char* const w = static_cast<char*>(ws);
     const BwdArgs8 a{d.q, d.s, d.idx, d.ww, d.x, dy, dx, d.k > 0 ? dw : nullptr, reinterpret_cast<uint16_t*>(w),
                      reinterpret_cast<float*>(w + p.off_un), reinterpret_cast<uint16_t*>(w + p.off_wwt),
-                     reinterpret_cast<uint16_t*>(w + p.off_xwt), reinterpret_cast<float*>(w + p.off_part), (int32_t)M,
-                     (int32_t)d.N, (int32_t)d.K, d.k, (int32_t)p.Np, (int32_t)p.Mp, (int32_t)p.kp, (int32_t)p.slices, 1};
+                     reinterpret_cast<uint16_t*>(w + p.off_xwt), reinterpret_cast<float*>(w + p.off_part),
+                     reinterpret_cast<i8_f4v*>(w + p.off_sums), (int32_t)M, (int32_t)d.N, (int32_t)d.K, d.k, (int32_t)p.Np,
+                     (int32_t)p.Mp, (int32_t)p.kp, (int32_t)p.slices, (int32_t)(up(M, kDxTokens) / kDxTokens), p.splits};
+    const int64_t turned = d.k > 0 ? ((dx ? p.kp * p.Np : 0) + (a.dw ? p.kp * p.Mp : 0) + 255) / 256 : 0;
+    const int64_t tokens = dx ? M : 0;
+    hipLaunchKernelGGL(k_int8_prepare, dim3((unsigned)(tokens + (turned < 1024 ? turned : 1024))), dim3(256), 0, s, a,
+                       (int)tokens);
     if (d.k > 0) {
-        const int64_t n = (a.dx ? p.kp * p.Np : 0) + (a.dw ? p.kp * p.Mp : 0);
-        const int64_t blocks = (n + 255) / 256;
-        hipLaunchKernelGGL(k_int8_weak_t, dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, s, a);
+        const int64_t dws = a.dw ? (d.N + 31) / 32 : 0, dxs = dx ? (M + 31) / 32 * p.slices : 0;
+        hipLaunchKernelGGL(k_int8_weak_sums, dim3((unsigned)(dws + dxs), (unsigned)(p.kp / 32)), dim3(64 * kWeakWaves), 0, s, a,
+                           (int)dws);
     }
-    if (a.dw)
-        hipLaunchKernelGGL(k_int8_weak_dw, dim3((unsigned)((d.N + 31) / 32), (unsigned)(p.kp / 32)), dim3(64 * kWeakWaves), 0,
-                           s, a);
     if (dx) {
-        if (d.k > 0)
-            hipLaunchKernelGGL(k_int8_weak_dx, dim3((unsigned)((M + 31) / 32), (unsigned)(p.kp / 32), (unsigned)p.slices),
-                               dim3(64 * kWeakWaves), 0, s, a);
-        hipLaunchKernelGGL(k_int8_scale_dy, dim3((unsigned)M), dim3(256), 0, s, a);
-        const hipError_t e = M > 128 ? launch_dx<4, 2, 2, 4>(a, s) : launch_dx<1, 1, 1, 4>(a, s);
-        if (e != hipSuccess)
-            return e;
-        if (d.k > 0) {
-            const int64_t blocks = (M * d.k + 255) / 256;
-            hipLaunchKernelGGL(k_int8_weak_put, dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, s, a);
-        }
+        hipLaunchKernelGGL(k_int8_dx, dim3((unsigned)(p.tiles * p.splits)), dim3(256), 0, s, a);
+        if (p.splits > 1)
+            hipLaunchKernelGGL(k_int8_dx_sum, dim3((unsigned)(16 * p.tiles)), dim3(64), 0, s, a, (int)p.tiles);
     }
     return hipGetLastError();
 }

@@ -151,6 +151,15 @@ __device__ __forceinline__ void store4(uint16_t* row, int c, int n, i8_f4v v)
             row[c + e] = (uint16_t)(d[e >> 1] >> (16 * (e & 1)));
 }
 
+// Byte of the 16-byte piece p of a row in the panel layout: panels of `rows` rows, 64
+// bytes of each row together (a stage of the tiled product; rows K bytes apart would
+// keep the loads to 64-byte pieces all over the matrix).
+__device__ __forceinline__ int64_t panel_at(int64_t row, int rows, int64_t row_bytes, int p)
+{
+    const int64_t panel = row / rows;
+    return panel * rows * row_bytes + ((int64_t)(p >> 2) * rows + (row - panel * rows)) * 64 + (p & 3) * 16;
+}
+
 // A block's place among `blocks`: consecutive places share an XCD (blocks go to the eight
 // XCDs in turn), so that neighbouring tiles meet in one L2.
 __device__ __forceinline__ int xcd_place(int block, int blocks)

@@ -256,8 +256,9 @@ hipError_t launch_linear_int8(const Int8Desc* d, int count, int64_t M, void* con
 
 // Its backward: padded sizes, row slices of the weak columns' part of dx, workspace offsets
 struct Int8BwdPlan {
-    int64_t Np, Mp, kp, slices;
-    size_t off_un, off_wwt, off_xwt, off_part, total;
+    int64_t Np, Mp, kp, slices, tiles;
+    int32_t splits;
+    size_t off_un, off_wwt, off_xwt, off_part, off_sums, total;
 };
 constexpr int64_t kInt8BwdMax = (int64_t)1 << 20;  // tokens and rows
 Int8BwdPlan int8_bwd_plan(int64_t N, int64_t K, int32_t k, int64_t M);
