@@ -29,23 +29,37 @@ struct NsItem {
     int32_t rows, cols;
     float scale;
     int32_t half;     // 1: fp16, 0: fp32
-    int32_t slices;   // of the long side (short form: Gram partials; long form: split sums)
-    int32_t block0;   // first block of its class's Gram launch
-    int32_t apply0;   // first block of its class's last launch
-    int32_t pad;
+    int32_t tiles;    // short form: 16-wide tiles of the short side (2, 4 or 6)
+    int32_t slices;   // of the long side, a block of k_ns_gram each
+    int32_t gram0, apply0;  // first blocks of k_ns_gram and k_ns_apply
 };
 static_assert(sizeof(NsItem) == 56, "table entry");
 
 constexpr int kNsArg = 64;  // table entries per launch of k_ns_table (kernel arguments below 4 KB)
 struct NsArgs {
     NsItem it[kNsArg];
-    int32_t count;
+    int32_t count, first;  // first: place of the first one in the table
 };
 
-__global__ __launch_bounds__(64) void k_ns_table(const NsArgs a, NsItem* table)
+// 16-element runs of the long side per wave of k_ns_apply, and elements per block
+constexpr int ns_runs(int T) { return T == 2 ? 4 : 2; }
+constexpr int ns_apply_len(int T) { return 4 * 16 * ns_runs(T); }
+
+// A block per matrix: its table entry, and which matrix each block of k_ns_gram and
+// k_ns_apply works on.
+__global__ __launch_bounds__(256) void k_ns_table(const NsArgs a, NsItem* table, int32_t* gram_item, int32_t* apply_item)
 {
-    if ((int)threadIdx.x < a.count)
-        table[threadIdx.x] = a.it[threadIdx.x];
+    const NsItem it = a.it[blockIdx.x];
+    const int at = a.first + blockIdx.x;
+    if (threadIdx.x == 0)
+        table[at] = it;
+    if (it.tiles == 0)
+        return;
+    for (int b = threadIdx.x; b < it.slices; b += 256)
+        gram_item[it.gram0 + b] = at;
+    const int blocks = (max(it.rows, it.cols) + ns_apply_len(it.tiles) - 1) / ns_apply_len(it.tiles);
+    for (int b = threadIdx.x; b < blocks; b += 256)
+        apply_item[it.apply0 + b] = at;
 }
 
 #define NS_GLOBAL __attribute__((address_space(1)))
@@ -59,144 +73,238 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t ns_rsrc(const char* p, int64_t
                                              0x00020000);
 }
 
-// element at byte offset off (elements of 2 or 4 bytes); out of range: 0
-__device__ __forceinline__ float ns_load(__amdgpu_buffer_rsrc_t r, int off, bool half)
-{
-    if (half)
-        return h2f((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
-    return __builtin_bit_cast(float, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
-}
+constexpr int kNsDead = 0x7fffff00;  // an offset that is out of every buffer's range (zeros)
 
-constexpr int kNsDead = 0x7ffffff0;  // an offset that is out of every buffer's range
-
-// the item whose blocks hold block b: items are in block order
-template <typename F>
-__device__ __forceinline__ int ns_item(const NsItem* t, int count, int b, F first)
+// N consecutive elements at byte offset off; those out of range are 0
+template <int N, bool HALF>
+__device__ __forceinline__ void ns_load(float (&v)[N], __amdgpu_buffer_rsrc_t r, int off)
 {
-    int lo = 0;
-    for (int hi = count; hi - lo > 1;) {
-        const int mid = (lo + hi) >> 1;
-        if (first(t[mid]) <= b)
-            lo = mid;
-        else
-            hi = mid;
+    if (HALF) {
+#pragma unroll
+        for (int e = 0; e < N; e++)
+            v[e] = h2f((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off + 2 * e, 0, 0));
+        return;
     }
-    return lo;
+    int e = 0;
+#pragma unroll
+    for (; e + 4 <= N; e += 4) {
+        const nf4 q = __builtin_bit_cast(nf4, __builtin_amdgcn_raw_buffer_load_b128(r, off + 4 * e, 0, 0));
+        v[e] = q.x, v[e + 1] = q.y, v[e + 2] = q.z, v[e + 3] = q.w;
+    }
+    if (N % 4) {
+        typedef float nf2 __attribute__((ext_vector_type(2)));
+        static_assert(N % 2 == 0, "pairs");
+        const nf2 q = __builtin_bit_cast(nf2, __builtin_amdgcn_raw_buffer_load_b64(r, off + 4 * e, 0, 0));
+        v[e] = q.x, v[e + 1] = q.y;
+    }
 }
 
 // ------------------------------------------------------ short form: the Gram matrix --
 
 constexpr int tri(int T) { return T * (T + 1) / 2; }
 
-// A block sums one slice of the long side: v_mfma_f64_16x16x4_f64, the same register as
-// both operands (lane l: short index l % 16 of a tile, long index l / 16). The partial
-// sums are kept in lane order, a tile pair (ti <= tj) after the other.
+// Index of the matrix's short side that entry r of its 16 T wide Gram matrix stands for: a
+// lane of k_ns_gram loads T consecutive ones of a tall matrix, one for each tile.
 template <int T>
-__global__ __launch_bounds__(256) void k_ns_gram(const NsItem* __restrict__ table, int count, char* ws)
+__device__ __forceinline__ int ns_short(int r, bool tall) { return tall ? (r & 15) * T + (r >> 4) : r; }
+
+// Sums over 4 long indices per instruction, v_mfma_f64_16x16x4_f64 with the same register
+// as both operands (lane l: short index l % 16 of a tile, long index l / 16). The tile
+// pairs ti <= tj are dealt out to WP waves, the long side to the other 4 / WP.
+template <int T, bool HALF>
+__device__ __forceinline__ void ns_gram(const NsItem& it, int slice, double* part, double (*red)[256])
 {
-    __shared__ double red[4][256];
-    const NsItem it = table[ns_item(table, count, blockIdx.x, [](const NsItem& i) { return i.block0; })];
+    constexpr int WP = T == 6 ? 4 : 1;                  // waves that share the pairs
+    constexpr int PAIRS = (tri(T) + WP - 1) / WP;       // of one wave
+    constexpr int U = T == 2 ? 8 : 4;                   // steps of 4 long indices in flight
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int slice = (int)blockIdx.x - it.block0;
-    const bool half = it.half != 0, tall = it.rows > it.cols;
-    const int sh = half ? 1 : 2;
+    constexpr int SH = HALF ? 1 : 2;
+    const bool tall = it.rows > it.cols;
     const int s = min(it.rows, it.cols), L = max(it.rows, it.cols);
     const int per = ((L + it.slices - 1) / it.slices + 3) & ~3;
     const int l0 = min(L, slice * per), len = min(L, l0 + per) - l0;
     const int i16 = lane & 15, kk = lane >> 4;
-    f64x4 acc[tri(T)];
+    f64x4 acc[PAIRS];
 #pragma unroll
-    for (int p = 0; p < tri(T); p++)
+    for (int p = 0; p < PAIRS; p++)
         acc[p] = f64x4{0.0, 0.0, 0.0, 0.0};
-    constexpr int U = T <= 2 ? 16 : (T <= 4 ? 8 : 4);  // 4-row steps in flight
-    const char* base = static_cast<const char*>(it.g);
-    // element (short i, long l) of the slice
-    const int64_t si = tall ? 1 : it.cols, sl = tall ? it.cols : 1;
-    base += (l0 * sl) << sh;
-    const __amdgpu_buffer_rsrc_t r =
-        ns_rsrc(base, (tall ? (int64_t)len * it.cols : (int64_t)it.rows * it.cols - l0) << sh);
-    int off[T];
+    const int64_t sl = tall ? it.cols : 1;  // elements from one long index to the next
+    const __amdgpu_buffer_rsrc_t r = ns_rsrc(static_cast<const char*>(it.g) + ((l0 * sl) << SH),
+                                             (tall ? (int64_t)len * it.cols : (int64_t)it.rows * it.cols - l0) << SH);
+    auto products = [&](const float (&v)[T]) {
+        double d[T];
 #pragma unroll
-    for (int t = 0; t < T; t++)
-        off[t] = t * 16 + i16 < s ? (int)(((t * 16 + i16) * si + kk * sl) << sh) : kNsDead;
-    const int step = (int)(sl * 4 << sh);
-    for (int b = wave * U; b < (len + 3) >> 2; b += 4 * U) {
-        float v[U][T];
+        for (int t = 0; t < T; t++)
+            d[t] = (double)v[t];
+        int n = 0;
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            const bool in = (b + u) * 4 + kk < len;
+        for (int ti = 0; ti < T; ti++)
 #pragma unroll
-            for (int t = 0; t < T; t++)
-                v[u][t] = ns_load(r, in && off[t] != kNsDead ? off[t] + (b + u) * step : kNsDead, half);
+            for (int tj = ti; tj < T; tj++, n++)
+                if (WP == 1 || n / PAIRS == wave)  // (uniform)
+                    acc[n % PAIRS] = __builtin_amdgcn_mfma_f64_16x16x4f64(d[ti], d[tj], acc[n % PAIRS], 0, 0, 0);
+    };
+    const int steps = (len + 3) >> 2;
+    if (tall) {
+        // T consecutive values of one row; those past the row's end belong to the next and
+        // are dropped
+        const int at = i16 * T < s ? (kk * it.cols + i16 * T) << SH : kNsDead;
+        for (int b = (WP == 1 ? wave * U : 0); b < steps; b += (WP == 1 ? 4 : 1) * U) {
+            float v[U][T];
+#pragma unroll
+            for (int u = 0; u < U; u++)
+                ns_load<T, HALF>(v[u], r, at != kNsDead && (b + u) * 4 + kk < len ? at + (((b + u) * 4 * it.cols) << SH) : kNsDead);
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+#pragma unroll
+                for (int t = 0; t < T; t++)
+                    v[u][t] = i16 * T + t < s ? v[u][t] : 0.0f;
+                products(v[u]);
+            }
         }
+    } else {
+        int at[T];
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            double d[T];
+        for (int t = 0; t < T; t++)
+            at[t] = t * 16 + i16 < s ? (int)(((int64_t)(t * 16 + i16) * it.cols + kk) << SH) : kNsDead;
+        for (int b = (WP == 1 ? wave * U : 0); b < steps; b += (WP == 1 ? 4 : 1) * U) {
+            float v[U][T];
 #pragma unroll
-            for (int t = 0; t < T; t++)
-                d[t] = (double)v[u][t];
-            int p = 0;
+            for (int u = 0; u < U; u++) {
+                const bool in = (b + u) * 4 + kk < len;
 #pragma unroll
-            for (int ti = 0; ti < T; ti++)
+                for (int t = 0; t < T; t++) {
+                    float one[1];
+                    const int off = in && at[t] != kNsDead ? at[t] + (((b + u) * 4) << SH) : kNsDead;
+                    if (HALF)
+                        one[0] = h2f((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
+                    else
+                        one[0] = __builtin_bit_cast(float, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+                    v[u][t] = one[0];
+                }
+            }
 #pragma unroll
-                for (int tj = ti; tj < T; tj++, p++)
-                    acc[p] = __builtin_amdgcn_mfma_f64_16x16x4f64(d[ti], d[tj], acc[p], 0, 0, 0);
+            for (int u = 0; u < U; u++)
+                products(v[u]);
         }
     }
-    double* part = reinterpret_cast<double*>(ws + it.off) + (int64_t)slice * tri(T) * 256;
+    // in lane order, a tile pair after the other
+    if (WP == 1) {
 #pragma unroll
-    for (int p = 0; p < tri(T); p++) {
-        __syncthreads();
+        for (int p = 0; p < PAIRS; p++) {
+            __syncthreads();
 #pragma unroll
-        for (int q = 0; q < 4; q++)
-            red[wave][q * 64 + lane] = acc[p][q];
-        __syncthreads();
-        part[p * 256 + tid] = ((red[0][tid] + red[1][tid]) + red[2][tid]) + red[3][tid];
+            for (int q = 0; q < 4; q++)
+                red[wave][q * 64 + lane] = acc[p][q];
+            __syncthreads();
+            part[p * 256 + tid] = ((red[0][tid] + red[1][tid]) + red[2][tid]) + red[3][tid];
+        }
+    } else {
+#pragma unroll
+        for (int p = 0; p < PAIRS; p++)
+            if (wave * PAIRS + p < tri(T))
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                    part[(wave * PAIRS + p) * 256 + q * 64 + lane] = acc[p][q];
     }
+}
+
+// A block sums one slice of one matrix's long side; blocks first ... of the short form's.
+// NARROW: the matrices of two tiles, which need few registers and many waves in flight.
+template <bool NARROW>
+__global__ __launch_bounds__(256) void k_ns_gram(const NsItem* __restrict__ table, const int32_t* __restrict__ item, char* ws,
+                                                 int first)
+{
+    __shared__ double red[4][256];
+    const int block = first + (int)blockIdx.x;
+    const NsItem it = table[__builtin_amdgcn_readfirstlane(item[block])];
+    const int slice = block - it.gram0;
+    double* part = reinterpret_cast<double*>(ws + it.off) + (int64_t)slice * tri(it.tiles) * 256;
+    if (NARROW)
+        it.half ? ns_gram<2, true>(it, slice, part, red) : ns_gram<2, false>(it, slice, part, red);
+    else if (it.tiles == 4)
+        it.half ? ns_gram<4, true>(it, slice, part, red) : ns_gram<4, false>(it, slice, part, red);
+    else
+        it.half ? ns_gram<6, true>(it, slice, part, red) : ns_gram<6, false>(it, slice, part, red);
+}
+
+// The slices' sums, to the first slice's place: a block per tile pair (blockIdx.x) and
+// matrix (blockIdx.y).
+__global__ __launch_bounds__(256) void k_ns_gram_sum(const NsItem* __restrict__ table, char* ws)
+{
+    const NsItem& it = table[blockIdx.y];
+    const int pairs = tri(it.tiles), slices = it.slices;
+    if ((int)blockIdx.x >= pairs || slices == 1)
+        return;
+    double* p = reinterpret_cast<double*>(ws + it.off) + (int)blockIdx.x * 256 + threadIdx.x;
+    double s = 0.0;
+    int sl = 0;
+    for (; sl + 8 <= slices; sl += 8) {
+        double v[8];
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            v[e] = p[(int64_t)(sl + e) * pairs * 256];
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            s += v[e];
+    }
+    for (; sl < slices; sl++)
+        s += p[(int64_t)sl * pairs * 256];
+    p[0] = s;
 }
 
 // ------------------------------------------------------- short form: the polynomial --
 
+constexpr int kNsWaves = 8;
+
 // Element q of lane l of a 16 x 16 fp64 result: row 4 q + l / 16, column l % 16
 __device__ __forceinline__ int ns_drow(int q, int lane) { return 4 * q + (lane >> 4); }
 
-template <int T, int NW>
+template <int T>
 struct NsPoly {
     static constexpr int S = 16 * T;
-    static constexpr int TILES = (tri(T) + NW - 1) / NW;  // result tiles per wave
+    static constexpr int TILES = (tri(T) + kNsWaves - 1) / kNsWaves;  // result tiles per wave
+    // place of entry (r, c): rows four entries longer, so that the four rows of an operand
+    // read, and the sixteen of a mirrored write, spread over the banks
+    static constexpr int LD = S + 4;
+    static __device__ __forceinline__ int at(int r, int c) { return r * LD + c; }
 };
 
 // X Y for symmetric matrices that commute, the upper tiles of this wave
-template <int T, int NW>
-__device__ __forceinline__ void ns_mul(const double (*X)[16 * T], const double (*Y)[16 * T], f64x4 (&acc)[NsPoly<T, NW>::TILES],
-                                       const int (&ti)[NsPoly<T, NW>::TILES], const int (&tj)[NsPoly<T, NW>::TILES], int lane)
+template <int T>
+__device__ __forceinline__ void ns_mul(const double* X, const double* Y, f64x4 (&acc)[NsPoly<T>::TILES],
+                                       const int (&ti)[NsPoly<T>::TILES], const int (&tj)[NsPoly<T>::TILES], int lane)
 {
+    using P = NsPoly<T>;
     const int i16 = lane & 15, kk = lane >> 4;
+    int xa[P::TILES], ya[P::TILES];
 #pragma unroll
-    for (int p = 0; p < NsPoly<T, NW>::TILES; p++)
+    for (int p = 0; p < P::TILES; p++) {
         acc[p] = f64x4{0.0, 0.0, 0.0, 0.0};
-#pragma unroll 4
-    for (int k0 = 0; k0 < 16 * T; k0 += 4)
+        xa[p] = P::at(kk, ti[p] * 16 + i16);
+        ya[p] = P::at(kk, tj[p] * 16 + i16);
+    }
+#pragma unroll 6
+    for (int k0 = 0; k0 < P::S; k0 += 4)
 #pragma unroll
-        for (int p = 0; p < NsPoly<T, NW>::TILES; p++)
-            acc[p] = __builtin_amdgcn_mfma_f64_16x16x4f64(X[k0 + kk][ti[p] * 16 + i16], Y[k0 + kk][tj[p] * 16 + i16], acc[p],
-                                                          0, 0, 0);
+        for (int p = 0; p < P::TILES; p++)
+            acc[p] = __builtin_amdgcn_mfma_f64_16x16x4f64(X[xa[p] + k0 * P::LD], Y[ya[p] + k0 * P::LD], acc[p], 0, 0, 0);
 }
 
-template <int T, int NW>
-__device__ __forceinline__ void ns_store(double (*X)[16 * T], const f64x4 (&v)[NsPoly<T, NW>::TILES],
-                                         const int (&ti)[NsPoly<T, NW>::TILES], const int (&tj)[NsPoly<T, NW>::TILES], int lane)
+template <int T>
+__device__ __forceinline__ void ns_store(double* X, const f64x4 (&v)[NsPoly<T>::TILES], const int (&ti)[NsPoly<T>::TILES],
+                                         const int (&tj)[NsPoly<T>::TILES], int lane)
 {
 #pragma unroll
-    for (int p = 0; p < NsPoly<T, NW>::TILES; p++)
+    for (int p = 0; p < NsPoly<T>::TILES; p++)
 #pragma unroll
         for (int q = 0; q < 4; q++) {
             // (below the diagonal of a tile on it: the mirror image, whose sum may round otherwise)
             const int r = ti[p] * 16 + ns_drow(q, lane), c = tj[p] * 16 + (lane & 15);
             if (r <= c) {
-                X[r][c] = v[p][q];
-                X[c][r] = v[p][q];
+                X[NsPoly<T>::at(r, c)] = v[p][q];
+                X[NsPoly<T>::at(c, r)] = v[p][q];
             }
         }
 }
@@ -206,22 +314,25 @@ struct NsCoef {
     int32_t steps;
 };
 
-// One block per matrix: sums the partials, |G|^2 is their trace; then the steps. Waves
-// past the tiles repeat the last tile (the same values to the same places).
-template <int T, int NW>
-__global__ __launch_bounds__(64 * NW) void k_ns_poly(const NsItem* __restrict__ table, char* ws, const NsCoef k)
+// |G|^2 is the Gram matrix's trace; then the steps, on the S x S matrices A, Q in LDS and
+// the waves' result tiles. Waves past the tiles repeat the last tile (the same values to
+// the same places).
+template <int T>
+__device__ __forceinline__ void ns_poly(const NsItem& it, char* ws, const NsCoef& k, double* A, double* Q)
 {
-    constexpr int S = 16 * T, TL = NsPoly<T, NW>::TILES;
-    __shared__ double A[S][S];
-    __shared__ double Q[S][S];
-    const NsItem it = table[blockIdx.x];
+    using PL = NsPoly<T>;
+    constexpr int S = PL::S, TL = PL::TILES;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int ti[TL], tj[TL], tp[TL];
+    int ti[TL], tj[TL];
+    f64x4 v[TL], P[TL], N[TL];
+    const double* part = reinterpret_cast<const double*>(ws + it.off);
 #pragma unroll
     for (int p = 0; p < TL; p++) {
         int n = min(wave * TL + p, tri(T) - 1);
-        tp[p] = n;
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+            v[p][q] = part[n * 256 + q * 64 + lane];
         int i = 0;
         while (n >= T - i) {
             n -= T - i;
@@ -230,32 +341,21 @@ __global__ __launch_bounds__(64 * NW) void k_ns_poly(const NsItem* __restrict__ 
         ti[p] = i;
         tj[p] = i + n;
     }
-    const double* part = reinterpret_cast<const double*>(ws + it.off);
-    f64x4 v[TL], P[TL], N[TL];
-#pragma unroll
-    for (int p = 0; p < TL; p++)
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-            double x = 0.0;
-            for (int sl = 0; sl < it.slices; sl++)
-                x += part[((int64_t)sl * tri(T) + tp[p]) * 256 + q * 64 + lane];
-            v[p][q] = x;
-        }
-    ns_store<T, NW>(A, v, ti, tj, lane);
+    ns_store<T>(A, v, ti, tj, lane);
     __syncthreads();
     double tr = 0.0;
     for (int i = 0; i < S; i++)
-        tr += A[i][i];
+        tr += A[PL::at(i, i)];
     const double inv = 1.0 / (sqrt(tr) + k.eps);
     __syncthreads();
 #pragma unroll
     for (int p = 0; p < TL; p++)
         v[p] = v[p] * inv * inv;
-    ns_store<T, NW>(A, v, ti, tj, lane);
+    ns_store<T>(A, v, ti, tj, lane);
     __syncthreads();
     for (int t = 0; t < k.steps; t++) {
         // v: A's tiles. N = A^2, then Q = a + b A + c A^2
-        ns_mul<T, NW>(A, A, N, ti, tj, lane);
+        ns_mul<T>(A, A, N, ti, tj, lane);
 #pragma unroll
         for (int p = 0; p < TL; p++)
 #pragma unroll
@@ -263,15 +363,15 @@ __global__ __launch_bounds__(64 * NW) void k_ns_poly(const NsItem* __restrict__ 
                 const bool diag = ti[p] == tj[p] && ns_drow(q, lane) == (lane & 15);
                 N[p][q] = k.c * N[p][q] + k.b * v[p][q] + (diag ? k.a : 0.0);
             }
-        ns_store<T, NW>(Q, N, ti, tj, lane);
+        ns_store<T>(Q, N, ti, tj, lane);
         __syncthreads();
         const bool last = t + 1 == k.steps;
         if (!last) {  // A <- (A Q) Q
-            ns_mul<T, NW>(A, Q, v, ti, tj, lane);
+            ns_mul<T>(A, Q, v, ti, tj, lane);
             __syncthreads();
-            ns_store<T, NW>(A, v, ti, tj, lane);
+            ns_store<T>(A, v, ti, tj, lane);
             __syncthreads();
-            ns_mul<T, NW>(A, Q, v, ti, tj, lane);
+            ns_mul<T>(A, Q, v, ti, tj, lane);
             __syncthreads();
         }
         if (t == 0) {
@@ -279,19 +379,20 @@ __global__ __launch_bounds__(64 * NW) void k_ns_poly(const NsItem* __restrict__ 
             for (int p = 0; p < TL; p++)
                 P[p] = N[p];
         } else {  // P <- P Q, through A's place
-            ns_store<T, NW>(A, P, ti, tj, lane);
+            ns_store<T>(A, P, ti, tj, lane);
             __syncthreads();
-            ns_mul<T, NW>(A, Q, P, ti, tj, lane);
+            ns_mul<T>(A, Q, P, ti, tj, lane);
             __syncthreads();
         }
         if (!last) {
-            ns_store<T, NW>(A, v, ti, tj, lane);
+            ns_store<T>(A, v, ti, tj, lane);
             __syncthreads();
         }
     }
-    // the matrix's factor, with the norm and the scale, over the first partials
+    // the matrix's factor, with the norm and the scale, over the partials
     float* out = reinterpret_cast<float*>(ws + it.off);
     const double f = inv * (double)it.scale;
+    const bool tall = it.rows > it.cols;
 #pragma unroll
     for (int p = 0; p < TL; p++)
 #pragma unroll
@@ -299,53 +400,69 @@ __global__ __launch_bounds__(64 * NW) void k_ns_poly(const NsItem* __restrict__ 
             const int r = ti[p] * 16 + ns_drow(q, lane), c = tj[p] * 16 + (lane & 15);
             const float x = (float)(P[p][q] * f);
             if (r <= c) {
-                out[r * S + c] = x;
-                out[c * S + r] = x;
+                out[ns_short<T>(r, tall) * S + ns_short<T>(c, tall)] = x;
+                out[ns_short<T>(c, tall) * S + ns_short<T>(r, tall)] = x;
             }
         }
 }
 
-// --------------------------------------------------------- short form: the product --
+// One block per matrix.
+__global__ __launch_bounds__(64 * kNsWaves) void k_ns_poly(const NsItem* __restrict__ table, char* ws, const NsCoef k)
+{
+    __shared__ double lds[2][96 * NsPoly<6>::LD];
+    const NsItem it = table[blockIdx.x];
+    if (it.tiles == 2)
+        ns_poly<2>(it, ws, k, lds[0], lds[1]);
+    else if (it.tiles == 4)
+        ns_poly<4>(it, ws, k, lds[0], lds[1]);
+    else
+        ns_poly<6>(it, ws, k, lds[0], lds[1]);
+}
 
-constexpr int kNsRun = 8;  // 16-element runs of the long side per wave
+// --------------------------------------------------------- short form: the product --
 
 // out = G F (tall) or F G (wide), F the symmetric factor: v_mfma_f32_16x16x4_f32 with F's
 // rows as A and G as B; a wave holds a run of 16 of the long side in registers before it
 // writes any of it, so out may be G. The contraction index 16 st + 4 (l / 16) + u is taken
-// by product u of step st, so that a lane's four are consecutive.
-template <int T>
-__global__ __launch_bounds__(256) void k_ns_apply(const NsItem* __restrict__ table, int count, const char* ws)
+// by product u of step st, so that a lane's four are consecutive in a tall matrix's row, as
+// are the four results it ends with.
+template <int T, bool HALF>
+__device__ __forceinline__ void ns_apply(const NsItem& it, int block, const float* f, float* F)
 {
-    constexpr int S = 16 * T, LD = S + 4;
-    __shared__ float F[S][LD];
-    const NsItem it = table[ns_item(table, count, blockIdx.x, [](const NsItem& i) { return i.apply0; })];
+    constexpr int S = 16 * T, LD = S + 4, SH = HALF ? 1 : 2;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const float* f = reinterpret_cast<const float*>(ws + it.off);
-    for (int e = tid; e < S * S; e += 256)
-        F[e / S][e % S] = f[e];
+    for (int e = tid; e < S * S / 4; e += 256)
+        *reinterpret_cast<nf4*>(&F[e / (S / 4) * LD + e % (S / 4) * 4]) = reinterpret_cast<const nf4*>(f)[e];
     __syncthreads();
-    const bool half = it.half != 0, tall = it.rows > it.cols;
-    const int sh = half ? 1 : 2;
+    const bool tall = it.rows > it.cols;
     const int s = min(it.rows, it.cols), L = max(it.rows, it.cols);
     const int n16 = lane & 15, kk = lane >> 4;
     const int64_t si = tall ? 1 : it.cols, sl = tall ? it.cols : 1;
-    const int l0 = ((int)blockIdx.x - it.apply0) * 64 * kNsRun + wave * 16 * kNsRun;
-    for (int run = 0; run < kNsRun; run++) {
-        const int lb = l0 + run * 16;
+    for (int run = 0; run < ns_runs(T); run++) {
+        const int lb = block * ns_apply_len(T) + (run * 4 + wave) * 16;
         if (lb >= L)
             return;
         const int len = min(16, L - lb);
-        const char* base = static_cast<const char*>(it.g) + ((lb * sl) << sh);
-        const __amdgpu_buffer_rsrc_t r = ns_rsrc(base, (tall ? (int64_t)len * it.cols : (int64_t)it.rows * it.cols - lb) << sh);
+        const __amdgpu_buffer_rsrc_t r = ns_rsrc(static_cast<const char*>(it.g) + ((lb * sl) << SH),
+                                                 (tall ? (int64_t)len * it.cols : (int64_t)it.rows * it.cols - lb) << SH);
         float v[T][4];
 #pragma unroll
-        for (int st = 0; st < T; st++)
+        for (int st = 0; st < T; st++) {
+            const int i = 16 * st + 4 * kk;
+            if (tall) {
+                // (values past the row's end meet F's zeros; where one of them is not
+                // finite, neither is the result anywhere)
+                ns_load<4, HALF>(v[st], r, i < s && n16 < len ? (n16 * it.cols + i) << SH : kNsDead);
+            } else {
 #pragma unroll
-            for (int u = 0; u < 4; u++) {
-                const int i = 16 * st + 4 * kk + u;
-                v[st][u] = ns_load(r, i < s && n16 < len ? (int)((i * si + n16 * sl) << sh) : kNsDead, half);
+                for (int u = 0; u < 4; u++) {
+                    const int off = i + u < s && n16 < len ? (int)(((int64_t)(i + u) * it.cols + n16) << SH) : kNsDead;
+                    v[st][u] = HALF ? h2f((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0))
+                                    : __builtin_bit_cast(float, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+                }
             }
+        }
         nf4 acc[T];
 #pragma unroll
         for (int t = 0; t < T; t++)
@@ -354,28 +471,54 @@ __global__ __launch_bounds__(256) void k_ns_apply(const NsItem* __restrict__ tab
         for (int st = 0; st < T; st++)
 #pragma unroll
             for (int t = 0; t < T; t++) {
-                const nf4 a = *reinterpret_cast<const nf4*>(&F[t * 16 + n16][16 * st + 4 * kk]);
+                const nf4 a = *reinterpret_cast<const nf4*>(&F[(t * 16 + n16) * LD + 16 * st + 4 * kk]);
 #pragma unroll
                 for (int u = 0; u < 4; u++)
                     acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[u], v[st][u], acc[t], 0, 0, 0);
             }
         if (n16 < len) {
-            char* ob = static_cast<char*>(it.out) + ((lb * sl) << sh);
+            char* ob = static_cast<char*>(it.out) + ((lb * sl) << SH);
 #pragma unroll
-            for (int t = 0; t < T; t++)
+            for (int t = 0; t < T; t++) {
+                const int i = t * 16 + 4 * kk;
+                if (tall && i + 4 <= s) {
+                    typedef float f4_any __attribute__((ext_vector_type(4), aligned(4)));
+                    typedef uint32_t u2_any __attribute__((ext_vector_type(2), aligned(2)));
+                    const int64_t at = n16 * (int64_t)it.cols + i;
+                    if (HALF)
+                        *(NS_GLOBAL u2_any*)(uintptr_t)(ob + 2 * at) =
+                            u2_any{f2h(acc[t][0]) | ((uint32_t)f2h(acc[t][1]) << 16), f2h(acc[t][2]) | ((uint32_t)f2h(acc[t][3]) << 16)};
+                    else
+                        *(NS_GLOBAL f4_any*)(uintptr_t)(ob + 4 * at) = f4_any{acc[t][0], acc[t][1], acc[t][2], acc[t][3]};
+                    continue;
+                }
 #pragma unroll
-                for (int q = 0; q < 4; q++) {
-                    const int i = t * 16 + 4 * kk + q;
-                    if (i < s) {
-                        const int64_t at = i * si + n16 * sl;
-                        if (half)
+                for (int q = 0; q < 4; q++)
+                    if (i + q < s) {
+                        const int64_t at = (i + q) * si + n16 * sl;
+                        if (HALF)
                             ((NS_GLOBAL uint16_t*)(uintptr_t)ob)[at] = f2h(acc[t][q]);
                         else
                             ((NS_GLOBAL float*)(uintptr_t)ob)[at] = acc[t][q];
                     }
-                }
+            }
         }
     }
+}
+
+__global__ __launch_bounds__(256) void k_ns_apply(const NsItem* __restrict__ table, const int32_t* __restrict__ item,
+                                                  const char* ws)
+{
+    __shared__ float F[96 * 100];
+    const NsItem it = table[__builtin_amdgcn_readfirstlane(item[blockIdx.x])];
+    const int block = (int)blockIdx.x - it.apply0;
+    const float* f = reinterpret_cast<const float*>(ws + it.off);
+    if (it.tiles == 2)
+        it.half ? ns_apply<2, true>(it, block, f, F) : ns_apply<2, false>(it, block, f, F);
+    else if (it.tiles == 4)
+        it.half ? ns_apply<4, true>(it, block, f, F) : ns_apply<4, false>(it, block, f, F);
+    else
+        it.half ? ns_apply<6, true>(it, block, f, F) : ns_apply<6, false>(it, block, f, F);
 }
 
 // ----------------------------------------------------------------- long form --
@@ -675,15 +818,14 @@ __global__ __launch_bounds__(256) void k_nsl_step(const NsItem* __restrict__ tab
 // ------------------------------------------------------------------ the plan --
 
 constexpr int kNsShort = 96;  // short sides of the short form
-int ns_class(int64_t s) { return s > kNsShort ? 3 : (s > 64 ? 2 : (s > 32 ? 1 : 0)); }
-constexpr int kNsTiles[3] = {2, 4, 6};
+int ns_tiles(int64_t s) { return s > kNsShort ? 0 : (s > 64 ? 6 : (s > 32 ? 4 : 2)); }
 
-// slices of the long side in the short form: at least 256 long, 64 at most (their
-// partials are added by one block)
-int ns_slices(int64_t l)
+// slices of the long side in the short form: at least 256 long (128 for wide Gram
+// matrices, whose products take longer), at most 128
+int ns_slices(int64_t l, int T)
 {
-    const int64_t n = (l + 255) / 256;
-    return (int)(n < 64 ? n : 64);
+    const int64_t len = T == 2 ? 256 : 128, n = (l + len - 1) / len;
+    return (int)(n < 128 ? n : 128);
 }
 
 int64_t ns_bytes(int64_t rows, int64_t cols)
@@ -691,21 +833,35 @@ int64_t ns_bytes(int64_t rows, int64_t cols)
     const int64_t s = rows < cols ? rows : cols, l = rows < cols ? cols : rows;
     if (s == 0)
         return 0;
-    const int c = ns_class(s);
-    if (c == 3)
+    const int T = ns_tiles(s);
+    if (T == 0)
         return ns_long(rows, cols).total;
-    const int64_t part = (int64_t)ns_slices(l) * tri(kNsTiles[c]) * 2048, f = 4LL * 256 * kNsTiles[c] * kNsTiles[c];
+    const int64_t part = (int64_t)ns_slices(l, T) * tri(T) * 2048, f = 4LL * 256 * T * T;
     return ((part > f ? part : f) + 255) / 256 * 256;
+}
+
+int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+// Blocks of k_ns_gram and k_ns_apply of one matrix
+int64_t ns_gram_blocks(int64_t s, int64_t l) { return s > 0 && ns_tiles(s) ? ns_slices(l, ns_tiles(s)) : 0; }
+int64_t ns_apply_blocks(int64_t s, int64_t l)
+{
+    const int T = ns_tiles(s);
+    return s > 0 && T ? (l + ns_apply_len(T) - 1) / ns_apply_len(T) : 0;
 }
 
 }  // namespace
 
 size_t orthogonalize_workspace_bytes(const OrthoEntry* items, int count)
 {
-    int64_t total = ((int64_t)count * sizeof(NsItem) + 255) / 256 * 256;
-    for (int i = 0; i < count; i++)
+    int64_t total = up256((int64_t)count * sizeof(NsItem)), grams = 0, applies = 0;
+    for (int i = 0; i < count; i++) {
+        const int64_t s = items[i].rows < items[i].cols ? items[i].rows : items[i].cols, l = items[i].rows + items[i].cols - s;
         total += ns_bytes(items[i].rows, items[i].cols);
-    return (size_t)total;
+        grams += ns_gram_blocks(s, l);
+        applies += ns_apply_blocks(s, l);
+    }
+    return (size_t)(total + up256(4 * grams) + up256(4 * applies));
 }
 
 bool orthogonalize_fits(int64_t rows, int64_t cols)
@@ -719,82 +875,86 @@ hipError_t launch_orthogonalize(const OrthoEntry* items, int count, double a, do
 {
     char* const w = static_cast<char*>(ws);
     NsItem* const table = reinterpret_cast<NsItem*>(w);
-    int64_t off = ((int64_t)count * sizeof(NsItem) + 255) / 256 * 256;
-    // the table in the order of the classes, the widest first
-    int first[4], n[4] = {0, 0, 0, 0};
-    int64_t grams[3] = {0, 0, 0}, applies[3] = {0, 0, 0};
+    int64_t grams = 0, applies = 0;
+    for (int i = 0; i < count; i++) {
+        const int64_t sd = items[i].rows < items[i].cols ? items[i].rows : items[i].cols, ld = items[i].rows + items[i].cols - sd;
+        grams += ns_gram_blocks(sd, ld);
+        applies += ns_apply_blocks(sd, ld);
+    }
+    int64_t off = up256((int64_t)count * sizeof(NsItem));
+    int32_t* const gram_item = reinterpret_cast<int32_t*>(w + off);
+    off += up256(4 * grams);
+    int32_t* const apply_item = reinterpret_cast<int32_t*>(w + off);
+    off += up256(4 * applies);
+    // the table: the long form, then the short one, the widest first (they take longest)
+    grams = applies = 0;
+    int longs = 0, shorts = 0;
+    unsigned pairs = 0;
     int64_t lsq = 0, ltile = 0, lgram = 0, lsum = 0, lpoly = 0, lstep = 0;
+    auto most = [](auto& v, auto x) { v = v > x ? v : x; };
     NsArgs args{};
-    int done = 0;
-    for (int cl = 3; cl >= 0; cl--) {
-        first[cl] = done + args.count;
+    auto flush = [&] {
+        if (args.count > 0)
+            hipLaunchKernelGGL(k_ns_table, dim3((unsigned)args.count), dim3(256), 0, s, args, table, gram_item, apply_item);
+        args.first += args.count;
+        args.count = 0;
+    };
+    int64_t wide = 0;  // blocks of k_ns_gram for more than two tiles
+    for (const int T : {0, 6, 4, 2}) {
+        if (T == 2)
+            wide = grams;
         for (int i = 0; i < count; i++) {
             const OrthoEntry& e = items[i];
-            const int64_t sd = e.rows < e.cols ? e.rows : e.cols, ld = e.rows < e.cols ? e.cols : e.rows;
-            if (sd == 0 || ns_class(sd) != cl)
+            const int64_t sd = e.rows < e.cols ? e.rows : e.cols, ld = e.rows + e.cols - sd;
+            if (sd == 0 || ns_tiles(sd) != T)
                 continue;
-            NsItem it{e.g, e.out, off, (int32_t)e.rows, (int32_t)e.cols, e.scale, e.half, 0, 0, 0, 0};
+            NsItem it{e.g, e.out, off, (int32_t)e.rows, (int32_t)e.cols, e.scale, e.half, T, 0, (int32_t)grams, (int32_t)applies};
             off += ns_bytes(e.rows, e.cols);
-            n[cl]++;
-            if (cl < 3) {
-                it.slices = ns_slices(ld);
-                it.block0 = (int32_t)grams[cl];
-                it.apply0 = (int32_t)applies[cl];
-                grams[cl] += it.slices;
-                applies[cl] += (ld + 64 * kNsRun - 1) / (64 * kNsRun);
+            if (T > 0) {
+                it.slices = ns_slices(ld, T);
+                grams += ns_gram_blocks(sd, ld);
+                applies += ns_apply_blocks(sd, ld);
+                most(pairs, (unsigned)tri(T));
+                shorts++;
             } else {
                 const NsLong p = ns_long(e.rows, e.cols);
-                const int64_t T = p.sp / 64, up = T * (T + 1) / 2;
-                auto most = [](int64_t& v, int64_t x) { v = v > x ? v : x; };
-                most(lsq, p.sqn);
-                most(ltile, T * (p.lp / 64));
-                most(lgram, up * p.splits);
-                most(lsum, p.splits > 1 ? up * 16 : 0);
-                most(lpoly, up);
-                most(lstep, T * (p.lp / 64));
+                const int64_t n = p.sp / 64, upper = n * (n + 1) / 2;
+                most(lsq, (int64_t)p.sqn);
+                most(ltile, n * (p.lp / 64));
+                most(lgram, upper * p.splits);
+                most(lsum, p.splits > 1 ? upper * 16 : 0);
+                most(lpoly, upper);
+                most(lstep, n * (p.lp / 64));
+                longs++;
             }
             args.it[args.count++] = it;
-            if (args.count == kNsArg) {
-                hipLaunchKernelGGL(k_ns_table, dim3(1), dim3(64), 0, s, args, table + done);
-                done += kNsArg;
-                args.count = 0;
-            }
+            if (args.count == kNsArg)
+                flush();
         }
     }
-    if (args.count > 0)
-        hipLaunchKernelGGL(k_ns_table, dim3(1), dim3(64), 0, s, args, table + done);
-    const NsCoef k{a, b, c, eps, steps};
-    if (n[2] > 0)
-        hipLaunchKernelGGL(k_ns_gram<6>, dim3((unsigned)grams[2]), dim3(256), 0, s, table + first[2], n[2], w);
-    if (n[1] > 0)
-        hipLaunchKernelGGL(k_ns_gram<4>, dim3((unsigned)grams[1]), dim3(256), 0, s, table + first[1], n[1], w);
-    if (n[0] > 0)
-        hipLaunchKernelGGL(k_ns_gram<2>, dim3((unsigned)grams[0]), dim3(256), 0, s, table + first[0], n[0], w);
-    if (n[2] > 0)
-        hipLaunchKernelGGL((k_ns_poly<6, 8>), dim3((unsigned)n[2]), dim3(512), 0, s, table + first[2], w, k);
-    if (n[1] > 0)
-        hipLaunchKernelGGL((k_ns_poly<4, 4>), dim3((unsigned)n[1]), dim3(256), 0, s, table + first[1], w, k);
-    if (n[0] > 0)
-        hipLaunchKernelGGL((k_ns_poly<2, 4>), dim3((unsigned)n[0]), dim3(256), 0, s, table + first[0], w, k);
-    if (n[2] > 0)
-        hipLaunchKernelGGL(k_ns_apply<6>, dim3((unsigned)applies[2]), dim3(256), 0, s, table + first[2], n[2], w);
-    if (n[1] > 0)
-        hipLaunchKernelGGL(k_ns_apply<4>, dim3((unsigned)applies[1]), dim3(256), 0, s, table + first[1], n[1], w);
-    if (n[0] > 0)
-        hipLaunchKernelGGL(k_ns_apply<2>, dim3((unsigned)applies[0]), dim3(256), 0, s, table + first[0], n[0], w);
-    if (n[3] > 0) {
-        const NsItem* const t = table + first[3];
-        const unsigned y = (unsigned)n[3];
-        hipLaunchKernelGGL(k_nsl_sumsq, dim3((unsigned)lsq, y), dim3(256), 0, s, t, w);
-        hipLaunchKernelGGL(k_nsl_init, dim3((unsigned)ltile, y), dim3(256), 0, s, t, w, eps);
+    flush();
+    if (shorts > 0) {
+        const NsItem* const t = table + longs;
+        if (wide > 0)
+            hipLaunchKernelGGL(k_ns_gram<false>, dim3((unsigned)wide), dim3(256), 0, s, table, gram_item, w, 0);
+        if (grams > wide)
+            hipLaunchKernelGGL(k_ns_gram<true>, dim3((unsigned)(grams - wide)), dim3(256), 0, s, table, gram_item, w, (int)wide);
+        hipLaunchKernelGGL(k_ns_gram_sum, dim3(pairs, (unsigned)shorts), dim3(256), 0, s, t, w);
+        hipLaunchKernelGGL(k_ns_poly, dim3((unsigned)shorts), dim3(64 * kNsWaves), 0, s, t, w, NsCoef{a, b, c, eps, steps});
+        hipLaunchKernelGGL(k_ns_apply, dim3((unsigned)applies), dim3(256), 0, s, table, apply_item, w);
+    }
+    if (longs > 0) {
+        const unsigned y = (unsigned)longs;
+        hipLaunchKernelGGL(k_nsl_sumsq, dim3((unsigned)lsq, y), dim3(256), 0, s, table, w);
+        hipLaunchKernelGGL(k_nsl_init, dim3((unsigned)ltile, y), dim3(256), 0, s, table, w, eps);
         for (int st = 0; st < steps; st++) {
-            hipLaunchKernelGGL(k_nsl_gram, dim3((unsigned)lgram, y), dim3(256), 0, s, t, w, st & 1);
+            hipLaunchKernelGGL(k_nsl_gram, dim3((unsigned)lgram, y), dim3(256), 0, s, table, w, st & 1);
             if (lsum > 0)
-                hipLaunchKernelGGL(k_nsl_sum, dim3((unsigned)lsum, y), dim3(256), 0, s, t, w);
-            hipLaunchKernelGGL(k_nsl_poly, dim3((unsigned)lpoly, y), dim3(256), 0, s, t, w, (float)b, (float)c);
-            hipLaunchKernelGGL(k_nsl_step, dim3((unsigned)lstep, y), dim3(256), 0, s, t, w, (float)a, st & 1);
+                hipLaunchKernelGGL(k_nsl_sum, dim3((unsigned)lsum, y), dim3(256), 0, s, table, w);
+            hipLaunchKernelGGL(k_nsl_poly, dim3((unsigned)lpoly, y), dim3(256), 0, s, table, w, (float)b, (float)c);
+            hipLaunchKernelGGL(k_nsl_step, dim3((unsigned)lstep, y), dim3(256), 0, s, table, w, (float)a, st & 1);
         }
-        hipLaunchKernelGGL(k_nsl_out, dim3((unsigned)ltile, y), dim3(256), 0, s, t, w, steps & 1);
+        hipLaunchKernelGGL(k_nsl_out, dim3((unsigned)ltile, y), dim3(256), 0, s, table, w, steps & 1);
     }
     return hipGetLastError();
 }
