@@ -10,8 +10,11 @@
 // Gram matrix squares the singular values, and the polynomial lifts the small ones by
 // up to a^steps: both run in fp64 (in fp32 a direction at 1e-3 of the largest would come
 // out 1 % off). Longer short sides run the steps as they stand, X in fp32.
+#include <cmath>
+
 #include "owq_device.h"
 #include "owq_launch.h"
+#include "owq_stage.h"
 
 namespace owq {
 
@@ -523,33 +526,45 @@ __global__ __launch_bounds__(256) void k_ns_apply(const NsItem* __restrict__ tab
 
 // ----------------------------------------------------------------- long form --
 
-// Workspace of one matrix of the long form, fp32, X with the long side contiguous and
-// both sides padded to 64 with zeros (the products need no edges): X, X', A, B, then
-// the split sums of A, then the partial sums of squares.
+// X, A = X X^T and B = b A + c A^2 are kept as pairs of fp16 values, a number times 2^m and
+// what its rounding left: 22 bits, and 2^-25 of the scaled number absolutely, which is as
+// good as fp32 here (relative error of the result 2.33e-6 against 2.29e-6 with fp32 for a
+// Gaussian 300 x 1200 matrix, 5.1e-6 against 4.8e-6 with singular values down to 1e-4 of
+// the largest). So each product is three on the fp16 matrix cores (high by high, high by
+// low twice; low by low lies below the pairs' precision), with fp32 sums: 5 times the rate
+// of the fp32 matrix instructions. m comes from a bound of the singular values after each
+// step, which the caller of the kernels works out from the coefficients, so nothing
+// overflows.
+//
+// X lies with the long side contiguous, both sides padded to 128 with zeros.
 struct NsLong {
-    int64_t sp, lp;
-    int64_t x0, x1, A, B, parts, sq, total;  // byte offsets
+    int64_t sp, lp, tiles;
+    int64_t x, x_next, A, B, parts, sq, total;  // byte offsets; high planes first, low behind
     int32_t splits, sqn;
 };
+
+constexpr int kNsTile = 128, kNsDepth = 32;  // of the products: tile, contraction per stage
 
 __host__ __device__ inline NsLong ns_long(int64_t rows, int64_t cols)
 {
     NsLong n{};
     const int64_t s = rows < cols ? rows : cols, l = rows < cols ? cols : rows;
-    n.sp = (s + 63) / 64 * 64;
-    n.lp = (l + 63) / 64 * 64;
-    const int64_t tiles = (n.sp / 64) * (n.sp / 64 + 1) / 2;
-    // 256 CUs want two blocks each; a split takes at least 256 of the long side
-    int64_t sp = (512 + tiles - 1) / tiles;
-    sp = sp < n.lp / 256 ? sp : n.lp / 256;
+    n.sp = (s + kNsTile - 1) / kNsTile * kNsTile;
+    n.lp = (l + kNsTile - 1) / kNsTile * kNsTile;
+    const int64_t t = n.sp / kNsTile;
+    n.tiles = t * (t + 1) / 2;  // on and above A's diagonal
+    // the long side in as many parts as give every CU a block, each of at least 8 stages
+    int64_t sp = 256 / n.tiles;
+    sp = sp < n.lp / (8 * kNsDepth) ? sp : n.lp / (8 * kNsDepth);
     n.splits = (int32_t)(sp < 1 ? 1 : sp);
-    n.sqn = (int32_t)((rows * cols + 16383) / 16384 < 1024 ? (rows * cols + 16383) / 16384 : 1024);
+    const int64_t sq = (rows * cols + 16383) / 16384;
+    n.sqn = (int32_t)(sq < 1024 ? sq : 1024);
     int64_t off = 0;
-    n.x0 = off, off += 4 * n.sp * n.lp;
-    n.x1 = off, off += 4 * n.sp * n.lp;
+    n.x = off, off += 4 * n.sp * n.lp;
+    n.x_next = off, off += 4 * n.sp * n.lp;
     n.A = off, off += 4 * n.sp * n.sp;
     n.B = off, off += 4 * n.sp * n.sp;
-    n.parts = off, off += n.splits > 1 ? 4 * n.splits * n.sp * n.sp : 0;
+    n.parts = off, off += 4 * n.splits * n.tiles * kNsTile * kNsTile;
     n.sq = off, off += 8 * n.sqn;
     n.total = (off + 255) / 256 * 256;
     return n;
@@ -576,18 +591,48 @@ __global__ __launch_bounds__(256) void k_nsl_sumsq(const NsItem* __restrict__ ta
     if ((int)blockIdx.x >= n.sqn)
         return;
     const int64_t total = (int64_t)it.rows * it.cols;
-    double s = 0.0;
-    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)n.sqn * 256) {
-        const float v = it.half ? h2f(static_cast<const uint16_t*>(it.g)[e]) : static_cast<const float*>(it.g)[e];
-        s = __builtin_fma((double)v, (double)v, s);
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+    auto add = [&](float v, int e) { s[e] = __builtin_fma((double)v, (double)v, s[e]); };
+    // four consecutive elements per thread, at any element's address
+    typedef float f4_any __attribute__((ext_vector_type(4), aligned(4)));
+    typedef uint16_t h4_any __attribute__((ext_vector_type(4), aligned(2)));
+    const int64_t step = (int64_t)n.sqn * 256, quads = total >> 2;
+    for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < quads; q += step) {
+        if (it.half) {
+            const h4_any v = ((const NS_GLOBAL h4_any*)(uintptr_t)it.g)[q];
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                add(h2f(v[e]), e);
+        } else {
+            const f4_any v = ((const NS_GLOBAL f4_any*)(uintptr_t)it.g)[q];
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                add(v[e], e);
+        }
     }
-    s = ns_block_sum(s, red);
+    if (blockIdx.x == 0 && (int)threadIdx.x < (int)(total & 3)) {
+        const int64_t e = (quads << 2) + threadIdx.x;
+        add(it.half ? h2f(static_cast<const uint16_t*>(it.g)[e]) : static_cast<const float*>(it.g)[e], 0);
+    }
+    const double sum = ns_block_sum((s[0] + s[1]) + (s[2] + s[3]), red);
     if (threadIdx.x == 0)
-        reinterpret_cast<double*>(ws + it.off + n.sq)[blockIdx.x] = s;
+        reinterpret_cast<double*>(ws + it.off + n.sq)[blockIdx.x] = sum;
 }
 
-// X = G / (|G| + eps), the long side contiguous, padded with zeros. 64 x 64 tiles.
-__global__ __launch_bounds__(256) void k_nsl_init(const NsItem* __restrict__ table, char* ws, double eps)
+// The pair of a number that is scaled already
+struct NsPair {
+    uint16_t hi, lo;
+};
+__device__ __forceinline__ NsPair ns_pair(float v)
+{
+    NsPair p;
+    p.hi = f2h(v);
+    p.lo = f2h(v - h2f(p.hi));
+    return p;
+}
+
+// X = G / (|G| + eps), padded with zeros. 64 x 64 tiles.
+__global__ __launch_bounds__(256) void k_nsl_init(const NsItem* __restrict__ table, char* ws, double eps, float scale)
 {
     __shared__ double red[4];
     __shared__ float tile[64][65];
@@ -596,32 +641,48 @@ __global__ __launch_bounds__(256) void k_nsl_init(const NsItem* __restrict__ tab
     const int64_t tl = n.lp / 64;
     if (blockIdx.x >= (n.sp / 64) * tl)
         return;
-    const double* sq = reinterpret_cast<const double*>(ws + it.off + n.sq);
-    double s = 0.0;
-    for (int i = threadIdx.x; i < n.sqn; i += 256)
-        s += sq[i];
-    const double inv = 1.0 / (sqrt(ns_block_sum(s, red)) + eps);
     const bool tall = it.rows > it.cols;
     const int64_t i0 = blockIdx.x / tl * 64, l0 = blockIdx.x % tl * 64;
     const int c = threadIdx.x & 63, r0 = threadIdx.x >> 6;
-    for (int r = r0; r < 64; r += 4) {
-        const int64_t row = (tall ? l0 : i0) + r, col = (tall ? i0 : l0) + c;
-        float v = 0.0f;
-        if (row < it.rows && col < it.cols) {
-            const int64_t e = row * it.cols + col;
-            v = it.half ? h2f(static_cast<const uint16_t*>(it.g)[e]) : static_cast<const float*>(it.g)[e];
-            v = (float)((double)v * inv);
+    const int64_t row0 = (tall ? l0 : i0) + r0, col = (tall ? i0 : l0) + c, e0 = row0 * it.cols + col;
+    float v[16];
+    auto load = [&](auto* p) {
+        const int rows = col < it.cols ? (int)min((int64_t)64, it.rows - row0) : 0;
+#pragma unroll
+        for (int q = 0; q < 16; q++, p += 4 * (int64_t)it.cols) {
+            v[q] = 0.0f;
+            if (4 * q < rows) {
+                if constexpr (sizeof(*p) == 2)
+                    v[q] = h2f(*p);
+                else
+                    v[q] = *p;
+            }
         }
-        tile[r][c] = v;
-    }
-    __syncthreads();
-    float* x = reinterpret_cast<float*>(ws + it.off + n.x0);
+    };
+    if (it.half)
+        load(static_cast<const uint16_t*>(it.g) + e0);
+    else
+        load(static_cast<const float*>(it.g) + e0);
+    const double* sq = reinterpret_cast<const double*>(ws + it.off + n.sq);
+    double part[4];
+#pragma unroll
+    for (int q = 0; q < 4; q++)
+        part[q] = (int)threadIdx.x + 256 * q < n.sqn ? sq[threadIdx.x + 256 * q] : 0.0;
+    const double inv = 1.0 / (sqrt(ns_block_sum((part[0] + part[1]) + (part[2] + part[3]), red)) + eps);
     for (int r = r0; r < 64; r += 4)
-        x[(i0 + r) * n.lp + l0 + c] = tall ? tile[c][r] : tile[r][c];
+        tile[r][c] = (float)((double)v[(r - r0) / 4] * inv) * scale;
+    __syncthreads();
+    uint16_t* x = reinterpret_cast<uint16_t*>(ws + it.off + n.x);
+    for (int r = r0; r < 64; r += 4) {
+        const NsPair p = ns_pair(tall ? tile[c][r] : tile[r][c]);
+        const int64_t at = (i0 + r) * n.lp + l0 + c;
+        x[at] = p.hi;
+        x[n.sp * n.lp + at] = p.lo;
+    }
 }
 
-// out = scale X
-__global__ __launch_bounds__(256) void k_nsl_out(const NsItem* __restrict__ table, const char* ws, int from1)
+// out = scale X, X times 2^m taken back by `unscale`
+__global__ __launch_bounds__(256) void k_nsl_out(const NsItem* __restrict__ table, const char* ws, int from, float unscale)
 {
     __shared__ float tile[64][65];
     const NsItem it = table[blockIdx.y];
@@ -632,9 +693,17 @@ __global__ __launch_bounds__(256) void k_nsl_out(const NsItem* __restrict__ tabl
     const bool tall = it.rows > it.cols;
     const int64_t i0 = blockIdx.x / tl * 64, l0 = blockIdx.x % tl * 64;
     const int c = threadIdx.x & 63, r0 = threadIdx.x >> 6;
-    const float* x = reinterpret_cast<const float*>(ws + it.off + (from1 ? n.x1 : n.x0));
-    for (int r = r0; r < 64; r += 4)
-        tile[r][c] = x[(i0 + r) * n.lp + l0 + c] * it.scale;
+    const uint16_t* x = reinterpret_cast<const uint16_t*>(ws + it.off + (from ? n.x_next : n.x));
+    uint16_t hi[16], lo[16];
+    const int64_t at0 = (i0 + r0) * n.lp + l0 + c;
+#pragma unroll
+    for (int q = 0; q < 16; q++) {
+        hi[q] = x[at0 + 4 * q * n.lp];
+        lo[q] = x[at0 + 4 * q * n.lp + n.sp * n.lp];
+    }
+#pragma unroll
+    for (int q = 0; q < 16; q++)
+        tile[r0 + 4 * q][c] = (h2f(hi[q]) + h2f(lo[q])) * unscale * it.scale;
     __syncthreads();
     for (int r = r0; r < 64; r += 4) {
         const int64_t row = (tall ? l0 : i0) + r, col = (tall ? i0 : l0) + c;
@@ -649,52 +718,144 @@ __global__ __launch_bounds__(256) void k_nsl_out(const NsItem* __restrict__ tabl
     }
 }
 
-// acc[4] += 64 x 64 tile of Xrows Yrows^T over columns k0 .. k1 (NT: both with the
-// contraction contiguous), or of Xrows Y (NN: Y [k][ldy]). 4 waves of 32 x 32, v_mfma_f32_32x32x2.
-template <bool NT>
-__device__ __forceinline__ void ns_tile(const float* X, int64_t ldx, const float* Y, int64_t ldy, int64_t k0, int64_t k1,
-                                        nf16& acc)
+// A 128 x 128 tile of P Q^T over stages c0 .. c1 - 1 of the contraction, 8 waves of 32 (P) x
+// 64 (Q), in a ring of four stages as in the integer form's product. (128 x 256 tiles, six
+// stages half as deep: 112 against 119 us for X' of a 2048 x 4096 matrix, but 27 against 18
+// with a short side of 221; two blocks per CU of half as deep stages: 139.) P: rows with the
+// contraction contiguous (pitch p_pitch). Q: likewise, or (TURN) rows along the contraction,
+// 128 columns of each, which ds_read_tr turns round. Both as high and low planes, p_low and
+// q_low bytes apart. Result element r of a lane: Q's row or column l % 32 (of 32 f), P's row
+// 8 (r / 4) + 4 (l / 32) + r % 4, or the other way round (TURN: four consecutive columns).
+constexpr int kNsPlane = kNsTile * 64, kNsStage = 4 * kNsPlane;
+typedef short ns_s4 __attribute__((ext_vector_type(4)));
+
+template <bool TURN>
+__device__ __forceinline__ void ns_product(const char* p, int64_t p_pitch, int64_t p_low, const char* q, int64_t q_pitch,
+                                           int64_t q_low, int c0, int c1, char* s0, char* s1, char* s2, char* s3,
+                                           nf16 (&acc)[2])
 {
-    constexpr int KC = 32;
-    __shared__ float xs[64][KC + 1];
-    __shared__ float ys[NT ? 64 : KC][NT ? KC + 1 : 64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int l32 = lane & 31, h = lane >> 5, wm = wave & 1, wn = wave >> 1;
-    for (int64_t k = k0; k < k1; k += KC) {
-        nf4 xv[2], yv[2];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wp = wave & 3, wq = wave >> 2;
+    const int l32 = lane & 31, h = lane >> 5;
+    // a wave loads half a plane: planes P high, P low, Q high, Q low
+    const int plane = wave >> 1;
+    const bool turned = TURN && plane >= 2;
+    const int64_t pitch = plane < 2 ? p_pitch : q_pitch;
+    const char* const from = (plane < 2 ? p + (plane & 1) * p_low : q + (plane & 1) * q_low);
+    int src[4];
 #pragma unroll
-        for (int t = 0; t < 2; t++) {
-            const int u = t * 256 + tid;
-            xv[t] = *reinterpret_cast<const nf4*>(X + (u >> 3) * ldx + k + (u & 7) * 4);
-            yv[t] = NT ? *reinterpret_cast<const nf4*>(Y + (u >> 3) * ldy + k + (u & 7) * 4)
-                       : *reinterpret_cast<const nf4*>(Y + (k + (u >> 4)) * ldy + (u & 15) * 4);
+    for (int t = 0; t < 4; t++) {
+        const int u = (wave & 1) * 256 + t * 64 + lane;
+        // turned: row u / 16 of the stage; piece c of it in slot c ^ 4 (row % 4), so that the
+        // 64 bytes that a read takes of each of four rows lie in different banks
+        src[t] = turned ? (u >> 4) * (int)pitch + ((u & 15) ^ (((u >> 4) & 3) << 2)) * 16
+                        : stage_row(u) * (int)pitch + stage_piece(u) * 16;
+    }
+    const __amdgpu_buffer_rsrc_t whole =
+        uniform_rsrc(from, turned ? (int64_t)c1 * kNsDepth * pitch : (int64_t)kNsTile * pitch);
+    auto dma = [&](int c, char* stage) {
+        const int dead = c < c1 ? 0 : kDeadLoad, cc = min(c, c1 - 1);
+        // (turned: the rows may reach far, so the descriptor moves)
+        const __amdgpu_buffer_rsrc_t r =
+            turned ? uniform_rsrc(from + (int64_t)cc * kNsDepth * pitch, (int64_t)kNsDepth * pitch) : whole;
+        const int o = turned ? 0 : cc * 64;
+#pragma unroll
+        for (int t = 0; t < 4; t++)
+            dma16_lds(r, stage + plane * kNsPlane + ((wave & 1) * 4 + t) * 1024, (src[t] + o) | dead);
+    };
+    // operand reads of 16-deep step st: P's 32 rows, Q's two times 32
+    const int pa[2] = {wp * 2048 + stage_at(l32, h), wp * 2048 + stage_at(l32, 2 + h)};
+    int qa[2][2];
+#pragma unroll
+    for (int st = 0; st < 2; st++)
+#pragma unroll
+        for (int f = 0; f < 2; f++) {
+            if (TURN) {
+                // in a group of 16 lanes, lane i names 4 columns of row i / 4 and gets
+                // column i of the 4 rows; the rows 4 further on by a second read
+                const int row = 16 * st + 8 * h + ((lane & 15) >> 2);
+                const int col = wq * 64 + 32 * f + 16 * ((lane >> 4) & 1) + (lane & 3) * 4;
+                qa[st][f] = 2 * kNsPlane + row * 256 + (((col >> 3) ^ ((row & 3) << 2)) * 16) + (col & 4) * 2;
+            } else
+                qa[st][f] = 2 * kNsPlane + (wq * 2 + f) * 2048 + stage_at(l32, 2 * st + h);
         }
-        __syncthreads();
+    half8_t pv[2][2], qv[2][2][2];  // [set][high, low], [set][high, low][f]
+    auto read = [&](const char* stage, int st) {
 #pragma unroll
-        for (int t = 0; t < 2; t++) {
-            const int u = t * 256 + tid;
+        for (int e = 0; e < 2; e++) {
+            pv[st][e] = *reinterpret_cast<const half8_t*>(stage + e * kNsPlane + pa[st]);
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                xs[u >> 3][(u & 7) * 4 + e] = xv[t][e];
-                if (NT)
-                    ys[u >> 3][(u & 7) * 4 + e] = yv[t][e];
-                else
-                    ys[u >> 4][(u & 15) * 4 + e] = yv[t][e];
+            for (int f = 0; f < 2; f++) {
+                const char* at = stage + e * kNsPlane + qa[st][f];
+                if (TURN) {
+                    const ns_s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) ns_s4*)at);
+                    const ns_s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) ns_s4*)(at + 4 * 256));
+                    qv[st][e][f] = __builtin_bit_cast(half8_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+                } else
+                    qv[st][e][f] = *reinterpret_cast<const half8_t*>(at);
             }
         }
-        __syncthreads();
+    };
+    auto mul = [&](int st) {
 #pragma unroll
-        for (int st = 0; st < KC / 2; st++) {
-            const float a = xs[wm * 32 + l32][2 * st + h];
-            const float b = NT ? ys[wn * 32 + l32][2 * st + h] : ys[2 * st + h][wn * 32 + l32];
-            acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, acc, 0, 0, 0);
+        for (int e = 0; e < 3; e++)  // high high, high low, low high
+#pragma unroll
+            for (int f = 0; f < 2; f++) {
+                const half8_t a = pv[st][e == 2 ? 1 : 0], b = qv[st][e == 1 ? 1 : 0][f];
+                acc[f] = TURN ? __builtin_amdgcn_mfma_f32_32x32x16_f16(b, a, acc[f], 0, 0, 0)
+                              : __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, acc[f], 0, 0, 0);
+            }
+#pragma unroll
+        for (int e = 0; e < 6; e++) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
         }
+    };
+    auto step = [&](int c, const char* cur, const char* next, char* fill) {
+        stage_barrier<4, 15>();
+        dma(c + 3, fill);
+        if (c < c1) {
+            read(cur, 1);
+            mul(0);
+            read(next, 0);
+            mul(1);
+            // the reads of cur are done before this wave lets it be overwritten
+#pragma unroll
+            for (int e = 0; e < 2; e++)
+                asm volatile("" ::"v"(pv[1][e]), "v"(qv[1][e][0]), "v"(qv[1][e][1]));
+        }
+    };
+    dma(c0, s0);
+    dma(c0 + 1, s1);
+    dma(c0 + 2, s2);
+    stage_barrier<8>();
+    read(s0, 0);
+    for (int c = c0; c < c1; c += 4) {
+        step(c, s0, s1, s3);
+        step(c + 1, s1, s2, s0);
+        step(c + 2, s2, s3, s1);
+        step(c + 3, s3, s0, s2);
     }
+#pragma unroll
+    for (int e = 0; e < 2; e++)
+        asm volatile("" ::"v"(pv[0][e]), "v"(qv[0][e][0]), "v"(qv[0][e][1]));
+    stage_barrier<0>();  // the loads past the end have written their zeros
 }
 
-__device__ __forceinline__ void ns_upper(int64_t n, int64_t T, int64_t& ti, int64_t& tj)
+#define NS_STAGES                                                        \
+    __shared__ __attribute__((aligned(1024))) char s0[kNsStage];         \
+    __shared__ __attribute__((aligned(1024))) char s1[kNsStage];         \
+    __shared__ __attribute__((aligned(1024))) char s2[kNsStage];         \
+    __shared__ __attribute__((aligned(1024))) char s3[kNsStage];         \
+    nf16 acc[2];                                                         \
+    for (int f = 0; f < 2; f++)                                          \
+        for (int r = 0; r < 16; r++)                                     \
+            acc[f][r] = 0.0f
+
+__device__ __forceinline__ void ns_upper(int n, int T, int& ti, int& tj)
 {
-    int64_t i = 0;
+    int i = 0;
     while (n >= T - i) {
         n -= T - i;
         i++;
@@ -703,116 +864,202 @@ __device__ __forceinline__ void ns_upper(int64_t n, int64_t T, int64_t& ti, int6
     tj = i + n;
 }
 
-// row and column of element r of a lane in the block's 64 x 64 tile
-__device__ __forceinline__ int ns_row(int r)
+// A = X X^T: tiles on and above the diagonal, `splits` parts of the long side each, in lane order
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_nsl_gram(const NsItem* __restrict__ table,
+                                                                                             char* ws, int from)
 {
+    NS_STAGES;
+    const NsItem it = table[blockIdx.y];
+    const NsLong n = ns_long(it.rows, it.cols);
+    if (blockIdx.x >= n.tiles * n.splits)
+        return;
+    int ti, tj;
+    ns_upper((int)blockIdx.x / n.splits, (int)(n.sp / kNsTile), ti, tj);
+    const int sl = (int)blockIdx.x % n.splits, all = (int)(n.lp / kNsDepth);
+    const char* x = ws + it.off + (from ? n.x_next : n.x);
+    const int64_t pitch = 2 * n.lp, low = 2 * n.sp * n.lp;
+    ns_product<false>(x + ti * kNsTile * pitch, pitch, low, x + tj * kNsTile * pitch, pitch, low, (int)((int64_t)all * sl / n.splits),
+                      (int)((int64_t)all * (sl + 1) / n.splits), s0, s1, s2, s3, acc);
+    nf4* part = reinterpret_cast<nf4*>(ws + it.off + n.parts) + (int64_t)blockIdx.x * (kNsTile * kNsTile / 4) +
+                (threadIdx.x >> 6) * 512 + (threadIdx.x & 63);
+#pragma unroll
+    for (int f = 0; f < 2; f++)
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            part[(f * 4 + e) * 64] = nf4{acc[f][4 * e], acc[f][4 * e + 1], acc[f][4 * e + 2], acc[f][4 * e + 3]};
+}
+
+// Four numbers of a symmetric matrix, rows i .. i + 3 of column j, to both their places
+__device__ __forceinline__ void ns_put(uint16_t* m, int64_t pitch, int64_t low, int i, int j, nf4 v)
+{
+    NsPair p[4];
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+        p[e] = ns_pair(v[e]);
+    if (i + 3 <= j) {
+        *reinterpret_cast<uint2*>(m + j * pitch + i) = make_uint2(p[0].hi | ((uint32_t)p[1].hi << 16), p[2].hi | ((uint32_t)p[3].hi << 16));
+        *reinterpret_cast<uint2*>(m + low + j * pitch + i) =
+            make_uint2(p[0].lo | ((uint32_t)p[1].lo << 16), p[2].lo | ((uint32_t)p[3].lo << 16));
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            m[(i + e) * pitch + j] = p[e].hi;
+            m[low + (i + e) * pitch + j] = p[e].lo;
+        }
+    } else if (i <= j) {  // the diagonal runs through the four
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            if (i + e <= j) {
+                m[(i + e) * pitch + j] = m[j * pitch + i + e] = p[e].hi;
+                m[low + (i + e) * pitch + j] = m[low + j * pitch + i + e] = p[e].lo;
+            }
+    }
+}
+
+// The four numbers of two words of a high and of a low plane
+__device__ __forceinline__ nf4 ns_join(uint2 hi, uint2 lo)
+{
+    const uint32_t ph[2] = {hi.x, hi.y}, pl[2] = {lo.x, lo.y};
+    nf4 v;
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+        v[k] = h2f((uint16_t)(ph[k >> 1] >> (16 * (k & 1)))) + h2f((uint16_t)(pl[k >> 1] >> (16 * (k & 1))));
+    return v;
+}
+
+// The parts' sums: a wave per 32 x 32 piece's quarter. scale: 2^(m of A - 2 m of X)
+__global__ __launch_bounds__(256) void k_nsl_sum(const NsItem* __restrict__ table, char* ws, float scale)
+{
+    const NsItem it = table[blockIdx.y];
+    const NsLong n = ns_long(it.rows, it.cols);
+    const int tile = (int)blockIdx.x >> 4;
+    if (tile >= n.tiles)
+        return;
+    int ti, tj;
+    ns_upper(tile, (int)(n.sp / kNsTile), ti, tj);
+    const int at = ((int)blockIdx.x & 15) * 256 + threadIdx.x;  // vector of four of the tile
+    const nf4* p = reinterpret_cast<const nf4*>(ws + it.off + n.parts) + (int64_t)tile * n.splits * (kNsTile * kNsTile / 4) + at;
+    nf4 s = p[0];
+    int sl = 1;
+    for (; sl + 4 <= n.splits; sl += 4) {
+        nf4 v[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            v[e] = p[(int64_t)(sl + e) * (kNsTile * kNsTile / 4)];
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            s += v[e];
+    }
+    for (; sl < n.splits; sl++)
+        s += p[(int64_t)sl * (kNsTile * kNsTile / 4)];
+    const int wave = at >> 9, f = (at >> 8) & 1, e = (at >> 6) & 3, lane = at & 63;
+    ns_put(reinterpret_cast<uint16_t*>(ws + it.off + n.A), n.sp, n.sp * n.sp, ti * kNsTile + (wave & 3) * 32 + 8 * e + 4 * (lane >> 5),
+           tj * kNsTile + (wave >> 2) * 64 + 32 * f + (lane & 31), s * scale);
+}
+
+// B = b A + c A^2; b and c with the powers of two of A and B
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_nsl_poly(const NsItem* __restrict__ table,
+                                                                                             char* ws, float b, float c)
+{
+    NS_STAGES;
+    const NsItem it = table[blockIdx.y];
+    const NsLong n = ns_long(it.rows, it.cols);
+    if (blockIdx.x >= n.tiles)
+        return;
+    int ti, tj;
+    ns_upper((int)blockIdx.x, (int)(n.sp / kNsTile), ti, tj);
+    const char* A = ws + it.off + n.A;
+    const int64_t pitch = 2 * n.sp, low = 2 * n.sp * n.sp;
+    ns_product<false>(A + ti * kNsTile * pitch, pitch, low, A + tj * kNsTile * pitch, pitch, low, 0, (int)(n.sp / kNsDepth), s0, s1,
+                      s2, s3, acc);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    return (wave & 1) * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-}
-__device__ __forceinline__ int ns_col() { return (threadIdx.x >> 7) * 32 + (threadIdx.x & 31); }
-
-// A = X X^T: upper tiles, `splits` parts of the long side each
-__global__ __launch_bounds__(256) void k_nsl_gram(const NsItem* __restrict__ table, char* ws, int from1)
-{
-    const NsItem it = table[blockIdx.y];
-    const NsLong n = ns_long(it.rows, it.cols);
-    const int64_t T = n.sp / 64, tiles = T * (T + 1) / 2;
-    if (blockIdx.x >= tiles * n.splits)
-        return;
-    int64_t ti, tj;
-    ns_upper(blockIdx.x / n.splits, T, ti, tj);
-    const int64_t sl = blockIdx.x % n.splits, per = (n.lp / 64 + n.splits - 1) / n.splits * 64;
-    const int64_t k0 = sl * per, k1 = k0 + per < n.lp ? k0 + per : n.lp;
-    const float* x = reinterpret_cast<const float*>(ws + it.off + (from1 ? n.x1 : n.x0));
-    nf16 acc;
+    const uint16_t* a = reinterpret_cast<const uint16_t*>(A);
+    const int i0 = ti * kNsTile + (wave & 3) * 32 + 4 * (lane >> 5), j0 = tj * kNsTile + (wave >> 2) * 64 + (lane & 31);
+    uint2 hi[8], lo[8];  // all loads before the first store
 #pragma unroll
-    for (int r = 0; r < 16; r++)
-        acc[r] = 0.0f;
-    ns_tile<true>(x + ti * 64 * n.lp, n.lp, x + tj * 64 * n.lp, n.lp, k0, k1, acc);
-    float* out = reinterpret_cast<float*>(ws + it.off + (n.splits > 1 ? n.parts : n.A)) + (n.splits > 1 ? sl * n.sp * n.sp : 0);
+    for (int q = 0; q < 8; q++) {
+        const uint16_t* at = a + (j0 + 32 * (q >> 2)) * n.sp + i0 + 8 * (q & 3);
+        hi[q] = *reinterpret_cast<const uint2*>(at);
+        lo[q] = *reinterpret_cast<const uint2*>(at + n.sp * n.sp);
+    }
 #pragma unroll
-    for (int r = 0; r < 16; r++) {
-        const int64_t row = ti * 64 + ns_row(r), col = tj * 64 + ns_col();
-        if (row <= col) {
-            out[row * n.sp + col] = acc[r];
-            if (n.splits == 1)
-                out[col * n.sp + row] = acc[r];
-        }
+    for (int q = 0; q < 8; q++) {
+        const nf4 x = ns_join(hi[q], lo[q]);
+        nf4 v;
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            v[k] = __builtin_fmaf(c, acc[q >> 2][4 * (q & 3) + k], b * x[k]);
+        ns_put(reinterpret_cast<uint16_t*>(ws + it.off + n.B), n.sp, n.sp * n.sp, i0 + 8 * (q & 3), j0 + 32 * (q >> 2), v);
     }
 }
 
-// the parts' sums, and their mirror image
-__global__ __launch_bounds__(256) void k_nsl_sum(const NsItem* __restrict__ table, char* ws)
+// X' = a X + B X; a and the product with the powers of two of X, B and X'
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_nsl_step(const NsItem* __restrict__ table,
+                                                                                             char* ws, float a, float scale, int from)
 {
+    NS_STAGES;
     const NsItem it = table[blockIdx.y];
     const NsLong n = ns_long(it.rows, it.cols);
-    const int64_t T = n.sp / 64, tiles = T * (T + 1) / 2;
-    if (n.splits == 1 || blockIdx.x >= tiles * 16)
+    const int T = (int)(n.sp / kNsTile);
+    if (blockIdx.x >= T * (n.lp / kNsTile))
         return;
-    int64_t ti, tj;
-    ns_upper(blockIdx.x >> 4, T, ti, tj);
-    const int64_t row = ti * 64 + ((blockIdx.x & 15) * 4 + (threadIdx.x >> 6)), col = tj * 64 + (threadIdx.x & 63);
-    if (row > col)
-        return;
-    const float* p = reinterpret_cast<const float*>(ws + it.off + n.parts) + row * n.sp + col;
-    float s = 0.0f;
-    for (int i = 0; i < n.splits; i++)
-        s += p[i * n.sp * n.sp];
-    float* A = reinterpret_cast<float*>(ws + it.off + n.A);
-    A[row * n.sp + col] = s;
-    A[col * n.sp + row] = s;
-}
-
-// B = b A + c A^2
-__global__ __launch_bounds__(256) void k_nsl_poly(const NsItem* __restrict__ table, char* ws, float b, float c)
-{
-    const NsItem it = table[blockIdx.y];
-    const NsLong n = ns_long(it.rows, it.cols);
-    const int64_t T = n.sp / 64;
-    if (blockIdx.x >= T * (T + 1) / 2)
-        return;
-    int64_t ti, tj;
-    ns_upper(blockIdx.x, T, ti, tj);
-    const float* A = reinterpret_cast<const float*>(ws + it.off + n.A);
-    nf16 acc;
+    const int place = xcd_place((int)blockIdx.x, (int)(T * (n.lp / kNsTile)));
+    const int ti = place % T;
+    const int64_t l0 = (int64_t)(place / T) * kNsTile;
+    const char* x = ws + it.off + (from ? n.x_next : n.x);
+    const char* B = ws + it.off + n.B;
+    const int64_t low = n.sp * n.lp;
+    ns_product<true>(B + ti * kNsTile * (2 * n.sp), 2 * n.sp, 2 * n.sp * n.sp, x + 2 * l0, 2 * n.lp, 2 * low, 0, (int)(n.sp / kNsDepth),
+                     s0, s1, s2, s3, acc);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint16_t* xo = reinterpret_cast<const uint16_t*>(x);
+    uint16_t* y = reinterpret_cast<uint16_t*>(ws + it.off + (from ? n.x : n.x_next));
+    const int64_t at0 = (ti * kNsTile + (wave & 3) * 32 + (lane & 31)) * n.lp + l0 + (wave >> 2) * 64 + 4 * (lane >> 5);
+    uint2 hi[8], lo[8];  // all loads before the first store
 #pragma unroll
-    for (int r = 0; r < 16; r++)
-        acc[r] = 0.0f;
-    ns_tile<true>(A + ti * 64 * n.sp, n.sp, A + tj * 64 * n.sp, n.sp, 0, n.sp, acc);
-    float* B = reinterpret_cast<float*>(ws + it.off + n.B);
+    for (int q = 0; q < 8; q++) {
+        hi[q] = *reinterpret_cast<const uint2*>(xo + at0 + 8 * q);
+        lo[q] = *reinterpret_cast<const uint2*>(xo + low + at0 + 8 * q);
+    }
 #pragma unroll
-    for (int r = 0; r < 16; r++) {
-        const int64_t row = ti * 64 + ns_row(r), col = tj * 64 + ns_col();
-        const float v = __builtin_fmaf(c, acc[r], b * A[row * n.sp + col]);
-        if (row <= col) {
-            B[row * n.sp + col] = v;
-            B[col * n.sp + row] = v;
-        }
+    for (int q = 0; q < 8; q++) {
+        const nf4 v = ns_join(hi[q], lo[q]);
+        NsPair p[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            p[k] = ns_pair(__builtin_fmaf(a, v[k], acc[q >> 2][4 * (q & 3) + k] * scale));
+        *reinterpret_cast<uint2*>(y + at0 + 8 * q) = make_uint2(p[0].hi | ((uint32_t)p[1].hi << 16), p[2].hi | ((uint32_t)p[3].hi << 16));
+        *reinterpret_cast<uint2*>(y + low + at0 + 8 * q) = make_uint2(p[0].lo | ((uint32_t)p[1].lo << 16), p[2].lo | ((uint32_t)p[3].lo << 16));
     }
 }
 
-// X' = a X + B X
-__global__ __launch_bounds__(256) void k_nsl_step(const NsItem* __restrict__ table, char* ws, float a, int from1)
+// Powers of two that bring numbers of at most `bound` below 2^14, as exponents
+int ns_exponent(double bound)
 {
-    const NsItem it = table[blockIdx.y];
-    const NsLong n = ns_long(it.rows, it.cols);
-    const int64_t T = n.sp / 64;
-    if (blockIdx.x >= T * (n.lp / 64))
-        return;
-    const int64_t ti = blockIdx.x % T, tl = blockIdx.x / T;
-    const float* x = reinterpret_cast<const float*>(ws + it.off + (from1 ? n.x1 : n.x0));
-    float* y = reinterpret_cast<float*>(ws + it.off + (from1 ? n.x0 : n.x1));
-    const float* B = reinterpret_cast<const float*>(ws + it.off + n.B);
-    nf16 acc;
-#pragma unroll
-    for (int r = 0; r < 16; r++)
-        acc[r] = 0.0f;
-    ns_tile<false>(B + ti * 64 * n.sp, n.sp, x + tl * 64, n.lp, 0, n.sp, acc);
-#pragma unroll
-    for (int r = 0; r < 16; r++) {
-        const int64_t at = (ti * 64 + ns_row(r)) * n.lp + tl * 64 + ns_col();
-        y[at] = __builtin_fmaf(a, x[at], acc[r]);
+    int e = 0;
+    std::frexp(bound > 1e-30 ? (bound < 1e30 ? bound : 1e30) : 1e-30, &e);  // bound <= 2^e
+    return 14 - e;
+}
+
+// Bounds of what a step holds: the elements of A and of B (no element of a symmetric matrix
+// passes its largest |eigenvalue|) and the singular values that it leaves, from those it
+// finds (at most x) and its polynomial on a grid over [0, x]. 1e-3 is for what lies between
+// the grid's points and for roundings; much more would grow from step to step where the
+// polynomial leaves its range (with 3.4445, -4.775, 2.0315, 1.2025 maps into itself and 1.27
+// does not). Above 2^14 the pairs have a factor of 4 left.
+struct NsBound {
+    double a, b, next;
+};
+NsBound ns_bound(double x, double a, double b, double c)
+{
+    NsBound n{x * x, 0.0, 0.0};
+    for (int i = 0; i <= 1024; i++) {
+        const double v = x * i / 1024.0, l = v * v;
+        n.b = std::fmax(n.b, std::fabs(b * l + c * l * l));
+        n.next = std::fmax(n.next, std::fabs(v * (a + b * l + c * l * l)));
     }
+    n.b *= 1.001;
+    n.next *= 1.001;
+    return n;
 }
 
 // ------------------------------------------------------------------ the plan --
@@ -890,7 +1137,7 @@ hipError_t launch_orthogonalize(const OrthoEntry* items, int count, double a, do
     grams = applies = 0;
     int longs = 0, shorts = 0;
     unsigned pairs = 0;
-    int64_t lsq = 0, ltile = 0, lgram = 0, lsum = 0, lpoly = 0, lstep = 0;
+    int64_t lsq = 0, ltile = 0, lgram = 0, lpoly = 0, lstep = 0;
     auto most = [](auto& v, auto x) { v = v > x ? v : x; };
     NsArgs args{};
     auto flush = [&] {
@@ -918,13 +1165,11 @@ hipError_t launch_orthogonalize(const OrthoEntry* items, int count, double a, do
                 shorts++;
             } else {
                 const NsLong p = ns_long(e.rows, e.cols);
-                const int64_t n = p.sp / 64, upper = n * (n + 1) / 2;
                 most(lsq, (int64_t)p.sqn);
-                most(ltile, n * (p.lp / 64));
-                most(lgram, upper * p.splits);
-                most(lsum, p.splits > 1 ? upper * 16 : 0);
-                most(lpoly, upper);
-                most(lstep, n * (p.lp / 64));
+                most(ltile, (p.sp / 64) * (p.lp / 64));
+                most(lgram, p.tiles * p.splits);
+                most(lpoly, p.tiles);
+                most(lstep, (p.sp / kNsTile) * (p.lp / kNsTile));
                 longs++;
             }
             args.it[args.count++] = it;
@@ -946,15 +1191,24 @@ hipError_t launch_orthogonalize(const OrthoEntry* items, int count, double a, do
     if (longs > 0) {
         const unsigned y = (unsigned)longs;
         hipLaunchKernelGGL(k_nsl_sumsq, dim3((unsigned)lsq, y), dim3(256), 0, s, table, w);
-        hipLaunchKernelGGL(k_nsl_init, dim3((unsigned)ltile, y), dim3(256), 0, s, table, w, eps);
+        auto two = [](int e) { return (float)std::ldexp(1.0, e); };
+        double bound = 1.0;
+        int mx = ns_exponent(bound);
+        hipLaunchKernelGGL(k_nsl_init, dim3((unsigned)ltile, y), dim3(256), 0, s, table, w, eps, two(mx));
         for (int st = 0; st < steps; st++) {
-            hipLaunchKernelGGL(k_nsl_gram, dim3((unsigned)lgram, y), dim3(256), 0, s, table, w, st & 1);
-            if (lsum > 0)
-                hipLaunchKernelGGL(k_nsl_sum, dim3((unsigned)lsum, y), dim3(256), 0, s, table, w);
-            hipLaunchKernelGGL(k_nsl_poly, dim3((unsigned)lpoly, y), dim3(256), 0, s, table, w, (float)b, (float)c);
-            hipLaunchKernelGGL(k_nsl_step, dim3((unsigned)lstep, y), dim3(256), 0, s, table, w, (float)a, st & 1);
+            const NsBound n = ns_bound(bound, a, b, c);
+            const int ma = ns_exponent(n.a), mb = ns_exponent(n.b);
+            bound = n.next;
+            const int next = ns_exponent(bound);
+            hipLaunchKernelGGL(k_nsl_gram, dim3((unsigned)lgram, y), dim3(512), 0, s, table, w, st & 1);
+            hipLaunchKernelGGL(k_nsl_sum, dim3((unsigned)(16 * lpoly), y), dim3(256), 0, s, table, w, two(ma - 2 * mx));
+            hipLaunchKernelGGL(k_nsl_poly, dim3((unsigned)lpoly, y), dim3(512), 0, s, table, w, (float)(b * two(mb - ma)),
+                               (float)(c * two(mb - 2 * ma)));
+            hipLaunchKernelGGL(k_nsl_step, dim3((unsigned)lstep, y), dim3(512), 0, s, table, w, (float)(a * two(next - mx)),
+                               two(next - mb - mx), st & 1);
+            mx = next;
         }
-        hipLaunchKernelGGL(k_nsl_out, dim3((unsigned)ltile, y), dim3(256), 0, s, table, w, steps & 1);
+        hipLaunchKernelGGL(k_nsl_out, dim3((unsigned)ltile, y), dim3(256), 0, s, table, w, steps & 1, two(-mx));
     }
     return hipGetLastError();
 }
