@@ -33,7 +33,7 @@ struct NsItem {
     float scale;
     int32_t half;     // 1: fp16, 0: fp32
     int32_t tiles;    // short form: 16-wide tiles of the short side (2, 4 or 6)
-    int32_t slices;   // of the long side, a block of k_ns_gram each
+    int32_t slices;   // of the long side, a block of k_ns_gram each (long form: parts, a block each per tile)
     int32_t gram0, apply0;  // first blocks of k_ns_gram and k_ns_apply
 };
 static_assert(sizeof(NsItem) == 56, "table entry");
@@ -536,38 +536,75 @@ __global__ __launch_bounds__(256) void k_ns_apply(const NsItem* __restrict__ tab
 // step, which the caller of the kernels works out from the coefficients, so nothing
 // overflows.
 //
-// X lies with the long side contiguous, both sides padded to 128 with zeros.
+// A number's high and low halves lie 32 bytes apart: 16 highs, 16 lows, 16 highs, ... along
+// a row, so that 16 of a row are one run of 64 bytes, which is what a stage of the products
+// takes. X lies with the long side contiguous, padded with zeros: the short side to 128, the
+// long side to 256.
 struct NsLong {
-    int64_t sp, lp, tiles;
-    int64_t x, x_next, A, B, parts, sq, total;  // byte offsets; high planes first, low behind
-    int32_t splits, sqn;
+    int64_t sp, lp;
+    int64_t sq, x, x_next, A, B, parts;  // byte offsets
+    int32_t sqn;
+    int32_t high;         // tiles of 128 down the short side
+    int32_t wide;         // tiles of A and of X' are 128 x 256, else 128 x 128
+    int32_t tiles, gram;  // tiles of A on and above the diagonal, parts of the long side
+    int32_t squares;      // the same of A^2, 128 x 128
 };
 
-constexpr int kNsTile = 128, kNsDepth = 32;  // of the products: tile, contraction per stage
+constexpr int kNsTile = 128, kNsDepth = 16;  // of the products: rows of a tile, contraction per stage
+constexpr int kNsMaxParts = 64;
 
-__host__ __device__ inline NsLong ns_long(int64_t rows, int64_t cols)
+// gram: the parts, ns_parts' choice
+__host__ __device__ inline NsLong ns_long(int64_t rows, int64_t cols, int32_t gram)
 {
-    NsLong n{};
+    NsLong n;
     const int64_t s = rows < cols ? rows : cols, l = rows < cols ? cols : rows;
-    n.sp = (s + kNsTile - 1) / kNsTile * kNsTile;
-    n.lp = (l + kNsTile - 1) / kNsTile * kNsTile;
-    const int64_t t = n.sp / kNsTile;
-    n.tiles = t * (t + 1) / 2;  // on and above A's diagonal
-    // the long side in as many parts as give every CU a block, each of at least 8 stages
-    int64_t sp = 256 / n.tiles;
-    sp = sp < n.lp / (8 * kNsDepth) ? sp : n.lp / (8 * kNsDepth);
-    n.splits = (int32_t)(sp < 1 ? 1 : sp);
-    const int64_t sq = (rows * cols + 16383) / 16384;
+    n.sp = (s + 127) & ~(int64_t)127;
+    n.lp = (l + 255) & ~(int64_t)255;
+    n.high = (int)(n.sp >> 7);
+    n.squares = n.high * (n.high + 1) / 2;
+    // 128 x 256 where they fill the 256 CUs (X' of 2048 x 4096: 100 against 112 us), else
+    // twice as many that half as many bytes feed
+    n.wide = n.high * (n.lp >> 8) >= 256;
+    const int half = (n.high + 1) / 2;
+    n.tiles = n.wide ? half * (half + 1) - (n.high & 1) : n.squares;
+    n.gram = gram;
+    const int64_t sq = (s * l + 16383) >> 14;
     n.sqn = (int32_t)(sq < 1024 ? sq : 1024);
-    int64_t off = 0;
-    n.x = off, off += 4 * n.sp * n.lp;
-    n.x_next = off, off += 4 * n.sp * n.lp;
-    n.A = off, off += 4 * n.sp * n.sp;
-    n.B = off, off += 4 * n.sp * n.sp;
-    n.parts = off, off += 4 * n.splits * n.tiles * kNsTile * kNsTile;
-    n.sq = off, off += 8 * n.sqn;
-    n.total = (off + 255) / 256 * 256;
+    n.sq = 0;
+    n.x = 8192;
+    n.x_next = n.x + 4 * n.sp * n.lp;
+    n.A = n.x_next + 4 * n.sp * n.lp;
+    n.B = n.A + 4 * n.sp * n.sp;
+    n.parts = n.B + 4 * n.sp * n.sp;
     return n;
+}
+
+int64_t ns_long_bytes(const NsLong& n) { return n.parts + (int64_t)n.gram * n.tiles * (n.wide ? 2 : 1) * (4 * 128 * 128); }
+
+// The long side in parts: the rounds of 256 blocks that they take (0.35 us per 128 x 128 and
+// stage) against the partial tiles that are written and read (64 KB each, at 4 TB/s); a part
+// has at least 16 stages.
+int ns_parts(int64_t rows, int64_t cols)
+{
+    const NsLong n = ns_long(rows, cols, 1);
+    const int stages = (int)(n.lp / kNsDepth);
+    double best = 0.0;
+    int parts = 1;
+    for (int p = 1; p <= kNsMaxParts && (p == 1 || p * 16 <= stages); p++) {
+        const int rounds = (n.tiles * p + 255) / 256;
+        const double t = (n.wide ? 2 : 1) * rounds * ((stages + p - 1) / p) * 0.35 + (double)(p * n.squares) * 0.033;
+        if (p == 1 || t < best) {
+            best = t;
+            parts = p;
+        }
+    }
+    return parts;
+}
+
+// place of element (r, c) of a matrix of pairs in 16-bit units; its low half lies 16 further on
+__host__ __device__ inline int64_t ns_place(int64_t r, int64_t c, int64_t pitch)
+{
+    return 2 * r * pitch + ((c >> 4) << 5) + (c & 15);
 }
 
 __device__ __forceinline__ double ns_block_sum(double v, double* red)
@@ -587,7 +624,7 @@ __global__ __launch_bounds__(256) void k_nsl_sumsq(const NsItem* __restrict__ ta
 {
     __shared__ double red[4];
     const NsItem it = table[blockIdx.y];
-    const NsLong n = ns_long(it.rows, it.cols);
+    const NsLong n = ns_long(it.rows, it.cols, it.slices);
     if ((int)blockIdx.x >= n.sqn)
         return;
     const int64_t total = (int64_t)it.rows * it.cols;
@@ -637,7 +674,7 @@ __global__ __launch_bounds__(256) void k_nsl_init(const NsItem* __restrict__ tab
     __shared__ double red[4];
     __shared__ float tile[64][65];
     const NsItem it = table[blockIdx.y];
-    const NsLong n = ns_long(it.rows, it.cols);
+    const NsLong n = ns_long(it.rows, it.cols, it.slices);
     const int64_t tl = n.lp / 64;
     if (blockIdx.x >= (n.sp / 64) * tl)
         return;
@@ -675,9 +712,9 @@ __global__ __launch_bounds__(256) void k_nsl_init(const NsItem* __restrict__ tab
     uint16_t* x = reinterpret_cast<uint16_t*>(ws + it.off + n.x);
     for (int r = r0; r < 64; r += 4) {
         const NsPair p = ns_pair(tall ? tile[c][r] : tile[r][c]);
-        const int64_t at = (i0 + r) * n.lp + l0 + c;
+        const int64_t at = ns_place(i0 + r, l0 + c, n.lp);
         x[at] = p.hi;
-        x[n.sp * n.lp + at] = p.lo;
+        x[at + 16] = p.lo;
     }
 }
 
@@ -686,7 +723,7 @@ __global__ __launch_bounds__(256) void k_nsl_out(const NsItem* __restrict__ tabl
 {
     __shared__ float tile[64][65];
     const NsItem it = table[blockIdx.y];
-    const NsLong n = ns_long(it.rows, it.cols);
+    const NsLong n = ns_long(it.rows, it.cols, it.slices);
     const int64_t tl = n.lp / 64;
     if (blockIdx.x >= (n.sp / 64) * tl)
         return;
@@ -695,11 +732,11 @@ __global__ __launch_bounds__(256) void k_nsl_out(const NsItem* __restrict__ tabl
     const int c = threadIdx.x & 63, r0 = threadIdx.x >> 6;
     const uint16_t* x = reinterpret_cast<const uint16_t*>(ws + it.off + (from ? n.x_next : n.x));
     uint16_t hi[16], lo[16];
-    const int64_t at0 = (i0 + r0) * n.lp + l0 + c;
+    const int64_t at0 = ns_place(i0 + r0, l0 + c, n.lp);
 #pragma unroll
     for (int q = 0; q < 16; q++) {
-        hi[q] = x[at0 + 4 * q * n.lp];
-        lo[q] = x[at0 + 4 * q * n.lp + n.sp * n.lp];
+        hi[q] = x[at0 + 8 * q * n.lp];
+        lo[q] = x[at0 + 8 * q * n.lp + 16];
     }
 #pragma unroll
     for (int q = 0; q < 16; q++)
@@ -718,318 +755,459 @@ __global__ __launch_bounds__(256) void k_nsl_out(const NsItem* __restrict__ tabl
     }
 }
 
-// A 128 x 128 tile of P Q^T over stages c0 .. c1 - 1 of the contraction, 8 waves of 32 (P) x
-// 64 (Q), in a ring of four stages as in the integer form's product. (128 x 256 tiles, six
-// stages half as deep: 112 against 119 us for X' of a 2048 x 4096 matrix, but 27 against 18
-// with a short side of 221; two blocks per CU of half as deep stages: 139.) P: rows with the
-// contraction contiguous (pitch p_pitch). Q: likewise, or (TURN) rows along the contraction,
-// 128 columns of each, which ds_read_tr turns round. Both as high and low planes, p_low and
-// q_low bytes apart. Result element r of a lane: Q's row or column l % 32 (of 32 f), P's row
-// 8 (r / 4) + 4 (l / 32) + r % 4, or the other way round (TURN: four consecutive columns).
-constexpr int kNsPlane = kNsTile * 64, kNsStage = 4 * kNsPlane;
+// A tile of P Q^T over stages c0 .. c1 - 1 of the contraction, 128 rows of P by 128 FP of Q,
+// 8 waves of 32 FP x 64, operands read one stage ahead, in a ring of six stages (FP = 2) or of
+// eight with a barrier for every second one (FP = 1: its stages are half as long). P: rows
+// with the contraction contiguous (pitch in bytes), Q: likewise, q_rows of them, or (TURN)
+// rows along the contraction, 128 FP columns of each, which ds_read_tr turns round. Result
+// element r of a lane in acc[g][f]: Q's row (of 32 (2 wq + f)) l % 32, P's row
+// 8 (r / 4) + 4 (l / 32) + r % 4 (of 32 (FP wp + g)), or the other way round (TURN: four
+// consecutive columns).
+constexpr int kNsStageP = kNsTile * 64;
 typedef short ns_s4 __attribute__((ext_vector_type(4)));
 
-template <bool TURN>
-__device__ __forceinline__ void ns_product(const char* p, int64_t p_pitch, int64_t p_low, const char* q, int64_t q_pitch,
-                                           int64_t q_low, int c0, int c1, char* s0, char* s1, char* s2, char* s3,
-                                           nf16 (&acc)[2])
+template <int FP, bool TURN>
+__device__ __forceinline__ void ns_product(const char* p, int64_t p_pitch, const char* q, int64_t q_pitch, int q_rows, int c0,
+                                           int c1, char* s0, char* s1, char* s2, char* s3, char* s4, char* s5, char* s6,
+                                           char* s7, nf16 (&acc)[FP][2])
 {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wp = wave & 3, wq = wave >> 2;
+    const int wp = FP == 2 ? wave & 1 : wave & 3, wq = FP == 2 ? wave >> 1 : wave >> 2;
     const int l32 = lane & 31, h = lane >> 5;
-    // a wave loads half a plane: planes P high, P low, Q high, Q low
-    const int plane = wave >> 1;
-    const bool turned = TURN && plane >= 2;
-    const int64_t pitch = plane < 2 ? p_pitch : q_pitch;
-    const char* const from = (plane < 2 ? p + (plane & 1) * p_low : q + (plane & 1) * q_low);
-    int src[4];
+    // turned: 64 FP-byte units per row; unit c of row r in slot c ^ (2 (r % 2) + 8 (r / 2 % 2)),
+    // so that the two times 32 bytes that a read takes of each of four rows lie in different banks
+    auto turn = [](int row) { return ((row & 1) << 1) | ((row & 2) << 2); };
+    const int up = wave * 64 + lane;
+    const int src_p = stage_row(up) * (int)p_pitch + stage_piece(up) * 16;
+    int src_q[FP];
 #pragma unroll
-    for (int t = 0; t < 4; t++) {
-        const int u = (wave & 1) * 256 + t * 64 + lane;
-        // turned: row u / 16 of the stage; piece c of it in slot c ^ 4 (row % 4), so that the
-        // 64 bytes that a read takes of each of four rows lie in different banks
-        src[t] = turned ? (u >> 4) * (int)pitch + ((u & 15) ^ (((u >> 4) & 3) << 2)) * 16
-                        : stage_row(u) * (int)pitch + stage_piece(u) * 16;
+    for (int t = 0; t < FP; t++) {
+        const int u = (wave * FP + t) * 64 + lane, row = u / (32 * FP);
+        src_q[t] = TURN ? row * (int)q_pitch + ((u & (32 * FP - 1)) ^ turn(row)) * 16
+                        : stage_row(u) * (int)q_pitch + stage_piece(u) * 16;
     }
-    const __amdgpu_buffer_rsrc_t whole =
-        uniform_rsrc(from, turned ? (int64_t)c1 * kNsDepth * pitch : (int64_t)kNsTile * pitch);
+    const __amdgpu_buffer_rsrc_t rp = uniform_rsrc(p, (int64_t)kNsTile * p_pitch);
+    const __amdgpu_buffer_rsrc_t rq = uniform_rsrc(q, (int64_t)(TURN ? kNsDepth : q_rows) * q_pitch);
     auto dma = [&](int c, char* stage) {
         const int dead = c < c1 ? 0 : kDeadLoad, cc = min(c, c1 - 1);
+        dma16_lds(rp, stage + wave * 1024, (src_p + cc * 64) | dead);
         // (turned: the rows may reach far, so the descriptor moves)
         const __amdgpu_buffer_rsrc_t r =
-            turned ? uniform_rsrc(from + (int64_t)cc * kNsDepth * pitch, (int64_t)kNsDepth * pitch) : whole;
-        const int o = turned ? 0 : cc * 64;
+            TURN ? uniform_rsrc(q + (int64_t)cc * kNsDepth * q_pitch, (int64_t)kNsDepth * q_pitch) : rq;
 #pragma unroll
-        for (int t = 0; t < 4; t++)
-            dma16_lds(r, stage + plane * kNsPlane + ((wave & 1) * 4 + t) * 1024, (src[t] + o) | dead);
+        for (int t = 0; t < FP; t++)
+            dma16_lds(r, stage + kNsStageP + (wave * FP + t) * 1024, (src_q[t] + (TURN ? 0 : cc * 64)) | dead);
     };
-    // operand reads of 16-deep step st: P's 32 rows, Q's two times 32
-    const int pa[2] = {wp * 2048 + stage_at(l32, h), wp * 2048 + stage_at(l32, 2 + h)};
-    int qa[2][2];
+    int pa[2], qa[2][2];  // [high, low]
 #pragma unroll
-    for (int st = 0; st < 2; st++)
+    for (int e = 0; e < 2; e++) {
+        pa[e] = wp * FP * 2048 + stage_at(l32, 2 * e + h);
 #pragma unroll
         for (int f = 0; f < 2; f++) {
             if (TURN) {
-                // in a group of 16 lanes, lane i names 4 columns of row i / 4 and gets
-                // column i of the 4 rows; the rows 4 further on by a second read
-                const int row = 16 * st + 8 * h + ((lane & 15) >> 2);
-                const int col = wq * 64 + 32 * f + 16 * ((lane >> 4) & 1) + (lane & 3) * 4;
-                qa[st][f] = 2 * kNsPlane + row * 256 + (((col >> 3) ^ ((row & 3) << 2)) * 16) + (col & 4) * 2;
+                // in a group of 16 lanes, lane i names 4 columns of row i / 4 and gets column
+                // i of the 4 rows; the rows 4 further on by a second read
+                const int row = 8 * h + ((lane & 15) >> 2);
+                const int unit = (wq * 4 + 2 * f + ((lane >> 4) & 1)) * 4 + 2 * e + ((lane & 3) >> 1);
+                qa[e][f] = kNsStageP + row * (512 * FP) + (unit ^ turn(row)) * 16 + (lane & 1) * 8;
             } else
-                qa[st][f] = 2 * kNsPlane + (wq * 2 + f) * 2048 + stage_at(l32, 2 * st + h);
+                qa[e][f] = kNsStageP + (wq * 2 + f) * 2048 + stage_at(l32, 2 * e + h);
         }
-    half8_t pv[2][2], qv[2][2][2];  // [set][high, low], [set][high, low][f]
+    }
+    half8_t pv[2][2][FP], qv[2][2][2];  // [set][high, low][g or f]
     auto read = [&](const char* stage, int st) {
 #pragma unroll
         for (int e = 0; e < 2; e++) {
-            pv[st][e] = *reinterpret_cast<const half8_t*>(stage + e * kNsPlane + pa[st]);
+#pragma unroll
+            for (int g = 0; g < FP; g++)
+                pv[st][e][g] = *reinterpret_cast<const half8_t*>(stage + pa[e] + g * 2048);
 #pragma unroll
             for (int f = 0; f < 2; f++) {
-                const char* at = stage + e * kNsPlane + qa[st][f];
+                const char* at = stage + qa[e][f];
                 if (TURN) {
                     const ns_s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) ns_s4*)at);
-                    const ns_s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) ns_s4*)(at + 4 * 256));
+                    const ns_s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        (__attribute__((address_space(3))) ns_s4*)(at + 4 * 512 * FP));
                     qv[st][e][f] = __builtin_bit_cast(half8_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
                 } else
                     qv[st][e][f] = *reinterpret_cast<const half8_t*>(at);
             }
         }
     };
-    auto mul = [&](int st) {
+    auto hold = [&](int st) {  // the reads of this set are done here
+#pragma unroll
+        for (int e = 0; e < 2; e++)
+            asm volatile("" ::"v"(pv[st][e][0]), "v"(pv[st][e][FP - 1]), "v"(qv[st][e][0]), "v"(qv[st][e][1]));
+    };
+    auto mul = [&](int c, int st, const char* next) {
+        if (c >= c1)
+            return;
+        read(next, st ^ 1);
 #pragma unroll
         for (int e = 0; e < 3; e++)  // high high, high low, low high
 #pragma unroll
-            for (int f = 0; f < 2; f++) {
-                const half8_t a = pv[st][e == 2 ? 1 : 0], b = qv[st][e == 1 ? 1 : 0][f];
-                acc[f] = TURN ? __builtin_amdgcn_mfma_f32_32x32x16_f16(b, a, acc[f], 0, 0, 0)
-                              : __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, acc[f], 0, 0, 0);
-            }
+            for (int g = 0; g < FP; g++)
 #pragma unroll
-        for (int e = 0; e < 6; e++) {
+                for (int f = 0; f < 2; f++) {
+                    const half8_t a = pv[st][e == 2 ? 1 : 0][g], b = qv[st][e == 1 ? 1 : 0][f];
+                    acc[g][f] = TURN ? __builtin_amdgcn_mfma_f32_32x32x16_f16(b, a, acc[g][f], 0, 0, 0)
+                                     : __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, acc[g][f], 0, 0, 0);
+                }
+#pragma unroll
+        for (int e = 0; e < 6 * FP; e++) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, FP == 2 ? 1 : 2, 0);
         }
-    };
-    auto step = [&](int c, const char* cur, const char* next, char* fill) {
-        stage_barrier<4, 15>();
-        dma(c + 3, fill);
-        if (c < c1) {
-            read(cur, 1);
-            mul(0);
-            read(next, 0);
-            mul(1);
-            // the reads of cur are done before this wave lets it be overwritten
-#pragma unroll
-            for (int e = 0; e < 2; e++)
-                asm volatile("" ::"v"(pv[1][e]), "v"(qv[1][e][0]), "v"(qv[1][e][1]));
-        }
+        hold(st);
     };
     dma(c0, s0);
     dma(c0 + 1, s1);
     dma(c0 + 2, s2);
-    stage_barrier<8>();
-    read(s0, 0);
-    for (int c = c0; c < c1; c += 4) {
-        step(c, s0, s1, s3);
-        step(c + 1, s1, s2, s0);
-        step(c + 2, s2, s3, s1);
-        step(c + 3, s3, s0, s2);
+    dma(c0 + 3, s3);
+    dma(c0 + 4, s4);
+    if constexpr (FP == 2) {
+        auto step = [&](int c, int st, const char* next, char* fill) {
+            stage_barrier<9, 15>();  // stage c + 1 has arrived, everyone has read stage c - 1
+            dma(c + 5, fill);
+            mul(c, st, next);
+        };
+        stage_barrier<12>();
+        read(s0, 0);
+        for (int c = c0; c < c1; c += 6) {
+            step(c, 0, s1, s5);
+            step(c + 1, 1, s2, s0);
+            step(c + 2, 0, s3, s1);
+            step(c + 3, 1, s4, s2);
+            step(c + 4, 0, s5, s3);
+            step(c + 5, 1, s0, s4);
+        }
+    } else {
+        auto step = [&](int c, const char* n1, const char* n2, char* f1, char* f2) {
+            stage_barrier<6, 15>();  // stage c + 2 has arrived, everyone has read stage c - 1
+            dma(c + 6, f1);
+            dma(c + 7, f2);
+            mul(c, 0, n1);
+            mul(c + 1, 1, n2);
+        };
+        dma(c0 + 5, s5);
+        stage_barrier<10>();
+        read(s0, 0);
+        for (int c = c0; c < c1; c += 8) {
+            step(c, s1, s2, s6, s7);
+            step(c + 2, s3, s4, s0, s1);
+            step(c + 4, s5, s6, s2, s3);
+            step(c + 6, s7, s0, s4, s5);
+        }
     }
-#pragma unroll
-    for (int e = 0; e < 2; e++)
-        asm volatile("" ::"v"(pv[0][e]), "v"(qv[0][e][0]), "v"(qv[0][e][1]));
+    hold(0);
+    hold(1);
     stage_barrier<0>();  // the loads past the end have written their zeros
 }
 
-#define NS_STAGES                                                        \
-    __shared__ __attribute__((aligned(1024))) char s0[kNsStage];         \
-    __shared__ __attribute__((aligned(1024))) char s1[kNsStage];         \
-    __shared__ __attribute__((aligned(1024))) char s2[kNsStage];         \
-    __shared__ __attribute__((aligned(1024))) char s3[kNsStage];         \
-    nf16 acc[2];                                                         \
-    for (int f = 0; f < 2; f++)                                          \
-        for (int r = 0; r < 16; r++)                                     \
-            acc[f][r] = 0.0f
+#define NS_STAGES                                                                              \
+    constexpr int kStage = kNsStageP * (FP + 1), kSpare = FP == 1 ? kStage : 16;               \
+    __shared__ __attribute__((aligned(1024))) char s0[kStage], s1[kStage], s2[kStage], s3[kStage], s4[kStage], s5[kStage], \
+        s6[kSpare], s7[kSpare]
 
-__device__ __forceinline__ void ns_upper(int n, int T, int& ti, int& tj)
+template <int FP>
+__device__ __forceinline__ void ns_clear(nf16 (&acc)[FP][2])
 {
-    int i = 0;
-    while (n >= T - i) {
-        n -= T - i;
-        i++;
-    }
-    ti = i;
-    tj = i + n;
+#pragma unroll
+    for (int g = 0; g < FP; g++)
+#pragma unroll
+        for (int f = 0; f < 2; f++)
+#pragma unroll
+            for (int r = 0; r < 16; r++)
+                acc[g][f][r] = 0.0f;
 }
 
-// A = X X^T: tiles on and above the diagonal, `splits` parts of the long side each, in lane order
+// Tile n of those on and above the diagonal of a matrix T tiles high
+template <int FP>
+__device__ __forceinline__ void ns_upper(int n, int T, int& ti, int& tj)
+{
+    tj = 0;
+    for (;;) {
+        const int here = min(T, (tj + 1) * FP);
+        if (n < here)
+            break;
+        n -= here;
+        tj++;
+    }
+    ti = n;
+}
+
+// A = X X^T, the tiles on and above the diagonal, parts of the long side each, left in lane
+// order
+template <int FP>
+__device__ __forceinline__ void ns_gram_tile(const NsLong& n, char* ws, int from, int block, char* s0, char* s1, char* s2, char* s3,
+                                             char* s4, char* s5, char* s6, char* s7)
+{
+    nf16 acc[FP][2];
+    ns_clear(acc);
+    // an XCD takes consecutive places: the tiles of one part together
+    const int place = xcd_place(block, n.tiles * n.gram);
+    const int tile = place % n.tiles, part = place / n.tiles, all = (int)(n.lp / kNsDepth);
+    int ti, tj;
+    ns_upper<FP>(tile, n.high, ti, tj);
+    const char* x = ws + (from ? n.x_next : n.x);
+    const int64_t pitch = 4 * n.lp;
+    ns_product<FP, false>(x + ti * kNsTile * pitch, pitch, x + (int64_t)tj * (128 * FP) * pitch, pitch,
+                          (int)min((int64_t)(128 * FP), n.sp - tj * (128 * FP)), all * part / n.gram, all * (part + 1) / n.gram, s0,
+                          s1, s2, s3, s4, s5, s6, s7, acc);
+    nf4* to = reinterpret_cast<nf4*>(ws + n.parts) + (int64_t)(tile * n.gram + part) * (kNsTile * 32 * FP) +
+              (threadIdx.x >> 6) * (512 * FP) + (threadIdx.x & 63);
+#pragma unroll
+    for (int g = 0; g < FP; g++)
+#pragma unroll
+        for (int f = 0; f < 2; f++)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                to[((g * 2 + f) * 4 + e) * 64] =
+                    nf4{acc[g][f][4 * e], acc[g][f][4 * e + 1], acc[g][f][4 * e + 2], acc[g][f][4 * e + 3]};
+}
+
+template <int FP>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_nsl_gram(const NsItem* __restrict__ table,
                                                                                              char* ws, int from)
 {
     NS_STAGES;
     const NsItem it = table[blockIdx.y];
-    const NsLong n = ns_long(it.rows, it.cols);
-    if (blockIdx.x >= n.tiles * n.splits)
+    const NsLong n = ns_long(it.rows, it.cols, it.slices);
+    if (n.wide != (FP == 2) || (int)blockIdx.x >= n.tiles * n.gram)
         return;
-    int ti, tj;
-    ns_upper((int)blockIdx.x / n.splits, (int)(n.sp / kNsTile), ti, tj);
-    const int sl = (int)blockIdx.x % n.splits, all = (int)(n.lp / kNsDepth);
-    const char* x = ws + it.off + (from ? n.x_next : n.x);
-    const int64_t pitch = 2 * n.lp, low = 2 * n.sp * n.lp;
-    ns_product<false>(x + ti * kNsTile * pitch, pitch, low, x + tj * kNsTile * pitch, pitch, low, (int)((int64_t)all * sl / n.splits),
-                      (int)((int64_t)all * (sl + 1) / n.splits), s0, s1, s2, s3, acc);
-    nf4* part = reinterpret_cast<nf4*>(ws + it.off + n.parts) + (int64_t)blockIdx.x * (kNsTile * kNsTile / 4) +
-                (threadIdx.x >> 6) * 512 + (threadIdx.x & 63);
-#pragma unroll
-    for (int f = 0; f < 2; f++)
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-            part[(f * 4 + e) * 64] = nf4{acc[f][4 * e], acc[f][4 * e + 1], acc[f][4 * e + 2], acc[f][4 * e + 3]};
+    ns_gram_tile<FP>(n, ws + it.off, from, (int)blockIdx.x, s0, s1, s2, s3, s4, s5, s6, s7);
 }
 
-// Four numbers of a symmetric matrix, rows i .. i + 3 of column j, to both their places
-__device__ __forceinline__ void ns_put(uint16_t* m, int64_t pitch, int64_t low, int i, int j, nf4 v)
+// Results leave by way of LDS, a wave's 32 x 32 at a time, in runs of 16 numbers per lane (64
+// bytes: highs and lows). kNsPiece: floats that a wave needs for it.
+constexpr int kNsPitch = 33, kNsPiece = 32 * kNsPitch;
+
+struct NsRun {
+    uint4 q[4];  // 16 highs, 16 lows
+};
+__device__ __forceinline__ NsRun ns_get(const uint16_t* p)
 {
-    NsPair p[4];
+    NsRun r;
 #pragma unroll
-    for (int e = 0; e < 4; e++)
-        p[e] = ns_pair(v[e]);
-    if (i + 3 <= j) {
-        *reinterpret_cast<uint2*>(m + j * pitch + i) = make_uint2(p[0].hi | ((uint32_t)p[1].hi << 16), p[2].hi | ((uint32_t)p[3].hi << 16));
-        *reinterpret_cast<uint2*>(m + low + j * pitch + i) =
-            make_uint2(p[0].lo | ((uint32_t)p[1].lo << 16), p[2].lo | ((uint32_t)p[3].lo << 16));
+    for (int i = 0; i < 4; i++)
+        r.q[i] = reinterpret_cast<const uint4*>(p)[i];
+    return r;
+}
+__device__ __forceinline__ float ns_value(const NsRun& r, int i)
+{
+    const uint4 h = r.q[i >> 3], l = r.q[2 + (i >> 3)];
+    const uint32_t wh = (i & 6) == 0 ? h.x : (i & 6) == 2 ? h.y : (i & 6) == 4 ? h.z : h.w;
+    const uint32_t wl = (i & 6) == 0 ? l.x : (i & 6) == 2 ? l.y : (i & 6) == 4 ? l.z : l.w;
+    return h2f((uint16_t)(wh >> (16 * (i & 1)))) + h2f((uint16_t)(wl >> (16 * (i & 1))));
+}
+__device__ __forceinline__ void ns_put(uint16_t* p, const float (&v)[16])
+{
+    uint32_t w[16];
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-            m[(i + e) * pitch + j] = p[e].hi;
-            m[low + (i + e) * pitch + j] = p[e].lo;
-        }
-    } else if (i <= j) {  // the diagonal runs through the four
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-            if (i + e <= j) {
-                m[(i + e) * pitch + j] = m[j * pitch + i + e] = p[e].hi;
-                m[low + (i + e) * pitch + j] = m[low + j * pitch + i + e] = p[e].lo;
-            }
+    for (int i = 0; i < 8; i++) {
+        const NsPair a = ns_pair(v[2 * i]), b = ns_pair(v[2 * i + 1]);
+        w[i] = a.hi | ((uint32_t)b.hi << 16);
+        w[8 + i] = a.lo | ((uint32_t)b.lo << 16);
     }
-}
-
-// The four numbers of two words of a high and of a low plane
-__device__ __forceinline__ nf4 ns_join(uint2 hi, uint2 lo)
-{
-    const uint32_t ph[2] = {hi.x, hi.y}, pl[2] = {lo.x, lo.y};
-    nf4 v;
 #pragma unroll
-    for (int k = 0; k < 4; k++)
-        v[k] = h2f((uint16_t)(ph[k >> 1] >> (16 * (k & 1)))) + h2f((uint16_t)(pl[k >> 1] >> (16 * (k & 1))));
-    return v;
+    for (int i = 0; i < 4; i++)
+        reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
-// The parts' sums: a wave per 32 x 32 piece's quarter. scale: 2^(m of A - 2 m of X)
+// LDS of one wave: its writes before its reads (they run in order)
+__device__ __forceinline__ void ns_wave_lds()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// A 32 x 32 piece of a symmetric matrix, at (ib, jb) on or above the diagonal, to both its
+// places; v as the products leave it: row 8 (r / 4) + 4 (lane / 32) + r % 4, column lane % 32
+__device__ __forceinline__ void ns_put_both(uint16_t* m, int64_t pitch, int ib, int jb, const nf16& v, float* T, int lane)
+{
+#pragma unroll
+    for (int r = 0; r < 16; r++)
+        T[(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * kNsPitch + (lane & 31)] = v[r];
+    ns_wave_lds();
+    const int row = lane >> 1, c0 = (lane & 1) * 16;
+    float up[16];
+#pragma unroll
+    for (int c = 0; c < 16; c++)  // on the diagonal the upper half serves both
+        up[c] = ib == jb && c0 + c < row ? T[(c0 + c) * kNsPitch + row] : T[row * kNsPitch + c0 + c];
+    ns_put(m + ns_place(ib + row, jb + c0, pitch), up);
+    if (ib != jb) {
+#pragma unroll
+        for (int c = 0; c < 16; c++)
+            up[c] = T[(c0 + c) * kNsPitch + row];
+        ns_put(m + ns_place(jb + row, ib + c0, pitch), up);
+    }
+    ns_wave_lds();
+}
+
+// The parts' sums, a block per 32 x 32 piece: a wave adds every fourth part, the first adds
+// theirs. scale: the power of two of A over that of X squared
+template <int FP>
+__device__ __forceinline__ void ns_sum(const NsLong& n, char* ws, int piece, float scale, float* lds)
+{
+    constexpr int V = kNsTile * 32 * FP;  // vectors of four in a tile
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tile = piece / (16 * FP), at = piece % (16 * FP);
+    int ti, tj;
+    ns_upper<FP>(tile, n.high, ti, tj);
+    const int wave = at / (2 * FP), g = FP == 2 ? (at >> 1) & 1 : 0, f = at & 1;
+    const int wp = FP == 2 ? wave & 1 : wave & 3, wq = FP == 2 ? wave >> 1 : wave >> 2;
+    const int ib = ti * kNsTile + (wp * FP + g) * 32, jb = tj * (128 * FP) + (wq * 2 + f) * 32;
+    if (jb >= n.sp || ib > jb)
+        return;
+    const nf4* p = reinterpret_cast<const nf4*>(ws + n.parts) + (int64_t)tile * n.gram * V + at * 256 + lane;
+    nf16 s;
+#pragma unroll
+    for (int r = 0; r < 16; r++)
+        s[r] = 0.0f;
+    for (int part = w; part < n.gram; part += 8) {
+        nf4 v[2][4];
+#pragma unroll
+        for (int u = 0; u < 2; u++)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                v[u][e] = part + 4 * u < n.gram ? p[(int64_t)(part + 4 * u) * V + e * 64] : nf4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int u = 0; u < 2; u++)
+#pragma unroll
+            for (int r = 0; r < 16; r++)
+                s[r] += v[u][r >> 2][r & 3];
+    }
+    nf4* mine = reinterpret_cast<nf4*>(lds) + (w - 1) * 256 + lane;
+    if (w > 0) {
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            mine[e * 64] = nf4{s[4 * e], s[4 * e + 1], s[4 * e + 2], s[4 * e + 3]};
+    }
+    __syncthreads();
+    if (w > 0)
+        return;
+#pragma unroll
+    for (int u = 1; u < 4; u++)
+#pragma unroll
+        for (int r = 0; r < 16; r++)
+            s[r] += mine[u * 256 + (r >> 2) * 64][r & 3];
+    ns_wave_lds();
+    ns_put_both(reinterpret_cast<uint16_t*>(ws + n.A), n.sp, ib, jb, s * scale, lds, lane);
+}
+
 __global__ __launch_bounds__(256) void k_nsl_sum(const NsItem* __restrict__ table, char* ws, float scale)
 {
+    __shared__ __attribute__((aligned(16))) float lds[3 * 1024 > kNsPiece ? 3 * 1024 : kNsPiece];
     const NsItem it = table[blockIdx.y];
-    const NsLong n = ns_long(it.rows, it.cols);
-    const int tile = (int)blockIdx.x >> 4;
-    if (tile >= n.tiles)
+    const NsLong n = ns_long(it.rows, it.cols, it.slices);
+    if ((int)blockIdx.x >= n.tiles * (n.wide ? 32 : 16))
         return;
-    int ti, tj;
-    ns_upper(tile, (int)(n.sp / kNsTile), ti, tj);
-    const int at = ((int)blockIdx.x & 15) * 256 + threadIdx.x;  // vector of four of the tile
-    const nf4* p = reinterpret_cast<const nf4*>(ws + it.off + n.parts) + (int64_t)tile * n.splits * (kNsTile * kNsTile / 4) + at;
-    nf4 s = p[0];
-    int sl = 1;
-    for (; sl + 4 <= n.splits; sl += 4) {
-        nf4 v[4];
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-            v[e] = p[(int64_t)(sl + e) * (kNsTile * kNsTile / 4)];
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-            s += v[e];
-    }
-    for (; sl < n.splits; sl++)
-        s += p[(int64_t)sl * (kNsTile * kNsTile / 4)];
-    const int wave = at >> 9, f = (at >> 8) & 1, e = (at >> 6) & 3, lane = at & 63;
-    ns_put(reinterpret_cast<uint16_t*>(ws + it.off + n.A), n.sp, n.sp * n.sp, ti * kNsTile + (wave & 3) * 32 + 8 * e + 4 * (lane >> 5),
-           tj * kNsTile + (wave >> 2) * 64 + 32 * f + (lane & 31), s * scale);
+    if (n.wide)
+        ns_sum<2>(n, ws + it.off, (int)blockIdx.x, scale, lds);
+    else
+        ns_sum<1>(n, ws + it.off, (int)blockIdx.x, scale, lds);
 }
 
 // B = b A + c A^2; b and c with the powers of two of A and B
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_nsl_poly(const NsItem* __restrict__ table,
                                                                                              char* ws, float b, float c)
 {
+    constexpr int FP = 1;
     NS_STAGES;
     const NsItem it = table[blockIdx.y];
-    const NsLong n = ns_long(it.rows, it.cols);
-    if (blockIdx.x >= n.tiles)
+    const NsLong n = ns_long(it.rows, it.cols, it.slices);
+    if ((int)blockIdx.x >= n.squares)
         return;
+    nf16 acc[1][2];
+    ns_clear(acc);
     int ti, tj;
-    ns_upper((int)blockIdx.x, (int)(n.sp / kNsTile), ti, tj);
+    ns_upper<1>((int)blockIdx.x, n.high, ti, tj);
     const char* A = ws + it.off + n.A;
-    const int64_t pitch = 2 * n.sp, low = 2 * n.sp * n.sp;
-    ns_product<false>(A + ti * kNsTile * pitch, pitch, low, A + tj * kNsTile * pitch, pitch, low, 0, (int)(n.sp / kNsDepth), s0, s1,
-                      s2, s3, acc);
+    const int64_t pitch = 4 * n.sp;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint16_t* a = reinterpret_cast<const uint16_t*>(A);
-    const int i0 = ti * kNsTile + (wave & 3) * 32 + 4 * (lane >> 5), j0 = tj * kNsTile + (wave >> 2) * 64 + (lane & 31);
-    uint2 hi[8], lo[8];  // all loads before the first store
+    const int ib = ti * kNsTile + (wave & 3) * 32, jb = tj * kNsTile + (wave >> 2) * 64;
+    // (from below the diagonal: four of a column lie side by side there)
+    uint2 hi[8], lo[8];
 #pragma unroll
     for (int q = 0; q < 8; q++) {
-        const uint16_t* at = a + (j0 + 32 * (q >> 2)) * n.sp + i0 + 8 * (q & 3);
-        hi[q] = *reinterpret_cast<const uint2*>(at);
-        lo[q] = *reinterpret_cast<const uint2*>(at + n.sp * n.sp);
+        const uint16_t* from = reinterpret_cast<const uint16_t*>(A) +
+                               ns_place(jb + 32 * (q >> 2) + (lane & 31), ib + 8 * (q & 3) + 4 * (lane >> 5), n.sp);
+        hi[q] = *reinterpret_cast<const uint2*>(from);
+        lo[q] = *reinterpret_cast<const uint2*>(from + 16);
     }
+    ns_product<1, false>(A + ti * kNsTile * pitch, pitch, A + tj * kNsTile * pitch, pitch, kNsTile, 0, (int)(n.sp / kNsDepth), s0, s1,
+                         s2, s3, s4, s5, s6, s7, acc);
+    float* T = reinterpret_cast<float*>(wave < 2 ? s0 : wave < 4 ? s1 : wave < 6 ? s2 : s3) + (wave & 1) * kNsPiece;
 #pragma unroll
-    for (int q = 0; q < 8; q++) {
-        const nf4 x = ns_join(hi[q], lo[q]);
-        nf4 v;
+    for (int f = 0; f < 2; f++) {
+        nf16 v;
 #pragma unroll
-        for (int k = 0; k < 4; k++)
-            v[k] = __builtin_fmaf(c, acc[q >> 2][4 * (q & 3) + k], b * x[k]);
-        ns_put(reinterpret_cast<uint16_t*>(ws + it.off + n.B), n.sp, n.sp * n.sp, i0 + 8 * (q & 3), j0 + 32 * (q >> 2), v);
+        for (int r = 0; r < 16; r++) {
+            const int q = f * 4 + (r >> 2);
+            const uint32_t h = r & 2 ? hi[q].y : hi[q].x, l = r & 2 ? lo[q].y : lo[q].x;
+            const float x = h2f((uint16_t)(h >> (16 * (r & 1)))) + h2f((uint16_t)(l >> (16 * (r & 1))));
+            v[r] = __builtin_fmaf(c, acc[0][f][r], b * x);
+        }
+        if (ib <= jb + 32 * f)
+            ns_put_both(reinterpret_cast<uint16_t*>(ws + it.off + n.B), n.sp, ib, jb + 32 * f, v, T, lane);
     }
 }
 
 // X' = a X + B X; a and the product with the powers of two of X, B and X'
+template <int FP>
+__device__ __forceinline__ void ns_step(const NsLong& n, char* ws, int block, float a, float scale, int from, char* s0, char* s1,
+                                        char* s2, char* s3, char* s4, char* s5, char* s6, char* s7)
+{
+    nf16 acc[FP][2];
+    ns_clear(acc);
+    const int high = n.high, place = xcd_place(block, high * (int)(n.lp / (128 * FP)));
+    const int ti = place % high;
+    const int64_t l0 = (int64_t)(place / high) * (128 * FP);
+    const char* x = ws + (from ? n.x_next : n.x);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wp = FP == 2 ? wave & 1 : wave & 3, wq = FP == 2 ? wave >> 1 : wave >> 2;
+    // this lane's runs of X: 16 of row lane / 2 of every 32 x 32 piece, there before the
+    // products are done
+    const int64_t at0 = ns_place(ti * kNsTile + wp * FP * 32 + (lane >> 1), l0 + wq * 64 + (lane & 1) * 16, n.lp);
+    NsRun old[FP][2];
+#pragma unroll
+    for (int g = 0; g < FP; g++)
+#pragma unroll
+        for (int f = 0; f < 2; f++)
+            old[g][f] = ns_get(reinterpret_cast<const uint16_t*>(x) + at0 + 64 * g * n.lp + 64 * f);
+    ns_product<FP, true>(ws + n.B + ti * kNsTile * (4 * n.sp), 4 * n.sp, x + 4 * l0, 4 * n.lp, 0, 0, (int)(n.sp / kNsDepth), s0, s1,
+                         s2, s3, s4, s5, s6, s7, acc);
+    uint16_t* y = reinterpret_cast<uint16_t*>(ws + (from ? n.x : n.x_next));
+    float* T = reinterpret_cast<float*>(wave < 2 ? s0 : wave < 4 ? s1 : wave < 6 ? s2 : s3) + (wave & 1) * kNsPiece;
+#pragma unroll
+    for (int g = 0; g < FP; g++)
+#pragma unroll
+        for (int f = 0; f < 2; f++) {
+#pragma unroll
+            for (int r = 0; r < 16; r++)
+                T[(lane & 31) * kNsPitch + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)] = acc[g][f][r];
+            ns_wave_lds();
+            float v[16];
+#pragma unroll
+            for (int c = 0; c < 16; c++)
+                v[c] = __builtin_fmaf(a, ns_value(old[g][f], c), T[(lane >> 1) * kNsPitch + (lane & 1) * 16 + c] * scale);
+            ns_put(y + at0 + 64 * g * n.lp + 64 * f, v);
+            ns_wave_lds();
+        }
+}
+
+template <int FP>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_nsl_step(const NsItem* __restrict__ table,
                                                                                              char* ws, float a, float scale, int from)
 {
     NS_STAGES;
     const NsItem it = table[blockIdx.y];
-    const NsLong n = ns_long(it.rows, it.cols);
-    const int T = (int)(n.sp / kNsTile);
-    if (blockIdx.x >= T * (n.lp / kNsTile))
+    const NsLong n = ns_long(it.rows, it.cols, it.slices);
+    if (n.wide != (FP == 2) || (int)blockIdx.x >= n.high * (int)(n.lp / (128 * FP)))
         return;
-    const int place = xcd_place((int)blockIdx.x, (int)(T * (n.lp / kNsTile)));
-    const int ti = place % T;
-    const int64_t l0 = (int64_t)(place / T) * kNsTile;
-    const char* x = ws + it.off + (from ? n.x_next : n.x);
-    const char* B = ws + it.off + n.B;
-    const int64_t low = n.sp * n.lp;
-    ns_product<true>(B + ti * kNsTile * (2 * n.sp), 2 * n.sp, 2 * n.sp * n.sp, x + 2 * l0, 2 * n.lp, 2 * low, 0, (int)(n.sp / kNsDepth),
-                     s0, s1, s2, s3, acc);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint16_t* xo = reinterpret_cast<const uint16_t*>(x);
-    uint16_t* y = reinterpret_cast<uint16_t*>(ws + it.off + (from ? n.x : n.x_next));
-    const int64_t at0 = (ti * kNsTile + (wave & 3) * 32 + (lane & 31)) * n.lp + l0 + (wave >> 2) * 64 + 4 * (lane >> 5);
-    uint2 hi[8], lo[8];  // all loads before the first store
-#pragma unroll
-    for (int q = 0; q < 8; q++) {
-        hi[q] = *reinterpret_cast<const uint2*>(xo + at0 + 8 * q);
-        lo[q] = *reinterpret_cast<const uint2*>(xo + low + at0 + 8 * q);
-    }
-#pragma unroll
-    for (int q = 0; q < 8; q++) {
-        const nf4 v = ns_join(hi[q], lo[q]);
-        NsPair p[4];
-#pragma unroll
-        for (int k = 0; k < 4; k++)
-            p[k] = ns_pair(__builtin_fmaf(a, v[k], acc[q >> 2][4 * (q & 3) + k] * scale));
-        *reinterpret_cast<uint2*>(y + at0 + 8 * q) = make_uint2(p[0].hi | ((uint32_t)p[1].hi << 16), p[2].hi | ((uint32_t)p[3].hi << 16));
-        *reinterpret_cast<uint2*>(y + low + at0 + 8 * q) = make_uint2(p[0].lo | ((uint32_t)p[1].lo << 16), p[2].lo | ((uint32_t)p[3].lo << 16));
-    }
+    ns_step<FP>(n, ws + it.off, (int)blockIdx.x, a, scale, from, s0, s1, s2, s3, s4, s5, s6, s7);
 }
 
 // Powers of two that bring numbers of at most `bound` below 2^14, as exponents
@@ -1075,6 +1253,8 @@ int ns_slices(int64_t l, int T)
     return (int)(n < 128 ? n : 128);
 }
 
+int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
 int64_t ns_bytes(int64_t rows, int64_t cols)
 {
     const int64_t s = rows < cols ? rows : cols, l = rows < cols ? cols : rows;
@@ -1082,12 +1262,10 @@ int64_t ns_bytes(int64_t rows, int64_t cols)
         return 0;
     const int T = ns_tiles(s);
     if (T == 0)
-        return ns_long(rows, cols).total;
+        return up256(ns_long_bytes(ns_long(rows, cols, ns_parts(rows, cols))));
     const int64_t part = (int64_t)ns_slices(l, T) * tri(T) * 2048, f = 4LL * 256 * T * T;
     return ((part > f ? part : f) + 255) / 256 * 256;
 }
-
-int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 // Blocks of k_ns_gram and k_ns_apply of one matrix
 int64_t ns_gram_blocks(int64_t s, int64_t l) { return s > 0 && ns_tiles(s) ? ns_slices(l, ns_tiles(s)) : 0; }
@@ -1137,7 +1315,7 @@ hipError_t launch_orthogonalize(const OrthoEntry* items, int count, double a, do
     grams = applies = 0;
     int longs = 0, shorts = 0;
     unsigned pairs = 0;
-    int64_t lsq = 0, ltile = 0, lgram = 0, lpoly = 0, lstep = 0;
+    int64_t lsq = 0, ltile = 0, lsum = 0, lpoly = 0, lgram[2] = {0, 0}, lstep[2] = {0, 0};  // [narrow, wide]
     auto most = [](auto& v, auto x) { v = v > x ? v : x; };
     NsArgs args{};
     auto flush = [&] {
@@ -1164,12 +1342,14 @@ hipError_t launch_orthogonalize(const OrthoEntry* items, int count, double a, do
                 most(pairs, (unsigned)tri(T));
                 shorts++;
             } else {
-                const NsLong p = ns_long(e.rows, e.cols);
+                it.slices = ns_parts(e.rows, e.cols);
+                const NsLong p = ns_long(e.rows, e.cols, it.slices);
                 most(lsq, (int64_t)p.sqn);
                 most(ltile, (p.sp / 64) * (p.lp / 64));
-                most(lgram, p.tiles * p.splits);
-                most(lpoly, p.tiles);
-                most(lstep, (p.sp / kNsTile) * (p.lp / kNsTile));
+                most(lsum, (int64_t)p.tiles * (p.wide ? 32 : 16));
+                most(lgram[p.wide], (int64_t)p.tiles * p.gram);
+                most(lpoly, (int64_t)p.squares);
+                most(lstep[p.wide], p.high * (p.lp / (p.wide ? 256 : 128)));
                 longs++;
             }
             args.it[args.count++] = it;
@@ -1200,12 +1380,18 @@ hipError_t launch_orthogonalize(const OrthoEntry* items, int count, double a, do
             const int ma = ns_exponent(n.a), mb = ns_exponent(n.b);
             bound = n.next;
             const int next = ns_exponent(bound);
-            hipLaunchKernelGGL(k_nsl_gram, dim3((unsigned)lgram, y), dim3(512), 0, s, table, w, st & 1);
-            hipLaunchKernelGGL(k_nsl_sum, dim3((unsigned)(16 * lpoly), y), dim3(256), 0, s, table, w, two(ma - 2 * mx));
+            if (lgram[0] > 0)
+                hipLaunchKernelGGL(k_nsl_gram<1>, dim3((unsigned)lgram[0], y), dim3(512), 0, s, table, w, st & 1);
+            if (lgram[1] > 0)
+                hipLaunchKernelGGL(k_nsl_gram<2>, dim3((unsigned)lgram[1], y), dim3(512), 0, s, table, w, st & 1);
+            hipLaunchKernelGGL(k_nsl_sum, dim3((unsigned)lsum, y), dim3(256), 0, s, table, w, two(ma - 2 * mx));
             hipLaunchKernelGGL(k_nsl_poly, dim3((unsigned)lpoly, y), dim3(512), 0, s, table, w, (float)(b * two(mb - ma)),
                                (float)(c * two(mb - 2 * ma)));
-            hipLaunchKernelGGL(k_nsl_step, dim3((unsigned)lstep, y), dim3(512), 0, s, table, w, (float)(a * two(next - mx)),
-                               two(next - mb - mx), st & 1);
+            const float fa = (float)(a * two(next - mx)), fs = two(next - mb - mx);
+            if (lstep[0] > 0)
+                hipLaunchKernelGGL(k_nsl_step<1>, dim3((unsigned)lstep[0], y), dim3(512), 0, s, table, w, fa, fs, st & 1);
+            if (lstep[1] > 0)
+                hipLaunchKernelGGL(k_nsl_step<2>, dim3((unsigned)lstep[1], y), dim3(512), 0, s, table, w, fa, fs, st & 1);
             mx = next;
         }
         hipLaunchKernelGGL(k_nsl_out, dim3((unsigned)ltile, y), dim3(256), 0, s, table, w, steps & 1, two(-mx));
