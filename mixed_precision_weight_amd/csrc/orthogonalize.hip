@@ -8,8 +8,9 @@
 // with a short side of up to kNsShort (the weak columns' gradients, low-rank factors) is
 // read twice and written once: its Gram matrix, the polynomial of it, the product. The
 // Gram matrix squares the singular values, and the polynomial lifts the small ones by
-// up to a^steps: both run in fp64 (in fp32 a direction at 1e-3 of the largest would come
-// out 1 % off). Longer short sides run the steps as they stand, X in fp32.
+// up to a^steps: the first is summed in fp64, the second runs on 40-bit fixed point (in fp32
+// a direction at 1e-3 of the largest would come out 1 % off). Longer short sides run the
+// steps as they stand, on pairs of fp16.
 #include <cmath>
 
 #include "owq_device.h"
@@ -22,6 +23,7 @@ namespace {
 
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 typedef float nf4 __attribute__((ext_vector_type(4)));
+typedef int ns_i4 __attribute__((ext_vector_type(4)));
 typedef float nf16 __attribute__((ext_vector_type(16)));
 
 // One matrix as the kernels see it (device table, written by k_ns_table)
@@ -261,55 +263,174 @@ __global__ __launch_bounds__(256) void k_ns_gram_sum(const NsItem* __restrict__ 
 
 constexpr int kNsWaves = 8;
 
-// Element q of lane l of a 16 x 16 fp64 result: row 4 q + l / 16, column l % 16
-__device__ __forceinline__ int ns_drow(int q, int lane) { return 4 * q + (lane >> 4); }
-
+// The polynomial works on numbers of 40 bits in fixed point: x = u I with |I| <= 2^38 and a
+// power of two u per matrix, found from its largest entry, and I in five digits base 256
+// from -128 to 127. A product of two matrices is then 19 products of digit matrices on the
+// 8-bit matrix cores, whose sums are exact: digits i and j of place i + j <= 5. What is left
+// out lies below 2^-40 of the product of the largest entries, and rounding to 40 bits is
+// 2^-39 of the largest entry. Such an error grows by up to a^2 = 12 per step along directions
+// far below the largest: some 1e-7 of the result after five steps. (Without place 5, 15
+// products and 2^-35, a direction at 1e-4 of the largest came out 4 % off; fp32 products,
+// 2^-24, do that at 1e-3; fp64 matrix instructions take 102 us against 60 for a short side
+// of 86. One matrix is one CU's work, so a card full of matrices does not help.)
 template <int T>
 struct NsPoly {
     static constexpr int S = 16 * T;
     static constexpr int TILES = (tri(T) + kNsWaves - 1) / kNsWaves;  // result tiles per wave
-    // place of entry (r, c): rows four entries longer, so that the four rows of an operand
-    // read, and the sixteen of a mirrored write, spread over the banks
-    static constexpr int LD = S + 4;
-    static __device__ __forceinline__ int at(int r, int c) { return r * LD + c; }
+    static constexpr int WAVES = T == 6 ? 8 : T == 4 ? 5 : 3;         // waves with tiles
+    static constexpr int KS = S > 64 ? 2 : 1;                         // 64-deep products
+    // digit matrices in LDS: rows of S bytes, 16 apart, so that 16 rows' pieces of 16 bytes
+    // fall on all 64 banks
+    static constexpr int PITCH = S + 16, PLANE = S * PITCH, MATRIX = 5 * PLANE;
 };
+constexpr int kNsLds = 3 * NsPoly<6>::MATRIX + 64;  // (the last rows' reads reach 16 bytes further)
 
-// X Y for symmetric matrices that commute, the upper tiles of this wave
+// The tiles of a wave: of tile row `ctr`, columns `par`; a symmetric matrix's tile (i, j) is
+// any wave's that has i and j. Nibbles by wave.
 template <int T>
-__device__ __forceinline__ void ns_mul(const double* X, const double* Y, f64x4 (&acc)[NsPoly<T>::TILES],
-                                       const int (&ti)[NsPoly<T>::TILES], const int (&tj)[NsPoly<T>::TILES], int lane)
+__device__ __forceinline__ void ns_tiles_of(int wave, int& ctr, int (&par)[NsPoly<T>::TILES])
 {
-    using P = NsPoly<T>;
-    const int i16 = lane & 15, kk = lane >> 4;
-    int xa[P::TILES], ya[P::TILES];
-#pragma unroll
-    for (int p = 0; p < P::TILES; p++) {
-        acc[p] = f64x4{0.0, 0.0, 0.0, 0.0};
-        xa[p] = P::at(kk, ti[p] * 16 + i16);
-        ya[p] = P::at(kk, tj[p] * 16 + i16);
+    auto nibble = [&](uint32_t v) { return (int)((v >> (4 * wave)) & 15); };
+    if constexpr (T == 6) {
+        ctr = nibble(0x42354100);
+        par[0] = nibble(0x52354130);
+        par[1] = nibble(0x53411241);
+        par[2] = nibble(0x53522352);
+    } else if constexpr (T == 4) {
+        ctr = nibble(0x23100);
+        par[0] = nibble(0x23120);
+        par[1] = nibble(0x31231);
+    } else {
+        ctr = nibble(0x100);
+        par[0] = nibble(0x110);
     }
-#pragma unroll 6
-    for (int k0 = 0; k0 < P::S; k0 += 4)
-#pragma unroll
-        for (int p = 0; p < P::TILES; p++)
-            acc[p] = __builtin_amdgcn_mfma_f64_16x16x4f64(X[xa[p] + k0 * P::LD], Y[ya[p] + k0 * P::LD], acc[p], 0, 0, 0);
 }
 
+// unit X Y for symmetric matrices that commute, this wave's tiles: element q of lane l is row
+// 4 (l / 16) + q of tile row ctr, column l % 16 of tile column par[p]
 template <int T>
-__device__ __forceinline__ void ns_store(double* X, const f64x4 (&v)[NsPoly<T>::TILES], const int (&ti)[NsPoly<T>::TILES],
-                                         const int (&tj)[NsPoly<T>::TILES], int lane)
+__device__ __forceinline__ void ns_mul(const char* X, const char* Y, double unit, f64x4 (&v)[NsPoly<T>::TILES], int ctr,
+                                       const int (&par)[NsPoly<T>::TILES], int lane)
 {
+    using P = NsPoly<T>;
+    const int at = (lane & 15) * P::PITCH + (lane >> 4) * 16;
+    ns_i4 x[P::KS][5];
 #pragma unroll
-    for (int p = 0; p < NsPoly<T>::TILES; p++)
+    for (int ks = 0; ks < P::KS; ks++)
+#pragma unroll
+        for (int i = 0; i < 5; i++) {
+            x[ks][i] = *reinterpret_cast<const ns_i4*>(X + i * P::PLANE + ctr * 16 * P::PITCH + at + ks * 64);
+            // past the matrix's columns: zeros (whatever Y's bytes are there)
+            if (P::S - ks * 64 < 64 && lane >= 32)
+                x[ks][i] = ns_i4{0, 0, 0, 0};
+        }
+#pragma unroll
+    for (int p = 0; p < P::TILES; p++) {
+        ns_i4 d[6] = {};
+#pragma unroll
+        for (int ks = 0; ks < P::KS; ks++) {
+            ns_i4 y[5];
+#pragma unroll
+            for (int j = 0; j < 5; j++)
+                y[j] = *reinterpret_cast<const ns_i4*>(Y + j * P::PLANE + par[p] * 16 * P::PITCH + at + ks * 64);
+#pragma unroll
+            for (int i = 0; i < 5; i++)
+#pragma unroll
+                for (int j = 0; j < 5 && i + j < 6; j++)
+                    d[i + j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[ks][i], y[j], d[i + j], 0, 0, 0);
+        }
+        // |d[n]| <= 5 * 96 * 2^14, so two places fit 32 bits together
 #pragma unroll
         for (int q = 0; q < 4; q++) {
-            // (below the diagonal of a tile on it: the mirror image, whose sum may round otherwise)
-            const int r = ti[p] * 16 + ns_drow(q, lane), c = tj[p] * 16 + (lane & 15);
-            if (r <= c) {
-                X[NsPoly<T>::at(r, c)] = v[p][q];
-                X[NsPoly<T>::at(c, r)] = v[p][q];
+            const double hi = (double)(d[0][q] * 256 + d[1][q]), mid = (double)(d[2][q] * 256 + d[3][q]), lo = (double)(d[4][q] * 256 + d[5][q]);
+            v[p][q] = unit * __builtin_fma(hi, 0x1p56, __builtin_fma(mid, 0x1p40, lo * 0x1p24));
+        }
+    }
+}
+
+// The scale of a matrix: E (biased exponent) with every entry below 2^(E - 1022)
+__device__ __forceinline__ double ns_two(int biased)
+{
+    return __builtin_bit_cast(double, (uint64_t)(uint32_t)biased << 52);
+}
+__device__ __forceinline__ double ns_up(int E) { return ns_two(2083 - E); }    // 2^38 over it
+__device__ __forceinline__ double ns_unit(int E) { return ns_two(E - 37); }    // and back
+
+// Largest of the wave's entries, as the upper half of a double in a float's bits (their order
+// is the same); infinite where one is not finite or leaves the range
+template <int TL>
+__device__ __forceinline__ float ns_top(const f64x4 (&v)[TL])
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int p = 0; p < TL; p++)
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const double x = v[p][q];  // (the cast of a vector's element itself reads element 0)
+            const uint32_t h = (uint32_t)(__builtin_bit_cast(uint64_t, x) >> 32) & 0x7fffffffu;
+            m = h > m ? h : m;
+        }
+    return wave_max_dpp(__builtin_bit_cast(float, m < 0x7f000000u ? m : 0x7f800000u));
+}
+// over the waves; bad: not finite
+template <int T>
+__device__ __forceinline__ int ns_exponent_of(const float* red, bool& bad)
+{
+    float m = red[0];
+#pragma unroll
+    for (int w = 1; w < NsPoly<T>::WAVES; w++)
+        m = fmaxf(m, red[w]);
+    const uint32_t b = __builtin_amdgcn_readfirstlane(__builtin_bit_cast(uint32_t, m));
+    bad = bad || b >= 0x7f000000u;
+    const int E = (int)(b >> 20);
+    return E < 64 ? 64 : E > 0x7f0 ? 0x7f0 : E;
+}
+
+// The digits of this wave's tiles to X, up = 2^38 over their bound. A byte of the low 40 bits
+// of I + 0x8080808080 is a digit + 128; the sum is in the constant that rounds to integers.
+template <int T>
+__device__ __forceinline__ void ns_store(char* X, const f64x4 (&v)[NsPoly<T>::TILES], double up, int ctr,
+                                         const int (&par)[NsPoly<T>::TILES], int lane)
+{
+    using P = NsPoly<T>;
+    const double magic = __builtin_bit_cast(double, (uint64_t)0x4338008080808080ull);
+    const uint32_t one = lane & 1 ? 0x03070105u : 0x06020400u, two = lane & 2 ? 0x03020706u : 0x05040100u;
+#pragma unroll
+    for (int p = 0; p < P::TILES; p++) {
+        uint32_t lo[4], hi[4], d[5];
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const uint64_t t = __builtin_bit_cast(uint64_t, __builtin_fma(v[p][q], up, magic));
+            lo[q] = (uint32_t)t;
+            hi[q] = (uint32_t)(t >> 32);
+        }
+        // d[i]: digit i of the lane's four rows
+        const uint32_t a01 = __builtin_amdgcn_perm(lo[1], lo[0], 0x05010400u), b01 = __builtin_amdgcn_perm(lo[1], lo[0], 0x07030602u);
+        const uint32_t a23 = __builtin_amdgcn_perm(lo[3], lo[2], 0x05010400u), b23 = __builtin_amdgcn_perm(lo[3], lo[2], 0x07030602u);
+        d[4] = __builtin_amdgcn_perm(a23, a01, 0x05040100u);
+        d[3] = __builtin_amdgcn_perm(a23, a01, 0x07060302u);
+        d[2] = __builtin_amdgcn_perm(b23, b01, 0x05040100u);
+        d[1] = __builtin_amdgcn_perm(b23, b01, 0x07060302u);
+        d[0] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(hi[3], hi[2], 0x0c0c0400u), __builtin_amdgcn_perm(hi[1], hi[0], 0x0c0c0400u),
+                                     0x05040100u);
+        char* const down = X + (par[p] * 16 + (lane & 15)) * P::PITCH + ctr * 16 + (lane >> 4) * 4;
+        char* const across = X + (ctr * 16 + (lane >> 4) * 4 + (lane & 3)) * P::PITCH + par[p] * 16 + (lane & 12);
+#pragma unroll
+        for (int i = 0; i < 5; i++) {
+            d[i] ^= 0x80808080u;
+            *reinterpret_cast<uint32_t*>(down + i * P::PLANE) = d[i];
+        }
+        if (par[p] != ctr) {
+            // four lanes' columns turned into rows: bytes exchanged with lane ^ 1, then ^ 2
+#pragma unroll
+            for (int i = 0; i < 5; i++) {
+                const uint32_t e = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)d[i], 0xb1, 0xf, 0xf, false);
+                const uint32_t w = __builtin_amdgcn_perm(e, d[i], one);
+                const uint32_t f = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w, 0x4e, 0xf, 0xf, false);
+                *reinterpret_cast<uint32_t*>(across + i * P::PLANE) = __builtin_amdgcn_perm(f, w, two);
             }
         }
+    }
 }
 
 struct NsCoef {
@@ -317,109 +438,154 @@ struct NsCoef {
     int32_t steps;
 };
 
-// |G|^2 is the Gram matrix's trace; then the steps, on the S x S matrices A, Q in LDS and
-// the waves' result tiles. Waves past the tiles repeat the last tile (the same values to
-// the same places).
+// |G|^2 is the Gram matrix's trace; then the steps, on A, Q = p(A) and the product P of the
+// Qs, whose digits lie in LDS and whose tiles v, N, pv the waves hold as well.
 template <int T>
-__device__ __forceinline__ void ns_poly(const NsItem& it, char* ws, const NsCoef& k, double* A, double* Q)
+__device__ __forceinline__ void ns_poly(const NsItem& it, char* ws, const NsCoef& k, char* lds, double* sums, float (*red)[kNsWaves])
 {
     using PL = NsPoly<T>;
     constexpr int S = PL::S, TL = PL::TILES;
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int ti[TL], tj[TL];
-    f64x4 v[TL], P[TL], N[TL];
+    char *const A = lds, *const Q = lds + PL::MATRIX, *const P = lds + 2 * PL::MATRIX;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bool on = wave < PL::WAVES;
+    int ctr = 0, par[TL] = {};
+    if (on)
+        ns_tiles_of<T>(wave, ctr, par);
+    f64x4 v[TL], N[TL], pv[TL];
+    bool diag[4];
     const double* part = reinterpret_cast<const double*>(ws + it.off);
+    double tr = 0.0;
 #pragma unroll
     for (int p = 0; p < TL; p++) {
-        int n = min(wave * TL + p, tri(T) - 1);
+        const bool turn = ctr > par[p];
+        const int i = turn ? par[p] : ctr, j = turn ? ctr : par[p], n = i * T - i * (i - 1) / 2 + j - i;
 #pragma unroll
-        for (int q = 0; q < 4; q++)
-            v[p][q] = part[n * 256 + q * 64 + lane];
-        int i = 0;
-        while (n >= T - i) {
-            n -= T - i;
-            i++;
+        for (int q = 0; q < 4; q++) {
+            const int r = 4 * (lane >> 4) + q, c = lane & 15;
+            diag[q] = r == c;
+            v[p][q] = part[n * 256 + (turn ? c * 16 + r : r * 16 + c)];
+            if (diag[q] && ctr == par[p] && p == 0)  // (a diagonal tile is its wave's first)
+                tr += v[p][q];
         }
-        ti[p] = i;
-        tj[p] = i + n;
     }
-    ns_store<T>(A, v, ti, tj, lane);
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1)
+        tr += shfl_xor_f64(tr, o);
+    if (lane == 0)
+        sums[wave] = on ? tr : 0.0;
     __syncthreads();
-    double tr = 0.0;
-    for (int i = 0; i < S; i++)
-        tr += A[PL::at(i, i)];
+    tr = 0.0;
+#pragma unroll
+    for (int w = 0; w < kNsWaves; w++)
+        tr += sums[w];
     const double inv = 1.0 / (sqrt(tr) + k.eps);
-    __syncthreads();
+    bool bad = !(tr < 0x1p1000);
 #pragma unroll
     for (int p = 0; p < TL; p++)
         v[p] = v[p] * inv * inv;
-    ns_store<T>(A, v, ti, tj, lane);
+    int eA = 1023, eQ, eR, eP = 0;  // (no entry passes the trace, 1)
+    if (on)
+        ns_store<T>(A, v, ns_up(eA), ctr, par, lane);
     __syncthreads();
     for (int t = 0; t < k.steps; t++) {
-        // v: A's tiles. N = A^2, then Q = a + b A + c A^2
-        ns_mul<T>(A, A, N, ti, tj, lane);
-#pragma unroll
-        for (int p = 0; p < TL; p++)
-#pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const bool diag = ti[p] == tj[p] && ns_drow(q, lane) == (lane & 15);
-                N[p][q] = k.c * N[p][q] + k.b * v[p][q] + (diag ? k.a : 0.0);
-            }
-        ns_store<T>(Q, N, ti, tj, lane);
-        __syncthreads();
         const bool last = t + 1 == k.steps;
-        if (!last) {  // A <- (A Q) Q
-            ns_mul<T>(A, Q, v, ti, tj, lane);
-            __syncthreads();
-            ns_store<T>(A, v, ti, tj, lane);
-            __syncthreads();
-            ns_mul<T>(A, Q, v, ti, tj, lane);
-            __syncthreads();
-        }
-        if (t == 0) {
+        // Q = a + b A + c A^2
+        if (on) {
+            ns_mul<T>(A, A, ns_unit(eA) * ns_unit(eA), N, ctr, par, lane);
 #pragma unroll
             for (int p = 0; p < TL; p++)
-                P[p] = N[p];
-        } else {  // P <- P Q, through A's place
-            ns_store<T>(A, P, ti, tj, lane);
-            __syncthreads();
-            ns_mul<T>(A, Q, P, ti, tj, lane);
-            __syncthreads();
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                    N[p][q] = k.c * N[p][q] + k.b * v[p][q] + (diag[q] && par[p] == ctr ? k.a : 0.0);
+            const float m = ns_top<TL>(N);
+            if (lane == 0)
+                red[0][wave] = m;
         }
-        if (!last) {
-            ns_store<T>(A, v, ti, tj, lane);
-            __syncthreads();
+        __syncthreads();
+        eQ = ns_exponent_of<T>(red[0], bad);
+        if (on) {
+            if (!last || t > 0)
+                ns_store<T>(Q, N, ns_up(eQ), ctr, par, lane);
+            if (t == 0) {
+                ns_store<T>(P, N, ns_up(eQ), ctr, par, lane);
+#pragma unroll
+                for (int p = 0; p < TL; p++)
+                    pv[p] = N[p];
+            }
         }
+        eP = t == 0 ? eQ : eP;
+        __syncthreads();
+        // A Q, and P <- P Q
+        if (on) {
+            if (t > 0) {
+                ns_mul<T>(P, Q, ns_unit(eP) * ns_unit(eQ), pv, ctr, par, lane);
+                const float m = ns_top<TL>(pv);
+                if (lane == 0)
+                    red[1][wave] = m;
+            }
+            if (!last) {
+                ns_mul<T>(A, Q, ns_unit(eA) * ns_unit(eQ), v, ctr, par, lane);
+                const float m = ns_top<TL>(v);
+                if (lane == 0)
+                    red[0][wave] = m;
+            }
+        }
+        if (last)
+            break;
+        __syncthreads();
+        eR = ns_exponent_of<T>(red[0], bad);
+        eP = t > 0 ? ns_exponent_of<T>(red[1], bad) : eP;
+        if (on) {
+            ns_store<T>(A, v, ns_up(eR), ctr, par, lane);
+            if (t > 0)
+                ns_store<T>(P, pv, ns_up(eP), ctr, par, lane);
+        }
+        __syncthreads();
+        // A <- (A Q) Q
+        if (on) {
+            ns_mul<T>(A, Q, ns_unit(eR) * ns_unit(eQ), v, ctr, par, lane);
+            const float m = ns_top<TL>(v);
+            if (lane == 0)
+                red[0][wave] = m;
+        }
+        __syncthreads();
+        eA = ns_exponent_of<T>(red[0], bad);
+        if (on)
+            ns_store<T>(A, v, ns_up(eA), ctr, par, lane);
+        __syncthreads();
     }
+    if (!on)
+        return;
     // the matrix's factor, with the norm and the scale, over the partials
     float* out = reinterpret_cast<float*>(ws + it.off);
-    const double f = inv * (double)it.scale;
+    const double f = bad ? __builtin_nan("") : inv * (double)it.scale;
     const bool tall = it.rows > it.cols;
 #pragma unroll
     for (int p = 0; p < TL; p++)
 #pragma unroll
         for (int q = 0; q < 4; q++) {
-            const int r = ti[p] * 16 + ns_drow(q, lane), c = tj[p] * 16 + (lane & 15);
-            const float x = (float)(P[p][q] * f);
-            if (r <= c) {
+            const int r = ctr * 16 + 4 * (lane >> 4) + q, c = par[p] * 16 + (lane & 15);
+            const float x = (float)(pv[p][q] * f);
+            out[ns_short<T>(c, tall) * S + ns_short<T>(r, tall)] = x;
+            if (par[p] != ctr)
                 out[ns_short<T>(r, tall) * S + ns_short<T>(c, tall)] = x;
-                out[ns_short<T>(c, tall) * S + ns_short<T>(r, tall)] = x;
-            }
         }
 }
 
 // One block per matrix.
 __global__ __launch_bounds__(64 * kNsWaves) void k_ns_poly(const NsItem* __restrict__ table, char* ws, const NsCoef k)
 {
-    __shared__ double lds[2][96 * NsPoly<6>::LD];
+    __shared__ __attribute__((aligned(16))) char lds[kNsLds];
+    __shared__ double sums[kNsWaves];
+    __shared__ float red[2][kNsWaves];
     const NsItem it = table[blockIdx.x];
     if (it.tiles == 2)
-        ns_poly<2>(it, ws, k, lds[0], lds[1]);
+        ns_poly<2>(it, ws, k, lds, sums, red);
     else if (it.tiles == 4)
-        ns_poly<4>(it, ws, k, lds[0], lds[1]);
+        ns_poly<4>(it, ws, k, lds, sums, red);
     else
-        ns_poly<6>(it, ws, k, lds[0], lds[1]);
+        ns_poly<6>(it, ws, k, lds, sums, red);
 }
 
 // --------------------------------------------------------- short form: the product --
