@@ -51,7 +51,8 @@ constexpr int ns_runs(int T) { return T == 2 ? 4 : 2; }
 constexpr int ns_apply_len(int T) { return 4 * 16 * ns_runs(T); }
 
 // A block per matrix: its table entry, and which matrix each block of k_ns_gram and
-// k_ns_apply works on.
+// k_ns_apply works on. The entries come as kernel arguments, so a captured call keeps its own
+// and no copy from the host is recorded; 4.6 us per 64 matrices.
 __global__ __launch_bounds__(256) void k_ns_table(const NsArgs a, NsItem* table, int32_t* gram_item, int32_t* apply_item)
 {
     const NsItem it = a.it[blockIdx.x];
@@ -217,6 +218,10 @@ __device__ __forceinline__ void ns_gram(const NsItem& it, int slice, double* par
 
 // A block sums one slice of one matrix's long side; blocks first ... of the short form's.
 // NARROW: the matrices of two tiles, which need few registers and many waves in flight.
+// Narrow ones are bound by memory and the fp64 matrix cores (busy 61 %): 192 matrices of 32
+// columns, 157 MB in 44 us (3.6 TB/s, and 30 MB of partial sums). Wide ones by the matrix
+// cores and the loads before them: 32 matrices 4096 x 86, 45 us, where the products alone
+// take 20.
 template <bool NARROW>
 __global__ __launch_bounds__(256) void k_ns_gram(const NsItem* __restrict__ table, const int32_t* __restrict__ item, char* ws,
                                                  int first)
@@ -235,7 +240,7 @@ __global__ __launch_bounds__(256) void k_ns_gram(const NsItem* __restrict__ tabl
 }
 
 // The slices' sums, to the first slice's place: a block per tile pair (blockIdx.x) and
-// matrix (blockIdx.y).
+// matrix (blockIdx.y). 224 matrices: 15 us, 75 MB at 5 TB/s; a few: one latency, 4.6 us.
 __global__ __launch_bounds__(256) void k_ns_gram_sum(const NsItem* __restrict__ table, char* ws)
 {
     const NsItem& it = table[blockIdx.y];
@@ -573,7 +578,8 @@ __device__ __forceinline__ void ns_poly(const NsItem& it, char* ws, const NsCoef
         }
 }
 
-// One block per matrix.
+// One block per matrix. Short sides up to 96 / 64: 60 / 29 us for five steps: 14 phases
+// of products (28 of the 60 us at the 8-bit rate of one CU), rounding to digits, two barriers.
 __global__ __launch_bounds__(64 * kNsWaves) void k_ns_poly(const NsItem* __restrict__ table, char* ws, const NsCoef k)
 {
     __shared__ __attribute__((aligned(16))) char lds[kNsLds];
@@ -594,7 +600,8 @@ __global__ __launch_bounds__(64 * kNsWaves) void k_ns_poly(const NsItem* __restr
 // rows as A and G as B; a wave holds a run of 16 of the long side in registers before it
 // writes any of it, so out may be G. The contraction index 16 st + 4 (l / 16) + u is taken
 // by product u of step st, so that a lane's four are consecutive in a tall matrix's row, as
-// are the four results it ends with.
+// are the four results it ends with. Bound by memory: 224 matrices, 406 MB in 95 us (4.3
+// TB/s; a copy reaches 5.15); 7 matrices: 12 us.
 template <int T, bool HALF>
 __device__ __forceinline__ void ns_apply(const NsItem& it, int block, const float* f, float* F)
 {
@@ -697,7 +704,7 @@ __global__ __launch_bounds__(256) void k_ns_apply(const NsItem* __restrict__ tab
 // good as fp32 here (relative error of the result 2.33e-6 against 2.29e-6 with fp32 for a
 // Gaussian 300 x 1200 matrix, 5.1e-6 against 4.8e-6 with singular values down to 1e-4 of
 // the largest). So each product is three on the fp16 matrix cores (high by high, high by
-// low twice; low by low lies below the pairs' precision), with fp32 sums: 5 times the rate
+// low twice; low by low lies below the pairs' precision), with fp32 sums: 3 times the rate
 // of the fp32 matrix instructions. m comes from a bound of the singular values after each
 // step, which the caller of the kernels works out from the coefficients, so nothing
 // overflows.
@@ -785,7 +792,8 @@ __device__ __forceinline__ double ns_block_sum(double v, double* red)
     return ((red[0] + red[1]) + red[2]) + red[3];
 }
 
-// blockIdx.y: the matrix, in all kernels of the long form
+// blockIdx.y: the matrix, in all kernels of the long form. 2048 x 4096 fp32: 8.8 us, 34 MB at
+// 3.8 TB/s.
 __global__ __launch_bounds__(256) void k_nsl_sumsq(const NsItem* __restrict__ table, char* ws)
 {
     __shared__ double red[4];
@@ -834,7 +842,8 @@ __device__ __forceinline__ NsPair ns_pair(float v)
     return p;
 }
 
-// X = G / (|G| + eps), padded with zeros. 64 x 64 tiles.
+// X = G / (|G| + eps), padded with zeros. 64 x 64 tiles. 2048 x 4096 fp32: 14.5 us, 67 MB at 4.6
+// TB/s.
 __global__ __launch_bounds__(256) void k_nsl_init(const NsItem* __restrict__ table, char* ws, double eps, float scale)
 {
     __shared__ double red[4];
@@ -884,7 +893,7 @@ __global__ __launch_bounds__(256) void k_nsl_init(const NsItem* __restrict__ tab
     }
 }
 
-// out = scale X, X times 2^m taken back by `unscale`
+// out = scale X, X times 2^m taken back by `unscale`. 2048 x 4096 fp32: 11.7 us, 5.7 TB/s.
 __global__ __launch_bounds__(256) void k_nsl_out(const NsItem* __restrict__ table, const char* ws, int from, float unscale)
 {
     __shared__ float tile[64][65];
@@ -929,6 +938,11 @@ __global__ __launch_bounds__(256) void k_nsl_out(const NsItem* __restrict__ tabl
 // element r of a lane in acc[g][f]: Q's row (of 32 (2 wq + f)) l % 32, P's row
 // 8 (r / 4) + 4 (l / 32) + r % 4 (of 32 (FP wp + g)), or the other way round (TURN: four
 // consecutive columns).
+//
+// X' of 2048 x 4096, 103 GFLOP in three products: 100 us, 1.03 PFLOP/s (the library's fp16 product
+// of 8192^3: 1.4). Products alone take 75 us of it, loads alone 61; the matrix cores are busy
+// 60 % of the cycles at 1.9 GHz and no LDS access meets a conflict. FP = 1 there: 112.
+// Two blocks per CU (FP = 1, rings of four): 139. Rows padded off powers of two: no change.
 constexpr int kNsStageP = kNsTile * 64;
 typedef short ns_s4 __attribute__((ext_vector_type(4)));
 
@@ -1104,7 +1118,7 @@ __device__ __forceinline__ void ns_upper(int n, int T, int& ti, int& tj)
 }
 
 // A = X X^T, the tiles on and above the diagonal, parts of the long side each, left in lane
-// order
+// order. 2048 x 4096: 59 us, three parts on 216 CUs (one part of 128 x 128 tiles, 136 CUs: 75).
 template <int FP>
 __device__ __forceinline__ void ns_gram_tile(const NsLong& n, char* ws, int from, int block, char* s0, char* s1, char* s2, char* s3,
                                              char* s4, char* s5, char* s6, char* s7)
@@ -1213,7 +1227,7 @@ __device__ __forceinline__ void ns_put_both(uint16_t* m, int64_t pitch, int ib, 
 }
 
 // The parts' sums, a block per 32 x 32 piece: a wave adds every fourth part, the first adds
-// theirs. scale: the power of two of A over that of X squared
+// theirs. scale: the power of two of A over that of X squared. 2048: 13 us, 45 MB.
 template <int FP>
 __device__ __forceinline__ void ns_sum(const NsLong& n, char* ws, int piece, float scale, float* lds)
 {
@@ -1276,7 +1290,8 @@ __global__ __launch_bounds__(256) void k_nsl_sum(const NsItem* __restrict__ tabl
         ns_sum<1>(n, ws + it.off, (int)blockIdx.x, scale, lds);
 }
 
-// B = b A + c A^2; b and c with the powers of two of A and B
+// B = b A + c A^2; b and c with the powers of two of A and B. 2048: 58 us on 136 of the CUs (128 x
+// 256 tiles in three parts and their sum: 45 + 12).
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_nsl_poly(const NsItem* __restrict__ table,
                                                                                              char* ws, float b, float c)
 {
