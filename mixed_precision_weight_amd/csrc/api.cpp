@@ -211,7 +211,7 @@ owq_status check_apart(const Span& out, const owq_layer* L)
 bool int8_sizes_ok(int64_t N, int64_t K, int32_t k, int64_t M)
 {
     return N >= 1 && N <= kMaxBlock && K >= 32 && K <= kMaxK && K % 32 == 0 && k >= 0 && k <= K && M >= 1 &&
-           M <= kMaxBlock && owq::int8_grid_fits(M, N);
+           M <= kMaxBlock && owq::int8_grid_fits(M, N, K);
 }
 
 owq_status check_int8_layer(const owq_integer_layer* L, int64_t M, const uint16_t* x, const uint16_t* y, hipStream_t s)
@@ -234,7 +234,7 @@ owq_status check_int8_layer(const owq_integer_layer* L, int64_t M, const uint16_
     if (!aligned(x, 16) || !aligned(L->codes, 16) || !aligned(L->scales, 4) || !aligned(y, 2) ||
         (L->k > 0 && (!aligned(L->weak_idx, 4) || !aligned(L->w_weak, 2))))
         return fail(OWQ_ERR_ALIGN, "misaligned pointer (x, codes: 16 B, scales, weak_idx: 4 B, fp16 arrays: 2 B)");
-    if (!owq::int8_grid_fits(M, L->N))
+    if (!owq::int8_grid_fits(M, L->N, L->K))
         return launch_status(hipErrorInvalidConfiguration, "8-bit form");
     return check_idx_on_host(L->weak_idx, L->k, L->K, s);
 }
@@ -1276,7 +1276,7 @@ owq_status owq_linear_integer_batched(const owq_integer_layer* Ls, const uint16_
         int64_t rows = 0;
         for (int32_t l = l0; l < count && l < l0 + owq::kInt8MaxLayers; l++)
             rows += (Ls[l].N + 15) / 16 * 16;
-        if (!owq::int8_grid_fits(M, rows))
+        if (!owq::int8_grid_fits(M, rows, Ls[l0].K))
             return launch_status(hipErrorInvalidConfiguration, "owq_linear_integer_batched launch");
     }
     hipError_t e = hipSuccess;

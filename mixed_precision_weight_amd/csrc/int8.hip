@@ -354,7 +354,7 @@ __global__ __launch_bounds__(256) void k_int8_gemv(const DecBatch b)
         }
 }
 
-// ------------------------------ up to 64 tokens: codes straight into the operands --
+// ------------------------------ few tokens: codes straight into the operands --
 
 struct MfvLayer {
     const int8_t* q;
@@ -377,9 +377,7 @@ constexpr int kMfvWaves = 4;  // waves that split K
 // (lane l: row l % 16, 16 columns 16 (l / 16) of a 64-column step) and the tokens as B,
 // which k_int8_tokens has laid out in that order. Both come straight from memory into the
 // operands, U steps ahead of their products. The waves' sums meet in LDS. Bound by the
-// codes' stream: 16 tokens, 11008 x 4096, 45 MB in 11 us (4.1 TB/s). Up to 64 tokens: with
-// both launches 14.1 us at 64 for 4096 x 4096 and 20.8 for 11008 x 4096, the tiled form at 65
-// 24.1 and 30.2; for 28672 x 8192 they meet, 87.6 and 85.0.
+// codes' stream: 16 tokens, 11008 x 4096, 45 MB in 11 us (4.1 TB/s).
 template <int RT, int MT, int U>
 __global__ __launch_bounds__(64 * kMfvWaves) void k_int8_mfv(const MfvBatch b)
 {
@@ -393,7 +391,7 @@ __global__ __launch_bounds__(64 * kMfvWaves) void k_int8_mfv(const MfvBatch b)
     const int N = L.N, K = L.K;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int row0 = ((int)blockIdx.x - L.block0) * 16 * RT;
+    const int row0 = ((int)blockIdx.x - L.block0) * 16 * RT, m0 = (int)blockIdx.y * 16 * MT;
     const int nb = min(N - row0, 16 * RT);
     const int r16 = lane & 15, g = lane >> 4;
     const __amdgpu_buffer_rsrc_t qr = bytes_rsrc(L.q + (int64_t)row0 * K, (int64_t)nb * K);
@@ -420,7 +418,7 @@ __global__ __launch_bounds__(64 * kMfvWaves) void k_int8_mfv(const MfvBatch b)
 #pragma unroll
             for (int m = 0; m < MT; m++)
                 v.x[u][m] = __builtin_bit_cast(
-                    i32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, m * 16 * L.Kq + lane * 16 + (st + u) * 1024 + dead, 0, 0));
+                    i32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, (m0 + m * 16) * L.Kq + lane * 16 + (st + u) * 1024 + dead, 0, 0));
         }
     };
     i32x4 acc[RT][MT];
@@ -454,7 +452,7 @@ __global__ __launch_bounds__(64 * kMfvWaves) void k_int8_mfv(const MfvBatch b)
     __syncthreads();
     const PairLayer P{nullptr, nullptr, nullptr, nullptr, L.ww, L.k};
     for (int t = wave; t < RT * MT; t += W) {
-        const int rb = 16 * (t / MT), m = 16 * (t % MT) + r16;
+        const int rb = 16 * (t / MT), m = m0 + 16 * (t % MT) + r16;
         if (rb >= nb)
             continue;
         i32x4 sum = part[0][t][lane];
@@ -818,6 +816,24 @@ GemmGrid gemm_grid(int64_t M, int64_t N, int64_t chunks)
 
 constexpr int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
+// Rows per block of the streaming product
+int mfv_rows(int64_t M) { return M <= 32 ? 16 : 32; }
+
+// Whether the codes stream past LDS. Above 64 tokens every further 64 read them again (from
+// L2 and the memory's cache), but in one launch after the tokens', where the tiles split K
+// and add the parts in a third: so where they would split, and the blocks together read at most 3
+// 2^20 columns. Streamed against tiled, us: 768 x 768, 128 tokens 9.1 | 11.9, 1024: 12.6 | 12.7;
+// 2731 x 1056, 128: 9.7 | 15.7, 1024: 25.1 | 28.5; 4096 x 4096, 128: 14.3 | 24.7, 256: 21.0 | 26.9,
+// 384 (at the limit): 28.2 | 28.1, 512: 34.8 | 29.9; 4096 x 11008, 128: 27.6 | 36.5, 192: 44.0 |
+// 37.0; without a split, 28672 x 1024, 128: 23.0 | 17.5.
+bool streams(int64_t M, int64_t N, int64_t K)
+{
+    if (M <= 64)
+        return true;
+    const int64_t tiles = (M + kGemmTokens - 1) / kGemmTokens * ((N + 127) / 128);
+    return M <= kInt8StreamMaxM && 2 * tiles <= kCus && (N + 31) / 32 * ((M + 63) / 64) * K <= 3 << 20;
+}
+
 }  // namespace
 
 Int8Plan int8_plan(int64_t N, int64_t K, int32_t k, int64_t M)
@@ -827,7 +843,7 @@ Int8Plan int8_plan(int64_t N, int64_t K, int32_t k, int64_t M)
         return p;
     p.Kq = up(K, kGemmCols);
     p.kp = (int32_t)up(k, 32);
-    if (M <= kInt8StreamMaxM) {
+    if (streams(M, N, K)) {
         p.off_sx = (size_t)(p.Kq * up(M, 16));
         p.off_xw = p.off_sx + (size_t)up(M * 4, 256);
         p.total = p.off_xw + (size_t)up(M * p.kp * 2, 256);
@@ -843,14 +859,11 @@ Int8Plan int8_plan(int64_t N, int64_t K, int32_t k, int64_t M)
     return p;
 }
 
-// Token tiles of 16 and row tiles of 16 per block of the streaming product
-int mfv_rows(int64_t M) { return M <= 32 ? 16 : 32; }
-
-bool int8_grid_fits(int64_t M, int64_t N)
+bool int8_grid_fits(int64_t M, int64_t N, int64_t K)
 {
     if (M <= kInt8GemvMaxM)
         return grid_fits((N + 4 * kDecRows - 1) / (4 * kDecRows), 256);
-    if (M <= kInt8StreamMaxM)
+    if (streams(M, N, K))
         return grid_fits((N + mfv_rows(M) - 1) / mfv_rows(M), 64 * kMfvWaves);
     return grid_fits(M, 256) && grid_fits(gemm_grid(M, N, 1024).blocks(), 512);
 }
@@ -908,7 +921,7 @@ hipError_t launch_linear_int8(const Int8Desc* d, int count, int64_t M, void* con
                              reinterpret_cast<float*>(w + p[l].off_sx), reinterpret_cast<uint16_t*>(w + p[l].off_xw), nullptr,
                              (int32_t)d[l].N, (int32_t)d[l].K, (int32_t)p[l].Kq, d[l].k, p[l].kp};
     }
-    if (M <= kInt8StreamMaxM) {
+    if (streams(M, d[0].N, d[0].K)) {
         MfvBatch b{};
         b.count = count;
         b.M = (int32_t)M;
@@ -929,7 +942,7 @@ hipError_t launch_linear_int8(const Int8Desc* d, int count, int64_t M, void* con
             hipLaunchKernelGGL((k_int8_tokens<true, 3>), tokens, dim3(256), 0, s, qb);
         else
             hipLaunchKernelGGL((k_int8_tokens<false, 3>), tokens, dim3(256), 0, s, qb);
-        const dim3 grid((unsigned)blocks), block(64 * kMfvWaves);
+        const dim3 grid((unsigned)blocks, M <= 64 ? 1u : (unsigned)((M + 63) / 64)), block(64 * kMfvWaves);
         if (M <= 16)
             hipLaunchKernelGGL((k_int8_mfv<1, 1, 8>), grid, block, 0, s, b);
         else if (M <= 32)
@@ -938,7 +951,7 @@ hipError_t launch_linear_int8(const Int8Desc* d, int count, int64_t M, void* con
             hipLaunchKernelGGL((k_int8_mfv<2, 4, 2>), grid, block, 0, s, b);
         return hipGetLastError();
     }
-    if (count != 1 || !int8_grid_fits(M, d[0].N))  // before the first launch
+    if (count != 1 || !int8_grid_fits(M, d[0].N, d[0].K))  // before the first launch
         return hipErrorInvalidConfiguration;
     char* const w = static_cast<char*>(ws[0]);
     QuantLayer& q = qb.L[0];

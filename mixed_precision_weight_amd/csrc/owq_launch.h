@@ -239,7 +239,7 @@ struct Int8Desc {
 constexpr int kInt8MaxLayers = 16;   // layers per launch
 constexpr int kInt8GemvMaxM = 4;     // tokens quantised by every block for itself
 constexpr int kInt8BatchMaxM = 16;    // tokens of the call for several layers
-constexpr int kInt8StreamMaxM = 64;   // tokens whose product streams the codes past LDS
+constexpr int kInt8StreamMaxM = 1024; // tokens whose product may stream the codes past LDS
 // Workspace of one layer at M tokens: their codes (Kq columns), scales, weak columns
 // padded to kp
 struct Int8Plan {
@@ -248,10 +248,10 @@ struct Int8Plan {
     size_t off_sx, off_xw, off_wwp, off_sums, total;
 };
 Int8Plan int8_plan(int64_t N, int64_t K, int32_t k, int64_t M);
-bool int8_grid_fits(int64_t M, int64_t N);  // one layer of N rows at M tokens
+bool int8_grid_fits(int64_t M, int64_t N, int64_t K);  // one layer of N rows at M tokens
 hipError_t launch_pack_int8(const uint16_t* W, int64_t N, int64_t K, const int32_t* idx, int32_t k, int8_t* codes,
                             float* scales, uint16_t* ww, hipStream_t s);
-// count <= kInt8MaxLayers, and 1 above kInt8StreamMaxM tokens; ws[l]: layer l's workspace
+// count <= kInt8MaxLayers, and 1 above kInt8BatchMaxM tokens; ws[l]: layer l's workspace
 hipError_t launch_linear_int8(const Int8Desc* d, int count, int64_t M, void* const* ws, hipStream_t s);
 
 // Its backward: padded sizes, row slices of the weak columns' part of dx, workspace offsets

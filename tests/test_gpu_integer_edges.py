@@ -65,6 +65,29 @@ def test_backward_past_31_bits(M, N, K):
     assert float((dw.double() - want).pow(2).mean().sqrt()) <= 16 * F32 * float(mag.pow(2).mean().sqrt())
 
 
+# the tiled product: whole tiles, halves, one and several parts of K, uneven last parts
+@pytest.mark.parametrize("M,N,K,k", [(1025, 1, 32, 0), (1025, 200, 96, 7), (1290, 513, 1056, 9), (1025, 40, 4128, 33),
+                                     (1300, 1031, 4096, 32), (257, 2048, 11008, 30), (300, 4096, 11008, 86), (513, 4100, 4096, 5),
+                                     (129, 8300, 8224, 63), (65, 16500, 160, 40), (2048, 5000, 416, 12)])
+def test_tiled_product(M, N, K, k):
+    owq = _owq()
+    L, idx = _layer(N, K, k, seed=M)
+    x = tokens(gen(M + N), M, K, idx)
+    x[M // 2] = 0
+    check_product(L, x, owq.linear_integer(L, x))
+
+
+@pytest.mark.parametrize("N,K,M", [(768, 768, 1024), (4096, 4096, 384), (4096, 4096, 385), (4096, 11008, 128), (16384, 64, 100)])
+def test_on_both_sides_of_the_streaming_limit(N, K, M):
+    owq = _owq()
+    L, idx = _layer(N, K, 6, seed=N + K)
+    x = tokens(gen(M), M, K, idx)
+    y = owq.linear_integer(L, x)
+    check_product(L, x, y)
+    # a token's outputs do not depend on the other tokens of the call
+    assert torch.equal(owq.linear_integer(L, x.flip(0).contiguous()).flip(0), y)
+
+
 @pytest.mark.parametrize("r,c", [(1 << 20, 3), (3, 1 << 20), (1 << 20, 100), (100, 1 << 20), (1, 1 << 20)])
 def test_longest_sides(r, c):
     owq = _owq()
