@@ -116,19 +116,31 @@ __global__ __launch_bounds__(256) void k_int8_prepare(const BwdArgs8 a, int toke
 
 // ------------------------------------------------------------------ weak sums --
 
-constexpr int kWeakWaves = 8;
+constexpr int kWeakParts = 8;  // of a sum: a wave each in k_int8_weak_sums, two per wave in k_int8_dx
 
-// The waves' 32 x 32 sums added in LDS in a fixed order; element r of lane l afterwards
-// in sum[r * 64 + l].
-__device__ __forceinline__ void add_waves(float (*red)[16 * 64], const i8_f16v& acc, int wave, int lane)
+typedef float* WeakLds[kWeakParts];
+
+// A part's 32 x 32 sums to LDS
+__device__ __forceinline__ void weak_part(const WeakLds& red, const i8_f16v& acc, int part, int lane)
 {
 #pragma unroll
-    for (int r = 0; r < 16; r++)
-        red[wave][r * 64 + lane] = acc[r];
+    for (int w = 0; w < kWeakParts; w++)
+        if (w == part)
+#pragma unroll
+            for (int r = 0; r < 16; r++)
+                red[w][r * 64 + lane] = acc[r];
+}
+
+// and the parts' in a fixed order, whoever made them; element r of lane l afterwards in
+// red[0][r * 64 + l].
+template <int W>
+__device__ __forceinline__ void add_parts(const WeakLds& red)
+{
     __syncthreads();
-    for (int e = threadIdx.x; e < 16 * 64; e += 64 * kWeakWaves) {
+    for (int e = threadIdx.x; e < 16 * 64; e += 64 * W) {
         float v = red[0][e];
-        for (int w = 1; w < kWeakWaves; w++)
+#pragma unroll
+        for (int w = 1; w < kWeakParts; w++)
             v += red[w][e];
         red[0][e] = v;
     }
@@ -136,34 +148,39 @@ __device__ __forceinline__ void add_waves(float (*red)[16 * 64], const i8_f16v& 
 }
 
 // dy w_weak: 32 tokens x 32 weak columns over a slice of the rows
-__device__ __forceinline__ void weak_dx(const BwdArgs8& a, float (*red)[16 * 64], int block)
+template <int W>
+__device__ __forceinline__ void weak_dx(const BwdArgs8& a, const WeakLds& red, int block, int cb)
 {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l32 = lane & 31, h = lane >> 5;
-    const int c0 = (int)blockIdx.y * 32, sl = block % a.slices, m0 = block / a.slices * 32;
+    const int c0 = cb * 32, sl = block % a.slices, m0 = block / a.slices * 32;
     const int steps = a.Np >> 4, per = (steps + a.slices - 1) / a.slices;
     const int s0 = sl * per, s1 = min(steps, s0 + per);
     const uint16_t* dy = a.dy + (int64_t)min(m0 + l32, a.M - 1) * a.N;
     const uint16_t* w = a.wwt + (int64_t)(c0 + l32) * a.Np;
-    i8_f16v acc;
+#pragma unroll 1
+    for (int part = wave; part < kWeakParts; part += W) {
+        i8_f16v acc;
 #pragma unroll
-    for (int r = 0; r < 16; r++)
-        acc[r] = 0.0f;
-    for (int st = s0 + wave; st < s1; st += kWeakWaves) {
-        const int n = st * 16 + 8 * h;
-        half8_t av;
-        if (n + 8 <= a.N) {
-            av = __builtin_bit_cast(half8_t, *reinterpret_cast<const u16x8_any*>(dy + n));
-        } else {
+        for (int r = 0; r < 16; r++)
+            acc[r] = 0.0f;
+        for (int st = s0 + part; st < s1; st += kWeakParts) {
+            const int n = st * 16 + 8 * h;
+            half8_t av;
+            if (n + 8 <= a.N) {
+                av = __builtin_bit_cast(half8_t, *reinterpret_cast<const u16x8_any*>(dy + n));
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; e++)
-                av[e] = __builtin_bit_cast(_Float16, n + e < a.N ? dy[n + e] : (uint16_t)0);
+                for (int e = 0; e < 8; e++)
+                    av[e] = __builtin_bit_cast(_Float16, n + e < a.N ? dy[n + e] : (uint16_t)0);
+            }
+            const half8_t bv = *reinterpret_cast<const half8_t*>(w + n);
+            acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(av, bv, acc, 0, 0, 0);
         }
-        const half8_t bv = *reinterpret_cast<const half8_t*>(w + n);
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(av, bv, acc, 0, 0, 0);
+        weak_part(red, acc, part, lane);
     }
-    add_waves(red, acc, wave, lane);
-    for (int e = threadIdx.x; e < 1024; e += 64 * kWeakWaves) {
+    add_parts<W>(red);
+    for (int e = threadIdx.x; e < 1024; e += 64 * W) {
         const int r = e >> 6, l = e & 63;
         const int m = m0 + 8 * (r >> 2) + 4 * (l >> 5) + (r & 3), c = c0 + (l & 31);
         if (m < a.M)
@@ -172,29 +189,34 @@ __device__ __forceinline__ void weak_dx(const BwdArgs8& a, float (*red)[16 * 64]
 }
 
 // dy^T x_weak: 32 rows x 32 weak columns over all tokens
-__device__ __forceinline__ void weak_dw(const BwdArgs8& a, float (*red)[16 * 64], int block)
+template <int W>
+__device__ __forceinline__ void weak_dw(const BwdArgs8& a, const WeakLds& red, int block, int cb)
 {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l32 = lane & 31, h = lane >> 5;
-    const int i0 = block * 32, c0 = (int)blockIdx.y * 32;
+    const int i0 = block * 32, c0 = cb * 32;
     const uint16_t* dy = a.dy + min(i0 + l32, a.N - 1);
     const uint16_t* xw = a.xwt + (int64_t)(c0 + l32) * a.Mp;
-    i8_f16v acc;
+#pragma unroll 1
+    for (int part = wave; part < kWeakParts; part += W) {
+        i8_f16v acc;
 #pragma unroll
-    for (int r = 0; r < 16; r++)
-        acc[r] = 0.0f;
-    for (int st = wave; st < a.Mp >> 4; st += kWeakWaves) {
-        const int m = st * 16 + 8 * h;
-        half8_t av;
+        for (int r = 0; r < 16; r++)
+            acc[r] = 0.0f;
+        for (int st = part; st < a.Mp >> 4; st += kWeakParts) {
+            const int m = st * 16 + 8 * h;
+            half8_t av;
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
-            const uint16_t v = dy[(int64_t)min(m + e, a.M - 1) * a.N];
-            av[e] = __builtin_bit_cast(_Float16, m + e < a.M ? v : (uint16_t)0);
+            for (int e = 0; e < 8; e++) {
+                const uint16_t v = dy[(int64_t)min(m + e, a.M - 1) * a.N];
+                av[e] = __builtin_bit_cast(_Float16, m + e < a.M ? v : (uint16_t)0);
+            }
+            acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(av, *reinterpret_cast<const half8_t*>(xw + m), acc, 0, 0, 0);
         }
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(av, *reinterpret_cast<const half8_t*>(xw + m), acc, 0, 0, 0);
+        weak_part(red, acc, part, lane);
     }
-    add_waves(red, acc, wave, lane);
-    for (int e = threadIdx.x; e < 1024; e += 64 * kWeakWaves) {
+    add_parts<W>(red);
+    for (int e = threadIdx.x; e < 1024; e += 64 * W) {
         const int r = e >> 6, l = e & 63;
         const int i = i0 + 8 * (r >> 2) + 4 * (l >> 5) + (r & 3), c = c0 + (l & 31);
         if (i < a.N && c < a.k)
@@ -205,34 +227,59 @@ __device__ __forceinline__ void weak_dw(const BwdArgs8& a, float (*red)[16 * 64]
 // Both sums over dy in one launch: the first `dws` blocks the weights', the others the tokens'.
 // 2048 tokens, 11008 rows, 32 weak columns: 31 us for 45 MB of dy that both read, at 2.9 TB/s;
 // the blocks take two rounds. (Four steps of loads in flight instead of one: no change.)
-__global__ __launch_bounds__(64 * kWeakWaves) void k_int8_weak_sums(const BwdArgs8 a, int dws)
+__global__ __launch_bounds__(64 * kWeakParts) void k_int8_weak_sums(const BwdArgs8 a, int dws)
 {
-    __shared__ float red[kWeakWaves][16 * 64];
+    __shared__ float lds[kWeakParts][16 * 64];
+    const WeakLds red = {lds[0], lds[1], lds[2], lds[3], lds[4], lds[5], lds[6], lds[7]};
     if ((int)blockIdx.x < dws)
-        weak_dw(a, red, xcd_place((int)blockIdx.x, dws));  // neighbours share lines of dy: 34 -> 31 us
+        weak_dw<kWeakParts>(a, red, xcd_place((int)blockIdx.x, dws), (int)blockIdx.y);  // neighbours share lines of dy: 34 -> 31 us
     else
-        weak_dx(a, red, (int)blockIdx.x - dws);
+        weak_dx<kWeakParts>(a, red, (int)blockIdx.x - dws, (int)blockIdx.y);
 }
 
-// dx's weak columns among columns j0 .. j0 + cols - 1, of tokens m0 .. m0 + n - 1, from the
-// slices' sums, by one wave, which has written other values there: over those.
-__device__ __forceinline__ void weak_put(const BwdArgs8& a, int m0, int n, int j0, int cols)
+// The weak columns among columns j0 .. j0 + cols - 1: places first .. last - 1 of idx. at: of
+// up to 64 weak columns, one per lane (one load; a search has a latency per halving).
+struct WeakRange {
+    int first, last, at;
+};
+__device__ __forceinline__ WeakRange weak_range(const BwdArgs8& a, int j0, int cols)
 {
-    if (a.k == 0)
+    WeakRange r{0, 0, 0};
+    const int end = min(j0 + cols, a.K);
+    if (a.k <= 64) {
+        const int lane = threadIdx.x & 63;
+        r.at = lane < a.k ? a.idx[lane] : a.K;
+        r.first = __builtin_popcountll(__builtin_amdgcn_ballot_w64(r.at < j0));
+        r.last = __builtin_popcountll(__builtin_amdgcn_ballot_w64(r.at < end));
+        return r;
+    }
+    auto below = [&](int j) {  // (they ascend)
+        int c = 0;
+        for (int hi = a.k; c < hi;) {
+            const int mid = (c + hi) >> 1;
+            if (__builtin_amdgcn_readfirstlane(a.idx[mid]) < j)
+                c = mid + 1;
+            else
+                hi = mid;
+        }
+        return c;
+    };
+    r.first = below(j0);
+    r.last = r.first;
+    while (r.last < a.k && __builtin_amdgcn_readfirstlane(a.idx[r.last]) < end)
+        r.last++;
+    return r;
+}
+
+// dx's weak columns of a range, of tokens m0 .. m0 + n - 1, from the slices' sums, by one wave,
+// which has written other values there: over those.
+__device__ __forceinline__ void weak_put(const BwdArgs8& a, const WeakRange& r, int m0, int n)
+{
+    if (r.first == r.last)
         return;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    int c = 0;  // the first weak column at or behind j0 (they ascend)
-    for (int hi = a.k; c < hi;) {
-        const int mid = (c + hi) >> 1;
-        if (__builtin_amdgcn_readfirstlane(a.idx[mid]) < j0)
-            c = mid + 1;
-        else
-            hi = mid;
-    }
-    for (; c < a.k; c++) {
-        const int j = __builtin_amdgcn_readfirstlane(a.idx[c]);
-        if (j < j0 || j >= min(j0 + cols, a.K))
-            break;
+    for (int c = r.first; c < r.last; c++) {
+        const int j = __builtin_amdgcn_readfirstlane(a.k <= 64 ? __builtin_amdgcn_readlane(r.at, c) : a.idx[c]);
         for (int t = threadIdx.x & 63; t < n; t += 64) {
             float v = 0.0f;
             for (int sl = 0; sl < a.slices; sl++)
@@ -255,10 +302,11 @@ typedef int i32x2 __attribute__((ext_vector_type(2)));
 // fused multiply-add makes code 2^-9, exactly. (Turning the codes round on the way into LDS
 // instead needs registers and eight-way bank conflicts: 315 us for 2048 tokens, 11008 x
 // 4096.) The columns are the matrix instruction's A, so that a lane ends with four
-// consecutive columns of one token. 2048 tokens, 11008 x 4096: 190 us, 0.97 PFLOP/s (the
+// consecutive columns of one token. Blocks past the `blocks` of the product (where k_int8_dx_sum
+// adds the product's parts and puts the weak columns in) make the weak sums beside it. 2048 tokens, 11008 x 4096: 190 us, 0.97 PFLOP/s (the
 // library's fp16 product reaches 1.4 at 8192^3), matrix cores busy 64 %, vector instructions
 // (widening) 30 % of the waves' cycles. 256 x 128 tiles of eight waves, one block per CU: 197.
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_int8_dx(const BwdArgs8 a)
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_int8_dx(const BwdArgs8 a, int blocks, int dws)
 {
     __shared__ __attribute__((aligned(1024))) char s0[kDxStage];
     __shared__ __attribute__((aligned(1024))) char s1[kDxStage];
@@ -273,7 +321,17 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave & 1, wj = wave >> 1;
     const int l32 = lane & 31, h = lane >> 5;
-    const int place = xcd_place((int)blockIdx.x, (int)gridDim.x), tiles = (int)gridDim.x / a.splits;
+    if ((int)blockIdx.x >= blocks) {
+        auto half = [](char* p, int i) { return reinterpret_cast<float*>(p) + 1024 * i; };
+        const WeakLds red = {half(s0, 0), half(s0, 1), half(s1, 0), half(s1, 1), half(s2, 0), half(s2, 1), half(s3, 0), half(s3, 1)};
+        const int e = (int)blockIdx.x - blocks, cbs = (a.k + 31) >> 5, block = e / cbs;
+        if (block < dws)
+            weak_dw<4>(a, red, block, e % cbs);
+        else
+            weak_dx<4>(a, red, block - dws, e % cbs);
+        return;
+    }
+    const int place = xcd_place((int)blockIdx.x, blocks), tiles = blocks / a.splits;
     const int tile = place % tiles, split = place / tiles;
     const int m0 = (tile % a.mblocks) * kDxTokens, j0 = (tile / a.mblocks) * kDxCols;
     const int mv = min(kDxTokens, M - m0);
@@ -417,6 +475,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
                         i8_f4v{acc[i][f][4 * q], acc[i][f][4 * q + 1], acc[i][f][4 * q + 2], acc[i][f][4 * q + 3]};
         return;
     }
+    const WeakRange range = weak_range(a, j0 + wj * 64, 64);
     // 32 tokens x 64 columns of the wave at a time: token t's piece p of 8 columns in slot
     // p ^ (t % 8) of its 128 bytes
     char* const mine = (wave < 2 ? s0 : s1) + (wave & 1) * 4096;
@@ -443,7 +502,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         }
         asm volatile("" ::: "memory");
     }
-    weak_put(a, m0 + wm * 64, min(64, M - (m0 + wm * 64)), j0 + wj * 64, 64);
+    weak_put(a, range, m0 + wm * 64, min(64, M - (m0 + wm * 64)));
 }
 
 // The splits' sums of 32 tokens x 32 columns, a wave each
@@ -456,6 +515,7 @@ __global__ __launch_bounds__(64) void k_int8_dx_sum(const BwdArgs8 a, int tiles)
     const int j0 = (tile / a.mblocks) * kDxCols + (wave >> 1) * 64 + 32 * f;
     if (m0 >= a.M || j0 >= a.K)
         return;
+    const WeakRange range = weak_range(a, j0, 32);
     const i8_f4v* p = a.sums + ((int64_t)tile * 4 + wave) * (16 * 64) + (i * 2 + f) * (4 * 64) + lane;
     i8_f4v sum[4];
 #pragma unroll
@@ -472,7 +532,7 @@ __global__ __launch_bounds__(64) void k_int8_dx_sum(const BwdArgs8 a, int tiles)
         for (int q = 0; q < 4; q++)
             store4(a.dx + (int64_t)m * a.K, j0 + 8 * q + 4 * h, a.K, sum[q] * f);
     }
-    weak_put(a, m0, min(32, a.M - m0), j0, 32);
+    weak_put(a, range, m0, min(32, a.M - m0));
 }
 
 // Blocks per tile: as many as fill the CUs, each with at least 8 stages
@@ -529,13 +589,16 @@ hipError_t launch_linear_int8_backward(const Int8Desc& d, const uint16_t* dy, in
     const int64_t tokens = dx ? M : 0;
     hipLaunchKernelGGL(k_int8_prepare, dim3((unsigned)(tokens + (turned < 1024 ? turned : 1024))), dim3(256), 0, s, a,
                        (int)tokens);
-    if (d.k > 0) {
-        const int64_t dws = a.dw ? (d.N + 31) / 32 : 0, dxs = dx ? (M + 31) / 32 * p.slices : 0;
-        hipLaunchKernelGGL(k_int8_weak_sums, dim3((unsigned)(dws + dxs), (unsigned)(p.kp / 32)), dim3(64 * kWeakWaves), 0, s, a,
+    const int64_t dws = a.dw ? (d.N + 31) / 32 : 0, dxs = dx && d.k > 0 ? (M + 31) / 32 * p.slices : 0;
+    // the weak sums: beside the product where its parts are added in a launch of their own
+    // (they go into dx there), else before it
+    const bool beside = dx && p.splits > 1;
+    if (!beside && dws + dxs > 0)
+        hipLaunchKernelGGL(k_int8_weak_sums, dim3((unsigned)(dws + dxs), (unsigned)(p.kp / 32)), dim3(64 * kWeakParts), 0, s, a,
                            (int)dws);
-    }
     if (dx) {
-        hipLaunchKernelGGL(k_int8_dx, dim3((unsigned)(p.tiles * p.splits)), dim3(256), 0, s, a);
+        const int64_t blocks = p.tiles * p.splits, more = beside ? (dws + dxs) * (p.kp / 32) : 0;
+        hipLaunchKernelGGL(k_int8_dx, dim3((unsigned)(blocks + more)), dim3(256), 0, s, a, (int)blocks, (int)dws);
         if (p.splits > 1)
             hipLaunchKernelGGL(k_int8_dx_sum, dim3((unsigned)(16 * p.tiles)), dim3(64), 0, s, a, (int)p.tiles);
     }
