@@ -645,8 +645,7 @@ size_t owq_linear_integer_workspace_bytes(int64_t N, int64_t K, int32_t k, int64
  *   y[m][i] = s_m scales[i] sum_j q_mj codes[i][j] + sum_c x[m][weak_idx[c]] w_weak[i][c]
  * with exact integer sums, the rest in fp32, y rounded to fp16 once. A token with an
  * infinity or NaN in a dense column has infinite or NaN outputs and leaves the others
- * as they are. x: fp16 [M][K]; y: fp16 [M][N]. One launch up to 4 tokens, two up to 64,
- * two or three above.
+ * as they are. x: fp16 [M][K]; y: fp16 [M][N]. One launch up to 4 tokens, two or three above.
  * workspace: >= owq_linear_integer_workspace_bytes(...) bytes, 256-byte aligned (may be NULL
  * where that is 0), contents ignored; calls sharing it must be ordered. y and workspace
  * must not overlap each other, x or the layer (OWQ_ERR_RANGE). M < 2^24; OWQ_ERR_SHAPE

@@ -591,14 +591,14 @@ hipError_t launch_linear_int8_backward(const Int8Desc& d, const uint16_t* dy, in
                        (int)tokens);
     const int64_t dws = a.dw ? (d.N + 31) / 32 : 0, dxs = dx && d.k > 0 ? (M + 31) / 32 * p.slices : 0;
     // the weak sums: beside the product where its parts are added in a launch of their own
-    // (they go into dx there), else before it
-    const bool beside = dx && p.splits > 1;
-    if (!beside && dws + dxs > 0)
+    // (they go into dx there) and one grid holds both, else before it
+    const int64_t blocks = p.tiles * p.splits, sums = (dws + dxs) * (p.kp / 32);
+    const bool beside = dx && p.splits > 1 && grid_fits(blocks + sums, 256);
+    if (!beside && sums > 0)
         hipLaunchKernelGGL(k_int8_weak_sums, dim3((unsigned)(dws + dxs), (unsigned)(p.kp / 32)), dim3(64 * kWeakParts), 0, s, a,
                            (int)dws);
     if (dx) {
-        const int64_t blocks = p.tiles * p.splits, more = beside ? (dws + dxs) * (p.kp / 32) : 0;
-        hipLaunchKernelGGL(k_int8_dx, dim3((unsigned)(blocks + more)), dim3(256), 0, s, a, (int)blocks, (int)dws);
+        hipLaunchKernelGGL(k_int8_dx, dim3((unsigned)(blocks + (beside ? sums : 0))), dim3(256), 0, s, a, (int)blocks, (int)dws);
         if (p.splits > 1)
             hipLaunchKernelGGL(k_int8_dx_sum, dim3((unsigned)(16 * p.tiles)), dim3(64), 0, s, a, (int)p.tiles);
     }
