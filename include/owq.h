@@ -667,7 +667,7 @@ owq_status owq_linear_integer_batched(const owq_integer_layer* Ls, const uint16_
                                    int32_t count, int64_t M, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of device workspace owq_linear_integer_backward needs (0 for sizes outside its
- * range): mostly 2 M N for the scaled gradients. */
+ * range): mostly 4 M N for the scaled gradients. */
 size_t owq_linear_integer_backward_workspace_bytes(int64_t N, int64_t K, int32_t k, int64_t M);
 
 /* Backward of owq_linear_integer for Weak Column Tuning, as owq_linear_backward ([PL] "Weak
@@ -678,9 +678,9 @@ size_t owq_linear_integer_backward_workspace_bytes(int64_t N, int64_t K, int32_t
  *   dw_weak[i][c] = sum_m dy[m][i] x[m][idx_c]     fp32 [N][k]
  * x: fp16 [M][K], read only for dw_weak (may be NULL without it); dy: fp16 [M][N]; dx,
  * dw_weak: outputs, each may be NULL. In the dense part of dx, dy times the scale is
- * rounded to fp16 after scaling each token by a power of two (11 bits of every term that
- * is not below 2^-28 of the token's largest; no term overflows); every other product is
- * exact and every sum fp32. Bitwise deterministic. No output and not the workspace may
+ * kept in 22 bits (a pair of fp16 values) after scaling each token by a power of two (every
+ * term that is not below 2^-18 of the token's largest, the others to 2^-40 of it; no term
+ * overflows); every other product is exact, every sum fp32, dx rounded to fp16 once. Bitwise deterministic. No output and not the workspace may
  * overlap one another, an input or the layer (OWQ_ERR_RANGE). M, N <= 2^20. workspace: >=
  * owq_linear_integer_backward_workspace_bytes(...) bytes, 256-byte aligned, contents ignored;
  * calls sharing it must be ordered. Errors as owq_linear_integer. */

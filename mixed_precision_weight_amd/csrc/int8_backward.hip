@@ -4,10 +4,13 @@
 //   dw_weak[i][c] = sum_m dy[m][i] x[m][idx_c]
 // (the rounding of the tokens to 8 bits passes gradients as the identity does).
 //
-// The dense part of dx runs on the fp16 matrix cores: dy_i scale_i is rounded to fp16
-// after scaling each token by a power of two (11 bits of every term that is not below
-// 2^-28 of the token's largest, and none overflows), the codes are exact in fp16. The
-// weak parts multiply dy and x as they are.
+// The dense part of dx runs on the fp16 matrix cores: dy_i scale_i is kept as a pair of fp16
+// values, itself rounded and what that left, after scaling each token by a power of two (22
+// bits, and none overflows; what lies below 2^-18 of the token's largest is held to 2^-40 of
+// it), the codes are exact in fp16: two products for one, so that dx is the fp32 sum rounded
+// once: 2.1e-4 against 64 bits, the fp16 result's own rounding. (One product with eleven bits of
+// dy_i scale_i takes 190 us instead of 340 for 2048 tokens, 11008 x 4096, and gives 2.9e-4.)
+// The weak parts multiply dy and x as they are.
 #include "owq_int8.h"
 
 namespace owq {
@@ -19,8 +22,9 @@ typedef float f4_any8 __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr int kDxTokens = 128, kDxCols = 128;  // of a tile
 constexpr int kDxRows = 32;                    // of the layer per stage
-constexpr int kDxStage = kDxTokens * 64 + kDxRows * kDxCols;
-constexpr int kDxLoads = 2 + 1;  // per wave and stage, of g and of the codes
+constexpr int kDxPlane = kDxTokens * 64;       // high halves of a stage's g; the low ones follow
+constexpr int kDxStage = 2 * kDxPlane + kDxRows * kDxCols;
+constexpr int kDxLoads = 4 + 1;  // per wave and stage, of g and of the codes
 
 struct BwdArgs8 {
     const int8_t* q;
@@ -31,7 +35,7 @@ struct BwdArgs8 {
     const uint16_t* dy;
     uint16_t* dx;
     float* dw;
-    uint16_t* g;     // [M][Np] in panels of kDxTokens
+    uint16_t* g;     // [M][Np] pairs in panels of kDxTokens: a stage's high halves, its low halves
     float* unscale;  // [M]
     uint16_t* wwt;   // [kp][Np]
     uint16_t* xwt;   // [kp][Mp]
@@ -42,10 +46,19 @@ struct BwdArgs8 {
 
 // ------------------------------------------------------- the scaled gradients --
 
+// Two values as a pair each: the words of the high and of the low halves
+__device__ __forceinline__ void dx_pairs(float a, float b, uint32_t& hi, uint32_t& lo)
+{
+    const uint16_t ha = f2h(a), hb = f2h(b);
+    hi = ha | ((uint32_t)hb << 16);
+    lo = f2h(a - h2f(ha)) | ((uint32_t)f2h(b - h2f(hb)) << 16);
+}
+
 // The first blocks: one per token, g = dy scale 2^e, the largest magnitude in [2^14, 2^15),
 // zeros from N to Np. The others: the weak weights and the tokens' weak columns with the
 // long side contiguous, padded with zeros: wwt[c][i], xwt[c][m]. Bound by memory: 2048 tokens
-// of 11008, 90 MB in 24 us (3.7 TB/s).
+// of 11008, 45 MB read twice, the second time from L2 or the memory's cache, and 90 MB written in 33
+// us (4.1 TB/s).
 __global__ __launch_bounds__(256) void k_int8_prepare(const BwdArgs8 a, int tokens)
 {
     __shared__ float red[4];
@@ -94,23 +107,26 @@ __global__ __launch_bounds__(256) void k_int8_prepare(const BwdArgs8 a, int toke
         a.unscale[m] = 512.0f / f;
     char* const g = reinterpret_cast<char*>(a.g);
     for (int p = tid * 8; p < a.Np; p += 2048) {  // Np is a multiple of 32
-        uint32_t o[4];
+        uint32_t o[4], r[4];
         if (p + 8 <= N) {
             const u16x8_any v = *reinterpret_cast<const u16x8_any*>(dy + p);
             const f4_any8 s0 = *reinterpret_cast<const f4_any8*>(a.s + p), s1 = *reinterpret_cast<const f4_any8*>(a.s + p + 4);
 #pragma unroll
             for (int e = 0; e < 4; e++)
-                o[e] = f2h(h2f(v[2 * e]) * (e < 2 ? s0[2 * e] : s1[2 * e - 4]) * f) |
-                       ((uint32_t)f2h(h2f(v[2 * e + 1]) * (e < 2 ? s0[2 * e + 1] : s1[2 * e - 3]) * f) << 16);
+                dx_pairs(h2f(v[2 * e]) * (e < 2 ? s0[2 * e] : s1[2 * e - 4]) * f,
+                         h2f(v[2 * e + 1]) * (e < 2 ? s0[2 * e + 1] : s1[2 * e - 3]) * f, o[e], r[e]);
         } else {
 #pragma unroll
             for (int e = 0; e < 4; e++) {
                 const int n = p + 2 * e;
-                o[e] = (n < N ? f2h(h2f(dy[n]) * a.s[n] * f) : 0u) |
-                       ((uint32_t)(n + 1 < N ? f2h(h2f(dy[n + 1]) * a.s[n + 1] * f) : 0u) << 16);
+                dx_pairs(n < N ? h2f(dy[n]) * a.s[n] * f : 0.0f, n + 1 < N ? h2f(dy[n + 1]) * a.s[n + 1] * f : 0.0f, o[e], r[e]);
             }
         }
-        *reinterpret_cast<uint4*>(g + panel_at(m, kDxTokens, (int64_t)2 * a.Np, p >> 3)) = make_uint4(o[0], o[1], o[2], o[3]);
+        // (a panel's stages of 32 rows, two planes each)
+        char* const at = g + m / kDxTokens * kDxTokens * 4 * a.Np + (int64_t)(p / kDxRows) * (2 * kDxPlane) + m % kDxTokens * 64 +
+                         p % kDxRows * 2;
+        *reinterpret_cast<uint4*>(at) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(at + kDxPlane) = make_uint4(r[0], r[1], r[2], r[3]);
     }
 }
 
@@ -295,26 +311,23 @@ typedef int i32x2 __attribute__((ext_vector_type(2)));
 
 // 128 tokens x 128 columns per block of 4 waves (64 x 64 each), two blocks per CU, which
 // run at their own pace; the contraction runs over the layer's rows, 32 at a time, in a
-// ring of six stages, two per barrier, that is filled two to four ahead by direct-to-LDS
-// loads: g (panels of 128 tokens, 64 bytes of each together) as in the forward product,
+// ring of four stages that is filled three ahead by direct-to-LDS loads: g (panels of 128
+// tokens, 64 bytes of each together, high and low halves apart) as in the forward product,
 // the codes as they lie. ds_read_tr turns 8 rows of the codes round on the way to the
 // registers, where they become fp16: a byte pair is read as two fp16 subnormals, which one
 // fused multiply-add makes code 2^-9, exactly. (Turning the codes round on the way into LDS
 // instead needs registers and eight-way bank conflicts: 315 us for 2048 tokens, 11008 x
 // 4096.) The columns are the matrix instruction's A, so that a lane ends with four
 // consecutive columns of one token. Blocks past the `blocks` of the product (where k_int8_dx_sum
-// adds the product's parts and puts the weak columns in) make the weak sums beside it. 2048 tokens, 11008 x 4096: 190 us, 0.97 PFLOP/s (the
-// library's fp16 product reaches 1.4 at 8192^3), matrix cores busy 64 %, vector instructions
-// (widening) 30 % of the waves' cycles. 256 x 128 tiles of eight waves, one block per CU: 197.
+// adds the product's parts and puts the weak columns in) make the weak sums beside it. 2048 tokens, 11008 x 4096: 340 us,
+// 1.09 PFLOP/s of both halves' products (the library's fp16 product reaches 1.4 at 8192^3; the card's
+// power holds the clock). Strips of 2, 4 or 8 token panels per XCD, which share more of g: no change.
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_int8_dx(const BwdArgs8 a, int blocks, int dws)
 {
     __shared__ __attribute__((aligned(1024))) char s0[kDxStage];
     __shared__ __attribute__((aligned(1024))) char s1[kDxStage];
     __shared__ __attribute__((aligned(1024))) char s2[kDxStage];
-    __shared__ __attribute__((aligned(1024))) char s3[kDxStage];
-    __shared__ __attribute__((aligned(1024))) char s4[kDxStage];
-    __shared__ __attribute__((aligned(1024))) char s5[kDxStage];
-    __shared__ float un[kDxTokens];
+    __shared__ __attribute__((aligned(1024))) char s3[kDxStage];  // (four stages of two blocks are a CU's whole LDS)
     constexpr int FM = 2, FJ = 2;
     const int M = a.M, N = a.N, K = a.K;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -334,8 +347,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const int place = xcd_place((int)blockIdx.x, blocks), tiles = blocks / a.splits;
     const int tile = place % tiles, split = place / tiles;
     const int m0 = (tile % a.mblocks) * kDxTokens, j0 = (tile / a.mblocks) * kDxCols;
-    const int mv = min(kDxTokens, M - m0);
-    const __amdgpu_buffer_rsrc_t gr = uniform_rsrc(a.g + (int64_t)m0 * a.Np, (int64_t)2 * kDxTokens * a.Np);
+    const __amdgpu_buffer_rsrc_t gr = uniform_rsrc(a.g + (int64_t)2 * m0 * a.Np, (int64_t)4 * kDxTokens * a.Np);
     int gsrc[2];
 #pragma unroll
     for (int t = 0; t < 2; t++) {
@@ -352,9 +364,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         const int i0 = min(c, c1 - 1) * kDxRows;  // (Np is N rounded up: the last stage has a row)
         const __amdgpu_buffer_rsrc_t qr = uniform_rsrc(a.q + (int64_t)i0 * K + j0, (int64_t)min(kDxRows, N - i0) * K - j0);
 #pragma unroll
-        for (int t = 0; t < 2; t++)
-            dma16_lds(gr, stage + (wave * 2 + t) * 1024, gsrc[t] + (i0 * (2 * kDxTokens) | dead));
-        dma16_lds(qr, stage + kDxTokens * 64 + wave * 1024, qsrc | dead);
+        for (int t = 0; t < 4; t++)
+            dma16_lds(gr, stage + (t >> 1) * kDxPlane + (wave * 2 + (t & 1)) * 1024,
+                      gsrc[t & 1] + (t >> 1) * kDxPlane + (i0 * (4 * kDxTokens) | dead));
+        dma16_lds(qr, stage + 2 * kDxPlane + wave * 1024, qsrc | dead);
     };
     i8_f16v acc[FM][FJ];
 #pragma unroll
@@ -373,12 +386,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
         for (int f = 0; f < FJ; f++) {
             const int r = 16 * st + 8 * h + ((lane & 15) >> 1), piece = (wj * FJ + f) * 2 + ((lane >> 4) & 1);
-            qa[st][f] = kDxTokens * 64 + r * kDxCols + ((piece ^ (r & 7)) * 16) + (lane & 1) * 8;
+            qa[st][f] = 2 * kDxPlane + r * kDxCols + ((piece ^ (r & 7)) * 16) + (lane & 1) * 8;
         }
     // codes as read (two 16-row steps of a stage) and as fp16, g: the codes are read two
     // steps ahead of their products and widened one ahead, g is read one ahead
     i32x2 raw[2][FJ];
-    half8_t cv[2][FJ], gv[2][FM];
+    half8_t cv[2][FJ], gv[2][2][FM];  // [step][high, low]
     auto read_codes = [&](const char* stage, int st) {
 #pragma unroll
         for (int f = 0; f < FJ; f++)
@@ -386,8 +399,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     };
     auto read_g = [&](const char* stage, int st) {
 #pragma unroll
-        for (int i = 0; i < FM; i++)
-            gv[st][i] = *reinterpret_cast<const half8_t*>(stage + (st ? p1 : p0) + i * 2048);
+        for (int e = 0; e < 2; e++)
+#pragma unroll
+            for (int i = 0; i < FM; i++)
+                gv[st][e][i] = *reinterpret_cast<const half8_t*>(stage + e * kDxPlane + (st ? p1 : p0) + i * 2048);
     };
     const half2_t mul = {(_Float16)32768.0f, (_Float16)32768.0f}, add = {(_Float16)-0.25f, (_Float16)-0.25f};
     auto widen = [&](int st) {
@@ -405,16 +420,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     };
     auto product = [&](int st) {
 #pragma unroll
-        for (int i = 0; i < FM; i++)
+        for (int e = 0; e < 2; e++)
 #pragma unroll
-            for (int f = 0; f < FJ; f++)
-                acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(cv[st][f], gv[st][i], acc[i][f], 0, 0, 0);
+            for (int i = 0; i < FM; i++)
+#pragma unroll
+                for (int f = 0; f < FJ; f++)
+                    acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(cv[st][f], gv[st][e][i], acc[i][f], 0, 0, 0);
         // the reads and the widening between the products
 #pragma unroll
-        for (int i = 0; i < FM * FJ; i++) {
+        for (int i = 0; i < 2 * FM * FJ; i++) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
         }
     };
     // products of the stage in cur, and the reads ahead from next
@@ -428,36 +445,31 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         widen(0);
         product(1);
     };
-    // two stages per barrier: c in sa, c + 1 in sb, c + 2 in next, all whole; c + 4 and c + 5
-    // go where the two before were
-    auto step = [&](int c, const char* sa, const char* sb, const char* next, char* fa, char* fb) {
+    // c in cur and c + 1 in next, whole; c + 3 goes where c - 1 was
+    auto step = [&](int c, const char* cur, const char* next, char* fill) {
         stage_barrier<kDxLoads, 15>();
-        dma(c + 4, fa);
-        dma(c + 5, fb);
+        dma(c + 3, fill);
         if (c < c1) {
-            stage(sa, sb);
-            stage(sb, next);
-            // their reads are done before this wave lets them be overwritten
+            stage(cur, next);
+            // its reads are done before this wave lets it be overwritten
 #pragma unroll
             for (int i = 0; i < FM; i++)
-                asm volatile("" ::"v"(gv[1][i]));
+                asm volatile("" ::"v"(gv[1][0][i]), "v"(gv[1][1][i]));
         }
     };
     dma(c0, s0);
     dma(c0 + 1, s1);
     dma(c0 + 2, s2);
-    dma(c0 + 3, s3);
-    if (tid < kDxTokens)
-        un[tid] = a.unscale[m0 + min(tid, mv - 1)];
     stage_barrier<0>();
     read_codes(s0, 0);
     read_codes(s0, 1);
     read_g(s0, 0);
     widen(0);
-    for (int c = c0; c < c1; c += 6) {  // (a stage past c1 holds zeros)
-        step(c, s0, s1, s2, s4, s5);
-        step(c + 2, s2, s3, s4, s0, s1);
-        step(c + 4, s4, s5, s0, s2, s3);
+    for (int c = c0; c < c1; c += 4) {  // (a stage past c1 holds zeros)
+        step(c, s0, s1, s3);
+        step(c + 1, s1, s2, s0);
+        step(c + 2, s2, s3, s1);
+        step(c + 3, s3, s0, s2);
     }
 #pragma unroll
     for (int f = 0; f < FJ; f++)
@@ -481,7 +493,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     char* const mine = (wave < 2 ? s0 : s1) + (wave & 1) * 4096;
 #pragma unroll
     for (int i = 0; i < FM; i++) {
-        const float sc = un[wm * 32 * FM + 32 * i + l32];
+        const float sc = a.unscale[min(m0 + wm * 32 * FM + 32 * i + l32, M - 1)];
 #pragma unroll
         for (int f = 0; f < FJ; f++)
 #pragma unroll
@@ -562,7 +574,7 @@ Int8BwdPlan int8_bwd_plan(int64_t N, int64_t K, int32_t k, int64_t M)
     int64_t sl = (512 + tiles - 1) / tiles;
     sl = sl < p.Np / 512 ? sl : p.Np / 512;
     p.slices = sl < 1 ? 1 : sl;
-    size_t off = (size_t)(2 * up(M, kDxTokens) * p.Np);  // whole panels
+    size_t off = (size_t)(4 * up(M, kDxTokens) * p.Np);  // whole panels
     auto take = [&](size_t& at, int64_t bytes) {
         at = off;
         off += (size_t)up(bytes, 256);
