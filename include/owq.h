@@ -712,7 +712,7 @@ size_t owq_orthogonalize_workspace_bytes(const owq_update* items, int32_t count)
  * coefficients, HOST array [3]; (1.875, -1.25, 0.375) converges to the factor itself,
  * (3.4445, -4.7750, 2.0315) lifts small values faster and ends between 0.7 and 1.2. |g|_F
  * is fp64; up to a shorter side of 96, X X^T is summed in fp64 and its polynomial runs on
- * 40-bit numbers; above, matrices are kept in 22 bits (pairs of fp16); all else is fp32, out
+ * 40-bit numbers, or on fp64 where the steps lift a direction more than 2^11 times; above, matrices are kept in 22 bits (pairs of fp16); all else is fp32, out
  * rounded once. A matrix of zeros gives zeros; one with an infinity or NaN gives NaN
  * throughout, and the others are as without it. 1 <= steps <= 16; coefficients finite;
  * eps > 0. Every out must be disjoint from every other out and, unless it is the matrix's

@@ -9,8 +9,9 @@
 // read twice and written once: its Gram matrix, the polynomial of it, the product. The
 // Gram matrix squares the singular values, and the polynomial lifts the small ones by
 // up to a^steps: the first is summed in fp64, the second runs on 40-bit fixed point (in fp32
-// a direction at 1e-3 of the largest would come out 1 % off). Longer short sides run the
-// steps as they stand, on pairs of fp16.
+// a direction at 1e-3 of the largest would come out 1 % off), or on fp64 where the steps lift
+// so far that 40 bits are not enough (ns_fixed). Longer short sides run the steps as they
+// stand, on pairs of fp16.
 #include <cmath>
 
 #include "owq_device.h"
@@ -274,7 +275,8 @@ constexpr int kNsWaves = 8;
 // 8-bit matrix cores, whose sums are exact: digits i and j of place i + j <= 5. What is left
 // out lies below 2^-40 of the product of the largest entries, and rounding to 40 bits is
 // 2^-39 of the largest entry. Such an error grows by up to a^2 = 12 per step along directions
-// far below the largest: some 1e-7 of the result after five steps. (Without place 5, 15
+// far below the largest: some 1e-7 of the result after five steps; ns_fixed says how far that
+// goes. (Without place 5, 15
 // products and 2^-35, a direction at 1e-4 of the largest came out 4 % off; fp32 products,
 // 2^-24, do that at 1e-3; fp64 matrix instructions take 102 us against 60 for a short side
 // of 86. One matrix is one CU's work, so a card full of matrices does not help.)
@@ -458,7 +460,8 @@ __device__ __forceinline__ void ns_poly(const NsItem& it, char* ws, const NsCoef
     if (on)
         ns_tiles_of<T>(wave, ctr, par);
     f64x4 v[TL], N[TL], pv[TL];
-    bool diag[4];
+    bool diag[4], one[4];  // one: on the diagonal of the matrix's own part, so that padding sets no unit
+    const bool tall = it.rows > it.cols;
     const double* part = reinterpret_cast<const double*>(ws + it.off);
     double tr = 0.0;
 #pragma unroll
@@ -469,6 +472,7 @@ __device__ __forceinline__ void ns_poly(const NsItem& it, char* ws, const NsCoef
         for (int q = 0; q < 4; q++) {
             const int r = 4 * (lane >> 4) + q, c = lane & 15;
             diag[q] = r == c;
+            one[q] = r == c && ns_short<T>(ctr * 16 + r, tall) < min(it.rows, it.cols);
             v[p][q] = part[n * 256 + (turn ? c * 16 + r : r * 16 + c)];
             if (diag[q] && ctr == par[p] && p == 0)  // (a diagonal tile is its wave's first)
                 tr += v[p][q];
@@ -502,7 +506,7 @@ __device__ __forceinline__ void ns_poly(const NsItem& it, char* ws, const NsCoef
             for (int p = 0; p < TL; p++)
 #pragma unroll
                 for (int q = 0; q < 4; q++)
-                    N[p][q] = k.c * N[p][q] + k.b * v[p][q] + (diag[q] && par[p] == ctr ? k.a : 0.0);
+                    N[p][q] = k.c * N[p][q] + k.b * v[p][q] + (one[q] && par[p] == ctr ? k.a : 0.0);
             const float m = ns_top<TL>(N);
             if (lane == 0)
                 red[0][wave] = m;
@@ -565,7 +569,6 @@ __device__ __forceinline__ void ns_poly(const NsItem& it, char* ws, const NsCoef
     // the matrix's factor, with the norm and the scale, over the partials
     float* out = reinterpret_cast<float*>(ws + it.off);
     const double f = bad ? __builtin_nan("") : inv * (double)it.scale;
-    const bool tall = it.rows > it.cols;
 #pragma unroll
     for (int p = 0; p < TL; p++)
 #pragma unroll
@@ -592,6 +595,174 @@ __global__ __launch_bounds__(64 * kNsWaves) void k_ns_poly(const NsItem* __restr
         ns_poly<4>(it, ws, k, lds, sums, red);
     else
         ns_poly<6>(it, ws, k, lds, sums, red);
+}
+
+// The same in fp64, for steps that lift the smallest directions further than 40 bits reach.
+// A direction that G lacks has an eigenvalue 0 in S, where rounding leaves one of either sign;
+// a negative one never turns back (p(S) = a + |b| |S| + c S^2 only grows), so S starts with
+// 2^-47 of its trace added to its diagonal: some eight times what the sums over 2^20 leave, and
+// along a direction that G has, no more than fp32 products lose (a singular value of 1e-6 of the
+// largest after 16 steps: 4.2e-3, where fp32 products give 2.8e-3). v_mfma_f64_16x16x4_f64, the
+// matrices in LDS with rows four entries longer, so that the four rows of an operand read, and
+// the sixteen of a mirrored write, spread over the banks. 22 us per step for a
+// short side of 86, where 40 bits take 12.
+constexpr double kNsShift = 0x1p-47;
+
+template <int T>
+struct NsPoly64 {
+    static constexpr int S = 16 * T, LD = S + 4;
+    static constexpr int TILES = (tri(T) + kNsWaves - 1) / kNsWaves;  // result tiles per wave
+    // Element q of lane l of a 16 x 16 result: row 4 q + l / 16, column l % 16
+    static __device__ __forceinline__ int row(int q, int lane) { return 4 * q + (lane >> 4); }
+};
+
+// X Y for symmetric matrices that commute, the upper tiles of this wave
+template <int T>
+__device__ __forceinline__ void ns_mul64(const double* X, const double* Y, f64x4 (&acc)[NsPoly64<T>::TILES],
+                                         const int (&ti)[NsPoly64<T>::TILES], const int (&tj)[NsPoly64<T>::TILES], int lane)
+{
+    using P = NsPoly64<T>;
+    const int i16 = lane & 15, kk = lane >> 4;
+    int xa[P::TILES], ya[P::TILES];
+#pragma unroll
+    for (int p = 0; p < P::TILES; p++) {
+        acc[p] = f64x4{0.0, 0.0, 0.0, 0.0};
+        xa[p] = kk * P::LD + ti[p] * 16 + i16;
+        ya[p] = kk * P::LD + tj[p] * 16 + i16;
+    }
+#pragma unroll 4
+    for (int k0 = 0; k0 < P::S; k0 += 4)
+#pragma unroll
+        for (int p = 0; p < P::TILES; p++)
+            acc[p] = __builtin_amdgcn_mfma_f64_16x16x4f64(X[xa[p] + k0 * P::LD], Y[ya[p] + k0 * P::LD], acc[p], 0, 0, 0);
+}
+
+template <int T>
+__device__ __forceinline__ void ns_store64(double* X, const f64x4 (&v)[NsPoly64<T>::TILES], const int (&ti)[NsPoly64<T>::TILES],
+                                           const int (&tj)[NsPoly64<T>::TILES], int lane)
+{
+    using P = NsPoly64<T>;
+#pragma unroll
+    for (int p = 0; p < P::TILES; p++)
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            // (below the diagonal of a tile on it: the mirror image, whose sum may round otherwise)
+            const int r = ti[p] * 16 + P::row(q, lane), c = tj[p] * 16 + (lane & 15);
+            if (r <= c) {
+                X[r * P::LD + c] = v[p][q];
+                X[c * P::LD + r] = v[p][q];
+            }
+        }
+}
+
+// The steps on A, Q in LDS and the waves' result tiles, the product P of the Qs through A's
+// place. Waves past the tiles repeat the last tile (the same values to the same places).
+template <int T>
+__device__ __forceinline__ void ns_poly64(const NsItem& it, char* ws, const NsCoef& k, double* A, double* Q)
+{
+    using PL = NsPoly64<T>;
+    constexpr int S = PL::S, TL = PL::TILES;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bool tall = it.rows > it.cols;
+    const int s = min(it.rows, it.cols);
+    int ti[TL], tj[TL];
+    bool diag[TL][4];  // on the diagonal of the matrix's own part
+    f64x4 v[TL], P[TL], N[TL];
+    const double* part = reinterpret_cast<const double*>(ws + it.off);
+#pragma unroll
+    for (int p = 0; p < TL; p++) {
+        int n = min(wave * TL + p, tri(T) - 1);
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+            v[p][q] = part[n * 256 + q * 64 + lane];
+        int i = 0;
+        while (n >= T - i) {
+            n -= T - i;
+            i++;
+        }
+        ti[p] = i;
+        tj[p] = i + n;
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+            diag[p][q] = n == 0 && PL::row(q, lane) == (lane & 15) && ns_short<T>(i * 16 + (lane & 15), tall) < s;
+    }
+    ns_store64<T>(A, v, ti, tj, lane);
+    __syncthreads();
+    double tr = 0.0;
+    for (int i = 0; i < S; i++)
+        tr += A[i * PL::LD + i];
+    const double inv = 1.0 / (sqrt(tr) + k.eps);
+    const bool bad = !(tr < 0x1p1000);
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < TL; p++)
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+            v[p][q] = v[p][q] * inv * inv + (diag[p][q] ? kNsShift : 0.0);
+    ns_store64<T>(A, v, ti, tj, lane);
+    __syncthreads();
+    for (int t = 0; t < k.steps; t++) {
+        const bool last = t + 1 == k.steps;
+        // v: A's tiles. N = A^2, then Q = a + b A + c A^2
+        ns_mul64<T>(A, A, N, ti, tj, lane);
+#pragma unroll
+        for (int p = 0; p < TL; p++)
+#pragma unroll
+            for (int q = 0; q < 4; q++)
+                N[p][q] = k.c * N[p][q] + k.b * v[p][q] + (diag[p][q] ? k.a : 0.0);
+        ns_store64<T>(Q, N, ti, tj, lane);
+        __syncthreads();
+        if (!last) {  // A <- (A Q) Q
+            ns_mul64<T>(A, Q, v, ti, tj, lane);
+            __syncthreads();
+            ns_store64<T>(A, v, ti, tj, lane);
+            __syncthreads();
+            ns_mul64<T>(A, Q, v, ti, tj, lane);
+            __syncthreads();
+        }
+        if (t == 0) {
+#pragma unroll
+            for (int p = 0; p < TL; p++)
+                P[p] = N[p];
+        } else {  // P <- P Q, through A's place
+            ns_store64<T>(A, P, ti, tj, lane);
+            __syncthreads();
+            ns_mul64<T>(A, Q, P, ti, tj, lane);
+            __syncthreads();
+        }
+        if (!last) {
+            ns_store64<T>(A, v, ti, tj, lane);
+            __syncthreads();
+        }
+    }
+    // the matrix's factor, with the norm and the scale, over the partials
+    float* out = reinterpret_cast<float*>(ws + it.off);
+    const double f = bad ? __builtin_nan("") : inv * (double)it.scale;
+#pragma unroll
+    for (int p = 0; p < TL; p++)
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const int r = ti[p] * 16 + PL::row(q, lane), c = tj[p] * 16 + (lane & 15);
+            const float x = (float)(P[p][q] * f);
+            if (r <= c) {
+                out[ns_short<T>(r, tall) * S + ns_short<T>(c, tall)] = x;
+                out[ns_short<T>(c, tall) * S + ns_short<T>(r, tall)] = x;
+            }
+        }
+}
+
+// One block per matrix
+__global__ __launch_bounds__(64 * kNsWaves) void k_ns_poly64(const NsItem* __restrict__ table, char* ws, const NsCoef k)
+{
+    __shared__ double lds[2][NsPoly64<6>::S * NsPoly64<6>::LD];
+    const NsItem it = table[blockIdx.x];
+    if (it.tiles == 2)
+        ns_poly64<2>(it, ws, k, lds[0], lds[1]);
+    else if (it.tiles == 4)
+        ns_poly64<4>(it, ws, k, lds[0], lds[1]);
+    else
+        ns_poly64<6>(it, ws, k, lds[0], lds[1]);
 }
 
 // --------------------------------------------------------- short form: the product --
@@ -1421,6 +1592,39 @@ NsBound ns_bound(double x, double a, double b, double c)
     return n;
 }
 
+// Whether 40 bits do for the short form's polynomial. What it leaves along a direction grows
+// with every step by the square of the factor p(S) that the step lifts it by, and is as small
+// as what fp32 products of X leave (2^-24, growing by p(S) itself) until those factors' largest
+// have multiplied to some 2^11. Relative error of a 700 x 86 matrix of rank 8 | that of fp32
+// products | with fp64 here, by that product: (3.4445, -4.775, 2.0315), 6 steps (1670) 6.9e-5 | 7.7e-5,
+// 7 (5753) 6.2e-4 | 2.1e-4 | 1.9e-4, 8 2e-2 | 8.4e-4 | 7.8e-4; (1.875, -1.25, 0.375), 12 steps (1888)
+// 7.2e-5 | 4.8e-5, 13 (3540) 2.4e-4 | 1e-4 | 1.2e-4, 14 1.3e-3 | 1.8e-4 | 2.2e-4; (3, -3.2, 1.2), 6
+// steps (729) 2.4e-5 | 2.7e-5, 8 (6561) 9.8e-4 | 2.2e-4 | 2.1e-4. Up to 16 steps fp64 stays near fp32
+// products; five steps of 4096 x 86 take 92 us with 40 bits, eight 128, and eight with fp64 204.
+// The largest of |p| and of the singular values that a step leaves lie at the ends of its
+// range or where the derivatives vanish.
+bool ns_fixed(double a, double b, double c, int steps)
+{
+    double x2 = 1.0, growth = 1.0;  // the largest eigenvalue of S
+    for (int t = 0; t < steps; t++) {
+        auto p = [&](double l) { return std::fabs(a + b * l + c * l * l); };
+        double most = std::fmax(p(0.0), p(x2)), next = x2 * p(x2) * p(x2);
+        const double top = -b / (2.0 * c);
+        if (top > 0.0 && top < x2)
+            most = std::fmax(most, p(top));
+        // d/dx x p(x^2) = a + 3 b l + 5 c l^2
+        const double disc = 9.0 * b * b - 20.0 * a * c;
+        for (const double sign : {-1.0, 1.0}) {
+            const double l = c != 0.0 ? (-3.0 * b + sign * std::sqrt(disc)) / (10.0 * c) : -a / (3.0 * b);
+            if (l > 0.0 && l < x2)
+                next = std::fmax(next, l * p(l) * p(l));
+        }
+        growth *= most;
+        x2 = next;
+    }
+    return growth <= 2048.0;  // (a NaN is not)
+}
+
 // ------------------------------------------------------------------ the plan --
 
 constexpr int kNsShort = 96;  // short sides of the short form
@@ -1546,7 +1750,11 @@ hipError_t launch_orthogonalize(const OrthoEntry* items, int count, double a, do
         if (grams > wide)
             hipLaunchKernelGGL(k_ns_gram<true>, dim3((unsigned)(grams - wide)), dim3(256), 0, s, table, gram_item, w, (int)wide);
         hipLaunchKernelGGL(k_ns_gram_sum, dim3(pairs, (unsigned)shorts), dim3(256), 0, s, t, w);
-        hipLaunchKernelGGL(k_ns_poly, dim3((unsigned)shorts), dim3(64 * kNsWaves), 0, s, t, w, NsCoef{a, b, c, eps, steps});
+        const NsCoef coef{a, b, c, eps, steps};
+        if (ns_fixed(a, b, c, steps))
+            hipLaunchKernelGGL(k_ns_poly, dim3((unsigned)shorts), dim3(64 * kNsWaves), 0, s, t, w, coef);
+        else
+            hipLaunchKernelGGL(k_ns_poly64, dim3((unsigned)shorts), dim3(64 * kNsWaves), 0, s, t, w, coef);
         hipLaunchKernelGGL(k_ns_apply, dim3((unsigned)applies), dim3(256), 0, s, table, apply_item, w);
     }
     if (longs > 0) {
