@@ -380,12 +380,12 @@ __device__ __forceinline__ float ns_top(const f64x4 (&v)[TL])
     return wave_max_dpp(__builtin_bit_cast(float, m < 0x7f000000u ? m : 0x7f800000u));
 }
 // over the waves; bad: not finite
-template <int T>
+template <int WAVES>
 __device__ __forceinline__ int ns_exponent_of(const float* red, bool& bad)
 {
     float m = red[0];
 #pragma unroll
-    for (int w = 1; w < NsPoly<T>::WAVES; w++)
+    for (int w = 1; w < WAVES; w++)
         m = fmaxf(m, red[w]);
     const uint32_t b = __builtin_amdgcn_readfirstlane(__builtin_bit_cast(uint32_t, m));
     bad = bad || b >= 0x7f000000u;
@@ -445,6 +445,36 @@ struct NsCoef {
     int32_t steps;
 };
 
+// |G| + eps = m 2^e, m in [1/2, 1): 1 / m, and e. So numbers stay in range whatever |G| and eps
+// are: G enters the product times 2^-e, the Gram matrix here times 2^-2e, and a matrix of
+// zeros stays one.
+struct NsNorm {
+    double inv;
+    int e;
+};
+__device__ __forceinline__ NsNorm ns_norm(double trace, double eps)
+{
+    const double n = sqrt(trace) + eps;
+    return NsNorm{1.0 / __builtin_amdgcn_frexp_mant(n), __builtin_amdgcn_frexp_exp(n)};
+}
+
+// out = 2^(p + es) (P 2^-p / m ms) (G 2^-e), with scale = ms 2^es and every entry of P below 2^p:
+// what an entry of P becomes, and, behind the factor, the exponents for G and for out.
+struct NsFactor {
+    double f;
+    int p;
+};
+template <int S>
+__device__ __forceinline__ NsFactor ns_factor(const NsItem& it, const NsNorm& n, int p, bool bad, float* out)
+{
+    if (threadIdx.x == 0) {
+        reinterpret_cast<int*>(out)[S * S] = -n.e;
+        reinterpret_cast<int*>(out)[S * S + 1] = p + __builtin_amdgcn_frexp_expf(it.scale);
+    }
+    return NsFactor{bad ? __builtin_nan("") : n.inv * (double)__builtin_amdgcn_frexp_mantf(it.scale), p};
+}
+__device__ __forceinline__ float ns_entry(const NsFactor& f, double v) { return (float)__builtin_amdgcn_ldexp(v * f.f, -f.p); }
+
 // |G|^2 is the Gram matrix's trace; then the steps, on A, Q = p(A) and the product P of the
 // Qs, whose digits lie in LDS and whose tiles v, N, pv the waves hold as well.
 template <int T>
@@ -488,11 +518,13 @@ __device__ __forceinline__ void ns_poly(const NsItem& it, char* ws, const NsCoef
 #pragma unroll
     for (int w = 0; w < kNsWaves; w++)
         tr += sums[w];
-    const double inv = 1.0 / (sqrt(tr) + k.eps);
+    const NsNorm norm = ns_norm(tr, k.eps);
     bool bad = !(tr < 0x1p1000);
 #pragma unroll
     for (int p = 0; p < TL; p++)
-        v[p] = v[p] * inv * inv;
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+            v[p][q] = __builtin_amdgcn_ldexp(v[p][q] * norm.inv * norm.inv, -2 * norm.e);
     int eA = 1023, eQ, eR, eP = 0;  // (no entry passes the trace, 1)
     if (on)
         ns_store<T>(A, v, ns_up(eA), ctr, par, lane);
@@ -512,7 +544,7 @@ __device__ __forceinline__ void ns_poly(const NsItem& it, char* ws, const NsCoef
                 red[0][wave] = m;
         }
         __syncthreads();
-        eQ = ns_exponent_of<T>(red[0], bad);
+        eQ = ns_exponent_of<PL::WAVES>(red[0], bad);
         if (on) {
             if (!last || t > 0)
                 ns_store<T>(Q, N, ns_up(eQ), ctr, par, lane);
@@ -543,8 +575,8 @@ __device__ __forceinline__ void ns_poly(const NsItem& it, char* ws, const NsCoef
         if (last)
             break;
         __syncthreads();
-        eR = ns_exponent_of<T>(red[0], bad);
-        eP = t > 0 ? ns_exponent_of<T>(red[1], bad) : eP;
+        eR = ns_exponent_of<PL::WAVES>(red[0], bad);
+        eP = t > 0 ? ns_exponent_of<PL::WAVES>(red[1], bad) : eP;
         if (on) {
             ns_store<T>(A, v, ns_up(eR), ctr, par, lane);
             if (t > 0)
@@ -559,22 +591,24 @@ __device__ __forceinline__ void ns_poly(const NsItem& it, char* ws, const NsCoef
                 red[0][wave] = m;
         }
         __syncthreads();
-        eA = ns_exponent_of<T>(red[0], bad);
+        eA = ns_exponent_of<PL::WAVES>(red[0], bad);
         if (on)
             ns_store<T>(A, v, ns_up(eA), ctr, par, lane);
         __syncthreads();
     }
+    __syncthreads();
     if (!on)
         return;
+    eP = k.steps > 1 ? ns_exponent_of<PL::WAVES>(red[1], bad) : eP;
     // the matrix's factor, with the norm and the scale, over the partials
     float* out = reinterpret_cast<float*>(ws + it.off);
-    const double f = bad ? __builtin_nan("") : inv * (double)it.scale;
+    const NsFactor f = ns_factor<S>(it, norm, eP - 1022, bad, out);
 #pragma unroll
     for (int p = 0; p < TL; p++)
 #pragma unroll
         for (int q = 0; q < 4; q++) {
             const int r = ctr * 16 + 4 * (lane >> 4) + q, c = par[p] * 16 + (lane & 15);
-            const float x = (float)(pv[p][q] * f);
+            const float x = ns_entry(f, pv[p][q]);
             out[ns_short<T>(c, tall) * S + ns_short<T>(r, tall)] = x;
             if (par[p] != ctr)
                 out[ns_short<T>(r, tall) * S + ns_short<T>(c, tall)] = x;
@@ -658,7 +692,7 @@ __device__ __forceinline__ void ns_store64(double* X, const f64x4 (&v)[NsPoly64<
 // The steps on A, Q in LDS and the waves' result tiles, the product P of the Qs through A's
 // place. Waves past the tiles repeat the last tile (the same values to the same places).
 template <int T>
-__device__ __forceinline__ void ns_poly64(const NsItem& it, char* ws, const NsCoef& k, double* A, double* Q)
+__device__ __forceinline__ void ns_poly64(const NsItem& it, char* ws, const NsCoef& k, double* A, double* Q, float* red)
 {
     using PL = NsPoly64<T>;
     constexpr int S = PL::S, TL = PL::TILES;
@@ -692,14 +726,14 @@ __device__ __forceinline__ void ns_poly64(const NsItem& it, char* ws, const NsCo
     double tr = 0.0;
     for (int i = 0; i < S; i++)
         tr += A[i * PL::LD + i];
-    const double inv = 1.0 / (sqrt(tr) + k.eps);
-    const bool bad = !(tr < 0x1p1000);
+    const NsNorm norm = ns_norm(tr, k.eps);
+    bool bad = !(tr < 0x1p1000);
     __syncthreads();
 #pragma unroll
     for (int p = 0; p < TL; p++)
 #pragma unroll
         for (int q = 0; q < 4; q++)
-            v[p][q] = v[p][q] * inv * inv + (diag[p][q] ? kNsShift : 0.0);
+            v[p][q] = __builtin_amdgcn_ldexp(v[p][q] * norm.inv * norm.inv, -2 * norm.e) + (diag[p][q] ? kNsShift : 0.0);
     ns_store64<T>(A, v, ti, tj, lane);
     __syncthreads();
     for (int t = 0; t < k.steps; t++) {
@@ -737,14 +771,19 @@ __device__ __forceinline__ void ns_poly64(const NsItem& it, char* ws, const NsCo
         }
     }
     // the matrix's factor, with the norm and the scale, over the partials
+    const float m = ns_top<TL>(P);
+    if (lane == 0)
+        red[wave] = m;
+    __syncthreads();
+    const int eP = ns_exponent_of<kNsWaves>(red, bad);
     float* out = reinterpret_cast<float*>(ws + it.off);
-    const double f = bad ? __builtin_nan("") : inv * (double)it.scale;
+    const NsFactor f = ns_factor<S>(it, norm, eP - 1022, bad, out);
 #pragma unroll
     for (int p = 0; p < TL; p++)
 #pragma unroll
         for (int q = 0; q < 4; q++) {
             const int r = ti[p] * 16 + PL::row(q, lane), c = tj[p] * 16 + (lane & 15);
-            const float x = (float)(P[p][q] * f);
+            const float x = ns_entry(f, P[p][q]);
             if (r <= c) {
                 out[ns_short<T>(r, tall) * S + ns_short<T>(c, tall)] = x;
                 out[ns_short<T>(c, tall) * S + ns_short<T>(r, tall)] = x;
@@ -756,13 +795,14 @@ __device__ __forceinline__ void ns_poly64(const NsItem& it, char* ws, const NsCo
 __global__ __launch_bounds__(64 * kNsWaves) void k_ns_poly64(const NsItem* __restrict__ table, char* ws, const NsCoef k)
 {
     __shared__ double lds[2][NsPoly64<6>::S * NsPoly64<6>::LD];
+    __shared__ float red[kNsWaves];
     const NsItem it = table[blockIdx.x];
     if (it.tiles == 2)
-        ns_poly64<2>(it, ws, k, lds[0], lds[1]);
+        ns_poly64<2>(it, ws, k, lds[0], lds[1], red);
     else if (it.tiles == 4)
-        ns_poly64<4>(it, ws, k, lds[0], lds[1]);
+        ns_poly64<4>(it, ws, k, lds[0], lds[1], red);
     else
-        ns_poly64<6>(it, ws, k, lds[0], lds[1]);
+        ns_poly64<6>(it, ws, k, lds[0], lds[1], red);
 }
 
 // --------------------------------------------------------- short form: the product --
@@ -782,6 +822,7 @@ __device__ __forceinline__ void ns_apply(const NsItem& it, int block, const floa
     for (int e = tid; e < S * S / 4; e += 256)
         *reinterpret_cast<nf4*>(&F[e / (S / 4) * LD + e % (S / 4) * 4]) = reinterpret_cast<const nf4*>(f)[e];
     __syncthreads();
+    const int eg = reinterpret_cast<const int*>(f)[S * S], eo = reinterpret_cast<const int*>(f)[S * S + 1];  // (ns_factor)
     const bool tall = it.rows > it.cols;
     const int s = min(it.rows, it.cols), L = max(it.rows, it.cols);
     const int n16 = lane & 15, kk = lane >> 4;
@@ -803,8 +844,8 @@ __device__ __forceinline__ void ns_apply(const NsItem& it, int block, const floa
                 ns_load<4, HALF>(v[st], r, i < s && n16 < len ? (n16 * it.cols + i) << SH : kNsDead);
             } else {
 #pragma unroll
-                for (int u = 0; u < 4; u++) {
-                    const int off = i + u < s && n16 < len ? (int)(((int64_t)(i + u) * it.cols + n16) << SH) : kNsDead;
+                for (int u = 0; u < 4; u++) {  // (rows past the last are out of range)
+                    const int off = n16 < len ? (int)(((int64_t)(i + u) * it.cols + n16) << SH) : kNsDead;
                     v[st][u] = HALF ? h2f((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0))
                                     : __builtin_bit_cast(float, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
                 }
@@ -815,7 +856,10 @@ __device__ __forceinline__ void ns_apply(const NsItem& it, int block, const floa
         for (int t = 0; t < T; t++)
             acc[t] = nf4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int st = 0; st < T; st++)
+        for (int st = 0; st < T; st++) {
+#pragma unroll
+            for (int u = 0; u < 4; u++)
+                v[st][u] = __builtin_amdgcn_ldexpf(v[st][u], eg);
 #pragma unroll
             for (int t = 0; t < T; t++) {
                 const nf4 a = *reinterpret_cast<const nf4*>(&F[(t * 16 + n16) * LD + 16 * st + 4 * kk]);
@@ -823,11 +867,15 @@ __device__ __forceinline__ void ns_apply(const NsItem& it, int block, const floa
                 for (int u = 0; u < 4; u++)
                     acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[u], v[st][u], acc[t], 0, 0, 0);
             }
+        }
         if (n16 < len) {
             char* ob = static_cast<char*>(it.out) + ((lb * sl) << SH);
 #pragma unroll
             for (int t = 0; t < T; t++) {
                 const int i = t * 16 + 4 * kk;
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                    acc[t][q] = __builtin_amdgcn_ldexpf(acc[t][q], eo);
                 if (tall && i + 4 <= s) {
                     typedef float f4_any __attribute__((ext_vector_type(4), aligned(4)));
                     typedef uint32_t u2_any __attribute__((ext_vector_type(2), aligned(2)));
@@ -1051,7 +1099,8 @@ __global__ __launch_bounds__(256) void k_nsl_init(const NsItem* __restrict__ tab
 #pragma unroll
     for (int q = 0; q < 4; q++)
         part[q] = (int)threadIdx.x + 256 * q < n.sqn ? sq[threadIdx.x + 256 * q] : 0.0;
-    const double inv = 1.0 / (sqrt(ns_block_sum((part[0] + part[1]) + (part[2] + part[3]), red)) + eps);
+    const double sum = ns_block_sum((part[0] + part[1]) + (part[2] + part[3]), red);
+    const double inv = sum == 0.0 ? 0.0 : 1.0 / (sqrt(sum) + eps);  // (1 / eps may be infinite)
     for (int r = r0; r < 64; r += 4)
         tile[r][c] = (float)((double)v[(r - r0) / 4] * inv) * scale;
     __syncthreads();
@@ -1648,7 +1697,7 @@ int64_t ns_bytes(int64_t rows, int64_t cols)
     const int T = ns_tiles(s);
     if (T == 0)
         return up256(ns_long_bytes(ns_long(rows, cols, ns_parts(rows, cols))));
-    const int64_t part = (int64_t)ns_slices(l, T) * tri(T) * 2048, f = 4LL * 256 * T * T;
+    const int64_t part = (int64_t)ns_slices(l, T) * tri(T) * 2048, f = 4LL * 256 * T * T + 8;  // (with two exponents)
     return ((part > f ? part : f) + 255) / 256 * 256;
 }
 
