@@ -902,11 +902,12 @@ __device__ __forceinline__ void ns_apply(const NsItem& it, int block, const floa
 }
 
 __global__ __launch_bounds__(256) void k_ns_apply(const NsItem* __restrict__ table, const int32_t* __restrict__ item,
-                                                  const char* ws)
+                                                  const char* ws, int first)
 {
     __shared__ float F[96 * 100];
-    const NsItem it = table[__builtin_amdgcn_readfirstlane(item[blockIdx.x])];
-    const int block = (int)blockIdx.x - it.apply0;
+    const int at = first + (int)blockIdx.x;
+    const NsItem it = table[__builtin_amdgcn_readfirstlane(item[at])];
+    const int block = at - it.apply0;
     const float* f = reinterpret_cast<const float*>(ws + it.off);
     if (it.tiles == 2)
         it.half ? ns_apply<2, true>(it, block, f, F) : ns_apply<2, false>(it, block, f, F);
@@ -1723,6 +1724,9 @@ size_t orthogonalize_workspace_bytes(const OrthoEntry* items, int count)
     return (size_t)(total + up256(4 * grams) + up256(4 * applies));
 }
 
+// (every launch but k_ns_apply's, which goes in ranges, stays below 2^32 threads for the largest
+// sides and list: k_ns_gram 4096 x 128 blocks of 256, the long form's kernels at most
+// 2^22 of 256 per matrix)
 bool orthogonalize_fits(int64_t rows, int64_t cols)
 {
     const int64_t s = rows < cols ? rows : cols, l = rows < cols ? cols : rows;
@@ -1804,7 +1808,12 @@ hipError_t launch_orthogonalize(const OrthoEntry* items, int count, double a, do
             hipLaunchKernelGGL(k_ns_poly, dim3((unsigned)shorts), dim3(64 * kNsWaves), 0, s, t, w, coef);
         else
             hipLaunchKernelGGL(k_ns_poly64, dim3((unsigned)shorts), dim3(64 * kNsWaves), 0, s, t, w, coef);
-        hipLaunchKernelGGL(k_ns_apply, dim3((unsigned)applies), dim3(256), 0, s, table, apply_item, w);
+        // (4096 matrices of 2^20 x 1 are 2^24 blocks, more than a grid's 2^32 threads)
+        constexpr int64_t kMost = (int64_t)1 << 23;
+        static_assert(grid_fits(kMost, 256), "blocks per launch");
+        for (int64_t first = 0; first < applies; first += kMost)
+            hipLaunchKernelGGL(k_ns_apply, dim3((unsigned)(applies - first < kMost ? applies - first : kMost)), dim3(256), 0, s,
+                               table, apply_item, w, (int)first);
     }
     if (longs > 0) {
         const unsigned y = (unsigned)longs;
