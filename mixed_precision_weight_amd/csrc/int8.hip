@@ -321,13 +321,16 @@ __global__ __launch_bounds__(256) void k_int8_gemv(const DecBatch b)
                 }
             }
     }
-    float part[R][M];
+    // the codes' sums over the wave in integers, so that they are exact, the weak columns' in fp32
+    float part[R][M], y[R][M];
 #pragma unroll
     for (int r = 0; r < R; r++) {
         const float sw = L.s[brow + min(wave * R + r, nb - 1)];
 #pragma unroll
-        for (int m = 0; m < M; m++)
-            part[r][m] = (float)acc[r][m] * (rs[m].scale * sw);  // a lane's sum is below 2^24: exact
+        for (int m = 0; m < M; m++) {
+            y[r][m] = (float)wave_sum_dpp(acc[r][m]) * (rs[m].scale * sw);
+            part[r][m] = 0.0f;
+        }
     }
     for (int c = lane; c < k; c += 64) {
         int j = L.idx[c];
@@ -348,7 +351,7 @@ __global__ __launch_bounds__(256) void k_int8_gemv(const DecBatch b)
     for (int r = 0; r < R; r++)
 #pragma unroll
         for (int m = 0; m < M; m++) {
-            const float v = wave_sum_dpp(part[r][m]);
+            const float v = k > 0 ? y[r][m] + wave_sum_dpp(part[r][m]) : y[r][m];
             if (lane == 0 && wave * R + r < nb)
                 L.y[(int64_t)m * N + brow + wave * R + r] = f2h(v);
         }

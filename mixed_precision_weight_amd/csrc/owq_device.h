@@ -142,6 +142,24 @@ __device__ __forceinline__ float wave_sum_dpp(float v)
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
+// The same for integers (exact, whatever the order)
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ int dpp_i(int v)
+{
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+}
+
+__device__ __forceinline__ int wave_sum_dpp(int v)
+{
+    v += dpp_i<0xb1>(v);
+    v += dpp_i<0x4e>(v);
+    v += dpp_i<0x124>(v);
+    v += dpp_i<0x128>(v);
+    v += dpp_i<0x142, 0xa>(v);
+    v += dpp_i<0x143, 0xc>(v);
+    return __builtin_amdgcn_readlane(v, 63);
+}
+
 // The same DPP pattern for min / max: lanes a row mask leaves out keep their own
 // value. Both are exact, so the order of the steps does not matter.
 template <int CTRL, int ROWS = 0xf>
