@@ -547,11 +547,17 @@ __global__ __launch_bounds__(64) void k_int8_dx_sum(const BwdArgs8 a, int tiles)
     weak_put(a, range, m0, min(32, a.M - m0));
 }
 
-// Blocks per tile: as many as fill the CUs, each with at least 8 stages
+// Blocks per tile: as many as leave one per CU (a CU takes two, but a part is 64 KB of sums
+// written and read again, and the weak sums beside the product want CUs too), each with at least 8
+// stages. The whole backward in us with 1 | 256 / tiles | 512 / tiles parts: one token of
+// 4096 x 4096 (32 tiles) 56 | 26 | 32; 64 of 11008 x 4096 (32) 138 | 48 | 55; 150 of 3584 x 3584 (56) 55 | 32 |
+// 34; 512 of 4096 x 4096 (128) 67 | 54 | 55; 1000 of 4096 x 1024 (64) 69 | 42 | 48; 400 of 11008 x 512 (16)
+// 153 | 56 | 67, and 51 with half as many; 2000 of 2816 x 320 (48) 57 | 41 | 53, and 37 with two; 1000 of
+// 28672 x 256 without weak columns (16) 321 | 82 | 89; 2048 of 768 x 768 (96) 33 | 33 | 37.
 int dx_splits(int64_t M, int64_t N, int64_t K)
 {
     const int64_t tiles = (M + kDxTokens - 1) / kDxTokens * ((K + kDxCols - 1) / kDxCols);
-    int64_t sp = 512 / tiles;
+    int64_t sp = 256 / tiles;
     const int64_t most = (N + kDxRows - 1) / kDxRows / 8;
     sp = sp < most ? sp : most;
     return (int)(sp < 1 ? 1 : sp);
@@ -569,7 +575,9 @@ Int8BwdPlan int8_bwd_plan(int64_t N, int64_t K, int32_t k, int64_t M)
     p.kp = up(k, 32);
     p.splits = dx_splits(M, N, K);
     p.tiles = up(M, kDxTokens) / kDxTokens * (up(K, kDxCols) / kDxCols);
-    // slices of the weak columns' sums: enough blocks, at least 512 rows each
+    // slices of the weak columns' sums: enough blocks, at least 512 rows each. Whole backward with
+    // 1 | these | twice as many, us: 64 tokens of 11008 x 4096 (21) 105 | 53 | 53; 77 of 2731 x 1056 (5)
+    // 32 | 20 | 22; 1000 of 4096 x 1024 (8) 61 | 47 | 52
     const int64_t tiles = (M + 31) / 32 * (p.kp / 32 > 0 ? p.kp / 32 : 1);
     int64_t sl = (512 + tiles - 1) / tiles;
     sl = sl < p.Np / 512 ? sl : p.Np / 512;
@@ -603,7 +611,10 @@ hipError_t launch_linear_int8_backward(const Int8Desc& d, const uint16_t* dy, in
                        (int)tokens);
     const int64_t dws = a.dw ? (d.N + 31) / 32 : 0, dxs = dx && d.k > 0 ? (M + 31) / 32 * p.slices : 0;
     // the weak sums: beside the product where its parts are added in a launch of their own
-    // (they go into dx there) and one grid holds both, else before it
+    // (they go into dx there) and one grid holds both, else before it. Beside | before, us: 77 tokens of
+    // 2731 x 1056 20 | 25; 64 of 11008 x 4096 48 | 53; 1000 of 4096 x 1024 42 | 47; 1000 of 28672 x 256 161 |
+    // 174; 2048 of 11008 x 512 119 | 119. First in that grid instead of last: mostly within 5 %
+    // either way, 36 % worse at worst (300 tokens of 11008 x 4096).
     const int64_t blocks = p.tiles * p.splits, sums = (dws + dxs) * (p.kp / 32);
     const bool beside = dx && p.splits > 1 && grid_fits(blocks + sums, 256);
     if (!beside && sums > 0)
