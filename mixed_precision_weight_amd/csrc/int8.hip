@@ -13,8 +13,10 @@ namespace {
 
 // -------------------------------------------------------------------- pack --
 
-// One block per row: the largest dense magnitude, then the codes and the weak weights. Bound by
-// memory: 11008 x 4096 in 38 .. 49 us, 135 MB at 2.8 .. 3.6 TB/s.
+// One block per row: the largest dense magnitude, then the codes and the weak weights, the row
+// read again from L2. 11008 x 4096: 37 us, 135 MB at 3.6 TB/s (a copy's 5.15 would take 26); what is
+// missing is the chain mask, row, largest magnitude, row in each block, of which the mask's 32 KB
+// of LDS leaves four to a CU. It runs once per layer.
 template <bool WIDE>
 __global__ __launch_bounds__(256) void k_pack_int8(const uint16_t* __restrict__ W, int K, const int32_t* __restrict__ idx,
                                                    int k, int8_t* __restrict__ codes, float* __restrict__ scales,
@@ -78,7 +80,9 @@ struct QuantBatch {
 // scale, its codes up to Kq columns (zeros past K) and its weak columns padded to kp with
 // zeros. The codes go in the order of that product's B operand (16 tokens together,
 // 64-column steps, lane 16 g + m holds the 16 columns g of token m). P: 16-column pieces a
-// thread holds (longer rows are read twice). A launch and a chain of three latencies (weak
+// thread holds (the rest of a longer row is read twice): one up to 4096 columns, else three. One | three,
+// us, tokens not in the caches: 16 tokens, 4096 x 11008, 21.3 | 20.7, 1024 x 12288 16.7 | 16.3; from
+// them, 1024 x 4096, 9.1 | 9.3. A launch and a chain of three latencies (weak
 // columns, token, largest magnitude): 3.6 us for 16 tokens of 4096.
 template <bool WIDE, int P>
 __global__ __launch_bounds__(256) void k_int8_tokens(const QuantBatch b)
@@ -137,14 +141,17 @@ __global__ __launch_bounds__(256) void k_int8_tokens(const QuantBatch b)
     }
 }
 
-// The tokens of the tiled product: a wave per token, which holds P pieces of 16 columns per
-// lane, so that only the mask of the weak columns is shared (one barrier). Codes and weak
+// The tokens of the tiled product: a wave per token, which holds 11 pieces of 16 columns per
+// lane (the rest of a longer row is read twice; 4 | 11 | 16 pieces, us, tokens not in the caches: 300
+// tokens, 4096 x 11008, 49.0 | 47.7 | 48.2, 2048 tokens 108 | 106 | 107, 300 of 4096 x 16384 60.7 | 60.0 |
+// 58.9, of 4096 x 4096 28.6 | 28.5 | 28.5), so that only the mask of the weak columns is shared (one barrier). Codes and weak
 // columns go in panels, and the blocks past the tokens lay the layer's weak weights out
 // alike. 2048 tokens of 4096: 9.5 us, 25 MB at 2.6 TB/s, each wave one chain of latencies;
 // 300 tokens of 11008: 9.3 us.
-template <bool WIDE, int P>
+template <bool WIDE>
 __global__ __launch_bounds__(256) void k_int8_token_panels(const QuantLayer L, int M)
 {
+    constexpr int P = 11;
     __shared__ DenseMask<WIDE> mask;
     const int tid = threadIdx.x, lane = tid & 63;
     const int K = L.K, kp = L.kp;
@@ -961,12 +968,10 @@ hipError_t launch_linear_int8(const Int8Desc* d, int count, int64_t M, void* con
     q.wwp = reinterpret_cast<uint16_t*>(w + p[0].off_wwp);
     const int64_t units = (d[0].N * (q.kp / 8) + 255) / 256;
     const dim3 panels((unsigned)((M + 3) / 4 + (units < 512 ? units : 512)));
-    if (longest <= 4096)
-        hipLaunchKernelGGL((k_int8_token_panels<true, 4>), panels, dim3(256), 0, s, q, (int)M);
-    else if (longest <= kWideMask)
-        hipLaunchKernelGGL((k_int8_token_panels<true, 11>), panels, dim3(256), 0, s, q, (int)M);
+    if (longest <= kWideMask)
+        hipLaunchKernelGGL(k_int8_token_panels<true>, panels, dim3(256), 0, s, q, (int)M);
     else
-        hipLaunchKernelGGL((k_int8_token_panels<false, 11>), panels, dim3(256), 0, s, q, (int)M);
+        hipLaunchKernelGGL(k_int8_token_panels<false>, panels, dim3(256), 0, s, q, (int)M);
     const GemmGrid g = gemm_grid(M, d[0].N, q.Kq / kGemmCols);
     const GemmArgs8 a{d[0].q, d[0].s, d[0].y, q.x8, q.sx, q.xw, q.wwp, (int32_t)M, (int32_t)d[0].N, (int32_t)d[0].K, q.Kq, q.kp,
                       (int32_t)((M + kGemmTokens - 1) / kGemmTokens), (int32_t)g.whole, g.splits,

@@ -1677,7 +1677,10 @@ bool ns_fixed(double a, double b, double c, int steps)
 
 // ------------------------------------------------------------------ the plan --
 
-constexpr int kNsShort = 96;  // short sides of the short form
+// Short sides of the short form: the digits of three 96 x 96 matrices fill a CU's LDS. Five steps,
+// short | long form, us: 96 x 96 95 | 164, 4096 x 96 94 | 172, 4096 x 64 50 | 172, 2^18 x 96 313 | 1205,
+// 32 of 4096 x 86 149 | 500; 4096 x 97 takes the long form's 174.
+constexpr int kNsShort = 96;
 int ns_tiles(int64_t s) { return s > kNsShort ? 0 : (s > 64 ? 6 : (s > 32 ? 4 : 2)); }
 
 // slices of the long side in the short form: at least 256 long (128 for wide Gram
