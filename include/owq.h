@@ -709,11 +709,16 @@ size_t owq_orthogonalize_workspace_bytes(const owq_update* items, int32_t count)
  *   X = g / (|g|_F + eps),  `steps` times  X <- a X + b (X X^T) X + c (X X^T)^2 X,
  *   out = scale X
  * which moves every singular value towards 1 and keeps the singular vectors. (a, b, c):
- * coefficients, HOST array [3]; (1.875, -1.25, 0.375) converges to the factor itself,
- * (3.4445, -4.7750, 2.0315) lifts small values faster and ends between 0.7 and 1.2. |g|_F
- * is fp64; up to a shorter side of 96, X X^T is summed in fp64 and its polynomial runs on
- * 40-bit numbers, or on fp64 where the steps lift a direction more than 2^11 times; above, matrices are kept in 22 bits (pairs of fp16); all else is fp32, out
- * rounded once. A matrix of zeros gives zeros; one with an infinity or NaN gives NaN
+ * coefficients, HOST array [3]; (1.875, -1.25, 0.375), the fifth-order iteration, converges to
+ * the factor itself, (3.4445, -4.7750, 2.0315), published with five steps and eps 1e-7 for the
+ * Muon optimiser (K. Jordan and others, 2024), lifts small values faster and ends between 0.7
+ * and 1.2. |g|_F is fp64; up to a shorter side of 96, X X^T is summed in fp64 and its
+ * polynomial runs on 40-bit numbers, or on fp64 where the steps lift a direction more than
+ * 2^11 times; above, matrices are kept in 22 bits (pairs of fp16); all else is fp32, out
+ * rounded once. As with fp32 products, what is rounded grows by up to |a| a step along the
+ * directions that g lacks (a gradient of fewer tokens than weak columns): with the second
+ * coefficients 2e-5 of out after 5 steps, 1e-2 after 10, of its own size from 13 on, where the
+ * singular values stay bounded. A matrix of zeros gives zeros; one with an infinity or NaN gives NaN
  * throughout, and the others are as without it. 1 <= steps <= 16; coefficients finite;
  * eps > 0. Every out must be disjoint from every other out and, unless it is the matrix's
  * own g, from every g; the workspace from all of them (OWQ_ERR_RANGE). workspace: >=

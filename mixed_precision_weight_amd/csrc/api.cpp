@@ -206,7 +206,7 @@ owq_status check_apart(const Span& out, const owq_layer* L)
                              {"w_weak", L->w_weak, 2 * N * k}});
 }
 
-// --- 8-bit form
+// --- integer form
 
 bool int8_sizes_ok(int64_t N, int64_t K, int32_t k, int64_t M)
 {
@@ -235,7 +235,7 @@ owq_status check_int8_layer(const owq_integer_layer* L, int64_t M, const uint16_
         (L->k > 0 && (!aligned(L->weak_idx, 4) || !aligned(L->w_weak, 2))))
         return fail(OWQ_ERR_ALIGN, "misaligned pointer (x, codes: 16 B, scales, weak_idx: 4 B, fp16 arrays: 2 B)");
     if (!owq::int8_grid_fits(M, L->N, L->K))
-        return launch_status(hipErrorInvalidConfiguration, "8-bit form");
+        return launch_status(hipErrorInvalidConfiguration, "integer form");
     return check_idx_on_host(L->weak_idx, L->k, L->K, s);
 }
 
@@ -1172,7 +1172,7 @@ owq_status owq_clip_grad_norm(const owq_grad* items, int32_t count, double max_n
     }
 }
 
-// ---------------------------------------------------------------- 8-bit form --
+// ---------------------------------------------------------------- integer form --
 
 owq_status owq_pack_integer(const uint16_t* W, int64_t N, int64_t K, const int32_t* weak_idx, int32_t k, int8_t* codes,
                          float* scales, uint16_t* w_weak, void* stream)

@@ -1,4 +1,4 @@
-// int8.hip -- the 8-bit form: pack and product (gfx950).
+// int8.hip -- the integer form: pack and product (gfx950).
 //
 //   y[m][i] = s_m scale_i sum_j q_mj code_ij + sum_c x[m][idx_c] w_weak[i][c]
 // with a token's dense columns quantised on the way in (s_m = t_m / 127, q_mj =

@@ -1,4 +1,4 @@
-// int8_backward.hip -- backward of the 8-bit form's linear for weak-column tuning (gfx950).
+// int8_backward.hip -- backward of the integer form's linear for weak-column tuning (gfx950).
 //
 //   dx[m][j]      = sum_i dy[m][i] W[i][j],  W = scale_i code_ij, the weak columns as they are
 //   dw_weak[i][c] = sum_m dy[m][i] x[m][idx_c]

@@ -1,6 +1,6 @@
-// owq_int8.h -- what the kernels of the 8-bit form share (gfx950).
+// owq_int8.h -- what the kernels of the integer form share (gfx950).
 //
-// The 8-bit form: codes int8 [N][K], rint(w * (127 / t)) with t the row's largest
+// The integer form: codes int8 [N][K], rint(w * (127 / t)) with t the row's largest
 // |w| over its dense columns, 0 at the weak columns; scale t / 127 per row; the weak
 // columns in fp16. A token is treated alike: its dense columns become int8 with the
 // token's own scale, its weak columns stay fp16. The products of codes are exact in

@@ -225,7 +225,7 @@ constexpr int kClipItems = 240;  // tensors per launch (kernel arguments below 4
 size_t clip_workspace_bytes(int count);
 hipError_t launch_clip(const ClipEntry* items, int count, double max_norm, float* norm, void* ws, hipStream_t s);
 
-// ----------------------------------------------------------------- 8-bit form --
+// ----------------------------------------------------------------- integer form --
 struct Int8Desc {
     const int8_t* q;      // [N][K]
     const float* s;       // [N]

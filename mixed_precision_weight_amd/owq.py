@@ -1419,7 +1419,8 @@ def linear_integer_backward(layer: dict, x: torch.Tensor | None, dy: torch.Tenso
 
 # --------------------------------------------------------- orthogonalised update
 
-# (a, b, c) of the quintic: lifts small singular values fastest and ends between 0.7 and 1.2
+# (a, b, c) of the quintic published for the Muon optimiser (K. Jordan and others, 2024): lifts
+# small singular values fastest and ends between 0.7 and 1.2
 NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
 
 
