@@ -141,17 +141,17 @@ __global__ __launch_bounds__(256) void k_int8_tokens(const QuantBatch b)
     }
 }
 
-// The tokens of the tiled product: a wave per token, which holds 11 pieces of 16 columns per
-// lane (the rest of a longer row is read twice; 4 | 11 | 16 pieces, us, tokens not in the caches: 300
-// tokens, 4096 x 11008, 49.0 | 47.7 | 48.2, 2048 tokens 108 | 106 | 107, 300 of 4096 x 16384 60.7 | 60.0 |
-// 58.9, of 4096 x 4096 28.6 | 28.5 | 28.5), so that only the mask of the weak columns is shared (one barrier). Codes and weak
+// The tokens of the tiled product: a wave per token, which holds P pieces of 16 columns per
+// lane (the rest of a longer row is read twice): 4 up to 4096 columns, else 11. 4 | 11 | 16 pieces, us:
+// 2048 tokens of 4096 columns 9.6 | 10.6 | - (this kernel); 300 tokens, 4096 x 11008, 49.0 | 47.7 | 48.2, 2048
+// tokens 108 | 106 | 107, 300 of 4096 x 16384 60.7 | 60.0 | 58.9 (the whole product, tokens not in the
+// caches). So only the mask of the weak columns is shared (one barrier). Codes and weak
 // columns go in panels, and the blocks past the tokens lay the layer's weak weights out
-// alike. 2048 tokens of 4096: 9.5 us, 25 MB at 2.6 TB/s, each wave one chain of latencies;
-// 300 tokens of 11008: 9.3 us.
-template <bool WIDE>
+// alike. 2048 tokens of 4096: 25 MB at 2.6 TB/s, each wave one chain of latencies; 300 tokens of
+// 11008: 9.3 us.
+template <bool WIDE, int P>
 __global__ __launch_bounds__(256) void k_int8_token_panels(const QuantLayer L, int M)
 {
-    constexpr int P = 11;
     __shared__ DenseMask<WIDE> mask;
     const int tid = threadIdx.x, lane = tid & 63;
     const int K = L.K, kp = L.kp;
@@ -387,7 +387,7 @@ constexpr int kMfvWaves = 4;  // waves that split K
 // (lane l: row l % 16, 16 columns 16 (l / 16) of a 64-column step) and the tokens as B,
 // which k_int8_tokens has laid out in that order. Both come straight from memory into the
 // operands, U steps ahead of their products. The waves' sums meet in LDS. Bound by the
-// codes' stream: 16 tokens, 11008 x 4096, 45 MB in 11 us (4.1 TB/s).
+// codes' stream: 16 tokens, 11008 x 4096, 45 MB in 12 us (3.8 TB/s).
 template <int RT, int MT, int U>
 __global__ __launch_bounds__(64 * kMfvWaves) void k_int8_mfv(const MfvBatch b)
 {
@@ -968,10 +968,12 @@ hipError_t launch_linear_int8(const Int8Desc* d, int count, int64_t M, void* con
     q.wwp = reinterpret_cast<uint16_t*>(w + p[0].off_wwp);
     const int64_t units = (d[0].N * (q.kp / 8) + 255) / 256;
     const dim3 panels((unsigned)((M + 3) / 4 + (units < 512 ? units : 512)));
-    if (longest <= kWideMask)
-        hipLaunchKernelGGL(k_int8_token_panels<true>, panels, dim3(256), 0, s, q, (int)M);
+    if (longest <= 4096)
+        hipLaunchKernelGGL((k_int8_token_panels<true, 4>), panels, dim3(256), 0, s, q, (int)M);
+    else if (longest <= kWideMask)
+        hipLaunchKernelGGL((k_int8_token_panels<true, 11>), panels, dim3(256), 0, s, q, (int)M);
     else
-        hipLaunchKernelGGL(k_int8_token_panels<false>, panels, dim3(256), 0, s, q, (int)M);
+        hipLaunchKernelGGL((k_int8_token_panels<false, 11>), panels, dim3(256), 0, s, q, (int)M);
     const GemmGrid g = gemm_grid(M, d[0].N, q.Kq / kGemmCols);
     const GemmArgs8 a{d[0].q, d[0].s, d[0].y, q.x8, q.sx, q.xw, q.wwp, (int32_t)M, (int32_t)d[0].N, (int32_t)d[0].K, q.Kq, q.kp,
                       (int32_t)((M + kGemmTokens - 1) / kGemmTokens), (int32_t)g.whole, g.splits,

@@ -319,9 +319,10 @@ typedef int i32x2 __attribute__((ext_vector_type(2)));
 // instead needs registers and eight-way bank conflicts: 315 us for 2048 tokens, 11008 x
 // 4096.) The columns are the matrix instruction's A, so that a lane ends with four
 // consecutive columns of one token. Blocks past the `blocks` of the product (where k_int8_dx_sum
-// adds the product's parts and puts the weak columns in) make the weak sums beside it. 2048 tokens, 11008 x 4096: 340 us,
-// 1.09 PFLOP/s of both halves' products (the library's fp16 product reaches 1.4 at 8192^3; the card's
-// power holds the clock). Strips of 2, 4 or 8 token panels per XCD, which share more of g: no change.
+// adds the product's parts and puts the weak columns in) make the weak sums beside it. 2048
+// tokens, 11008 x 4096: 336 us, 1.1 PFLOP/s of both halves' products, matrix cores busy 79 % (the
+// library's fp16 product reaches 1.4 at 8192^3; the card's power holds the clock). Strips of 2, 4 or 8
+// token panels per XCD, which share more of g: no change.
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_int8_dx(const BwdArgs8 a, int blocks, int dws)
 {
     __shared__ __attribute__((aligned(1024))) char s0[kDxStage];

@@ -615,8 +615,8 @@ __device__ __forceinline__ void ns_poly(const NsItem& it, char* ws, const NsCoef
         }
 }
 
-// One block per matrix. Short sides up to 96 / 64: 60 / 29 us for five steps: 14 phases
-// of products (28 of the 60 us at the 8-bit rate of one CU), rounding to digits, two barriers.
+// One block per matrix. Short sides up to 96 / 64: 61 / 30 us for five steps: 14 phases
+// of products (28 of the 61 us at the 8-bit rate of one CU), rounding to digits, two barriers.
 __global__ __launch_bounds__(64 * kNsWaves) void k_ns_poly(const NsItem* __restrict__ table, char* ws, const NsCoef k)
 {
     __shared__ __attribute__((aligned(16))) char lds[kNsLds];
