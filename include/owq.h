@@ -679,7 +679,7 @@ size_t owq_linear_integer_backward_workspace_bytes(int64_t N, int64_t K, int32_t
  * x: fp16 [M][K], read only for dw_weak (may be NULL without it); dy: fp16 [M][N]; dx,
  * dw_weak: outputs, each may be NULL. In the dense part of dx, dy times the scale is
  * kept in 22 bits (a pair of fp16 values) after scaling each token by a power of two (every
- * term that is not below 2^-18 of the token's largest, the others to 2^-40 of it; no term
+ * term that is not below 2^-17 of the token's largest, the others to 2^-39 of it; no term
  * overflows); every other product is exact, every sum fp32, dx rounded to fp16 once. Bitwise deterministic. No output and not the workspace may
  * overlap one another, an input or the layer (OWQ_ERR_RANGE). M, N <= 2^20. workspace: >=
  * owq_linear_integer_backward_workspace_bytes(...) bytes, 256-byte aligned, contents ignored;
